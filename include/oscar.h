@@ -87,6 +87,7 @@ typedef int oscar_status;
 #define OSCAR_DEVERR_NONFINITE 8     /* a group of rotated values held a NaN or an
                                         infinity; it was stored as a zero group
                                         (s = z = 0, codes 0)                            */
+#define OSCAR_DEVERR_NO_PAGES 16     /* the free list ran out of pages                  */
 
 #define OSCAR_VARIANT_OSCAR 0        /* R = U H P_br                                    */
 #define OSCAR_VARIANT_HADAMARD 1     /* R = H (data-oblivious baseline)                 */
@@ -401,6 +402,167 @@ oscar_status oscar_clip_threshold_device(int32_t num_kv_heads, int32_t d, int64_
  * 0 for invalid arguments. */
 size_t oscar_multiquery_workspace_size(const oscar_cache_desc* desc, int32_t batch, int32_t m_rows,
                                        int32_t max_seq_len);
+
+/* --------------------------------------------------------- the 8-bit cache
+ *
+ * A paged cache in 8 bits that needs no calibration: keys and values as they
+ * come (no rotation), one scale per (page of 16 tokens, KV head) for keys and
+ * one for values.  The pages about OSCAR name 8-bit caches only as what INT2 is
+ * smaller than ([Summary 1]); the format below is this library's.
+ *   A sequence of L tokens holds its first floor(L/16) pages in 8 bits, through
+ *   page_table[b * max_pages_per_seq + p] (equal ids share a page), and its last
+ *   L mod 16 tokens in bf16 in tail block tail_ids[b] (b itself when tail_ids is
+ *   null).  A page is coded once, when its 16 tokens are there, so its content
+ *   does not depend on the sizes of the calls that brought them.
+ *   Block of (page, KV head): 32*d + 16 bytes at (page*num_kv_heads + head) times
+ *   that: 16*d key codes, 16*d value codes, fp32 key scale, fp32 value scale, 8
+ *   spare bytes.  Tail block of (id, KV head): 16*d bf16 keys, 16*d bf16 values.
+ *   The order of elements is documented in csrc/kv8_layout.cuh.
+ *   With a the largest finite magnitude of the block: scale = fl32(a / top),
+ *   inv = fl32(top / a), code = round-half-even(fl32(x * inv)); OSCAR_KV8_INT8:
+ *   top 127, codes stored plus 128; OSCAR_KV8_E4M3: top 448, codes rounded to
+ *   e4m3.  Value = code * scale.  A block with a < 2^-100 is stored as zeros.  A
+ *   NaN is stored as 0 and an infinity as +-top (OSCAR_DEVERR_NONFINITE is set);
+ *   the tail keeps both as they are.
+ * Every pointer of the descriptor is 4-byte aligned, pool and tail 16-byte.
+ * d in {64, 128}; any G = num_q_heads / num_kv_heads >= 1.
+ * Kernels never trap: a page or tail id out of range is skipped (its tokens are
+ * left out) with OSCAR_DEVERR_PAGE_ID. */
+#define OSCAR_KV8_INT8 0
+#define OSCAR_KV8_E4M3 1
+
+typedef struct oscar_kv8_desc {
+  int32_t num_kv_heads;
+  int32_t num_q_heads;
+  int32_t head_dim;                /* 64 or 128                                       */
+  int32_t max_pages_per_seq;       /* row length of the page table                    */
+  int64_t num_pages;               /* physical pages in the pool                      */
+  int64_t num_tails;               /* tail blocks                                     */
+  void* pool;                      /* device                                          */
+  void* tail;                      /* device bf16                                     */
+  const int32_t* page_table;       /* device [batch][max_pages_per_seq]               */
+  const int32_t* tail_ids;         /* device [batch], or null: sequence b has tail b  */
+  int32_t* status;                 /* optional device word (OSCAR_DEVERR_* bits)      */
+  int32_t format;                  /* OSCAR_KV8_*                                     */
+} oscar_kv8_desc;
+
+/* Places new tokens behind those that each sequence holds: a prompt, a chunk of
+ * one, or a decode step's token.  Sequence b's rows are row_starts[b] ..
+ * row_starts[b+1] - 1 of k and v, at positions lens_before[b] onwards; rows from
+ * row_starts[batch] on are not read.  Pages that these rows complete are coded
+ * (their first tokens from the tail where they came earlier), the tokens behind
+ * the last whole page go to the tail.  The caller allocates the pages first
+ * (oscar_extend_pages with hold_back 15).
+ *   k, v: device bf16, 16-byte aligned, row i at i * k_stride (v_stride) elements,
+ *     [num_kv_heads][d] contiguous in a row; strides multiples of 8.
+ *   lens_before: device int32 [batch]; row_starts: device int32 [batch + 1],
+ *     ascending; total_rows: rows of k and v; max_new: no sequence brings more.
+ * A sequence with more rows than max_new, rows outside [0, total_rows) or
+ * positions behind its table is skipped with OSCAR_DEVERR_SEQ_LEN.  Two
+ * sequences must not have the same tail id.  Asynchronous. */
+oscar_status oscar_kv8_place(const oscar_kv8_desc* desc, const void* k, const void* v,
+                             int64_t k_stride, int64_t v_stride, const int32_t* lens_before,
+                             const int32_t* row_starts, int32_t batch, int64_t total_rows,
+                             int32_t max_new, void* stream);
+
+/* Reads tokens back as bf16 (code * scale rounded once; tail tokens as they are):
+ * rows row_starts[b] .. row_starts[b+1] - 1 of k_out and v_out get the tokens of
+ * sequence b from position first[b] on.  seq_lens: tokens stored.  k_out, v_out:
+ * device bf16 [total_rows][num_kv_heads][d], 16-byte aligned; rows behind
+ * row_starts[batch] are left as they were.  max_rows: no sequence asks for more.  A
+ * sequence that asks for tokens behind seq_lens[b] is skipped with
+ * OSCAR_DEVERR_SEQ_LEN.  Asynchronous. */
+oscar_status oscar_kv8_gather(const oscar_kv8_desc* desc, const int32_t* seq_lens,
+                              const int32_t* first, const int32_t* row_starts, int32_t batch,
+                              int64_t total_rows, int32_t max_rows, void* k_out, void* v_out,
+                              void* stream);
+
+/* Bytes of device workspace for oscar_kv8_attention; 0 for invalid arguments.  Does
+ * not grow with the batch (at most two partial results per resident CTA). */
+size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows,
+                                int32_t max_seq_len);
+
+/* Attention over the 8-bit cache, softmax scale 1/sqrt(d).
+ *   q, out: device bf16 [batch][m_rows][num_q_heads][d], 16-byte aligned; query
+ *     head hq reads KV head hq / G.
+ *   seq_lens: device int32 [batch], tokens stored (the rows' own included), 0 ..
+ *     max_seq_len; max_seq_len <= 16 * max_pages_per_seq + 15.
+ *   q_pos: null for a decode step (m_rows = 1: the row sees all tokens), else
+ *     device int32 [batch][m_rows]: row m of sequence b sees positions 0 ..
+ *     q_pos[b][m].
+ * A row that sees nothing (length 0, or a negative position: a padded row) gets
+ * zeros; a length outside its range or a position at or behind the length does
+ * too and sets OSCAR_DEVERR_SEQ_LEN.  workspace: oscar_kv8_workspace_size bytes,
+ * 16-byte aligned, no initial contents; calls that may overlap on the GPU need one
+ * each.  The result does not depend on the order in which CTAs run.  Asynchronous. */
+oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
+                                 const int32_t* q_pos, int32_t batch, int32_t m_rows,
+                                 int32_t max_seq_len, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- page tables and rotary positions */
+
+/* One step of a paged cache's bookkeeping on the device: sequence b grows from
+ * lens[b] by new_tokens[b] >= 0 tokens.
+ *   hold_back: the table holds pages for the tokens t < n - hold_back of a sequence
+ *     of n tokens: 0 for a BF16 cache, the window for INT2 pages, 15 for the 8-bit
+ *     cache (whole pages only).
+ *   page_table: int32 [batch][max_pages_per_seq]; entries of pages that a sequence
+ *     holds already are kept, those of its new pages are written with the ids
+ *     free_pages[c], free_pages[c + 1], ... in the order of sequences and pages,
+ *     c = *cursor.
+ *   lens_after [batch] (may be lens itself); page_starts [batch + 1]: index in
+ *     free_pages of each sequence's first new page, page_starts[batch] the next
+ *     step's cursor (cursor may point at it); row_starts [batch + 1]: prefix sums of
+ *     new_tokens.
+ *   seq_ids, positions [max_rows]: of every new token, in order, -1 from
+ *     row_starts[batch] on (what oscar_prefill_quantize and oscar_rope take);
+ *     slots [max_rows], optional: page id * 16 + position % 16, or -1 where the
+ *     table has no page for the token.
+ * All device memory; no two of the outputs may overlap.  A sequence with a
+ * negative length or count, or whose tokens do not fit its table row, gets no
+ * tokens, and rows beyond max_rows are not written (OSCAR_DEVERR_SEQ_LEN in
+ * *status); when free_pages runs out, the entries are -1 (OSCAR_DEVERR_NO_PAGES).
+ * status: optional.  Asynchronous. */
+oscar_status oscar_extend_pages(int32_t* page_table, int32_t max_pages_per_seq, const int32_t* lens,
+                                const int32_t* new_tokens, int32_t batch, int32_t hold_back,
+                                const int32_t* free_pages, int64_t num_free, const int32_t* cursor,
+                                int32_t* lens_after, int32_t* page_starts, int32_t* row_starts,
+                                int32_t* seq_ids, int32_t* positions, int64_t* slots,
+                                int64_t max_rows, int32_t* status, void* stream);
+
+/* Rotary frequencies as oscar_rope takes them: phases_out[i], i < rotary_dim / 2, is
+ * the fraction of a turn per token times 2^64, for f_i = base^(-2i/rotary_dim) /
+ * (2 pi) turns, slowed down for contexts longer than the model's own:
+ *   original_len = 0: f_i / factor (every frequency; factor 1: unscaled);
+ *   original_len > 0: by parts.  With r = f_i * original_len turns over the original
+ *     context and keep = clamp((r - low_turns) / (high_turns - low_turns), 0, 1):
+ *     (1 - keep) f_i / factor + keep f_i.
+ * base > 1, factor >= 1, low_turns < high_turns, all finite; rotary_dim even.
+ * Host call; phases_out is host memory, to be copied to the device once. */
+oscar_status oscar_rope_phases(double base, int32_t rotary_dim, double factor, int32_t original_len,
+                               double low_turns, double high_turns, uint64_t* phases_out);
+
+/* Rotary embedding of n rows of queries and keys: with t the phase of pair i at
+ * position m = positions[row], a' = A (a cos t - b sin t), b' = A (b cos t + a sin t),
+ * A = amplitude; (a, b) = channels (i, i + rotary_dim/2), or (2i, 2i + 1) when
+ * interleaved; channels from rotary_dim on are copied.  inverse = 1 turns back by t
+ * (the gradient with respect to the input; or to take a key to another position).
+ * The phase is exact modulo one turn at every position (64-bit integers); cos, sin
+ * and the rotation are fp32, rounded once to bf16.
+ *   q, q_out: device bf16, row stride q_stride, q_out_stride elements,
+ *     [num_q_heads][head_dim] contiguous in a row; k, k_out likewise
+ *     (num_q_heads or num_kv_heads 0: none).  An output may be its input (the same
+ *     pointer and stride), and may not overlap it otherwise.
+ *   positions: device int32 [n]; rows with a negative position are left as they
+ *     were.  phases: device uint64 [rotary_dim / 2], 8-byte aligned.
+ * head_dim in [2, 1024].  Asynchronous. */
+oscar_status oscar_rope(const void* q, const void* k, const int32_t* positions,
+                        const uint64_t* phases, int64_t n, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                        int32_t interleaved, float amplitude, int32_t inverse, int64_t q_stride,
+                        int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, void* q_out,
+                        void* k_out, void* stream);
 
 /* Number of SMs the split heuristics assume for the current device (>= 1). */
 int32_t oscar_device_sm_count(void);

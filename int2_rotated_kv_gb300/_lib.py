@@ -20,6 +20,8 @@ OSCAR_OK = 0
 STATUS_NAMES = {0: "OK", -1: "INVALID_ARG", -2: "UNSUPPORTED", -3: "WORKSPACE", -4: "CUDA",
                 -5: "NOT_CONVERGED"}
 DEVERR_PAGE_ID, DEVERR_TIMEOUT, DEVERR_SEQ_LEN, DEVERR_NONFINITE = 1, 2, 4, 8
+DEVERR_NO_PAGES = 16
+KV8_INT8, KV8_E4M3 = 0, 1
 VARIANT_OSCAR, VARIANT_HADAMARD, VARIANT_IDENTITY = 0, 1, 2
 EXPORTED = ("oscar_query_covariance", "oscar_score_covariance", "oscar_build_rotation",
             "oscar_prefill_quantize", "oscar_quantize_append", "oscar_decode_workspace_size",
@@ -30,7 +32,9 @@ EXPORTED = ("oscar_query_covariance", "oscar_score_covariance", "oscar_build_rot
             "oscar_decode_step_host",
             "oscar_calibration_workspace_size", "oscar_query_covariance_device",
             "oscar_score_covariance_device", "oscar_clip_threshold_device",
-            "oscar_prefill_quantize_trace", "oscar_quantize_append_trace")
+            "oscar_prefill_quantize_trace", "oscar_quantize_append_trace",
+            "oscar_kv8_place", "oscar_kv8_gather", "oscar_kv8_workspace_size",
+            "oscar_kv8_attention", "oscar_extend_pages", "oscar_rope_phases", "oscar_rope")
 
 
 class OscarError(RuntimeError):
@@ -52,6 +56,18 @@ class CacheDesc(ctypes.Structure):
         ("clip_k", ctypes.c_void_p), ("clip_v", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
         ("code_bits", ctypes.c_int32),
+    ]
+
+
+class Kv8Desc(ctypes.Structure):
+    _fields_ = [
+        ("num_kv_heads", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("num_tails", ctypes.c_int64),
+        ("pool", ctypes.c_void_p), ("tail", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("tail_ids", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+        ("format", ctypes.c_int32),
     ]
 
 
@@ -91,6 +107,15 @@ def lib() -> ctypes.CDLL:
             "oscar_score_covariance_device": (I32, [I32, I32, I32, I64, P, P, P, P, P,
                                                     ctypes.c_size_t, P]),
             "oscar_clip_threshold_device": (I32, [I32, I32, I64, P, P, D, P, P, ctypes.c_size_t, P]),
+            "oscar_kv8_place": (I32, [P, P, P, I64, I64, P, P, I32, I64, I32, P]),
+            "oscar_kv8_gather": (I32, [P, P, P, P, I32, I64, I32, P, P, P]),
+            "oscar_kv8_workspace_size": (ctypes.c_size_t, [P, I32, I32, I32]),
+            "oscar_kv8_attention": (I32, [P, P, P, P, I32, I32, I32, P, P, ctypes.c_size_t, P]),
+            "oscar_extend_pages": (I32, [P, I32, P, P, I32, I32, P, I64, P, P, P, P, P, P, P, I64, P,
+                                         P]),
+            "oscar_rope_phases": (I32, [D, I32, D, I32, D, D, P]),
+            "oscar_rope": (I32, [P, P, P, P, I64, I32, I32, I32, I32, I32, ctypes.c_float, I32, I64,
+                                 I64, I64, I64, P, P, P]),
             "oscar_status_string": (ctypes.c_char_p, [I32]),
             "oscar_version": (I32, []),
         }
@@ -384,6 +409,256 @@ def oscar_clip_threshold_device(x, r, percentile: float, clip_out, workspace, st
            lib().oscar_clip_threshold_device(hkv, d, n, _ptr(x), _ptr(r), float(percentile),
                                              _ptr(clip_out), _ptr(workspace), _ws_bytes(workspace),
                                              _stream(stream)))
+
+
+# --------------------------------- 8-bit cache, page tables, rotary positions
+#
+# These calls check their tensors (type, shape, strides, one device) and raise
+# ValueError; what the tensors hold is checked by the kernels.  They run on the
+# device of their tensors, on `stream` or that device's current stream.
+
+def _need(ok: bool, fn: str, what: str) -> None:
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _check_list(fn: str, device, **tensors) -> None:
+    """Contiguous int32 tensors on `device`."""
+    import torch
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor on {device}")
+
+
+def _token_stride(fn: str, name: str, t, heads: int, d: int, device) -> int:
+    """Row stride in elements of a bf16 tensor [n][heads][d] whose rows are contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3 or t.shape[1:] != (heads, d):
+        raise ValueError(f"{fn}: {name} must be a bfloat16 tensor [n][{heads}][{d}] on {device}")
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and heads > 1):
+        raise ValueError(f"{fn}: {name}: the heads of a row must be contiguous")
+    return row if t.shape[0] > 1 else heads * d
+
+
+def _launch(fn: str, device, stream, *args) -> None:
+    """Calls the library's `fn` with the stream appended, with `device` current."""
+    import torch
+    f = getattr(_LIB or lib(), fn)
+    index = device.index
+    # the current stream's handle without a Stream object around it (2 us a call)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, handle)
+    if status != OSCAR_OK:
+        raise OscarError(fn, status)
+
+
+@dataclasses.dataclass
+class Kv8Cache:
+    """Device tensors of one layer's 8-bit cache plus its C descriptor.
+
+    pool: uint8 [num_pages, Hkv, 32d + 16]; tail: bfloat16 [num_tails, Hkv, 2, 16d];
+    page_table: int32 [batch, max_pages_per_seq]; tail_ids: int32 [batch] or None
+    (sequence b has tail block b); status: int32 [1] or None; fmt: KV8_INT8 or
+    KV8_E4M3.  ``pages.allocate_kv8`` makes one.
+    """
+    num_kv_heads: int
+    num_q_heads: int
+    head_dim: int
+    pool: object
+    tail: object
+    page_table: object
+    fmt: int = KV8_INT8
+    tail_ids: object = None
+    status: object = None
+
+    def desc(self) -> Kv8Desc:
+        key = (_ptr(self.pool), _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
+               _ptr(self.status), self.fmt, self.num_q_heads)
+        cached = self.__dict__.get("_desc")
+        if cached is not None and cached[0] == key:
+            return cached[1]
+        import torch
+        fn, h, d, device = "Kv8Cache", self.num_kv_heads, self.head_dim, self.pool.device
+        _need(device.type == "cuda", fn, "pool must be on a CUDA device")
+        _need(self.pool.dtype == torch.uint8 and self.pool.is_contiguous()
+              and self.pool.shape[1:] == (h, 32 * d + 16), fn,
+              f"pool must be a contiguous uint8 tensor [num_pages][{h}][{32 * d + 16}]")
+        _need(self.tail.dtype == torch.bfloat16 and self.tail.is_contiguous()
+              and self.tail.device == device and self.tail.shape[1:] == (h, 2, 16 * d), fn,
+              f"tail must be a contiguous bfloat16 tensor [num_tails][{h}][2][{16 * d}] on {device}")
+        _check_list(fn, device, page_table=self.page_table)
+        _need(self.page_table.dim() == 2, fn, "page_table must be [batch][max_pages_per_seq]")
+        if self.tail_ids is not None:
+            _check_list(fn, device, tail_ids=self.tail_ids)
+            _need(self.tail_ids.numel() == self.page_table.shape[0], fn,
+                  "tail_ids must have an entry per row of the page table")
+        if self.status is not None:
+            _check_list(fn, device, status=self.status)
+        desc = Kv8Desc(h, self.num_q_heads, d, int(self.page_table.shape[1]),
+                       int(self.pool.shape[0]), int(self.tail.shape[0]), _ptr(self.pool),
+                       _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
+                       _ptr(self.status), self.fmt)
+        self.__dict__["_desc"] = (key, desc)
+        return desc
+
+
+def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int, stream=None):
+    """Place the rows of k and v (bf16 [n][Hkv][d], rows may be strided): sequence b's
+    rows row_starts[b] .. row_starts[b+1] - 1 go behind its lens_before[b] tokens.
+    max_new: the most rows that one sequence brings."""
+    fn, d = "oscar_kv8_place", cache.desc()
+    device = cache.pool.device
+    ks = _token_stride(fn, "k", k, cache.num_kv_heads, cache.head_dim, device)
+    vs = _token_stride(fn, "v", v, cache.num_kv_heads, cache.head_dim, device)
+    _check_list(fn, device, lens_before=lens_before, row_starts=row_starts)
+    batch = lens_before.numel()
+    _need(row_starts.numel() == batch + 1 and batch <= cache.page_table.shape[0], fn,
+          "row_starts must have batch + 1 entries, and the page table a row per sequence")
+    _need(v.shape[0] == k.shape[0], fn, "k and v must have the same rows")
+    _launch(fn, device, stream, ctypes.byref(d), k.data_ptr(), v.data_ptr(), ks, vs,
+            lens_before.data_ptr(), row_starts.data_ptr(), batch, k.shape[0], int(max_new))
+
+
+def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
+                     stream=None):
+    """Read tokens back as bf16: rows row_starts[b] .. row_starts[b+1] - 1 of k_out and
+    v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on."""
+    fn, d = "oscar_kv8_gather", cache.desc()
+    device = cache.pool.device
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _token_stride(fn, name, t, cache.num_kv_heads, cache.head_dim, device)
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+    _check_list(fn, device, seq_lens=seq_lens, first=first, row_starts=row_starts)
+    batch = seq_lens.numel()
+    _need(first.numel() == batch and row_starts.numel() == batch + 1
+          and batch <= cache.page_table.shape[0], fn,
+          "first must have batch entries, row_starts batch + 1, the page table a row per sequence")
+    _need(v_out.shape[0] == k_out.shape[0], fn, "k_out and v_out must have the same rows")
+    _launch(fn, device, stream, ctypes.byref(d), seq_lens.data_ptr(), first.data_ptr(),
+            row_starts.data_ptr(), batch, k_out.shape[0], int(max_rows), k_out.data_ptr(),
+            v_out.data_ptr())
+
+
+def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
+    d = cache.desc()
+    return int(lib().oscar_kv8_workspace_size(ctypes.byref(d), batch, m_rows, max_seq_len))
+
+
+def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,
+                        stream=None):
+    """Attention over the 8-bit cache.  Decode: q, out bf16 [B][Hq][d], every row sees
+    the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
+    row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros)."""
+    import torch
+    fn, d = "oscar_kv8_attention", cache.desc()
+    device = cache.pool.device
+    batch = seq_lens.numel()
+    heads = (cache.num_q_heads, cache.head_dim)
+    if q_pos is None:
+        m_rows, shape = 1, (batch, *heads)
+        _check_list(fn, device, seq_lens=seq_lens)
+    else:
+        _check_list(fn, device, seq_lens=seq_lens, q_pos=q_pos)
+        _need(q_pos.dim() == 2 and q_pos.shape[0] == batch, fn, "q_pos must be [batch][rows]")
+        m_rows = q_pos.shape[1]
+        shape = (batch, m_rows, *heads)
+    for name, t in (("q", q), ("out", out)):
+        if (t.dtype != torch.bfloat16 or t.device != device or t.shape != shape
+                or not t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be a contiguous bfloat16 tensor {list(shape)} "
+                             f"on {device}")
+    _need(batch <= cache.page_table.shape[0], fn, "the page table must have a row per sequence")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {device}")
+    _launch(fn, device, stream, ctypes.byref(d), q.data_ptr(), seq_lens.data_ptr(), _ptr(q_pos),
+            batch, m_rows, int(max_seq_len), out.data_ptr(), workspace.data_ptr(),
+            _ws_bytes(workspace))
+
+
+def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_after, page_starts,
+                       row_starts, seq_ids, positions, slots=None, hold_back: int = 0, status=None,
+                       stream=None):
+    """Grow every sequence by new_tokens[b]: new page-table entries from free_pages
+    (from index cursor[0] on), lengths, prefix sums and the lists of the new tokens.
+    page_starts[B] is the next call's cursor (pass page_starts[-1:]); lens_after may
+    be lens.  Rows of seq_ids, positions and slots behind the new tokens become -1."""
+    import torch
+    fn, device = "oscar_extend_pages", page_table.device
+    _need(device.type == "cuda", fn, "page_table must be on a CUDA device")
+    _check_list(fn, device, page_table=page_table, lens=lens, new_tokens=new_tokens,
+                free_pages=free_pages, cursor=cursor, lens_after=lens_after,
+                page_starts=page_starts, row_starts=row_starts, seq_ids=seq_ids,
+                positions=positions)
+    batch, rows = lens.numel(), seq_ids.numel()
+    _need(page_table.dim() == 2 and page_table.shape[0] >= batch, fn,
+          "page_table must be [batch][max_pages_per_seq]")
+    _need(new_tokens.numel() == batch and lens_after.numel() == batch and cursor.numel() >= 1
+          and page_starts.numel() == batch + 1 and row_starts.numel() == batch + 1, fn,
+          "new_tokens and lens_after must have batch entries, page_starts and row_starts batch + 1")
+    _need(positions.numel() == rows, fn, "seq_ids and positions must have the same rows")
+    if slots is not None and (slots.dtype != torch.int64 or slots.device != device
+                              or not slots.is_contiguous() or slots.numel() != rows):
+        raise ValueError(f"{fn}: slots must be a contiguous int64 tensor on {device} with a row "
+                         "per seq_ids row")
+    if status is not None:
+        _check_list(fn, device, status=status)
+    _launch(fn, device, stream, page_table.data_ptr(), page_table.shape[1], lens.data_ptr(),
+            new_tokens.data_ptr(), batch, int(hold_back), free_pages.data_ptr(),
+            free_pages.numel(), cursor.data_ptr(), lens_after.data_ptr(), page_starts.data_ptr(),
+            row_starts.data_ptr(), seq_ids.data_ptr(), positions.data_ptr(), _ptr(slots), rows,
+            _ptr(status))
+
+
+def oscar_rope_phases(base: float, rotary_dim: int, factor: float = 1.0, original_len: int = 0,
+                      low_turns: float = 1.0, high_turns: float = 32.0) -> np.ndarray:
+    """Rotary frequencies of oscar_rope, uint64 [rotary_dim / 2] (turns per token times
+    2^64): unscaled, divided by `factor`, or (original_len > 0) scaled by parts."""
+    out = np.zeros(max(int(rotary_dim) // 2, 1), np.uint64)
+    _check("oscar_rope_phases",
+           lib().oscar_rope_phases(float(base), int(rotary_dim), float(factor), int(original_len),
+                                   float(low_turns), float(high_turns), _np_ptr(out)))
+    return out
+
+
+def oscar_rope(q, k, positions, phases, q_out=None, k_out=None, interleaved: bool = False,
+               amplitude: float = 1.0, inverse: bool = False, stream=None):
+    """Rotary embedding of q [n][Hq][d] and k [n][Hkv][d] (bf16, rows may be strided;
+    either may be None) at int32 positions [n] (negative: the row is left as it was).
+    phases: oscar_rope_phases' words on the device as int64 (or uint64) [rotary_dim / 2].
+    q_out, k_out: outputs, in place when None."""
+    import torch
+    fn = "oscar_rope"
+    some = q if q is not None else k
+    _need(some is not None and some.dim() == 3, fn, "q or k must be given, as [n][heads][d]")
+    device, (n, _, d) = some.device, some.shape
+    _need(device.type == "cuda", fn, "q and k must be on a CUDA device")
+    args = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            _need(y is None, fn, f"{name}_out without {name}")
+            args.append((0, 0, 0, None, None))
+            continue
+        y = x if y is None else y
+        heads = x.shape[1]
+        xs = _token_stride(fn, name, x, heads, d, device)
+        ys = xs if y is x else _token_stride(fn, name + "_out", y, heads, d, device)
+        _need(x.shape[0] == n and y.shape[0] == n, fn, "q, k and the outputs must have the same rows")
+        args.append((heads, xs, ys, x.data_ptr(), y.data_ptr()))
+    _check_list(fn, device, positions=positions)
+    _need(positions.numel() == n, fn, "positions must have an entry per row")
+    if (phases.dtype not in (torch.int64, torch.uint64) or phases.device != device
+            or not phases.is_contiguous()):
+        raise ValueError(f"{fn}: phases must be contiguous 64-bit integers on {device}")
+    (hq, qs, qos, qp, qop), (hk, ks, kos, kp, kop) = args
+    _launch(fn, device, stream, qp, kp, positions.data_ptr(), phases.data_ptr(), n, hq, hk, d,
+            2 * phases.numel(), int(interleaved), float(amplitude), int(inverse), qs, ks, qos, kos,
+            qop, kop)
 
 
 def oscar_device_sm_count() -> int:

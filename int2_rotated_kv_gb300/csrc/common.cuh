@@ -246,6 +246,9 @@ inline oscar_status check_desc(const oscar_cache_desc* c, bool needs_int2, bool 
 // 2-bit code planes of the cache: 1 (INT2) or 2 (the INT4 variant)
 inline int code_planes(const oscar_cache_desc* c) { return c->code_bits == 4 ? 2 : 1; }
 
+// Checks shared by the calls on the 8-bit cache (kv8_attention.cu).
+oscar_status check_kv8(const oscar_kv8_desc* c);
+
 int sm_count();
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (function, device).

@@ -1,0 +1,947 @@
+// Attention over the 8-bit cache (kv8_layout.cuh): decode and several query rows
+// per sequence, split over the context.
+//
+//   out[b][m][hq] = sum_t softmax_t(q . k_t / sqrt(d)) v_t,  t <= position of row m,
+// with k_t = code * s_K(page, head), v_t = code * s_V(page, head) for tokens in
+// whole pages and bf16 keys and values for the tokens of the tail.
+//
+// The codes go to the tensor cores as exact fp16 operands (two byte permutes per
+// four int8 codes, one conversion per two e4m3 codes), keys as the A operand of
+// q.K and values, transposed, as the A operand of p.V; 8 query columns (row, query
+// head) fill the N dimension and NT tiles of them share every unpacked code:
+//   logit = s_K * (sum_c (u_c - 128) q_c),  the -128 sum_c q_c as the initial
+//     accumulator (int8); q enters as fp16 scaled by a power of two per column,
+//     which keeps all 8 bits of every bf16 within 2^-21 of the column's largest.
+//   o += (p s_V) code,  p s_V rounded once to fp16 (2^-12 relative, unbiased) and
+//     weighed by 2^(6-E), E the exponent of the largest s_V so far.  int8 value
+//     codes lose their 128 before the MMA (one fp16 add per two codes): summed
+//     with it over hundreds of pages, the accumulator's truncation of sums of
+//     p s_V (code + 128) is a bias of 2e-3 of the output where values cancel.
+// Softmax statistics, accumulators and the merges are fp32.  Tail tokens are exact
+// in bf16 on the K side and use fp32 p on the V side.
+//
+// Work split.  The (sequence, tile of query columns, KV head) units, each a run of
+// pages, are laid end to end, and every CTA takes an equal share of the pages,
+// found from the lengths on the device: ragged batches finish together.  A CTA
+// whose share ends inside a unit leaves a partial (at most two per CTA, so the
+// workspace does not grow with the batch); a second kernel merges those units.
+// Within a CTA the eight warps take pages in turn, each through its own ring of
+// bulk copies, and merge through shared memory at a unit's end; the ring already
+// fills for the next unit meanwhile.
+//
+// Bound by HBM: 2d + 1 bytes per token and KV head.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "kv8_layout.cuh"
+
+namespace oscar {
+
+constexpr int kAWarps = 8;
+constexpr int kAThreads = 32 * kAWarps;
+constexpr int kMaxCtas = 1024;
+constexpr float kLowest = -3.402823466e38f;   // running maximum before the first logit
+constexpr float kLag = 8.f;                   // the maximum is raised when passed by 2^8
+
+struct Kv8Params {
+  int hkv, hq, G, max_pages;
+  int64_t n_pages, n_tails;
+  const uint8_t* pool;
+  const uint8_t* tail;
+  const int32_t* page_table;
+  const int32_t* tail_ids;
+  int32_t* status;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* seq_lens;
+  const int32_t* q_pos;    // null: one row per sequence, at its last token
+  int m_rows, cols, tiles, entries, max_len;   // cols = m_rows * G; entries = batch * tiles
+  int whole_units;         // one CTA per unit, no partials
+  float scale_log2;
+  int4* info;              // per CTA: unit entry, KV head, parts of the unit that starts in it
+  float* part;             // [2 * CTAs][8 * NT * (D + 2)]
+};
+
+template <int D, int NT>
+struct Kv8Cfg {
+  using F = Kv8Fmt<D>;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;             // per SM
+  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  static constexpr int kStride = D + 4;                     // floats per column when merging
+  static constexpr int kRing = kAWarps * kStages * F::kBlock;
+  static constexpr int kMerge = kAWarps * 8 * kStride * 4;
+  static constexpr int kStat = kAWarps * 8 * NT * 4;        // one of m, l
+  static constexpr int kTailOff = kRing;
+  static constexpr int kMergeOff = kTailOff + F::kTailBytes;
+  static constexpr int kStatOff = kMergeOff + kMerge;
+  static constexpr int kBarOff = kStatOff + 2 * kStat;
+  static constexpr int kBytes = kBarOff + (kAWarps * kStages + 1) * 8;
+  static constexpr int kSlot = 8 * NT * (D + 2);            // floats of one partial
+};
+
+// A sequence's tile of query columns: pages it has to visit (at least one, so that
+// a tile that sees nothing still writes its zeros).
+struct Entry {
+  int b, tile, len, vis, n8, pages;
+};
+
+__device__ __forceinline__ int row_limit(const Kv8Params& p, int b, int row, int len) {
+  const int pos = p.q_pos[static_cast<size_t>(b) * p.m_rows + row];
+  return pos >= 0 && pos < len ? pos + 1 : 0;
+}
+
+template <int NT>
+__device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
+  Entry t;
+  t.b = e / p.tiles;
+  t.tile = e - t.b * p.tiles;
+  const int len = p.seq_lens[t.b];
+  t.len = len >= 0 && len <= p.max_len ? len : 0;
+  if (p.q_pos) {
+    const int r0 = t.tile * 8 * NT / p.G;
+    const int r1 = min(p.cols - 1, t.tile * 8 * NT + 8 * NT - 1) / p.G;
+    t.vis = 0;
+    for (int r = r0; r <= r1; ++r) t.vis = max(t.vis, row_limit(p, t.b, r, t.len));
+  } else {
+    t.vis = t.len;
+  }
+  const int whole = t.len / kPage;
+  t.n8 = min(whole, (t.vis + kPage - 1) / kPage);
+  t.pages = max(1, t.n8 + (t.vis > whole * kPage ? 1 : 0));
+  return t;
+}
+
+// The columns of one unit as a lane sees them: operands for column gid of each
+// tile, factors and limits for columns 2tig and 2tig + 1.
+template <int D, int NT>
+struct Query {
+  uint32_t b[NT][D / 16][2];
+  float fac[NT][2];     // log2-domain logit per unit of q.code, before s_K
+  float init[NT][2];    // -128 sum q (int8)
+  int vis[NT][2];
+  int vis_min;          // smallest over the unit's columns
+};
+
+// First element of column `col` of the tile; null when the tile has fewer columns.
+__device__ __forceinline__ const uint16_t* column(const Kv8Params& p, const Entry& t, int h,
+                                                  int col, int D) {
+  if (col >= p.cols) return nullptr;
+  const int row = col / p.G, g = col - row * p.G;
+  return p.q + ((static_cast<size_t>(t.b) * p.m_rows + row) * p.hq + h * p.G + g) * D;
+}
+
+template <int D, int NT, bool kE4m3>
+__device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, int h, int lane,
+                                           Query<D, NT>& q) {
+  const int gid = lane >> 2, tig = lane & 3;
+  q.vis_min = 0x7fffffff;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = (t.tile * NT + nt) * 8 + gid;
+    const uint16_t* src = column(p, t, h, col, D);
+    int vis = 0x7fffffff;
+    if (src) vis = p.q_pos ? row_limit(p, t.b, col / p.G, t.len) : t.len;
+    uint4 raw[D / 32];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const uint4* s = reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig);
+      raw[2 * j] = src ? s[0] : make_uint4(0, 0, 0, 0);
+      raw[2 * j + 1] = src ? s[1] : make_uint4(0, 0, 0, 0);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo_value(w[x])), fabsf(bf16_hi_value(w[x]))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // the largest magnitude goes to [2^7, 2^8)
+    const int exponent = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
+    const int up = amax > 0.f ? max(-96, min(100, 7 - exponent)) : 0;
+    const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // four channels: one k-step of this lane
+        const float x0 = bf16_lo_value(w[2 * half]) * mul, x1 = bf16_hi_value(w[2 * half]) * mul;
+        const float x2 = bf16_lo_value(w[2 * half + 1]) * mul;
+        const float x3 = bf16_hi_value(w[2 * half + 1]) * mul;
+        // the pairs of kv8_operands
+        const uint32_t b0 = kE4m3 ? pack_half2(x0, x1) : pack_half2(x0, x2);
+        const uint32_t b1 = kE4m3 ? pack_half2(x2, x3) : pack_half2(x1, x3);
+        q.b[nt][2 * i + half][0] = b0;
+        q.b[nt][2 * i + half][1] = b1;
+        sum += (half_lo(b0) + half_hi(b0)) + (half_lo(b1) + half_hi(b1));
+      }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const float fac =
+        p.scale_log2 * __uint_as_float(static_cast<uint32_t>((kE4m3 ? 0 : 24) - up + 127) << 23);
+    const float init = kE4m3 ? 0.f : sum * (-128.f / 16777216.f);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      q.fac[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * tig + 4 * c);
+      q.init[nt][c] = __shfl_sync(0xffffffffu, init, 8 * tig + 4 * c);
+      q.vis[nt][c] = __shfl_sync(0xffffffffu, vis, 8 * tig + 4 * c);
+    }
+    q.vis_min = min(q.vis_min, __reduce_min_sync(0xffffffffu, vis));
+  }
+}
+
+// A warp's running result for its columns.  o: accumulator tiles, element
+// [2i + y][r + 2x] is channel 32i + 4gid + 2y + x of column 2tig + r.
+template <int D, int NT>
+struct Running {
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+  float vmax, vmul;      // power of two that no s_V so far exceeds, and 2^6 / vmax
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void reset(Running<D, NT>& s) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s.o[nt][i][0] = s.o[nt][i][1] = s.o[nt][i][2] = s.o[nt][i][3] = 0.f;
+    s.m[nt][0] = s.m[nt][1] = kLowest;
+    s.l[nt][0] = s.l[nt][1] = 0.f;
+  }
+  s.vmax = 9.62964972193618e-35f;   // 2^-113, below every scale but 0
+  s.vmul = 64.f / 9.62964972193618e-35f;
+}
+
+// Raises the running maxima where a logit passes one by more than kLag (so p <=
+// 2^kLag) and rescales; lg: rows gid, gid + 8 of the tile in the accumulator layout.
+template <int D, int NT>
+__device__ __forceinline__ void raise_max(Running<D, NT>& s, const float (&lg)[NT][4]) {
+  bool over = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) over |= fmaxf(lg[nt][c], lg[nt][2 + c]) > s.m[nt][c] + kLag;
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float top = fmaxf(lg[nt][c], lg[nt][2 + c]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        top = fmaxf(top, s.m[nt][c]);
+        const float a = top == s.m[nt][c] ? 1.f : fast_exp2(s.m[nt][c] - top);
+        s.m[nt][c] = top;
+        s.l[nt][c] *= a;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          s.o[nt][i][c] *= a;
+          s.o[nt][i][2 + c] *= a;
+        }
+      }
+    }
+  }
+}
+
+// One page of codes at `st`.  shown: false for a page id that was refused.
+template <int D, int NT, bool kE4m3>
+__device__ __forceinline__ void page(const uint8_t* st, int page0, bool shown, int lane,
+                                     const Query<D, NT>& q, Running<D, NT>& s) {
+  using F = Kv8Fmt<D>;
+  const int gid = lane >> 2;
+  const uint4* kb = reinterpret_cast<const uint4*>(st);
+  float lg[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    lg[nt][0] = lg[nt][2] = q.init[nt][0];
+    lg[nt][1] = lg[nt][3] = q.init[nt][1];
+  }
+  const float2 sc = *reinterpret_cast<const float2*>(st + F::kScales);
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const uint4 k0 = kb[(2 * j) * 32 + lane], k1 = kb[(2 * j + 1) * 32 + lane];
+    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t a0, a1, a2, a3;
+      kv8_operands<kE4m3>(w0[w], a0, a2);
+      kv8_operands<kE4m3>(w1[w], a1, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_f16(lg[nt], a0, a1, a2, a3, q.b[nt][4 * j + w][0], q.b[nt][4 * j + w][1]);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float f0 = sc.x * q.fac[nt][0], f1 = sc.x * q.fac[nt][1];
+    lg[nt][0] *= f0; lg[nt][1] *= f1; lg[nt][2] *= f0; lg[nt][3] *= f1;
+  }
+  if (!shown || page0 + kPage > q.vis_min) {
+    const int t = page0 + 2 * gid;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (!shown || t >= q.vis[nt][c]) lg[nt][c] = -INFINITY;
+        if (!shown || t + 1 >= q.vis[nt][c]) lg[nt][2 + c] = -INFINITY;
+      }
+  }
+  raise_max<D, NT>(s, lg);
+  if (sc.y > s.vmax) {   // a larger value scale than any page before (the warp's own, uniform)
+    const float up = __uint_as_float((__float_as_uint(sc.y) & 0x7f800000u) + 0x00800000u);
+    const float a = s.vmax / up;   // a power of two
+    s.vmax = up;
+    s.vmul *= a;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s.o[nt][i][r] *= a;
+  }
+  // 2^6 s_V / vmax: p s_V / vmax <= 2^8, so the fp16 weights stay below 2^14
+  const float vs = sc.y * s.vmul;
+  uint32_t b0[NT], b1[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float p0 = fast_exp2(lg[nt][0] - s.m[nt][0]), p1 = fast_exp2(lg[nt][1] - s.m[nt][1]);
+    const float p2 = fast_exp2(lg[nt][2] - s.m[nt][0]), p3 = fast_exp2(lg[nt][3] - s.m[nt][1]);
+    s.l[nt][0] += p0 + p2;
+    s.l[nt][1] += p1 + p3;
+    // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
+    // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
+    b0[nt] = movmatrix_trans(pack_half2(p0 * vs, p1 * vs));
+    b1[nt] = movmatrix_trans(pack_half2(p2 * vs, p3 * vs));
+    if constexpr (kE4m3) {   // pairs (4tig, 4tig + 1), (4tig + 2, 4tig + 3)
+      const uint32_t lo = __byte_perm(b0[nt], b1[nt], 0x5410);
+      b1[nt] = __byte_perm(b0[nt], b1[nt], 0x7632);
+      b0[nt] = lo;
+    }
+  }
+  const uint4* vb = reinterpret_cast<const uint4*>(st + F::kCodes);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 v = vb[i * 32 + lane];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      uint32_t a0, a1, a2, a3;
+      kv8_signed_operands<kE4m3>(w[2 * y], a0, a2);
+      kv8_signed_operands<kE4m3>(w[2 * y + 1], a1, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(s.o[nt][2 * i + y], a0, a1, a2, a3, b0[nt], b1[nt]);
+    }
+  }
+}
+
+// Brings the accumulators to the units of the values.
+template <int D, int NT, bool kE4m3>
+__device__ __forceinline__ void unscale(Running<D, NT>& s) {
+  // weights carried 2^6 / vmax, int8 codes 2^-24; two factors stay in range
+  const float up = kE4m3 ? 1.f / 64.f : 262144.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        s.o[nt][i][r] = s.o[nt][i][r] * up * s.vmax;
+}
+
+// The tail: n bf16 tokens from position page0 at `st`; accumulators already in the
+// units of the values.  At most 15 tokens once per unit: p.V in fp32 on the CUDA
+// cores, which also keeps a NaN or an infinity of a token that a row does not see
+// out of that row.
+template <int D, int NT>
+__device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uint8_t* st, int page0,
+                            int n, int lane, const Query<D, NT>& q, Running<D, NT>& s) {
+  using F = Kv8Fmt<D>;
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint4* kb = reinterpret_cast<const uint4*>(st);
+  float lg[NT][4] = {};
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const int c0 = ((2 * j) * 32 + lane) * 2, c1 = ((2 * j + 1) * 32 + lane) * 2;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {   // 8 channels: two k-steps
+      const uint4 k0 = kb[c0 + x], k1 = kb[c1 + x];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint16_t* src = column(p, t, h, (t.tile * NT + nt) * 8 + gid, D);
+        const uint4 qv = src ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig + 8 * x)
+                             : make_uint4(0, 0, 0, 0);
+        mma_bf16(lg[nt], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+        mma_bf16(lg[nt], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int seen = min(n, q.vis[nt][c] - page0);   // tokens of the tail this column sees
+      lg[nt][c] = 2 * gid < seen ? lg[nt][c] * p.scale_log2 : -INFINITY;
+      lg[nt][2 + c] = 2 * gid + 1 < seen ? lg[nt][2 + c] * p.scale_log2 : -INFINITY;
+    }
+  raise_max<D, NT>(s, lg);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lg[nt][r] = fast_exp2(lg[nt][r] - s.m[nt][r & 1]);
+    s.l[nt][0] += lg[nt][0] + lg[nt][2];
+    s.l[nt][1] += lg[nt][1] + lg[nt][3];
+  }
+  const uint16_t* vb = reinterpret_cast<const uint16_t*>(st) + F::kTailHalf;
+  for (int i = 0; i < n; ++i) {
+    float v[D / 16][2];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {   // the lane's channels 32 (c/4) + 4 gid + c%4
+      const int chunk = kv8_value_chunk(i >> 2, (c >> 2) * 8 + gid);
+      v[c >> 1][c & 1] = bf16_to_float(vb[chunk * 16 + 4 * (c & 3) + (i & 3)]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float w0 = __shfl_sync(0xffffffffu, (i & 1) ? lg[nt][2] : lg[nt][0], 4 * (i >> 1) + tig);
+      const float w1 = __shfl_sync(0xffffffffu, (i & 1) ? lg[nt][3] : lg[nt][1], 4 * (i >> 1) + tig);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        if (w0 != 0.f) {
+          s.o[nt][k][0] = fmaf(w0, v[k][0], s.o[nt][k][0]);
+          s.o[nt][k][2] = fmaf(w0, v[k][1], s.o[nt][k][2]);
+        }
+        if (w1 != 0.f) {
+          s.o[nt][k][1] = fmaf(w1, v[k][0], s.o[nt][k][1]);
+          s.o[nt][k][3] = fmaf(w1, v[k][1], s.o[nt][k][3]);
+        }
+      }
+    }
+  }
+}
+
+// A warp's ring of page copies: n_in issued, n_out consumed since the kernel's
+// start, so the phases run on from unit to unit.
+struct Ring {
+  uint32_t n_in, n_out, shown;   // shown: bit per stage, the page id was valid
+  int next_id;
+  bool alive;                    // false after a copy that did not arrive in time
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void issue(const Kv8Params& p, const Entry& t, int h, int pg, int end,
+                                      int warp, int lane, uint8_t* smem, uint64_t* bars, Ring& r) {
+  using C = Kv8Cfg<D, NT>;
+  const int s = r.n_in % C::kStages;
+  const bool ok = r.next_id >= 0 && r.next_id < p.n_pages;
+  r.shown = (r.shown & ~(1u << s)) | (static_cast<uint32_t>(ok) << s);
+  if (lane == 0) {
+    if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+    uint64_t* bar = bars + warp * C::kStages + s;
+    const int64_t block = static_cast<int64_t>(ok ? r.next_id : 0) * p.hkv + h;
+    mbar_arrive_expect_tx(bar, C::F::kBlock);
+    bulk_g2s(smem + (warp * C::kStages + s) * C::F::kBlock, p.pool + block * C::F::kBlock,
+             C::F::kBlock, bar);
+  }
+  ++r.n_in;
+  if (pg + kAWarps < end)
+    r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + pg + kAWarps];
+}
+
+// Starts the copies of a warp's first pages of a unit.
+template <int D, int NT>
+__device__ __forceinline__ void start_unit(const Kv8Params& p, const Entry& t, int h, int first,
+                                           int end, int warp, int lane, uint8_t* smem,
+                                           uint64_t* bars, Ring& r) {
+  if (first >= end || !r.alive) return;
+  r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + first];
+#pragma unroll
+  for (int i = 0; i < Kv8Cfg<D, NT>::kStages; ++i)
+    if (first + i * kAWarps < end)
+      issue<D, NT>(p, t, h, first + i * kAWarps, end, warp, lane, smem, bars, r);
+}
+
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kAWarps; ++w) total += scratch[w];
+  __syncthreads();
+  return total;
+}
+
+// The entry that holds page `at` of the entries laid end to end (each weighed by
+// the KV heads), and the pages before it.
+template <int NT>
+__device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int& entry,
+                           int64_t& before) {
+  __shared__ int found;
+  __shared__ int64_t found_before;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  if (tid == 0) found = -1;
+  __syncthreads();
+  for (int e0 = 0; e0 < p.entries; e0 += kAThreads) {
+    const int e = e0 + tid;
+    const int64_t v = e < p.entries ? static_cast<int64_t>(entry_of<NT>(p, e).pages) * p.hkv : 0;
+    int64_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int64_t off = base, all = base;
+#pragma unroll
+    for (int w = 0; w < kAWarps; ++w) {
+      if (w < warp) off += scratch[w];
+      all += scratch[w];
+    }
+    incl += off;
+    if (v > 0 && incl - v <= at && at < incl) {
+      found = e;
+      found_before = incl - v;
+    }
+    __syncthreads();
+    if (found >= 0) break;
+    base = all;
+  }
+  entry = found;
+  before = found_before;
+}
+
+template <int D, int NT, bool kE4m3>
+__global__ void __launch_bounds__(kAThreads, (Kv8Cfg<D, NT>::kCtas))
+kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
+  using C = Kv8Cfg<D, NT>;
+  using F = Kv8Fmt<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scratch[kAWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* tail_bar = bars + kAWarps * C::kStages;
+  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff);
+  float* sm_l = sm_m + kAWarps * 8 * NT;
+  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff);
+  if (tid <= kAWarps * C::kStages) mbar_init(bars + tid, 1);
+  fence_mbar_init();
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  // this CTA's pages [at, end) of all units laid end to end, and its first unit
+  int e = 0, h = 0;
+  int64_t at = 0, end = 0, share = 0, unit0 = 0;   // unit0: first page of the current unit
+  Entry t;
+  if (p.whole_units) {
+    e = blockIdx.x / p.hkv;
+    h = blockIdx.x - e * p.hkv;
+    t = entry_of<NT>(p, e);
+    end = share = t.pages;
+  } else {
+    int64_t sum = 0;
+    if (p.entries == 1) {
+      t = entry_of<NT>(p, 0);
+      sum = t.pages;
+    } else {
+      for (int i = tid; i < p.entries; i += kAThreads) sum += entry_of<NT>(p, i).pages;
+      sum = block_sum(sum, scratch);
+    }
+    const int64_t total = sum * p.hkv;
+    share = max(static_cast<int64_t>(min_share), (total + gridDim.x - 1) / gridDim.x);
+    at = blockIdx.x * share;
+    end = min(total, at + share);
+    if (at >= end) {
+      if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    int64_t before = 0;
+    if (p.entries > 1) {
+      find_entry<NT>(p, at, scratch, e, before);
+      t = entry_of<NT>(p, e);
+    }
+    h = static_cast<int>((at - before) / t.pages);
+    unit0 = before + static_cast<int64_t>(h) * t.pages;
+  }
+
+  Ring ring{0, 0, 0, 0, true};
+  uint32_t tails = 0;           // tail copies so far: the barrier's phase
+  int4 owned = make_int4(0, 0, 0, 0);
+  // the tail copy of a unit; by thread 0, after every reader of the one before
+  auto start_tail = [&](const Entry& t, int h, int64_t unit0) -> bool {
+    const int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
+    if (p1 <= t.n8 || t.vis <= t.len / kPage * kPage) return false;   // not this CTA's, or none
+    const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
+    const bool ok = id >= 0 && id < p.n_tails;
+    if (tid == 0) {
+      if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+      mbar_arrive_expect_tx(tail_bar, F::kTailBytes);
+      bulk_g2s(smem + C::kTailOff, p.tail + ((ok ? id : 0) * p.hkv + h) * F::kTailBytes,
+               F::kTailBytes, tail_bar);
+    }
+    return ok;
+  };
+  auto has_tail = [&](const Entry& t, int p1) {
+    return p1 > t.n8 && t.vis > t.len / kPage * kPage;
+  };
+  int p0 = static_cast<int>(at - unit0);
+  int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
+  start_unit<D, NT>(p, t, h, p0 + warp, min(p1, t.n8), warp, lane, smem, bars, ring);
+  bool tail_ok = start_tail(t, h, unit0);
+
+  for (;;) {
+    Query<D, NT> q;
+    load_query<D, NT, kE4m3>(p, t, h, lane, q);
+    Running<D, NT> s;
+    reset<D, NT>(s);
+    if (p0 == 0 && h == 0 && t.tile == 0 && tid == 0 && p.status) {
+      const int len = p.seq_lens[t.b];
+      if (len < 0 || len > p.max_len) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+    }
+    if (p.q_pos && p0 == 0 && h == 0 && tid < 8 * NT && p.status) {
+      const int row = (t.tile * 8 * NT + tid) / p.G;
+      if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
+        atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+    }
+    const int end8 = min(p1, t.n8);
+    for (int pg = p0 + warp; pg < end8 && ring.alive; pg += kAWarps) {
+      const int st = ring.n_out % C::kStages;
+      const bool got = mbar_wait(bars + warp * C::kStages + st, (ring.n_out / C::kStages) & 1,
+                                 p.status);
+      ++ring.n_out;
+      if (!__all_sync(0xffffffffu, got)) {   // leave no copy in flight, then stop reading pages
+        for (; ring.n_out < ring.n_in; ++ring.n_out)
+          mbar_wait(bars + warp * C::kStages + ring.n_out % C::kStages,
+                    (ring.n_out / C::kStages) & 1, p.status);
+        ring.alive = false;
+        break;
+      }
+      page<D, NT, kE4m3>(smem + (warp * C::kStages + st) * F::kBlock, pg * kPage,
+                         (ring.shown >> st) & 1u, lane, q, s);
+      __syncwarp();
+      if (pg + C::kStages * kAWarps < end8)
+        issue<D, NT>(p, t, h, pg + C::kStages * kAWarps, end8, warp, lane, smem, bars, ring);
+    }
+    unscale<D, NT, kE4m3>(s);
+    const bool tail_here = has_tail(t, p1);
+    if (tail_here && warp == (t.n8 - p0) % kAWarps) {
+      const bool got = mbar_wait(tail_bar, tails & 1, p.status);
+      if (__all_sync(0xffffffffu, got) && tail_ok)
+        tail_tokens<D, NT>(p, t, h, smem + C::kTailOff, t.len / kPage * kPage, t.len % kPage, lane,
+                           q, s);
+    }
+    tails += tail_here;
+
+    // the next unit of this CTA: its copies start before this one is merged
+    const Entry tc = t;
+    const int hc = h, c0 = p0, c1 = p1;
+    const int64_t u0 = unit0;
+    const bool more = u0 + c1 < end;
+    if (more) {
+      unit0 = u0 + tc.pages;
+      if (++h == p.hkv) {
+        h = 0;
+        t = entry_of<NT>(p, ++e);
+      }
+      p0 = 0;
+      p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
+      start_unit<D, NT>(p, t, h, warp, min(p1, t.n8), warp, lane, smem, bars, ring);
+    }
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = s.l[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (gid == 0) {
+          sm_m[(warp * NT + nt) * 8 + 2 * tig + c] = s.m[nt][c];
+          sm_l[(warp * NT + nt) * 8 + 2 * tig + c] = l;
+        }
+      }
+    __syncthreads();
+    if (more) tail_ok = start_tail(t, h, unit0);
+    const bool complete = c0 == 0 && c1 == tc.pages;
+    float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * C::kSlot;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float top = kLowest;
+#pragma unroll
+        for (int w = 0; w < kAWarps; ++w) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + 2 * tig + c]);
+        const float a = fast_exp2(s.m[nt][c] - top);
+        float* dst = merge + (warp * 8 + 2 * tig + c) * C::kStride + 4 * gid;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          *reinterpret_cast<float4*>(dst + 32 * i) =
+              make_float4(s.o[nt][2 * i][c] * a, s.o[nt][2 * i][2 + c] * a,
+                          s.o[nt][2 * i + 1][c] * a, s.o[nt][2 * i + 1][2 + c] * a);
+      }
+      __syncthreads();
+      if (tid < 8 * D / 4) {
+        const int col = tid / (D / 4), ch = 4 * (tid % (D / 4));
+        float top = kLowest, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAWarps; ++w) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + col]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAWarps; ++w) {
+          l = fmaf(sm_l[(w * NT + nt) * 8 + col], fast_exp2(sm_m[(w * NT + nt) * 8 + col] - top), l);
+          const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
+          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
+        const int gcol = (tc.tile * NT + nt) * 8 + col;
+        if (complete) {
+          if (gcol < p.cols) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zeros
+            const int row = gcol / p.G, g = gcol - row * p.G;
+            uint16_t* dst = p.out +
+                ((static_cast<size_t>(tc.b) * p.m_rows + row) * p.hq + hc * p.G + g) * D + ch;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
+          }
+        } else if (gcol < p.cols) {
+          *reinterpret_cast<float4*>(slot + (nt * 8 + col) * D + ch) = o;
+          if (ch == 0)
+            *reinterpret_cast<float2*>(slot + 8 * NT * D + 2 * (nt * 8 + col)) = make_float2(top, l);
+        }
+      }
+      __syncthreads();
+    }
+    if (!complete && c0 == 0)   // the unit goes on in the next CTAs: they hold its other parts
+      owned = make_int4(e, hc, static_cast<int>((u0 + tc.pages - 1) / share) - blockIdx.x + 1, 0);
+    if (!more) break;
+  }
+  if (tid == 0 && !p.whole_units) p.info[blockIdx.x] = owned;
+}
+
+// Merges the units that lie in several CTAs: block (CTA in which the unit starts,
+// column), thread = channel.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
+  using C = Kv8Cfg<D, NT>;
+  __shared__ float w[kMaxCtas];
+  __shared__ float red[D / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int4 own = p.info[blockIdx.x];
+  const int n = own.z;
+  const int b = own.x / p.tiles, tile = own.x - b * p.tiles;
+  const int col = blockIdx.y, gcol = tile * 8 * NT + col;
+  if (n == 0 || gcol >= p.cols) return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
+  auto slot = [&](int j) {
+    const size_t cta = blockIdx.x + static_cast<size_t>(j);
+    return p.part + (2 * cta + (j == 0 ? 1 : 0)) * C::kSlot;
+  };
+  float top = kLowest;
+  for (int j = tid; j < n; j += D) top = fmaxf(top, slot(j)[8 * NT * D + 2 * col]);
+  top = warp_max(top);
+  if (lane == 0) red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) top = fmaxf(top, red[i]);
+  __syncthreads();
+  float l = 0.f;
+  for (int j = tid; j < n; j += D) {
+    const float2 ml = *reinterpret_cast<const float2*>(slot(j) + 8 * NT * D + 2 * col);
+    const float a = fast_exp2(ml.x - top);
+    w[j] = a;
+    l = fmaf(a, ml.y, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) l += red[i];
+  float acc = w[0] * slot(0)[col * D + tid];
+  const float* next = slot(1) + col * D + tid;
+#pragma unroll 8
+  for (int j = 1; j < n; ++j) {
+    acc = fmaf(w[j], *next, acc);
+    next += 2 * C::kSlot;
+  }
+  const int row = gcol / p.G, g = gcol - row * p.G;
+  const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+  p.out[((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + tid] =
+      __bfloat16_as_ushort(y);
+}
+
+template <typename Kern, typename... Args>
+cudaError_t launch_kv8(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Query columns of a unit in tiles of 8: 1, 2 or 4, the fewest that hold a KV
+// head's columns (a wider unit reads its pages once for all of them).
+inline int column_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+
+constexpr int kWholePages = 64;   // see kv8_plan
+constexpr int kMinShare = 8;      // pages of a CTA: one per warp
+
+struct Kv8Plan {
+  int nt;
+  bool whole;
+  int64_t tiles, entries, ctas;
+  size_t info, total;   // workspace bytes: the CTAs' records, all
+};
+
+// false: sizes outside the supported range.
+inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int64_t max_len,
+                     Kv8Plan* out) {
+  Kv8Plan p{};
+  const int64_t cols = m_rows * (c->num_q_heads / c->num_kv_heads);
+  p.nt = column_tiles(cols);
+  p.tiles = (cols + 8 * p.nt - 1) / (8 * p.nt);
+  p.entries = batch * p.tiles;
+  if (cols > (1 << 30) || p.entries > (1 << 30) || p.entries * c->num_kv_heads > 0x7fffffff)
+    return false;
+  const int64_t units = p.entries * c->num_kv_heads;
+  const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);
+  const int64_t resident =
+      std::min<int64_t>(kMaxCtas, oscar_host::sm_count() * static_cast<int64_t>(p.nt == 1 ? 2 : 1));
+  p.whole = pages <= kWholePages && units <= resident;
+  p.ctas = p.whole ? units : std::min(resident, (units * pages + kMinShare - 1) / kMinShare);
+  const int d = c->head_dim;
+  p.info = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
+  p.total = p.whole ? 16
+                    : p.info + static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (d + 2) * sizeof(float);
+  *out = p;
+  return true;
+}
+
+template <int D, int NT, bool kE4m3>
+oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
+  using C = Kv8Cfg<D, NT>;
+  const auto kernel = kv8_attention_kernel<D, NT, kE4m3>;
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes))
+    return OSCAR_ERR_CUDA;
+  if (launch_kv8(kernel, dim3(static_cast<unsigned>(pl.ctas)), dim3(kAThreads), C::kBytes, st, p,
+                 kMinShare) != cudaSuccess)
+    return OSCAR_ERR_CUDA;
+  if (!pl.whole &&
+      launch_kv8(kv8_merge_kernel<D, NT>,
+                 dim3(static_cast<unsigned>(pl.ctas), static_cast<unsigned>(std::min(p.cols, 8 * NT))),
+                 dim3(D), 0, st, p) != cudaSuccess)
+    return OSCAR_ERR_CUDA;
+  return OSCAR_OK;
+}
+
+template <int D, bool kE4m3>
+oscar_status run_kv8_nt(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
+  return pl.nt == 1   ? run_kv8<D, 1, kE4m3>(p, pl, st)
+         : pl.nt == 2 ? run_kv8<D, 2, kE4m3>(p, pl, st)
+                      : run_kv8<D, 4, kE4m3>(p, pl, st);
+}
+
+}  // namespace oscar
+
+namespace oscar_host {
+
+oscar_status check_kv8(const oscar_kv8_desc* c) {
+  if (!c) return OSCAR_ERR_INVALID_ARG;
+  if (c->num_kv_heads < 1 || c->num_q_heads < 1 || c->max_pages_per_seq < 1 || c->num_pages < 1 ||
+      c->num_tails < 1)
+    return OSCAR_ERR_INVALID_ARG;
+  if (!head_dim_ok(c->head_dim)) return OSCAR_ERR_UNSUPPORTED;
+  if (c->format != OSCAR_KV8_INT8 && c->format != OSCAR_KV8_E4M3) return OSCAR_ERR_UNSUPPORTED;
+  if (c->num_q_heads % c->num_kv_heads) return OSCAR_ERR_INVALID_ARG;
+  if (!c->pool || !c->tail || !c->page_table) return OSCAR_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->pool) | reinterpret_cast<uintptr_t>(c->tail)) & 15)
+    return OSCAR_ERR_INVALID_ARG;
+  return OSCAR_OK;
+}
+
+}  // namespace oscar_host
+
+using namespace oscar;
+
+extern "C" {
+
+size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows,
+                                int32_t max_seq_len) {
+  Kv8Plan pl;
+  if (oscar_host::check_kv8(desc) != OSCAR_OK || batch < 1 || m_rows < 1 || max_seq_len < 1 ||
+      !kv8_plan(desc, batch, m_rows, max_seq_len, &pl))
+    return 0;
+  return pl.total;
+}
+
+oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
+                                 const int32_t* q_pos, int32_t batch, int32_t m_rows,
+                                 int32_t max_seq_len, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const oscar_status s = oscar_host::check_kv8(desc);
+  if (s != OSCAR_OK) return s;
+  if (batch < 0 || m_rows < 0 || max_seq_len < 1 || (!q_pos && m_rows > 1))
+    return OSCAR_ERR_INVALID_ARG;
+  if (batch == 0 || m_rows == 0) return OSCAR_OK;
+  if (!q || !seq_lens || !out || !workspace) return OSCAR_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(workspace)) & 15)
+    return OSCAR_ERR_INVALID_ARG;
+  // whole pages go through the table, the last tokens through the tail
+  if (max_seq_len > static_cast<int64_t>(desc->max_pages_per_seq) * kPage + kPage - 1)
+    return OSCAR_ERR_INVALID_ARG;
+  Kv8Plan pl;
+  if (!kv8_plan(desc, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
+  if (workspace_bytes < pl.total) return OSCAR_ERR_WORKSPACE;
+  Kv8Params p{};
+  p.hkv = desc->num_kv_heads;
+  p.hq = desc->num_q_heads;
+  p.G = p.hq / p.hkv;
+  p.max_pages = desc->max_pages_per_seq;
+  p.n_pages = desc->num_pages;
+  p.n_tails = desc->num_tails;
+  p.pool = static_cast<const uint8_t*>(desc->pool);
+  p.tail = static_cast<const uint8_t*>(desc->tail);
+  p.page_table = desc->page_table;
+  p.tail_ids = desc->tail_ids;
+  p.status = desc->status;
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.seq_lens = seq_lens;
+  p.q_pos = q_pos;
+  p.m_rows = m_rows;
+  p.cols = m_rows * p.G;
+  p.tiles = static_cast<int>(pl.tiles);
+  p.entries = static_cast<int>(pl.entries);
+  p.max_len = max_seq_len;
+  p.whole_units = pl.whole ? 1 : 0;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(desc->head_dim)));
+  p.info = static_cast<int4*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.info);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = desc->format == OSCAR_KV8_E4M3;
+  if (desc->head_dim == 128)
+    return e4m3 ? run_kv8_nt<128, true>(p, pl, st) : run_kv8_nt<128, false>(p, pl, st);
+  return e4m3 ? run_kv8_nt<64, true>(p, pl, st) : run_kv8_nt<64, false>(p, pl, st);
+}
+
+}  // extern "C"

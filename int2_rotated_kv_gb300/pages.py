@@ -117,3 +117,27 @@ def allocate(pp: PagePlan, *, hkv: int, hq: int, d: int, sink: int, window: int,
                  t(r_k, torch.float32), t(r_v, torch.float32), t(clip_k, torch.float32),
                  t(clip_v, torch.float32),
                  torch.zeros(1, dtype=torch.int32, device=dev) if with_status else None, code_bits)
+
+
+def kv8_bytes_per_page(hkv: int, d: int) -> int:
+    """Pool bytes of one page of the 8-bit cache: codes of 16 keys and 16 values and
+    two fp32 scales (and 8 spare bytes) per KV head."""
+    return hkv * (32 * d + 16)
+
+
+def allocate_kv8(num_pages: int, batch: int, max_pages: int, *, hkv: int, hq: int, d: int, device,
+                 fmt: int = 0, num_tails: int | None = None, with_status: bool = True):
+    """Zeroed pools of an 8-bit cache and an empty page table (all -1) for `batch`
+    sequences; returns a binding ``Kv8Cache``.  ``oscar_extend_pages`` with
+    hold_back 15 fills the table."""
+    import torch
+
+    from ._lib import Kv8Cache
+    dev = torch.device(device)
+    return Kv8Cache(
+        hkv, hq, d,
+        torch.zeros((num_pages, hkv, 32 * d + 16), dtype=torch.uint8, device=dev),
+        torch.zeros((batch if num_tails is None else num_tails, hkv, 2, 16 * d),
+                    dtype=torch.bfloat16, device=dev),
+        torch.full((batch, max_pages), -1, dtype=torch.int32, device=dev), fmt,
+        None, torch.zeros(1, dtype=torch.int32, device=dev) if with_status else None)

@@ -26,6 +26,8 @@ Modules
   cache      expected page-pool contents for prefill and decode-append.
   attention  softmax attention over the mixed BF16 / INT2 cache, by the plain
              definition (reconstruct keys and values, then attend).
+  kv8        the 8-bit cache: block codes and layout, attention over the values
+             they stand for, page bookkeeping of a step, rotary embedding.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test against
 closed forms, textbook cases, library routines or brute force, except the

@@ -1,0 +1,336 @@
+"""GPU parity of the 8-bit cache: placement byte for byte, reading back, attention of
+one and several rows, against the fp64 oracle; and what the calls refuse or report."""
+import numpy as np
+import pytest
+
+import gpu_harness as H
+import kv8_harness as K
+from int2_rotated_kv_gb300 import synth
+from oracle import kv8
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [kv8.INT8, kv8.E4M3]
+
+
+# ---------------------------------------------------------------------- placing
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 3), (128, 8), (64, 5)])
+def test_placing_in_any_pieces_gives_the_same_pages(fmt, d, hkv):
+    """Prompts, chunks that start and end inside pages, single tokens, sequences that
+    rest: pages and tails byte for byte after every call."""
+    s = K.Sequences(5, hkv, hkv, d, fmt, 140, seed=d + hkv + fmt, permute_tails=hkv == 3)
+    for new in ([1, 0, 15, 16, 17], [1, 5, 1, 1, 31], [16, 11, 0, 47, 1], [13, 1, 33, 2, 0],
+                [1, 1, 1, 1, 1], [20, 0, 15, 3, 40]):
+        s.place(new, packed=hkv == 8)
+        s.check_pools()
+    assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_placing_special_values(fmt):
+    """Zero and tiny blocks, the largest and smallest bf16 values, NaN and infinities."""
+    d, hkv = 64, 1
+    s = K.Sequences(1, hkv, hkv, d, fmt, 200)
+    k, v = K.draw(s.rng, 16 * 9 + 5, hkv, d)
+    big = float(synth.bf16_from_bits(np.array([0x7F7F], np.uint16))[0])
+    k[0:16] = 0.0
+    k[16:32] = synth.bf16_round(np.full((16, 1, d), 2.0 ** -101, np.float32))
+    k[32:48] = 2.0 ** -100
+    k[48] = big
+    v[48:64] *= np.float32(2.0 ** -90)
+    v[0, 0, 0] = -big
+    k[64, 0, 3], k[65, 0, 4], k[66, 0, 5] = np.nan, np.inf, -np.inf
+    v[80:96] = np.nan
+    v[96:112] = np.inf
+    v[97, 0, 1] = -1e-39          # a subnormal, and nothing else that is finite
+    k[112:128, 0] = np.linspace(-1, 1, 16 * d).reshape(16, d)
+    k[112:128] = synth.bf16_round(k[112:128])
+    k[148, 0, 0] = np.nan         # stays in the tail as it is
+    s.place([16 * 9 + 5], k, v)
+    s.check_pools()
+    assert H.status(s.cache) == H.lib().DEVERR_NONFINITE
+
+
+def test_rows_behind_the_last_sequence_and_other_streams():
+    """Rows that belong to no sequence are not read; a call on another stream."""
+    t = H.torch()
+    s = K.Sequences(3, 2, 2, 128, kv8.INT8, 100)
+    stream = t.cuda.Stream()
+    stream.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(stream):
+        s.place([33, 0, 20], extra_rows=7)
+    s.place([1, 2, 0], stream=stream, max_new=50)
+    stream.synchronize()
+    s.check_pools()
+
+
+def test_placing_reports_what_it_skips():
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(2, 1, 1, 64, kv8.INT8, 64)
+    s.place([10, 20])
+    k, v = (H.bf16_tensor(x) for x in K.draw(s.rng, 30, 1, 64))
+
+    def call(lens, starts, max_new):
+        L.oscar_kv8_place(s.cache, k, v, s.i32(lens), s.i32(starts), max_new)
+        st = H.status(s.cache)
+        s.cache.status.zero_()
+        return st
+
+    assert call([10, 20], [0, 9, 9], 8) == L.DEVERR_SEQ_LEN          # more rows than max_new
+    assert call([10, 20], [0, 0, 31], 64) == L.DEVERR_SEQ_LEN        # rows behind the tensors
+    assert call([10, 20], [5, 0, 0], 64) == L.DEVERR_SEQ_LEN         # descending
+    assert call([-1, 20], [0, 4, 4], 64) == L.DEVERR_SEQ_LEN
+    assert call([70, 20], [0, 16, 16], 64) == L.DEVERR_SEQ_LEN       # behind the page table
+    s.cache.page_table[0, 0] = -1
+    s.cache.page_table[1, 1] = s.cache.pool.shape[0]
+    assert call([0, 20], [0, 16, 28], 64) == L.DEVERR_PAGE_ID
+    s.cache.page_table.copy_(t.from_numpy(s.table))
+    s.cache.tail_ids = s.i32([-1, s.cache.tail.shape[0]])
+    assert call([10, 20], [0, 3, 6], 64) == L.DEVERR_PAGE_ID
+    s.cache.tail_ids = None
+    s.check_pools()                                                   # none of it wrote anything
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,hkv", [(64, 2), (128, 3)])
+def test_gather(fmt, d, hkv):
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(4, hkv, hkv, d, fmt, 120, seed=7)
+    s.place([100, 0, 31, 64])
+    first, count = np.array([3, 0, 30, 16]), np.array([97, 0, 1, 33])
+    starts = np.concatenate([[0], np.cumsum(count)])
+    n = starts[-1]
+    ko, vo = (t.full((n + 2, hkv, d), 7.0, dtype=t.bfloat16, device=H.DEV) for _ in range(2))
+    L.oscar_kv8_gather(s.cache, s.i32(s.lens), s.i32(first), s.i32(starts), 97, ko, vo)
+    t.cuda.synchronize()
+    for kv, out in enumerate((ko, vo)):
+        got = out.float().cpu().numpy()
+        assert (got[n:] == 7).all()
+        for b in range(4):
+            for h in range(hkv):
+                y = s.stored(b, h)[kv][first[b]:first[b] + count[b]].astype(np.float32)
+                np.testing.assert_array_equal(got[starts[b]:starts[b + 1], h], synth.bf16_round(y))
+    assert H.status(s.cache) == 0
+    ko.fill_(7.0)
+    L.oscar_kv8_gather(s.cache, s.i32(s.lens), s.i32([4, 0, 0, 0]), s.i32(starts), 97, ko, vo)
+    assert H.status(s.cache) == L.DEVERR_SEQ_LEN                      # 4 + 97 > 100 tokens
+    assert (ko[:97] == 7).all()
+
+
+# -------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,hkv,g", [(64, 1, 4), (128, 2, 1), (128, 2, 4), (64, 3, 3), (128, 1, 8),
+                                     (128, 1, 16), (64, 1, 40)])
+def test_decode_matches_oracle(fmt, d, hkv, g):
+    """Ragged lengths, with none, one token, and ends on and beside page borders."""
+    lens = [0, 1, 15, 16, 17, 33, 700, 2607, 1024]
+    s = K.Sequences(len(lens), hkv, hkv * g, d, fmt, 2700, seed=g)
+    s.place(lens)
+    q = K.queries(s.rng, len(lens), 1, hkv * g, d)
+    got = s.attend(q)
+    s.check_attention(got, q)
+    assert H.status(s.cache) == 0
+    # fewer tokens than placed pages hold: whole pages are read from the pool all the same
+    short = np.array([0, 1, 15, 16, 16, 32, 688, 1600, 1008])
+    s2 = s.attend(q, lens=short)
+    for b in (4, 5, 6, 7, 8):
+        one = np.zeros_like(short)
+        one[b] = short[b]
+        s.check_attention(s2, q, lens=one, heads={(b, h) for h in range(hkv)})
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,hkv,g,m", [(64, 1, 4, 2), (128, 2, 4, 3), (128, 1, 1, 11), (128, 2, 4, 9),
+                                       (64, 2, 8, 5), (128, 1, 3, 37)])
+def test_rows_match_oracle(fmt, d, hkv, g, m):
+    """Several rows: the last positions, positions all over the context in no order,
+    rows that see nothing, and rows behind the end (zeros, reported)."""
+    lens = [40, 0, 555, 1700]
+    s = K.Sequences(4, hkv, hkv * g, d, fmt, 1800, seed=m)
+    s.place(lens)
+    q = K.queries(s.rng, 4, m, hkv * g, d)
+    pos = np.array([[L - m + i if L >= m else i for i in range(m)] for L in lens])
+    pos[1] = -1
+    pos[2] = s.rng.integers(0, 555, m)
+    pos[2, 0], pos[2, 1] = 0, -5
+    got = s.attend(q, pos)
+    s.check_attention(got, q, pos)
+    assert (got[1] == 0).all() and (got[2, 1] == 0).all()
+    assert H.status(s.cache) == 0
+    pos[3, 0] = 1700
+    got = s.attend(q, pos)
+    assert (got[3, 0] == 0).all() and H.status(s.cache) == H.lib().DEVERR_SEQ_LEN
+    s.check_attention(got, q, pos)
+
+
+@pytest.mark.parametrize("fmt,hkv,g", [(kv8.INT8, 8, 4), (kv8.E4M3, 2, 8)])
+def test_long_context(fmt, hkv, g):
+    """One sequence over every CTA of the grid."""
+    n = 40013
+    s = K.Sequences(1, hkv, hkv * g, 128, fmt, n, seed=3)
+    s.place([n])
+    q = K.queries(s.rng, 1, 1, hkv * g, 128)
+    got = s.attend(q)
+    s.check_attention(got, q, heads={(0, 0), (0, hkv - 1)})
+
+
+def test_many_short_sequences():
+    """More units than CTAs: several units per CTA, units over CTA borders."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 120, 300)
+    s = K.Sequences(300, 4, 8, 64, kv8.INT8, 120, seed=5)
+    s.place(lens)
+    q = K.queries(s.rng, 300, 1, 8, 64)
+    got = s.attend(q, max_len=120)
+    s.check_attention(got, q)
+    got2 = s.attend(q, max_len=120 + 7)          # another max_len: other shares, no other results
+    s.check_attention(got2, q)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_scales_of_values_and_queries(fmt):
+    """Value scales that differ by 2^20 from page to page, in both directions; queries from
+    1e-20 to 1e4 (logits to saturation)."""
+    s = K.Sequences(2, 1, 4, 128, fmt, 1500, seed=9)
+    k, v = K.draw(s.rng, 1500 + 900, 1, 128)
+    grow = np.exp2(np.arange(1500) // 16 % 41 - 20.0)[:, None, None].astype(np.float32)
+    v[:1500] *= grow
+    v[1500:] /= grow[:900]
+    s.place([1500, 900], k, v)
+    for scale in (1e-20, 1.0, 1e4):
+        q = K.queries(s.rng, 2, 1, 4, 128, scale)
+        s.check_attention(s.attend(q), q)
+    s.check_pools()
+
+
+def test_a_token_that_a_row_does_not_see_does_not_reach_it():
+    """NaN and infinity in the tail: rows before them keep finite outputs, rows behind
+    them get what the softmax gives."""
+    s = K.Sequences(1, 1, 2, 64, kv8.INT8, 100)
+    k, v = K.draw(s.rng, 90, 1, 64)
+    v[85, 0, 7], v[86, 0, 9], k[88, 0, 3] = np.nan, np.inf, np.nan
+    s.place([90], k, v)
+    pos = np.array([[79, 84, 85, 86, 87, 88, 89, 80, -1]])
+    q = K.queries(s.rng, 1, 9, 2, 64)
+    got = s.attend(q, pos)
+    assert np.isfinite(got[0, [0, 1, 7, 8]]).all()
+    assert np.isnan(got[0, 2, :, 7]).all() and np.isfinite(np.delete(got[0, 2], 7, -1)).all()
+    assert np.isinf(got[0, 3, :, 9]).all() and np.isnan(got[0, 5]).all()
+    finite = np.array([[79, 84, -1, -1, -1, -1, -1, 80, -1]])
+    clean = got.copy()
+    clean[0, 2:7] = 0
+    s.check_attention(clean, q, finite)
+
+
+def test_queries_that_are_not_finite():
+    s = K.Sequences(2, 1, 4, 64, kv8.INT8, 100)
+    s.place([70, 50])
+    q = K.queries(s.rng, 2, 1, 4, 64)
+    q[0, 0, 1, 5] = np.nan
+    q[0, 0, 2] = 0.0
+    got = s.attend(q)
+    assert np.isnan(got[0, 0, 1]).all()
+    rest = got.copy()
+    q[0, 0, 1, 5] = 0.0
+    rest[0, 0, 1] = s.attend(q)[0, 0, 1]
+    s.check_attention(rest, q)
+
+
+def test_bad_pages_and_lengths_are_reported_and_left_out():
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(2, 2, 4, 128, kv8.E4M3, 400)
+    s.place([390, 100])
+    q = K.queries(s.rng, 2, 1, 4, 128)
+    good = s.attend(q)
+    s.cache.page_table[0, 3] = -1
+    s.cache.page_table[0, 9] = s.cache.pool.shape[0]
+    got = s.attend(q)
+    assert H.status(s.cache) == L.DEVERR_PAGE_ID
+    s.check_attention(got, q, drop=(3, 9), heads={(0, 0), (0, 1)})
+    np.testing.assert_array_equal(got[1], good[1])
+    s.cache.page_table.copy_(t.from_numpy(s.table))
+    s.cache.status.zero_()
+    s.cache.tail_ids = s.i32([s.cache.tail.shape[0], 1])
+    got = s.attend(q)
+    assert H.status(s.cache) == L.DEVERR_PAGE_ID
+    s.check_attention(got, q, drop=(24,), heads={(0, 0), (0, 1)})
+    s.cache.tail_ids = None
+    s.cache.status.zero_()
+    got = s.attend(q, lens=[-3, 401], max_len=400)
+    assert H.status(s.cache) == L.DEVERR_SEQ_LEN and (got == 0).all()
+    s.cache.status.zero_()
+    np.testing.assert_array_equal(s.attend(q), good)
+
+
+def test_page_offsets_beyond_4_gib():
+    """Page ids whose blocks lie past 2^32 bytes."""
+    t = H.torch()
+    s = K.Sequences(1, 8, 8, 128, kv8.INT8, 64)
+    need = (5 << 30) // (8 * 4112)
+    s.cache.pool = t.empty((need, 8, 4112), dtype=t.uint8, device=H.DEV)
+    ids = np.array([need - 1, 3, need - 2, need // 2 + 1], np.int32)
+    s.cache.page_table.copy_(t.from_numpy(ids[None]))
+    s.place([64])
+    q = K.queries(s.rng, 1, 1, 8, 128)
+    s.check_attention(s.attend(q), q)
+    order = kv8.orders(128)
+    for p, i in enumerate(ids):
+        scale, codes = kv8.block(s.v[0][16 * p:16 * p + 16, 7], kv8.INT8)
+        blk = s.cache.pool[int(i), 7].cpu().numpy()
+        np.testing.assert_array_equal(blk[2048:4096][order[1]], codes)
+
+
+def test_same_bits_again_and_from_a_graph():
+    """The same call twice, with a dirty workspace between, and a captured call replayed
+    after its inputs changed: bit-equal outputs."""
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(3, 4, 16, 128, kv8.INT8, 3100, seed=2)
+    s.place([3000, 77, 1500])
+    q = K.queries(s.rng, 3, 1, 16, 128)
+    a = s.attend(q)
+    np.testing.assert_array_equal(a, s.attend(q))
+    lens, qt = s.i32(s.lens), H.bf16_tensor(q[:, 0])
+    out = t.zeros_like(qt)
+    ws = t.full((L.oscar_kv8_workspace_size(s.cache, 3, 1, 3100),), 0x7F, dtype=t.uint8, device=H.DEV)
+    stream = t.cuda.Stream()
+    with t.cuda.stream(stream):
+        L.oscar_kv8_attention(s.cache, qt, lens, 3100, out, ws)
+    stream.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        L.oscar_kv8_attention(s.cache, qt, lens, 3100, out, ws)
+    out.zero_()
+    graph.replay()
+    t.cuda.synchronize()
+    np.testing.assert_array_equal(H.from_bf16(out), s.attend(q, max_len=3100)[:, 0])
+    s.place([40, 3, 1])
+    lens.copy_(s.i32(s.lens))
+    q2 = K.queries(s.rng, 3, 1, 16, 128)
+    qt.copy_(H.bf16_tensor(q2[:, 0]))
+    graph.replay()
+    graph.replay()
+    t.cuda.synchronize()
+    s.check_attention(H.from_bf16(out)[:, None], q2)
+
+
+def test_calls_on_two_streams_with_their_own_workspaces():
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(2, 8, 32, 128, kv8.E4M3, 5000, seed=4)
+    s.place([4999, 2500])
+    q = K.queries(s.rng, 2, 1, 32, 128)
+    want = s.attend(q)
+    qt, lens = H.bf16_tensor(q[:, 0]), s.i32(s.lens)
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream() for _ in range(2)]
+    size = L.oscar_kv8_workspace_size(s.cache, 2, 1, 4999)
+    outs = [t.zeros_like(qt) for _ in range(8)]
+    spaces = [t.empty(size, dtype=t.uint8, device=H.DEV) for _ in range(2)]
+    t.cuda.synchronize()
+    for i in range(8):
+        L.oscar_kv8_attention(s.cache, qt, lens, 4999, outs[i], spaces[i % 2], stream=streams[i % 2])
+    t.cuda.synchronize()
+    for o in outs:
+        np.testing.assert_array_equal(H.from_bf16(o), want[:, 0])
