@@ -422,36 +422,46 @@ def _need(ok: bool, fn: str, what: str) -> None:
         raise ValueError(f"{fn}: {what}")
 
 
-def _check_list(fn: str, device, **tensors) -> None:
-    """Contiguous int32 tensors on `device`."""
+# A decode step's calls take less time on the GPU than checks written at leisure take
+# on the host: each of these reads an attribute of a tensor once, and a message is put
+# together only when it is raised.
+
+def _i32(fn: str, name: str, t, index: int) -> int:
+    """The address of a contiguous int32 tensor on CUDA device `index`."""
     import torch
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor on {device}")
+    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor on cuda:{index}")
+    return t.data_ptr()
 
 
-def _token_stride(fn: str, name: str, t, heads: int, d: int, device) -> int:
+def _rows(fn: str, name: str, t, n: int, heads: int, d: int, index: int) -> int:
     """Row stride in elements of a bf16 tensor [n][heads][d] whose rows are contiguous."""
     import torch
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3 or t.shape[1:] != (heads, d):
-        raise ValueError(f"{fn}: {name} must be a bfloat16 tensor [n][{heads}][{d}] on {device}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != (n, heads, d):
+        raise ValueError(f"{fn}: {name} must be a bfloat16 tensor [{n}][{heads}][{d}] on cuda:{index}")
     row, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and heads > 1):
         raise ValueError(f"{fn}: {name}: the heads of a row must be contiguous")
-    return row if t.shape[0] > 1 else heads * d
+    return row if n > 1 else heads * d
 
 
-def _launch(fn: str, device, stream, *args) -> None:
-    """Calls the library's `fn` with the stream appended, with `device` current."""
+def _device_of(fn: str, name: str, t) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{fn}: {name} must be on a CUDA device")
+    return index
+
+
+def _launch(fn: str, index: int, stream, *args) -> None:
+    """Calls the library's `fn` with the stream appended, with device `index` current."""
     import torch
     f = getattr(_LIB or lib(), fn)
-    index = device.index
-    # the current stream's handle without a Stream object around it (2 us a call)
+    # the current stream's handle without a Stream object around it
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = f(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = f(*args, handle)
     if status != OSCAR_OK:
         raise OscarError(fn, status)
@@ -477,77 +487,85 @@ class Kv8Cache:
     status: object = None
 
     def desc(self) -> Kv8Desc:
-        key = (_ptr(self.pool), _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
-               _ptr(self.status), self.fmt, self.num_q_heads)
+        return self._checked()[0]
+
+    def _checked(self):
+        """(descriptor, device index, pages-table rows), checked again when a tensor or a
+        field has been replaced."""
+        key = (self.pool.data_ptr(), self.tail.data_ptr(), self.page_table.data_ptr(),
+               _ptr(self.tail_ids), _ptr(self.status), self.fmt, self.num_q_heads,
+               self.num_kv_heads, self.head_dim, self.page_table.shape, self.pool.shape,
+               self.tail.shape)
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:
             return cached[1]
         import torch
-        fn, h, d, device = "Kv8Cache", self.num_kv_heads, self.head_dim, self.pool.device
-        _need(device.type == "cuda", fn, "pool must be on a CUDA device")
-        _need(self.pool.dtype == torch.uint8 and self.pool.is_contiguous()
+        fn, h, d = "Kv8Cache", self.num_kv_heads, self.head_dim
+        index = _device_of(fn, "pool", self.pool)
+        _need(self.pool.dtype is torch.uint8 and self.pool.is_contiguous()
               and self.pool.shape[1:] == (h, 32 * d + 16), fn,
               f"pool must be a contiguous uint8 tensor [num_pages][{h}][{32 * d + 16}]")
-        _need(self.tail.dtype == torch.bfloat16 and self.tail.is_contiguous()
-              and self.tail.device == device and self.tail.shape[1:] == (h, 2, 16 * d), fn,
-              f"tail must be a contiguous bfloat16 tensor [num_tails][{h}][2][{16 * d}] on {device}")
-        _check_list(fn, device, page_table=self.page_table)
+        _need(self.tail.dtype is torch.bfloat16 and self.tail.is_contiguous()
+              and self.tail.get_device() == index and self.tail.shape[1:] == (h, 2, 16 * d), fn,
+              f"tail must be a contiguous bfloat16 tensor [num_tails][{h}][2][{16 * d}] on cuda:{index}")
+        _i32(fn, "page_table", self.page_table, index)
         _need(self.page_table.dim() == 2, fn, "page_table must be [batch][max_pages_per_seq]")
+        rows = int(self.page_table.shape[0])
         if self.tail_ids is not None:
-            _check_list(fn, device, tail_ids=self.tail_ids)
-            _need(self.tail_ids.numel() == self.page_table.shape[0], fn,
+            _i32(fn, "tail_ids", self.tail_ids, index)
+            _need(self.tail_ids.numel() == rows, fn,
                   "tail_ids must have an entry per row of the page table")
         if self.status is not None:
-            _check_list(fn, device, status=self.status)
+            _i32(fn, "status", self.status, index)
         desc = Kv8Desc(h, self.num_q_heads, d, int(self.page_table.shape[1]),
                        int(self.pool.shape[0]), int(self.tail.shape[0]), _ptr(self.pool),
                        _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
                        _ptr(self.status), self.fmt)
-        self.__dict__["_desc"] = (key, desc)
-        return desc
+        found = (desc, ctypes.byref(desc), index, rows)
+        self.__dict__["_desc"] = (key, found)
+        return found
 
 
 def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int, stream=None):
     """Place the rows of k and v (bf16 [n][Hkv][d], rows may be strided): sequence b's
     rows row_starts[b] .. row_starts[b+1] - 1 go behind its lens_before[b] tokens.
     max_new: the most rows that one sequence brings."""
-    fn, d = "oscar_kv8_place", cache.desc()
-    device = cache.pool.device
-    ks = _token_stride(fn, "k", k, cache.num_kv_heads, cache.head_dim, device)
-    vs = _token_stride(fn, "v", v, cache.num_kv_heads, cache.head_dim, device)
-    _check_list(fn, device, lens_before=lens_before, row_starts=row_starts)
+    fn = "oscar_kv8_place"
+    _, desc, index, rows = cache._checked()
+    n, h, d = k.shape[0], cache.num_kv_heads, cache.head_dim
+    ks = _rows(fn, "k", k, n, h, d, index)
+    vs = _rows(fn, "v", v, n, h, d, index)
+    lens, starts = _i32(fn, "lens_before", lens_before, index), _i32(fn, "row_starts", row_starts, index)
     batch = lens_before.numel()
-    _need(row_starts.numel() == batch + 1 and batch <= cache.page_table.shape[0], fn,
-          "row_starts must have batch + 1 entries, and the page table a row per sequence")
-    _need(v.shape[0] == k.shape[0], fn, "k and v must have the same rows")
-    _launch(fn, device, stream, ctypes.byref(d), k.data_ptr(), v.data_ptr(), ks, vs,
-            lens_before.data_ptr(), row_starts.data_ptr(), batch, k.shape[0], int(max_new))
+    if row_starts.numel() != batch + 1 or batch > rows:
+        raise ValueError(f"{fn}: row_starts must have batch + 1 entries, and the page table a row "
+                         "per sequence")
+    _launch(fn, index, stream, desc, k.data_ptr(), v.data_ptr(), ks, vs, lens, starts, batch, n,
+            max_new)
 
 
 def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
                      stream=None):
     """Read tokens back as bf16: rows row_starts[b] .. row_starts[b+1] - 1 of k_out and
     v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on."""
-    fn, d = "oscar_kv8_gather", cache.desc()
-    device = cache.pool.device
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _token_stride(fn, name, t, cache.num_kv_heads, cache.head_dim, device)
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous")
-    _check_list(fn, device, seq_lens=seq_lens, first=first, row_starts=row_starts)
+    fn = "oscar_kv8_gather"
+    _, desc, index, rows = cache._checked()
+    n, h, d = k_out.shape[0], cache.num_kv_heads, cache.head_dim
+    if (_rows(fn, "k_out", k_out, n, h, d, index) != h * d
+            or _rows(fn, "v_out", v_out, n, h, d, index) != h * d):
+        raise ValueError(f"{fn}: k_out and v_out must be contiguous")
+    lens, begin = _i32(fn, "seq_lens", seq_lens, index), _i32(fn, "first", first, index)
+    starts = _i32(fn, "row_starts", row_starts, index)
     batch = seq_lens.numel()
-    _need(first.numel() == batch and row_starts.numel() == batch + 1
-          and batch <= cache.page_table.shape[0], fn,
-          "first must have batch entries, row_starts batch + 1, the page table a row per sequence")
-    _need(v_out.shape[0] == k_out.shape[0], fn, "k_out and v_out must have the same rows")
-    _launch(fn, device, stream, ctypes.byref(d), seq_lens.data_ptr(), first.data_ptr(),
-            row_starts.data_ptr(), batch, k_out.shape[0], int(max_rows), k_out.data_ptr(),
+    if first.numel() != batch or row_starts.numel() != batch + 1 or batch > rows:
+        raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1, and the page "
+                         "table a row per sequence")
+    _launch(fn, index, stream, desc, lens, begin, starts, batch, n, max_rows, k_out.data_ptr(),
             v_out.data_ptr())
 
 
 def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
-    d = cache.desc()
-    return int(lib().oscar_kv8_workspace_size(ctypes.byref(d), batch, m_rows, max_seq_len))
+    return int(lib().oscar_kv8_workspace_size(cache._checked()[1], batch, m_rows, max_seq_len))
 
 
 def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,
@@ -556,29 +574,27 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
     the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
     row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros)."""
     import torch
-    fn, d = "oscar_kv8_attention", cache.desc()
-    device = cache.pool.device
-    batch = seq_lens.numel()
-    heads = (cache.num_q_heads, cache.head_dim)
+    fn = "oscar_kv8_attention"
+    _, desc, index, rows = cache._checked()
+    lens, batch = _i32(fn, "seq_lens", seq_lens, index), seq_lens.numel()
     if q_pos is None:
-        m_rows, shape = 1, (batch, *heads)
-        _check_list(fn, device, seq_lens=seq_lens)
+        m_rows, pos, shape = 1, None, (batch, cache.num_q_heads, cache.head_dim)
     else:
-        _check_list(fn, device, seq_lens=seq_lens, q_pos=q_pos)
-        _need(q_pos.dim() == 2 and q_pos.shape[0] == batch, fn, "q_pos must be [batch][rows]")
+        pos = _i32(fn, "q_pos", q_pos, index)
+        if q_pos.dim() != 2 or q_pos.shape[0] != batch:
+            raise ValueError(f"{fn}: q_pos must be [batch][rows]")
         m_rows = q_pos.shape[1]
-        shape = (batch, m_rows, *heads)
-    for name, t in (("q", q), ("out", out)):
-        if (t.dtype != torch.bfloat16 or t.device != device or t.shape != shape
+        shape = (batch, m_rows, cache.num_q_heads, cache.head_dim)
+    for t in (q, out):
+        if (t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape
                 or not t.is_contiguous()):
-            raise ValueError(f"{fn}: {name} must be a contiguous bfloat16 tensor {list(shape)} "
-                             f"on {device}")
-    _need(batch <= cache.page_table.shape[0], fn, "the page table must have a row per sequence")
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {device}")
-    _launch(fn, device, stream, ctypes.byref(d), q.data_ptr(), seq_lens.data_ptr(), _ptr(q_pos),
-            batch, m_rows, int(max_seq_len), out.data_ptr(), workspace.data_ptr(),
-            _ws_bytes(workspace))
+            raise ValueError(f"{fn}: q and out must be contiguous bfloat16 tensors {list(shape)} "
+                             f"on cuda:{index}")
+    if batch > rows or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: the page table must have a row per sequence, and the workspace be "
+                         f"a contiguous tensor on cuda:{index}")
+    _launch(fn, index, stream, desc, q.data_ptr(), lens, pos, batch, m_rows, max_seq_len,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_after, page_starts,
@@ -589,30 +605,30 @@ def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_af
     page_starts[B] is the next call's cursor (pass page_starts[-1:]); lens_after may
     be lens.  Rows of seq_ids, positions and slots behind the new tokens become -1."""
     import torch
-    fn, device = "oscar_extend_pages", page_table.device
-    _need(device.type == "cuda", fn, "page_table must be on a CUDA device")
-    _check_list(fn, device, page_table=page_table, lens=lens, new_tokens=new_tokens,
-                free_pages=free_pages, cursor=cursor, lens_after=lens_after,
-                page_starts=page_starts, row_starts=row_starts, seq_ids=seq_ids,
-                positions=positions)
+    fn = "oscar_extend_pages"
+    index = _device_of(fn, "page_table", page_table)
     batch, rows = lens.numel(), seq_ids.numel()
-    _need(page_table.dim() == 2 and page_table.shape[0] >= batch, fn,
-          "page_table must be [batch][max_pages_per_seq]")
-    _need(new_tokens.numel() == batch and lens_after.numel() == batch and cursor.numel() >= 1
-          and page_starts.numel() == batch + 1 and row_starts.numel() == batch + 1, fn,
-          "new_tokens and lens_after must have batch entries, page_starts and row_starts batch + 1")
-    _need(positions.numel() == rows, fn, "seq_ids and positions must have the same rows")
-    if slots is not None and (slots.dtype != torch.int64 or slots.device != device
+    args = [_i32(fn, name, t, index) for name, t in (
+        ("page_table", page_table), ("lens", lens), ("new_tokens", new_tokens),
+        ("free_pages", free_pages), ("cursor", cursor), ("lens_after", lens_after),
+        ("page_starts", page_starts), ("row_starts", row_starts), ("seq_ids", seq_ids),
+        ("positions", positions))]
+    if page_table.dim() != 2 or page_table.shape[0] < batch:
+        raise ValueError(f"{fn}: page_table must be [batch][max_pages_per_seq]")
+    if (new_tokens.numel() != batch or lens_after.numel() != batch or cursor.numel() < 1
+            or page_starts.numel() != batch + 1 or row_starts.numel() != batch + 1):
+        raise ValueError(f"{fn}: new_tokens and lens_after must have batch entries, page_starts and "
+                         "row_starts batch + 1, cursor one")
+    if positions.numel() != rows:
+        raise ValueError(f"{fn}: seq_ids and positions must have the same rows")
+    if slots is not None and (slots.dtype is not torch.int64 or slots.get_device() != index
                               or not slots.is_contiguous() or slots.numel() != rows):
-        raise ValueError(f"{fn}: slots must be a contiguous int64 tensor on {device} with a row "
-                         "per seq_ids row")
-    if status is not None:
-        _check_list(fn, device, status=status)
-    _launch(fn, device, stream, page_table.data_ptr(), page_table.shape[1], lens.data_ptr(),
-            new_tokens.data_ptr(), batch, int(hold_back), free_pages.data_ptr(),
-            free_pages.numel(), cursor.data_ptr(), lens_after.data_ptr(), page_starts.data_ptr(),
-            row_starts.data_ptr(), seq_ids.data_ptr(), positions.data_ptr(), _ptr(slots), rows,
-            _ptr(status))
+        raise ValueError(f"{fn}: slots must be a contiguous int64 tensor on cuda:{index} with a "
+                         "row per seq_ids row")
+    table, before, new, free, at, after, ps, rs, ids, pos = args
+    _launch(fn, index, stream, table, page_table.shape[1], before, new, batch, hold_back, free,
+            free_pages.numel(), at, after, ps, rs, ids, pos, _ptr(slots), rows,
+            None if status is None else _i32(fn, "status", status, index))
 
 
 def oscar_rope_phases(base: float, rotary_dim: int, factor: float = 1.0, original_len: int = 0,
@@ -634,31 +650,33 @@ def oscar_rope(q, k, positions, phases, q_out=None, k_out=None, interleaved: boo
     q_out, k_out: outputs, in place when None."""
     import torch
     fn = "oscar_rope"
-    some = q if q is not None else k
-    _need(some is not None and some.dim() == 3, fn, "q or k must be given, as [n][heads][d]")
-    device, (n, _, d) = some.device, some.shape
-    _need(device.type == "cuda", fn, "q and k must be on a CUDA device")
-    args = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            _need(y is None, fn, f"{name}_out without {name}")
-            args.append((0, 0, 0, None, None))
-            continue
-        y = x if y is None else y
-        heads = x.shape[1]
-        xs = _token_stride(fn, name, x, heads, d, device)
-        ys = xs if y is x else _token_stride(fn, name + "_out", y, heads, d, device)
-        _need(x.shape[0] == n and y.shape[0] == n, fn, "q, k and the outputs must have the same rows")
-        args.append((heads, xs, ys, x.data_ptr(), y.data_ptr()))
-    _check_list(fn, device, positions=positions)
-    _need(positions.numel() == n, fn, "positions must have an entry per row")
-    if (phases.dtype not in (torch.int64, torch.uint64) or phases.device != device
+    some = k if q is None else q
+    if some is None or some.dim() != 3:
+        raise ValueError(f"{fn}: q or k must be given, as [n][heads][d]")
+    index = _device_of(fn, "q and k", some)
+    n, _, d = some.shape
+    hq = hk = qs = ks = qos = kos = 0
+    qp = kp = qop = kop = None
+    if q is not None:
+        hq = q.shape[1]
+        qs = qos = _rows(fn, "q", q, n, hq, d, index)
+        qp = qop = q.data_ptr()
+        if q_out is not None:
+            qos, qop = _rows(fn, "q_out", q_out, n, hq, d, index), q_out.data_ptr()
+    if k is not None:
+        hk = k.shape[1]
+        ks = kos = _rows(fn, "k", k, n, hk, d, index)
+        kp = kop = k.data_ptr()
+        if k_out is not None:
+            kos, kop = _rows(fn, "k_out", k_out, n, hk, d, index), k_out.data_ptr()
+    pos = _i32(fn, "positions", positions, index)
+    if positions.numel() != n or (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError(f"{fn}: positions must have an entry per row, and an output its input")
+    if (phases.dtype not in (torch.int64, torch.uint64) or phases.get_device() != index
             or not phases.is_contiguous()):
-        raise ValueError(f"{fn}: phases must be contiguous 64-bit integers on {device}")
-    (hq, qs, qos, qp, qop), (hk, ks, kos, kp, kop) = args
-    _launch(fn, device, stream, qp, kp, positions.data_ptr(), phases.data_ptr(), n, hq, hk, d,
-            2 * phases.numel(), int(interleaved), float(amplitude), int(inverse), qs, ks, qos, kos,
-            qop, kop)
+        raise ValueError(f"{fn}: phases must be contiguous 64-bit integers on cuda:{index}")
+    _launch(fn, index, stream, qp, kp, pos, phases.data_ptr(), n, hq, hk, d, 2 * phases.numel(),
+            1 if interleaved else 0, amplitude, 1 if inverse else 0, qs, ks, qos, kos, qop, kop)
 
 
 def oscar_device_sm_count() -> int:

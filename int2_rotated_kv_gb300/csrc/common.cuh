@@ -251,7 +251,8 @@ oscar_status check_kv8(const oscar_kv8_desc* c);
 
 int sm_count();
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (function, device).
-bool allow_smem(const void* func, int bytes);
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (function, device);
+// clusters: clusters of up to 16 CTAs too.
+bool allow_smem(const void* func, int bytes, bool clusters = false);
 
 }  // namespace oscar_host

@@ -1670,7 +1670,7 @@ const void* mapped_range(const void* p, size_t bytes) {
   return a.devicePointer;
 }
 
-bool allow_smem(const void* func, int bytes) {
+bool allow_smem(const void* func, int bytes, bool clusters) {
   static std::mutex mu;
   static std::vector<std::pair<const void*, int>> done;   // (function, device)
   int dev = 0;
@@ -1679,6 +1679,9 @@ bool allow_smem(const void* func, int bytes) {
   for (auto& d : done)
     if (d.first == func && d.second == dev) return true;
   if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  if (clusters &&
+      cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return false;
   done.emplace_back(func, dev);
   return true;

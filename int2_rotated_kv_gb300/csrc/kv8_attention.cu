@@ -20,26 +20,33 @@
 // Softmax statistics, accumulators and the merges are fp32.  Tail tokens are exact
 // in bf16 on the K side and use fp32 p on the V side.
 //
-// Work split.  The (sequence, tile of query columns, KV head) units, each a run of
-// pages, are laid end to end, and every CTA takes an equal share of the pages,
-// found from the lengths on the device: ragged batches finish together.  A CTA
-// whose share ends inside a unit leaves a partial (at most two per CTA, so the
-// workspace does not grow with the batch); a second kernel merges those units.
-// Within a CTA the eight warps take pages in turn, each through its own ring of
-// bulk copies, and merge through shared memory at a unit's end; the ring already
-// fills for the next unit meanwhile.
+// Work split, by what there is of (sequence, tile of query columns, KV head) units,
+// each a run of pages (kv8_plan has the rule):
+//   - many short units: a team of 1, 2, 4 or 8 warps per unit.
+//   - few units, moderate lengths: a thread-block cluster per unit.  Each of its CTAs
+//     (16 warps, one CTA per SM) takes an equal run of the unit's pages, and the CTAs
+//     merge through distributed shared memory: one launch, no workspace.
+//   - else the units are laid end to end, and every CTA (8 warps, two per SM) takes an
+//     equal share of the pages, found from the lengths on the device: ragged batches
+//     finish together.  A CTA whose share ends inside a unit leaves a partial (at most
+//     two per CTA, so the workspace does not grow with the batch); a second kernel
+//     merges those units.
+// Within a CTA the warps take pages in turn, each through its own ring of bulk copies,
+// and merge through shared memory at a unit's end; the ring already fills for the
+// next unit meanwhile.
 //
 // Bound by HBM: 2d + 1 bytes per token and KV head.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <utility>
+#include <vector>
 
 #include "common.cuh"
 #include "kv8_layout.cuh"
 
 namespace oscar {
 
-constexpr int kAWarps = 8;
-constexpr int kAThreads = 32 * kAWarps;
 constexpr int kMaxCtas = 1024;
 constexpr float kLowest = -3.402823466e38f;   // running maximum before the first logit
 constexpr float kLag = 8.f;                   // the maximum is raised when passed by 2^8
@@ -57,27 +64,34 @@ struct Kv8Params {
   const int32_t* seq_lens;
   const int32_t* q_pos;    // null: one row per sequence, at its last token
   int m_rows, cols, tiles, entries, max_len;   // cols = m_rows * G; entries = batch * tiles
-  int whole_units;         // one CTA per unit, no partials
+  int cluster;             // CTAs per unit when clusters serve units
+  int team;                // warps per unit when teams of warps do
   float scale_log2;
   int4* info;              // per CTA: unit entry, KV head, parts of the unit that starts in it
   float* part;             // [2 * CTAs][8 * NT * (D + 2)]
 };
 
-template <int D, int NT>
+enum Kv8Mode { kShares, kCluster, kTeams };
+
+template <int D, int NT, Kv8Mode kMode>
 struct Kv8Cfg {
   using F = Kv8Fmt<D>;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;             // per SM
+  static constexpr int kWarps = kMode == kCluster ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = NT == 1 && kMode != kCluster ? 2 : 1;   // per SM
   static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  static constexpr int kWarpRing = kStages * F::kBlock;
   static constexpr int kStride = D + 4;                     // floats per column when merging
-  static constexpr int kRing = kAWarps * kStages * F::kBlock;
-  static constexpr int kMerge = kAWarps * 8 * kStride * 4;
-  static constexpr int kStat = kAWarps * 8 * NT * 4;        // one of m, l
-  static constexpr int kTailOff = kRing;
-  static constexpr int kMergeOff = kTailOff + F::kTailBytes;
-  static constexpr int kStatOff = kMergeOff + kMerge;
-  static constexpr int kBarOff = kStatOff + 2 * kStat;
-  static constexpr int kBytes = kBarOff + (kAWarps * kStages + 1) * 8;
+  static constexpr int kMerge = kWarps * 8 * kStride * 4;
+  static constexpr int kStat = kWarps * 8 * NT * 4;         // one of m, l
   static constexpr int kSlot = 8 * NT * (D + 2);            // floats of one partial
+  static constexpr int kMergeOff = kWarps * kWarpRing;
+  static constexpr int kStatOff = kMergeOff + kMerge;
+  static constexpr int kPartOff = kStatOff + 2 * kStat;     // a cluster's CTA: its partial
+  static constexpr int kBarOff = kPartOff + (kMode == kCluster ? kSlot * 4 : 0);
+  static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
+  static_assert(kMode == kShares || NT == 1, "clusters and teams serve one tile of columns per unit");
+  static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
 };
 
 // A sequence's tile of query columns: pages it has to visit (at least one, so that
@@ -355,9 +369,10 @@ __device__ __forceinline__ void unscale(Running<D, NT>& s) {
 }
 
 // The tail: n bf16 tokens from position page0 at `st`; accumulators already in the
-// units of the values.  At most 15 tokens once per unit: p.V in fp32 on the CUDA
-// cores, which also keeps a NaN or an infinity of a token that a row does not see
-// out of that row.
+// units of the values.  q.K in bf16 (exact products).  p.V in bf16 with p as a pair of
+// bf16 (2^-17); when a value is not finite, or a column does not see all n tokens, in
+// fp32 on the CUDA cores instead, which keeps a NaN or an infinity of a token out of
+// the rows that do not see it.
 template <int D, int NT>
 __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uint8_t* st, int page0,
                             int n, int lane, const Query<D, NT>& q, Running<D, NT>& s) {
@@ -397,13 +412,52 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
     s.l[nt][0] += lg[nt][0] + lg[nt][2];
     s.l[nt][1] += lg[nt][1] + lg[nt][3];
   }
-  const uint16_t* vb = reinterpret_cast<const uint16_t*>(st) + F::kTailHalf;
+  const uint4* vb = kb + 2 * D;   // 16 * d keys before them
+  // tokens 4tig, 4tig + 1 and 4tig + 2, 4tig + 3 of a channel's words, where there are any
+  const int have = n - 4 * tig;
+  const uint32_t m01 = (have > 0 ? 0xffffu : 0u) | (have > 1 ? 0xffff0000u : 0u);
+  const uint32_t m23 = (have > 2 ? 0xffffu : 0u) | (have > 3 ? 0xffff0000u : 0u);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m01 & 0x7fff7fffu, v.y & m23 & 0x7fff7fffu),
+                                 __vmaxu2(v.z & m01 & 0x7fff7fffu, v.w & m23 & 0x7fff7fffu)));
+  }
+  const bool plain = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
+  if (q.vis_min >= page0 + n && __all_sync(0xffffffffu, plain)) {
+    uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t h0 = pack_bf162(lg[nt][0], lg[nt][1]), h1 = pack_bf162(lg[nt][2], lg[nt][3]);
+      const uint32_t l0 = pack_bf162(lg[nt][0] - bf16_lo_value(h0), lg[nt][1] - bf16_hi_value(h0));
+      const uint32_t l1 = pack_bf162(lg[nt][2] - bf16_lo_value(h1), lg[nt][3] - bf16_hi_value(h1));
+      const uint32_t t0 = movmatrix_trans(h0), t1 = movmatrix_trans(h1);
+      const uint32_t u0 = movmatrix_trans(l0), u1 = movmatrix_trans(l1);
+      bh[nt][0] = __byte_perm(t0, t1, 0x5410);
+      bh[nt][1] = __byte_perm(t0, t1, 0x7632);
+      bl[nt][0] = __byte_perm(u0, u1, 0x5410);
+      bl[nt][1] = __byte_perm(u0, u1, 0x7632);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
+      v.x &= m01; v.y &= m23; v.z &= m01; v.w &= m23;   // slots without a token may hold anything
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_bf16(s.o[nt][i], v.x, v.z, v.y, v.w, bh[nt][0], bh[nt][1]);
+        mma_bf16(s.o[nt][i], v.x, v.z, v.y, v.w, bl[nt][0], bl[nt][1]);
+      }
+    }
+    return;
+  }
+  const uint16_t* ve = reinterpret_cast<const uint16_t*>(st) + F::kTailHalf;
   for (int i = 0; i < n; ++i) {
     float v[D / 16][2];
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {   // the lane's channels 32 (c/4) + 4 gid + c%4
       const int chunk = kv8_value_chunk(i >> 2, (c >> 2) * 8 + gid);
-      v[c >> 1][c & 1] = bf16_to_float(vb[chunk * 16 + 4 * (c & 3) + (i & 3)]);
+      v[c >> 1][c & 1] = bf16_to_float(ve[chunk * 16 + 4 * (c & 3) + (i & 3)]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -424,46 +478,97 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
   }
 }
 
-// A warp's ring of page copies: n_in issued, n_out consumed since the kernel's
-// start, so the phases run on from unit to unit.
+// A warp's ring of page copies: n_in issued, n_out consumed since the kernel's start, so
+// the phases run on from unit to unit.  A tail block takes the whole ring (and one
+// barrier's turn), so it comes when the pages before it have been consumed.
 struct Ring {
-  uint32_t n_in, n_out, shown;   // shown: bit per stage, the page id was valid
+  uint8_t* base;
+  uint64_t* bars;
+  uint32_t n_in, n_out, shown;   // shown: bit per stage, the id was valid
   int next_id;
   bool alive;                    // false after a copy that did not arrive in time
+  bool tail_issued;
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void issue(const Kv8Params& p, const Entry& t, int h, int pg, int end,
-                                      int warp, int lane, uint8_t* smem, uint64_t* bars, Ring& r) {
-  using C = Kv8Cfg<D, NT>;
+template <typename C>
+__device__ __forceinline__ void copy_in(const Kv8Params& p, bool ok, const uint8_t* src, int bytes,
+                                        uint8_t* dst, int lane, Ring& r) {
   const int s = r.n_in % C::kStages;
-  const bool ok = r.next_id >= 0 && r.next_id < p.n_pages;
   r.shown = (r.shown & ~(1u << s)) | (static_cast<uint32_t>(ok) << s);
   if (lane == 0) {
     if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-    uint64_t* bar = bars + warp * C::kStages + s;
-    const int64_t block = static_cast<int64_t>(ok ? r.next_id : 0) * p.hkv + h;
-    mbar_arrive_expect_tx(bar, C::F::kBlock);
-    bulk_g2s(smem + (warp * C::kStages + s) * C::F::kBlock, p.pool + block * C::F::kBlock,
-             C::F::kBlock, bar);
+    mbar_arrive_expect_tx(r.bars + s, bytes);
+    bulk_g2s(dst, src, bytes, r.bars + s);
   }
   ++r.n_in;
-  if (pg + kAWarps < end)
-    r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + pg + kAWarps];
 }
 
-// Starts the copies of a warp's first pages of a unit.
-template <int D, int NT>
-__device__ __forceinline__ void start_unit(const Kv8Params& p, const Entry& t, int h, int first,
-                                           int end, int warp, int lane, uint8_t* smem,
-                                           uint64_t* bars, Ring& r) {
-  if (first >= end || !r.alive) return;
-  r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + first];
-#pragma unroll
-  for (int i = 0; i < Kv8Cfg<D, NT>::kStages; ++i)
-    if (first + i * kAWarps < end)
-      issue<D, NT>(p, t, h, first + i * kAWarps, end, warp, lane, smem, bars, r);
+// The copy of page pg (a refused id copies page 0, which is then not looked at); `step`
+// pages on is the warp's next.
+template <typename C>
+__device__ __forceinline__ void issue(const Kv8Params& p, const Entry& t, int h, int pg, int end,
+                                      int step, int lane, Ring& r) {
+  const bool ok = r.next_id >= 0 && r.next_id < p.n_pages;
+  const int64_t block = static_cast<int64_t>(ok ? r.next_id : 0) * p.hkv + h;
+  copy_in<C>(p, ok, p.pool + block * C::F::kBlock, C::F::kBlock,
+             r.base + r.n_in % C::kStages * C::F::kBlock, lane, r);
+  if (pg + step < end) r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + pg + step];
 }
+
+template <typename C>
+__device__ __forceinline__ void issue_tail(const Kv8Params& p, const Entry& t, int h, int lane, Ring& r) {
+  const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
+  const bool ok = id >= 0 && id < p.n_tails;
+  copy_in<C>(p, ok, p.tail + ((ok ? id : 0) * p.hkv + h) * C::F::kTailBytes, C::F::kTailBytes, r.base,
+             lane, r);
+  r.tail_issued = true;
+}
+
+// Waits for the oldest copy; false when it did not come in time, with no copy left in flight.
+template <typename C>
+__device__ __forceinline__ bool copied(const Kv8Params& p, Ring& r, int& s) {
+  s = r.n_out % C::kStages;
+  const bool got = mbar_wait(r.bars + s, (r.n_out / C::kStages) & 1, p.status);
+  ++r.n_out;
+  if (__all_sync(0xffffffffu, got)) return true;
+  for (; r.n_out < r.n_in; ++r.n_out)
+    mbar_wait(r.bars + r.n_out % C::kStages, (r.n_out / C::kStages) & 1, p.status);
+  r.alive = false;
+  return false;
+}
+
+// A warp's part of pages [p0, p1) of a unit: pages first, first + step, ... below end, and
+// the tail if it is this warp's.
+struct Part {
+  int first, end;
+  bool tail;
+};
+
+__device__ __forceinline__ Part part_of(const Entry& t, int p0, int p1, int warp, int step) {
+  Part a;
+  a.first = p0 + warp;
+  a.end = min(p1, t.n8);
+  a.tail = p1 > t.n8 && t.vis > t.len / kPage * kPage && warp == (t.n8 - p0) % step;
+  return a;
+}
+
+// Starts the first copies of a warp's part (its ring is empty).
+template <typename C>
+__device__ __forceinline__ void start_part(const Kv8Params& p, const Entry& t, int h, const Part& a,
+                                           int step, int lane, Ring& r) {
+  r.tail_issued = false;
+  if (!r.alive) return;
+  if (a.first < a.end) {
+    r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + a.first];
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i)
+      if (a.first + i * step < a.end) issue<C>(p, t, h, a.first + i * step, a.end, step, lane, r);
+  } else if (a.tail) {
+    issue_tail<C>(p, t, h, lane, r);
+  }
+}
+
+constexpr int kScanWarps = 8;   // the CTAs that find their share
 
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
 #pragma unroll
@@ -472,7 +577,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kAWarps; ++w) total += scratch[w];
+  for (int w = 0; w < kScanWarps; ++w) total += scratch[w];
   __syncthreads();
   return total;
 }
@@ -488,7 +593,7 @@ __device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int
   int64_t base = 0;
   if (tid == 0) found = -1;
   __syncthreads();
-  for (int e0 = 0; e0 < p.entries; e0 += kAThreads) {
+  for (int e0 = 0; e0 < p.entries; e0 += 32 * kScanWarps) {
     const int e = e0 + tid;
     const int64_t v = e < p.entries ? static_cast<int64_t>(entry_of<NT>(p, e).pages) * p.hkv : 0;
     int64_t incl = v;
@@ -501,7 +606,7 @@ __device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int
     __syncthreads();
     int64_t off = base, all = base;
 #pragma unroll
-    for (int w = 0; w < kAWarps; ++w) {
+    for (int w = 0; w < kScanWarps; ++w) {
       if (w < warp) off += scratch[w];
       all += scratch[w];
     }
@@ -518,42 +623,130 @@ __device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int
   before = found_before;
 }
 
-template <int D, int NT, bool kE4m3>
-__global__ void __launch_bounds__(kAThreads, (Kv8Cfg<D, NT>::kCtas))
+// Channels ch .. ch + 3 of an output row; a row that sees nothing (l = 0) gets zeros.
+__device__ __forceinline__ void store_row(const Kv8Params& p, int b, int h, int gcol, int ch, int D,
+                                          float4 o, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int row = gcol / p.G, g = gcol - row * p.G;
+  uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D + ch;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+
+// Address of this CTA's shared-memory word `p` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Merges the partials of a cluster's CTAs (8 columns in `slot` of each); every CTA
+// writes its share of the unit's outputs.
+template <int D>
+__device__ __forceinline__ void merge_cluster(const Kv8Params& p, const Entry& t, int h,
+                                              const float* slot) {
+  cluster_sync();
+  const int n = p.cluster, rank = blockIdx.x % n;
+  const int per = (8 * D / 4 + n - 1) / n;      // float4 of each CTA
+  const int i = rank * per + threadIdx.x;
+  if (threadIdx.x < per && i < 8 * D / 4) {
+    const int col = i / (D / 4), ch = 4 * (i % (D / 4)), gcol = t.tile * 8 + col;
+    if (gcol < p.cols) {
+      float top = kLowest, l = 0.f;
+      for (int r = 0; r < n; ++r)
+        top = fmaxf(top, cluster_load2(cluster_address(slot + 8 * D + 2 * col, r)).x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int r = 0; r < n; ++r) {
+        const float2 ml = cluster_load2(cluster_address(slot + 8 * D + 2 * col, r));
+        const float4 x = cluster_load4(cluster_address(slot + col * D + ch, r));
+        const float a = fast_exp2(ml.x - top);
+        l = fmaf(a, ml.y, l);
+        o.x = fmaf(a, x.x, o.x); o.y = fmaf(a, x.y, o.y);
+        o.z = fmaf(a, x.z, o.z); o.w = fmaf(a, x.w, o.w);
+      }
+      store_row(p, t.b, h, gcol, ch, D, o, l);
+    }
+  }
+  cluster_sync();   // no CTA leaves while its shared memory is read
+}
+
+// A barrier of the `team` warps that serve a unit (teams: barrier 1 + number of the team).
+template <Kv8Mode kMode>
+__device__ __forceinline__ void team_sync(int team, int number) {
+  if constexpr (kMode != kTeams) {
+    __syncthreads();
+  } else if (team == 1) {
+    __syncwarp();
+  } else {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(1 + number), "r"(32 * team) : "memory");
+  }
+}
+
+template <int D, int NT, bool kE4m3, Kv8Mode kMode>
+__global__ void __launch_bounds__((Kv8Cfg<D, NT, kMode>::kThreads), (Kv8Cfg<D, NT, kMode>::kCtas))
 kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
-  using C = Kv8Cfg<D, NT>;
-  using F = Kv8Fmt<D>;
+  using C = Kv8Cfg<D, NT, kMode>;
+  constexpr int kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scratch[kAWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
+  // the warps of a unit (all, or a team of them) and this one's place among them
+  const int team = kMode == kTeams ? p.team : kWarps;
+  const int number = kMode == kTeams ? (tid >> 5) / team : 0;
+  const int warp = (tid >> 5) - number * team;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* tail_bar = bars + kAWarps * C::kStages;
-  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff);
-  float* sm_l = sm_m + kAWarps * 8 * NT;
-  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff);
-  if (tid <= kAWarps * C::kStages) mbar_init(bars + tid, 1);
+  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff) + number * team * 8 * NT;
+  float* sm_l = sm_m + kWarps * 8 * NT;
+  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
+  if (tid < kWarps * C::kStages) mbar_init(bars + tid, 1);
   fence_mbar_init();
   __syncthreads();
   pdl_wait();
   pdl_trigger();
 
-  // this CTA's pages [at, end) of all units laid end to end, and its first unit
+  // this team's pages [at, end) of all units laid end to end, and its first unit
   int e = 0, h = 0;
   int64_t at = 0, end = 0, share = 0, unit0 = 0;   // unit0: first page of the current unit
   Entry t;
-  if (p.whole_units) {
-    e = blockIdx.x / p.hkv;
-    h = blockIdx.x - e * p.hkv;
+  if constexpr (kMode == kTeams) {   // a whole unit
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / team) + number;
+    if (unit >= static_cast<int64_t>(p.entries) * p.hkv) return;
+    e = static_cast<int>(unit / p.hkv);
+    h = static_cast<int>(unit - static_cast<int64_t>(e) * p.hkv);
     t = entry_of<NT>(p, e);
-    end = share = t.pages;
+    end = t.pages;
+  } else if constexpr (kMode == kCluster) {   // this CTA's run of the cluster's unit
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
+    e = unit / p.hkv;
+    h = unit - e * p.hkv;
+    t = entry_of<NT>(p, e);
+    at = static_cast<int64_t>(t.pages) * rank / p.cluster;
+    end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
   } else {
+    __shared__ int64_t scratch[kScanWarps];
     int64_t sum = 0;
     if (p.entries == 1) {
       t = entry_of<NT>(p, 0);
       sum = t.pages;
     } else {
-      for (int i = tid; i < p.entries; i += kAThreads) sum += entry_of<NT>(p, i).pages;
+      for (int i = tid; i < p.entries; i += C::kThreads) sum += entry_of<NT>(p, i).pages;
       sum = block_sum(sum, scratch);
     }
     const int64_t total = sum * p.hkv;
@@ -573,79 +766,49 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     unit0 = before + static_cast<int64_t>(h) * t.pages;
   }
 
-  Ring ring{0, 0, 0, 0, true};
-  uint32_t tails = 0;           // tail copies so far: the barrier's phase
+  Ring ring{smem + (tid >> 5) * C::kWarpRing, bars + (tid >> 5) * C::kStages, 0, 0, 0, 0, true, false};
   int4 owned = make_int4(0, 0, 0, 0);
-  // the tail copy of a unit; by thread 0, after every reader of the one before
-  auto start_tail = [&](const Entry& t, int h, int64_t unit0) -> bool {
-    const int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
-    if (p1 <= t.n8 || t.vis <= t.len / kPage * kPage) return false;   // not this CTA's, or none
-    const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
-    const bool ok = id >= 0 && id < p.n_tails;
-    if (tid == 0) {
-      if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-      mbar_arrive_expect_tx(tail_bar, F::kTailBytes);
-      bulk_g2s(smem + C::kTailOff, p.tail + ((ok ? id : 0) * p.hkv + h) * F::kTailBytes,
-               F::kTailBytes, tail_bar);
-    }
-    return ok;
-  };
-  auto has_tail = [&](const Entry& t, int p1) {
-    return p1 > t.n8 && t.vis > t.len / kPage * kPage;
-  };
   int p0 = static_cast<int>(at - unit0);
   int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
-  start_unit<D, NT>(p, t, h, p0 + warp, min(p1, t.n8), warp, lane, smem, bars, ring);
-  bool tail_ok = start_tail(t, h, unit0);
+  Part mine = part_of(t, p0, p1, warp, team);
+  start_part<C>(p, t, h, mine, team, lane, ring);
 
   for (;;) {
     Query<D, NT> q;
     load_query<D, NT, kE4m3>(p, t, h, lane, q);
     Running<D, NT> s;
     reset<D, NT>(s);
-    if (p0 == 0 && h == 0 && t.tile == 0 && tid == 0 && p.status) {
+    if (p0 == 0 && h == 0 && t.tile == 0 && warp == 0 && lane == 0 && p.status) {
       const int len = p.seq_lens[t.b];
       if (len < 0 || len > p.max_len) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
-    if (p.q_pos && p0 == 0 && h == 0 && tid < 8 * NT && p.status) {
-      const int row = (t.tile * 8 * NT + tid) / p.G;
+    if (p.q_pos && p0 == 0 && h == 0 && warp == 0 && lane < 8 * NT && p.status) {
+      const int row = (t.tile * 8 * NT + lane) / p.G;
       if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
         atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
-    const int end8 = min(p1, t.n8);
-    for (int pg = p0 + warp; pg < end8 && ring.alive; pg += kAWarps) {
-      const int st = ring.n_out % C::kStages;
-      const bool got = mbar_wait(bars + warp * C::kStages + st, (ring.n_out / C::kStages) & 1,
-                                 p.status);
-      ++ring.n_out;
-      if (!__all_sync(0xffffffffu, got)) {   // leave no copy in flight, then stop reading pages
-        for (; ring.n_out < ring.n_in; ++ring.n_out)
-          mbar_wait(bars + warp * C::kStages + ring.n_out % C::kStages,
-                    (ring.n_out / C::kStages) & 1, p.status);
-        ring.alive = false;
-        break;
-      }
-      page<D, NT, kE4m3>(smem + (warp * C::kStages + st) * F::kBlock, pg * kPage,
-                         (ring.shown >> st) & 1u, lane, q, s);
+    for (int pg = mine.first; pg < mine.end && ring.alive; pg += team) {
+      int st;
+      if (!copied<C>(p, ring, st)) break;
+      page<D, NT, kE4m3>(ring.base + st * C::F::kBlock, pg * kPage, (ring.shown >> st) & 1u, lane, q, s);
       __syncwarp();
-      if (pg + C::kStages * kAWarps < end8)
-        issue<D, NT>(p, t, h, pg + C::kStages * kAWarps, end8, warp, lane, smem, bars, ring);
+      if (pg + C::kStages * team < mine.end)
+        issue<C>(p, t, h, pg + C::kStages * team, mine.end, team, lane, ring);
     }
     unscale<D, NT, kE4m3>(s);
-    const bool tail_here = has_tail(t, p1);
-    if (tail_here && warp == (t.n8 - p0) % kAWarps) {
-      const bool got = mbar_wait(tail_bar, tails & 1, p.status);
-      if (__all_sync(0xffffffffu, got) && tail_ok)
-        tail_tokens<D, NT>(p, t, h, smem + C::kTailOff, t.len / kPage * kPage, t.len % kPage, lane,
-                           q, s);
+    if (mine.tail && ring.alive) {
+      if (!ring.tail_issued) issue_tail<C>(p, t, h, lane, ring);
+      int st;
+      if (copied<C>(p, ring, st) && ((ring.shown >> st) & 1u))
+        tail_tokens<D, NT>(p, t, h, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q, s);
+      __syncwarp();
     }
-    tails += tail_here;
 
     // the next unit of this CTA: its copies start before this one is merged
     const Entry tc = t;
     const int hc = h, c0 = p0, c1 = p1;
     const int64_t u0 = unit0;
-    const bool more = u0 + c1 < end;
+    const bool more = kMode == kShares && u0 + c1 < end;
     if (more) {
       unit0 = u0 + tc.pages;
       if (++h == p.hkv) {
@@ -654,7 +817,8 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       }
       p0 = 0;
       p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
-      start_unit<D, NT>(p, t, h, warp, min(p1, t.n8), warp, lane, smem, bars, ring);
+      mine = part_of(t, p0, p1, warp, team);
+      start_part<C>(p, t, h, mine, team, lane, ring);
     }
 
 #pragma unroll
@@ -670,17 +834,19 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           sm_l[(warp * NT + nt) * 8 + 2 * tig + c] = l;
         }
       }
-    __syncthreads();
-    if (more) tail_ok = start_tail(t, h, unit0);
+    team_sync<kMode>(team, number);
     const bool complete = c0 == 0 && c1 == tc.pages;
-    float* slot = p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * C::kSlot;
+    float* slot = kMode == kCluster
+        ? reinterpret_cast<float*>(smem + C::kPartOff)
+        : p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * C::kSlot;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < kAWarps; ++w) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + 2 * tig + c]);
+        for (int w = 0; w < kWarps; ++w)
+          if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + 2 * tig + c]);
         const float a = fast_exp2(s.m[nt][c] - top);
         float* dst = merge + (warp * 8 + 2 * tig + c) * C::kStride + 4 * gid;
 #pragma unroll
@@ -689,49 +855,50 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
               make_float4(s.o[nt][2 * i][c] * a, s.o[nt][2 * i][2 + c] * a,
                           s.o[nt][2 * i + 1][c] * a, s.o[nt][2 * i + 1][2 + c] * a);
       }
-      __syncthreads();
-      if (tid < 8 * D / 4) {
-        const int col = tid / (D / 4), ch = 4 * (tid % (D / 4));
+      team_sync<kMode>(team, number);
+      for (int i = warp * 32 + lane; i < 8 * D / 4; i += 32 * team) {
+        const int col = i / (D / 4), ch = 4 * (i % (D / 4));
+        const int gcol = (tc.tile * NT + nt) * 8 + col;
+        if (kMode != kCluster && gcol >= p.cols) continue;
         float top = kLowest, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kAWarps; ++w) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + col]);
+        for (int w = 0; w < kWarps; ++w)
+          if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + col]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kAWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
+          if (kMode == kTeams && w >= team) break;
           l = fmaf(sm_l[(w * NT + nt) * 8 + col], fast_exp2(sm_m[(w * NT + nt) * 8 + col] - top), l);
           const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
           o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
         }
-        const int gcol = (tc.tile * NT + nt) * 8 + col;
-        if (complete) {
-          if (gcol < p.cols) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zeros
-            const int row = gcol / p.G, g = gcol - row * p.G;
-            uint16_t* dst = p.out +
-                ((static_cast<size_t>(tc.b) * p.m_rows + row) * p.hq + hc * p.G + g) * D + ch;
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
-          }
-        } else if (gcol < p.cols) {
+        if (kMode != kCluster && (kMode == kTeams || complete)) {
+          store_row(p, tc.b, hc, gcol, ch, D, o, l);
+        } else {
           *reinterpret_cast<float4*>(slot + (nt * 8 + col) * D + ch) = o;
           if (ch == 0)
             *reinterpret_cast<float2*>(slot + 8 * NT * D + 2 * (nt * 8 + col)) = make_float2(top, l);
         }
       }
-      __syncthreads();
+      if (kMode != kTeams) __syncthreads();   // before the buffers are written again
     }
+    if constexpr (kMode == kCluster) {
+      merge_cluster<D>(p, tc, hc, slot);
+      return;
+    }
+    if constexpr (kMode == kTeams) return;
     if (!complete && c0 == 0)   // the unit goes on in the next CTAs: they hold its other parts
       owned = make_int4(e, hc, static_cast<int>((u0 + tc.pages - 1) / share) - blockIdx.x + 1, 0);
     if (!more) break;
   }
-  if (tid == 0 && !p.whole_units) p.info[blockIdx.x] = owned;
+  if (tid == 0) p.info[blockIdx.x] = owned;
 }
 
 // Merges the units that lie in several CTAs: block (CTA in which the unit starts,
 // column), thread = channel.
 template <int D, int NT>
 __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
-  using C = Kv8Cfg<D, NT>;
+  using C = Kv8Cfg<D, NT, kShares>;
   __shared__ float w[kMaxCtas];
   __shared__ float red[D / 32];
   pdl_wait();
@@ -783,18 +950,21 @@ __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv
 }
 
 template <typename Kern, typename... Args>
-cudaError_t launch_kv8(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+cudaError_t launch_kv8(Kern kernel, int cluster, dim3 grid, int threads, size_t smem, cudaStream_t st,
                        Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = block;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -802,15 +972,88 @@ cudaError_t launch_kv8(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStre
 // head's columns (a wider unit reads its pages once for all of them).
 inline int column_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
-constexpr int kWholePages = 64;   // see kv8_plan
 constexpr int kMinShare = 8;      // pages of a CTA: one per warp
+constexpr int kMaxCluster = 16;
+constexpr int kTeamPages = 128;
+
+// How many clusters of 1 .. 16 CTAs (one per SM) the current device holds at once;
+// a GPC's SMs bound them (a GB300: 7 of 16, 8 of 12, 15 of 9, 36 of 4, 152 of 1).
+struct ClusterSizes {
+  int active[kMaxCluster + 1];
+};
+
+// (The kernel for d = 128 stands for all: every cluster kernel fills an SM.)
+const ClusterSizes& cluster_sizes() {
+  static std::mutex mu;
+  static std::vector<std::pair<int, ClusterSizes>> known;   // device
+  static const ClusterSizes none{};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return none;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& k : known)
+    if (k.first == dev) return k.second;
+  using C = Kv8Cfg<128, 1, kCluster>;
+  const auto kernel = kv8_attention_kernel<128, 1, false, kCluster>;
+  ClusterSizes s{};
+  if (oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) {
+    for (int c = 1; c <= kMaxCluster; ++c) {
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = static_cast<unsigned>(c);
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(static_cast<unsigned>(c));
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kBytes;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&s.active[c], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        s.active[c] = 0;
+      }
+    }
+  }
+  known.reserve(64);   // references into it stay valid
+  known.emplace_back(dev, s);
+  return known.back().second;
+}
 
 struct Kv8Plan {
-  int nt;
-  bool whole;
+  int nt, cluster, team;   // cluster > 0: CTAs per unit; team > 0: warps per unit
   int64_t tiles, entries, ctas;
   size_t info, total;   // workspace bytes: the CTAs' records, all
 };
+
+// Clusters or shares.  The largest cluster of which the device holds one per unit at a
+// time; its CTA streams its pages at 0.06 us each (d = 128).  Shares run at the memory's
+// rate, 0.00064 us a page over all units, but only over the tokens there are (several
+// sequences: taken as three quarters of the longest, the host does not know the
+// lengths), and cost a second
+// kernel and longer first and last waves, 6 us.  Measured, 8 KV heads: one sequence of
+// 32k 18.6 us against 23.9, of 128k 48.7 against 54.
+inline int cluster_of(int64_t batch, int64_t units, int64_t pages) {
+  const ClusterSizes& s = cluster_sizes();
+  int c = kMaxCluster;
+  while (c > 0 && s.active[c] < units) --c;
+  if (c == 0) return 0;
+  c = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c, pages / 8)));   // half the warps busy
+  const double alone = 0.06 * static_cast<double>(pages) / c;
+  const double ragged = batch > 1 ? 0.75 : 1.0;
+  const double shared = 6.0 + 0.00064 * ragged * static_cast<double>(units) * static_cast<double>(pages);
+  return alone < shared ? c : 0;
+}
+
+// Warps per unit where units are many and short: as many as give every warp slot of the
+// device (16 an SM) about one unit.  0: not this form.  Shares pay a merge and a fill of
+// the rings per unit, teams the spread of lengths; at d = 128, 8 KV heads, teams against
+// shares: 256 sequences of 100-200 tokens 22.8 us against 55.1, 100 of 500-1000 36.5
+// against 45.3, 40 of 1000-2000 33.8 both, 40 of 2000-4000 58.6 against 50.3.
+inline int team_of(int64_t units, int64_t pages, int64_t sms) {
+  if (units <= sms || pages > kTeamPages) return 0;
+  int team = 8;
+  while (team > 1 && (units * team > 16 * sms || team > pages)) team /= 2;
+  return team;
+}
 
 // false: sizes outside the supported range.
 inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int64_t max_len,
@@ -826,31 +1069,44 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
   const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);
   const int64_t resident =
       std::min<int64_t>(kMaxCtas, oscar_host::sm_count() * static_cast<int64_t>(p.nt == 1 ? 2 : 1));
-  p.whole = pages <= kWholePages && units <= resident;
-  p.ctas = p.whole ? units : std::min(resident, (units * pages + kMinShare - 1) / kMinShare);
+  if (p.nt == 1) {
+    p.team = team_of(units, pages, oscar_host::sm_count());
+    if (!p.team) p.cluster = cluster_of(batch, units, pages);
+  }
+  p.ctas = p.team      ? (units * p.team + 7) / 8
+           : p.cluster ? units * p.cluster
+                       : std::min(resident, (units * pages + kMinShare - 1) / kMinShare);
   const int d = c->head_dim;
   p.info = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
-  p.total = p.whole ? 16
-                    : p.info + static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (d + 2) * sizeof(float);
+  p.total = p.cluster || p.team
+                ? 16
+                : p.info + static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (d + 2) * sizeof(float);
   *out = p;
   return true;
 }
 
+template <int D, int NT, bool kE4m3, Kv8Mode kMode>
+oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
+  using C = Kv8Cfg<D, NT, kMode>;
+  const auto kernel = kv8_attention_kernel<D, NT, kE4m3, kMode>;
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, kMode == kCluster))
+    return OSCAR_ERR_CUDA;
+  return launch_kv8(kernel, kMode == kCluster ? pl.cluster : 1, dim3(static_cast<unsigned>(pl.ctas)),
+                    C::kThreads, C::kBytes, st, p, kMinShare) == cudaSuccess
+             ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
 template <int D, int NT, bool kE4m3>
 oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  using C = Kv8Cfg<D, NT>;
-  const auto kernel = kv8_attention_kernel<D, NT, kE4m3>;
-  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes))
-    return OSCAR_ERR_CUDA;
-  if (launch_kv8(kernel, dim3(static_cast<unsigned>(pl.ctas)), dim3(kAThreads), C::kBytes, st, p,
-                 kMinShare) != cudaSuccess)
-    return OSCAR_ERR_CUDA;
-  if (!pl.whole &&
-      launch_kv8(kv8_merge_kernel<D, NT>,
-                 dim3(static_cast<unsigned>(pl.ctas), static_cast<unsigned>(std::min(p.cols, 8 * NT))),
-                 dim3(D), 0, st, p) != cudaSuccess)
-    return OSCAR_ERR_CUDA;
-  return OSCAR_OK;
+  if constexpr (NT == 1) {
+    if (pl.team) return launch_attention<D, 1, kE4m3, kTeams>(p, pl, st);
+    if (pl.cluster) return launch_attention<D, 1, kE4m3, kCluster>(p, pl, st);
+  }
+  const oscar_status s = launch_attention<D, NT, kE4m3, kShares>(p, pl, st);
+  if (s != OSCAR_OK) return s;
+  const dim3 grid(static_cast<unsigned>(pl.ctas), static_cast<unsigned>(std::min(p.cols, 8 * NT)));
+  return launch_kv8(kv8_merge_kernel<D, NT>, 1, grid, D, 0, st, p) == cudaSuccess ? OSCAR_OK
+                                                                                 : OSCAR_ERR_CUDA;
 }
 
 template <int D, bool kE4m3>
@@ -933,7 +1189,8 @@ oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, cons
   p.tiles = static_cast<int>(pl.tiles);
   p.entries = static_cast<int>(pl.entries);
   p.max_len = max_seq_len;
-  p.whole_units = pl.whole ? 1 : 0;
+  p.cluster = pl.cluster;
+  p.team = pl.team;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(desc->head_dim)));
   p.info = static_cast<int4*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.info);

@@ -59,6 +59,7 @@ struct PagesParams {
   int64_t* slots;
   int32_t* status;
   int fill;   // the scan's CTA also writes rows and table entries
+  int wide;   // the row lists take 16-byte stores
 };
 
 __device__ __forceinline__ int pages_held(int n, int hold) {
@@ -81,28 +82,55 @@ __device__ __forceinline__ int fresh_page(const PagesParams& p, int first, int p
   return at < p.n_free ? p.free_pages[at] : -1;
 }
 
-// Rows and new table entries, `i` of `n` workers.
+// Rows and new table entries, `i` of `n` workers.  A worker writes runs of four rows:
+// one bisection, then the next sequence where its rows end.
 __device__ __forceinline__ void fill_rows(const PagesParams& p, int64_t i, int64_t n) {
   const int64_t rows = p.row_starts[p.batch];
-  for (int64_t r = i; r < p.max_rows; r += n) {
-    int b = -1, pos = -1;
-    int64_t slot = -1;
-    if (r < rows) {
-      b = sequence_of(p.row_starts, p.batch, static_cast<int>(r));
-      const int start = p.row_starts[b], after = p.lens_after[b];
-      const int before = after - (p.row_starts[b + 1] - start);
-      pos = before + static_cast<int>(r) - start;
-      const int pg = pos / kPage;
-      if (p.slots && pg < p.max_pages && pg < pages_held(after, p.hold)) {
-        const int held = pages_held(before, p.hold);
+  for (int64_t r0 = 4 * i; r0 < p.max_rows; r0 += 4 * n) {
+    int b = -1, end = -1, start = 0, before = 0, held = 0, holds = 0;   // of the run's current sequence
+    int ids[4], pos[4];
+    int64_t slot[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = r0 + j;
+      ids[j] = pos[j] = -1;
+      slot[j] = -1;
+      if (r >= rows || r >= p.max_rows) continue;
+      if (r >= end) {
+        if (b < 0) b = sequence_of(p.row_starts, p.batch, static_cast<int>(r));
+        else while (p.row_starts[b + 1] <= r) ++b;
+        start = p.row_starts[b];
+        end = p.row_starts[b + 1];
+        const int after = p.lens_after[b];
+        before = after - (end - start);
+        held = pages_held(before, p.hold);
+        holds = min(pages_held(after, p.hold), p.max_pages);
+      }
+      ids[j] = b;
+      pos[j] = before + static_cast<int>(r) - start;
+      const int pg = pos[j] / kPage;
+      if (p.slots && pg < holds) {
         const int id = pg >= held ? fresh_page(p, p.page_starts[b], pg, held)
                                   : p.table[static_cast<size_t>(b) * p.max_pages + pg];
-        if (id >= 0) slot = static_cast<int64_t>(id) * kPage + pos % kPage;
+        if (id >= 0) slot[j] = static_cast<int64_t>(id) * kPage + pos[j] % kPage;
       }
     }
-    p.seq_ids[r] = b;
-    p.positions[r] = pos;
-    if (p.slots) p.slots[r] = slot;
+    if (p.wide && r0 + 4 <= p.max_rows) {
+      *reinterpret_cast<int4*>(p.seq_ids + r0) = make_int4(ids[0], ids[1], ids[2], ids[3]);
+      *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (p.slots) {
+        reinterpret_cast<longlong2*>(p.slots + r0)[0] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2*>(p.slots + r0)[1] = make_longlong2(slot[2], slot[3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r0 + j >= p.max_rows) break;
+        p.seq_ids[r0 + j] = ids[j];
+        p.positions[r0 + j] = pos[j];
+        if (p.slots) p.slots[r0 + j] = slot[j];
+      }
+    }
   }
   const int first = p.page_starts[0];
   const int64_t fresh = static_cast<int64_t>(p.page_starts[p.batch]) - first;
@@ -198,6 +226,7 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(const __grid_
 // ----------------------------------------------------------------------- rotary
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;   // per CTA, at most
 
 struct RopeParams {
   int hq, hkv, d, half, tokens;   // half: rotated pairs per head; tokens per CTA
@@ -212,24 +241,98 @@ struct RopeParams {
   int copy;   // the output is not the input: unrotated channels are copied
 };
 
-__device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, float2 c0, float2 c1, uint32_t& x,
-                                        uint32_t& y) {
+// Two pairs (low and high halves of a and b); r: cos, sin of the first, of the second.
+__device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, float4 r, uint32_t& x, uint32_t& y) {
   const float a0 = bf16_lo_value(a), a1 = bf16_hi_value(a);
   const float b0 = bf16_lo_value(b), b1 = bf16_hi_value(b);
-  x = pack_bf162(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-  y = pack_bf162(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+  x = pack_bf162(a0 * r.x - b0 * r.y, a1 * r.z - b1 * r.w);
+  y = pack_bf162(b0 * r.x + a0 * r.y, b1 * r.z + a1 * r.w);
 }
 
-// kInter: pairs (2i, 2i + 1), else (i, i + half).  kVec: 16-byte accesses (the
-// rotated part in runs of 8 channels, pointers and strides 16-byte aligned), else
-// one pair, or one unrotated channel, at a time.
+// One item of a head vector: a run of rotated pairs (it < pairs), else of channels that
+// are copied.  kInter: pairs (2i, 2i + 1), else (i, i + half).  kVec: 16-byte accesses
+// (the rotated part in runs of 8 channels, pointers and strides 16-byte aligned), else
+// one pair, or one channel, at a time.  Loading and storing are apart so that a thread
+// has the loads of two items in flight.
+template <bool kInter, bool kVec>
+struct RopeItem {
+  uint4 a, b;
+  uint16_t* dst;
+  const float2* c;
+
+  __device__ __forceinline__ void load(const RopeParams& p, const float2* cs, int64_t row, int t, int h,
+                                       int it, int pairs) {
+    const uint16_t* src;
+    if (h < p.hq) {
+      src = p.q + row * p.q_stride + h * p.d;
+      dst = p.q_out + row * p.q_out_stride + h * p.d;
+    } else {
+      src = p.k + row * p.k_stride + (h - p.hq) * p.d;
+      dst = p.k_out + row * p.k_out_stride + (h - p.hq) * p.d;
+    }
+    c = cs + t * p.half;
+    constexpr int kRun = kVec ? 8 : 1;
+    if (it >= pairs) {
+      const int ch = 2 * p.half + (it - pairs) * kRun;
+      dst += ch;
+      if constexpr (kVec) a = *reinterpret_cast<const uint4*>(src + ch);
+      else a.x = src[ch];
+    } else if constexpr (kVec) {
+      dst += 8 * it;
+      c += (kInter ? 4 : 8) * it;
+      a = *reinterpret_cast<const uint4*>(src + 8 * it);
+      if constexpr (!kInter) b = *reinterpret_cast<const uint4*>(src + p.half + 8 * it);
+    } else {
+      const int at = kInter ? 2 * it : it;
+      dst += at;
+      c += it;
+      a.x = src[at];
+      b.x = src[at + (kInter ? 1 : p.half)];
+    }
+  }
+
+  __device__ __forceinline__ void store(const RopeParams& p, int it, int pairs) const {
+    if (it >= pairs) {
+      if constexpr (kVec) *reinterpret_cast<uint4*>(dst) = a;
+      else *dst = static_cast<uint16_t>(a.x);
+    } else if constexpr (!kVec) {
+      const float x = bf16_to_float(static_cast<uint16_t>(a.x));
+      const float y = bf16_to_float(static_cast<uint16_t>(b.x));
+      dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x * c->x - y * c->y));
+      dst[kInter ? 1 : p.half] = __bfloat16_as_ushort(__float2bfloat16_rn(y * c->x + x * c->y));
+    } else if constexpr (kInter) {
+      const float4* r = reinterpret_cast<const float4*>(c);   // two pairs each
+      const float4 r0 = r[0], r1 = r[1];
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(turn(a.x, r0.x, r0.y), turn(a.y, r0.z, r0.w), turn(a.z, r1.x, r1.y),
+                     turn(a.w, r1.z, r1.w));
+    } else {
+      const float4* r = reinterpret_cast<const float4*>(c);
+      uint4 x, y;
+      rotate2(a.x, b.x, r[0], x.x, y.x);
+      rotate2(a.y, b.y, r[1], x.y, y.y);
+      rotate2(a.z, b.z, r[2], x.z, y.z);
+      rotate2(a.w, b.w, r[3], x.w, y.w);
+      *reinterpret_cast<uint4*>(dst) = x;
+      *reinterpret_cast<uint4*>(dst + p.half) = y;
+    }
+  }
+
+  static __device__ __forceinline__ uint32_t turn(uint32_t w, float c, float s) {
+    const float x = bf16_lo_value(w), y = bf16_hi_value(w);
+    return pack_bf162(x * c - y * s, y * c + x * s);
+  }
+};
+
 template <bool kInter, bool kVec>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 cs[];   // [tokens][half]: A cos, A sin
+  extern __shared__ __align__(16) float2 cs[];   // [tokens][half]: A cos, A sin
+  __shared__ int pos[kRopeTokens];
   pdl_wait();
   pdl_trigger();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.n - t0));
+  if (threadIdx.x < nt) pos[threadIdx.x] = p.positions[t0 + threadIdx.x];
   for (int i = threadIdx.x; i < nt * p.half; i += kRopeThreads) {
     const int t = i / p.half, j = i - t * p.half;
     const int m = p.positions[t0 + t];
@@ -245,48 +348,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   // items of a head: rotated pairs in runs, then the unrotated channels in runs
   const int pairs = kVec ? (kInter ? p.half / 4 : p.half / 8) : p.half;
   const int items = pairs + (p.copy ? (p.d - 2 * p.half) / kRun : 0);
-  const int total = nt * heads * items;
-  for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-    const int th = i / items, it = i - th * items;
-    const int t = th / heads, h = th - t * heads;
-    if (p.positions[t0 + t] < 0) continue;   // a padded row: left as it was
-    const uint16_t* src = h < p.hq ? p.q + (t0 + t) * p.q_stride + h * p.d
-                                   : p.k + (t0 + t) * p.k_stride + (h - p.hq) * p.d;
-    uint16_t* dst = h < p.hq ? p.q_out + (t0 + t) * p.q_out_stride + h * p.d
-                             : p.k_out + (t0 + t) * p.k_out_stride + (h - p.hq) * p.d;
-    const float2* c = cs + t * p.half;
-    if (it >= pairs) {
-      const int ch = 2 * p.half + (it - pairs) * kRun;
-      if constexpr (kVec) *reinterpret_cast<uint4*>(dst + ch) = *reinterpret_cast<const uint4*>(src + ch);
-      else dst[ch] = src[ch];
-    } else if constexpr (!kVec) {
-      const int a = kInter ? 2 * it : it, b = kInter ? 2 * it + 1 : it + p.half;
-      const float x = bf16_to_float(src[a]), y = bf16_to_float(src[b]);
-      const float2 w = c[it];
-      dst[a] = __bfloat16_as_ushort(__float2bfloat16_rn(x * w.x - y * w.y));
-      dst[b] = __bfloat16_as_ushort(__float2bfloat16_rn(y * w.x + x * w.y));
-    } else if constexpr (kInter) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * it);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float2 r = c[4 * it + x];
-        const float a = bf16_lo_value(w[x]), b = bf16_hi_value(w[x]);
-        o[x] = pack_bf162(a * r.x - b * r.y, b * r.x + a * r.y);
+  // A thread keeps its item and steps over heads and tokens: one division in all.
+  // Items beyond the threads go round again; threads left over do nothing.
+  const int step = max(1, kRopeThreads / items);
+  const int first = threadIdx.x / items;
+  if (first >= step) return;
+  for (int it = threadIdx.x - first * items; it < items; it += kRopeThreads) {
+    int t = 0, h = first;
+    auto settle = [&] {   // on to the next head that exists, in a row that is not padding
+      while (true) {
+        for (; h >= heads && t < nt; h -= heads) ++t;
+        if (t >= nt || pos[t] >= 0) return;
+        h += step;
       }
-      *reinterpret_cast<uint4*>(dst + 8 * it) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * it);
-      const uint4 b = *reinterpret_cast<const uint4*>(src + p.half + 8 * it);
-      uint4 x, y;
-      const float2* r = c + 8 * it;
-      rotate2(a.x, b.x, r[0], r[1], x.x, y.x);
-      rotate2(a.y, b.y, r[2], r[3], x.y, y.y);
-      rotate2(a.z, b.z, r[4], r[5], x.z, y.z);
-      rotate2(a.w, b.w, r[6], r[7], x.w, y.w);
-      *reinterpret_cast<uint4*>(dst + 8 * it) = x;
-      *reinterpret_cast<uint4*>(dst + p.half + 8 * it) = y;
+    };
+    settle();
+    while (t < nt) {
+      RopeItem<kInter, kVec> x, y;
+      x.load(p, cs, t0 + t, t, h, it, pairs);
+      h += step;
+      settle();
+      const bool two = t < nt;
+      if (two) {
+        y.load(p, cs, t0 + t, t, h, it, pairs);
+        h += step;
+        settle();
+      }
+      x.store(p, it, pairs);
+      if (two) y.store(p, it, pairs);
     }
   }
 }
@@ -330,12 +419,14 @@ oscar_status oscar_extend_pages(int32_t* page_table, int32_t max_pages_per_seq, 
   p.slots = slots;
   p.status = status;
   p.fill = max_rows <= kInlineRows ? 1 : 0;
+  p.wide = ((reinterpret_cast<uintptr_t>(seq_ids) | reinterpret_cast<uintptr_t>(positions) |
+             reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
   cudaLaunchAttribute attr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(kScanThreads), 0, st, &attr);
   if (cudaLaunchKernelEx(&cfg, extend_scan_kernel, p) != cudaSuccess) return OSCAR_ERR_CUDA;
   if (!p.fill) {
-    const int64_t want = (max_rows + kFillThreads - 1) / kFillThreads;
+    const int64_t want = (max_rows + 4 * kFillThreads - 1) / (4 * kFillThreads);
     const int64_t most = static_cast<int64_t>(oscar_host::sm_count()) * 8;
     cfg = pdl_config(dim3(static_cast<unsigned>(std::min(want, most))), dim3(kFillThreads), 0, st, &attr);
     if (cudaLaunchKernelEx(&cfg, extend_fill_kernel, p) != cudaSuccess) return OSCAR_ERR_CUDA;
@@ -414,7 +505,12 @@ oscar_status oscar_rope(const void* q, const void* k, const int32_t* positions,
         reinterpret_cast<uintptr_t>(num_kv_heads ? k : nullptr) |
         reinterpret_cast<uintptr_t>(num_q_heads ? q_out : nullptr) |
         reinterpret_cast<uintptr_t>(num_kv_heads ? k_out : nullptr)) & 15) == 0;
-  p.tokens = 4;
+  // About four items a thread: fewer leave the angles' cost bare, more make the last,
+  // partly filled wave of CTAs long (72 heads x 16 items, 5003 tokens: 4 tokens a CTA
+  // 55.9 us, one token a CTA 31.5 us).
+  const int64_t items = heads * (vec ? (p.half / (interleaved ? 4 : 8) + (p.copy ? (head_dim - rotary_dim) / 8 : 0))
+                                     : (p.half + (p.copy ? head_dim - rotary_dim : 0)));
+  p.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, 4 * kRopeThreads / items)));
   const int64_t ctas = (n + p.tokens - 1) / p.tokens;
   if (ctas > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(p.tokens) * p.half * sizeof(float2);

@@ -191,6 +191,24 @@ def test_many_short_sequences():
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("batch,hkv,d,lo,hi", [
+    (170, 1, 64, 1, 90), (330, 2, 64, 0, 60), (330, 4, 128, 0, 40), (900, 3, 64, 0, 33),
+    (90, 2, 128, 1, 2300), (3, 60, 128, 2000, 2400), (200, 1, 64, 2000, 2200)])
+def test_every_split_of_the_work(fmt, batch, hkv, d, lo, hi):
+    """Teams of 8, 4, 2 and 1 warps, and equal shares over many units: sampled units."""
+    rng = np.random.default_rng(hi)
+    lens = rng.integers(lo, hi + 1, batch)
+    lens[0], lens[-1] = lo, hi
+    s = K.Sequences(batch, hkv, 2 * hkv, d, fmt, hi, seed=batch)
+    s.place(lens)
+    q = K.queries(s.rng, batch, 1, 2 * hkv, d)
+    got = s.attend(q)
+    heads = {(int(b), int(h)) for b, h in zip(rng.integers(0, batch, 60), rng.integers(0, hkv, 60))}
+    s.check_attention(got, q, heads=heads | {(0, 0), (batch - 1, hkv - 1)})
+    assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_scales_of_values_and_queries(fmt):
     """Value scales that differ by 2^20 from page to page, in both directions; queries from
     1e-20 to 1e4 (logits to saturation)."""
