@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liboscar.so")
 SOURCES = ["host_rotation.cpp", "quantize.cu", "decode.cu", "calib.cu",
-           "kv8_attention.cu", "kv8_cache.cu", "positions.cu"]
+           "kv8_attention.cu", "kv8_rows.cu", "kv8_cache.cu", "positions.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -42,34 +42,9 @@
 #include <utility>
 #include <vector>
 
-#include "common.cuh"
-#include "kv8_layout.cuh"
+#include "kv8_units.cuh"
 
 namespace oscar {
-
-constexpr int kMaxCtas = 1024;
-constexpr float kLowest = -3.402823466e38f;   // running maximum before the first logit
-constexpr float kLag = 8.f;                   // the maximum is raised when passed by 2^8
-
-struct Kv8Params {
-  int hkv, hq, G, max_pages;
-  int64_t n_pages, n_tails;
-  const uint8_t* pool;
-  const uint8_t* tail;
-  const int32_t* page_table;
-  const int32_t* tail_ids;
-  int32_t* status;
-  const uint16_t* q;
-  uint16_t* out;
-  const int32_t* seq_lens;
-  const int32_t* q_pos;    // null: one row per sequence, at its last token
-  int m_rows, cols, tiles, entries, max_len;   // cols = m_rows * G; entries = batch * tiles
-  int cluster;             // CTAs per unit when clusters serve units
-  int team;                // warps per unit when teams of warps do
-  float scale_log2;
-  int4* info;              // per CTA: unit entry, KV head, parts of the unit that starts in it
-  float* part;             // [2 * CTAs][8 * NT * (D + 2)]
-};
 
 enum Kv8Mode { kShares, kCluster, kTeams };
 
@@ -84,7 +59,7 @@ struct Kv8Cfg {
   static constexpr int kStride = D + 4;                     // floats per column when merging
   static constexpr int kMerge = kWarps * 8 * kStride * 4;
   static constexpr int kStat = kWarps * 8 * NT * 4;         // one of m, l
-  static constexpr int kSlot = 8 * NT * (D + 2);            // floats of one partial
+  static constexpr int kSlot = kv8_slot<D, NT>();
   static constexpr int kMergeOff = kWarps * kWarpRing;
   static constexpr int kStatOff = kMergeOff + kMerge;
   static constexpr int kPartOff = kStatOff + 2 * kStat;     // a cluster's CTA: its partial
@@ -93,38 +68,6 @@ struct Kv8Cfg {
   static_assert(kMode == kShares || NT == 1, "clusters and teams serve one tile of columns per unit");
   static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
 };
-
-// A sequence's tile of query columns: pages it has to visit (at least one, so that
-// a tile that sees nothing still writes its zeros).
-struct Entry {
-  int b, tile, len, vis, n8, pages;
-};
-
-__device__ __forceinline__ int row_limit(const Kv8Params& p, int b, int row, int len) {
-  const int pos = p.q_pos[static_cast<size_t>(b) * p.m_rows + row];
-  return pos >= 0 && pos < len ? pos + 1 : 0;
-}
-
-template <int NT>
-__device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
-  Entry t;
-  t.b = e / p.tiles;
-  t.tile = e - t.b * p.tiles;
-  const int len = p.seq_lens[t.b];
-  t.len = len >= 0 && len <= p.max_len ? len : 0;
-  if (p.q_pos) {
-    const int r0 = t.tile * 8 * NT / p.G;
-    const int r1 = min(p.cols - 1, t.tile * 8 * NT + 8 * NT - 1) / p.G;
-    t.vis = 0;
-    for (int r = r0; r <= r1; ++r) t.vis = max(t.vis, row_limit(p, t.b, r, t.len));
-  } else {
-    t.vis = t.len;
-  }
-  const int whole = t.len / kPage;
-  t.n8 = min(whole, (t.vis + kPage - 1) / kPage);
-  t.pages = max(1, t.n8 + (t.vis > whole * kPage ? 1 : 0));
-  return t;
-}
 
 // The columns of one unit as a lane sees them: operands for column gid of each
 // tile, factors and limits for columns 2tig and 2tig + 1.
@@ -136,14 +79,6 @@ struct Query {
   int vis[NT][2];
   int vis_min;          // smallest over the unit's columns
 };
-
-// First element of column `col` of the tile; null when the tile has fewer columns.
-__device__ __forceinline__ const uint16_t* column(const Kv8Params& p, const Entry& t, int h,
-                                                  int col, int D) {
-  if (col >= p.cols) return nullptr;
-  const int row = col / p.G, g = col - row * p.G;
-  return p.q + ((static_cast<size_t>(t.b) * p.m_rows + row) * p.hq + h * p.G + g) * D;
-}
 
 template <int D, int NT, bool kE4m3>
 __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, int h, int lane,
@@ -568,61 +503,6 @@ __device__ __forceinline__ void start_part(const Kv8Params& p, const Entry& t, i
   }
 }
 
-constexpr int kScanWarps = 8;   // the CTAs that find their share
-
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kScanWarps; ++w) total += scratch[w];
-  __syncthreads();
-  return total;
-}
-
-// The entry that holds page `at` of the entries laid end to end (each weighed by
-// the KV heads), and the pages before it.
-template <int NT>
-__device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int& entry,
-                           int64_t& before) {
-  __shared__ int found;
-  __shared__ int64_t found_before;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t base = 0;
-  if (tid == 0) found = -1;
-  __syncthreads();
-  for (int e0 = 0; e0 < p.entries; e0 += 32 * kScanWarps) {
-    const int e = e0 + tid;
-    const int64_t v = e < p.entries ? static_cast<int64_t>(entry_of<NT>(p, e).pages) * p.hkv : 0;
-    int64_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int64_t off = base, all = base;
-#pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-      if (w < warp) off += scratch[w];
-      all += scratch[w];
-    }
-    incl += off;
-    if (v > 0 && incl - v <= at && at < incl) {
-      found = e;
-      found_before = incl - v;
-    }
-    __syncthreads();
-    if (found >= 0) break;
-    base = all;
-  }
-  entry = found;
-  before = found_before;
-}
-
 // Channels ch .. ch + 3 of an output row; a row that sees nothing (l = 0) gets zeros.
 __device__ __forceinline__ void store_row(const Kv8Params& p, int b, int h, int gcol, int ch, int D,
                                           float4 o, float l) {
@@ -740,30 +620,19 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     at = static_cast<int64_t>(t.pages) * rank / p.cluster;
     end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
   } else {
-    __shared__ int64_t scratch[kScanWarps];
-    int64_t sum = 0;
-    if (p.entries == 1) {
-      t = entry_of<NT>(p, 0);
-      sum = t.pages;
-    } else {
-      for (int i = tid; i < p.entries; i += C::kThreads) sum += entry_of<NT>(p, i).pages;
-      sum = block_sum(sum, scratch);
-    }
-    const int64_t total = sum * p.hkv;
-    share = max(static_cast<int64_t>(min_share), (total + gridDim.x - 1) / gridDim.x);
-    at = blockIdx.x * share;
-    end = min(total, at + share);
-    if (at >= end) {
+    __shared__ int64_t scratch[kWarps];
+    Share sh;
+    if (!find_share<NT, kWarps>(p, min_share, scratch, sh)) {
       if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }
-    int64_t before = 0;
-    if (p.entries > 1) {
-      find_entry<NT>(p, at, scratch, e, before);
-      t = entry_of<NT>(p, e);
-    }
-    h = static_cast<int>((at - before) / t.pages);
-    unit0 = before + static_cast<int64_t>(h) * t.pages;
+    at = sh.at;
+    end = sh.end;
+    share = sh.share;
+    unit0 = sh.unit0;
+    e = sh.e;
+    h = sh.h;
+    t = sh.t;
   }
 
   Ring ring{smem + (tid >> 5) * C::kWarpRing, bars + (tid >> 5) * C::kStages, 0, 0, 0, 0, true, false};
@@ -898,7 +767,7 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 // column), thread = channel.
 template <int D, int NT>
 __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
-  using C = Kv8Cfg<D, NT, kShares>;
+  constexpr int kSlot = kv8_slot<D, NT>();
   __shared__ float w[kMaxCtas];
   __shared__ float red[D / 32];
   pdl_wait();
@@ -912,7 +781,7 @@ __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv
   // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
   auto slot = [&](int j) {
     const size_t cta = blockIdx.x + static_cast<size_t>(j);
-    return p.part + (2 * cta + (j == 0 ? 1 : 0)) * C::kSlot;
+    return p.part + (2 * cta + (j == 0 ? 1 : 0)) * kSlot;
   };
   float top = kLowest;
   for (int j = tid; j < n; j += D) top = fmaxf(top, slot(j)[8 * NT * D + 2 * col]);
@@ -941,7 +810,7 @@ __global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv
 #pragma unroll 8
   for (int j = 1; j < n; ++j) {
     acc = fmaf(w[j], *next, acc);
-    next += 2 * C::kSlot;
+    next += 2 * kSlot;
   }
   const int row = gcol / p.G, g = gcol - row * p.G;
   const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
@@ -968,11 +837,11 @@ cudaError_t launch_kv8(Kern kernel, int cluster, dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Query columns of a unit in tiles of 8: 1, 2 or 4, the fewest that hold a KV
-// head's columns (a wider unit reads its pages once for all of them).
-inline int column_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+// Query columns of a unit in tiles of 8: 1 or 2, the fewest that hold a KV head's
+// columns, and beyond them units of 128 (kv8_rows.cu).
+inline int column_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : kRowsNT; }
 
-constexpr int kMinShare = 8;      // pages of a CTA: one per warp
+constexpr int kMinShare = 8;      // pages of a CTA: one per warp, or a tile of 128 tokens
 constexpr int kMaxCluster = 16;
 constexpr int kTeamPages = 128;
 
@@ -1096,24 +965,24 @@ oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_
              ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-template <int D, int NT, bool kE4m3>
-oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  if constexpr (NT == 1) {
-    if (pl.team) return launch_attention<D, 1, kE4m3, kTeams>(p, pl, st);
-    if (pl.cluster) return launch_attention<D, 1, kE4m3, kCluster>(p, pl, st);
-  }
-  const oscar_status s = launch_attention<D, NT, kE4m3, kShares>(p, pl, st);
-  if (s != OSCAR_OK) return s;
+template <int D, int NT>
+oscar_status launch_merge(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(pl.ctas), static_cast<unsigned>(std::min(p.cols, 8 * NT)));
   return launch_kv8(kv8_merge_kernel<D, NT>, 1, grid, D, 0, st, p) == cudaSuccess ? OSCAR_OK
                                                                                  : OSCAR_ERR_CUDA;
 }
 
 template <int D, bool kE4m3>
-oscar_status run_kv8_nt(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  return pl.nt == 1   ? run_kv8<D, 1, kE4m3>(p, pl, st)
-         : pl.nt == 2 ? run_kv8<D, 2, kE4m3>(p, pl, st)
-                      : run_kv8<D, 4, kE4m3>(p, pl, st);
+oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
+  if (pl.team) return launch_attention<D, 1, kE4m3, kTeams>(p, pl, st);
+  if (pl.cluster) return launch_attention<D, 1, kE4m3, kCluster>(p, pl, st);
+  const oscar_status s = pl.nt == 1   ? launch_attention<D, 1, kE4m3, kShares>(p, pl, st)
+                         : pl.nt == 2 ? launch_attention<D, 2, kE4m3, kShares>(p, pl, st)
+                                      : run_kv8_rows(p, D, kE4m3, pl.ctas, kMinShare, st);
+  if (s != OSCAR_OK) return s;
+  return pl.nt == 1   ? launch_merge<D, 1>(p, pl, st)
+         : pl.nt == 2 ? launch_merge<D, 2>(p, pl, st)
+                      : launch_merge<D, kRowsNT>(p, pl, st);
 }
 
 }  // namespace oscar
@@ -1197,8 +1066,8 @@ oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = desc->format == OSCAR_KV8_E4M3;
   if (desc->head_dim == 128)
-    return e4m3 ? run_kv8_nt<128, true>(p, pl, st) : run_kv8_nt<128, false>(p, pl, st);
-  return e4m3 ? run_kv8_nt<64, true>(p, pl, st) : run_kv8_nt<64, false>(p, pl, st);
+    return e4m3 ? run_kv8<128, true>(p, pl, st) : run_kv8<128, false>(p, pl, st);
+  return e4m3 ? run_kv8<64, true>(p, pl, st) : run_kv8<64, false>(p, pl, st);
 }
 
 }  // extern "C"

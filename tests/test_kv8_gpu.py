@@ -166,6 +166,68 @@ def test_rows_match_oracle(fmt, d, hkv, g, m):
     s.check_attention(got, q, pos)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,hkv,g,m", [(128, 2, 1, 17), (64, 1, 2, 64), (128, 1, 4, 33), (128, 1, 2, 130),
+                                       (64, 3, 8, 18)])
+def test_many_rows_match_oracle(fmt, d, hkv, g, m):
+    """More query columns than the decode form holds, one tile of 128 and several: every
+    number of pages in the last tile of tokens, with and without a tail behind it, rows at
+    the end, all over, and padded."""
+    lens = [5, 16, 16 * 3 + 1, 16 * 6 + 15, 16 * 7 + 4, 16 * 8, 16 * 8 + 2, 16 * 11 + 9, 16 * 15 + 3,
+            16 * 20, 1333, 0, 2500]
+    b = len(lens)
+    s = K.Sequences(b, hkv, hkv * g, d, fmt, 2500, seed=m + d)
+    s.place(lens)
+    q = K.queries(s.rng, b, m, hkv * g, d)
+    pos = np.array([[L - m + i for i in range(m)] for L in lens])
+    pos[pos < 0] = -1
+    pos[10] = s.rng.integers(0, 1333, m)
+    got = s.attend(q, pos)
+    assert (got[pos < 0] == 0).all()
+    # all the short sequences, and of the long ones every third row
+    s.check_attention(got[:10], q[:10], pos[:10], lens=np.array(lens[:10]))
+    thin, some = pos.copy(), got.copy()
+    keep = np.arange(m) % 3 == 0
+    thin[:, ~keep], some[:, ~keep] = -1, 0
+    s.check_attention(some, q, thin, heads={(i, h) for i in (10, 11, 12) for h in range(hkv)})
+    assert H.status(s.cache) == 0
+    pos[0, 0] = 5
+    assert (s.attend(q, pos)[0, 0] == 0).all() and H.status(s.cache) == H.lib().DEVERR_SEQ_LEN
+
+
+def test_many_rows_with_odd_tails_and_bad_pages():
+    """NaN and infinities in the tail reach the rows that see them only; refused pages and
+    tails are left out and reported."""
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(2, 1, 2, 64, kv8.INT8, 700)
+    k, v = K.draw(s.rng, 90 + 650, 1, 64)
+    v[85, 0, 7], v[86, 0, 9], k[88, 0, 3] = np.nan, np.inf, np.nan
+    s.place([90, 650], k, v)
+    pos = np.array([[79, 84, 85, 86, 87, 88, 89, 80, -1] * 3, np.arange(650 - 27, 650)])
+    q = K.queries(s.rng, 2, 27, 2, 64)
+    got = s.attend(q, pos)
+    for i in (0, 9, 18):
+        assert np.isfinite(got[0, [i, i + 1, i + 7, i + 8]]).all()
+        assert np.isnan(got[0, i + 2, :, 7]).all() and np.isfinite(np.delete(got[0, i + 2], 7, -1)).all()
+        assert np.isinf(got[0, i + 3, :, 9]).all() and np.isnan(got[0, i + 5]).all()
+    clean, seen = got.copy(), pos.copy()
+    for i in range(27):
+        if i % 9 in (2, 3, 4, 5, 6):
+            clean[0, i], seen[0, i] = 0, -1
+    s.check_attention(clean, q, seen)
+    s.cache.page_table[1, 3] = -1
+    s.cache.page_table[1, 33] = s.cache.pool.shape[0]
+    got = s.attend(q, pos)
+    assert H.status(s.cache) == L.DEVERR_PAGE_ID
+    s.check_attention(got, q, pos, drop=(3, 33), heads={(1, 0)})
+    s.cache.page_table.copy_(t.from_numpy(s.table))
+    s.cache.status.zero_()
+    s.cache.tail_ids = s.i32([0, -1])
+    got = s.attend(q, pos)
+    assert H.status(s.cache) == L.DEVERR_PAGE_ID
+    s.check_attention(got, q, pos, drop=(40,), heads={(1, 0)})
+
+
 @pytest.mark.parametrize("fmt,hkv,g", [(kv8.INT8, 8, 4), (kv8.E4M3, 2, 8)])
 def test_long_context(fmt, hkv, g):
     """One sequence over every CTA of the grid."""
@@ -209,9 +271,10 @@ def test_every_split_of_the_work(fmt, batch, hkv, d, lo, hi):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_scales_of_values_and_queries(fmt):
+@pytest.mark.parametrize("m", [1, 3, 6])
+def test_scales_of_values_and_queries(fmt, m):
     """Value scales that differ by 2^20 from page to page, in both directions; queries from
-    1e-20 to 1e4 (logits to saturation)."""
+    1e-20 to 1e4 (logits to saturation); each form of the kernel."""
     s = K.Sequences(2, 1, 4, 128, fmt, 1500, seed=9)
     k, v = K.draw(s.rng, 1500 + 900, 1, 128)
     grow = np.exp2(np.arange(1500) // 16 % 41 - 20.0)[:, None, None].astype(np.float32)
@@ -219,8 +282,9 @@ def test_scales_of_values_and_queries(fmt):
     v[1500:] /= grow[:900]
     s.place([1500, 900], k, v)
     for scale in (1e-20, 1.0, 1e4):
-        q = K.queries(s.rng, 2, 1, 4, 128, scale)
-        s.check_attention(s.attend(q), q)
+        q = K.queries(s.rng, 2, m, 4, 128, scale)
+        pos = None if m == 1 else np.array([[1500 - m + i for i in range(m)], [900 - m + i for i in range(m)]])
+        s.check_attention(s.attend(q, pos), q, pos)
     s.check_pools()
 
 
