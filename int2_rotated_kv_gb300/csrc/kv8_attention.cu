@@ -763,59 +763,73 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   if (tid == 0) p.info[blockIdx.x] = owned;
 }
 
-// Merges the units that lie in several CTAs: block (CTA in which the unit starts,
-// column), thread = channel.
-template <int D, int NT>
-__global__ void __launch_bounds__(D) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int kSlot = kv8_slot<D, NT>();
-  __shared__ float w[kMaxCtas];
-  __shared__ float red[D / 32];
+// Merges the units that lie in several CTAs.  Block: (CTA in which the unit starts, columns);
+// kSplit warps share the parts of a column, a lane has D / 32 channels.
+template <int D, int NT, int kSplit>
+__global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int kSlot = kv8_slot<D, NT>(), kPer = D / 32;
+  __shared__ float partial[8][D];
   pdl_wait();
   pdl_trigger();
   const int4 own = p.info[blockIdx.x];
   const int n = own.z;
+  if (n == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kSplit;
   const int b = own.x / p.tiles, tile = own.x - b * p.tiles;
-  const int col = blockIdx.y, gcol = tile * 8 * NT + col;
-  if (n == 0 || gcol >= p.cols) return;
-  const int tid = threadIdx.x, lane = tid & 31;
-  // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
-  auto slot = [&](int j) {
-    const size_t cta = blockIdx.x + static_cast<size_t>(j);
-    return p.part + (2 * cta + (j == 0 ? 1 : 0)) * kSlot;
-  };
-  float top = kLowest;
-  for (int j = tid; j < n; j += D) top = fmaxf(top, slot(j)[8 * NT * D + 2 * col]);
-  top = warp_max(top);
-  if (lane == 0) red[tid >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) top = fmaxf(top, red[i]);
-  __syncthreads();
+  const int col = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 * NT + col;
+  const bool live = col < 8 * NT && gcol < p.cols;
+  float acc[kPer] = {};
   float l = 0.f;
-  for (int j = tid; j < n; j += D) {
-    const float2 ml = *reinterpret_cast<const float2*>(slot(j) + 8 * NT * D + 2 * col);
-    const float a = fast_exp2(ml.x - top);
-    w[j] = a;
-    l = fmaf(a, ml.y, l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[tid >> 5] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) l += red[i];
-  float acc = w[0] * slot(0)[col * D + tid];
-  const float* next = slot(1) + col * D + tid;
+  if (live) {
+    // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
+    auto slot = [&](int j) {
+      return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
+    };
+    auto stats = [&](int j) {   // (maximum, sum) of part j
+      return j < n ? *reinterpret_cast<const float2*>(slot(j) + 8 * NT * D + 2 * col) : make_float2(kLowest, 0.f);
+    };
+    float top = kLowest;
+    for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(j).x);
+    top = warp_max(top);
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const float2 ml = stats(j0 + lane);
+      const float w = j0 + lane < n ? fast_exp2(ml.x - top) : 0.f;
+      l = fmaf(w, ml.y, l);
+      const int m = min(32, n - j0);
 #pragma unroll 8
-  for (int j = 1; j < n; ++j) {
-    acc = fmaf(w[j], *next, acc);
-    next += 2 * kSlot;
+      for (int j = sub; j < m; j += kSplit) {
+        const float a = __shfl_sync(0xffffffffu, w, j);
+        const float* x = slot(j0 + j) + col * D + kPer * lane;
+        if constexpr (kPer == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(x);
+          acc[0] = fmaf(a, v.x, acc[0]); acc[1] = fmaf(a, v.y, acc[1]);
+          acc[2] = fmaf(a, v.z, acc[2]); acc[3] = fmaf(a, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(x);
+          acc[0] = fmaf(a, v.x, acc[0]); acc[1] = fmaf(a, v.y, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   }
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) partial[warp][kPer * lane + k] = acc[k];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int s = 1; s < kSplit; ++s)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int row = gcol / p.G, g = gcol - row * p.G;
-  const __nv_bfloat16 y = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
-  p.out[((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + tid] =
-      __bfloat16_as_ushort(y);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(
+      p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + kPer * lane);
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf162(acc[k] * inv, acc[k + 1] * inv);
 }
 
 template <typename Kern, typename... Args>
@@ -965,11 +979,14 @@ oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_
              ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
+// Few columns with many parts each: four warps a column; 128 with few: one.
 template <int D, int NT>
 oscar_status launch_merge(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(pl.ctas), static_cast<unsigned>(std::min(p.cols, 8 * NT)));
-  return launch_kv8(kv8_merge_kernel<D, NT>, 1, grid, D, 0, st, p) == cudaSuccess ? OSCAR_OK
-                                                                                 : OSCAR_ERR_CUDA;
+  constexpr int kSplit = NT <= 2 ? 4 : 1, kCols = 8 / kSplit;
+  const dim3 grid(static_cast<unsigned>(pl.ctas),
+                  static_cast<unsigned>((std::min(p.cols, 8 * NT) + kCols - 1) / kCols));
+  return launch_kv8(kv8_merge_kernel<D, NT, kSplit>, 1, grid, 256, 0, st, p) == cudaSuccess
+             ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 template <int D, bool kE4m3>

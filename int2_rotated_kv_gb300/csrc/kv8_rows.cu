@@ -11,14 +11,16 @@
 // shared and tensor memory.  The value scale of a page rides in the exponent: w is
 // p s_V, rounded once to fp16, and the sum of p is that of w / s_V.
 //
-// One CTA per SM, 14 warps:
-//   0-3, 4-7  softmax of even and odd tiles ("streams", each with its own S, w, O in
-//             tensor memory, own maxima and sums, merged at the unit's end): reads S
-//             twice, for the maximum and for w, which overwrites S;
-//   8-11      raw pages -> fp16 K and V tiles, 128-byte swizzled, two of each; the
-//             queries of a unit;
-//   12        page ids and bulk copies, a ring of 7 x 4 pages (keys and values apart);
-//   13        MMAs from one lane.
+// One CTA per SM, 17 warps:
+//   0-3, 4-7      softmax of even and odd tiles ("streams", each with its own S, w, O in
+//                 tensor memory, own maxima and sums, merged at the unit's end): reads S
+//                 twice, for the maximum and for w, which overwrites S;
+//   8-11, 12-15   pages -> fp16 K tiles and V tiles, 128-byte swizzled, two of each (the
+//                 former also the queries of a unit).  A warp has two pages of every tile;
+//                 each lane copies (cp.async) the chunks that it will convert itself, three
+//                 pages ahead, so nothing is waited for but its own copies.  (As bulk
+//                 copies of 2 KB, 24 a tile, the copies alone took 3400 cycles a tile.)
+//   16            MMAs from one lane.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (d each); w in the first half of S.
 // What bounds it: shared memory, 1536 cycles a tile at d = 128 (fp16 tiles written once
@@ -30,26 +32,26 @@
 
 namespace oscar {
 
-constexpr int kRWarps = 14;
+constexpr int kRWarps = 17;
+constexpr int kRAhead = 3;         // pages that a converting warp has on their way
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRTile = 128;        // tokens of a tile
-constexpr int kREntries = 7;       // raw ring: 4 pages of keys or of values each
 constexpr int kRHidden = 0x7fff0000;   // position of a page slot that holds no page
 
 template <int D>
 struct RowsSmem {
   using F = Kv8Fmt<D>;
   static constexpr int kTile16 = kRTile * D * 2;           // fp16 K or V tile, or Q
-  static constexpr int kEntry = 4 * F::kCodes + 64;        // codes, and 4 x 16 bytes of scales
   static constexpr int kK = 0;
   static constexpr int kV = 2 * kTile16;
   static constexpr int kQ = 4 * kTile16;
-  static constexpr int kRaw = 5 * kTile16;
-  static constexpr int kMeta = kRaw + kREntries * kEntry;  // float4 [4][8]: s_K, log2 s_V, 1/s_V, position
+  static constexpr int kPage16 = F::kCodes + 16;           // codes of a page, and its scales
+  static constexpr int kRaw = 5 * kTile16;                 // [8 warps][kRAhead] of them
+  static constexpr int kMeta = kRaw + 8 * kRAhead * kPage16;   // float4 [4][8]: s_K, log2 s_V, 1/s_V, position
   static constexpr int kFac = kMeta + 512;                 // float [2][128]
   static constexpr int kMl = kFac + 1024;                  // float2 [2][2][128]
-  static constexpr int kValid = kMl + 4096;                // int [kREntries], then int bad[4]
-  static constexpr int kBars = kValid + 64;
+  static constexpr int kBad = kMl + 4096;                  // int [4]: tails that are not finite
+  static constexpr int kBars = kBad + 64;
   static constexpr int kMisc = kBars + 40 * 8;
   static constexpr int kBytes = kMisc + 64;
   static constexpr int kAlloc = kBytes + 1024;             // the base is rounded up to 1024 bytes
@@ -57,7 +59,6 @@ struct RowsSmem {
 };
 
 struct RowsBars {
-  uint64_t rawfull[kREntries], rawempty[kREntries];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // fp16 tiles, by tile number
   uint64_t sfull[2], pfull[2], wdone[2];               // S ready, w ready, w used, by stream
   uint64_t qfull[2], oempty[2];                        // by unit: queries ready, O read
@@ -76,7 +77,7 @@ struct Walk {
     p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
     n8 = max(0, min(p1, t.n8) - p0);
     tail = p1 > t.n8 && t.vis > t.len / kPage * kPage;
-    tiles = tail ? n8 / 8 + 1 + (n8 % 8 == 7 ? 1 : 0) : (n8 + 7) / 8;
+    tiles = (n8 + (tail ? 1 : 0) + 7) / 8;
   }
   __device__ __forceinline__ void start(const Share& s) {
     e = s.e;
@@ -98,12 +99,35 @@ struct Walk {
     set();
     return true;
   }
-  // Page slots of tile i: pages in slots 0 .. n - 1, the tail's two slots from `tail_slot`
-  // (-1: none; it does not cross the border of four slots), slots in use.
-  __device__ __forceinline__ void slots(int i, int& n, int& tail_slot, int& used) const {
+  // Page slots of tile i: pages in slots 0 .. n - 1, the tail in slot `tail_slot` (-1: none).
+  __device__ __forceinline__ void slots(int i, int& n, int& tail_slot) const {
     n = max(0, min(8, n8 - 8 * i));
-    tail_slot = tail && i == tiles - 1 ? ((n & 3) == 3 ? n + 1 : n) : -1;
-    used = tail_slot >= 0 ? tail_slot + 2 : n;
+    tail_slot = tail && i == tiles - 1 ? n : -1;
+  }
+};
+
+// Page ids of a unit as a warp holds them: four tiles' (32 pages), a lane each, and the next
+// four's on their way.
+struct PageIds {
+  const int32_t* row;
+  int now, ahead;
+
+  __device__ __forceinline__ PageIds(const Kv8Params& p, const Walk& u, int lane) {
+    row = p.page_table + static_cast<size_t>(u.t.b) * p.max_pages + u.p0;
+    now = -1;
+    ahead = lane < u.n8 ? row[lane] : -1;
+  }
+  // to be called for every tile in order
+  __device__ __forceinline__ void tile(const Kv8Params& p, const Walk& u, int i, int lane) {
+    if (i % 4) return;
+    now = ahead;
+    const int pg = 8 * i + 32 + lane;
+    ahead = pg < u.n8 ? row[pg] : -1;
+  }
+  // block of the page in `slot` of tile i; -1: no page, or an id out of range
+  __device__ __forceinline__ int64_t block(const Kv8Params& p, const Walk& u, int i, int slot) const {
+    const int id = __shfl_sync(0xffffffffu, now, (8 * i + slot) & 31);
+    return 8 * i + slot < u.n8 && id >= 0 && id < p.n_pages ? static_cast<int64_t>(id) * p.hkv + u.h : -1;
   }
 };
 
@@ -119,6 +143,70 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& a, uint32_t& b)
     const __half2 t = __hadd2(*reinterpret_cast<const __half2*>(&y), less);
     a = *reinterpret_cast<const uint32_t*>(&s);
     b = *reinterpret_cast<const uint32_t*>(&t);
+  }
+}
+
+// Asynchronous copies of 16 bytes into shared memory, in groups.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(kLeft) : "memory");
+}
+
+// A lane's chunk c of a page's key codes: 16 channels from 64 (c / 2) + 16 (lane / 8) of token
+// lane % 8 + 8 (c % 2), so that the eight lanes of a store phase, in eight rows, meet all
+// the banks of the swizzled tile.
+__device__ __forceinline__ int key_chunk_of(int lane, int c) {
+  return kv8_key_chunk((lane & 7) + 8 * (c & 1), 4 * (c >> 1) + (lane >> 3));
+}
+
+// Its place in the page's 16 rows; half: 8 channels of it.
+__device__ __forceinline__ uint32_t key_place(int lane, int c, int half) {
+  return (c >> 1) * (kRTile * 128) + 1024 * (c & 1) + 128 * (lane & 7) +
+         16 * ((2 * (lane >> 3) + half) ^ (lane & 7));
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ void store_keys(uint8_t* dst, int c, int lane, uint4 x) {
+  uint32_t o[8];
+  code_pairs<kE4m3>(x.x, o[0], o[1]);
+  code_pairs<kE4m3>(x.y, o[2], o[3]);
+  code_pairs<kE4m3>(x.z, o[4], o[5]);
+  code_pairs<kE4m3>(x.w, o[6], o[7]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, 0)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Two neighbouring chunks of value codes (pair 32 c + lane of a page: 4 channels x 8 tokens)
+// as fp16: channel x pairs of tokens.
+template <bool kE4m3>
+__device__ __forceinline__ void value_square(uint4 x, uint4 y, uint32_t (&o)[4][4]) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    code_pairs<kE4m3>(a[k], o[k][0], o[k][1]);
+    code_pairs<kE4m3>(b[k], o[k][2], o[k][3]);
+  }
+}
+
+// The square into the rows (channels) of a 64-token atom at `dst`, page slot w of four.
+// Every other pair of channel groups stores its channels in the order 2, 3, 0, 1, for the
+// banks as above.
+template <int D>
+__device__ __forceinline__ void store_square(uint8_t* dst, int c, int w, int lane, const uint32_t (&o)[4][4]) {
+  const int cg = lane >> 1, tg = lane & 1;
+  const bool turn = (cg >> 1) & 1;
+  uint8_t* to = dst + (64 * c + 4 * cg) * 128;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = turn ? k ^ 2 : k;
+    const uint32_t chunk = static_cast<uint32_t>((2 * w + tg) ^ (4 * (cg & 1) + at));
+    *reinterpret_cast<uint4*>(to + at * 128 + 16 * chunk) =
+        make_uint4(turn ? o[k ^ 2][0] : o[k][0], turn ? o[k ^ 2][1] : o[k][1],
+                   turn ? o[k ^ 2][2] : o[k][2], turn ? o[k ^ 2][3] : o[k][3]);
   }
 }
 
@@ -162,6 +250,153 @@ __device__ __forceinline__ uint32_t tail_magnitude(const uint16_t* area, int whi
   return __reduce_max_sync(0xffffffffu, top);
 }
 
+// The tail's element block (keys, then values) of a unit; ok: its id is in range.
+template <int D>
+__device__ __forceinline__ const uint16_t* tail_block(const Kv8Params& p, int b, int h, bool& ok) {
+  const int64_t id = p.tail_ids ? p.tail_ids[b] : b;
+  ok = id >= 0 && id < p.n_tails;
+  return reinterpret_cast<const uint16_t*>(p.tail) + ((ok ? id : 0) * p.hkv + h) * (2 * Kv8Fmt<D>::kTailHalf);
+}
+
+// The tail's keys as 16 fp16 rows at dst, scaled by a power of two; returns what the softmax
+// needs of the slot, and sets *bad when a value there is not finite.  Once per unit.
+template <int D>
+__device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int len, uint8_t* dst,
+                                         int lane, volatile int* bad) {
+  bool ok, odd;
+  const uint16_t* area = tail_block<D>(p, b, h, ok);
+  const int n = len % kPage;
+  const int up = scale_up(tail_magnitude<D>(area, 0, n, lane, odd));
+  const int up_v = scale_up(tail_magnitude<D>(area + Kv8Fmt<D>::kTailHalf, 1, n, lane, odd));
+  const float mul = power_of_two(up);
+  for (int c = 0; c < D / 32; ++c) {
+    for (int part = 0; part < 2; ++part) {
+      const uint4 x = reinterpret_cast<const uint4*>(area)[2 * key_chunk_of(lane, c) + part];
+      *reinterpret_cast<uint4*>(dst + key_place(lane, c, part)) =
+          make_uint4(half_pair(x.x, mul), half_pair(x.y, mul), half_pair(x.z, mul), half_pair(x.w, mul));
+    }
+  }
+  if (lane == 0) {
+    *bad = odd && ok;
+    if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+  }
+  return make_float4(power_of_two(-up), static_cast<float>(-up_v), power_of_two(up_v),
+                     __int_as_float(ok ? len / kPage * kPage : kRHidden));
+}
+
+// The tail's values into page slot w of the atom at dst; what is not finite, or not a token,
+// becomes 0 (the epilogue adds the former).
+template <int D>
+__device__ __noinline__ void tail_values(const Kv8Params& p, int b, int h, int len, uint8_t* dst, int w,
+                                        int lane) {
+  bool ok, odd;
+  const uint16_t* area = tail_block<D>(p, b, h, ok) + Kv8Fmt<D>::kTailHalf;
+  const int n = len % kPage;
+  const float mul = power_of_two(scale_up(tail_magnitude<D>(area, 1, n, lane, odd)));
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t o[4][4];   // channel x pairs of tokens
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const uint4 x = reinterpret_cast<const uint4*>(area)[4 * (32 * c + lane) + 2 * part];
+      const uint4 y = reinterpret_cast<const uint4*>(area)[4 * (32 * c + lane) + 2 * part + 1];
+      const uint32_t a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int t0 = 8 * (lane & 1) + 4 * part + 2 * (k & 1);
+        uint32_t v = a[k];
+        if (t0 >= n || (v & 0x7fffu) >= 0x7f80u) v &= 0xffff0000u;
+        if (t0 + 1 >= n || ((v >> 16) & 0x7fffu) >= 0x7f80u) v &= 0xffffu;
+        o[k >> 1][2 * part + (k & 1)] = half_pair(v, mul);
+      }
+    }
+    store_square<D>(dst, c, w, lane, o);
+  }
+}
+
+// 2^x; unlike fast_exp2 free to move among its neighbours.
+__device__ __forceinline__ float rows_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The largest exponent s_K fac S + log2 s_V of a thread's row over a tile's visible tokens.
+// A page's 16 columns at a time, the next page's on their way.
+template <bool kMasked>
+__device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float fac, int vis) {
+  float big = -INFINITY;
+  auto page = [&](const uint32_t (&s)[16], int j) {
+    const float4 pm = mt[j];
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]);
+    if constexpr (kMasked) {
+      const int seen = vis - __float_as_int(pm.w);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = k < seen ? x[k] : -INFINITY;
+    }
+#pragma unroll
+    for (int n = 8; n > 0; n /= 2)
+#pragma unroll
+      for (int k = 0; k < n; ++k) x[k] = fmaxf(x[k], x[k + n]);
+    // (a hidden page's -inf times a scale of 0 would be NaN)
+    big = fmaxf(big, kMasked && x[0] == -INFINITY ? x[0] : fmaf(x[0], pm.x * fac, pm.y));
+  };
+  uint32_t a[16], b[16];
+  tc_request16(ts, a);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    tc_wait_ld(a);
+    tc_request16(ts + 16 * (j + 1), b);
+    page(a, j);
+    tc_wait_ld(b);
+    if (j < 6) tc_request16(ts + 16 * (j + 2), a);
+    page(b, j + 1);
+  }
+  return big;
+}
+
+// w = 2^(s_K fac S + log2 s_V - m) of the row, as fp16 over the columns of S that have been
+// read; returns the sum of w / s_V.
+template <bool kMasked>
+__device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, float fac, int vis, float m) {
+  float l = 0.f;
+  auto page = [&](const uint32_t (&s)[16], int j) {
+    const float4 pm = mt[j];
+    const float f = pm.x * fac, off = pm.y - m;
+    const int seen = vis - __float_as_int(pm.w);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t out[8];
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float x0 = rows_exp2(fmaf(__uint_as_float(s[k]), f, off));
+      float x1 = rows_exp2(fmaf(__uint_as_float(s[k + 1]), f, off));
+      if constexpr (kMasked) {
+        x0 = k < seen ? x0 : 0.f;
+        x1 = k + 1 < seen ? x1 : 0.f;
+      }
+      sum[k & 2] += x0;
+      sum[(k & 2) + 1] += x1;
+      out[k / 2] = pack_half2(x0, x1);
+    }
+    tc_st8(ts + 8 * j, out);
+    const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if (!kMasked || seen > 0) l = fmaf(all, pm.z, l);
+  };
+  uint32_t a[16], b[16];
+  tc_request16(ts, a);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    tc_wait_ld(a);
+    tc_request16(ts + 16 * (j + 1), b);
+    page(a, j);
+    tc_wait_ld(b);
+    if (j < 6) tc_request16(ts + 16 * (j + 2), a);
+    page(b, j + 1);
+  }
+  return l;
+}
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kRThreads, 1)
 kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
@@ -174,19 +409,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   RowsBars* bar = reinterpret_cast<RowsBars*>(smem + S::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
-  volatile int* n_copies = reinterpret_cast<volatile int*>(smem + S::kMisc + 8);
   float4* meta = reinterpret_cast<float4*>(smem + S::kMeta);
   float* facs = reinterpret_cast<float*>(smem + S::kFac);
   float2* mls = reinterpret_cast<float2*>(smem + S::kMl);
-  volatile int* valid = reinterpret_cast<volatile int*>(smem + S::kValid);
-  volatile int* bad_tail = valid + kREntries;
+  volatile int* bad_tail = reinterpret_cast<volatile int*>(smem + S::kBad);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kREntries; ++i) {
-      mbar_init(&bar->rawfull[i], 1);
-      mbar_init(&bar->rawempty[i], 4);
-    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->kfull[i], 4);
       mbar_init(&bar->kempty[i], 1);
@@ -202,10 +431,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     mbar_init(&bar->odone, 1);
     mbar_init(&bar->mlfull, 8);
     *abort_flag = 0;
-    *n_copies = 0;
     fence_mbar_init();
   }
-  if (warp == 13) tc_alloc(tmem_slot, 512);
+  if (warp == 16) tc_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -235,62 +463,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     if (lane == 0) tc_arrive(b);
   };
 
-  if (any && warp == 12) {
-    // ---------------------------------------------------------------- copies
-    uint32_t r = 0;
-    for (bool go = true; go; go = u.next(p)) {
-      if (u.tiles == 0) continue;
-      const int32_t* row = p.page_table + static_cast<size_t>(u.t.b) * p.max_pages + u.p0;
-      // ids of 32 pages from 32 * window, and of the 32 after them
-      auto ids_of = [&](int window) { const int i = 32 * window + lane; return i < u.n8 ? row[i] : -1; };
-      int window = 0, ids0 = ids_of(0), ids1 = ids_of(1);
-      const int64_t tail_id = p.tail_ids ? p.tail_ids[u.t.b] : u.t.b;
-      const bool tail_ok = tail_id >= 0 && tail_id < p.n_tails;
-      const uint8_t* tail = p.tail + ((tail_ok ? tail_id : 0) * p.hkv + u.h) * F::kTailBytes;
-      bool ok = true;
-      // keys of tile i + 1, then values of tile i
-      for (int step = 0; step < 2 * u.tiles && ok; ++step) {
-        const bool keys = step == 0 || (step & 1 && step < 2 * u.tiles - 1);
-        const int i = keys ? (step + 1) / 2 : (step == 2 * u.tiles - 1 ? u.tiles - 1 : step / 2 - 1);
-        int n, tail_slot, used;
-        u.slots(i, n, tail_slot, used);
-        for (; !keys && i / 4 > window; ++window) {
-          ids0 = ids1;
-          ids1 = ids_of(window + 2);
-        }
-        for (int half = 0; half < (used + 3) / 4; ++half, ++r) {
-          const int en = r % kREntries;
-          if (!(ok = wait(&bar->rawempty[en], r / kREntries + 1))) break;
-          // lanes 0-3: codes of slots 4 half + lane; lanes 4-7: their scales
-          const int slot = 4 * half + (lane & 3);
-          const int id = __shfl_sync(0xffffffffu, i / 4 == window ? ids0 : ids1, (8 * i + slot) & 31);
-          const bool page = slot < n, ends = slot == tail_slot;
-          const bool good = page ? id >= 0 && id < p.n_pages : ends && tail_ok;
-          const uint32_t mask = __ballot_sync(0xffffffffu, lane < 4 && good);
-          if (lane < 4 && (page || ends) && !good && keys && p.status)
-            atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-          const int pages = __popc(__ballot_sync(0xffffffffu, lane < 4 && page));
-          const int tails = __popc(__ballot_sync(0xffffffffu, lane < 4 && ends));
-          if (lane == 0) {
-            valid[en] = static_cast<int>(mask);
-            mbar_arrive_expect_tx(&bar->rawfull[en],
-                                  pages * (F::kCodes + (keys ? 16 : 0)) + tails * 2 * F::kCodes);
-            *n_copies = static_cast<int>(r) + 1;
-          }
-          __syncwarp();
-          uint8_t* dst = smem + S::kRaw + en * S::kEntry;
-          const uint8_t* blk = p.pool + (static_cast<int64_t>(page && good ? id : 0) * p.hkv + u.h) * F::kBlock;
-          if (lane < 4) {
-            if (page) bulk_g2s(dst + lane * F::kCodes, blk + (keys ? 0 : F::kCodes), F::kCodes, &bar->rawfull[en]);
-            else if (ends) bulk_g2s(dst + lane * F::kCodes, tail + (keys ? 0 : 2 * F::kCodes), 2 * F::kCodes, &bar->rawfull[en]);
-          } else if (lane < 8 && keys && page) {
-            bulk_g2s(dst + 4 * F::kCodes + 16 * (lane & 3), blk + F::kScales, 16, &bar->rawfull[en]);
-          }
-        }
-      }
-      if (!ok) break;
-    }
-  } else if (any && warp == 13) {
+  if (any && warp == 16) {
     // ------------------------------------------------------------------ MMAs
     if (lane == 0) {
       constexpr uint32_t id_s = tc_idesc_f16(kRTile, kRTile), id_o = tc_idesc_f16(kRTile, D);
@@ -346,24 +519,98 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         mbar_wait(&bar->odone, seg & 1u, p.status);
       }
     }
-  } else if (any && warp >= 8) {
-    // -------------------------------------------------------- fp16 operands
-    const int w = warp - 8;
-    uint32_t r = 0, g0 = 0, seg = 0;
-    for (bool go = true; go; go = u.next(p)) {
+  } else if (any && warp >= 12) {
+    // ---------------------------------------------------- values as fp16 operands
+    const int w = warp - 12;   // page slots w and w + 4 of every tile
+    uint8_t* raw = smem + S::kRaw + (4 + w) * kRAhead * S::kPage16;
+    uint32_t g = 0;
+    for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
+      PageIds ids(p, u, lane);
+      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2), as lanes need it
+      auto request = [&](int k) {
+        if (k < 2 * u.tiles) {
+          if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
+          const int64_t block = ids.block(p, u, k / 2, w + 4 * (k & 1));
+          const uint8_t* src = p.pool + block * F::kBlock + F::kCodes + 32 * lane;
+          uint8_t* to = raw + k % kRAhead * S::kPage16 + 16 * lane;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            if (block >= 0) copy16(to + 512 * c, src + 1024 * (c >> 1) + 16 * (c & 1));
+            else *reinterpret_cast<uint4*>(to + 512 * c) = make_uint4(0, 0, 0, 0);
+        }
+        copies_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < kRAhead; ++k) request(k);
+      for (int i = 0; i < u.tiles; ++i, ++g) {
+        const uint32_t buf = g & 1;
+        int n, tail_slot;
+        u.slots(i, n, tail_slot);
+        if (!(ok = wait(&bar->vempty[buf], (g >> 1) + 1))) break;
+        uint8_t* dst = smem + S::kV + buf * S::kTile16;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int k = 2 * i + half;
+          copies_wait<kRAhead - 1>();
+          const uint4* mine = reinterpret_cast<const uint4*>(raw + k % kRAhead * S::kPage16) + lane;
+          if (4 * half + w != tail_slot) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t o[4][4];
+              value_square<kE4m3>(mine[64 * c], mine[64 * c + 32], o);
+              store_square<D>(dst + half * (D * 128), c, w, lane, o);
+            }
+          } else {
+            tail_values<D>(p, u.t.b, u.h, u.t.len, dst + half * (D * 128), w, lane);
+          }
+          request(k + kRAhead);
+        }
+        fence_proxy_async();
+        arrive(&bar->vfull[buf]);
+      }
+      copies_wait<0>();
+    }
+  } else if (any && warp >= 8) {
+    // ------------------------------------------- queries and keys as fp16 operands
+    const int w = warp - 8;   // page slots w and w + 4 of every tile
+    uint8_t* raw = smem + S::kRaw + w * kRAhead * S::kPage16;
+    uint32_t g = 0, seg = 0;
+    for (bool go = true, ok = true; go && ok; go = u.next(p)) {
+      if (u.tiles == 0) continue;
+      PageIds ids(p, u, lane);
+      uint32_t shown = 0;   // bit k % 4: page k is one
+      auto request = [&](int k) {
+        if (k < 2 * u.tiles) {
+          if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
+          const int slot = w + 4 * (k & 1);
+          const int64_t block = ids.block(p, u, k / 2, slot);
+          if (block < 0 && lane == 0 && 8 * (k / 2) + slot < u.n8 && p.status)
+            atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+          shown = (shown & ~(1u << (k & 3))) | ((block >= 0 ? 1u : 0u) << (k & 3));
+          const uint8_t* src = p.pool + block * F::kBlock;
+          uint8_t* to = raw + k % kRAhead * S::kPage16;
+          if (lane == 0 && block >= 0) copy16(to + F::kCodes, src + F::kScales);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            if (block >= 0) copy16(to + 512 * c + 16 * lane, src + 16 * key_chunk_of(lane, c));
+            else *reinterpret_cast<uint4*>(to + 512 * c + 16 * lane) = make_uint4(0, 0, 0, 0);
+        }
+        copies_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < kRAhead; ++k) request(k);
       if (!wait(&bar->qempty, seg + 1)) break;
       // and the unit before the last has been read (what is kept by unit comes round again)
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
       {   // a query column per thread: fp16 scaled by a power of two
         const int rr = 32 * w + lane;
         const uint16_t* src = column(p, u.t, u.h, u.t.tile * 128 + rr, D);
-        uint4 q[D / 8];
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
-          q[c] = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+          const uint4 q = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
@@ -372,144 +619,51 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         }
         const int up = scale_up(top);
         const float mul = power_of_two(up);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 q = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(smem + S::kQ + tc_sw128_offset(rr, 8 * c, kRTile)) =
-              make_uint4(half_pair(q[c].x, mul), half_pair(q[c].y, mul), half_pair(q[c].z, mul),
-                         half_pair(q[c].w, mul));
+              make_uint4(half_pair(q.x, mul), half_pair(q.y, mul), half_pair(q.z, mul), half_pair(q.w, mul));
+        }
         facs[(seg & 1) * 128 + rr] = p.scale_log2 * power_of_two(-up);
         fence_proxy_async();
         arrive(&bar->qfull[seg & 1]);
       }
-      const int n_tail = u.t.len % kPage;
-      const int64_t tail_id = p.tail_ids ? p.tail_ids[u.t.b] : u.t.b;
-      const bool tail_ok = tail_id >= 0 && tail_id < p.n_tails;
-      const uint16_t* tail = reinterpret_cast<const uint16_t*>(
-          p.tail + ((tail_ok ? tail_id : 0) * p.hkv + u.h) * F::kTailBytes);
-      int up_v = 0;
-      bool ok = true;
-      for (int step = 0; step < 2 * u.tiles && ok; ++step) {   // in the order of the copies
-        const bool keys = step == 0 || (step & 1 && step < 2 * u.tiles - 1);
-        const int i = keys ? (step + 1) / 2 : (step == 2 * u.tiles - 1 ? u.tiles - 1 : step / 2 - 1);
-        const uint32_t g = g0 + i, buf = g & 1;
-        int n, tail_slot, used;
-        u.slots(i, n, tail_slot, used);
-        uint8_t* dst = smem + (keys ? S::kK : S::kV) + buf * S::kTile16;
-        if (!(ok = wait(keys ? &bar->kempty[buf] : &bar->vempty[buf], (g >> 1) + 1))) break;
+      for (int i = 0; i < u.tiles; ++i, ++g) {
+        const uint32_t buf = g & 1;
+        int n, tail_slot;
+        u.slots(i, n, tail_slot);
+        if (!(ok = wait(&bar->kempty[buf], (g >> 1) + 1))) break;
+        uint8_t* dst = smem + S::kK + buf * S::kTile16 + 2048 * w;
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int slot = 4 * half + w;
-          const bool page = slot < n, ends = slot == tail_slot;
-          const bool copies = half < (used + 3) / 4;
-          const int en = r % kREntries;
-          if (copies && !(ok = wait(&bar->rawfull[en], r / kREntries))) break;
-          const uint8_t* raw = smem + S::kRaw + en * S::kEntry + w * F::kCodes;
-          const bool good = copies && ((valid[en] >> w) & 1);
-          if (keys) {
-            float4 m = make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
-            if (page) {
-              const uint4* chunks = reinterpret_cast<const uint4*>(raw);
+          const int k = 2 * i + half, slot = 4 * half + w;
+          copies_wait<kRAhead - 1>();
+          const uint8_t* page = raw + k % kRAhead * S::kPage16;
+          float4 m = make_float4(0.f, 0.f, 0.f, 0.f);   // what the softmax needs of the page
+          if (slot != tail_slot) {
+            const uint4* mine = reinterpret_cast<const uint4*>(page) + lane;
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                const uint4 x = chunks[32 * c + lane];
-                uint32_t o[8];
-                code_pairs<kE4m3>(x.x, o[0], o[1]);
-                code_pairs<kE4m3>(x.y, o[2], o[3]);
-                code_pairs<kE4m3>(x.z, o[4], o[5]);
-                code_pairs<kE4m3>(x.w, o[6], o[7]);
-                const int row = 16 * slot + 2 * (lane >> 2) + (c & 1);
-                const int ch = 64 * (c >> 1) + 16 * (lane & 3);
-                // lanes of odd pairs of rows store their halves in the other order: no bank conflicts
-                const int first = (lane >> 2) & 1;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int part = k ^ first;
-                  *reinterpret_cast<uint4*>(dst + tc_sw128_offset(row, ch + 8 * part, kRTile)) =
-                      part ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-                }
-              }
-              const float2 sc = *reinterpret_cast<const float2*>(
-                  smem + S::kRaw + en * S::kEntry + 4 * F::kCodes + 16 * w);
+            for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, mine[32 * c]);
+            if (lane == 0) {
+              const float2 sc = *reinterpret_cast<const float2*>(page + F::kCodes);
               // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
               const bool live = sc.y > 0.f;
-              m = make_float4(sc.x, live ? log2f(sc.y) : 0.f, live ? 1.f / sc.y : 1.f,
-                              __int_as_float(good ? (u.p0 + 8 * i + slot) * kPage : kRHidden));
-            } else if (ends) {
-              bool odd;
-              const int up = scale_up(tail_magnitude<D>(tail, 0, n_tail, lane, odd));
-              const uint32_t top = tail_magnitude<D>(tail + F::kTailHalf, 1, n_tail, lane, odd);
-              up_v = scale_up(top);
-              if (lane == 0) bad_tail[seg & 3] = odd && tail_ok;
-              const float mul = power_of_two(up);
-              const uint4* chunks = reinterpret_cast<const uint4*>(raw);
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                const int row = 16 * slot + 2 * (lane >> 2) + (c & 1);
-                const int ch = 64 * (c >> 1) + 16 * (lane & 3);
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                  const uint4 x = chunks[2 * (32 * c + lane) + part];
-                  *reinterpret_cast<uint4*>(dst + tc_sw128_offset(row, ch + 8 * part, kRTile)) =
-                      make_uint4(half_pair(x.x, mul), half_pair(x.y, mul), half_pair(x.z, mul),
-                                 half_pair(x.w, mul));
-                }
-              }
-              m = make_float4(power_of_two(-up), static_cast<float>(-up_v), power_of_two(up_v),
-                              __int_as_float(good ? u.t.len / kPage * kPage : kRHidden));
+              m = (shown >> (k & 3)) & 1
+                      ? make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
+                                    __int_as_float((u.p0 + 8 * i + slot) * kPage))
+                      : make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
             }
-            if (lane == 0) meta[(g & 3) * 8 + slot] = m;
           } else {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {   // 4 channels x 8 tokens
-              const int pair = 32 * c + lane, cg = pair >> 1, tg = pair & 1;
-              uint32_t o[4][4];
-              if (page) {
-                const uint4* chunks = reinterpret_cast<const uint4*>(raw) + 2 * pair;
-                const uint4 x = chunks[0], y = chunks[1];
-                const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  code_pairs<kE4m3>(a[k], o[k][0], o[k][1]);
-                  code_pairs<kE4m3>(b[k], o[k][2], o[k][3]);
-                }
-              } else if (ends) {
-                // what is not finite, or not a token, becomes 0 (the epilogue adds the former)
-                up_v = __shfl_sync(0xffffffffu, up_v, 0);
-                const float mul = power_of_two(up_v);
-                const uint4* chunks = reinterpret_cast<const uint4*>(raw) + 4 * pair;
-#pragma unroll
-                for (int half4 = 0; half4 < 2; ++half4) {
-                  const uint4 x = chunks[2 * half4], y = chunks[2 * half4 + 1];
-                  const uint32_t a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const int t0 = 8 * tg + 4 * half4 + 2 * (k & 1);
-                    uint32_t v = a[k];
-                    if (t0 >= n_tail || (v & 0x7fffu) >= 0x7f80u) v &= 0xffff0000u;
-                    if (t0 + 1 >= n_tail || ((v >> 16) & 0x7fffu) >= 0x7f80u) v &= 0xffffu;
-                    o[k >> 1][2 * half4 + (k & 1)] = half_pair(v, mul);
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0u;
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(dst + tc_sw128_offset(4 * cg + k, 16 * slot + 8 * tg, D)) =
-                    make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-            }
+            m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * half, lane, bad_tail + (seg & 3));
           }
-          if (copies) {
-            arrive(&bar->rawempty[en]);
-            ++r;
-          }
+          if (lane == 0) meta[(g & 3) * 8 + slot] = m;
+          request(k + kRAhead);
         }
-        if (!ok) break;
         fence_proxy_async();
-        arrive(keys ? &bar->kfull[buf] : &bar->vfull[buf]);
+        arrive(&bar->kfull[buf]);
       }
-      if (!ok) break;
-      g0 += u.tiles;
+      copies_wait<0>();
       ++seg;
     }
   } else if (any) {
@@ -523,7 +677,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     for (bool go = true; go; go = u.next(p)) {
       const int gcol = u.t.tile * 128 + rr;
       const int row = gcol < p.cols ? gcol / p.G : 0;
-      int vis = 0;
+      int vis = kRHidden;   // a column that does not exist hides nothing that is there
       if (gcol < p.cols) vis = p.q_pos ? row_limit(p, u.t.b, row, u.t.len) : u.t.len;
       if (u.p0 == 0 && u.h == 0 && p.status && st == 0) {
         const int len = p.seq_lens[u.t.b];
@@ -536,81 +690,42 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (u.tiles > 0) {
         if (!wait(&bar->qfull[seg & 1], seg >> 1)) break;
         const float fac = facs[(seg & 1) * 128 + rr];
+        const bool idle = __all_sync(0xffffffffu, gcol >= p.cols);
         bool ok = true;
         for (int i = st; i < u.tiles; i += 2) {
           if (!(ok = wait(&bar->sfull[st], count))) break;
           ++count;
           tc_fence_after();
           const float4* mt = meta + ((g0 + i) & 3) * 8;
+          if (idle) {   // no column of this warp exists: its rows of w and O may hold anything
+            tc_fence_before();
+            arrive(&bar->pfull[st]);
+            continue;
+          }
           bool hides = false;
 #pragma unroll
           for (int j = 0; j < 8; ++j) hides |= __float_as_int(mt[j].w) + kPage > vis;
           const bool masked = __any_sync(0xffffffffu, hides);
-          // the largest exponent of this tile
-          float big = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float s[32];
-            tc_ld32(ts + 32 * c, s);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 pm = mt[2 * c + j];
-              float x = -INFINITY;
-              if (masked) {
-                const int seen = vis - __float_as_int(pm.w);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x = fmaxf(x, k < seen ? s[16 * j + k] : -INFINITY);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x = fmaxf(x, s[16 * j + k]);
-              }
-              // (a hidden page's -inf times a scale of 0 would be NaN)
-              big = fmaxf(big, x == -INFINITY ? x : fmaf(x, pm.x * fac, pm.y));
-            }
-          }
+          const float big = masked ? rows_max<true>(ts, mt, fac, vis) : rows_max<false>(ts, mt, fac, vis);
           const bool over = big > m + kLag;
           if (__any_sync(0xffffffffu, over)) {
             const float up = over ? big : m;
-            const float a = over ? fast_exp2(m - up) : 1.f;
+            const float a = over ? rows_exp2(m - up) : 1.f;
             m = up;
             l *= a;
             if (i > 1) {   // the stream's O so far (its last MMA finished before this S began)
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
-                tc_ld16(to + 16 * c, o);
+                tc_request16(to + 16 * c, o);
+                tc_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
                 tc_st16(to + 16 * c, o);
               }
             }
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float s[32];
-            tc_ld32(ts + 32 * c, s);
-            uint32_t out[16];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 pm = mt[2 * c + j];
-              const float f = pm.x * fac, off = pm.y - m;
-              const int seen = masked ? vis - __float_as_int(pm.w) : kPage;
-              float sum = 0.f;
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                float x0 = fast_exp2(fmaf(s[16 * j + k], f, off));
-                float x1 = fast_exp2(fmaf(s[16 * j + k + 1], f, off));
-                if (masked) {
-                  x0 = k < seen ? x0 : 0.f;
-                  x1 = k + 1 < seen ? x1 : 0.f;
-                }
-                sum += x0 + x1;
-                out[8 * j + k / 2] = pack_half2(x0, x1);
-              }
-              if (!masked || seen > 0) l = fmaf(sum, pm.z, l);
-            }
-            tc_st16(ts + 16 * c, out);   // columns of S that have been read
-          }
+          l += masked ? rows_weights<true>(ts, mt, fac, vis, m) : rows_weights<false>(ts, mt, fac, vis, m);
           tc_wait_st();
           tc_fence_before();
           arrive(&bar->pfull[st]);
@@ -624,7 +739,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         tc_fence_after();
         const float2 other = ml[128 * (1 - st) + rr];
         top = fmaxf(m, other.x);
-        const float mine = fast_exp2(m - top), theirs = fast_exp2(other.x - top);
+        const float mine = rows_exp2(m - top), theirs = rows_exp2(other.x - top);
         l = l * mine + other.y * theirs;
         a0 = st ? theirs : mine;
         a1 = st ? mine : theirs;
@@ -646,13 +761,15 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         for (int k = 0; k < 16; ++k) o[k] = 0.f;
         if (u.tiles > 0) {
           uint32_t x[16];
-          tc_ld16(lanes + 2 * kRTile + ch, x);
+          tc_request16(lanes + 2 * kRTile + ch, x);
+          tc_wait_ld(x);
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = __uint_as_float(x[k]) * a0;
         }
         if (u.tiles > 1) {
           uint32_t x[16];
-          tc_ld16(lanes + 2 * kRTile + D + ch, x);
+          tc_request16(lanes + 2 * kRTile + D + ch, x);
+          tc_wait_ld(x);
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = fmaf(__uint_as_float(x[k]), a1, o[k]);
         }
@@ -694,18 +811,11 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     if (tid == 0) p.info[blockIdx.x] = *abort_flag ? make_int4(0, 0, 0, 0) : owned;
   }
 
-  // ---- after a give-up, copies in flight land before the CTA ends (the MMAs' own thread
-  // has waited for them)
+  // ---- after a give-up the MMAs' own thread has waited for those in flight
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && tid == 0) {
-    const int n = *n_copies;
-    for (int r = max(0, n - kREntries); r < n; ++r)
-      mbar_wait(&bar->rawfull[r % kREntries], static_cast<uint32_t>(r / kREntries) & 1u, p.status);
-  }
-  __syncthreads();
-  if (warp == 13) {
+  if (warp == 16) {
     tc_fence_after();
     tc_dealloc(tmem, 512);
   }
