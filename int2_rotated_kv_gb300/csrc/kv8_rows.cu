@@ -527,13 +527,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
       PageIds ids(p, u, lane);
-      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2), as lanes need it
-      auto request = [&](int k) {
+      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2) into ring place `at`
+      auto request = [&](int k, int at) {
         if (k < 2 * u.tiles) {
           if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
           const int64_t block = ids.block(p, u, k / 2, w + 4 * (k & 1));
           const uint8_t* src = p.pool + block * F::kBlock + F::kCodes + 32 * lane;
-          uint8_t* to = raw + k % kRAhead * S::kPage16 + 16 * lane;
+          uint8_t* to = raw + at * S::kPage16 + 16 * lane;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
             if (block >= 0) copy16(to + 512 * c, src + 1024 * (c >> 1) + 16 * (c & 1));
@@ -542,30 +542,51 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         copies_commit();
       };
 #pragma unroll
-      for (int k = 0; k < kRAhead; ++k) request(k);
+      for (int k = 0; k < kRAhead; ++k) request(k, k);
+      int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
         int n, tail_slot;
         u.slots(i, n, tail_slot);
         if (!(ok = wait(&bar->vempty[buf], (g >> 1) + 1))) break;
         uint8_t* dst = smem + S::kV + buf * S::kTile16;
+        const int next = at == kRAhead - 1 ? 0 : at + 1;
+        copies_wait<kRAhead - 2>();
+        const uint4* page0 = reinterpret_cast<const uint4*>(raw + at * S::kPage16) + lane;
+        const uint4* page1 = reinterpret_cast<const uint4*>(raw + next * S::kPage16) + lane;
+        if (w != tail_slot && w + 4 != tail_slot) {   // both pages' codes in flight together
+          uint4 x[2][D / 32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int k = 2 * i + half;
-          copies_wait<kRAhead - 1>();
-          const uint4* mine = reinterpret_cast<const uint4*>(raw + k % kRAhead * S::kPage16) + lane;
-          if (4 * half + w != tail_slot) {
+          for (int c = 0; c < D / 32; ++c) {
+            x[0][c] = page0[32 * c];
+            x[1][c] = page1[32 * c];
+          }
 #pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t o[4][4];
+              value_square<kE4m3>(x[half][2 * c], x[half][2 * c + 1], o);
+              store_square<D>(dst + half * (D * 128), c, w, lane, o);
+            }
+        } else {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (4 * half + w == tail_slot) {
+              tail_values<D>(p, u.t.b, u.h, u.t.len, dst + half * (D * 128), w, lane);
+              continue;
+            }
+            const uint4* mine = half ? page1 : page0;
             for (int c = 0; c < D / 64; ++c) {
               uint32_t o[4][4];
               value_square<kE4m3>(mine[64 * c], mine[64 * c + 32], o);
               store_square<D>(dst + half * (D * 128), c, w, lane, o);
             }
-          } else {
-            tail_values<D>(p, u.t.b, u.h, u.t.len, dst + half * (D * 128), w, lane);
           }
-          request(k + kRAhead);
         }
+        request(2 * i + kRAhead, at);
+        request(2 * i + kRAhead + 1, next);
+        at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->vfull[buf]);
       }
@@ -580,7 +601,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (u.tiles == 0) continue;
       PageIds ids(p, u, lane);
       uint32_t shown = 0;   // bit k % 4: page k is one
-      auto request = [&](int k) {
+      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2) into ring place `at`
+      auto request = [&](int k, int at) {
         if (k < 2 * u.tiles) {
           if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
           const int slot = w + 4 * (k & 1);
@@ -589,8 +611,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
           shown = (shown & ~(1u << (k & 3))) | ((block >= 0 ? 1u : 0u) << (k & 3));
           const uint8_t* src = p.pool + block * F::kBlock;
-          uint8_t* to = raw + k % kRAhead * S::kPage16;
-          if (lane == 0 && block >= 0) copy16(to + F::kCodes, src + F::kScales);
+          uint8_t* to = raw + at * S::kPage16;
+          // the scales by the lane that will read them
+          if (lane == (k & 1) && block >= 0) copy16(to + F::kCodes, src + F::kScales);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
             if (block >= 0) copy16(to + 512 * c + 16 * lane, src + 16 * key_chunk_of(lane, c));
@@ -599,7 +622,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         copies_commit();
       };
 #pragma unroll
-      for (int k = 0; k < kRAhead; ++k) request(k);
+      for (int k = 0; k < kRAhead; ++k) request(k, k);
       if (!wait(&bar->qempty, seg + 1)) break;
       // and the unit before the last has been read (what is kept by unit comes round again)
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
@@ -629,37 +652,57 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         fence_proxy_async();
         arrive(&bar->qfull[seg & 1]);
       }
+      int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
         int n, tail_slot;
         u.slots(i, n, tail_slot);
         if (!(ok = wait(&bar->kempty[buf], (g >> 1) + 1))) break;
         uint8_t* dst = smem + S::kK + buf * S::kTile16 + 2048 * w;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int k = 2 * i + half, slot = 4 * half + w;
-          copies_wait<kRAhead - 1>();
-          const uint8_t* page = raw + k % kRAhead * S::kPage16;
-          float4 m = make_float4(0.f, 0.f, 0.f, 0.f);   // what the softmax needs of the page
-          if (slot != tail_slot) {
-            const uint4* mine = reinterpret_cast<const uint4*>(page) + lane;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, mine[32 * c]);
-            if (lane == 0) {
-              const float2 sc = *reinterpret_cast<const float2*>(page + F::kCodes);
-              // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
-              const bool live = sc.y > 0.f;
-              m = (shown >> (k & 3)) & 1
-                      ? make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
-                                    __int_as_float((u.p0 + 8 * i + slot) * kPage))
-                      : make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
-            }
-          } else {
-            m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * half, lane, bad_tail + (seg & 3));
+        const int next = at == kRAhead - 1 ? 0 : at + 1;
+        copies_wait<kRAhead - 2>();
+        const uint8_t* page0 = raw + at * S::kPage16;
+        const uint8_t* page1 = raw + next * S::kPage16;
+        if (lane < 2 && 4 * lane + w != tail_slot) {   // what the softmax needs of the two pages
+          const int slot = 4 * lane + w;
+          float4 m = make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
+          if ((shown >> ((2 * i + lane) & 3)) & 1) {
+            const float2 sc = *reinterpret_cast<const float2*>((lane ? page1 : page0) + F::kCodes);
+            // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
+            const bool live = sc.y > 0.f;
+            m = make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
+                            __int_as_float((u.p0 + 8 * i + slot) * kPage));
           }
-          if (lane == 0) meta[(g & 3) * 8 + slot] = m;
-          request(k + kRAhead);
+          meta[(g & 3) * 8 + slot] = m;
         }
+        const uint4* mine0 = reinterpret_cast<const uint4*>(page0) + lane;
+        const uint4* mine1 = reinterpret_cast<const uint4*>(page1) + lane;
+        if (w != tail_slot && w + 4 != tail_slot) {   // both pages' codes in flight together
+          uint4 x[2][D / 32];
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            x[0][c] = mine0[32 * c];
+            x[1][c] = mine1[32 * c];
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
+        } else {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (4 * half + w == tail_slot) {
+              const float4 m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * half, lane, bad_tail + (seg & 3));
+              if (lane == 0) meta[(g & 3) * 8 + 4 * half + w] = m;
+              continue;
+            }
+            for (int c = 0; c < D / 32; ++c)
+              store_keys<kE4m3>(dst + 8192 * half, c, lane, (half ? mine1 : mine0)[32 * c]);
+          }
+        }
+        request(2 * i + kRAhead, at);
+        request(2 * i + kRAhead + 1, next);
+        at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->kfull[buf]);
       }
