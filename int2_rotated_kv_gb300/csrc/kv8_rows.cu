@@ -11,7 +11,7 @@
 // shared and tensor memory.  The value scale of a page rides in the exponent: w is
 // p s_V, rounded once to fp16, and the sum of p is that of w / s_V.
 //
-// One CTA per SM, 17 warps:
+// One CTA per SM, 18 warps:
 //   0-3, 4-7      softmax of even and odd tiles ("streams", each with its own S, w, O in
 //                 tensor memory, own maxima and sums, merged at the unit's end): reads S
 //                 twice, for the maximum and for w, which overwrites S;
@@ -20,7 +20,7 @@
 //                 each lane copies (cp.async) the chunks that it will convert itself, three
 //                 pages ahead, so nothing is waited for but its own copies.  (As bulk
 //                 copies of 2 KB, 24 a tile, the copies alone took 3400 cycles a tile.)
-//   16            MMAs from one lane.
+//   16, 17        MMAs of a stream, from one lane each.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (d each); w in the first half of S.
 // What bounds it: shared memory, 1536 cycles a tile at d = 128 (fp16 tiles written once
@@ -32,7 +32,7 @@
 
 namespace oscar {
 
-constexpr int kRWarps = 17;
+constexpr int kRWarps = 18;
 constexpr int kRAhead = 3;         // pages that a converting warp has on their way
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRTile = 128;        // tokens of a tile
@@ -62,7 +62,7 @@ struct RowsBars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // fp16 tiles, by tile number
   uint64_t sfull[2], pfull[2], wdone[2];               // S ready, w ready, w used, by stream
   uint64_t qfull[2], oempty[2];                        // by unit: queries ready, O read
-  uint64_t qempty, odone, mlfull;
+  uint64_t qempty, odone, mlfull, last[2];
 };
 static_assert(sizeof(RowsBars) <= 40 * 8, "barriers fit");
 
@@ -321,38 +321,39 @@ __device__ __forceinline__ float rows_exp2(float x) {
 }
 
 // The largest exponent s_K fac S + log2 s_V of a thread's row over a tile's visible tokens.
-// A page's 16 columns at a time, the next page's on their way.
+// Two pages' 32 columns at a time, the next two pages' on their way.
 template <bool kMasked>
 __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float fac, int vis) {
   float big = -INFINITY;
-  auto page = [&](const uint32_t (&s)[16], int j) {
-    const float4 pm = mt[j];
-    float x[16];
+  auto pages = [&](const uint32_t (&s)[32], int j0) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(s[k]);
-    if constexpr (kMasked) {
+    for (int j = 0; j < 2; ++j) {
+      const float4 pm = mt[j0 + j];
       const int seen = vis - __float_as_int(pm.w);
+      float x[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = k < seen ? x[k] : -INFINITY;
+      for (int k = 0; k < 16; ++k) x[k] = !kMasked || k < seen ? __uint_as_float(s[16 * j + k]) : -INFINITY;
+#pragma unroll
+      for (int n = 8; n > 0; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k) x[k] = fmaxf(x[k], x[k + n]);
+      // (a hidden page's -inf times a scale of 0 would be NaN)
+      big = fmaxf(big, kMasked && x[0] == -INFINITY ? x[0] : fmaf(x[0], pm.x * fac, pm.y));
     }
-#pragma unroll
-    for (int n = 8; n > 0; n /= 2)
-#pragma unroll
-      for (int k = 0; k < n; ++k) x[k] = fmaxf(x[k], x[k + n]);
-    // (a hidden page's -inf times a scale of 0 would be NaN)
-    big = fmaxf(big, kMasked && x[0] == -INFINITY ? x[0] : fmaf(x[0], pm.x * fac, pm.y));
   };
-  uint32_t a[16], b[16];
-  tc_request16(ts, a);
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    tc_wait_ld(a);
-    tc_request16(ts + 16 * (j + 1), b);
-    page(a, j);
-    tc_wait_ld(b);
-    if (j < 6) tc_request16(ts + 16 * (j + 2), a);
-    page(b, j + 1);
-  }
+  uint32_t a[32], b[32];
+  tc_request32(ts, a);
+  tc_wait_ld(a);
+  tc_request32(ts + 32, b);
+  pages(a, 0);
+  tc_wait_ld(b);
+  tc_request32(ts + 64, a);
+  pages(b, 2);
+  tc_wait_ld(a);
+  tc_request32(ts + 96, b);
+  pages(a, 4);
+  tc_wait_ld(b);
+  pages(b, 6);
   return big;
 }
 
@@ -361,39 +362,44 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
 template <bool kMasked>
 __device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, float fac, int vis, float m) {
   float l = 0.f;
-  auto page = [&](const uint32_t (&s)[16], int j) {
-    const float4 pm = mt[j];
-    const float f = pm.x * fac, off = pm.y - m;
-    const int seen = vis - __float_as_int(pm.w);
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t out[8];
+  auto pages = [&](const uint32_t (&s)[32], int j0) {
+    uint32_t out[16];
 #pragma unroll
-    for (int k = 0; k < 16; k += 2) {
-      float x0 = rows_exp2(fmaf(__uint_as_float(s[k]), f, off));
-      float x1 = rows_exp2(fmaf(__uint_as_float(s[k + 1]), f, off));
-      if constexpr (kMasked) {
-        x0 = k < seen ? x0 : 0.f;
-        x1 = k + 1 < seen ? x1 : 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const float4 pm = mt[j0 + j];
+      const float f = pm.x * fac, off = pm.y - m;
+      const int seen = vis - __float_as_int(pm.w);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float x0 = rows_exp2(fmaf(__uint_as_float(s[16 * j + k]), f, off));
+        float x1 = rows_exp2(fmaf(__uint_as_float(s[16 * j + k + 1]), f, off));
+        if constexpr (kMasked) {
+          x0 = k < seen ? x0 : 0.f;
+          x1 = k + 1 < seen ? x1 : 0.f;
+        }
+        sum[k & 2] += x0;
+        sum[(k & 2) + 1] += x1;
+        out[8 * j + k / 2] = pack_half2(x0, x1);
       }
-      sum[k & 2] += x0;
-      sum[(k & 2) + 1] += x1;
-      out[k / 2] = pack_half2(x0, x1);
+      const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (!kMasked || seen > 0) l = fmaf(all, pm.z, l);
     }
-    tc_st8(ts + 8 * j, out);
-    const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    if (!kMasked || seen > 0) l = fmaf(all, pm.z, l);
+    tc_st16(ts + 8 * j0, out);
   };
-  uint32_t a[16], b[16];
-  tc_request16(ts, a);
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    tc_wait_ld(a);
-    tc_request16(ts + 16 * (j + 1), b);
-    page(a, j);
-    tc_wait_ld(b);
-    if (j < 6) tc_request16(ts + 16 * (j + 2), a);
-    page(b, j + 1);
-  }
+  uint32_t a[32], b[32];
+  tc_request32(ts, a);
+  tc_wait_ld(a);
+  tc_request32(ts + 32, b);
+  pages(a, 0);
+  tc_wait_ld(b);
+  tc_request32(ts + 64, a);
+  pages(b, 2);
+  tc_wait_ld(a);
+  tc_request32(ts + 96, b);
+  pages(a, 4);
+  tc_wait_ld(b);
+  pages(b, 6);
   return l;
 }
 
@@ -424,11 +430,12 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       mbar_init(&bar->sfull[i], 1);
       mbar_init(&bar->pfull[i], 4);
       mbar_init(&bar->wdone[i], 1);
+      mbar_init(&bar->last[i], 1);
       mbar_init(&bar->qfull[i], 4);
       mbar_init(&bar->oempty[i], 8);
     }
-    mbar_init(&bar->qempty, 1);
-    mbar_init(&bar->odone, 1);
+    mbar_init(&bar->qempty, 2);
+    mbar_init(&bar->odone, 2);
     mbar_init(&bar->mlfull, 8);
     *abort_flag = 0;
     fence_mbar_init();
@@ -463,63 +470,61 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     if (lane == 0) tc_arrive(b);
   };
 
-  if (any && warp == 16) {
+  if (any && (warp == 16 || warp == 17)) {
     // ------------------------------------------------------------------ MMAs
+    // a stream's, so that neither waits behind the other
     if (lane == 0) {
       constexpr uint32_t id_s = tc_idesc_f16(kRTile, kRTile), id_o = tc_idesc_f16(kRTile, D);
       constexpr int kAtom = kRTile * 128;   // 64 channels of K or Q
       constexpr int kAtomV = D * 128;       // 64 tokens of V
+      const int st = warp - 16;
       uint32_t g0 = 0, seg = 0;             // tiles before this unit, units with tiles
-      uint32_t count[2] = {0, 0};           // tiles of each stream whose O has been issued
+      uint32_t count = 0;                   // tiles of the stream whose O has been issued
       bool ok = true;
       for (bool go = true; go && ok; go = u.next(p)) {
         if (u.tiles == 0) continue;
         if (!(ok = wait1(&bar->qfull[seg & 1], seg >> 1))) break;
-        for (int i = 0; i <= u.tiles && ok; ++i) {
-          if (i < u.tiles) {   // S of tile i, once w of the stream's tile before has been used
-            const uint32_t g = g0 + i, buf = g & 1, st = i & 1;
-            ok = wait1(&bar->kfull[buf], g >> 1);
-            if (ok && count[st]) ok = wait1(&bar->wdone[st], count[st] - 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t a0 = sb + S::kQ, b0 = sb + S::kK + buf * S::kTile16;
+        for (int i = st; i < u.tiles && ok; i += 2) {
+          const uint32_t g = g0 + i, buf = g & 1;
+          // S of the tile, once w of the stream's tile before, which lies in it, has been used
+          ok = wait1(&bar->kfull[buf], g >> 1) && (count == 0 || wait1(&bar->wdone[st], count - 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a0 = sb + S::kQ, b0 = sb + S::kK + buf * S::kTile16;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * kAtom + (kk & 3) * 32;
-              tc_mma(tmem + st * kRTile, tc_desc_sw128(a0 + off), tc_desc_sw128(b0 + off), id_s, kk != 0);
-            }
-            tc_commit(&bar->sfull[st]);
-            tc_commit(&bar->kempty[buf]);
-            if (i == u.tiles - 1) tc_commit(&bar->qempty);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kAtom + (kk & 3) * 32;
+            tc_mma(tmem + st * kRTile, tc_desc_sw128(a0 + off), tc_desc_sw128(b0 + off), id_s, kk != 0);
           }
-          if (i > 0) {         // O of tile i - 1
-            const uint32_t g = g0 + i - 1, buf = g & 1, st = (i - 1) & 1;
-            ok = wait1(&bar->pfull[st], count[st]) && wait1(&bar->vfull[buf], g >> 1);
-            if (ok && i <= 2 && seg > 0)   // the unit before has been read
-              ok = wait1(&bar->oempty[(seg - 1) & 1], (seg - 1) >> 1);
-            if (!ok) break;
-            ++count[st];
-            tc_fence_after();
-            const uint32_t b0 = sb + S::kV + buf * S::kTile16;
+          tc_commit(&bar->sfull[st]);
+          tc_commit(&bar->kempty[buf]);
+          // O, once the unit before has been read
+          ok = wait1(&bar->pfull[st], count) && wait1(&bar->vfull[buf], g >> 1) &&
+               (i > 1 || seg == 0 || wait1(&bar->oempty[(seg - 1) & 1], (seg - 1) >> 1));
+          if (!ok) break;
+          ++count;
+          tc_fence_after();
+          const uint32_t v0 = sb + S::kV + buf * S::kTile16;
 #pragma unroll
-            for (int kk = 0; kk < kRTile / 16; ++kk)
-              tc_mma_ts(tmem + 2 * kRTile + st * D, tmem + st * kRTile + 8 * kk,
-                        tc_desc_sw128(b0 + (kk >> 2) * kAtomV + (kk & 3) * 32), id_o, i > 2 || kk != 0);
-            tc_commit(&bar->vempty[buf]);
-            tc_commit(&bar->wdone[st]);
-          }
+          for (int kk = 0; kk < kRTile / 16; ++kk)
+            tc_mma_ts(tmem + 2 * kRTile + st * D, tmem + st * kRTile + 8 * kk,
+                      tc_desc_sw128(v0 + (kk >> 2) * kAtomV + (kk & 3) * 32), id_o, i > 1 || kk != 0);
+          tc_commit(&bar->vempty[buf]);
+          tc_commit(&bar->wdone[st]);
         }
         if (!ok) break;
+        // both streams' MMAs of the unit: its queries may go, its O is complete
+        tc_commit(&bar->qempty);
         tc_commit(&bar->odone);
         g0 += u.tiles;
         ++seg;
       }
-      if (!ok) {   // MMAs in flight finish before the CTA ends: the phase after odone's next
-        tc_commit(&bar->odone);
-        mbar_wait(&bar->odone, seg & 1u, p.status);
+      if (!ok) {   // MMAs in flight finish before the CTA ends
+        tc_commit(&bar->last[st]);
+        mbar_wait(&bar->last[st], 0, p.status);
       }
     }
-  } else if (any && warp >= 12) {
+  } else if (any && warp >= 12 && warp < 16) {
     // ---------------------------------------------------- values as fp16 operands
     const int w = warp - 12;   // page slots w and w + 4 of every tile
     uint8_t* raw = smem + S::kRaw + (4 + w) * kRAhead * S::kPage16;
@@ -592,7 +597,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       }
       copies_wait<0>();
     }
-  } else if (any && warp >= 8) {
+  } else if (any && warp >= 8 && warp < 12) {
     // ------------------------------------------- queries and keys as fp16 operands
     const int w = warp - 8;   // page slots w and w + 4 of every tile
     uint8_t* raw = smem + S::kRaw + w * kRAhead * S::kPage16;
@@ -709,7 +714,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       copies_wait<0>();
       ++seg;
     }
-  } else if (any) {
+  } else if (any && warp < 8) {
     // --------------------------------------------------------------- softmax
     const int st = warp >> 2;                      // stream: even or odd tiles
     const int rr = 32 * (warp & 3) + lane;         // query column of the tile
