@@ -453,13 +453,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   if (!any && tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk u;
   if (any) u.start(sh);
-  // A wait of one thread, or of a warp together (one answer for all lanes); false: give up.
+  // A wait of a warp together (one answer for all lanes); false: give up.
   // No barrier completes a second phase before all that wait for the first have passed.
-  auto wait1 = [&](uint64_t* b, uint32_t parity) -> bool {
-    const bool ok = mbar_wait(b, parity & 1u, p.status) && !*abort_flag;
-    if (!ok) *abort_flag = 1;
-    return ok;
-  };
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, p.status) && !*abort_flag);
     if (!ok) *abort_flag = 1;
@@ -472,23 +467,23 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 
   if (any && (warp == 16 || warp == 17)) {
     // ------------------------------------------------------------------ MMAs
-    // a stream's, so that neither waits behind the other
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc_f16(kRTile, kRTile), id_o = tc_idesc_f16(kRTile, D);
-      constexpr int kAtom = kRTile * 128;   // 64 channels of K or Q
-      constexpr int kAtomV = D * 128;       // 64 tokens of V
-      const int st = warp - 16;
-      uint32_t g0 = 0, seg = 0;             // tiles before this unit, units with tiles
-      uint32_t count = 0;                   // tiles of the stream whose O has been issued
-      bool ok = true;
-      for (bool go = true; go && ok; go = u.next(p)) {
-        if (u.tiles == 0) continue;
-        if (!(ok = wait1(&bar->qfull[seg & 1], seg >> 1))) break;
-        for (int i = st; i < u.tiles && ok; i += 2) {
-          const uint32_t g = g0 + i, buf = g & 1;
-          // S of the tile, once w of the stream's tile before, which lies in it, has been used
-          ok = wait1(&bar->kfull[buf], g >> 1) && (count == 0 || wait1(&bar->wdone[st], count - 1));
-          if (!ok) break;
+    // a stream's, so that neither waits behind the other; lane 0 issues
+    constexpr uint32_t id_s = tc_idesc_f16(kRTile, kRTile), id_o = tc_idesc_f16(kRTile, D);
+    constexpr int kAtom = kRTile * 128;   // 64 channels of K or Q
+    constexpr int kAtomV = D * 128;       // 64 tokens of V
+    const int st = warp - 16;
+    uint32_t g0 = 0, seg = 0;             // tiles before this unit, units with tiles
+    uint32_t count = 0;                   // tiles of the stream whose O has been issued
+    bool ok = true;
+    for (bool go = true; go && ok; go = u.next(p)) {
+      if (u.tiles == 0) continue;
+      if (!(ok = wait(&bar->qfull[seg & 1], seg >> 1))) break;
+      for (int i = st; i < u.tiles && ok; i += 2) {
+        const uint32_t g = g0 + i, buf = g & 1;
+        // S of the tile, once w of the stream's tile before, which lies in it, has been used
+        ok = wait(&bar->kfull[buf], g >> 1) && (count == 0 || wait(&bar->wdone[st], count - 1));
+        if (!ok) break;
+        if (lane == 0) {
           tc_fence_after();
           const uint32_t a0 = sb + S::kQ, b0 = sb + S::kK + buf * S::kTile16;
 #pragma unroll
@@ -498,11 +493,14 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           }
           tc_commit(&bar->sfull[st]);
           tc_commit(&bar->kempty[buf]);
-          // O, once the unit before has been read
-          ok = wait1(&bar->pfull[st], count) && wait1(&bar->vfull[buf], g >> 1) &&
-               (i > 1 || seg == 0 || wait1(&bar->oempty[(seg - 1) & 1], (seg - 1) >> 1));
-          if (!ok) break;
-          ++count;
+        }
+        __syncwarp();
+        // O, once the unit before has been read
+        ok = wait(&bar->pfull[st], count) && wait(&bar->vfull[buf], g >> 1) &&
+             (i > 1 || seg == 0 || wait(&bar->oempty[(seg - 1) & 1], (seg - 1) >> 1));
+        if (!ok) break;
+        ++count;
+        if (lane == 0) {
           tc_fence_after();
           const uint32_t v0 = sb + S::kV + buf * S::kTile16;
 #pragma unroll
@@ -512,17 +510,20 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           tc_commit(&bar->vempty[buf]);
           tc_commit(&bar->wdone[st]);
         }
-        if (!ok) break;
-        // both streams' MMAs of the unit: its queries may go, its O is complete
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) {   // the stream's MMAs of the unit: its queries may go, its O is complete
         tc_commit(&bar->qempty);
         tc_commit(&bar->odone);
-        g0 += u.tiles;
-        ++seg;
       }
-      if (!ok) {   // MMAs in flight finish before the CTA ends
-        tc_commit(&bar->last[st]);
-        mbar_wait(&bar->last[st], 0, p.status);
-      }
+      __syncwarp();
+      g0 += u.tiles;
+      ++seg;
+    }
+    if (!ok && lane == 0) {   // MMAs in flight finish before the CTA ends
+      tc_commit(&bar->last[st]);
+      mbar_wait(&bar->last[st], 0, p.status);
     }
   } else if (any && warp >= 12 && warp < 16) {
     // ---------------------------------------------------- values as fp16 operands

@@ -48,25 +48,48 @@ __device__ __forceinline__ int row_limit(const Kv8Params& p, int b, int row, int
   return pos >= 0 && pos < len ? pos + 1 : 0;
 }
 
-template <int NT>
-__device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
+// Tokens that the rows of a tile see: the furthest row's.  kWarp: called by whole warps with
+// one tile, each lane its rows; else by a thread on its own (eight loads in flight).
+template <int NT, bool kWarp>
+__device__ __forceinline__ int tile_limit(const Kv8Params& p, int b, int tile, int len) {
+  const int r0 = tile * 8 * NT / p.G;
+  const int r1 = min(p.cols - 1, tile * 8 * NT + 8 * NT - 1) / p.G;
+  if constexpr (kWarp) {
+    int vis = 0;
+    for (int r = r0 + (threadIdx.x & 31); r <= r1; r += 32) vis = max(vis, row_limit(p, b, r, len));
+    return __reduce_max_sync(0xffffffffu, vis);
+  }
+  int vis = row_limit(p, b, r1, len);   // rows are mostly in order
+  if (vis == len) return vis;
+#pragma unroll 8
+  for (int r = r0; r < r1; ++r) vis = max(vis, row_limit(p, b, r, len));
+  return vis;
+}
+
+template <int NT, bool kWarp>
+__device__ __forceinline__ Entry make_entry(const Kv8Params& p, int e) {
   Entry t;
   t.b = e / p.tiles;
   t.tile = e - t.b * p.tiles;
   const int len = p.seq_lens[t.b];
   t.len = len >= 0 && len <= p.max_len ? len : 0;
-  if (p.q_pos) {
-    const int r0 = t.tile * 8 * NT / p.G;
-    const int r1 = min(p.cols - 1, t.tile * 8 * NT + 8 * NT - 1) / p.G;
-    t.vis = 0;
-    for (int r = r0; r <= r1; ++r) t.vis = max(t.vis, row_limit(p, t.b, r, t.len));
-  } else {
-    t.vis = t.len;
-  }
+  t.vis = p.q_pos ? tile_limit<NT, kWarp>(p, t.b, t.tile, t.len) : t.len;
   const int whole = t.len / kPage;
   t.n8 = min(whole, (t.vis + kPage - 1) / kPage);
   t.pages = max(1, t.n8 + (t.vis > whole * kPage ? 1 : 0));
   return t;
+}
+
+// By whole warps.
+template <int NT>
+__device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
+  return make_entry<NT, true>(p, e);
+}
+
+// Pages of an entry's units of all KV heads, by a thread on its own.
+template <int NT>
+__device__ __forceinline__ int64_t entry_pages(const Kv8Params& p, int e) {
+  return static_cast<int64_t>(make_entry<NT, false>(p, e).pages) * p.hkv;
 }
 
 // First element of column `col` of the tile; null when the tile has fewer columns.
@@ -77,59 +100,25 @@ __device__ __forceinline__ const uint16_t* column(const Kv8Params& p, const Entr
   return p.q + ((static_cast<size_t>(t.b) * p.m_rows + row) * p.hq + h * p.G + g) * D;
 }
 
-// Sum over the CTA's kWarps warps; scratch: a word for each.
+// Inclusive prefix sum over the CTA's threads, and the sum of all; scratch: a word per warp.
 template <int kWarps>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += scratch[w];
-  __syncthreads();
-  return total;
-}
-
-// The entry that holds page `at` of the entries laid end to end (each weighed by
-// the KV heads), and the pages before it.
-template <int NT, int kWarps>
-__device__ void find_entry(const Kv8Params& p, int64_t at, int64_t* scratch, int& entry,
-                           int64_t& before) {
-  __shared__ int found;
-  __shared__ int64_t found_before;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t base = 0;
-  if (tid == 0) found = -1;
-  __syncthreads();
-  for (int e0 = 0; e0 < p.entries; e0 += 32 * kWarps) {
-    const int e = e0 + tid;
-    const int64_t v = e < p.entries ? static_cast<int64_t>(entry_of<NT>(p, e).pages) * p.hkv : 0;
-    int64_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int64_t off = base, all = base;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) off += scratch[w];
-      all += scratch[w];
-    }
-    incl += off;
-    if (v > 0 && incl - v <= at && at < incl) {
-      found = e;
-      found_before = incl - v;
-    }
-    __syncthreads();
-    if (found >= 0) break;
-    base = all;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
-  entry = found;
-  before = found_before;
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) v += scratch[w];
+    all += scratch[w];
+  }
+  __syncthreads();
+  return v;
 }
 
 // This CTA's equal share [at, end) of the pages of all units laid end to end, the unit
@@ -142,15 +131,19 @@ struct Share {
 
 template <int NT, int kWarps>
 __device__ bool find_share(const Kv8Params& p, int min_share, int64_t* scratch, Share& s) {
-  int64_t sum = 0, before = 0;
+  constexpr int kThreads = 32 * kWarps;
+  __shared__ int found;
+  __shared__ int64_t found_before;
+  const int tid = threadIdx.x;
+  // a thread's entry, of up to kThreads; of more, the sums of kThreads at a time
+  int64_t v = 0, incl = 0, total = 0;
   if (p.entries == 1) {
     s.t = entry_of<NT>(p, 0);
-    sum = s.t.pages;
+    total = static_cast<int64_t>(s.t.pages) * p.hkv;
   } else {
-    for (int i = threadIdx.x; i < p.entries; i += 32 * kWarps) sum += entry_of<NT>(p, i).pages;
-    sum = block_sum<kWarps>(sum, scratch);
+    for (int e = tid; e < p.entries; e += kThreads) v += entry_pages<NT>(p, e);
+    incl = block_scan<kWarps>(v, scratch, total);
   }
-  const int64_t total = sum * p.hkv;
   // at least, and in multiples of, min_share
   s.share = max(static_cast<int64_t>(1), (total + static_cast<int64_t>(gridDim.x) * min_share - 1) /
                                              (static_cast<int64_t>(gridDim.x) * min_share)) * min_share;
@@ -158,8 +151,26 @@ __device__ bool find_share(const Kv8Params& p, int min_share, int64_t* scratch, 
   s.end = min(total, s.at + s.share);
   if (s.at >= s.end) return false;
   s.e = 0;
+  int64_t before = 0;
   if (p.entries > 1) {
-    find_entry<NT, kWarps>(p, s.at, scratch, s.e, before);
+    for (int e0 = 0; e0 < p.entries; e0 += kThreads) {
+      int64_t all = total;
+      if (p.entries > kThreads) {
+        v = e0 + tid < p.entries ? entry_pages<NT>(p, e0 + tid) : 0;
+        incl = before + block_scan<kWarps>(v, scratch, all);
+      }
+      if (s.at < before + all) {   // in these entries: one thread's
+        if (incl - v <= s.at && s.at < incl) {
+          found = e0 + tid;
+          found_before = incl - v;
+        }
+        break;
+      }
+      before += all;
+    }
+    __syncthreads();
+    s.e = found;
+    before = found_before;
     s.t = entry_of<NT>(p, s.e);
   }
   s.h = static_cast<int>((s.at - before) / s.t.pages);

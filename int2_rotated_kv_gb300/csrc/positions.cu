@@ -324,14 +324,8 @@ struct RopeItem {
   }
 };
 
-template <bool kInter, bool kVec>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ __align__(16) float2 cs[];   // [tokens][half]: A cos, A sin
-  __shared__ int pos[kRopeTokens];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.n - t0));
+// cos and sin of a CTA's tokens, and their positions, in shared memory.
+__device__ __forceinline__ void rope_angles(const RopeParams& p, int64_t t0, int nt, float2* cs, int* pos) {
   if (threadIdx.x < nt) pos[threadIdx.x] = p.positions[t0 + threadIdx.x];
   for (int i = threadIdx.x; i < nt * p.half; i += kRopeThreads) {
     const int t = i / p.half, j = i - t * p.half;
@@ -343,6 +337,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     cs[i] = make_float2(p.amplitude * c, p.amplitude * p.sign * s);
   }
   __syncthreads();
+}
+
+template <bool kInter, bool kVec>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 cs[];   // [tokens][half]: A cos, A sin
+  __shared__ int pos[kRopeTokens];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.n - t0));
+  rope_angles(p, t0, nt, cs, pos);
   const int heads = p.hq + p.hkv;
   constexpr int kRun = kVec ? 8 : 1;
   // items of a head: rotated pairs in runs, then the unrotated channels in runs
@@ -377,6 +382,61 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       x.store(p, it, pairs);
       if (two) y.store(p, it, pairs);
     }
+  }
+}
+
+// Runs of 8 channels (16-byte accesses) where the rotated part is not made of such runs:
+// a run's partners may lie across two others, so the head vectors of a round pass through
+// shared memory.  A round: as many head vectors as the CTA has threads for.
+template <bool kInter>
+__global__ void __launch_bounds__(kRopeThreads) rope_runs_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 cs[];   // [tokens][half]: A cos, A sin
+  __shared__ __align__(16) uint16_t rows[8 * kRopeThreads];
+  __shared__ int pos[kRopeTokens];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.n - t0));
+  rope_angles(p, t0, nt, cs, pos);
+  const int heads = p.hq + p.hkv, items = p.d / 8, step = kRopeThreads / items;
+  const int vec = threadIdx.x / items, c0 = 8 * (threadIdx.x - vec * items);
+  int t = 0, h = vec;
+  for (int r = 0; r < nt * heads; r += step) {
+    for (; h >= heads && t < nt; h -= heads) ++t;
+    const bool mine = vec < step && t < nt && pos[t] >= 0;
+    const int64_t row = t0 + t;
+    const bool is_q = h < p.hq;
+    if (mine)
+      *reinterpret_cast<uint4*>(rows + vec * p.d + c0) = *reinterpret_cast<const uint4*>(
+          (is_q ? p.q + row * p.q_stride + h * p.d : p.k + row * p.k_stride + (h - p.hq) * p.d) + c0);
+    __syncthreads();
+    if (mine) {
+      const uint16_t* x = rows + vec * p.d;
+      const float2* w = cs + t * p.half;
+      uint32_t out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = c0 + 2 * k + e;
+          const bool first = kInter ? e == 0 : c < p.half;
+          const int pair = kInter ? c >> 1 : first ? c : c - p.half;
+          y[e] = bf16_to_float(x[c]);
+          if (c < 2 * p.half) {
+            const float other = bf16_to_float(x[kInter ? c ^ 1 : first ? c + p.half : c - p.half]);
+            const float2 a = w[pair];
+            y[e] = first ? y[e] * a.x - other * a.y : y[e] * a.x + other * a.y;
+          }
+        }
+        out[k] = pack_bf162(y[0], y[1]);
+      }
+      *reinterpret_cast<uint4*>((is_q ? p.q_out + row * p.q_out_stride + h * p.d
+                                      : p.k_out + row * p.k_out_stride + (h - p.hq) * p.d) + c0) =
+          make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    __syncthreads();
+    h += step;
   }
 }
 
@@ -498,18 +558,20 @@ oscar_status oscar_rope(const void* q, const void* k, const int32_t* positions,
   p.amplitude = amplitude;
   p.sign = inverse ? -1.f : 1.f;
   p.copy = (num_q_heads && q_out != q) || (num_kv_heads && k_out != k);
-  const bool vec =
-      p.half % (interleaved ? 4 : 8) == 0 && head_dim % 8 == 0 &&
-      ((p.q_stride | p.k_stride | p.q_out_stride | p.k_out_stride) & 7) == 0 &&
-      ((reinterpret_cast<uintptr_t>(num_q_heads ? q : nullptr) |
-        reinterpret_cast<uintptr_t>(num_kv_heads ? k : nullptr) |
-        reinterpret_cast<uintptr_t>(num_q_heads ? q_out : nullptr) |
-        reinterpret_cast<uintptr_t>(num_kv_heads ? k_out : nullptr)) & 15) == 0;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(num_q_heads ? q : nullptr) |
+                         reinterpret_cast<uintptr_t>(num_kv_heads ? k : nullptr) |
+                         reinterpret_cast<uintptr_t>(num_q_heads ? q_out : nullptr) |
+                         reinterpret_cast<uintptr_t>(num_kv_heads ? k_out : nullptr)) & 15) == 0;
+  const bool vec = p.half % (interleaved ? 4 : 8) == 0 && head_dim % 8 == 0 &&
+      ((p.q_stride | p.k_stride | p.q_out_stride | p.k_out_stride) & 7) == 0 && aligned;
+  const bool runs = !vec && head_dim % 8 == 0 && head_dim <= 8 * kRopeThreads &&
+      ((p.q_stride | p.k_stride | p.q_out_stride | p.k_out_stride) & 7) == 0 && aligned;
   // About four items a thread: fewer leave the angles' cost bare, more make the last,
   // partly filled wave of CTAs long (72 heads x 16 items, 5003 tokens: 4 tokens a CTA
   // 55.9 us, one token a CTA 31.5 us).
-  const int64_t items = heads * (vec ? (p.half / (interleaved ? 4 : 8) + (p.copy ? (head_dim - rotary_dim) / 8 : 0))
-                                     : (p.half + (p.copy ? head_dim - rotary_dim : 0)));
+  const int64_t items = heads * (runs  ? head_dim / 8
+                                 : vec ? p.half / (interleaved ? 4 : 8) + (p.copy ? (head_dim - rotary_dim) / 8 : 0)
+                                       : p.half + (p.copy ? head_dim - rotary_dim : 0));
   p.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, 4 * kRopeThreads / items)));
   const int64_t ctas = (n + p.tokens - 1) / p.tokens;
   if (ctas > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;
@@ -517,11 +579,10 @@ oscar_status oscar_rope(const void* q, const void* k, const int32_t* positions,
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(ctas)), dim3(kRopeThreads),
                                             smem, static_cast<cudaStream_t>(stream), &attr);
-  const cudaError_t e =
-      interleaved ? (vec ? cudaLaunchKernelEx(&cfg, rope_kernel<true, true>, p)
-                         : cudaLaunchKernelEx(&cfg, rope_kernel<true, false>, p))
-                  : (vec ? cudaLaunchKernelEx(&cfg, rope_kernel<false, true>, p)
-                         : cudaLaunchKernelEx(&cfg, rope_kernel<false, false>, p));
+  const auto kernel = runs  ? (interleaved ? rope_runs_kernel<true> : rope_runs_kernel<false>)
+                      : vec ? (interleaved ? rope_kernel<true, true> : rope_kernel<false, true>)
+                            : (interleaved ? rope_kernel<true, false> : rope_kernel<false, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 

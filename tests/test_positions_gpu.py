@@ -153,7 +153,9 @@ def _rope_check(got, x, pos, phases, inter, amplitude=1.0, inverse=False):
 @pytest.mark.parametrize("n,hq,hkv,d,rd,inter", [
     (1, 32, 8, 128, 128, False), (37, 4, 1, 64, 64, True), (5, 3, 3, 128, 64, False),
     (9, 8, 2, 128, 40, True), (6, 2, 1, 70, 10, False), (11, 1, 0, 96, 96, False),
-    (3, 0, 2, 64, 6, True), (129, 16, 2, 256, 32, False), (2, 1, 1, 2, 2, True)])
+    (3, 0, 2, 64, 6, True), (129, 16, 2, 256, 32, False), (2, 1, 1, 2, 2, True), (41, 5, 2, 128, 74, False),
+    (17, 3, 1, 64, 62, True), (7, 33, 8, 72, 26, False), (5, 2, 1, 1024, 1024, False),
+    (4, 1, 1, 1024, 1022, False)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_rope_matches_oracle(n, hq, hkv, d, rd, inter, in_place):
     t, L = H.torch(), H.lib()
