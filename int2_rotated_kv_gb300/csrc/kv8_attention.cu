@@ -463,11 +463,11 @@ __device__ __forceinline__ void issue_tail(const Kv8Params& p, const Entry& t, i
 template <typename C>
 __device__ __forceinline__ bool copied(const Kv8Params& p, Ring& r, int& s) {
   s = r.n_out % C::kStages;
-  const bool got = mbar_wait(r.bars + s, (r.n_out / C::kStages) & 1, p.status);
+  const bool got = wait_copy(r.bars + s, (r.n_out / C::kStages) & 1, p.status);
   ++r.n_out;
   if (__all_sync(0xffffffffu, got)) return true;
   for (; r.n_out < r.n_in; ++r.n_out)
-    mbar_wait(r.bars + r.n_out % C::kStages, (r.n_out / C::kStages) & 1, p.status);
+    wait_longer(r.bars + r.n_out % C::kStages, (r.n_out / C::kStages) & 1, p.status);
   r.alive = false;
   return false;
 }
@@ -620,9 +620,9 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     at = static_cast<int64_t>(t.pages) * rank / p.cluster;
     end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
   } else {
-    __shared__ int64_t scratch[kWarps];
-    Share sh;
-    if (!find_share<NT, kWarps>(p, min_share, scratch, sh)) {
+    bool any;
+    const Share sh = find_share<NT, kWarps>(p, min_share, any);
+    if (!any) {
       if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }

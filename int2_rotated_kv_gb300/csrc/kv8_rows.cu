@@ -15,8 +15,8 @@
 //   0-3, 4-7      softmax of even and odd tiles ("streams", each with its own S, w, O in
 //                 tensor memory, own maxima and sums, merged at the unit's end): reads S
 //                 twice, for the maximum and for w, which overwrites S;
-//   8-11, 12-15   pages -> fp16 K tiles and V tiles, 128-byte swizzled, two of each (the
-//                 former also the queries of a unit).  A warp has two pages of every tile;
+//   8-11, 12-15   pages -> fp16 K tiles and V tiles, 128-byte swizzled, two of each, and
+//                 the queries of a unit.  A warp has two pages of every tile;
 //                 each lane copies (cp.async) the chunks that it will convert itself, three
 //                 pages ahead, so nothing is waited for but its own copies.  (As bulk
 //                 copies of 2 KB, 24 a tile, the copies alone took 3400 cycles a tile.)
@@ -90,14 +90,18 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const Kv8Params& p) {
     if (unit0 + p1 >= end) return false;
-    unit0 += t.pages;
-    if (++h == p.hkv) {
-      h = 0;
-      t = entry_of<kRowsNT>(p, ++e);
-    }
-    p0 = 0;
-    set();
+    *this = after(p, *this);
     return true;
+  }
+  static __device__ __noinline__ Walk after(const Kv8Params& p, Walk u) {
+    u.unit0 += u.t.pages;
+    if (++u.h == p.hkv) {
+      u.h = 0;
+      u.t = entry_of<kRowsNT>(p, ++u.e);
+    }
+    u.p0 = 0;
+    u.set();
+    return u;
   }
   // Page slots of tile i: pages in slots 0 .. n - 1, the tail in slot `tail_slot` (-1: none).
   __device__ __forceinline__ void slots(int i, int& n, int& tail_slot) const {
@@ -228,6 +232,7 @@ __device__ __forceinline__ uint32_t tail_magnitude(const uint16_t* area, int whi
                                                    bool& bad) {
   uint32_t top = 0;
   bool odd = false;
+#pragma unroll 1
   for (int c = lane; c < D; c += 32) {   // chunks of 16 elements
     const uint4* s = reinterpret_cast<const uint4*>(area + 16 * c);
     const uint4 a = s[0], b = s[1];
@@ -269,7 +274,9 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
   const int up = scale_up(tail_magnitude<D>(area, 0, n, lane, odd));
   const int up_v = scale_up(tail_magnitude<D>(area + Kv8Fmt<D>::kTailHalf, 1, n, lane, odd));
   const float mul = power_of_two(up);
+#pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
     for (int part = 0; part < 2; ++part) {
       const uint4 x = reinterpret_cast<const uint4*>(area)[2 * key_chunk_of(lane, c) + part];
       *reinterpret_cast<uint4*>(dst + key_place(lane, c, part)) =
@@ -293,6 +300,7 @@ __device__ __noinline__ void tail_values(const Kv8Params& p, int b, int h, int l
   const uint16_t* area = tail_block<D>(p, b, h, ok) + Kv8Fmt<D>::kTailHalf;
   const int n = len % kPage;
   const float mul = power_of_two(scale_up(tail_magnitude<D>(area, 1, n, lane, odd)));
+#pragma unroll 1
   for (int c = 0; c < D / 64; ++c) {
     uint32_t o[4][4];   // channel x pairs of tokens
 #pragma unroll
@@ -310,6 +318,46 @@ __device__ __noinline__ void tail_values(const Kv8Params& p, int b, int h, int l
       }
     }
     store_square<D>(dst, c, w, lane, o);
+  }
+}
+
+// Sixteen query columns of a unit (the w-th of eight parts) as fp16 rows of the operand at
+// dst, each scaled by a power of two; facs gets what a logit in the log2 domain is per unit of
+// S.  D / 8 lanes a column, four loads in flight.
+template <int D>
+__device__ __noinline__ void load_queries(const Kv8Params& p, int b, int h, int tile, int w, int lane,
+                                          uint8_t* dst, float* facs) {
+  constexpr int kLanes = D / 8, kCols = 32 / kLanes;   // lanes of a column, columns at once
+  const int part = lane % kLanes;
+  int rr = 16 * w + lane / kLanes, col = tile * 128 + rr;
+  int row = col / p.G, g = col - row * p.G;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16 / kCols; i0 += 4) {
+    uint4 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t* src = p.q + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D;
+      q[i] = col < p.cols ? reinterpret_cast<const uint4*>(src)[part] : make_uint4(0, 0, 0, 0);
+      col += kCols;
+      for (g += kCols; g >= p.G; g -= p.G) ++row;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i, rr += kCols) {
+      const uint32_t x[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      uint32_t top = 0;   // largest finite magnitude
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int up = scale_up(top);
+      const float mul = power_of_two(up);
+      *reinterpret_cast<uint4*>(dst + tc_sw128_offset(rr, 8 * part, kRTile)) =
+          make_uint4(half_pair(x[0], mul), half_pair(x[1], mul), half_pair(x[2], mul), half_pair(x[3], mul));
+      if (part == 0) facs[rr] = p.scale_log2 * power_of_two(-up);
+    }
   }
 }
 
@@ -343,17 +391,16 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
   };
   uint32_t a[32], b[32];
   tc_request32(ts, a);
+#pragma unroll 1
+  for (int j = 0; j < 8; j += 4) {
+    tc_wait_ld(a);
+    tc_request32(ts + 16 * j + 32, b);
+    pages(a, j);
+    tc_wait_ld(b);
+    tc_request32(ts + (j == 0 ? 64 : 0), a);   // (the last one is not looked at)
+    pages(b, j + 2);
+  }
   tc_wait_ld(a);
-  tc_request32(ts + 32, b);
-  pages(a, 0);
-  tc_wait_ld(b);
-  tc_request32(ts + 64, a);
-  pages(b, 2);
-  tc_wait_ld(a);
-  tc_request32(ts + 96, b);
-  pages(a, 4);
-  tc_wait_ld(b);
-  pages(b, 6);
   return big;
 }
 
@@ -389,17 +436,16 @@ __device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, flo
   };
   uint32_t a[32], b[32];
   tc_request32(ts, a);
+#pragma unroll 1
+  for (int j = 0; j < 8; j += 4) {
+    tc_wait_ld(a);
+    tc_request32(ts + 16 * j + 32, b);
+    pages(a, j);
+    tc_wait_ld(b);
+    tc_request32(ts + (j == 0 ? 64 : 0), a);   // (the last one is not looked at)
+    pages(b, j + 2);
+  }
   tc_wait_ld(a);
-  tc_request32(ts + 32, b);
-  pages(a, 0);
-  tc_wait_ld(b);
-  tc_request32(ts + 64, a);
-  pages(b, 2);
-  tc_wait_ld(a);
-  tc_request32(ts + 96, b);
-  pages(a, 4);
-  tc_wait_ld(b);
-  pages(b, 6);
   return l;
 }
 
@@ -409,7 +455,6 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   using S = RowsSmem<D>;
   using F = Kv8Fmt<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t scratch[kRWarps];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   RowsBars* bar = reinterpret_cast<RowsBars*>(smem + S::kBars);
@@ -431,7 +476,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       mbar_init(&bar->pfull[i], 4);
       mbar_init(&bar->wdone[i], 1);
       mbar_init(&bar->last[i], 1);
-      mbar_init(&bar->qfull[i], 4);
+      mbar_init(&bar->qfull[i], 8);
       mbar_init(&bar->oempty[i], 8);
     }
     mbar_init(&bar->qempty, 2);
@@ -448,15 +493,15 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   pdl_wait();
   pdl_trigger();
 
-  Share sh;
-  const bool any = find_share<kRowsNT, kRWarps>(p, min_share, scratch, sh);
+  bool any;
+  const Share sh = find_share<kRowsNT, kRWarps>(p, min_share, any);
   if (!any && tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk u;
   if (any) u.start(sh);
   // A wait of a warp together (one answer for all lanes); false: give up.
   // No barrier completes a second phase before all that wait for the first have passed.
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, p.status) && !*abort_flag);
+    const bool ok = __all_sync(0xffffffffu, wait_copy(b, parity & 1u, p.status) && !*abort_flag);
     if (!ok) *abort_flag = 1;
     return ok;
   };
@@ -529,7 +574,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     // ---------------------------------------------------- values as fp16 operands
     const int w = warp - 12;   // page slots w and w + 4 of every tile
     uint8_t* raw = smem + S::kRaw + (4 + w) * kRAhead * S::kPage16;
-    uint32_t g = 0;
+    uint32_t g = 0, seg = 0;
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
       PageIds ids(p, u, lane);
@@ -547,8 +592,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         }
         copies_commit();
       };
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kRAhead; ++k) request(k, k);
+      if (!wait(&bar->qempty, seg + 1)) break;
+      if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
+      load_queries<D>(p, u.t.b, u.h, u.t.tile, 4 + w, lane, smem + S::kQ, facs + (seg & 1) * 128);
+      fence_proxy_async();
+      arrive(&bar->qfull[seg & 1]);
       int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
@@ -583,6 +633,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
               continue;
             }
             const uint4* mine = half ? page1 : page0;
+#pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
               uint32_t o[4][4];
               value_square<kE4m3>(mine[64 * c], mine[64 * c + 32], o);
@@ -590,13 +641,14 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             }
           }
         }
-        request(2 * i + kRAhead, at);
-        request(2 * i + kRAhead + 1, next);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
         at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->vfull[buf]);
       }
       copies_wait<0>();
+      ++seg;
     }
   } else if (any && warp >= 8 && warp < 12) {
     // ------------------------------------------- queries and keys as fp16 operands
@@ -627,37 +679,14 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         }
         copies_commit();
       };
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kRAhead; ++k) request(k, k);
       if (!wait(&bar->qempty, seg + 1)) break;
       // and the unit before the last has been read (what is kept by unit comes round again)
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
-      {   // a query column per thread: fp16 scaled by a power of two
-        const int rr = 32 * w + lane;
-        const uint16_t* src = column(p, u.t, u.h, u.t.tile * 128 + rr, D);
-        uint32_t top = 0;
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 q = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
-            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-          }
-        }
-        const int up = scale_up(top);
-        const float mul = power_of_two(up);
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 q = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(smem + S::kQ + tc_sw128_offset(rr, 8 * c, kRTile)) =
-              make_uint4(half_pair(q.x, mul), half_pair(q.y, mul), half_pair(q.z, mul), half_pair(q.w, mul));
-        }
-        facs[(seg & 1) * 128 + rr] = p.scale_log2 * power_of_two(-up);
-        fence_proxy_async();
-        arrive(&bar->qfull[seg & 1]);
-      }
+      load_queries<D>(p, u.t.b, u.h, u.t.tile, w, lane, smem + S::kQ, facs + (seg & 1) * 128);
+      fence_proxy_async();
+      arrive(&bar->qfull[seg & 1]);
       int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
@@ -702,12 +731,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
               if (lane == 0) meta[(g & 3) * 8 + 4 * half + w] = m;
               continue;
             }
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c)
               store_keys<kE4m3>(dst + 8192 * half, c, lane, (half ? mine1 : mine0)[32 * c]);
           }
         }
-        request(2 * i + kRAhead, at);
-        request(2 * i + kRAhead + 1, next);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
         at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->kfull[buf]);
@@ -763,7 +793,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             m = up;
             l *= a;
             if (i > 1) {   // the stream's O so far (its last MMA finished before this S began)
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
                 tc_request16(to + 16 * c, o);
@@ -802,7 +832,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const uint16_t* tail = reinterpret_cast<const uint16_t*>(p.tail + (tail_id * p.hkv + u.h) * F::kTailBytes) +
           F::kTailHalf;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {   // 16 channels
         const int ch = st * (D / 2) + 16 * c;
         float o[16];
@@ -823,6 +853,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           for (int k = 0; k < 16; ++k) o[k] = fmaf(__uint_as_float(x[k]), a1, o[k]);
         }
         if (odd) {   // values of the tail that are not finite, to the rows that see them
+#pragma unroll 1
           for (int t = 0; t < u.t.len - tail0 && tail0 + t < vis; ++t)
 #pragma unroll
             for (int k = 0; k < 16; ++k) {

@@ -49,19 +49,20 @@ __device__ __forceinline__ int row_limit(const Kv8Params& p, int b, int row, int
 }
 
 // Tokens that the rows of a tile see: the furthest row's.  kWarp: called by whole warps with
-// one tile, each lane its rows; else by a thread on its own (eight loads in flight).
+// one tile, each lane its rows; else by a thread on its own (four loads in flight).
 template <int NT, bool kWarp>
 __device__ __forceinline__ int tile_limit(const Kv8Params& p, int b, int tile, int len) {
   const int r0 = tile * 8 * NT / p.G;
   const int r1 = min(p.cols - 1, tile * 8 * NT + 8 * NT - 1) / p.G;
   if constexpr (kWarp) {
     int vis = 0;
+#pragma unroll 1
     for (int r = r0 + (threadIdx.x & 31); r <= r1; r += 32) vis = max(vis, row_limit(p, b, r, len));
     return __reduce_max_sync(0xffffffffu, vis);
   }
   int vis = row_limit(p, b, r1, len);   // rows are mostly in order
   if (vis == len) return vis;
-#pragma unroll 8
+#pragma unroll 4
   for (int r = r0; r < r1; ++r) vis = max(vis, row_limit(p, b, r, len));
   return vis;
 }
@@ -84,12 +85,6 @@ __device__ __forceinline__ Entry make_entry(const Kv8Params& p, int e) {
 template <int NT>
 __device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
   return make_entry<NT, true>(p, e);
-}
-
-// Pages of an entry's units of all KV heads, by a thread on its own.
-template <int NT>
-__device__ __forceinline__ int64_t entry_pages(const Kv8Params& p, int e) {
-  return static_cast<int64_t>(make_entry<NT, false>(p, e).pages) * p.hkv;
 }
 
 // First element of column `col` of the tile; null when the tile has fewer columns.
@@ -129,53 +124,72 @@ struct Share {
   Entry t;
 };
 
+// (Kept out of line, and its loops rolled: code that a CTA runs once costs its fetches.)
 template <int NT, int kWarps>
-__device__ bool find_share(const Kv8Params& p, int min_share, int64_t* scratch, Share& s) {
+__device__ __noinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
   constexpr int kThreads = 32 * kWarps;
-  __shared__ int found;
+  __shared__ int64_t scratch[kWarps];
+  __shared__ Entry found;
+  __shared__ int found_number;
   __shared__ int64_t found_before;
   const int tid = threadIdx.x;
-  // a thread's entry, of up to kThreads; of more, the sums of kThreads at a time
-  int64_t v = 0, incl = 0, total = 0;
-  if (p.entries == 1) {
-    s.t = entry_of<NT>(p, 0);
-    total = static_cast<int64_t>(s.t.pages) * p.hkv;
-  } else {
-    for (int e = tid; e < p.entries; e += kThreads) v += entry_pages<NT>(p, e);
-    incl = block_scan<kWarps>(v, scratch, total);
-  }
-  // at least, and in multiples of, min_share
-  s.share = max(static_cast<int64_t>(1), (total + static_cast<int64_t>(gridDim.x) * min_share - 1) /
-                                             (static_cast<int64_t>(gridDim.x) * min_share)) * min_share;
-  s.at = blockIdx.x * s.share;
-  s.end = min(total, s.at + s.share);
-  if (s.at >= s.end) return false;
-  s.e = 0;
-  int64_t before = 0;
-  if (p.entries > 1) {
+  Share s{};
+  int64_t before = 0, total = 0;
+  // pass 0: the sum; pass 1: the entry that holds `at`, kThreads at a time (of no more
+  // entries than that, with what pass 0 found)
+  Entry own{};
+  int64_t v = 0, incl = 0, all = 0;
+  const bool few = p.entries <= kThreads;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
     for (int e0 = 0; e0 < p.entries; e0 += kThreads) {
-      int64_t all = total;
-      if (p.entries > kThreads) {
-        v = e0 + tid < p.entries ? entry_pages<NT>(p, e0 + tid) : 0;
-        incl = before + block_scan<kWarps>(v, scratch, all);
-      }
-      if (s.at < before + all) {   // in these entries: one thread's
-        if (incl - v <= s.at && s.at < incl) {
-          found = e0 + tid;
-          found_before = incl - v;
+      if (pass == 0 || !few) {
+        v = 0;
+        if (e0 + tid < p.entries) {
+          own = make_entry<NT, false>(p, e0 + tid);
+          v = static_cast<int64_t>(own.pages) * p.hkv;
         }
-        break;
+        incl = block_scan<kWarps>(v, scratch, all);
       }
-      before += all;
+      if (pass == 0) {
+        total += all;
+      } else {
+        if (s.at < before + all) {   // one thread's
+          if (before + incl - v <= s.at && s.at < before + incl) {
+            found = own;
+            found_number = e0 + tid;
+            found_before = before + incl - v;
+          }
+          break;
+        }
+        before += all;
+      }
     }
-    __syncthreads();
-    s.e = found;
-    before = found_before;
-    s.t = entry_of<NT>(p, s.e);
+    if (pass == 0) {   // at least, and in multiples of, min_share
+      const int64_t step = static_cast<int64_t>(gridDim.x) * min_share;
+      s.share = max(static_cast<int64_t>(1), (total + step - 1) / step) * min_share;
+      s.at = blockIdx.x * s.share;
+      s.end = min(total, s.at + s.share);
+      any = s.at < s.end;
+      if (!any) return s;
+    }
   }
-  s.h = static_cast<int>((s.at - before) / s.t.pages);
-  s.unit0 = before + static_cast<int64_t>(s.h) * s.t.pages;
-  return true;
+  __syncthreads();
+  s.e = found_number;
+  s.t = found;
+  // (the entry's pages are fewer than 2^31 for all heads of a cache that exists)
+  s.h = static_cast<int>((s.at - found_before) / s.t.pages);
+  s.unit0 = found_before + static_cast<int64_t>(s.h) * s.t.pages;
+  return s;
+}
+
+// mbar_wait with the rare part out of line.
+static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return mbar_wait(bar, parity, status);
+}
+__device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, status);
 }
 
 // Many query columns (tiles of 128) on the tensor-memory MMAs: kv8_rows.cu.
