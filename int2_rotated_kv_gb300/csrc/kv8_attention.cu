@@ -463,7 +463,7 @@ __device__ __forceinline__ void issue_tail(const Kv8Params& p, const Entry& t, i
 template <typename C>
 __device__ __forceinline__ bool copied(const Kv8Params& p, Ring& r, int& s) {
   s = r.n_out % C::kStages;
-  const bool got = wait_copy(r.bars + s, (r.n_out / C::kStages) & 1, p.status);
+  const bool got = mbar_wait(r.bars + s, (r.n_out / C::kStages) & 1, p.status);
   ++r.n_out;
   if (__all_sync(0xffffffffu, got)) return true;
   for (; r.n_out < r.n_in; ++r.n_out)

@@ -368,6 +368,28 @@ __device__ __forceinline__ float rows_exp2(float x) {
   return y;
 }
 
+// Two fp32 values in one operand, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The largest exponent s_K fac S + log2 s_V of a thread's row over a tile's visible tokens.
 // Two pages' 32 columns at a time, the next two pages' on their way.
 template <bool kMasked>
@@ -382,11 +404,10 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = !kMasked || k < seen ? __uint_as_float(s[16 * j + k]) : -INFINITY;
 #pragma unroll
-      for (int n = 8; n > 0; n /= 2)
-#pragma unroll
-        for (int k = 0; k < n; ++k) x[k] = fmaxf(x[k], x[k + n]);
+      for (int k = 0; k < 5; ++k) x[k] = max3(x[k], x[k + 5], x[k + 10]);
+      const float top = fmaxf(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[15]));
       // (a hidden page's -inf times a scale of 0 would be NaN)
-      big = fmaxf(big, kMasked && x[0] == -INFINITY ? x[0] : fmaf(x[0], pm.x * fac, pm.y));
+      big = fmaxf(big, kMasked && top == -INFINITY ? top : fmaf(top, pm.x * fac, pm.y));
     }
   };
   uint32_t a[32], b[32];
@@ -415,22 +436,23 @@ __device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, flo
     for (int j = 0; j < 2; ++j) {
       const float4 pm = mt[j0 + j];
       const float f = pm.x * fac, off = pm.y - m;
+      const uint64_t f2 = two(f, f), off2 = two(off, off);
       const int seen = vis - __float_as_int(pm.w);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2];
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
-        float x0 = rows_exp2(fmaf(__uint_as_float(s[16 * j + k]), f, off));
-        float x1 = rows_exp2(fmaf(__uint_as_float(s[16 * j + k + 1]), f, off));
+        const uint64_t e = fma2(two(__uint_as_float(s[16 * j + k]), __uint_as_float(s[16 * j + k + 1])), f2, off2);
+        float x0 = rows_exp2(first(e)), x1 = rows_exp2(second(e));
         if constexpr (kMasked) {
           x0 = k < seen ? x0 : 0.f;
           x1 = k + 1 < seen ? x1 : 0.f;
         }
-        sum[k & 2] += x0;
-        sum[(k & 2) + 1] += x1;
+        const uint64_t x = two(x0, x1);
+        sum[(k >> 1) & 1] = k < 4 ? x : add2(sum[(k >> 1) & 1], x);
         out[8 * j + k / 2] = pack_half2(x0, x1);
       }
-      const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (!kMasked || seen > 0) l = fmaf(all, pm.z, l);
+      const uint64_t all = add2(sum[0], sum[1]);
+      if (!kMasked || seen > 0) l = fmaf(first(all) + second(all), pm.z, l);
     }
     tc_st16(ts + 8 * j0, out);
   };
