@@ -17,8 +17,8 @@
 //                 twice, for the maximum and for w, which overwrites S;
 //   8-11, 12-15   pages -> fp16 K tiles and V tiles, 128-byte swizzled, two of each, and
 //                 the queries of a unit.  A warp has two pages of every tile;
-//                 each lane copies (cp.async) the chunks that it will convert itself, three
-//                 pages ahead, so nothing is waited for but its own copies.  (As bulk
+//                 each lane copies (cp.async) chunks of its warp's pages, three
+//                 pages ahead, so nothing is waited for but the warp's own copies.  (As bulk
 //                 copies of 2 KB, 24 a tile, the copies alone took 3400 cycles a tile.)
 //   16, 17        MMAs of a stream, from one lane each.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
@@ -160,28 +160,33 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(kLeft) : "memory");
 }
 
-// A lane's chunk c of a page's key codes: 16 channels from 64 (c / 2) + 16 (lane / 8) of token
-// lane % 8 + 8 (c % 2), so that the eight lanes of a store phase, in eight rows, meet all
-// the banks of the swizzled tile.
-__device__ __forceinline__ int key_chunk_of(int lane, int c) {
-  return kv8_key_chunk((lane & 7) + 8 * (c & 1), 4 * (c >> 1) + (lane >> 3));
-}
-
-// Its place in the page's 16 rows; half: 8 channels of it.
+// A lane's chunk c of a page's key codes is chunk 32 c + lane (a copy of 16 bytes a lane reads
+// 512 in a row; permuted copies cost the 65-row case 5 us): token 2 (lane / 4) + c % 2, channels
+// 16 (lane % 4) + 64 (c / 2) and on.  Its place in the page's 16 rows of the swizzled tile;
+// half: 8 channels of it.  Every other four lanes store their halves in the other order, so that
+// the eight of a store phase, in two rows, meet all the banks.
 __device__ __forceinline__ uint32_t key_place(int lane, int c, int half) {
-  return (c >> 1) * (kRTile * 128) + 1024 * (c & 1) + 128 * (lane & 7) +
-         16 * ((2 * (lane >> 3) + half) ^ (lane & 7));
+  const int t = 2 * (lane >> 2) + (c & 1);
+  return (c >> 1) * (kRTile * 128) + 128 * t + 16 * ((2 * (lane & 3) + half) ^ (t & 7));
 }
+__device__ __forceinline__ int key_half(int lane, int part) { return part ^ ((lane >> 2) & 1); }
 
 template <bool kE4m3>
 __device__ __forceinline__ void store_keys(uint8_t* dst, int c, int lane, uint4 x) {
+  const bool turn = key_half(lane, 0);
   uint32_t o[8];
-  code_pairs<kE4m3>(x.x, o[0], o[1]);
-  code_pairs<kE4m3>(x.y, o[2], o[3]);
-  code_pairs<kE4m3>(x.z, o[4], o[5]);
-  code_pairs<kE4m3>(x.w, o[6], o[7]);
-  *reinterpret_cast<uint4*>(dst + key_place(lane, c, 0)) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(dst + key_place(lane, c, 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+  code_pairs<kE4m3>(turn ? x.z : x.x, o[0], o[1]);
+  code_pairs<kE4m3>(turn ? x.w : x.y, o[2], o[3]);
+  code_pairs<kE4m3>(turn ? x.x : x.z, o[4], o[5]);
+  code_pairs<kE4m3>(turn ? x.y : x.w, o[6], o[7]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, key_half(lane, 0))) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, key_half(lane, 1))) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Where chunk 32 c + lane of a page's value codes is kept, so that the two chunks of a lane's
+// square (below) are at 64 c + lane and 64 c + 32 + (lane ^ 4): copies and reads meet all banks.
+__device__ __forceinline__ int value_ring(int lane, int c) {
+  return 64 * (c >> 1) + 32 * (lane & 1) + ((16 * (c & 1) + (lane >> 1)) ^ (4 * (lane & 1)));
 }
 
 // Two neighbouring chunks of value codes (pair 32 c + lane of a page: 4 channels x 8 tokens)
@@ -278,7 +283,7 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
   for (int c = 0; c < D / 32; ++c) {
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {
-      const uint4 x = reinterpret_cast<const uint4*>(area)[2 * key_chunk_of(lane, c) + part];
+      const uint4 x = reinterpret_cast<const uint4*>(area)[2 * (32 * c + lane) + part];
       *reinterpret_cast<uint4*>(dst + key_place(lane, c, part)) =
           make_uint4(half_pair(x.x, mul), half_pair(x.y, mul), half_pair(x.z, mul), half_pair(x.w, mul));
     }
@@ -605,12 +610,12 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         if (k < 2 * u.tiles) {
           if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
           const int64_t block = ids.block(p, u, k / 2, w + 4 * (k & 1));
-          const uint8_t* src = p.pool + block * F::kBlock + F::kCodes + 32 * lane;
-          uint8_t* to = raw + at * S::kPage16 + 16 * lane;
+          const uint8_t* src = p.pool + block * F::kBlock + F::kCodes + 16 * lane;
+          uint8_t* to = raw + at * S::kPage16;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            if (block >= 0) copy16(to + 512 * c, src + 1024 * (c >> 1) + 16 * (c & 1));
-            else *reinterpret_cast<uint4*>(to + 512 * c) = make_uint4(0, 0, 0, 0);
+            if (block >= 0) copy16(to + 16 * value_ring(lane, c), src + 512 * c);
+            else *reinterpret_cast<uint4*>(to + 16 * value_ring(lane, c)) = make_uint4(0, 0, 0, 0);
         }
         copies_commit();
       };
@@ -626,19 +631,25 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         const uint32_t buf = g & 1;
         int n, tail_slot;
         u.slots(i, n, tail_slot);
-        if (!(ok = wait(&bar->vempty[buf], (g >> 1) + 1))) break;
         uint8_t* dst = smem + S::kV + buf * S::kTile16;
         const int next = at == kRAhead - 1 ? 0 : at + 1;
         copies_wait<kRAhead - 2>();
-        const uint4* page0 = reinterpret_cast<const uint4*>(raw + at * S::kPage16) + lane;
-        const uint4* page1 = reinterpret_cast<const uint4*>(raw + next * S::kPage16) + lane;
-        if (w != tail_slot && w + 4 != tail_slot) {   // both pages' codes in flight together
-          uint4 x[2][D / 32];
+        __syncwarp();   // all lanes' copies
+        const uint4* page0 = reinterpret_cast<const uint4*>(raw + at * S::kPage16);
+        const uint4* page1 = reinterpret_cast<const uint4*>(raw + next * S::kPage16);
+        uint4 x[2][D / 32];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            x[0][c] = page0[32 * c];
-            x[1][c] = page1[32 * c];
-          }
+        for (int c = 0; c < D / 32; ++c) {
+          x[0][c] = page0[32 * c + (lane ^ (4 * (c & 1)))];
+          x[1][c] = page1[32 * c + (lane ^ (4 * (c & 1)))];
+        }
+        __syncwarp();
+        // the pages after the next, into the places just read (none in a tile with a tail)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
+        at = next == kRAhead - 1 ? 0 : next + 1;
+        if (!(ok = wait(&bar->vempty[buf], (g >> 1) + 1))) break;
+        if (w != tail_slot && w + 4 != tail_slot) {
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -658,14 +669,11 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
               uint32_t o[4][4];
-              value_square<kE4m3>(mine[64 * c], mine[64 * c + 32], o);
+              value_square<kE4m3>(mine[64 * c + lane], mine[64 * c + 32 + (lane ^ 4)], o);
               store_square<D>(dst + half * (D * 128), c, w, lane, o);
             }
           }
         }
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
-        at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->vfull[buf]);
       }
@@ -696,7 +704,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           if (lane == (k & 1) && block >= 0) copy16(to + F::kCodes, src + F::kScales);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            if (block >= 0) copy16(to + 512 * c + 16 * lane, src + 16 * key_chunk_of(lane, c));
+            if (block >= 0) copy16(to + 512 * c + 16 * lane, src + 512 * c + 16 * lane);
             else *reinterpret_cast<uint4*>(to + 512 * c + 16 * lane) = make_uint4(0, 0, 0, 0);
         }
         copies_commit();
@@ -714,15 +722,15 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         const uint32_t buf = g & 1;
         int n, tail_slot;
         u.slots(i, n, tail_slot);
-        if (!(ok = wait(&bar->kempty[buf], (g >> 1) + 1))) break;
         uint8_t* dst = smem + S::kK + buf * S::kTile16 + 2048 * w;
         const int next = at == kRAhead - 1 ? 0 : at + 1;
         copies_wait<kRAhead - 2>();
         const uint8_t* page0 = raw + at * S::kPage16;
         const uint8_t* page1 = raw + next * S::kPage16;
-        if (lane < 2 && 4 * lane + w != tail_slot) {   // what the softmax needs of the two pages
-          const int slot = 4 * lane + w;
-          float4 m = make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
+        // what the softmax needs of the two pages
+        const int slot = 4 * (lane & 1) + w;
+        float4 m = make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
+        if (lane < 2) {
           if ((shown >> ((2 * i + lane) & 3)) & 1) {
             const float2 sc = *reinterpret_cast<const float2*>((lane ? page1 : page0) + F::kCodes);
             // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
@@ -730,17 +738,22 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             m = make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
                             __int_as_float((u.p0 + 8 * i + slot) * kPage));
           }
-          meta[(g & 3) * 8 + slot] = m;
         }
         const uint4* mine0 = reinterpret_cast<const uint4*>(page0) + lane;
         const uint4* mine1 = reinterpret_cast<const uint4*>(page1) + lane;
-        if (w != tail_slot && w + 4 != tail_slot) {   // both pages' codes in flight together
-          uint4 x[2][D / 32];
+        uint4 x[2][D / 32];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            x[0][c] = mine0[32 * c];
-            x[1][c] = mine1[32 * c];
-          }
+        for (int c = 0; c < D / 32; ++c) {
+          x[0][c] = mine0[32 * c];
+          x[1][c] = mine1[32 * c];
+        }
+        // the pages after the next, into the places just read (none in a tile with a tail)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
+        at = next == kRAhead - 1 ? 0 : next + 1;
+        if (!(ok = wait(&bar->kempty[buf], (g >> 1) + 1))) break;
+        if (lane < 2 && slot != tail_slot) meta[(g & 3) * 8 + slot] = m;
+        if (w != tail_slot && w + 4 != tail_slot) {
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -758,9 +771,6 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
               store_keys<kE4m3>(dst + 8192 * half, c, lane, (half ? mine1 : mine0)[32 * c]);
           }
         }
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
-        at = next == kRAhead - 1 ? 0 : next + 1;
         fence_proxy_async();
         arrive(&bar->kfull[buf]);
       }
