@@ -16,10 +16,10 @@
 //                 tensor memory, own maxima and sums, merged at the unit's end): reads S
 //                 twice, for the maximum and for w, which overwrites S;
 //   8-11, 12-15   pages -> fp16 K tiles and V tiles, 128-byte swizzled, two of each, and
-//                 the queries of a unit.  A warp has two pages of every tile;
-//                 each lane copies (cp.async) chunks of its warp's pages, three
-//                 pages ahead, so nothing is waited for but the warp's own copies.  (As bulk
-//                 copies of 2 KB, 24 a tile, the copies alone took 3400 cycles a tile.)
+//                 the queries of a unit.  A warp has two pages of every tile, whose codes it
+//                 holds in registers from one tile to the next.  (As bulk copies of 2 KB, 24 a
+//                 tile, the copies alone took 3400 cycles a tile; by cp.async the 65-row case
+//                 takes 121 us.)
 //   16, 17        MMAs of a stream, from one lane each.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (d each); w in the first half of S.
@@ -33,7 +33,6 @@
 namespace oscar {
 
 constexpr int kRWarps = 18;
-constexpr int kRAhead = 3;         // pages that a converting warp has on their way
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRTile = 128;        // tokens of a tile
 constexpr int kRHidden = 0x7fff0000;   // position of a page slot that holds no page
@@ -45,9 +44,7 @@ struct RowsSmem {
   static constexpr int kK = 0;
   static constexpr int kV = 2 * kTile16;
   static constexpr int kQ = 4 * kTile16;
-  static constexpr int kPage16 = F::kCodes + 16;           // codes of a page, and its scales
-  static constexpr int kRaw = 5 * kTile16;                 // [8 warps][kRAhead] of them
-  static constexpr int kMeta = kRaw + 8 * kRAhead * kPage16;   // float4 [4][8]: s_K, log2 s_V, 1/s_V, position
+  static constexpr int kMeta = 5 * kTile16;                  // float4 [4][8]: s_K, log2 s_V, 1/s_V, position
   static constexpr int kFac = kMeta + 512;                 // float [2][128]
   static constexpr int kMl = kFac + 1024;                  // float2 [2][2][128]
   static constexpr int kBad = kMl + 4096;                  // int [4]: tails that are not finite
@@ -103,20 +100,17 @@ struct Walk {
     u.set();
     return u;
   }
-  // Page slots of tile i: pages in slots 0 .. n - 1, the tail in slot `tail_slot` (-1: none).
-  __device__ __forceinline__ void slots(int i, int& n, int& tail_slot) const {
-    n = max(0, min(8, n8 - 8 * i));
-    tail_slot = tail && i == tiles - 1 ? n : -1;
-  }
+  // The tail's page slot in tile i; -1: none.
+  __device__ __forceinline__ int tail_slot(int i) const { return tail && i == tiles - 1 ? n8 - 8 * i : -1; }
 };
 
-// Page ids of a unit as a warp holds them: four tiles' (32 pages), a lane each, and the next
-// four's on their way.
-struct PageIds {
+// Blocks of a unit's pages as a warp holds them: four tiles' (32 pages), a lane each, and the
+// next four's page ids on their way.
+struct PageBlocks {
   const int32_t* row;
-  int now, ahead;
+  int now, ahead;   // -1: no page, or (in `now`) an id out of range
 
-  __device__ __forceinline__ PageIds(const Kv8Params& p, const Walk& u, int lane) {
+  __device__ __forceinline__ PageBlocks(const Kv8Params& p, const Walk& u, int lane) {
     row = p.page_table + static_cast<size_t>(u.t.b) * p.max_pages + u.p0;
     now = -1;
     ahead = lane < u.n8 ? row[lane] : -1;
@@ -124,18 +118,27 @@ struct PageIds {
   // to be called for every tile in order
   __device__ __forceinline__ void tile(const Kv8Params& p, const Walk& u, int i, int lane) {
     if (i % 4) return;
-    now = ahead;
+    const bool ok = ahead >= 0 && ahead < p.n_pages;
+    if (!ok && 8 * i + lane < u.n8 && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+    now = ok ? ahead * p.hkv + u.h : -1;   // (2^31 blocks are more than a cache can have)
     const int pg = 8 * i + 32 + lane;
     ahead = pg < u.n8 ? row[pg] : -1;
   }
-  // block of the page in `slot` of tile i; -1: no page, or an id out of range
-  __device__ __forceinline__ int64_t block(const Kv8Params& p, const Walk& u, int i, int slot) const {
-    const int id = __shfl_sync(0xffffffffu, now, (8 * i + slot) & 31);
-    return 8 * i + slot < u.n8 && id >= 0 && id < p.n_pages ? static_cast<int64_t>(id) * p.hkv + u.h : -1;
+  __device__ __forceinline__ int block(int i, int slot) const {
+    return __shfl_sync(0xffffffffu, now, (8 * i + slot) & 31);
   }
 };
 
-// Sixteen codes as fp16 pairs in order, exact.
+// 16 bytes; volatile: where it stands, well ahead of its use.
+__device__ __forceinline__ uint4 load16(const uint8_t* src) {
+  uint4 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src));
+  return x;
+}
+
+// Four codes as fp16 pairs in order, exact.
 template <bool kE4m3>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
   if constexpr (kE4m3) {
@@ -150,72 +153,47 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& a, uint32_t& b)
   }
 }
 
-// Asynchronous copies of 16 bytes into shared memory, in groups.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(kLeft) : "memory");
-}
-
-// A lane's chunk c of a page's key codes is chunk 32 c + lane (a copy of 16 bytes a lane reads
-// 512 in a row; permuted copies cost the 65-row case 5 us): token 2 (lane / 4) + c % 2, channels
-// 16 (lane % 4) + 64 (c / 2) and on.  Its place in the page's 16 rows of the swizzled tile;
-// half: 8 channels of it.  Every other four lanes store their halves in the other order, so that
-// the eight of a store phase, in two rows, meet all the banks.
+// A lane's chunk c of a page's key codes is chunk 32 c + lane (a load of 16 bytes a lane reads
+// 512 in a row): token 2 (lane / 4) + c % 2, channels 16 (lane % 4) + 64 (c / 2) and on.  Its
+// place in the page's 16 rows of the swizzled tile; half: 8 channels of it.  Every other four
+// lanes store their halves in the other order, so that the eight of a store phase, in two
+// rows, meet all the banks.
 __device__ __forceinline__ uint32_t key_place(int lane, int c, int half) {
   const int t = 2 * (lane >> 2) + (c & 1);
   return (c >> 1) * (kRTile * 128) + 128 * t + 16 * ((2 * (lane & 3) + half) ^ (t & 7));
 }
-__device__ __forceinline__ int key_half(int lane, int part) { return part ^ ((lane >> 2) & 1); }
 
 template <bool kE4m3>
 __device__ __forceinline__ void store_keys(uint8_t* dst, int c, int lane, uint4 x) {
-  const bool turn = key_half(lane, 0);
+  const int turn = (lane >> 2) & 1;
   uint32_t o[8];
   code_pairs<kE4m3>(turn ? x.z : x.x, o[0], o[1]);
   code_pairs<kE4m3>(turn ? x.w : x.y, o[2], o[3]);
   code_pairs<kE4m3>(turn ? x.x : x.z, o[4], o[5]);
   code_pairs<kE4m3>(turn ? x.y : x.w, o[6], o[7]);
-  *reinterpret_cast<uint4*>(dst + key_place(lane, c, key_half(lane, 0))) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(dst + key_place(lane, c, key_half(lane, 1))) = make_uint4(o[4], o[5], o[6], o[7]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, turn)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(dst + key_place(lane, c, turn ^ 1)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Where chunk 32 c + lane of a page's value codes is kept, so that the two chunks of a lane's
-// square (below) are at 64 c + lane and 64 c + 32 + (lane ^ 4): copies and reads meet all banks.
-__device__ __forceinline__ int value_ring(int lane, int c) {
-  return 64 * (c >> 1) + 32 * (lane & 1) + ((16 * (c & 1) + (lane >> 1)) ^ (4 * (lane & 1)));
+// Its chunk c of value codes: channels 32 c + 4 (lane / 4) and on, tokens 4 (lane % 4) and on.
+// Where four tokens of the channel that it stores k-th lie, as fp16, in a 64-token atom's rows
+// (channels), page slot w of four.  Every other pair of channel groups stores its channels in
+// the order 2, 3, 0, 1, for the banks as above.
+__device__ __forceinline__ int value_channel(int lane, int k) { return k ^ ((lane >> 2) & 2); }
+__device__ __forceinline__ uint32_t value_place(int lane, int c, int w, int k) {
+  const int ch = 4 * (lane >> 2) + value_channel(lane, k), tg = lane & 3;
+  return (32 * c + ch) * 128 + 16 * ((2 * w + (tg >> 1)) ^ (ch & 7)) + 8 * (tg & 1);
 }
 
-// Two neighbouring chunks of value codes (pair 32 c + lane of a page: 4 channels x 8 tokens)
-// as fp16: channel x pairs of tokens.
 template <bool kE4m3>
-__device__ __forceinline__ void value_square(uint4 x, uint4 y, uint32_t (&o)[4][4]) {
-  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+__device__ __forceinline__ void store_values(uint8_t* dst, int c, int w, int lane, uint4 x) {
+  const bool turn = value_channel(lane, 0);
+  const uint32_t in[4] = {turn ? x.z : x.x, turn ? x.w : x.y, turn ? x.x : x.z, turn ? x.y : x.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    code_pairs<kE4m3>(a[k], o[k][0], o[k][1]);
-    code_pairs<kE4m3>(b[k], o[k][2], o[k][3]);
-  }
-}
-
-// The square into the rows (channels) of a 64-token atom at `dst`, page slot w of four.
-// Every other pair of channel groups stores its channels in the order 2, 3, 0, 1, for the
-// banks as above.
-template <int D>
-__device__ __forceinline__ void store_square(uint8_t* dst, int c, int w, int lane, const uint32_t (&o)[4][4]) {
-  const int cg = lane >> 1, tg = lane & 1;
-  const bool turn = (cg >> 1) & 1;
-  uint8_t* to = dst + (64 * c + 4 * cg) * 128;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int at = turn ? k ^ 2 : k;
-    const uint32_t chunk = static_cast<uint32_t>((2 * w + tg) ^ (4 * (cg & 1) + at));
-    *reinterpret_cast<uint4*>(to + at * 128 + 16 * chunk) =
-        make_uint4(turn ? o[k ^ 2][0] : o[k][0], turn ? o[k ^ 2][1] : o[k][1],
-                   turn ? o[k ^ 2][2] : o[k][2], turn ? o[k ^ 2][3] : o[k][3]);
+    uint2 o;
+    code_pairs<kE4m3>(in[k], o.x, o.y);
+    *reinterpret_cast<uint2*>(dst + value_place(lane, c, w, k)) = o;
   }
 }
 
@@ -282,9 +260,9 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
 #pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-      const uint4 x = reinterpret_cast<const uint4*>(area)[2 * (32 * c + lane) + part];
-      *reinterpret_cast<uint4*>(dst + key_place(lane, c, part)) =
+    for (int half = 0; half < 2; ++half) {
+      const uint4 x = reinterpret_cast<const uint4*>(area)[2 * (32 * c + lane) + half];
+      *reinterpret_cast<uint4*>(dst + key_place(lane, c, half)) =
           make_uint4(half_pair(x.x, mul), half_pair(x.y, mul), half_pair(x.z, mul), half_pair(x.w, mul));
     }
   }
@@ -306,23 +284,19 @@ __device__ __noinline__ void tail_values(const Kv8Params& p, int b, int h, int l
   const int n = len % kPage;
   const float mul = power_of_two(scale_up(tail_magnitude<D>(area, 1, n, lane, odd)));
 #pragma unroll 1
-  for (int c = 0; c < D / 64; ++c) {
-    uint32_t o[4][4];   // channel x pairs of tokens
+  for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const uint16_t* four = area + 16 * (32 * c + lane) + 4 * value_channel(lane, k);
+      uint2 x = *reinterpret_cast<const uint2*>(four);
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const uint4 x = reinterpret_cast<const uint4*>(area)[4 * (32 * c + lane) + 2 * part];
-      const uint4 y = reinterpret_cast<const uint4*>(area)[4 * (32 * c + lane) + 2 * part + 1];
-      const uint32_t a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int t0 = 8 * (lane & 1) + 4 * part + 2 * (k & 1);
-        uint32_t v = a[k];
-        if (t0 >= n || (v & 0x7fffu) >= 0x7f80u) v &= 0xffff0000u;
-        if (t0 + 1 >= n || ((v >> 16) & 0x7fffu) >= 0x7f80u) v &= 0xffffu;
-        o[k >> 1][2 * part + (k & 1)] = half_pair(v, mul);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t& v = j < 2 ? x.x : x.y;
+        const uint32_t mask = j & 1 ? 0xffff0000u : 0xffffu;
+        if (4 * (lane & 3) + j >= n || (v & mask & 0x7fff7fffu) >= (0x7f807f80u & mask)) v &= ~mask;
       }
+      *reinterpret_cast<uint2*>(dst + value_place(lane, c, w, k)) = make_uint2(half_pair(x.x, mul), half_pair(x.y, mul));
     }
-    store_square<D>(dst, c, w, lane, o);
   }
 }
 
@@ -600,181 +574,108 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   } else if (any && warp >= 12 && warp < 16) {
     // ---------------------------------------------------- values as fp16 operands
     const int w = warp - 12;   // page slots w and w + 4 of every tile
-    uint8_t* raw = smem + S::kRaw + (4 + w) * kRAhead * S::kPage16;
     uint32_t g = 0, seg = 0;
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
-      PageIds ids(p, u, lane);
-      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2) into ring place `at`
-      auto request = [&](int k, int at) {
-        if (k < 2 * u.tiles) {
-          if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
-          const int64_t block = ids.block(p, u, k / 2, w + 4 * (k & 1));
-          const uint8_t* src = p.pool + block * F::kBlock + F::kCodes + 16 * lane;
-          uint8_t* to = raw + at * S::kPage16;
+      PageBlocks blocks(p, u, lane);
+      uint4 x[2][D / 32];
+      // the codes of this warp's pages of tile i
+      auto request = [&](int i) {
+        blocks.tile(p, u, i, lane);
+        const int b[2] = {blocks.block(i, w), blocks.block(i, w + 4)};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            if (block >= 0) copy16(to + 16 * value_ring(lane, c), src + 512 * c);
-            else *reinterpret_cast<uint4*>(to + 16 * value_ring(lane, c)) = make_uint4(0, 0, 0, 0);
+        for (int half = 0; half < 2; ++half) {
+          const uint8_t* src = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + F::kCodes + 16 * lane;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
         }
-        copies_commit();
       };
-#pragma unroll 1
-      for (int k = 0; k < kRAhead; ++k) request(k, k);
+      request(0);
       if (!wait(&bar->qempty, seg + 1)) break;
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
       load_queries<D>(p, u.t.b, u.h, u.t.tile, 4 + w, lane, smem + S::kQ, facs + (seg & 1) * 128);
       fence_proxy_async();
       arrive(&bar->qfull[seg & 1]);
-      int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
-        int n, tail_slot;
-        u.slots(i, n, tail_slot);
         uint8_t* dst = smem + S::kV + buf * S::kTile16;
-        const int next = at == kRAhead - 1 ? 0 : at + 1;
-        copies_wait<kRAhead - 2>();
-        __syncwarp();   // all lanes' copies
-        const uint4* page0 = reinterpret_cast<const uint4*>(raw + at * S::kPage16);
-        const uint4* page1 = reinterpret_cast<const uint4*>(raw + next * S::kPage16);
-        uint4 x[2][D / 32];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          x[0][c] = page0[32 * c + (lane ^ (4 * (c & 1)))];
-          x[1][c] = page1[32 * c + (lane ^ (4 * (c & 1)))];
-        }
-        __syncwarp();
-        // the pages after the next, into the places just read (none in a tile with a tail)
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
-        at = next == kRAhead - 1 ? 0 : next + 1;
         if (!(ok = wait(&bar->vempty[buf], (g >> 1) + 1))) break;
-        if (w != tail_slot && w + 4 != tail_slot) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t o[4][4];
-              value_square<kE4m3>(x[half][2 * c], x[half][2 * c + 1], o);
-              store_square<D>(dst + half * (D * 128), c, w, lane, o);
-            }
-        } else {
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (4 * half + w == tail_slot) {
-              tail_values<D>(p, u.t.b, u.h, u.t.len, dst + half * (D * 128), w, lane);
-              continue;
-            }
-            const uint4* mine = half ? page1 : page0;
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t o[4][4];
-              value_square<kE4m3>(mine[64 * c + lane], mine[64 * c + 32 + (lane ^ 4)], o);
-              store_square<D>(dst + half * (D * 128), c, w, lane, o);
-            }
-          }
+          for (int c = 0; c < D / 32; ++c) store_values<kE4m3>(dst + half * (D * 128), c, w, lane, x[half][c]);
+        const int slot = u.tail_slot(i);
+        if (i + 1 < u.tiles) {
+          request(i + 1);
+        } else if (slot >= 0 && (slot & 3) == w) {   // over the zeros that stood for it
+          __syncwarp();
+          tail_values<D>(p, u.t.b, u.h, u.t.len, dst + (slot >> 2) * (D * 128), w, lane);
         }
         fence_proxy_async();
         arrive(&bar->vfull[buf]);
       }
-      copies_wait<0>();
       ++seg;
     }
   } else if (any && warp >= 8 && warp < 12) {
     // ------------------------------------------- queries and keys as fp16 operands
     const int w = warp - 8;   // page slots w and w + 4 of every tile
-    uint8_t* raw = smem + S::kRaw + w * kRAhead * S::kPage16;
     uint32_t g = 0, seg = 0;
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
-      PageIds ids(p, u, lane);
-      uint32_t shown = 0;   // bit k % 4: page k is one
-      // this warp's page k of the unit (slot w + 4 (k % 2) of tile k / 2) into ring place `at`
-      auto request = [&](int k, int at) {
-        if (k < 2 * u.tiles) {
-          if (k % 2 == 0) ids.tile(p, u, k / 2, lane);
-          const int slot = w + 4 * (k & 1);
-          const int64_t block = ids.block(p, u, k / 2, slot);
-          if (block < 0 && lane == 0 && 8 * (k / 2) + slot < u.n8 && p.status)
-            atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-          shown = (shown & ~(1u << (k & 3))) | ((block >= 0 ? 1u : 0u) << (k & 3));
-          const uint8_t* src = p.pool + block * F::kBlock;
-          uint8_t* to = raw + at * S::kPage16;
-          // the scales by the lane that will read them
-          if (lane == (k & 1) && block >= 0) copy16(to + F::kCodes, src + F::kScales);
+      PageBlocks blocks(p, u, lane);
+      uint4 x[2][D / 32];
+      float2 sc;      // lanes 0 and 1: scales of the two pages
+      bool shown;     // and whether there is one
+      // codes and scales of this warp's pages of tile i
+      auto request = [&](int i) {
+        blocks.tile(p, u, i, lane);
+        const int b[2] = {blocks.block(i, w), blocks.block(i, w + 4)};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            if (block >= 0) copy16(to + 512 * c + 16 * lane, src + 512 * c + 16 * lane);
-            else *reinterpret_cast<uint4*>(to + 512 * c + 16 * lane) = make_uint4(0, 0, 0, 0);
+        for (int half = 0; half < 2; ++half) {
+          const uint8_t* src = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + 16 * lane;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
         }
-        copies_commit();
+        const int mine = lane ? b[1] : b[0];
+        shown = mine >= 0;
+        if (lane < 2 && shown)
+          sc = __ldg(reinterpret_cast<const float2*>(p.pool + static_cast<int64_t>(mine) * F::kBlock + F::kScales));
       };
-#pragma unroll 1
-      for (int k = 0; k < kRAhead; ++k) request(k, k);
+      request(0);
       if (!wait(&bar->qempty, seg + 1)) break;
       // and the unit before the last has been read (what is kept by unit comes round again)
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
       load_queries<D>(p, u.t.b, u.h, u.t.tile, w, lane, smem + S::kQ, facs + (seg & 1) * 128);
       fence_proxy_async();
       arrive(&bar->qfull[seg & 1]);
-      int at = 0;   // ring place of the tile's first page
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
-        int n, tail_slot;
-        u.slots(i, n, tail_slot);
         uint8_t* dst = smem + S::kK + buf * S::kTile16 + 2048 * w;
-        const int next = at == kRAhead - 1 ? 0 : at + 1;
-        copies_wait<kRAhead - 2>();
-        const uint8_t* page0 = raw + at * S::kPage16;
-        const uint8_t* page1 = raw + next * S::kPage16;
-        // what the softmax needs of the two pages
-        const int slot = 4 * (lane & 1) + w;
-        float4 m = make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
-        if (lane < 2) {
-          if ((shown >> ((2 * i + lane) & 3)) & 1) {
-            const float2 sc = *reinterpret_cast<const float2*>((lane ? page1 : page0) + F::kCodes);
-            // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
-            const bool live = sc.y > 0.f;
-            m = make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
-                            __int_as_float((u.p0 + 8 * i + slot) * kPage));
-          }
-        }
-        const uint4* mine0 = reinterpret_cast<const uint4*>(page0) + lane;
-        const uint4* mine1 = reinterpret_cast<const uint4*>(page1) + lane;
-        uint4 x[2][D / 32];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          x[0][c] = mine0[32 * c];
-          x[1][c] = mine1[32 * c];
-        }
-        // the pages after the next, into the places just read (none in a tile with a tail)
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) request(2 * i + kRAhead + k, k ? next : at);
-        at = next == kRAhead - 1 ? 0 : next + 1;
         if (!(ok = wait(&bar->kempty[buf], (g >> 1) + 1))) break;
-        if (lane < 2 && slot != tail_slot) meta[(g & 3) * 8 + slot] = m;
-        if (w != tail_slot && w + 4 != tail_slot) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
-        } else {
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (4 * half + w == tail_slot) {
-              const float4 m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * half, lane, bad_tail + (seg & 3));
-              if (lane == 0) meta[(g & 3) * 8 + 4 * half + w] = m;
-              continue;
-            }
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c)
-              store_keys<kE4m3>(dst + 8192 * half, c, lane, (half ? mine1 : mine0)[32 * c]);
-          }
+          for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
+        if (lane < 2) {   // what the softmax needs of the two pages
+          const int slot = 4 * lane + w;
+          // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
+          const bool live = sc.y > 0.f;
+          meta[(g & 3) * 8 + slot] =
+              shown ? make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
+                                  __int_as_float((u.p0 + 8 * i + slot) * kPage))
+                    : make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
+        }
+        const int slot = u.tail_slot(i);
+        if (i + 1 < u.tiles) {
+          request(i + 1);
+        } else if (slot >= 0 && (slot & 3) == w) {   // over the zeros that stood for it
+          __syncwarp();
+          const float4 m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * (slot >> 2), lane, bad_tail + (seg & 3));
+          if (lane == 0) meta[(g & 3) * 8 + slot] = m;
         }
         fence_proxy_async();
         arrive(&bar->kfull[buf]);
       }
-      copies_wait<0>();
       ++seg;
     }
   } else if (any && warp < 8) {
