@@ -765,8 +765,9 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 
 // Merges the units that lie in several CTAs.  Block: (CTA in which the unit starts, columns);
 // kSplit warps share the parts of a column, a lane has D / 32 channels.
-template <int D, int NT, int kSplit>
+template <int D, int NT>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int kSplit = 4;   // warps of a column: few columns, with many parts each
   constexpr int kSlot = kv8_slot<D, NT>(), kPer = D / 32;
   __shared__ float partial[8][D];
   pdl_wait();
@@ -813,16 +814,14 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   }
-  if constexpr (kSplit > 1) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) partial[warp][kPer * lane + k] = acc[k];
-    __syncthreads();
-    if (sub != 0) return;
+  for (int k = 0; k < kPer; ++k) partial[warp][kPer * lane + k] = acc[k];
+  __syncthreads();
+  if (sub != 0) return;
 #pragma unroll
-    for (int s = 1; s < kSplit; ++s)
+  for (int s = 1; s < kSplit; ++s)
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
-  }
+    for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
   if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int row = gcol / p.G, g = gcol - row * p.G;
@@ -830,6 +829,56 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
       p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + kPer * lane);
 #pragma unroll
   for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf162(acc[k] * inv, acc[k + 1] * inv);
+}
+
+// The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns
+// each: a lane per column, a warp per 16 channels.
+template <int D>
+__global__ void __launch_bounds__(2 * D) kv8_merge_rows_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int kSlot = kv8_slot<D, kRowsNT>();
+  pdl_wait();
+  pdl_trigger();
+  const int4 own = p.info[blockIdx.x];
+  const int n = own.z;
+  if (n == 0) return;
+  const int ch = 16 * (threadIdx.x >> 5), col = 32 * blockIdx.y + (threadIdx.x & 31);
+  const int b = own.x / p.tiles, tile = own.x - b * p.tiles, gcol = tile * 128 + col;
+  if (gcol >= p.cols) return;
+  // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
+  auto slot = [&](int j) {
+    return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
+  };
+  auto stats = [&](int j) { return *reinterpret_cast<const float2*>(slot(j) + 128 * D + 2 * col); };
+  float top = kLowest;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) top = fmaxf(top, stats(j).x);
+  float acc[16] = {};
+  float l = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float2 ml = stats(j);
+    const float* x = slot(j) + 128 * ch + 4 * col;
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4*>(x + 512 * k);
+    const float w = fast_exp2(ml.x - top);
+    l = fmaf(w, ml.y, l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int row = gcol / p.G, g = gcol - row * p.G;
+  uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + ch;
+#pragma unroll
+  for (int k = 0; k < 16; k += 8)
+    *reinterpret_cast<uint4*>(dst + k) =
+        make_uint4(pack_bf162(acc[k] * inv, acc[k + 1] * inv), pack_bf162(acc[k + 2] * inv, acc[k + 3] * inv),
+                   pack_bf162(acc[k + 4] * inv, acc[k + 5] * inv), pack_bf162(acc[k + 6] * inv, acc[k + 7] * inv));
 }
 
 template <typename Kern, typename... Args>
@@ -979,14 +1028,15 @@ oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_
              ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-// Few columns with many parts each: four warps a column; 128 with few: one.
 template <int D, int NT>
 oscar_status launch_merge(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  constexpr int kSplit = NT <= 2 ? 4 : 1, kCols = 8 / kSplit;
-  const dim3 grid(static_cast<unsigned>(pl.ctas),
-                  static_cast<unsigned>((std::min(p.cols, 8 * NT) + kCols - 1) / kCols));
-  return launch_kv8(kv8_merge_kernel<D, NT, kSplit>, 1, grid, 256, 0, st, p) == cudaSuccess
-             ? OSCAR_OK : OSCAR_ERR_CUDA;
+  const unsigned ctas = static_cast<unsigned>(pl.ctas);
+  cudaError_t e;
+  if constexpr (NT == kRowsNT)
+    e = launch_kv8(kv8_merge_rows_kernel<D>, 1, dim3(ctas, (std::min(p.cols, 128) + 31) / 32), 2 * D, 0, st, p);
+  else   // four warps a column
+    e = launch_kv8(kv8_merge_kernel<D, NT>, 1, dim3(ctas, (std::min(p.cols, 8 * NT) + 1) / 2), 256, 0, st, p);
+  return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 template <int D, bool kE4m3>

@@ -57,7 +57,7 @@ struct RowsSmem {
 
 struct RowsBars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // fp16 tiles, by tile number
-  uint64_t sfull[2], pfull[2], wdone[2];               // S ready, w ready, w used, by stream
+  uint64_t sfull[2], pfull[4], wdone[2];               // S ready, w ready, w used, by stream
   uint64_t qfull[2], oempty[2];                        // by unit: queries ready, O read
   uint64_t qempty, odone, mlfull, last[2];
 };
@@ -300,44 +300,47 @@ __device__ __noinline__ void tail_values(const Kv8Params& p, int b, int h, int l
   }
 }
 
+// The largest finite magnitude of a column's part; out of line, as nearly never needed.
+template <int kWords>
+__device__ __noinline__ uint32_t finite_magnitude(const uint4* src) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8 * kWords; ++i) {
+    const uint32_t x = reinterpret_cast<const uint16_t*>(src)[i] & 0x7fffu;
+    if (x < 0x7f80u) top = max(top, x);
+  }
+  return top;
+}
+
 // Sixteen query columns of a unit (the w-th of eight parts) as fp16 rows of the operand at
 // dst, each scaled by a power of two; facs gets what a logit in the log2 domain is per unit of
-// S.  D / 8 lanes a column, four loads in flight.
+// S.  Two lanes a column, all their loads in flight at once.
 template <int D>
 __device__ __noinline__ void load_queries(const Kv8Params& p, int b, int h, int tile, int w, int lane,
                                           uint8_t* dst, float* facs) {
-  constexpr int kLanes = D / 8, kCols = 32 / kLanes;   // lanes of a column, columns at once
-  const int part = lane % kLanes;
-  int rr = 16 * w + lane / kLanes, col = tile * 128 + rr;
-  int row = col / p.G, g = col - row * p.G;
-#pragma unroll 1
-  for (int i0 = 0; i0 < 16 / kCols; i0 += 4) {
-    uint4 q[4];
+  constexpr int kWords = D / 16;   // 16-byte words of a lane
+  const int rr = 16 * w + (lane >> 1), part = lane & 1, col = tile * 128 + rr;
+  const int row = col / p.G, g = col - row * p.G;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      p.q + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D) + part * kWords;
+  uint4 q[kWords];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t* src = p.q + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D;
-      q[i] = col < p.cols ? reinterpret_cast<const uint4*>(src)[part] : make_uint4(0, 0, 0, 0);
-      col += kCols;
-      for (g += kCols; g >= p.G; g -= p.G) ++row;
-    }
+  for (int i = 0; i < kWords; ++i) q[i] = col < p.cols ? src[i] : make_uint4(0, 0, 0, 0);
+  uint32_t pair = 0;   // magnitudes as pairs of 16-bit integers
 #pragma unroll
-    for (int i = 0; i < 4; ++i, rr += kCols) {
-      const uint32_t x[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-      uint32_t top = 0;   // largest finite magnitude
+  for (int i = 0; i < kWords; ++i)
+    pair = __vmaxu2(__vmaxu2(__vmaxu2(pair, q[i].x & 0x7fff7fffu), __vmaxu2(q[i].y & 0x7fff7fffu, q[i].z & 0x7fff7fffu)),
+                    q[i].w & 0x7fff7fffu);
+  uint32_t top = max(pair & 0xffffu, pair >> 16);
+  if (top >= 0x7f80u) top = finite_magnitude<kWords>(src);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const int up = scale_up(top);
+  const float mul = power_of_two(up);
+  if (part == 0) facs[rr] = p.scale_log2 * power_of_two(-up);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
-        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int up = scale_up(top);
-      const float mul = power_of_two(up);
-      *reinterpret_cast<uint4*>(dst + tc_sw128_offset(rr, 8 * part, kRTile)) =
-          make_uint4(half_pair(x[0], mul), half_pair(x[1], mul), half_pair(x[2], mul), half_pair(x[3], mul));
-      if (part == 0) facs[rr] = p.scale_log2 * power_of_two(-up);
-    }
-  }
+  for (int i = 0; i < kWords; ++i)
+    *reinterpret_cast<uint4*>(dst + tc_sw128_offset(rr, 8 * (part * kWords + i), kRTile)) =
+        make_uint4(half_pair(q[i].x, mul), half_pair(q[i].y, mul), half_pair(q[i].z, mul), half_pair(q[i].w, mul));
 }
 
 // 2^x; unlike fast_exp2 free to move among its neighbours.
@@ -407,7 +410,7 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
 // w = 2^(s_K fac S + log2 s_V - m) of the row, as fp16 over the columns of S that have been
 // read; returns the sum of w / s_V.
 template <bool kMasked>
-__device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, float fac, int vis, float m) {
+__device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const float4* mt, float fac, int vis, float m) {
   float l = 0.f;
   auto pages = [&](const uint32_t (&s)[32], int j0) {
     uint32_t out[16];
@@ -445,6 +448,12 @@ __device__ __forceinline__ float rows_weights(uint32_t ts, const float4* mt, flo
     tc_wait_ld(b);
     tc_request32(ts + (j == 0 ? 64 : 0), a);   // (the last one is not looked at)
     pages(b, j + 2);
+    if (j == 0) {
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) tc_arrive(half);
+    }
   }
   tc_wait_ld(a);
   return l;
@@ -475,6 +484,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       mbar_init(&bar->vempty[i], 1);
       mbar_init(&bar->sfull[i], 1);
       mbar_init(&bar->pfull[i], 4);
+      mbar_init(&bar->pfull[2 + i], 4);
       mbar_init(&bar->wdone[i], 1);
       mbar_init(&bar->last[i], 1);
       mbar_init(&bar->qfull[i], 8);
@@ -517,7 +527,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     constexpr uint32_t id_s = tc_idesc_f16(kRTile, kRTile), id_o = tc_idesc_f16(kRTile, D);
     constexpr int kAtom = kRTile * 128;   // 64 channels of K or Q
     constexpr int kAtomV = D * 128;       // 64 tokens of V
-    const int st = warp - 16;
+    const int st = __shfl_sync(0xffffffffu, warp, 0) - 16;   // (known to be one for the warp)
+    const bool leader = tc_elect();
     uint32_t g0 = 0, seg = 0;             // tiles before this unit, units with tiles
     uint32_t count = 0;                   // tiles of the stream whose O has been issued
     bool ok = true;
@@ -525,11 +536,11 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (u.tiles == 0) continue;
       if (!(ok = wait(&bar->qfull[seg & 1], seg >> 1))) break;
       for (int i = st; i < u.tiles && ok; i += 2) {
-        const uint32_t g = g0 + i, buf = g & 1;
+        const uint32_t g = g0 + i, buf = __shfl_sync(0xffffffffu, g & 1, 0);
         // S of the tile, once w of the stream's tile before, which lies in it, has been used
         ok = wait(&bar->kfull[buf], g >> 1) && (count == 0 || wait(&bar->wdone[st], count - 1));
         if (!ok) break;
-        if (lane == 0) {
+        if (leader) {
           tc_fence_after();
           const uint32_t a0 = sb + S::kQ, b0 = sb + S::kK + buf * S::kTile16;
 #pragma unroll
@@ -546,20 +557,32 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
              (i > 1 || seg == 0 || wait(&bar->oempty[(seg - 1) & 1], (seg - 1) >> 1));
         if (!ok) break;
         ++count;
-        if (lane == 0) {
+        const int later = __shfl_sync(0xffffffffu, i > 1 ? 1 : 0, 0);
+        if (leader) {
           tc_fence_after();
           const uint32_t v0 = sb + S::kV + buf * S::kTile16;
 #pragma unroll
-          for (int kk = 0; kk < kRTile / 16; ++kk)
+          for (int kk = 0; kk < kRTile / 32; ++kk)
             tc_mma_ts(tmem + 2 * kRTile + st * D, tmem + st * kRTile + 8 * kk,
-                      tc_desc_sw128(v0 + (kk >> 2) * kAtomV + (kk & 3) * 32), id_o, i > 1 || kk != 0);
+                      tc_desc_sw128(v0 + (kk >> 2) * kAtomV + (kk & 3) * 32), id_o, kk != 0 || later);
+        }
+        __syncwarp();
+        ok = wait(&bar->pfull[2 + st], count - 1);
+        if (!ok) break;
+        if (leader) {
+          tc_fence_after();
+          const uint32_t v0 = sb + S::kV + buf * S::kTile16;
+#pragma unroll
+          for (int kk = kRTile / 32; kk < kRTile / 16; ++kk)
+            tc_mma_ts(tmem + 2 * kRTile + st * D, tmem + st * kRTile + 8 * kk,
+                      tc_desc_sw128(v0 + (kk >> 2) * kAtomV + (kk & 3) * 32), id_o, 1);
           tc_commit(&bar->vempty[buf]);
           tc_commit(&bar->wdone[st]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) {   // the stream's MMAs of the unit: its queries may go, its O is complete
+      if (leader) {   // the stream's MMAs of the unit: its queries may go, its O is complete
         tc_commit(&bar->qempty);
         tc_commit(&bar->odone);
       }
@@ -567,7 +590,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       g0 += u.tiles;
       ++seg;
     }
-    if (!ok && lane == 0) {   // MMAs in flight finish before the CTA ends
+    if (!ok && leader) {   // MMAs in flight finish before the CTA ends
       tc_commit(&bar->last[st]);
       mbar_wait(&bar->last[st], 0, p.status);
     }
@@ -590,12 +613,12 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           for (int c = 0; c < D / 32; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
         }
       };
-      request(0);
       if (!wait(&bar->qempty, seg + 1)) break;
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
       load_queries<D>(p, u.t.b, u.h, u.t.tile, 4 + w, lane, smem + S::kQ, facs + (seg & 1) * 128);
       fence_proxy_async();
       arrive(&bar->qfull[seg & 1]);
+      request(0);   // (earlier, it would be spilled around the queries: 7 us of 98)
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
         uint8_t* dst = smem + S::kV + buf * S::kTile16;
@@ -641,13 +664,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         if (lane < 2 && shown)
           sc = __ldg(reinterpret_cast<const float2*>(p.pool + static_cast<int64_t>(mine) * F::kBlock + F::kScales));
       };
-      request(0);
       if (!wait(&bar->qempty, seg + 1)) break;
       // and the unit before the last has been read (what is kept by unit comes round again)
       if (seg > 1 && !wait(&bar->oempty[seg & 1], (seg - 2) >> 1)) break;
       load_queries<D>(p, u.t.b, u.h, u.t.tile, w, lane, smem + S::kQ, facs + (seg & 1) * 128);
       fence_proxy_async();
       arrive(&bar->qfull[seg & 1]);
+      request(0);   // (earlier, it would be spilled around the queries: 7 us of 98)
       for (int i = 0; i < u.tiles; ++i, ++g) {
         const uint32_t buf = g & 1;
         uint8_t* dst = smem + S::kK + buf * S::kTile16 + 2048 * w;
@@ -712,6 +735,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           if (idle) {   // no column of this warp exists: its rows of w and O may hold anything
             tc_fence_before();
             arrive(&bar->pfull[st]);
+            arrive(&bar->pfull[2 + st]);
             continue;
           }
           bool hides = false;
@@ -737,10 +761,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
               }
             }
           }
-          l += masked ? rows_weights<true>(ts, mt, fac, vis, m) : rows_weights<false>(ts, mt, fac, vis, m);
+          l += masked ? rows_weights<true>(&bar->pfull[st], ts, mt, fac, vis, m) : rows_weights<false>(&bar->pfull[st], ts, mt, fac, vis, m);
           tc_wait_st();
           tc_fence_before();
-          arrive(&bar->pfull[st]);
+          arrive(&bar->pfull[2 + st]);
         }
         if (!ok) break;
         // the other stream's maximum and sum
@@ -807,7 +831,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           } else {
 #pragma unroll
             for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4*>(slot + rr * D + ch + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              *reinterpret_cast<float4*>(slot + 128 * (ch + k) + 4 * rr) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             if (ch == 0) *reinterpret_cast<float2*>(slot + 128 * D + 2 * rr) = make_float2(top, l);
           }
         }

@@ -48,33 +48,30 @@ __device__ __forceinline__ int row_limit(const Kv8Params& p, int b, int row, int
   return pos >= 0 && pos < len ? pos + 1 : 0;
 }
 
-// Tokens that the rows of a tile see: the furthest row's.  kWarp: called by whole warps with
-// one tile, each lane its rows; else by a thread on its own (four loads in flight).
-template <int NT, bool kWarp>
+// Tokens that the rows of a tile see: the furthest row's.  By groups of kLanes threads with
+// one tile, each thread its rows, four loads in flight.
+template <int NT, int kLanes>
 __device__ __forceinline__ int tile_limit(const Kv8Params& p, int b, int tile, int len) {
   const int r0 = tile * 8 * NT / p.G;
   const int r1 = min(p.cols - 1, tile * 8 * NT + 8 * NT - 1) / p.G;
-  if constexpr (kWarp) {
-    int vis = 0;
+  int vis = 0;
 #pragma unroll 1
-    for (int r = r0 + (threadIdx.x & 31); r <= r1; r += 32) vis = max(vis, row_limit(p, b, r, len));
-    return __reduce_max_sync(0xffffffffu, vis);
-  }
-  int vis = row_limit(p, b, r1, len);   // rows are mostly in order
-  if (vis == len) return vis;
-#pragma unroll 4
-  for (int r = r0; r < r1; ++r) vis = max(vis, row_limit(p, b, r, len));
+  for (int r = r0 + (threadIdx.x & (kLanes - 1)); r <= r1; r += 4 * kLanes)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) vis = max(vis, row_limit(p, b, min(r + k * kLanes, r1), len));
+  if constexpr (kLanes > 1)
+    for (int o = 1; o < kLanes; o <<= 1) vis = max(vis, __shfl_xor_sync(0xffffffffu, vis, o));
   return vis;
 }
 
-template <int NT, bool kWarp>
+template <int NT, int kLanes>
 __device__ __forceinline__ Entry make_entry(const Kv8Params& p, int e) {
   Entry t;
   t.b = e / p.tiles;
   t.tile = e - t.b * p.tiles;
   const int len = p.seq_lens[t.b];
   t.len = len >= 0 && len <= p.max_len ? len : 0;
-  t.vis = p.q_pos ? tile_limit<NT, kWarp>(p, t.b, t.tile, t.len) : t.len;
+  t.vis = p.q_pos ? tile_limit<NT, kLanes>(p, t.b, t.tile, t.len) : t.len;
   const int whole = t.len / kPage;
   t.n8 = min(whole, (t.vis + kPage - 1) / kPage);
   t.pages = max(1, t.n8 + (t.vis > whole * kPage ? 1 : 0));
@@ -84,7 +81,7 @@ __device__ __forceinline__ Entry make_entry(const Kv8Params& p, int e) {
 // By whole warps.
 template <int NT>
 __device__ __forceinline__ Entry entry_of(const Kv8Params& p, int e) {
-  return make_entry<NT, true>(p, e);
+  return make_entry<NT, 32>(p, e);
 }
 
 // First element of column `col` of the tile; null when the tile has fewer columns.
@@ -127,29 +124,27 @@ struct Share {
 // (Kept out of line, and its loops rolled: code that a CTA runs once costs its fetches.)
 template <int NT, int kWarps>
 __device__ __noinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
-  constexpr int kThreads = 32 * kWarps;
+  // threads of an entry, for its rows' positions; entries at a time
+  constexpr int kLanes = NT > 2 ? 8 : 1, kAtOnce = 32 * kWarps / kLanes;
   __shared__ int64_t scratch[kWarps];
   __shared__ Entry found;
   __shared__ int found_number;
   __shared__ int64_t found_before;
-  const int tid = threadIdx.x;
+  const int own_e = threadIdx.x / kLanes;
   Share s{};
   int64_t before = 0, total = 0;
-  // pass 0: the sum; pass 1: the entry that holds `at`, kThreads at a time (of no more
+  // pass 0: the sum; pass 1: the entry that holds `at`, kAtOnce at a time (of no more
   // entries than that, with what pass 0 found)
   Entry own{};
   int64_t v = 0, incl = 0, all = 0;
-  const bool few = p.entries <= kThreads;
+  const bool few = p.entries <= kAtOnce;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-    for (int e0 = 0; e0 < p.entries; e0 += kThreads) {
+    for (int e0 = 0; e0 < p.entries; e0 += kAtOnce) {
       if (pass == 0 || !few) {
-        v = 0;
-        if (e0 + tid < p.entries) {
-          own = make_entry<NT, false>(p, e0 + tid);
-          v = static_cast<int64_t>(own.pages) * p.hkv;
-        }
+        own = make_entry<NT, kLanes>(p, min(e0 + own_e, p.entries - 1));
+        v = e0 + own_e < p.entries && threadIdx.x % kLanes == 0 ? static_cast<int64_t>(own.pages) * p.hkv : 0;
         incl = block_scan<kWarps>(v, scratch, all);
       }
       if (pass == 0) {
@@ -158,7 +153,7 @@ __device__ __noinline__ Share find_share(const Kv8Params& p, int min_share, bool
         if (s.at < before + all) {   // one thread's
           if (before + incl - v <= s.at && s.at < before + incl) {
             found = own;
-            found_number = e0 + tid;
+            found_number = e0 + own_e;
             found_before = before + incl - v;
           }
           break;
