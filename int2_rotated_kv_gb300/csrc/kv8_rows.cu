@@ -413,9 +413,9 @@ template <bool kMasked>
 __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const float4* mt, float fac, int vis, float m) {
   float l = 0.f;
   auto pages = [&](const uint32_t (&s)[32], int j0) {
-    uint32_t out[16];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+      uint32_t out[8];
       const float4 pm = mt[j0 + j];
       const float f = pm.x * fac, off = pm.y - m;
       const uint64_t f2 = two(f, f), off2 = two(off, off);
@@ -431,12 +431,12 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
         }
         const uint64_t x = two(x0, x1);
         sum[(k >> 1) & 1] = k < 4 ? x : add2(sum[(k >> 1) & 1], x);
-        out[8 * j + k / 2] = pack_half2(x0, x1);
+        out[k / 2] = pack_half2(x0, x1);
       }
+      tc_st8(ts + 8 * (j0 + j), out);
       const uint64_t all = add2(sum[0], sum[1]);
       if (!kMasked || seen > 0) l = fmaf(first(all) + second(all), pm.z, l);
     }
-    tc_st16(ts + 8 * j0, out);
   };
   uint32_t a[32], b[32];
   tc_request32(ts, a);

@@ -121,9 +121,10 @@ struct Share {
   Entry t;
 };
 
-// (Kept out of line, and its loops rolled: code that a CTA runs once costs its fetches.)
+// (Its loops rolled: code that a CTA runs once costs its fetches.  Not out of line: there the
+// parameters are read through memory, 2% of the 65-row case.)
 template <int NT, int kWarps>
-__device__ __noinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
+__device__ __forceinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
   // threads of an entry, for its rows' positions; entries at a time
   constexpr int kLanes = NT > 2 ? 8 : 1, kAtOnce = 32 * kWarps / kLanes;
   __shared__ int64_t scratch[kWarps];
