@@ -25,7 +25,6 @@
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (d each); w in the first half of S.
 // What bounds it: shared memory, 1536 cycles a tile at d = 128 (fp16 tiles written once
 // and read by the MMAs, Q read per tile), above the 1024 cycles of the MMAs.
-#include <algorithm>
 
 #include "kv8_units.cuh"
 #include "tcgen05.cuh"
@@ -35,6 +34,9 @@ namespace oscar {
 constexpr int kRWarps = 18;
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRTile = 128;        // tokens of a tile
+// A page of zeros (value scale 0) counts its tokens as one of scale 2^-64: far enough below any
+// page that matters not to push its weights out of fp16, and still in reach of fp32 sums.
+constexpr int kRZero = 64;
 constexpr int kRHidden = 0x7fff0000;   // position of a page slot that holds no page
 
 template <int D>
@@ -255,7 +257,8 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
   const uint16_t* area = tail_block<D>(p, b, h, ok);
   const int n = len % kPage;
   const int up = scale_up(tail_magnitude<D>(area, 0, n, lane, odd));
-  const int up_v = scale_up(tail_magnitude<D>(area + Kv8Fmt<D>::kTailHalf, 1, n, lane, odd));
+  const uint32_t top_v = tail_magnitude<D>(area + Kv8Fmt<D>::kTailHalf, 1, n, lane, odd);
+  const int up_v = top_v ? scale_up(top_v) : kRZero;
   const float mul = power_of_two(up);
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
@@ -681,10 +684,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
         if (lane < 2) {   // what the softmax needs of the two pages
           const int slot = 4 * lane + w;
-          // a page of zeros (scale 0) still counts its tokens: weight 1, values 0
           const bool live = sc.y > 0.f;
           meta[(g & 3) * 8 + slot] =
-              shown ? make_float4(sc.x, live ? __log2f(sc.y) : 0.f, live ? __fdividef(1.f, sc.y) : 1.f,
+              shown ? make_float4(sc.x, live ? __log2f(sc.y) : -kRZero, live ? __fdividef(1.f, sc.y) : power_of_two(kRZero),
                                   __int_as_float((u.p0 + 8 * i + slot) * kPage))
                     : make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
         }

@@ -288,6 +288,26 @@ def test_scales_of_values_and_queries(fmt, m):
     s.check_pools()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+def test_pages_of_zeros_among_small_values(fmt, m):
+    """Values of 1e-5 beside pages, and a tail, whose values are all zero: the zeros' weights
+    count, and take no precision from the others."""
+    s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=m)
+    n = np.array([650, 16 * 20, 16 * 9 + 7])
+    k, v = K.draw(s.rng, int(n.sum()), 1, 128)
+    v = synth.bf16_round(v * np.float32(1e-5))
+    v[32:64] = 0
+    v[16 * 30:16 * 31] = 0
+    v[640:650] = 0                    # the first sequence's tail
+    v[650:650 + 16 * 19] = 0          # all but the second's last page
+    s.place(n, k, v)
+    q = K.queries(s.rng, 3, m, 4, 128)
+    pos = None if m == 1 else np.stack([np.arange(x - m, x) for x in n])
+    s.check_attention(s.attend(q, pos), q, pos)
+    assert H.status(s.cache) == 0
+
+
 def test_a_token_that_a_row_does_not_see_does_not_reach_it():
     """NaN and infinity in the tail: rows before them keep finite outputs, rows behind
     them get what the softmax gives."""
@@ -416,3 +436,64 @@ def test_calls_on_two_streams_with_their_own_workspaces():
     t.cuda.synchronize()
     for o in outs:
         np.testing.assert_array_equal(H.from_bf16(o), want[:, 0])
+
+
+def test_a_descriptor_is_checked_again_when_a_tensor_is_replaced():
+    """Also by one at the same address."""
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(3, 1, 1, 64, kv8.INT8, 100, permute_tails=True)
+    s.place([20, 30, 40])
+    q = K.queries(s.rng, 3, 1, 1, 64)
+    s.attend(q)
+    table, tails, pool = s.cache.page_table, s.cache.tail_ids, s.cache.pool
+    for name, bad in (("page_table", table.view(t.float32)), ("tail_ids", tails[:2]),
+                      ("pool", pool.view(t.int8)), ("tail", s.cache.tail.view(t.float16))):
+        good = getattr(s.cache, name)
+        setattr(s.cache, name, bad)
+        with pytest.raises(ValueError):
+            s.attend(q)
+        setattr(s.cache, name, good)
+    s.check_attention(s.attend(q), q)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, "tests")
+import torch
+import kv8_harness as K
+from oracle import kv8
+from int2_rotated_kv_gb300 import _lib as L
+s = K.Sequences(2, 2, 8, 128, kv8.INT8, 400)
+new, ws = [300, 77], torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+k, v = K.draw(s.rng, 377, 2, 128)
+q = K.queries(s.rng, 2, 40, 8, 128)
+from gpu_harness import bf16_tensor, from_bf16
+kt, vt, qt = bf16_tensor(k), bf16_tensor(v), bf16_tensor(q)
+one, before, starts, lens = qt[:, 0].contiguous(), s.i32([0, 0]), s.i32([0, 300, 377]), s.i32(new)
+pos = s.i32([range(260, 300), range(37, 77)])
+out, out1 = torch.zeros_like(qt), torch.zeros_like(one)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    L.oscar_kv8_place(s.cache, kt, vt, before, starts, 300)
+    L.oscar_kv8_attention(s.cache, one, lens, 400, out1, ws)
+    L.oscar_kv8_attention(s.cache, qt, lens, 400, out, ws, q_pos=pos)
+s.k, s.v = [k[:300], k[300:]], [v[:300], v[300:]]
+for _ in range(2):
+    out.zero_(), out1.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    s.check_attention(from_bf16(out1).reshape(2, 1, 8, 128), q[:, :1])
+    s.check_attention(from_bf16(out).reshape(2, 40, 8, 128), q, pos.cpu().numpy())
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.split()[-1] == "captured", r.stdout + r.stderr
