@@ -492,10 +492,14 @@ class Kv8Cache:
     def _checked(self):
         """(descriptor, device index, pages-table rows), checked again when a tensor or a
         field has been replaced."""
-        key = (self.pool.data_ptr(), self.tail.data_ptr(), self.page_table.data_ptr(),
-               _ptr(self.tail_ids), _ptr(self.status), self.fmt, self.num_q_heads,
-               self.num_kv_heads, self.head_dim, self.page_table.shape, self.pool.shape,
-               self.tail.shape)
+        pool, tail, table, ids, status = (self.pool, self.tail, self.page_table, self.tail_ids,
+                                          self.status)
+        key = (pool.data_ptr(), pool.shape, pool.dtype, pool.is_contiguous(),
+               tail.data_ptr(), tail.shape, tail.dtype, tail.is_contiguous(),
+               table.data_ptr(), table.shape, table.dtype, table.is_contiguous(),
+               None if ids is None else (ids.data_ptr(), ids.shape, ids.dtype, ids.is_contiguous()),
+               None if status is None else (status.data_ptr(), status.dtype),
+               self.fmt, self.num_q_heads, self.num_kv_heads, self.head_dim)
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:
             return cached[1]
@@ -565,7 +569,10 @@ def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int
 
 
 def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
-    return int(lib().oscar_kv8_workspace_size(cache._checked()[1], batch, m_rows, max_seq_len))
+    import torch
+    _, desc, index, _ = cache._checked()
+    with torch.cuda.device(index):   # its number of SMs counts
+        return int(lib().oscar_kv8_workspace_size(desc, batch, m_rows, max_seq_len))
 
 
 def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,

@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <new>
 #include <type_traits>
 #include <utility>
 #include <vector>
@@ -1683,7 +1684,10 @@ bool allow_smem(const void* func, int bytes, bool clusters) {
   if (clusters &&
       cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return false;
-  done.emplace_back(func, dev);
+  try {
+    done.emplace_back(func, dev);
+  } catch (const std::bad_alloc&) {   // set again by the next call
+  }
   return true;
 }
 

@@ -37,10 +37,8 @@
 //
 // Bound by HBM: 2d + 1 bytes per token and KV head.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <mutex>
-#include <utility>
-#include <vector>
 
 #include "kv8_units.cuh"
 
@@ -915,39 +913,46 @@ struct ClusterSizes {
 };
 
 // (The kernel for d = 128 stands for all: every cluster kernel fills an SM.)
-const ClusterSizes& cluster_sizes() {
-  static std::mutex mu;
-  static std::vector<std::pair<int, ClusterSizes>> known;   // device
-  static const ClusterSizes none{};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return none;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const auto& k : known)
-    if (k.first == dev) return k.second;
+ClusterSizes count_clusters() {
   using C = Kv8Cfg<128, 1, kCluster>;
   const auto kernel = kv8_attention_kernel<128, 1, false, kCluster>;
   ClusterSizes s{};
-  if (oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) {
-    for (int c = 1; c <= kMaxCluster; ++c) {
-      cudaLaunchConfig_t cfg{};
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = static_cast<unsigned>(c);
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.gridDim = dim3(static_cast<unsigned>(c));
-      cfg.blockDim = dim3(C::kThreads);
-      cfg.dynamicSmemBytes = C::kBytes;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&s.active[c], kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        s.active[c] = 0;
-      }
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) return s;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(c);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(c));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&s.active[c], kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      s.active[c] = 0;
     }
   }
-  known.reserve(64);   // references into it stay valid
-  known.emplace_back(dev, s);
-  return known.back().second;
+  return s;
+}
+
+// Counted once per device.  (Threads that are the first at once all count, to the same end.)
+ClusterSizes cluster_sizes() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];   // [0]: whether the others are
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return {};
+  if (dev >= kDevices) return count_clusters();
+  ClusterSizes s{};
+  if (known[dev][0].load(std::memory_order_acquire)) {
+    for (int c = 1; c <= kMaxCluster; ++c) s.active[c] = known[dev][c].load(std::memory_order_relaxed);
+    return s;
+  }
+  s = count_clusters();
+  for (int c = 1; c <= kMaxCluster; ++c) known[dev][c].store(s.active[c], std::memory_order_relaxed);
+  known[dev][0].store(1, std::memory_order_release);
+  return s;
 }
 
 struct Kv8Plan {
@@ -964,7 +969,7 @@ struct Kv8Plan {
 // kernel and longer first and last waves, 6 us.  Measured, 8 KV heads: one sequence of
 // 32k 18.6 us against 23.9, of 128k 48.7 against 54.
 inline int cluster_of(int64_t batch, int64_t units, int64_t pages) {
-  const ClusterSizes& s = cluster_sizes();
+  const ClusterSizes s = cluster_sizes();
   int c = kMaxCluster;
   while (c > 0 && s.active[c] < units) --c;
   if (c == 0) return 0;
