@@ -8,7 +8,7 @@
 // The codes go to the tensor cores as exact fp16 operands (two byte permutes per
 // four int8 codes, one conversion per two e4m3 codes), keys as the A operand of
 // q.K and values, transposed, as the A operand of p.V; 8 query columns (row, query
-// head) fill the N dimension and NT tiles of them share every unpacked code:
+// head) fill the N dimension:
 //   logit = s_K * (sum_c (u_c - 128) q_c),  the -128 sum_c q_c as the initial
 //     accumulator (int8); q enters as fp16 scaled by a power of two per column,
 //     which keeps all 8 bits of every bf16 within 2^-21 of the column's largest.
@@ -46,169 +46,153 @@ namespace oscar {
 
 enum Kv8Mode { kShares, kCluster, kTeams };
 
-template <int D, int NT, Kv8Mode kMode>
+template <int D, Kv8Mode kMode>
 struct Kv8Cfg {
   using F = Kv8Fmt<D>;
   static constexpr int kWarps = kMode == kCluster ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = NT == 1 && kMode != kCluster ? 2 : 1;   // per SM
-  static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+  static constexpr int kCtas = kMode != kCluster ? 2 : 1;   // per SM
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarpRing = kStages * F::kBlock;
   static constexpr int kStride = D + 4;                     // floats per column when merging
   static constexpr int kMerge = kWarps * 8 * kStride * 4;
-  static constexpr int kStat = kWarps * 8 * NT * 4;         // one of m, l
-  static constexpr int kSlot = kv8_slot<D, NT>();
+  static constexpr int kStat = kWarps * 8 * 4;              // one of m, l
+  static constexpr int kSlot = kv8_slot<D, 1>();
   static constexpr int kMergeOff = kWarps * kWarpRing;
   static constexpr int kStatOff = kMergeOff + kMerge;
   static constexpr int kPartOff = kStatOff + 2 * kStat;     // a cluster's CTA: its partial
   static constexpr int kBarOff = kPartOff + (kMode == kCluster ? kSlot * 4 : 0);
   static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
-  static_assert(kMode == kShares || NT == 1, "clusters and teams serve one tile of columns per unit");
   static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
 };
 
-// The columns of one unit as a lane sees them: operands for column gid of each
-// tile, factors and limits for columns 2tig and 2tig + 1.
-template <int D, int NT>
+// The columns of one unit as a lane sees them: operands for column gid, factors and limits for
+// columns 2tig and 2tig + 1.
+template <int D>
 struct Query {
-  uint32_t b[NT][D / 16][2];
-  float fac[NT][2];     // log2-domain logit per unit of q.code, before s_K
-  float init[NT][2];    // -128 sum q (int8)
-  int vis[NT][2];
-  int vis_min;          // smallest over the unit's columns
+  uint32_t b[D / 16][2];
+  float fac[2];     // log2-domain logit per unit of q.code, before s_K
+  float init[2];    // -128 sum q (int8)
+  int vis[2];
+  int vis_min;      // smallest over the unit's columns
 };
 
-template <int D, int NT, bool kE4m3>
+template <int D, bool kE4m3>
 __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, int h, int lane,
-                                           Query<D, NT>& q) {
+                                           Query<D>& q) {
   const int gid = lane >> 2, tig = lane & 3;
-  q.vis_min = 0x7fffffff;
+  const int col = t.tile * 8 + gid;
+  const uint16_t* src = column(p, t, h, col, D);
+  int vis = 0x7fffffff;
+  if (src) vis = p.q_pos ? row_limit(p, t.b, col / p.G, t.len) : t.len;
+  uint4 raw[D / 32];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int col = (t.tile * NT + nt) * 8 + gid;
-    const uint16_t* src = column(p, t, h, col, D);
-    int vis = 0x7fffffff;
-    if (src) vis = p.q_pos ? row_limit(p, t.b, col / p.G, t.len) : t.len;
-    uint4 raw[D / 32];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const uint4* s = reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig);
-      raw[2 * j] = src ? s[0] : make_uint4(0, 0, 0, 0);
-      raw[2 * j + 1] = src ? s[1] : make_uint4(0, 0, 0, 0);
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo_value(w[x])), fabsf(bf16_hi_value(w[x]))));
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // the largest magnitude goes to [2^7, 2^8)
-    const int exponent = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
-    const int up = amax > 0.f ? max(-96, min(100, 7 - exponent)) : 0;
-    const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {   // four channels: one k-step of this lane
-        const float x0 = bf16_lo_value(w[2 * half]) * mul, x1 = bf16_hi_value(w[2 * half]) * mul;
-        const float x2 = bf16_lo_value(w[2 * half + 1]) * mul;
-        const float x3 = bf16_hi_value(w[2 * half + 1]) * mul;
-        // the pairs of kv8_operands
-        const uint32_t b0 = kE4m3 ? pack_half2(x0, x1) : pack_half2(x0, x2);
-        const uint32_t b1 = kE4m3 ? pack_half2(x2, x3) : pack_half2(x1, x3);
-        q.b[nt][2 * i + half][0] = b0;
-        q.b[nt][2 * i + half][1] = b1;
-        sum += (half_lo(b0) + half_hi(b0)) + (half_lo(b1) + half_hi(b1));
-      }
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    const float fac =
-        p.scale_log2 * __uint_as_float(static_cast<uint32_t>((kE4m3 ? 0 : 24) - up + 127) << 23);
-    const float init = kE4m3 ? 0.f : sum * (-128.f / 16777216.f);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      q.fac[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * tig + 4 * c);
-      q.init[nt][c] = __shfl_sync(0xffffffffu, init, 8 * tig + 4 * c);
-      q.vis[nt][c] = __shfl_sync(0xffffffffu, vis, 8 * tig + 4 * c);
-    }
-    q.vis_min = min(q.vis_min, __reduce_min_sync(0xffffffffu, vis));
+  for (int j = 0; j < D / 64; ++j) {
+    const uint4* s = reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig);
+    raw[2 * j] = src ? s[0] : make_uint4(0, 0, 0, 0);
+    raw[2 * j + 1] = src ? s[1] : make_uint4(0, 0, 0, 0);
   }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo_value(w[x])), fabsf(bf16_hi_value(w[x]))));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // the largest magnitude goes to [2^7, 2^8)
+  const int exponent = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
+  const int up = amax > 0.f ? max(-96, min(100, 7 - exponent)) : 0;
+  const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {   // four channels: one k-step of this lane
+      const float x0 = bf16_lo_value(w[2 * half]) * mul, x1 = bf16_hi_value(w[2 * half]) * mul;
+      const float x2 = bf16_lo_value(w[2 * half + 1]) * mul;
+      const float x3 = bf16_hi_value(w[2 * half + 1]) * mul;
+      // the pairs of kv8_operands
+      const uint32_t b0 = kE4m3 ? pack_half2(x0, x1) : pack_half2(x0, x2);
+      const uint32_t b1 = kE4m3 ? pack_half2(x2, x3) : pack_half2(x1, x3);
+      q.b[2 * i + half][0] = b0;
+      q.b[2 * i + half][1] = b1;
+      sum += (half_lo(b0) + half_hi(b0)) + (half_lo(b1) + half_hi(b1));
+    }
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  const float fac =
+      p.scale_log2 * __uint_as_float(static_cast<uint32_t>((kE4m3 ? 0 : 24) - up + 127) << 23);
+  const float init = kE4m3 ? 0.f : sum * (-128.f / 16777216.f);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    q.fac[c] = __shfl_sync(0xffffffffu, fac, 8 * tig + 4 * c);
+    q.init[c] = __shfl_sync(0xffffffffu, init, 8 * tig + 4 * c);
+    q.vis[c] = __shfl_sync(0xffffffffu, vis, 8 * tig + 4 * c);
+  }
+  q.vis_min = __reduce_min_sync(0xffffffffu, vis);
 }
 
 // A warp's running result for its columns.  o: accumulator tiles, element
 // [2i + y][r + 2x] is channel 32i + 4gid + 2y + x of column 2tig + r.
-template <int D, int NT>
+template <int D>
 struct Running {
-  float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  float o[D / 16][4];
+  float m[2], l[2];
   float vmax, vmul;      // power of two that no s_V so far exceeds, and 2^6 / vmax
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void reset(Running<D, NT>& s) {
+template <int D>
+__device__ __forceinline__ void reset(Running<D>& s) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) s.o[nt][i][0] = s.o[nt][i][1] = s.o[nt][i][2] = s.o[nt][i][3] = 0.f;
-    s.m[nt][0] = s.m[nt][1] = kLowest;
-    s.l[nt][0] = s.l[nt][1] = 0.f;
-  }
+  for (int i = 0; i < D / 16; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
+  s.m[0] = s.m[1] = kLowest;
+  s.l[0] = s.l[1] = 0.f;
   s.vmax = 9.62964972193618e-35f;   // 2^-113, below every scale but 0
   s.vmul = 64.f / 9.62964972193618e-35f;
 }
 
 // Raises the running maxima where a logit passes one by more than kLag (so p <=
 // 2^kLag) and rescales; lg: rows gid, gid + 8 of the tile in the accumulator layout.
-template <int D, int NT>
-__device__ __forceinline__ void raise_max(Running<D, NT>& s, const float (&lg)[NT][4]) {
+template <int D>
+__device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
   bool over = false;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) over |= fmaxf(lg[nt][c], lg[nt][2 + c]) > s.m[nt][c] + kLag;
+  for (int c = 0; c < 2; ++c) over |= fmaxf(lg[c], lg[2 + c]) > s.m[c] + kLag;
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int c = 0; c < 2; ++c) {
+      float top = fmaxf(lg[c], lg[2 + c]);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      top = fmaxf(top, s.m[c]);
+      const float a = top == s.m[c] ? 1.f : fast_exp2(s.m[c] - top);
+      s.m[c] = top;
+      s.l[c] *= a;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float top = fmaxf(lg[nt][c], lg[nt][2 + c]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        top = fmaxf(top, s.m[nt][c]);
-        const float a = top == s.m[nt][c] ? 1.f : fast_exp2(s.m[nt][c] - top);
-        s.m[nt][c] = top;
-        s.l[nt][c] *= a;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          s.o[nt][i][c] *= a;
-          s.o[nt][i][2 + c] *= a;
-        }
+      for (int i = 0; i < D / 16; ++i) {
+        s.o[i][c] *= a;
+        s.o[i][2 + c] *= a;
       }
     }
   }
 }
 
-// One page of codes at `st`.  shown: false for a page id that was refused.
-template <int D, int NT, bool kE4m3>
-__device__ __forceinline__ void page(const uint8_t* st, int page0, bool shown, int lane,
-                                     const Query<D, NT>& q, Running<D, NT>& s) {
+// One page of codes at `st`.
+template <int D, bool kE4m3>
+__device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, const Query<D>& q,
+                                     Running<D>& s) {
   using F = Kv8Fmt<D>;
   const int gid = lane >> 2;
   const uint4* kb = reinterpret_cast<const uint4*>(st);
-  float lg[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    lg[nt][0] = lg[nt][2] = q.init[nt][0];
-    lg[nt][1] = lg[nt][3] = q.init[nt][1];
-  }
+  float lg[4];
+  lg[0] = lg[2] = q.init[0];
+  lg[1] = lg[3] = q.init[1];
   const float2 sc = *reinterpret_cast<const float2*>(st + F::kScales);
 #pragma unroll
   for (int j = 0; j < D / 64; ++j) {
@@ -219,57 +203,44 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, bool shown, i
       uint32_t a0, a1, a2, a3;
       kv8_operands<kE4m3>(w0[w], a0, a2);
       kv8_operands<kE4m3>(w1[w], a1, a3);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        mma_f16(lg[nt], a0, a1, a2, a3, q.b[nt][4 * j + w][0], q.b[nt][4 * j + w][1]);
+      mma_f16(lg, a0, a1, a2, a3, q.b[4 * j + w][0], q.b[4 * j + w][1]);
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float f0 = sc.x * q.fac[nt][0], f1 = sc.x * q.fac[nt][1];
-    lg[nt][0] *= f0; lg[nt][1] *= f1; lg[nt][2] *= f0; lg[nt][3] *= f1;
-  }
-  if (!shown || page0 + kPage > q.vis_min) {
+  const float f0 = sc.x * q.fac[0], f1 = sc.x * q.fac[1];
+  lg[0] *= f0; lg[1] *= f1; lg[2] *= f0; lg[3] *= f1;
+  if (page0 + kPage > q.vis_min) {
     const int t = page0 + 2 * gid;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!shown || t >= q.vis[nt][c]) lg[nt][c] = -INFINITY;
-        if (!shown || t + 1 >= q.vis[nt][c]) lg[nt][2 + c] = -INFINITY;
-      }
+    for (int c = 0; c < 2; ++c) {
+      if (t >= q.vis[c]) lg[c] = -INFINITY;
+      if (t + 1 >= q.vis[c]) lg[2 + c] = -INFINITY;
+    }
   }
-  raise_max<D, NT>(s, lg);
+  raise_max<D>(s, lg);
   if (sc.y > s.vmax) {   // a larger value scale than any page before (the warp's own, uniform)
     const float up = __uint_as_float((__float_as_uint(sc.y) & 0x7f800000u) + 0x00800000u);
     const float a = s.vmax / up;   // a power of two
     s.vmax = up;
     s.vmul *= a;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s.o[nt][i][r] *= a;
+      for (int r = 0; r < 4; ++r) s.o[i][r] *= a;
   }
   // 2^6 s_V / vmax: p s_V / vmax <= 2^8, so the fp16 weights stay below 2^14
   const float vs = sc.y * s.vmul;
-  uint32_t b0[NT], b1[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float p0 = fast_exp2(lg[nt][0] - s.m[nt][0]), p1 = fast_exp2(lg[nt][1] - s.m[nt][1]);
-    const float p2 = fast_exp2(lg[nt][2] - s.m[nt][0]), p3 = fast_exp2(lg[nt][3] - s.m[nt][1]);
-    s.l[nt][0] += p0 + p2;
-    s.l[nt][1] += p1 + p3;
-    // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
-    // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
-    b0[nt] = movmatrix_trans(pack_half2(p0 * vs, p1 * vs));
-    b1[nt] = movmatrix_trans(pack_half2(p2 * vs, p3 * vs));
-    if constexpr (kE4m3) {   // pairs (4tig, 4tig + 1), (4tig + 2, 4tig + 3)
-      const uint32_t lo = __byte_perm(b0[nt], b1[nt], 0x5410);
-      b1[nt] = __byte_perm(b0[nt], b1[nt], 0x7632);
-      b0[nt] = lo;
-    }
+  const float p0 = fast_exp2(lg[0] - s.m[0]), p1 = fast_exp2(lg[1] - s.m[1]);
+  const float p2 = fast_exp2(lg[2] - s.m[0]), p3 = fast_exp2(lg[3] - s.m[1]);
+  s.l[0] += p0 + p2;
+  s.l[1] += p1 + p3;
+  // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
+  // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
+  uint32_t b0 = movmatrix_trans(pack_half2(p0 * vs, p1 * vs));
+  uint32_t b1 = movmatrix_trans(pack_half2(p2 * vs, p3 * vs));
+  if constexpr (kE4m3) {   // pairs (4tig, 4tig + 1), (4tig + 2, 4tig + 3)
+    const uint32_t lo = __byte_perm(b0, b1, 0x5410);
+    b1 = __byte_perm(b0, b1, 0x7632);
+    b0 = lo;
   }
   const uint4* vb = reinterpret_cast<const uint4*>(st + F::kCodes);
 #pragma unroll
@@ -281,24 +252,21 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, bool shown, i
       uint32_t a0, a1, a2, a3;
       kv8_signed_operands<kE4m3>(w[2 * y], a0, a2);
       kv8_signed_operands<kE4m3>(w[2 * y + 1], a1, a3);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(s.o[nt][2 * i + y], a0, a1, a2, a3, b0[nt], b1[nt]);
+      mma_f16(s.o[2 * i + y], a0, a1, a2, a3, b0, b1);
     }
   }
 }
 
 // Brings the accumulators to the units of the values.
-template <int D, int NT, bool kE4m3>
-__device__ __forceinline__ void unscale(Running<D, NT>& s) {
+template <int D, bool kE4m3>
+__device__ __forceinline__ void unscale(Running<D>& s) {
   // weights carried 2^6 / vmax, int8 codes 2^-24; two factors stay in range
   const float up = kE4m3 ? 1.f / 64.f : 262144.f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        s.o[nt][i][r] = s.o[nt][i][r] * up * s.vmax;
+    for (int r = 0; r < 4; ++r)
+      s.o[i][r] = s.o[i][r] * up * s.vmax;
 }
 
 // The tail: n bf16 tokens from position page0 at `st`; accumulators already in the
@@ -306,45 +274,37 @@ __device__ __forceinline__ void unscale(Running<D, NT>& s) {
 // bf16 (2^-17); when a value is not finite, or a column does not see all n tokens, in
 // fp32 on the CUDA cores instead, which keeps a NaN or an infinity of a token out of
 // the rows that do not see it.
-template <int D, int NT>
+template <int D>
 __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uint8_t* st, int page0,
-                            int n, int lane, const Query<D, NT>& q, Running<D, NT>& s) {
+                            int n, int lane, const Query<D>& q, Running<D>& s) {
   using F = Kv8Fmt<D>;
   const int gid = lane >> 2, tig = lane & 3;
   const uint4* kb = reinterpret_cast<const uint4*>(st);
-  float lg[NT][4] = {};
+  float lg[4] = {};
 #pragma unroll
   for (int j = 0; j < D / 64; ++j) {
     const int c0 = ((2 * j) * 32 + lane) * 2, c1 = ((2 * j + 1) * 32 + lane) * 2;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {   // 8 channels: two k-steps
       const uint4 k0 = kb[c0 + x], k1 = kb[c1 + x];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint16_t* src = column(p, t, h, (t.tile * NT + nt) * 8 + gid, D);
-        const uint4 qv = src ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig + 8 * x)
-                             : make_uint4(0, 0, 0, 0);
-        mma_bf16(lg[nt], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
-        mma_bf16(lg[nt], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
-      }
+      const uint16_t* src = column(p, t, h, t.tile * 8 + gid, D);
+      const uint4 qv = src ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig + 8 * x)
+                           : make_uint4(0, 0, 0, 0);
+      mma_bf16(lg, k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+      mma_bf16(lg, k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int seen = min(n, q.vis[nt][c] - page0);   // tokens of the tail this column sees
-      lg[nt][c] = 2 * gid < seen ? lg[nt][c] * p.scale_log2 : -INFINITY;
-      lg[nt][2 + c] = 2 * gid + 1 < seen ? lg[nt][2 + c] * p.scale_log2 : -INFINITY;
-    }
-  raise_max<D, NT>(s, lg);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) lg[nt][r] = fast_exp2(lg[nt][r] - s.m[nt][r & 1]);
-    s.l[nt][0] += lg[nt][0] + lg[nt][2];
-    s.l[nt][1] += lg[nt][1] + lg[nt][3];
+  for (int c = 0; c < 2; ++c) {
+    const int seen = min(n, q.vis[c] - page0);   // tokens of the tail this column sees
+    lg[c] = 2 * gid < seen ? lg[c] * p.scale_log2 : -INFINITY;
+    lg[2 + c] = 2 * gid + 1 < seen ? lg[2 + c] * p.scale_log2 : -INFINITY;
   }
+  raise_max<D>(s, lg);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) lg[r] = fast_exp2(lg[r] - s.m[r & 1]);
+  s.l[0] += lg[0] + lg[2];
+  s.l[1] += lg[1] + lg[3];
   const uint4* vb = kb + 2 * D;   // 16 * d keys before them
   // tokens 4tig, 4tig + 1 and 4tig + 2, 4tig + 3 of a channel's words, where there are any
   const int have = n - 4 * tig;
@@ -359,28 +319,22 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
   }
   const bool plain = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
   if (q.vis_min >= page0 + n && __all_sync(0xffffffffu, plain)) {
-    uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t h0 = pack_bf162(lg[nt][0], lg[nt][1]), h1 = pack_bf162(lg[nt][2], lg[nt][3]);
-      const uint32_t l0 = pack_bf162(lg[nt][0] - bf16_lo_value(h0), lg[nt][1] - bf16_hi_value(h0));
-      const uint32_t l1 = pack_bf162(lg[nt][2] - bf16_lo_value(h1), lg[nt][3] - bf16_hi_value(h1));
-      const uint32_t t0 = movmatrix_trans(h0), t1 = movmatrix_trans(h1);
-      const uint32_t u0 = movmatrix_trans(l0), u1 = movmatrix_trans(l1);
-      bh[nt][0] = __byte_perm(t0, t1, 0x5410);
-      bh[nt][1] = __byte_perm(t0, t1, 0x7632);
-      bl[nt][0] = __byte_perm(u0, u1, 0x5410);
-      bl[nt][1] = __byte_perm(u0, u1, 0x7632);
-    }
+    uint32_t bh[2], bl[2];
+    const uint32_t h0 = pack_bf162(lg[0], lg[1]), h1 = pack_bf162(lg[2], lg[3]);
+    const uint32_t l0 = pack_bf162(lg[0] - bf16_lo_value(h0), lg[1] - bf16_hi_value(h0));
+    const uint32_t l1 = pack_bf162(lg[2] - bf16_lo_value(h1), lg[3] - bf16_hi_value(h1));
+    const uint32_t t0 = movmatrix_trans(h0), t1 = movmatrix_trans(h1);
+    const uint32_t u0 = movmatrix_trans(l0), u1 = movmatrix_trans(l1);
+    bh[0] = __byte_perm(t0, t1, 0x5410);
+    bh[1] = __byte_perm(t0, t1, 0x7632);
+    bl[0] = __byte_perm(u0, u1, 0x5410);
+    bl[1] = __byte_perm(u0, u1, 0x7632);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
       v.x &= m01; v.y &= m23; v.z &= m01; v.w &= m23;   // slots without a token may hold anything
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_bf16(s.o[nt][i], v.x, v.z, v.y, v.w, bh[nt][0], bh[nt][1]);
-        mma_bf16(s.o[nt][i], v.x, v.z, v.y, v.w, bl[nt][0], bl[nt][1]);
-      }
+      mma_bf16(s.o[i], v.x, v.z, v.y, v.w, bh[0], bh[1]);
+      mma_bf16(s.o[i], v.x, v.z, v.y, v.w, bl[0], bl[1]);
     }
     return;
   }
@@ -392,20 +346,17 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
       const int chunk = kv8_value_chunk(i >> 2, (c >> 2) * 8 + gid);
       v[c >> 1][c & 1] = bf16_to_float(ve[chunk * 16 + 4 * (c & 3) + (i & 3)]);
     }
+    const float w0 = __shfl_sync(0xffffffffu, (i & 1) ? lg[2] : lg[0], 4 * (i >> 1) + tig);
+    const float w1 = __shfl_sync(0xffffffffu, (i & 1) ? lg[3] : lg[1], 4 * (i >> 1) + tig);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float w0 = __shfl_sync(0xffffffffu, (i & 1) ? lg[nt][2] : lg[nt][0], 4 * (i >> 1) + tig);
-      const float w1 = __shfl_sync(0xffffffffu, (i & 1) ? lg[nt][3] : lg[nt][1], 4 * (i >> 1) + tig);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        if (w0 != 0.f) {
-          s.o[nt][k][0] = fmaf(w0, v[k][0], s.o[nt][k][0]);
-          s.o[nt][k][2] = fmaf(w0, v[k][1], s.o[nt][k][2]);
-        }
-        if (w1 != 0.f) {
-          s.o[nt][k][1] = fmaf(w1, v[k][0], s.o[nt][k][1]);
-          s.o[nt][k][3] = fmaf(w1, v[k][1], s.o[nt][k][3]);
-        }
+    for (int k = 0; k < D / 16; ++k) {
+      if (w0 != 0.f) {
+        s.o[k][0] = fmaf(w0, v[k][0], s.o[k][0]);
+        s.o[k][2] = fmaf(w0, v[k][1], s.o[k][2]);
+      }
+      if (w1 != 0.f) {
+        s.o[k][1] = fmaf(w1, v[k][0], s.o[k][1]);
+        s.o[k][3] = fmaf(w1, v[k][1], s.o[k][3]);
       }
     }
   }
@@ -577,10 +528,10 @@ __device__ __forceinline__ void team_sync(int team, int number) {
   }
 }
 
-template <int D, int NT, bool kE4m3, Kv8Mode kMode>
-__global__ void __launch_bounds__((Kv8Cfg<D, NT, kMode>::kThreads), (Kv8Cfg<D, NT, kMode>::kCtas))
+template <int D, bool kE4m3, Kv8Mode kMode>
+__global__ void __launch_bounds__((Kv8Cfg<D, kMode>::kThreads), (Kv8Cfg<D, kMode>::kCtas))
 kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
-  using C = Kv8Cfg<D, NT, kMode>;
+  using C = Kv8Cfg<D, kMode>;
   constexpr int kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -590,8 +541,8 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   const int number = kMode == kTeams ? (tid >> 5) / team : 0;
   const int warp = (tid >> 5) - number * team;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff) + number * team * 8 * NT;
-  float* sm_l = sm_m + kWarps * 8 * NT;
+  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff) + number * team * 8;
+  float* sm_l = sm_m + kWarps * 8;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
   if (tid < kWarps * C::kStages) mbar_init(bars + tid, 1);
   fence_mbar_init();
@@ -608,18 +559,18 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     if (unit >= static_cast<int64_t>(p.entries) * p.hkv) return;
     e = static_cast<int>(unit / p.hkv);
     h = static_cast<int>(unit - static_cast<int64_t>(e) * p.hkv);
-    t = entry_of<NT>(p, e);
+    t = entry_of<1>(p, e);
     end = t.pages;
   } else if constexpr (kMode == kCluster) {   // this CTA's run of the cluster's unit
     const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
     e = unit / p.hkv;
     h = unit - e * p.hkv;
-    t = entry_of<NT>(p, e);
+    t = entry_of<1>(p, e);
     at = static_cast<int64_t>(t.pages) * rank / p.cluster;
     end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
   } else {
     bool any;
-    const Share sh = find_share<NT, kWarps>(p, min_share, any);
+    const Share sh = find_share<1, kWarps>(p, min_share, any);
     if (!any) {
       if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
@@ -641,33 +592,34 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   start_part<C>(p, t, h, mine, team, lane, ring);
 
   for (;;) {
-    Query<D, NT> q;
-    load_query<D, NT, kE4m3>(p, t, h, lane, q);
-    Running<D, NT> s;
-    reset<D, NT>(s);
+    Query<D> q;
+    load_query<D, kE4m3>(p, t, h, lane, q);
+    Running<D> s;
+    reset<D>(s);
     if (p0 == 0 && h == 0 && t.tile == 0 && warp == 0 && lane == 0 && p.status) {
       const int len = p.seq_lens[t.b];
       if (len < 0 || len > p.max_len) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
-    if (p.q_pos && p0 == 0 && h == 0 && warp == 0 && lane < 8 * NT && p.status) {
-      const int row = (t.tile * 8 * NT + lane) / p.G;
+    if (p.q_pos && p0 == 0 && h == 0 && warp == 0 && lane < 8 && p.status) {
+      const int row = (t.tile * 8 + lane) / p.G;
       if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
         atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
     for (int pg = mine.first; pg < mine.end && ring.alive; pg += team) {
       int st;
       if (!copied<C>(p, ring, st)) break;
-      page<D, NT, kE4m3>(ring.base + st * C::F::kBlock, pg * kPage, (ring.shown >> st) & 1u, lane, q, s);
+      // (a refused id's stands for nothing, whatever it holds)
+      if ((ring.shown >> st) & 1u) page<D, kE4m3>(ring.base + st * C::F::kBlock, pg * kPage, lane, q, s);
       __syncwarp();
       if (pg + C::kStages * team < mine.end)
         issue<C>(p, t, h, pg + C::kStages * team, mine.end, team, lane, ring);
     }
-    unscale<D, NT, kE4m3>(s);
+    unscale<D, kE4m3>(s);
     if (mine.tail && ring.alive) {
       if (!ring.tail_issued) issue_tail<C>(p, t, h, lane, ring);
       int st;
       if (copied<C>(p, ring, st) && ((ring.shown >> st) & 1u))
-        tail_tokens<D, NT>(p, t, h, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q, s);
+        tail_tokens<D>(p, t, h, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q, s);
       __syncwarp();
     }
 
@@ -680,7 +632,7 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       unit0 = u0 + tc.pages;
       if (++h == p.hkv) {
         h = 0;
-        t = entry_of<NT>(p, ++e);
+        t = entry_of<1>(p, ++e);
       }
       p0 = 0;
       p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
@@ -689,66 +641,61 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     }
 
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = s.l[nt][c];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (gid == 0) {
-          sm_m[(warp * NT + nt) * 8 + 2 * tig + c] = s.m[nt][c];
-          sm_l[(warp * NT + nt) * 8 + 2 * tig + c] = l;
-        }
+    for (int c = 0; c < 2; ++c) {
+      float l = s.l[c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (gid == 0) {
+        sm_m[warp * 8 + 2 * tig + c] = s.m[c];
+        sm_l[warp * 8 + 2 * tig + c] = l;
       }
+    }
     team_sync<kMode>(team, number);
     const bool complete = c0 == 0 && c1 == tc.pages;
     float* slot = kMode == kCluster
         ? reinterpret_cast<float*>(smem + C::kPartOff)
         : p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * C::kSlot;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int c = 0; c < 2; ++c) {
+      float top = kLowest;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float top = kLowest;
+      for (int w = 0; w < kWarps; ++w)
+        if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[w * 8 + 2 * tig + c]);
+      const float a = fast_exp2(s.m[c] - top);
+      float* dst = merge + (warp * 8 + 2 * tig + c) * C::kStride + 4 * gid;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + 2 * tig + c]);
-        const float a = fast_exp2(s.m[nt][c] - top);
-        float* dst = merge + (warp * 8 + 2 * tig + c) * C::kStride + 4 * gid;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          *reinterpret_cast<float4*>(dst + 32 * i) =
-              make_float4(s.o[nt][2 * i][c] * a, s.o[nt][2 * i][2 + c] * a,
-                          s.o[nt][2 * i + 1][c] * a, s.o[nt][2 * i + 1][2 + c] * a);
-      }
-      team_sync<kMode>(team, number);
-      for (int i = warp * 32 + lane; i < 8 * D / 4; i += 32 * team) {
-        const int col = i / (D / 4), ch = 4 * (i % (D / 4));
-        const int gcol = (tc.tile * NT + nt) * 8 + col;
-        if (kMode != kCluster && gcol >= p.cols) continue;
-        float top = kLowest, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[(w * NT + nt) * 8 + col]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (kMode == kTeams && w >= team) break;
-          l = fmaf(sm_l[(w * NT + nt) * 8 + col], fast_exp2(sm_m[(w * NT + nt) * 8 + col] - top), l);
-          const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
-          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
-        }
-        if (kMode != kCluster && (kMode == kTeams || complete)) {
-          store_row(p, tc.b, hc, gcol, ch, D, o, l);
-        } else {
-          *reinterpret_cast<float4*>(slot + (nt * 8 + col) * D + ch) = o;
-          if (ch == 0)
-            *reinterpret_cast<float2*>(slot + 8 * NT * D + 2 * (nt * 8 + col)) = make_float2(top, l);
-        }
-      }
-      if (kMode != kTeams) __syncthreads();   // before the buffers are written again
+      for (int i = 0; i < D / 32; ++i)
+        *reinterpret_cast<float4*>(dst + 32 * i) =
+            make_float4(s.o[2 * i][c] * a, s.o[2 * i][2 + c] * a,
+                        s.o[2 * i + 1][c] * a, s.o[2 * i + 1][2 + c] * a);
     }
+    team_sync<kMode>(team, number);
+    for (int i = warp * 32 + lane; i < 8 * D / 4; i += 32 * team) {
+      const int col = i / (D / 4), ch = 4 * (i % (D / 4));
+      const int gcol = tc.tile * 8 + col;
+      if (kMode != kCluster && gcol >= p.cols) continue;
+      float top = kLowest, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[w * 8 + col]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (kMode == kTeams && w >= team) break;
+        l = fmaf(sm_l[w * 8 + col], fast_exp2(sm_m[w * 8 + col] - top), l);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
+        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+      }
+      if (kMode != kCluster && (kMode == kTeams || complete)) {
+        store_row(p, tc.b, hc, gcol, ch, D, o, l);
+      } else {
+        *reinterpret_cast<float4*>(slot + col * D + ch) = o;
+        if (ch == 0)
+          *reinterpret_cast<float2*>(slot + 8 * D + 2 * col) = make_float2(top, l);
+      }
+    }
+    if (kMode != kTeams) __syncthreads();   // before the buffers are written again
     if constexpr (kMode == kCluster) {
       merge_cluster<D>(p, tc, hc, slot);
       return;
@@ -763,10 +710,10 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 
 // Merges the units that lie in several CTAs.  Block: (CTA in which the unit starts, columns);
 // kSplit warps share the parts of a column, a lane has D / 32 channels.
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
   constexpr int kSplit = 4;   // warps of a column: few columns, with many parts each
-  constexpr int kSlot = kv8_slot<D, NT>(), kPer = D / 32;
+  constexpr int kSlot = kv8_slot<D, 1>(), kPer = D / 32;
   __shared__ float partial[8][D];
   pdl_wait();
   pdl_trigger();
@@ -775,8 +722,8 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
   if (n == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kSplit;
   const int b = own.x / p.tiles, tile = own.x - b * p.tiles;
-  const int col = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 * NT + col;
-  const bool live = col < 8 * NT && gcol < p.cols;
+  const int col = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 + col;
+  const bool live = col < 8 && gcol < p.cols;
   float acc[kPer] = {};
   float l = 0.f;
   if (live) {
@@ -785,7 +732,7 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
       return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
     };
     auto stats = [&](int j) {   // (maximum, sum) of part j
-      return j < n ? *reinterpret_cast<const float2*>(slot(j) + 8 * NT * D + 2 * col) : make_float2(kLowest, 0.f);
+      return j < n ? *reinterpret_cast<const float2*>(slot(j) + 8 * D + 2 * col) : make_float2(kLowest, 0.f);
     };
     float top = kLowest;
     for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(j).x);
@@ -830,53 +777,61 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 }
 
 // The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns
-// each: a lane per column, a warp per 16 channels.
+// each: a lane per column, a warp per 8 channels, eight parts in flight.
 template <int D>
-__global__ void __launch_bounds__(2 * D) kv8_merge_rows_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int kSlot = kv8_slot<D, kRowsNT>();
+__global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int kSlot = kv8_slot<D, kRowsNT>(), kFlight = 8;
   pdl_wait();
   pdl_trigger();
   const int4 own = p.info[blockIdx.x];
   const int n = own.z;
   if (n == 0) return;
-  const int ch = 16 * (threadIdx.x >> 5), col = 32 * blockIdx.y + (threadIdx.x & 31);
+  const int ch = 8 * (threadIdx.x >> 5), col = 32 * blockIdx.y + (threadIdx.x & 31);
   const int b = own.x / p.tiles, tile = own.x - b * p.tiles, gcol = tile * 128 + col;
   if (gcol >= p.cols) return;
-  // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
-  auto slot = [&](int j) {
-    return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
-  };
-  auto stats = [&](int j) { return *reinterpret_cast<const float2*>(slot(j) + 128 * D + 2 * col); };
-  float top = kLowest;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) top = fmaxf(top, stats(j).x);
-  float acc[16] = {};
-  float l = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const float2 ml = stats(j);
-    const float* x = slot(j) + 128 * ch + 4 * col;
-    float4 v[4];
+  float acc[8] = {};
+  float top = kLowest, l = 0.f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += kFlight) {
+    float2 ml[kFlight];
+    float4 v[kFlight][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4*>(x + 512 * k);
-    const float w = fast_exp2(ml.x - top);
-    l = fmaf(w, ml.y, l);
+    for (int j = 0; j < kFlight; ++j) {
+      // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
+      const int part = min(j0 + j, n - 1);
+      const float* slot = p.part + (2 * (blockIdx.x + static_cast<size_t>(part)) + (part == 0 ? 1 : 0)) * kSlot;
+      ml[j] = *reinterpret_cast<const float2*>(slot + 128 * D + 2 * col);
+      v[j][0] = *reinterpret_cast<const float4*>(slot + 128 * ch + 4 * col);
+      v[j][1] = *reinterpret_cast<const float4*>(slot + 128 * ch + 512 + 4 * col);
+    }
+    float high = top;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
-      acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
-      acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
-      acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
+    for (int j = 0; j < kFlight; ++j) high = fmaxf(high, ml[j].x);
+    const float old = fast_exp2(top - high);
+    top = high;
+    l *= old;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= old;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      if (j0 + j >= n) break;
+      const float w = fast_exp2(ml[j].x - top);
+      l = fmaf(w, ml[j].y, l);
+      acc[0] = fmaf(w, v[j][0].x, acc[0]);
+      acc[1] = fmaf(w, v[j][0].y, acc[1]);
+      acc[2] = fmaf(w, v[j][0].z, acc[2]);
+      acc[3] = fmaf(w, v[j][0].w, acc[3]);
+      acc[4] = fmaf(w, v[j][1].x, acc[4]);
+      acc[5] = fmaf(w, v[j][1].y, acc[5]);
+      acc[6] = fmaf(w, v[j][1].z, acc[6]);
+      acc[7] = fmaf(w, v[j][1].w, acc[7]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int row = gcol / p.G, g = gcol - row * p.G;
-  uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + ch;
-#pragma unroll
-  for (int k = 0; k < 16; k += 8)
-    *reinterpret_cast<uint4*>(dst + k) =
-        make_uint4(pack_bf162(acc[k] * inv, acc[k + 1] * inv), pack_bf162(acc[k + 2] * inv, acc[k + 3] * inv),
-                   pack_bf162(acc[k + 4] * inv, acc[k + 5] * inv), pack_bf162(acc[k + 6] * inv, acc[k + 7] * inv));
+  *reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + ch) =
+      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
+                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
 }
 
 template <typename Kern, typename... Args>
@@ -898,10 +853,6 @@ cudaError_t launch_kv8(Kern kernel, int cluster, dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Query columns of a unit in tiles of 8: 1 or 2, the fewest that hold a KV head's
-// columns, and beyond them units of 128 (kv8_rows.cu).
-inline int column_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : kRowsNT; }
-
 constexpr int kMinShare = 8;      // pages of a CTA: one per warp, or a tile of 128 tokens
 constexpr int kMaxCluster = 16;
 constexpr int kTeamPages = 128;
@@ -914,8 +865,8 @@ struct ClusterSizes {
 
 // (The kernel for d = 128 stands for all: every cluster kernel fills an SM.)
 ClusterSizes count_clusters() {
-  using C = Kv8Cfg<128, 1, kCluster>;
-  const auto kernel = kv8_attention_kernel<128, 1, false, kCluster>;
+  using C = Kv8Cfg<128, kCluster>;
+  const auto kernel = kv8_attention_kernel<128, false, kCluster>;
   ClusterSizes s{};
   if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) return s;
   for (int c = 1; c <= kMaxCluster; ++c) {
@@ -956,28 +907,46 @@ ClusterSizes cluster_sizes() {
 }
 
 struct Kv8Plan {
-  int nt, cluster, team;   // cluster > 0: CTAs per unit; team > 0: warps per unit
+  bool rows;           // tiles of 128 columns (kv8_rows.cu), else of 8
+  int cluster, team;   // cluster > 0: CTAs per unit; team > 0: warps per unit
   int64_t tiles, entries, ctas;
   size_t info, total;   // workspace bytes: the CTAs' records, all
 };
 
-// Clusters or shares.  The largest cluster of which the device holds one per unit at a
-// time; its CTA streams its pages at 0.06 us each (d = 128).  Shares run at the memory's
-// rate, 0.00064 us a page over all units, but only over the tokens there are (several
-// sequences: taken as three quarters of the longest, the host does not know the
-// lengths), and cost a second
-// kernel and longer first and last waves, 6 us.  Measured, 8 KV heads: one sequence of
-// 32k 18.6 us against 23.9, of 128k 48.7 against 54.
-inline int cluster_of(int64_t batch, int64_t units, int64_t pages) {
+// Several sequences are taken as three quarters of the longest: the host does not know the
+// lengths.
+inline double visited(int64_t batch, int64_t units, int64_t pages) {
+  return (batch > 1 ? 0.75 : 1.0) * static_cast<double>(units) * static_cast<double>(pages);
+}
+
+// Estimates in us.  Tiles of 8 columns: shares run at the memory's rate, 0.00064 us a page over
+// all units (d = 128), and cost a second kernel and longer first and last waves, 6 us; a
+// cluster's CTA streams its pages at 0.06 us each.
+inline double shares_us(int d, int64_t batch, int64_t units, int64_t pages) {
+  return 6.0 + (0.00036 + 0.00028 / 128 * d) * visited(batch, units, pages);
+}
+inline double cluster_us(int d, int64_t pages, int c) {
+  return (0.04 + 0.02 / 128 * d) * static_cast<double>(pages) / c;
+}
+
+// Tiles of 128: a start of 24 us (18 for d = 64), 0.08 us for each unit, 0.15 us for each of
+// the CTAs that a unit is spread over, whose parts are merged, and 0.001 us a page.
+inline double rows_us(int d, int64_t batch, int64_t units, int64_t pages, int64_t sms) {
+  return 12.0 + 12.0 / 128 * d + 0.08 * static_cast<double>(units) +
+         0.15 * static_cast<double>(std::min(sms / units, pages / kMinShare)) +
+         (0.00065 + 0.00038 / 128 * d) * visited(batch, units, pages);
+}
+
+// The largest cluster of which the device holds one per unit at a time; 0: shares are faster,
+// as they touch only the tokens there are, or there is none.  Measured, 8 KV heads: one
+// sequence of 32k 18.6 us against 23.9, of 128k 48.7 against 54.
+inline int cluster_of(int d, int64_t batch, int64_t units, int64_t pages) {
   const ClusterSizes s = cluster_sizes();
   int c = kMaxCluster;
   while (c > 0 && s.active[c] < units) --c;
   if (c == 0) return 0;
   c = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c, pages / 8)));   // half the warps busy
-  const double alone = 0.06 * static_cast<double>(pages) / c;
-  const double ragged = batch > 1 ? 0.75 : 1.0;
-  const double shared = 6.0 + 0.00064 * ragged * static_cast<double>(units) * static_cast<double>(pages);
-  return alone < shared ? c : 0;
+  return cluster_us(d, pages, c) < shares_us(d, batch, units, pages) ? c : 0;
 }
 
 // Warps per unit where units are many and short: as many as give every warp slot of the
@@ -997,35 +966,36 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
                      Kv8Plan* out) {
   Kv8Plan p{};
   const int64_t cols = m_rows * (c->num_q_heads / c->num_kv_heads);
-  p.nt = column_tiles(cols);
-  p.tiles = (cols + 8 * p.nt - 1) / (8 * p.nt);
-  p.entries = batch * p.tiles;
-  if (cols > (1 << 30) || p.entries > (1 << 30) || p.entries * c->num_kv_heads > 0x7fffffff)
+  const int64_t tiles8 = (cols + 7) / 8, tiles128 = (cols + 127) / 128;
+  if (cols > (1 << 30) || batch * tiles8 > (1 << 30) || batch * tiles8 * c->num_kv_heads > 0x7fffffff)
     return false;
-  const int64_t units = p.entries * c->num_kv_heads;
+  const int d = c->head_dim, h = c->num_kv_heads;
   const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);
-  const int64_t resident =
-      std::min<int64_t>(kMaxCtas, oscar_host::sm_count() * static_cast<int64_t>(p.nt == 1 ? 2 : 1));
-  if (p.nt == 1) {
-    p.team = team_of(units, pages, oscar_host::sm_count());
-    if (!p.team) p.cluster = cluster_of(batch, units, pages);
-  }
+  const int64_t sms = oscar_host::sm_count(), units8 = batch * tiles8 * h;
+  p.team = team_of(units8, pages, sms);
+  if (!p.team) p.cluster = cluster_of(d, batch, units8, pages);
+  const double narrow = p.cluster ? 6.0 + cluster_us(d, pages, p.cluster) : shares_us(d, batch, units8, pages);
+  p.rows = cols > 8 && rows_us(d, batch, batch * tiles128 * h, pages, sms) < narrow;
+  if (p.rows) p.team = p.cluster = 0;
+  p.tiles = p.rows ? tiles128 : tiles8;
+  p.entries = batch * p.tiles;
+  const int64_t units = p.entries * h;
+  const int64_t resident = std::min<int64_t>(kMaxCtas, p.rows ? sms : 2 * sms);
   p.ctas = p.team      ? (units * p.team + 7) / 8
            : p.cluster ? units * p.cluster
                        : std::min(resident, (units * pages + kMinShare - 1) / kMinShare);
-  const int d = c->head_dim;
   p.info = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
   p.total = p.cluster || p.team
                 ? 16
-                : p.info + static_cast<size_t>(p.ctas) * 2 * 8 * p.nt * (d + 2) * sizeof(float);
+                : p.info + static_cast<size_t>(p.ctas) * 2 * (p.rows ? 128 : 8) * (d + 2) * sizeof(float);
   *out = p;
   return true;
 }
 
-template <int D, int NT, bool kE4m3, Kv8Mode kMode>
+template <int D, bool kE4m3, Kv8Mode kMode>
 oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  using C = Kv8Cfg<D, NT, kMode>;
-  const auto kernel = kv8_attention_kernel<D, NT, kE4m3, kMode>;
+  using C = Kv8Cfg<D, kMode>;
+  const auto kernel = kv8_attention_kernel<D, kE4m3, kMode>;
   if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, kMode == kCluster))
     return OSCAR_ERR_CUDA;
   return launch_kv8(kernel, kMode == kCluster ? pl.cluster : 1, dim3(static_cast<unsigned>(pl.ctas)),
@@ -1033,28 +1003,25 @@ oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_
              ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-template <int D, int NT>
+template <int D>
 oscar_status launch_merge(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
   const unsigned ctas = static_cast<unsigned>(pl.ctas);
   cudaError_t e;
-  if constexpr (NT == kRowsNT)
-    e = launch_kv8(kv8_merge_rows_kernel<D>, 1, dim3(ctas, (std::min(p.cols, 128) + 31) / 32), 2 * D, 0, st, p);
+  if (pl.rows)
+    e = launch_kv8(kv8_merge_rows_kernel<D>, 1, dim3(ctas, (std::min(p.cols, 128) + 31) / 32), 4 * D, 0, st, p);
   else   // four warps a column
-    e = launch_kv8(kv8_merge_kernel<D, NT>, 1, dim3(ctas, (std::min(p.cols, 8 * NT) + 1) / 2), 256, 0, st, p);
+    e = launch_kv8(kv8_merge_kernel<D>, 1, dim3(ctas, (std::min(p.cols, 8) + 1) / 2), 256, 0, st, p);
   return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 template <int D, bool kE4m3>
 oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  if (pl.team) return launch_attention<D, 1, kE4m3, kTeams>(p, pl, st);
-  if (pl.cluster) return launch_attention<D, 1, kE4m3, kCluster>(p, pl, st);
-  const oscar_status s = pl.nt == 1   ? launch_attention<D, 1, kE4m3, kShares>(p, pl, st)
-                         : pl.nt == 2 ? launch_attention<D, 2, kE4m3, kShares>(p, pl, st)
-                                      : run_kv8_rows(p, D, kE4m3, pl.ctas, kMinShare, st);
+  if (pl.team) return launch_attention<D, kE4m3, kTeams>(p, pl, st);
+  if (pl.cluster) return launch_attention<D, kE4m3, kCluster>(p, pl, st);
+  const oscar_status s = pl.rows ? run_kv8_rows(p, D, kE4m3, pl.ctas, kMinShare, st)
+                                 : launch_attention<D, kE4m3, kShares>(p, pl, st);
   if (s != OSCAR_OK) return s;
-  return pl.nt == 1   ? launch_merge<D, 1>(p, pl, st)
-         : pl.nt == 2 ? launch_merge<D, 2>(p, pl, st)
-                      : launch_merge<D, kRowsNT>(p, pl, st);
+  return launch_merge<D>(p, pl, st);
 }
 
 }  // namespace oscar

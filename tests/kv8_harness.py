@@ -94,9 +94,22 @@ class Sequences:
         bad = np.argwhere(got != want)
         assert len(bad) == 0, (len(bad), bad[:5], got[tuple(bad[0])], want[tuple(bad[0])])
 
-    def attend(self, q, q_pos=None, max_len=None, lens=None, ws=None, stream=None):
-        """The library's output as float64, [B, M, Hq, d] (M = 1 for a decode step)."""
+    def attend(self, q, q_pos=None, max_len=None, lens=None, ws=None, stream=None, wide=0):
+        """The library's output as float64, [B, M, Hq, d] (M = 1 for a decode step).
+        wide: with a page table of that many columns, and lengths up to it announced: what
+        the library takes for a long context, and tiles of 128 query columns for."""
         t, L = H.torch(), H.lib()
+        if wide:
+            table = self.cache.page_table
+            self.cache.page_table = t.full((self.b, wide), -1, dtype=t.int32, device=H.DEV)
+            self.cache.page_table[:, :self.max_pages] = table
+            if q_pos is not None and q_pos.shape[1] * self.hq // self.hkv > 8:
+                size = L.oscar_kv8_workspace_size(self.cache, self.b, q_pos.shape[1], 16 * wide)
+                assert size > 5 << 20   # partial results of 128 columns
+            try:
+                return self.attend(q, q_pos, 16 * wide, lens, ws, stream)
+            finally:
+                self.cache.page_table = table
         lens = self.lens if lens is None else np.asarray(lens)
         m = 1 if q_pos is None else q_pos.shape[1]
         max_len = max(1, int(lens.max())) if max_len is None else max_len

@@ -11,6 +11,7 @@ from oracle import kv8
 pytestmark = pytest.mark.gpu
 
 FMTS = [kv8.INT8, kv8.E4M3]
+WIDE = [0, 131072]   # see kv8_harness.Sequences.attend
 
 
 # ---------------------------------------------------------------------- placing
@@ -142,10 +143,11 @@ def test_decode_matches_oracle(fmt, d, hkv, g):
         s.check_attention(s2, q, lens=one, heads={(b, h) for h in range(hkv)})
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d,hkv,g,m", [(64, 1, 4, 2), (128, 2, 4, 3), (128, 1, 1, 11), (128, 2, 4, 9),
                                        (64, 2, 8, 5), (128, 1, 3, 37)])
-def test_rows_match_oracle(fmt, d, hkv, g, m):
+def test_rows_match_oracle(fmt, d, hkv, g, m, wide):
     """Several rows: the last positions, positions all over the context in no order,
     rows that see nothing, and rows behind the end (zeros, reported)."""
     lens = [40, 0, 555, 1700]
@@ -156,20 +158,21 @@ def test_rows_match_oracle(fmt, d, hkv, g, m):
     pos[1] = -1
     pos[2] = s.rng.integers(0, 555, m)
     pos[2, 0], pos[2, 1] = 0, -5
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     s.check_attention(got, q, pos)
     assert (got[1] == 0).all() and (got[2, 1] == 0).all()
     assert H.status(s.cache) == 0
     pos[3, 0] = 1700
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     assert (got[3, 0] == 0).all() and H.status(s.cache) == H.lib().DEVERR_SEQ_LEN
     s.check_attention(got, q, pos)
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d,hkv,g,m", [(128, 2, 1, 17), (64, 1, 2, 64), (128, 1, 4, 33), (128, 1, 2, 130),
                                        (64, 3, 8, 18)])
-def test_many_rows_match_oracle(fmt, d, hkv, g, m):
+def test_many_rows_match_oracle(fmt, d, hkv, g, m, wide):
     """More query columns than the decode form holds, one tile of 128 and several: every
     number of pages in the last tile of tokens, with and without a tail behind it, rows at
     the end, all over, and padded."""
@@ -182,7 +185,7 @@ def test_many_rows_match_oracle(fmt, d, hkv, g, m):
     pos = np.array([[L - m + i for i in range(m)] for L in lens])
     pos[pos < 0] = -1
     pos[10] = s.rng.integers(0, 1333, m)
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     assert (got[pos < 0] == 0).all()
     # all the short sequences, and of the long ones every third row
     s.check_attention(got[:10], q[:10], pos[:10], lens=np.array(lens[:10]))
@@ -192,10 +195,11 @@ def test_many_rows_match_oracle(fmt, d, hkv, g, m):
     s.check_attention(some, q, thin, heads={(i, h) for i in (10, 11, 12) for h in range(hkv)})
     assert H.status(s.cache) == 0
     pos[0, 0] = 5
-    assert (s.attend(q, pos)[0, 0] == 0).all() and H.status(s.cache) == H.lib().DEVERR_SEQ_LEN
+    assert (s.attend(q, pos, wide=wide)[0, 0] == 0).all() and H.status(s.cache) == H.lib().DEVERR_SEQ_LEN
 
 
-def test_many_rows_with_odd_tails_and_bad_pages():
+@pytest.mark.parametrize("wide", WIDE)
+def test_many_rows_with_odd_tails_and_bad_pages(wide):
     """NaN and infinities in the tail reach the rows that see them only; refused pages and
     tails are left out and reported."""
     t, L = H.torch(), H.lib()
@@ -205,7 +209,7 @@ def test_many_rows_with_odd_tails_and_bad_pages():
     s.place([90, 650], k, v)
     pos = np.array([[79, 84, 85, 86, 87, 88, 89, 80, -1] * 3, np.arange(650 - 27, 650)])
     q = K.queries(s.rng, 2, 27, 2, 64)
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     for i in (0, 9, 18):
         assert np.isfinite(got[0, [i, i + 1, i + 7, i + 8]]).all()
         assert np.isnan(got[0, i + 2, :, 7]).all() and np.isfinite(np.delete(got[0, i + 2], 7, -1)).all()
@@ -217,13 +221,13 @@ def test_many_rows_with_odd_tails_and_bad_pages():
     s.check_attention(clean, q, seen)
     s.cache.page_table[1, 3] = -1
     s.cache.page_table[1, 33] = s.cache.pool.shape[0]
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     assert H.status(s.cache) == L.DEVERR_PAGE_ID
     s.check_attention(got, q, pos, drop=(3, 33), heads={(1, 0)})
     s.cache.page_table.copy_(t.from_numpy(s.table))
     s.cache.status.zero_()
     s.cache.tail_ids = s.i32([0, -1])
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     assert H.status(s.cache) == L.DEVERR_PAGE_ID
     s.check_attention(got, q, pos, drop=(40,), heads={(1, 0)})
 
@@ -270,9 +274,10 @@ def test_every_split_of_the_work(fmt, batch, hkv, d, lo, hi):
     assert H.status(s.cache) == 0
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m", [1, 3, 6])
-def test_scales_of_values_and_queries(fmt, m):
+def test_scales_of_values_and_queries(fmt, m, wide):
     """Value scales that differ by 2^20 from page to page, in both directions; queries from
     1e-20 to 1e4 (logits to saturation); each form of the kernel."""
     s = K.Sequences(2, 1, 4, 128, fmt, 1500, seed=9)
@@ -284,13 +289,14 @@ def test_scales_of_values_and_queries(fmt, m):
     for scale in (1e-20, 1.0, 1e4):
         q = K.queries(s.rng, 2, m, 4, 128, scale)
         pos = None if m == 1 else np.array([[1500 - m + i for i in range(m)], [900 - m + i for i in range(m)]])
-        s.check_attention(s.attend(q, pos), q, pos)
+        s.check_attention(s.attend(q, pos, wide=wide), q, pos)
     s.check_pools()
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m", [1, 3, 40])
-def test_pages_of_zeros_among_small_values(fmt, m):
+def test_pages_of_zeros_among_small_values(fmt, m, wide):
     """Values of 1e-5 beside pages, and a tail, whose values are all zero: the zeros' weights
     count, and take no precision from the others."""
     s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=m)
@@ -304,11 +310,12 @@ def test_pages_of_zeros_among_small_values(fmt, m):
     s.place(n, k, v)
     q = K.queries(s.rng, 3, m, 4, 128)
     pos = None if m == 1 else np.stack([np.arange(x - m, x) for x in n])
-    s.check_attention(s.attend(q, pos), q, pos)
+    s.check_attention(s.attend(q, pos, wide=wide), q, pos)
     assert H.status(s.cache) == 0
 
 
-def test_a_token_that_a_row_does_not_see_does_not_reach_it():
+@pytest.mark.parametrize("wide", WIDE)
+def test_a_token_that_a_row_does_not_see_does_not_reach_it(wide):
     """NaN and infinity in the tail: rows before them keep finite outputs, rows behind
     them get what the softmax gives."""
     s = K.Sequences(1, 1, 2, 64, kv8.INT8, 100)
@@ -317,7 +324,7 @@ def test_a_token_that_a_row_does_not_see_does_not_reach_it():
     s.place([90], k, v)
     pos = np.array([[79, 84, 85, 86, 87, 88, 89, 80, -1]])
     q = K.queries(s.rng, 1, 9, 2, 64)
-    got = s.attend(q, pos)
+    got = s.attend(q, pos, wide=wide)
     assert np.isfinite(got[0, [0, 1, 7, 8]]).all()
     assert np.isnan(got[0, 2, :, 7]).all() and np.isfinite(np.delete(got[0, 2], 7, -1)).all()
     assert np.isinf(got[0, 3, :, 9]).all() and np.isnan(got[0, 5]).all()
@@ -365,6 +372,47 @@ def test_bad_pages_and_lengths_are_reported_and_left_out():
     assert H.status(s.cache) == L.DEVERR_SEQ_LEN and (got == 0).all()
     s.cache.status.zero_()
     np.testing.assert_array_equal(s.attend(q), good)
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("m", [1, 3, 200])
+def test_a_refused_page_is_left_out_whatever_page_0_holds(m, wide):
+    """Codes and scales of all ones (NaN in e4m3 and in fp32) in page 0, ids out of range."""
+    s = K.Sequences(1, 2, 8, 128, kv8.E4M3, 800, seed=7)
+    s.place([733])
+    drop = sorted({3, 40} | set(np.flatnonzero(s.table[0] == 0).tolist()))
+    s.cache.pool[0].fill_(0xFF)
+    table = s.table.copy()
+    table[0, drop] = [-1, len(s.ids), -7][:len(drop)]
+    s.cache.page_table.copy_(H.torch().from_numpy(table))
+    s.cache.status = s.i32([0])
+    q = K.queries(s.rng, 1, m, 8, 128)
+    pos = None if m == 1 else np.arange(733 - m, 733)[None]
+    s.check_attention(s.attend(q, pos, wide=wide), q, pos, drop=drop)
+    assert H.status(s.cache) == H.lib().DEVERR_PAGE_ID
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("b,m,d,hkv,g,lo,hi", [
+    (1, 7, 128, 2, 4, 900, 900),       # clusters, several tiles of 8 columns
+    (3, 5, 64, 2, 8, 100, 400),
+    (1, 50, 128, 2, 4, 500, 500),      # teams
+    (20, 4, 128, 4, 4, 30, 300),
+    (30, 6, 64, 1, 4, 1500, 3000),     # shares
+])
+def test_several_tiles_of_eight_columns(fmt, b, m, d, hkv, g, lo, hi, wide):
+    """Rows that fill several narrow tiles, the last one partly, in each division of the work."""
+    s = K.Sequences(b, hkv, hkv * g, d, fmt, hi, seed=b + m)
+    n = s.rng.integers(lo, hi + 1, b)
+    s.place(n)
+    q = K.queries(s.rng, b, m, hkv * g, d)
+    pos = np.maximum(n[:, None] - m + np.arange(m), -1)
+    pos[0, -1] = -1                    # a padded row
+    pos[-1, 0] = n[-1] - 1             # and one out of order
+    got = s.attend(q, pos, wide=wide)
+    s.check_attention(got, q, pos)
+    assert not got[0, -1].any() and H.status(s.cache) == 0
 
 
 def test_page_offsets_beyond_4_gib():
