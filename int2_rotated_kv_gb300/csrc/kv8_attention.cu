@@ -20,8 +20,9 @@
 // Softmax statistics, accumulators and the merges are fp32.  Tail tokens are exact
 // in bf16 on the K side and use fp32 p on the V side.
 //
-// Work split, by what there is of (sequence, tile of query columns, KV head) units,
-// each a run of pages (kv8_plan has the rule):
+// Work split, by what there is of units, each a run of pages (kv8_plan has the rule).
+// A unit is (sequence, 8 query columns, KV head), or 128 columns where the estimates of
+// kv8_plan find that faster (kv8_rows.cu).
 //   - many short units: a team of 1, 2, 4 or 8 warps per unit.
 //   - few units, moderate lengths: a thread-block cluster per unit.  Each of its CTAs
 //     (16 warps, one CTA per SM) takes an equal run of the unit's pages, and the CTAs
@@ -35,7 +36,10 @@
 // and merge through shared memory at a unit's end; the ring already fills for the
 // next unit meanwhile.
 //
-// Bound by HBM: 2d + 1 bytes per token and KV head.
+// Bound by HBM: 2d + 1 bytes per token and KV head.  Measured, 8 KV heads, d = 128: 64
+// sequences of 4096-8192 tokens 135 us, 5990 GB/s (shares); one of 131071 tokens 48 us, 5610
+// GB/s (clusters of 16 for 7 heads would leave one for a second round, so 12; 96 of 152 SMs);
+// one of 32768 18.7 us, 3600 GB/s, of which 5 us are the launch, the first pages and the merge.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -9,7 +9,11 @@
 // One warp does one (page, KV head, keys or values): its 16 x d values are read
 // once into registers (all loads in flight before the first use), reduced, coded
 // and stored as 16-byte chunks.  Bound by HBM: 2 bytes read and 1 written per value
-// (place), 1 read and 2 written (gather).
+// (place), 1 read and 2 written (gather).  Measured, 32 prompts of 3001-4096 tokens, 8 KV
+// heads, d = 128, e4m3: placing and reading back 1.39 GB in 216 us, 6450 GB/s.  What it takes
+// is loads in flight: small CTAs, and 64 registers a thread for 32 warps an SM (CTAs of 8
+// warps at 80 registers: 235 us; at 48 registers the calls of one token take longer, 10.3 us
+// for 9.4).  One token a sequence: latency, a chain of lengths, tail and codes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,7 +21,7 @@
 
 namespace oscar {
 
-constexpr int kCWarps = 8;
+constexpr int kCWarps = 4;
 
 struct Kv8CacheParams {
   int hkv, max_pages, batch, pages_per_seq, max_rows;
@@ -249,11 +253,11 @@ __device__ __forceinline__ void store_tail(const Kv8CacheParams& p, const Span& 
   }
 }
 
-// blockIdx.x: (sequence, page of its rows), blockIdx.y: eight (KV head, K/V) each.
+// blockIdx.x: (sequence, page of its rows), blockIdx.y: kCWarps (KV head, K/V) each.
 // The warp of a sequence's first page also writes the tail: the first page may
 // take tokens from the tail that the last ones are about to overwrite.
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(32 * kCWarps) kv8_place_kernel(const __grid_constant__ Kv8CacheParams p) {
+__global__ void __launch_bounds__(32 * kCWarps, 8) kv8_place_kernel(const __grid_constant__ Kv8CacheParams p) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, unit = blockIdx.y * kCWarps + (threadIdx.x >> 5);
@@ -389,7 +393,7 @@ oscar_status cache_params(const oscar_kv8_desc* c, const int32_t* first, const i
   if (total_rows > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;   // row_starts are int32
   // pages that max_rows consecutive positions can touch
   const int64_t pages = (static_cast<int64_t>(max_rows) + kPage - 2) / kPage + 1;
-  if (pages * batch > 0x7fffffff || c->num_kv_heads > 4 * 65535) return OSCAR_ERR_UNSUPPORTED;
+  if (pages * batch > 0x7fffffff || c->num_kv_heads > kCWarps * 65535 / 2) return OSCAR_ERR_UNSUPPORTED;
   p->hkv = c->num_kv_heads;
   p->max_pages = c->max_pages_per_seq;
   p->batch = batch;
