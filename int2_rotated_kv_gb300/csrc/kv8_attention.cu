@@ -781,10 +781,11 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 }
 
 // The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns
-// each: a lane per column, a warp per 8 channels, eight parts in flight.
+// each: a lane per column, a warp per 8 channels, four parts in flight (eight: 2 us more where a
+// unit has few).
 template <int D>
 __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int kSlot = kv8_slot<D, kRowsNT>(), kFlight = 8;
+  constexpr int kSlot = kv8_slot<D, kRowsNT>(), kFlight = 4;
   pdl_wait();
   pdl_trigger();
   const int4 own = p.info[blockIdx.x];
@@ -802,7 +803,10 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
       // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
-      const int part = min(j0 + j, n - 1);
+      const int part = j0 + j;
+      ml[j] = make_float2(kLowest, 0.f);
+      v[j][0] = v[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (part >= n) continue;
       const float* slot = p.part + (2 * (blockIdx.x + static_cast<size_t>(part)) + (part == 0 ? 1 : 0)) * kSlot;
       ml[j] = *reinterpret_cast<const float2*>(slot + 128 * D + 2 * col);
       v[j][0] = *reinterpret_cast<const float4*>(slot + 128 * ch + 4 * col);
@@ -818,7 +822,6 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
     for (int k = 0; k < 8; ++k) acc[k] *= old;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
-      if (j0 + j >= n) break;
       const float w = fast_exp2(ml[j].x - top);
       l = fmaf(w, ml[j].y, l);
       acc[0] = fmaf(w, v[j][0].x, acc[0]);
@@ -857,7 +860,9 @@ cudaError_t launch_kv8(Kern kernel, int cluster, dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-constexpr int kMinShare = 8;      // pages of a CTA: one per warp, or a tile of 128 tokens
+// Pages of a CTA's share, at least and a multiple of: one per warp, or a tile of 128 tokens.
+// (16: 64 long sequences 133.3 us for 134.3, 36 columns over 40 sequences 83.6 for 82.3; 32: 87.9.)
+constexpr int kMinShare = 8;
 constexpr int kMaxCluster = 16;
 constexpr int kTeamPages = 128;
 

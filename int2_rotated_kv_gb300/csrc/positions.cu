@@ -43,7 +43,9 @@ inline cudaLaunchConfig_t pdl_config(dim3 grid, dim3 block, size_t smem, cudaStr
 
 constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
-constexpr int64_t kInlineRows = 2048;   // see oscar_extend_pages
+// Rows that the scan's CTA writes itself.  Itself against a grid of its own: 256 rows 4.7 us
+// against 7.2, 2048 rows 4.6 against 6.2, 4096 rows 5.5 against 6.0, 8192 rows 7.6 against 6.5.
+constexpr int64_t kInlineRows = 4096;
 
 struct PagesParams {
   int batch, max_pages, hold;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_scan_kernel(const __grid_
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cursor = *p.cursor;   // read before page_starts, which may hold it, is written
-  // totals before this round; a cursor that cannot be used, or has run past the list, gives no page
+  // totals before this turn; a cursor that cannot be used, or has run past the list, gives no page
   int64_t rows = 0, pages = cursor < 0 ? p.n_free : min(cursor, p.n_free);
   bool refused = cursor < 0;
   for (int b0 = 0; b0 < p.batch; b0 += kScanThreads) {
