@@ -486,6 +486,49 @@ def test_calls_on_two_streams_with_their_own_workspaces():
         np.testing.assert_array_equal(H.from_bf16(o), want[:, 0])
 
 
+def test_wide_tiles_on_two_streams_and_from_a_graph():
+    """Tiles of 128 columns: the same bits from two streams at once and from a graph, and a
+    replay after lengths, positions and queries changed."""
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(4, 8, 32, 128, kv8.INT8, 3100, seed=9)
+    s.place([3000, 1111, 2048, 17])
+    q = K.queries(s.rng, 4, 65, 32, 128)
+    pos = np.maximum(s.lens[:, None] - 65 + np.arange(65), -1)
+    size = L.oscar_kv8_workspace_size(s.cache, 4, 65, 3100)
+    assert size > 5 << 20
+    want = s.attend(q, pos, max_len=3100)
+    some = {(0, 1), (1, 7), (2, 0), (3, 5)}
+    s.check_attention(want, q, pos, heads=some)
+    qt, lens, at = H.bf16_tensor(q), s.i32(s.lens), s.i32(pos)
+    streams = [t.cuda.Stream() for _ in range(2)]
+    outs = [t.zeros_like(qt) for _ in range(6)]
+    spaces = [t.empty(size, dtype=t.uint8, device=H.DEV) for _ in range(2)]
+    t.cuda.synchronize()
+    for i in range(6):
+        L.oscar_kv8_attention(s.cache, qt, lens, 3100, outs[i], spaces[i % 2], q_pos=at,
+                              stream=streams[i % 2])
+    t.cuda.synchronize()
+    for o in outs:
+        np.testing.assert_array_equal(H.from_bf16(o), want)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        L.oscar_kv8_attention(s.cache, qt, lens, 3100, outs[0], spaces[0], q_pos=at)
+    outs[0].zero_()
+    graph.replay()
+    t.cuda.synchronize()
+    np.testing.assert_array_equal(H.from_bf16(outs[0]), want)
+    s.place([0, 40, 1, 800])
+    q = K.queries(s.rng, 4, 65, 32, 128)
+    pos = np.maximum(s.lens[:, None] - 65 + np.arange(65), -1)[:, ::-1].copy()
+    pos[2, 3:40] = -1
+    lens.copy_(s.i32(s.lens)), at.copy_(s.i32(pos)), qt.copy_(H.bf16_tensor(q))
+    graph.replay()
+    graph.replay()
+    t.cuda.synchronize()
+    s.check_attention(H.from_bf16(outs[0]), q, pos, heads=some)
+    assert H.status(s.cache) == 0
+
+
 def test_a_descriptor_is_checked_again_when_a_tensor_is_replaced():
     """Also by one at the same address."""
     t, L = H.torch(), H.lib()
