@@ -426,18 +426,28 @@ def _need(ok: bool, fn: str, what: str) -> None:
 # on the host: each of these reads an attribute of a tensor once, and a message is put
 # together only when it is raised.
 
+_INT32 = _INT64 = _BF16 = _raw_stream = _current_device = None
+
+
+def _bind_torch() -> None:
+    """What the checks use of torch, which is imported when the first tensor comes."""
+    global _INT32, _INT64, _BF16, _raw_stream, _current_device
+    import torch
+    _INT32, _INT64, _BF16 = torch.int32, torch.int64, torch.bfloat16
+    # the current stream's handle without a Stream object around it
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _i32(fn: str, name: str, t, index: int) -> int:
     """The address of a contiguous int32 tensor on CUDA device `index`."""
-    import torch
-    if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor on cuda:{index}")
     return t.data_ptr()
 
 
 def _rows(fn: str, name: str, t, n: int, heads: int, d: int, index: int) -> int:
     """Row stride in elements of a bf16 tensor [n][heads][d] whose rows are contiguous."""
-    import torch
-    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != (n, heads, d):
+    if t.dtype is not _BF16 or t.get_device() != index or t.shape != (n, heads, d):
         raise ValueError(f"{fn}: {name} must be a bfloat16 tensor [{n}][{heads}][{d}] on cuda:{index}")
     row, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and heads > 1):
@@ -446,6 +456,8 @@ def _rows(fn: str, name: str, t, n: int, heads: int, d: int, index: int) -> int:
 
 
 def _device_of(fn: str, name: str, t) -> int:
+    if _INT32 is None:
+        _bind_torch()
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{fn}: {name} must be on a CUDA device")
@@ -454,13 +466,12 @@ def _device_of(fn: str, name: str, t) -> int:
 
 def _launch(fn: str, index: int, stream, *args) -> None:
     """Calls the library's `fn` with the stream appended, with device `index` current."""
-    import torch
     f = getattr(_LIB or lib(), fn)
-    # the current stream's handle without a Stream object around it
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         status = f(*args, handle)
     else:
+        import torch
         with torch.cuda.device(index):
             status = f(*args, handle)
     if status != OSCAR_OK:
@@ -580,7 +591,6 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
     """Attention over the 8-bit cache.  Decode: q, out bf16 [B][Hq][d], every row sees
     the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
     row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros)."""
-    import torch
     fn = "oscar_kv8_attention"
     _, desc, index, rows = cache._checked()
     lens, batch = _i32(fn, "seq_lens", seq_lens, index), seq_lens.numel()
@@ -593,7 +603,7 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
         m_rows = q_pos.shape[1]
         shape = (batch, m_rows, cache.num_q_heads, cache.head_dim)
     for t in (q, out):
-        if (t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape
+        if (t.dtype is not _BF16 or t.get_device() != index or t.shape != shape
                 or not t.is_contiguous()):
             raise ValueError(f"{fn}: q and out must be contiguous bfloat16 tensors {list(shape)} "
                              f"on cuda:{index}")
@@ -611,15 +621,14 @@ def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_af
     (from index cursor[0] on), lengths, prefix sums and the lists of the new tokens.
     page_starts[B] is the next call's cursor (pass page_starts[-1:]); lens_after may
     be lens.  Rows of seq_ids, positions and slots behind the new tokens become -1."""
-    import torch
     fn = "oscar_extend_pages"
     index = _device_of(fn, "page_table", page_table)
     batch, rows = lens.numel(), seq_ids.numel()
-    args = [_i32(fn, name, t, index) for name, t in (
-        ("page_table", page_table), ("lens", lens), ("new_tokens", new_tokens),
-        ("free_pages", free_pages), ("cursor", cursor), ("lens_after", lens_after),
-        ("page_starts", page_starts), ("row_starts", row_starts), ("seq_ids", seq_ids),
-        ("positions", positions))]
+    table, before = _i32(fn, "page_table", page_table, index), _i32(fn, "lens", lens, index)
+    new, free = _i32(fn, "new_tokens", new_tokens, index), _i32(fn, "free_pages", free_pages, index)
+    at, after = _i32(fn, "cursor", cursor, index), _i32(fn, "lens_after", lens_after, index)
+    ps, rs = _i32(fn, "page_starts", page_starts, index), _i32(fn, "row_starts", row_starts, index)
+    ids, pos = _i32(fn, "seq_ids", seq_ids, index), _i32(fn, "positions", positions, index)
     if page_table.dim() != 2 or page_table.shape[0] < batch:
         raise ValueError(f"{fn}: page_table must be [batch][max_pages_per_seq]")
     if (new_tokens.numel() != batch or lens_after.numel() != batch or cursor.numel() < 1
@@ -628,11 +637,10 @@ def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_af
                          "row_starts batch + 1, cursor one")
     if positions.numel() != rows:
         raise ValueError(f"{fn}: seq_ids and positions must have the same rows")
-    if slots is not None and (slots.dtype is not torch.int64 or slots.get_device() != index
+    if slots is not None and (slots.dtype is not _INT64 or slots.get_device() != index
                               or not slots.is_contiguous() or slots.numel() != rows):
         raise ValueError(f"{fn}: slots must be a contiguous int64 tensor on cuda:{index} with a "
                          "row per seq_ids row")
-    table, before, new, free, at, after, ps, rs, ids, pos = args
     _launch(fn, index, stream, table, page_table.shape[1], before, new, batch, hold_back, free,
             free_pages.numel(), at, after, ps, rs, ids, pos, _ptr(slots), rows,
             None if status is None else _i32(fn, "status", status, index))
@@ -655,7 +663,6 @@ def oscar_rope(q, k, positions, phases, q_out=None, k_out=None, interleaved: boo
     either may be None) at int32 positions [n] (negative: the row is left as it was).
     phases: oscar_rope_phases' words on the device as int64 (or uint64) [rotary_dim / 2].
     q_out, k_out: outputs, in place when None."""
-    import torch
     fn = "oscar_rope"
     some = k if q is None else q
     if some is None or some.dim() != 3:
@@ -679,8 +686,8 @@ def oscar_rope(q, k, positions, phases, q_out=None, k_out=None, interleaved: boo
     pos = _i32(fn, "positions", positions, index)
     if positions.numel() != n or (q is None and q_out is not None) or (k is None and k_out is not None):
         raise ValueError(f"{fn}: positions must have an entry per row, and an output its input")
-    if (phases.dtype not in (torch.int64, torch.uint64) or phases.get_device() != index
-            or not phases.is_contiguous()):
+    if ((phases.dtype is not _INT64 and str(phases.dtype) != "torch.uint64")
+            or phases.get_device() != index or not phases.is_contiguous()):
         raise ValueError(f"{fn}: phases must be contiguous 64-bit integers on cuda:{index}")
     _launch(fn, index, stream, qp, kp, pos, phases.data_ptr(), n, hq, hk, d, 2 * phases.numel(),
             1 if interleaved else 0, amplitude, 1 if inverse else 0, qs, ks, qos, kos, qop, kop)
