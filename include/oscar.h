@@ -486,7 +486,7 @@ size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32
  *   q, out: device bf16 [batch][m_rows][num_q_heads][d], 16-byte aligned; query
  *     head hq reads KV head hq / G.
  *   seq_lens: device int32 [batch], tokens stored (the rows' own included), 0 ..
- *     max_seq_len; max_seq_len <= 16 * max_pages_per_seq + 15.
+ *     max_seq_len; max_seq_len <= 16 * max_pages_per_seq + 15, and <= 2^30.
  *   q_pos: null for a decode step (m_rows = 1: the row sees all tokens), else
  *     device int32 [batch][m_rows]: row m of sequence b sees positions 0 ..
  *     q_pos[b][m].

@@ -976,7 +976,8 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
   Kv8Plan p{};
   const int64_t cols = m_rows * (c->num_q_heads / c->num_kv_heads);
   const int64_t tiles8 = (cols + 7) / 8, tiles128 = (cols + 127) / 128;
-  if (cols > (1 << 30) || batch * tiles8 > (1 << 30) || batch * tiles8 * c->num_kv_heads > 0x7fffffff)
+  // (positions, and those of the pages behind the last, fit int32)
+  if (max_len > (1 << 30) || cols > (1 << 30) || batch * tiles8 > (1 << 30) || batch * tiles8 * c->num_kv_heads > 0x7fffffff)
     return false;
   const int d = c->head_dim, h = c->num_kv_heads;
   const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);

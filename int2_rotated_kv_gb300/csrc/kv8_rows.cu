@@ -698,7 +698,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           meta[(g & 3) * 8 + slot] =
               shown ? make_float4(sc.x, live ? __log2f(sc.y) : -kRZero, live ? __fdividef(1.f, sc.y) : power_of_two(kRZero),
                                   __int_as_float((u.p0 + 8 * i + slot) * kPage))
-                    : make_float4(0.f, 0.f, 0.f, __int_as_float(kRHidden));
+                    : make_float4(0.f, -INFINITY, 0.f, __int_as_float(kRHidden));   // weight 0 without a mask
         }
         const int slot = u.tail_slot(i);
         if (i + 1 < u.tiles) {
@@ -738,6 +738,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         if (!wait(&bar->qfull[seg & 1], seg >> 1)) break;
         const float fac = facs[(seg & 1) * 128 + rr];
         const bool idle = __all_sync(0xffffffffu, gcol >= p.cols);
+        const int vis_least = __reduce_min_sync(0xffffffffu, vis);
         bool ok = true;
         for (int i = st; i < u.tiles; i += 2) {
           if (!(ok = wait(&bar->sfull[st], count))) break;
@@ -750,10 +751,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             arrive(&bar->pfull[2 + st]);
             continue;
           }
-          bool hides = false;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) hides |= __float_as_int(mt[j].w) + kPage > vis;
-          const bool masked = __any_sync(0xffffffffu, hides);
+          const bool masked = (u.p0 + 8 * i + 8) * kPage > vis_least;   // (always with a tail)
           const float big = masked ? rows_max<true>(ts, mt, fac, vis) : rows_max<false>(ts, mt, fac, vis);
           const bool over = big > m + kLag;
           if (__any_sync(0xffffffffu, over)) {

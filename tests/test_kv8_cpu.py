@@ -63,8 +63,10 @@ def test_attention_refusals(L):
     big = _desc(L, max_pages_per_seq=8192)
     sizes = [lib.oscar_kv8_workspace_size(ctypes.byref(big), b, 1, 131072) for b in (1, 64, 4096)]
     assert sizes[0] == sizes[1] == sizes[2] > one          # per resident CTA, not per sequence
-    for bad in ((0, 1, 16), (1, 0, 16), (1, 1, 0)):
+    for bad in ((0, 1, 16), (1, 0, 16), (1, 1, 0), (1, 1, (1 << 30) + 1)):
         assert lib.oscar_kv8_workspace_size(d, *bad) == 0
+    d = ctypes.byref(_desc(L, max_pages_per_seq=1 << 27))
+    assert call(max_len=1 << 30) == -3 and call(max_len=(1 << 30) + 1) == -2
 
 
 def test_place_and_gather_refusals(L):
