@@ -27,14 +27,16 @@
 // at d = 128 and shared memory 1536 (fp16 tiles written once and read by the MMAs, Q read per
 // tile); a tile takes 2400, in which a K warp is busy for 1950 and a stream's chain S, softmax,
 // O is longer than its share.  Measured, d = 128, 8 KV heads, G = 4: 2048 rows over 32768 tokens
-// 1064 us, 1033 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 88 us, 540 TFLOP/s of
+// 1055 us, 1042 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86 us, 554 TFLOP/s of
 // rows that exist (260 columns are 3 tiles: a third of the work is for 4 of them).
 // Registers: 96 a thread for 18 warps.  Whatever is spilled in a role's loop costs more than
 // it saves elsewhere (16 registers' worth: 7 of 98 us), and code that is fetched cold costs its
 // fetches, so what runs once per unit is out of line or rolled.
 // Tried: one pass over S with the maximum of 32 (16) columns checked before their weights,
 // 1895 (1694) us where two passes take 1479, as every check waits for a vote; three V tiles,
-// 1420 us for 1185: shared memory that a tile more takes is L1's; setmaxnreg, no gain.
+// 1420 us for 1185: shared memory that a tile more takes is L1's; setmaxnreg, no gain; value
+// codes through a ring of asynchronous copies, 91 us for 86, or asked into L1 two tiles ahead,
+// 94; a page's successor requested before the other page is converted, 113.
 
 #include "kv8_units.cuh"
 #include "tcgen05.cuh"
