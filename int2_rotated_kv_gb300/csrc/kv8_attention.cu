@@ -939,7 +939,12 @@ inline double cluster_us(int d, int64_t pages, int c) {
 }
 
 // Tiles of 128: a start of 24 us (18 for d = 64), 0.08 us for each unit, 0.15 us for each of
-// the CTAs that a unit is spread over, whose parts are merged, and 0.001 us a page.
+// the CTAs that a unit is spread over, whose parts are merged, and 0.001 us a page.  Measured,
+// tiles of 8 against tiles of 128, in us (int8): d = 128, 8 KV heads, one sequence of 32k: 24
+// columns 32.7, 38.5; 32 columns 38.2, 38.6; 48 columns 68, 39.5; 64 sequences of 2000-4000: 16
+// columns 130, 164; 24 columns 183, 166; one sequence, 256 columns: 500 tokens 10.5, 21.8; 2000
+// tokens 19.8, 26.2; 4000 tokens 50, 26.5; d = 64, 2 KV heads, 40 sequences of 1000-2000: 64
+// columns 46.5, 29; one of 32k: 96 columns 23.7, 33.7.
 inline double rows_us(int d, int64_t batch, int64_t units, int64_t pages, int64_t sms) {
   return 12.0 + 12.0 / 128 * d + 0.08 * static_cast<double>(units) +
          0.15 * static_cast<double>(std::min(sms / units, pages / kMinShare)) +
