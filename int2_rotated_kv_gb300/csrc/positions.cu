@@ -9,7 +9,7 @@
 // sequence by bisection of the prefix sums.  Bound by latency (a chain of a scan and
 // two dependent loads) for a decode step, by the 16 bytes written per row for a
 // large prefill.  Measured: 256 sequences, a token each 4.6 us; 0.8 million rows
-// 8.7 us, 1500 GB/s of lists that stay in L2.
+// 7.4 us, 1750 GB/s of lists that stay in L2.
 //
 // oscar_rope.  For a rotated pair (a, b) at position m with frequency f turns per
 // token: a' = A (a cos 2 pi m f - b sin 2 pi m f), b' = A (b cos + a sin).  f is held
@@ -43,8 +43,11 @@ inline cudaLaunchConfig_t pdl_config(dim3 grid, dim3 block, size_t smem, cudaStr
 
 constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
+// Prefix sums that a filling CTA bisects in shared memory (0.8 million rows of 256 sequences: 7.4 us
+// against 8.6 from L1).
+constexpr int kSharedStarts = 2048;
 // Rows that the scan's CTA writes itself.  Itself against a grid of its own: 256 rows 4.7 us
-// against 7.2, 2048 rows 4.6 against 6.2, 4096 rows 5.5 against 6.0, 8192 rows 7.6 against 6.5.
+// against 5.6, 2048 rows 4.6 against 5.5, 4096 rows 5.4 against 5.3, 8192 rows 7.6 against 5.7.
 constexpr int64_t kInlineRows = 4096;
 
 struct PagesParams {
@@ -87,9 +90,11 @@ __device__ __forceinline__ int fresh_page(const PagesParams& p, int first, int p
 }
 
 // Rows and new table entries, `i` of `n` workers.  A worker writes runs of four rows:
-// one bisection, then the next sequence where its rows end.
-__device__ __forceinline__ void fill_rows(const PagesParams& p, int64_t i, int64_t n) {
-  const int64_t rows = p.row_starts[p.batch];
+// one bisection, then the next sequence where its rows end.  row_starts, page_starts: the
+// step's, or a copy of them in shared memory.
+__device__ __forceinline__ void fill_rows(const PagesParams& p, const int32_t* row_starts,
+                                          const int32_t* page_starts, int64_t i, int64_t n) {
+  const int64_t rows = row_starts[p.batch];
   for (int64_t r0 = 4 * i; r0 < p.max_rows; r0 += 4 * n) {
     int b = -1, end = -1, start = 0, before = 0, held = 0, holds = 0;   // of the run's current sequence
     int ids[4], pos[4];
@@ -101,10 +106,10 @@ __device__ __forceinline__ void fill_rows(const PagesParams& p, int64_t i, int64
       slot[j] = -1;
       if (r >= rows || r >= p.max_rows) continue;
       if (r >= end) {
-        if (b < 0) b = sequence_of(p.row_starts, p.batch, static_cast<int>(r));
-        else while (p.row_starts[b + 1] <= r) ++b;
-        start = p.row_starts[b];
-        end = p.row_starts[b + 1];
+        if (b < 0) b = sequence_of(row_starts, p.batch, static_cast<int>(r));
+        else while (row_starts[b + 1] <= r) ++b;
+        start = row_starts[b];
+        end = row_starts[b + 1];
         const int after = p.lens_after[b];
         before = after - (end - start);
         held = pages_held(before, p.hold);
@@ -114,7 +119,7 @@ __device__ __forceinline__ void fill_rows(const PagesParams& p, int64_t i, int64
       pos[j] = before + static_cast<int>(r) - start;
       const int pg = pos[j] / kPage;
       if (p.slots && pg < holds) {
-        const int id = pg >= held ? fresh_page(p, p.page_starts[b], pg, held)
+        const int id = pg >= held ? fresh_page(p, page_starts[b], pg, held)
                                   : p.table[static_cast<size_t>(b) * p.max_pages + pg];
         if (id >= 0) slot[j] = static_cast<int64_t>(id) * kPage + pos[j] % kPage;
       }
@@ -136,14 +141,14 @@ __device__ __forceinline__ void fill_rows(const PagesParams& p, int64_t i, int64
       }
     }
   }
-  const int first = p.page_starts[0];
-  const int64_t fresh = static_cast<int64_t>(p.page_starts[p.batch]) - first;
+  const int first = page_starts[0];
+  const int64_t fresh = static_cast<int64_t>(page_starts[p.batch]) - first;
   for (int64_t j = i; j < fresh; j += n) {
     const int at = first + static_cast<int>(j);
-    const int b = sequence_of(p.page_starts, p.batch, at);
+    const int b = sequence_of(page_starts, p.batch, at);
     const int after = p.lens_after[b];
-    const int held = pages_held(after - (p.row_starts[b + 1] - p.row_starts[b]), p.hold);
-    const int pg = held + at - p.page_starts[b];
+    const int held = pages_held(after - (row_starts[b + 1] - row_starts[b]), p.hold);
+    const int pg = held + at - page_starts[b];
     if (pg < p.max_pages)
       p.table[static_cast<size_t>(b) * p.max_pages + pg] = at < p.n_free ? p.free_pages[at] : -1;
   }
@@ -216,14 +221,24 @@ __global__ void __launch_bounds__(kScanThreads) extend_scan_kernel(const __grid_
   }
   if (p.fill) {
     __syncthreads();   // this CTA's global writes above are read back
-    fill_rows(p, tid, kScanThreads);
+    fill_rows(p, p.row_starts, p.page_starts, tid, kScanThreads);
   }
 }
 
 __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(const __grid_constant__ PagesParams p) {
+  __shared__ int32_t starts[2][kSharedStarts];
   pdl_wait();
   pdl_trigger();
-  fill_rows(p, static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x,
+  const bool few = p.batch < kSharedStarts;
+  if (few) {
+    for (int b = threadIdx.x; b <= p.batch; b += kFillThreads) {
+      starts[0][b] = p.row_starts[b];
+      starts[1][b] = p.page_starts[b];
+    }
+    __syncthreads();
+  }
+  fill_rows(p, few ? starts[0] : p.row_starts, few ? starts[1] : p.page_starts,
+            static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x,
             static_cast<int64_t>(gridDim.x) * kFillThreads);
 }
 
