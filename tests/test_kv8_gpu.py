@@ -122,21 +122,22 @@ def test_gather(fmt, d, hkv):
 
 # -------------------------------------------------------------------- attention
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d,hkv,g", [(64, 1, 4), (128, 2, 1), (128, 2, 4), (64, 3, 3), (128, 1, 8),
                                      (128, 1, 16), (64, 1, 40)])
-def test_decode_matches_oracle(fmt, d, hkv, g):
+def test_decode_matches_oracle(fmt, d, hkv, g, wide):
     """Ragged lengths, with none, one token, and ends on and beside page borders."""
     lens = [0, 1, 15, 16, 17, 33, 700, 2607, 1024]
     s = K.Sequences(len(lens), hkv, hkv * g, d, fmt, 2700, seed=g)
     s.place(lens)
     q = K.queries(s.rng, len(lens), 1, hkv * g, d)
-    got = s.attend(q)
+    got = s.attend(q, wide=wide)
     s.check_attention(got, q)
     assert H.status(s.cache) == 0
     # fewer tokens than placed pages hold: whole pages are read from the pool all the same
     short = np.array([0, 1, 15, 16, 16, 32, 688, 1600, 1008])
-    s2 = s.attend(q, lens=short)
+    s2 = s.attend(q, lens=short, wide=wide)
     for b in (4, 5, 6, 7, 8):
         one = np.zeros_like(short)
         one[b] = short[b]
