@@ -427,6 +427,14 @@ def test_page_offsets_beyond_4_gib():
     s.place([64])
     q = K.queries(s.rng, 1, 1, 8, 128)
     s.check_attention(s.attend(q), q)
+    rows, pos = K.queries(s.rng, 1, 20, 8, 128), np.arange(44, 64)[None]
+    for wide in WIDE:
+        s.check_attention(s.attend(rows, pos, wide=wide), rows, pos)
+    k, v = (t.empty((64, 8, 128), dtype=t.bfloat16, device=H.DEV) for _ in range(2))
+    H.lib().oscar_kv8_gather(s.cache, s.i32([64]), s.i32([0]), s.i32([0, 64]), 64, k, v)
+    for h in range(8):
+        for got, want in zip((k, v), s.stored(0, h)):
+            np.testing.assert_array_equal(H.from_bf16(got)[:, h], synth.bf16_round(want.astype(np.float32)))
     order = kv8.orders(128)
     for p, i in enumerate(ids):
         scale, codes = kv8.block(s.v[0][16 * p:16 * p + 16, 7], kv8.INT8)
