@@ -223,9 +223,9 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
   raise_max<D>(s, lg);
   if (sc.y > s.vmax) {   // a larger value scale than any page before (the warp's own, uniform)
     const float up = __uint_as_float((__float_as_uint(sc.y) & 0x7f800000u) + 0x00800000u);
-    const float a = s.vmax / up;   // a power of two
+    const float a = s.vmax / up;   // a power of two, or 0 where nothing of o is left beside this page
     s.vmax = up;
-    s.vmul *= a;
+    s.vmul = __uint_as_float((260u << 23) - __float_as_uint(up));   // 2^6 / up
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll

@@ -1,0 +1,84 @@
+"""Attention over the 8-bit cache far from unit scale: values, keys and queries from 2^-100
+to the largest bf16, pages of very different scales in one sequence, and logits that leave
+one token.  The bounds weigh every error by the softmax weight of the token that it belongs
+to, so that a page of huge values excuses nothing that it does not dominate."""
+import numpy as np
+import pytest
+
+import gpu_harness as H
+import kv8_harness as K
+from int2_rotated_kv_gb300 import synth
+from oracle import kv8
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [kv8.INT8, kv8.E4M3]
+WIDE = [0, 131072]   # see kv8_harness.Sequences.attend
+BIG = float(synth.bf16_from_bits(np.array([0x7F7F], np.uint16))[0])
+
+
+def bf16(x):
+    """Rounded to bf16; beyond the largest finite value, to that."""
+    return synth.bf16_round(np.clip(x, -BIG, BIG).astype(np.float32))
+
+
+def page_max(x):
+    """Largest magnitude of each token's block: its page's, or the tail's."""
+    out = np.zeros(len(x))
+    for p in range(0, len(x), 16):
+        out[p:p + 16] = np.abs(x[p:p + 16]).max()
+    return out
+
+
+def check(s, got, q, pos=None):
+    """Every output against fp64.  With p the softmax weights:
+      logits: fp32 sums of 128 products and an offset, 24 roundings of 2^-23 of
+        sum |q| 2 max|k| of the block, and 2^-21 of the logit for its scaling; an error of e
+        changes p by e relative, and so the numerator and the denominator;
+      weights 2^(logit + log2 s_V): ex2 and the logarithm of a scale of up to 2^121,
+        2^-14; rounded to fp16, 2^-12, or by 2^-25 where the largest weight of the unit is at
+        least 1: 2^-25 of max p s_V for a token, whose code is at most max|v| / s_V
+        (a tail's values: at most 2^8 where s_V is a power of two, so 2^-24 of max p max|v|);
+      fp32 sums: 2^-23 a page and 16 for the merges;
+      the output: half a bf16 step, 2^-8."""
+    m, g = got.shape[1], s.hq // s.hkv
+    for b in range(s.b):
+        n = len(s.k[b])
+        for h in range(s.hkv):
+            k, v = s.stored(b, h)
+            kmax, vmax = page_max(k), page_max(v)
+            for i in range(m):
+                u = n if pos is None else max(0, int(pos[b, i]) + 1)
+                for r in range(g):
+                    row, out = q[b, i, h * g + r].astype(np.float64), got[b, i, h * g + r]
+                    lg = k[:u] @ row / np.sqrt(s.d)
+                    p = np.exp(lg - lg.max())
+                    p /= p.sum()
+                    ref, w = p @ v[:u], p @ np.abs(v[:u])
+                    e = (24 * 2.0 ** -23 * np.abs(row).sum() * 2 * kmax[:u] / np.sqrt(s.d) + 2.0 ** -21 * np.abs(lg))
+                    assert (p * e).sum() < 0.05                    # a bound that says something
+                    tol = (2.0 ** -12 + 2.0 ** -14 + (u // 16 + 16) * 2.0 ** -23 + (p * e).sum()) * w
+                    tol += (p * e) @ np.abs(v[:u]) + u * 2.0 ** -24 * (p * vmax[:u]).max()
+                    assert (tol <= 0.06 * w.max()).all()
+                    tol += 2.0 ** -8 * (np.abs(ref) + tol)
+                    bad = ~(np.abs(out - ref) <= tol)
+                    assert not bad.any(), (b, h, r, i, n, u, int(bad.sum()), out[bad][:4], ref[bad][:4], tol[bad][:4])
+
+
+def rows_of(s, m):
+    """The last m positions of every sequence; null for a decode step."""
+    return None if m == 1 else np.stack([np.arange(x - m, x) for x in s.lens])
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("scale", [2.0 ** -95, 1e14, 1e22, 1e30])
+def test_values_of_any_size(fmt, m, wide, scale):
+    s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=m)
+    k, v = K.draw(s.rng, 645 + 320 + 151, 1, 128)
+    s.place([645, 320, 151], k, bf16(v * scale))
+    q = K.queries(s.rng, 3, m, 4, 128)
+    pos = rows_of(s, m)
+    check(s, s.attend(q, pos, wide=wide), q, pos)
+    assert H.status(s.cache) == 0
