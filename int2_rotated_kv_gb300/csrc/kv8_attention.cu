@@ -12,8 +12,9 @@
 //   logit = s_K * (sum_c (u_c - 128) q_c),  the -128 sum_c q_c as the initial
 //     accumulator (int8); q enters as fp16 scaled by a power of two per column,
 //     which keeps all 8 bits of every bf16 within 2^-21 of the column's largest.
-//   o += (p s_V) code,  p s_V rounded once to fp16 (2^-12 relative, unbiased) and
-//     weighed by 2^(6-E), E the exponent of the largest s_V so far.  int8 value
+//   o += (p s_V) code,  p s_V rounded once to fp16 (2^-12 relative, unbiased; the
+//     exponent carries s_V, see kv8_units.cuh) and lifted by 2^6, so that it has its
+//     11 bits down to 2^-20 of the column's largest p s_V.  int8 value
 //     codes lose their 128 before the MMA (one fp16 add per two codes): summed
 //     with it over hundreds of pages, the accumulator's truncation of sums of
 //     p s_V (code + 128) is a bias of 2e-3 of the output where values cancel.
@@ -147,8 +148,9 @@ template <int D>
 struct Running {
   float o[D / 16][4];
   float m[2], l[2];
-  float vmax, vmul;      // power of two that no s_V so far exceeds, and 2^6 / vmax
+  float high;            // the largest log2 s_V so far
 };
+constexpr float kLift = 6.f;   // pages' weights are carried times 2^6
 
 template <int D>
 __device__ __forceinline__ void reset(Running<D>& s) {
@@ -156,12 +158,12 @@ __device__ __forceinline__ void reset(Running<D>& s) {
   for (int i = 0; i < D / 16; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
   s.m[0] = s.m[1] = kLowest;
   s.l[0] = s.l[1] = 0.f;
-  s.vmax = 9.62964972193618e-35f;   // 2^-113, below every scale but 0
-  s.vmul = 64.f / 9.62964972193618e-35f;
+  s.high = -INFINITY;
 }
 
 // Raises the running maxima where a logit passes one by more than kLag (so p <=
-// 2^kLag) and rescales; lg: rows gid, gid + 8 of the tile in the accumulator layout.
+// 2^kLag) and rescales; lg: logits plus log2 s_V, rows gid, gid + 8 of the tile in the
+// accumulator layout.
 template <int D>
 __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
   bool over = false;
@@ -175,15 +177,41 @@ __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
       top = fmaxf(top, s.m[c]);
-      const float a = top == s.m[c] ? 1.f : fast_exp2(s.m[c] - top);
+      const float half = top == s.m[c] ? 1.f : fast_exp2(0.5f * (s.m[c] - top)), a = half * half;
       s.m[c] = top;
-      s.l[c] *= a;
+      s.l[c] = s.l[c] * half * half;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         s.o[i][c] *= a;
         s.o[i][2 + c] *= a;
       }
     }
+  }
+}
+
+// p of the tokens whose weight w has underflowed, for the sums of the two columns; lg as in
+// raise_max.  Out of line: for pages whose scale is next to nothing beside others' (kFar).
+static __device__ __noinline__ float2 lost_sums(float4 w, float4 lg, float off, float m0, float m1) {
+  float2 l = make_float2(0.f, 0.f);
+  if (w.x == 0.f) l.x += whole_exp2(lg.x - off - m0 + kSumLog2);
+  if (w.y == 0.f) l.y += whole_exp2(lg.y - off - m1 + kSumLog2);
+  if (w.z == 0.f) l.x += whole_exp2(lg.z - off - m0 + kSumLog2);
+  if (w.w == 0.f) l.y += whole_exp2(lg.w - off - m1 + kSumLog2);
+  return l;
+}
+
+// Adds a tile of weights to the sums; z: 2^kSumLog2 / s_V in the weights' units.
+template <int D>
+__device__ __forceinline__ void add_sums(Running<D>& s, const float (&w)[4], const float (&lg)[4], float off,
+                                         float z) {
+  s.l[0] = fmaf(w[0] + w[2], z, s.l[0]);
+  s.l[1] = fmaf(w[1] + w[3], z, s.l[1]);
+  s.high = fmaxf(s.high, off);
+  if (off < s.high - kFar) {
+    const float2 l = lost_sums(make_float4(w[0], w[1], w[2], w[3]), make_float4(lg[0], lg[1], lg[2], lg[3]),
+                               off, s.m[0], s.m[1]);
+    s.l[0] += l.x;
+    s.l[1] += l.y;
   }
 }
 
@@ -211,7 +239,12 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
     }
   }
   const float f0 = sc.x * q.fac[0], f1 = sc.x * q.fac[1];
-  lg[0] *= f0; lg[1] *= f1; lg[2] *= f0; lg[3] *= f1;
+  const bool live = sc.y > 0.f;
+  const float off = live ? fast_log2(sc.y) : kZeroLog2;
+  lg[0] = fmaf(lg[0], f0, off);
+  lg[1] = fmaf(lg[1], f1, off);
+  lg[2] = fmaf(lg[2], f0, off);
+  lg[3] = fmaf(lg[3], f1, off);
   if (page0 + kPage > q.vis_min) {
     const int t = page0 + 2 * gid;
 #pragma unroll
@@ -221,26 +254,16 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
     }
   }
   raise_max<D>(s, lg);
-  if (sc.y > s.vmax) {   // a larger value scale than any page before (the warp's own, uniform)
-    const float up = __uint_as_float((__float_as_uint(sc.y) & 0x7f800000u) + 0x00800000u);
-    const float a = s.vmax / up;   // a power of two, or 0 where nothing of o is left beside this page
-    s.vmax = up;
-    s.vmul = __uint_as_float((260u << 23) - __float_as_uint(up));   // 2^6 / up
+  // w <= 2^kLag, lifted by 2^6: below 2^14 in fp16
+  float w[4];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s.o[i][r] *= a;
-  }
-  // 2^6 s_V / vmax: p s_V / vmax <= 2^8, so the fp16 weights stay below 2^14
-  const float vs = sc.y * s.vmul;
-  const float p0 = fast_exp2(lg[0] - s.m[0]), p1 = fast_exp2(lg[1] - s.m[1]);
-  const float p2 = fast_exp2(lg[2] - s.m[0]), p3 = fast_exp2(lg[3] - s.m[1]);
-  s.l[0] += p0 + p2;
-  s.l[1] += p1 + p3;
+  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - (s.m[r & 1] - kLift));
+  // 1 / s_V (2^110 for zeros) times 2^(kSumLog2 - kLift)
+  add_sums<D>(s, w, lg, off, (live ? fast_inverse(sc.y) : 1.298074214633707e33f) * (1.f / 262144.f));
   // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
   // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
-  uint32_t b0 = movmatrix_trans(pack_half2(p0 * vs, p1 * vs));
-  uint32_t b1 = movmatrix_trans(pack_half2(p2 * vs, p3 * vs));
+  uint32_t b0 = movmatrix_trans(pack_half2(w[0], w[1]));
+  uint32_t b1 = movmatrix_trans(pack_half2(w[2], w[3]));
   if constexpr (kE4m3) {   // pairs (4tig, 4tig + 1), (4tig + 2, 4tig + 3)
     const uint32_t lo = __byte_perm(b0, b1, 0x5410);
     b1 = __byte_perm(b0, b1, 0x7632);
@@ -261,20 +284,29 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
   }
 }
 
-// Brings the accumulators to the units of the values.
+// Takes 2^kLift and the codes' 2^-24 (int8) off the accumulators.
 template <int D, bool kE4m3>
 __device__ __forceinline__ void unscale(Running<D>& s) {
-  // weights carried 2^6 / vmax, int8 codes 2^-24; two factors stay in range
   const float up = kE4m3 ? 1.f / 64.f : 262144.f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      s.o[i][r] = s.o[i][r] * up * s.vmax;
+    for (int r = 0; r < 4; ++r) s.o[i][r] *= up;
 }
 
-// The tail: n bf16 tokens from position page0 at `st`; accumulators already in the
-// units of the values.  q.K in bf16 (exact products).  p.V in bf16 with p as a pair of
+// The largest finite magnitude of a pair of bf16, or `top`.
+__device__ __forceinline__ uint32_t finite_max(uint32_t top, uint32_t w) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  return max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+}
+__device__ __forceinline__ uint32_t bf16_times(uint32_t w, __nv_bfloat162 x) {
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), x);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// The tail: n bf16 tokens from position page0 at `st`; unscaled accumulators.  q.K in bf16
+// (exact products).  Its values enter times a power of two that brings the largest finite one to
+// [2^7, 2^8), as if they were codes of the scale that undoes it.  w.V in bf16 with w as a pair of
 // bf16 (2^-17); when a value is not finite, or a column does not see all n tokens, in
 // fp32 on the CUDA cores instead, which keeps a NaN or an infinity of a token out of
 // the rows that do not see it.
@@ -298,35 +330,42 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
       mma_bf16(lg, k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
     }
   }
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int seen = min(n, q.vis[c] - page0);   // tokens of the tail this column sees
-    lg[c] = 2 * gid < seen ? lg[c] * p.scale_log2 : -INFINITY;
-    lg[2 + c] = 2 * gid + 1 < seen ? lg[2 + c] * p.scale_log2 : -INFINITY;
-  }
-  raise_max<D>(s, lg);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) lg[r] = fast_exp2(lg[r] - s.m[r & 1]);
-  s.l[0] += lg[0] + lg[2];
-  s.l[1] += lg[1] + lg[3];
   const uint4* vb = kb + 2 * D;   // 16 * d keys before them
   // tokens 4tig, 4tig + 1 and 4tig + 2, 4tig + 3 of a channel's words, where there are any
   const int have = n - 4 * tig;
   const uint32_t m01 = (have > 0 ? 0xffffu : 0u) | (have > 1 ? 0xffff0000u : 0u);
   const uint32_t m23 = (have > 2 ? 0xffffu : 0u) | (have > 3 ? 0xffff0000u : 0u);
-  uint32_t top = 0;
+  uint32_t top = 0, finite = 0;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m01 & 0x7fff7fffu, v.y & m23 & 0x7fff7fffu),
                                  __vmaxu2(v.z & m01 & 0x7fff7fffu, v.w & m23 & 0x7fff7fffu)));
+    finite = finite_max(finite_max(finite, v.x & m01), v.y & m23);
+    finite = finite_max(finite_max(finite, v.z & m01), v.w & m23);
   }
+  finite = __reduce_max_sync(0xffffffffu, finite);
+  const int up = finite ? scale_up(finite) : static_cast<int>(-kZeroLog2);
+  const float off = static_cast<float>(-up);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int seen = min(n, q.vis[c] - page0);   // tokens of the tail this column sees
+    lg[c] = 2 * gid < seen ? fmaf(lg[c], p.scale_log2, off) : -INFINITY;
+    lg[2 + c] = 2 * gid + 1 < seen ? fmaf(lg[2 + c], p.scale_log2, off) : -INFINITY;
+  }
+  raise_max<D>(s, lg);
+  float w[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - s.m[r & 1]);
+  add_sums<D>(s, w, lg, off, power_of_two(up) * (1.f / 4096.f));
+  const float mul = power_of_two(up);
   const bool plain = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
   if (q.vis_min >= page0 + n && __all_sync(0xffffffffu, plain)) {
+    const __nv_bfloat162 mul2 = __float2bfloat162_rn(mul);
     uint32_t bh[2], bl[2];
-    const uint32_t h0 = pack_bf162(lg[0], lg[1]), h1 = pack_bf162(lg[2], lg[3]);
-    const uint32_t l0 = pack_bf162(lg[0] - bf16_lo_value(h0), lg[1] - bf16_hi_value(h0));
-    const uint32_t l1 = pack_bf162(lg[2] - bf16_lo_value(h1), lg[3] - bf16_hi_value(h1));
+    const uint32_t h0 = pack_bf162(w[0], w[1]), h1 = pack_bf162(w[2], w[3]);
+    const uint32_t l0 = pack_bf162(w[0] - bf16_lo_value(h0), w[1] - bf16_hi_value(h0));
+    const uint32_t l1 = pack_bf162(w[2] - bf16_lo_value(h1), w[3] - bf16_hi_value(h1));
     const uint32_t t0 = movmatrix_trans(h0), t1 = movmatrix_trans(h1);
     const uint32_t u0 = movmatrix_trans(l0), u1 = movmatrix_trans(l1);
     bh[0] = __byte_perm(t0, t1, 0x5410);
@@ -336,7 +375,11 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
-      v.x &= m01; v.y &= m23; v.z &= m01; v.w &= m23;   // slots without a token may hold anything
+      // slots without a token may hold anything
+      v.x = bf16_times(v.x & m01, mul2);
+      v.y = bf16_times(v.y & m23, mul2);
+      v.z = bf16_times(v.z & m01, mul2);
+      v.w = bf16_times(v.w & m23, mul2);
       mma_bf16(s.o[i], v.x, v.z, v.y, v.w, bh[0], bh[1]);
       mma_bf16(s.o[i], v.x, v.z, v.y, v.w, bl[0], bl[1]);
     }
@@ -348,10 +391,10 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {   // the lane's channels 32 (c/4) + 4 gid + c%4
       const int chunk = kv8_value_chunk(i >> 2, (c >> 2) * 8 + gid);
-      v[c >> 1][c & 1] = bf16_to_float(ve[chunk * 16 + 4 * (c & 3) + (i & 3)]);
+      v[c >> 1][c & 1] = bf16_to_float(ve[chunk * 16 + 4 * (c & 3) + (i & 3)]) * mul;
     }
-    const float w0 = __shfl_sync(0xffffffffu, (i & 1) ? lg[2] : lg[0], 4 * (i >> 1) + tig);
-    const float w1 = __shfl_sync(0xffffffffu, (i & 1) ? lg[3] : lg[1], 4 * (i >> 1) + tig);
+    const float w0 = __shfl_sync(0xffffffffu, (i & 1) ? w[2] : w[0], 4 * (i >> 1) + tig);
+    const float w1 = __shfl_sync(0xffffffffu, (i & 1) ? w[3] : w[1], 4 * (i >> 1) + tig);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       if (w0 != 0.f) {
@@ -459,11 +502,11 @@ __device__ __forceinline__ void start_part(const Kv8Params& p, const Entry& t, i
 // Channels ch .. ch + 3 of an output row; a row that sees nothing (l = 0) gets zeros.
 __device__ __forceinline__ void store_row(const Kv8Params& p, int b, int h, int gcol, int ch, int D,
                                           float4 o, float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const Inverse inv = inverse_of(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D + ch;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf162(o.x * inv.a * inv.b, o.y * inv.a * inv.b),
+                                              pack_bf162(o.z * inv.a * inv.b, o.w * inv.a * inv.b));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -509,8 +552,8 @@ __device__ __forceinline__ void merge_cluster(const Kv8Params& p, const Entry& t
       for (int r = 0; r < n; ++r) {
         const float2 ml = cluster_load2(cluster_address(slot + 8 * D + 2 * col, r));
         const float4 x = cluster_load4(cluster_address(slot + col * D + ch, r));
-        const float a = fast_exp2(ml.x - top);
-        l = fmaf(a, ml.y, l);
+        const float half = fast_exp2(0.5f * (ml.x - top)), a = half * half;
+        l = fmaf(half * ml.y, half, l);
         o.x = fmaf(a, x.x, o.x); o.y = fmaf(a, x.y, o.y);
         o.z = fmaf(a, x.z, o.z); o.w = fmaf(a, x.w, o.w);
       }
@@ -687,7 +730,8 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (kMode == kTeams && w >= team) break;
-        l = fmaf(sm_l[w * 8 + col], fast_exp2(sm_m[w * 8 + col] - top), l);
+        const float half = fast_exp2(0.5f * (sm_m[w * 8 + col] - top));
+        l = fmaf(sm_l[w * 8 + col] * half, half, l);
         const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
         o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
       }
@@ -743,8 +787,8 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
     top = warp_max(top);
     for (int j0 = 0; j0 < n; j0 += 32) {
       const float2 ml = stats(j0 + lane);
-      const float w = j0 + lane < n ? fast_exp2(ml.x - top) : 0.f;
-      l = fmaf(w, ml.y, l);
+      const float half = j0 + lane < n ? fast_exp2(0.5f * (ml.x - top)) : 0.f, w = half * half;
+      l = fmaf(half * ml.y, half, l);
       const int m = min(32, n - j0);
 #pragma unroll 8
       for (int j = sub; j < m; j += kSplit) {
@@ -772,12 +816,13 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
   if (!live) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const Inverse inv = inverse_of(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + kPer * lane);
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf162(acc[k] * inv, acc[k + 1] * inv);
+  for (int k = 0; k < kPer; k += 2)
+    dst[k / 2] = pack_bf162(acc[k] * inv.a * inv.b, acc[k + 1] * inv.a * inv.b);
 }
 
 // The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns

@@ -211,13 +211,6 @@ __device__ __forceinline__ void store_values(uint8_t* dst, int c, int w, int lan
   }
 }
 
-// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.
-__device__ __forceinline__ int scale_up(uint32_t amax) {
-  return amax ? max(-96, min(100, 134 - static_cast<int>(amax >> 7))) : 0;
-}
-__device__ __forceinline__ float power_of_two(int e) {
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
 __device__ __forceinline__ uint32_t half_pair(uint32_t w, float mul) {
   return pack_half2(bf16_lo_value(w) * mul, bf16_hi_value(w) * mul);
 }

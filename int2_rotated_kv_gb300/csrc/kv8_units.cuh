@@ -11,6 +11,56 @@ constexpr int kMaxCtas = 1024;
 constexpr float kLowest = -3.402823466e38f;   // running maximum before the first logit
 constexpr float kLag = 8.f;                   // the maximum is raised when passed by 2^8
 
+// The running maximum m of a column is that of logit + log2 s_V (log2 domain), so a weight
+// w = 2^(logit + log2 s_V - m) is p s_V beside the largest p s_V that the column has met: a page
+// of huge values that nothing attends to takes no bits from the others.  Outputs are sums of
+// w code, l the sum of w / s_V, both in units of 2^m.  Value scales go from 2^-109 to 2^121:
+//   - a page of zeros counts as one of scale 2^-110, below every other (kZeroLog2);
+//   - l is carried times 2^-12, so that 2^25 tokens of the least scale stay below 2^128;
+//   - where a scale lies 2^96 or more below the largest met (kFar), w / s_V may be lost with w, and
+//     2^(logit - m) takes its place;
+//   - a change of m by x takes l times 2^(x/2) twice, as 2^x alone may underflow;
+//   - 1 / l is two factors.
+constexpr float kZeroLog2 = -110.f;
+constexpr float kSumLog2 = -12.f;
+constexpr float kFar = 96.f;
+
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.
+__device__ __forceinline__ int scale_up(uint32_t amax) {
+  return amax ? max(-96, min(100, 134 - static_cast<int>(amax >> 7))) : 0;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^x, subnormal results kept.
+__device__ __forceinline__ float whole_exp2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / l of a sum l (carried times 2^kSumLog2, perhaps subnormal), 0 for 0: the product of two.
+struct Inverse {
+  float a, b;
+};
+__device__ __forceinline__ Inverse inverse_of(float l) {
+  const float up = l < 7.888609052210118e-31f ? 1.2676506002282294e30f     // 2^-100, 2^100
+                   : l > 1.2676506002282294e30f ? 7.888609052210118e-31f
+                                                : 1.f;
+  return {l == 0.f ? 0.f : 1.f / (l * up), up * (1.f / 4096.f)};
+}
+
 struct Kv8Params {
   int hkv, hq, G, max_pages;
   int64_t n_pages, n_tails;

@@ -82,3 +82,24 @@ def test_values_of_any_size(fmt, m, wide, scale):
     pos = rows_of(s, m)
     check(s, s.attend(q, pos, wide=wide), q, pos)
     assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("jump", [22, 30, 60, 100])
+def test_a_page_of_huge_values_that_nothing_attends_to(fmt, m, wide, jump):
+    """Pages whose values are 2^jump above the others' and whose logits lie about 2^-100 below
+    in weight, first, in the middle and last: they take no precision from the others."""
+    s = K.Sequences(3, 1, 4, 64, fmt, 700, seed=jump)
+    k, v = K.draw(s.rng, 645 + 320 + 151, 1, 64)
+    k[:, :, 0] = 0
+    for at in (0, 16 * 21, 645 + 16 * 19, 965 + 16 * 4):
+        v[at:at + 16] *= np.float32(2.0 ** jump)
+        k[at:at + 16, :, 0] = -64
+    s.place([645, 320, 151], k, bf16(v))
+    q = K.queries(s.rng, 3, m, 4, 64)
+    q[..., 0] = 8.75
+    pos = rows_of(s, m)
+    check(s, s.attend(q, pos, wide=wide), q, pos)
+    assert H.status(s.cache) == 0
