@@ -76,7 +76,7 @@ struct Kv8Cfg {
 template <int D>
 struct Query {
   uint32_t b[D / 16][2];
-  float fac[2];     // log2-domain logit per unit of q.code, before s_K
+  float fac[2];     // log2-domain logit per unit of q.code, before s_K and the int8 codes' 2^24
   float init[2];    // -128 sum q (int8)
   int vis[2];
   int vis_min;      // smallest over the unit's columns
@@ -108,9 +108,8 @@ __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, i
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   // the largest magnitude goes to [2^7, 2^8)
-  const int exponent = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
-  const int up = amax > 0.f ? max(-96, min(100, 7 - exponent)) : 0;
-  const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+  const int up = scale_up(__float_as_uint(amax) >> 16);
+  const float mul = power_of_two(up);
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -130,8 +129,7 @@ __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, i
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  const float fac =
-      p.scale_log2 * __uint_as_float(static_cast<uint32_t>((kE4m3 ? 0 : 24) - up + 127) << 23);
+  const float fac = p.scale_log2 * power_of_two(-up);
   const float init = kE4m3 ? 0.f : sum * (-128.f / 16777216.f);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -238,7 +236,8 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
       mma_f16(lg, a0, a1, a2, a3, q.b[4 * j + w][0], q.b[4 * j + w][1]);
     }
   }
-  const float f0 = sc.x * q.fac[0], f1 = sc.x * q.fac[1];
+  constexpr float kUnit = kE4m3 ? 1.f : 16777216.f;
+  const float f0 = logit_factor(sc.x, q.fac[0], kUnit), f1 = logit_factor(sc.x, q.fac[1], kUnit);
   const bool live = sc.y > 0.f;
   const float off = live ? fast_log2(sc.y) : kZeroLog2;
   lg[0] = fmaf(lg[0], f0, off);

@@ -397,7 +397,7 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
       for (int k = 0; k < 5; ++k) x[k] = max3(x[k], x[k + 5], x[k + 10]);
       const float top = fmaxf(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[15]));
       // (a hidden page's -inf times a scale of 0 would be NaN)
-      big = fmaxf(big, kMasked && top == -INFINITY ? top : fmaf(top, pm.x * fac, pm.y));
+      big = fmaxf(big, kMasked && top == -INFINITY ? top : fmaf(top, logit_factor(pm.x, fac), pm.y));
     }
   };
   uint32_t a[32], b[32];
@@ -425,7 +425,7 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
     for (int j = 0; j < 2; ++j) {
       uint32_t out[8];
       const float4 pm = mt[j0 + j];
-      const float f = pm.x * fac, off = pm.y - m;
+      const float f = logit_factor(pm.x, fac), off = pm.y - m;
       const uint64_t f2 = two(f, f), off2 = two(off, off);
       const int seen = vis - __float_as_int(pm.w);
       uint64_t sum[2];

@@ -28,9 +28,15 @@ constexpr float kFar = 96.f;
 __device__ __forceinline__ float power_of_two(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.
+// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.  (Magnitudes
+// below 2^-113 come lower: both the power and its inverse stay normal.)
 __device__ __forceinline__ int scale_up(uint32_t amax) {
-  return amax ? max(-96, min(100, 134 - static_cast<int>(amax >> 7))) : 0;
+  return amax ? max(-120, min(120, 134 - static_cast<int>(amax >> 7))) : 0;
+}
+// A logit per unit of a column's q.K: the key scale times the column's factor, whose product may
+// overflow where q.K is 0 all the same.
+__device__ __forceinline__ float logit_factor(float scale, float fac, float unit = 1.f) {
+  return fminf(scale * fac * unit, 3.402823466e38f);
 }
 
 __device__ __forceinline__ float fast_log2(float x) {

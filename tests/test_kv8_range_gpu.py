@@ -103,3 +103,60 @@ def test_a_page_of_huge_values_that_nothing_attends_to(fmt, m, wide, jump):
     pos = rows_of(s, m)
     check(s, s.attend(q, pos, wide=wide), q, pos)
     assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+def test_the_largest_keys_against_tiny_queries(fmt, m, wide):
+    """Keys of about the largest bf16, queries of 2^-122 to 2^-121: logits of a few units."""
+    s = K.Sequences(2, 1, 4, 128, fmt, 400, seed=6)
+    k, v = K.draw(s.rng, 395 + 167, 1, 128)
+    k[:] = bf16(np.clip(k, -8, 8) * 2.0 ** 124)
+    s.place([395, 167], k, v)
+    q = bf16(s.rng.uniform(0.5, 1, (2, m, 4, 128)) * np.where(s.rng.random((2, m, 4, 128)) < 0.5, -1, 1) * 2.0 ** -121)
+    pos = rows_of(s, m)
+    check(s, s.attend(q, pos, wide=wide), q, pos)
+    assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("qexp,kexp", [(13, 0), (-60, 74), (113, -97), (126, -99)])
+def test_logits_that_leave_one_token(fmt, m, wide, qexp, kexp):
+    """Queries of one channel, and per channel a few tokens whose keys beat all before them or
+    after them by at least half a unit: a difference of 300 in the logit, so the output is that
+    token's value: p s_V rounded to fp16, 2^-12, s_V itself through its logarithm, 2^-14, and the
+    output to bf16, 2^-8."""
+    lens = [645, 320, 151]
+    s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=m)
+    n = sum(lens)
+    _, v = K.draw(s.rng, n, 1, 128)
+    k = np.zeros((n, 1, 128))
+    at = 0
+    for length in lens:
+        k[at] = 0.5
+        for c in range(128):
+            t = np.sort(s.rng.choice(np.arange(1, length), 6, replace=False))
+            k[at + t, 0, c] = np.arange(1, 7) if c % 2 else s.rng.permutation(np.arange(1, 7))
+        at += length
+    s.place(lens, bf16(k * 2.0 ** kexp), v)
+    q = np.zeros((3, m, 4, 128), np.float32)
+    chan = s.rng.integers(0, 128, (3, m, 4))
+    np.put_along_axis(q, chan[..., None], np.float32(2.0 ** qexp), -1)
+    pos = None if m == 1 else np.stack([s.rng.integers(0, x, m) for x in lens])
+    got = s.attend(q, pos, wide=wide)
+    for b in range(3):
+        kk, vv = s.stored(b, 0)
+        for i in range(m):
+            u = lens[b] if pos is None else pos[b, i] + 1
+            for r in range(4):
+                key = kk[:u, chan[b, i, r]]
+                best = int(key.argmax())
+                second = np.delete(key, best).max() if u > 1 else -np.inf
+                assert key[best] - second >= 0.4 * 2.0 ** kexp
+                want = vv[best]
+                bad = ~(np.abs(got[b, i, r] - want) <= (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -14) * 1.01 * np.abs(want))
+                assert not bad.any(), (b, i, r, u, best, got[b, i, r][bad][:4], want[bad][:4])
+    assert H.status(s.cache) == 0
