@@ -76,7 +76,8 @@ struct Kv8Cfg {
 template <int D>
 struct Query {
   uint32_t b[D / 16][2];
-  float fac[2];     // log2-domain logit per unit of q.code, before s_K and the int8 codes' 2^24
+  float fac[2];     // log2-domain logit per unit of q.code, before s_K; of the int8 codes' 2^24 it
+                    // has 2^18, and s_K gets 2^6, as neither takes all without overflow
   float init[2];    // -128 sum q (int8)
   int vis[2];
   int vis_min;      // smallest over the unit's columns
@@ -129,7 +130,7 @@ __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, i
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  const float fac = p.scale_log2 * power_of_two(-up);
+  const float fac = p.scale_log2 * power_of_two(-up) * (kE4m3 ? 1.f : 262144.f);
   const float init = kE4m3 ? 0.f : sum * (-128.f / 16777216.f);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -146,9 +147,12 @@ template <int D>
 struct Running {
   float o[D / 16][4];
   float m[2], l[2];
-  float high;            // the largest log2 s_V so far
+  bool odd;              // a scale has been above the window of is_odd
 };
-constexpr float kLift = 6.f;   // pages' weights are carried times 2^6
+// Here m lies kLift below the largest logit + log2 s_V (weights reach 2^14).
+constexpr int kLift = 6;
+constexpr int kLiftedSum = kSumLog2 - kLift;                 // l is carried times 2^kLiftedSum
+constexpr float kLiftedUnit = kSumUnit / (1 << kLift);
 
 template <int D>
 __device__ __forceinline__ void reset(Running<D>& s) {
@@ -156,17 +160,17 @@ __device__ __forceinline__ void reset(Running<D>& s) {
   for (int i = 0; i < D / 16; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
   s.m[0] = s.m[1] = kLowest;
   s.l[0] = s.l[1] = 0.f;
-  s.high = -INFINITY;
+  s.odd = false;
 }
 
-// Raises the running maxima where a logit passes one by more than kLag (so p <=
-// 2^kLag) and rescales; lg: logits plus log2 s_V, rows gid, gid + 8 of the tile in the
+// Raises the running maxima where a logit passes one by more than kLag (so w <=
+// 2^(kLag + kLift)) and rescales; lg: logits plus log2 s_V, rows gid, gid + 8 of the tile in the
 // accumulator layout.
 template <int D>
 __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
   bool over = false;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) over |= fmaxf(lg[c], lg[2 + c]) > s.m[c] + kLag;
+  for (int c = 0; c < 2; ++c) over |= fmaxf(lg[c], lg[2 + c]) > s.m[c] + (kLag + kLift);
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -174,7 +178,7 @@ __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      top = fmaxf(top, s.m[c]);
+      top = fmaxf(top - kLift, s.m[c]);
       const float half = top == s.m[c] ? 1.f : fast_exp2(0.5f * (s.m[c] - top)), a = half * half;
       s.m[c] = top;
       s.l[c] = s.l[c] * half * half;
@@ -188,24 +192,24 @@ __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
 }
 
 // p of the tokens whose weight w has underflowed, for the sums of the two columns; lg as in
-// raise_max.  Out of line: for pages whose scale is next to nothing beside others' (kFar).
+// raise_max.  Out of line: for pages of scales that are next to nothing beside others'.
 static __device__ __noinline__ float2 lost_sums(float4 w, float4 lg, float off, float m0, float m1) {
   float2 l = make_float2(0.f, 0.f);
-  if (w.x == 0.f) l.x += whole_exp2(lg.x - off - m0 + kSumLog2);
-  if (w.y == 0.f) l.y += whole_exp2(lg.y - off - m1 + kSumLog2);
-  if (w.z == 0.f) l.x += whole_exp2(lg.z - off - m0 + kSumLog2);
-  if (w.w == 0.f) l.y += whole_exp2(lg.w - off - m1 + kSumLog2);
+  if (w.x == 0.f) l.x += whole_exp2(lg.x - off - m0 + kLiftedSum);
+  if (w.y == 0.f) l.y += whole_exp2(lg.y - off - m1 + kLiftedSum);
+  if (w.z == 0.f) l.x += whole_exp2(lg.z - off - m0 + kLiftedSum);
+  if (w.w == 0.f) l.y += whole_exp2(lg.w - off - m1 + kLiftedSum);
   return l;
 }
 
-// Adds a tile of weights to the sums; z: 2^kSumLog2 / s_V in the weights' units.
+// Adds a page's weights to the sums; z: 2^kLiftedSum / s_V.
 template <int D>
 __device__ __forceinline__ void add_sums(Running<D>& s, const float (&w)[4], const float (&lg)[4], float off,
                                          float z) {
   s.l[0] = fmaf(w[0] + w[2], z, s.l[0]);
   s.l[1] = fmaf(w[1] + w[3], z, s.l[1]);
-  s.high = fmaxf(s.high, off);
-  if (off < s.high - kFar) {
+  if (is_odd(off) || s.odd) {
+    s.odd |= off > 0.f;
     const float2 l = lost_sums(make_float4(w[0], w[1], w[2], w[3]), make_float4(lg[0], lg[1], lg[2], lg[3]),
                                off, s.m[0], s.m[1]);
     s.l[0] += l.x;
@@ -236,10 +240,9 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
       mma_f16(lg, a0, a1, a2, a3, q.b[4 * j + w][0], q.b[4 * j + w][1]);
     }
   }
-  constexpr float kUnit = kE4m3 ? 1.f : 16777216.f;
-  const float f0 = logit_factor(sc.x, q.fac[0], kUnit), f1 = logit_factor(sc.x, q.fac[1], kUnit);
-  const bool live = sc.y > 0.f;
-  const float off = live ? fast_log2(sc.y) : kZeroLog2;
+  const float sk = kE4m3 ? sc.x : sc.x * 64.f;
+  const float f0 = logit_factor(sk, q.fac[0]), f1 = logit_factor(sk, q.fac[1]);
+  const float scale = fmaxf(sc.y, kZeroScale), off = fast_log2(scale);
   lg[0] = fmaf(lg[0], f0, off);
   lg[1] = fmaf(lg[1], f1, off);
   lg[2] = fmaf(lg[2], f0, off);
@@ -253,12 +256,10 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
     }
   }
   raise_max<D>(s, lg);
-  // w <= 2^kLag, lifted by 2^6: below 2^14 in fp16
   float w[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - (s.m[r & 1] - kLift));
-  // 1 / s_V (2^110 for zeros) times 2^(kSumLog2 - kLift)
-  add_sums<D>(s, w, lg, off, (live ? fast_inverse(sc.y) : 1.298074214633707e33f) * (1.f / 262144.f));
+  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - s.m[r & 1]);
+  add_sums<D>(s, w, lg, off, fast_inverse(scale) * kLiftedUnit);
   // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
   // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
   uint32_t b0 = movmatrix_trans(pack_half2(w[0], w[1]));
@@ -283,14 +284,15 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
   }
 }
 
-// Takes 2^kLift and the codes' 2^-24 (int8) off the accumulators.
+// Takes the int8 codes' 2^-24 off the accumulators.
 template <int D, bool kE4m3>
 __device__ __forceinline__ void unscale(Running<D>& s) {
-  const float up = kE4m3 ? 1.f / 64.f : 262144.f;
+  if constexpr (!kE4m3) {
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s.o[i][r] *= up;
+      for (int r = 0; r < 4; ++r) s.o[i][r] *= 16777216.f;
+  }
 }
 
 // The largest finite magnitude of a pair of bf16, or `top`.
@@ -334,14 +336,23 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
   const int have = n - 4 * tig;
   const uint32_t m01 = (have > 0 ? 0xffffu : 0u) | (have > 1 ? 0xffff0000u : 0u);
   const uint32_t m23 = (have > 2 ? 0xffffu : 0u) | (have > 3 ? 0xffff0000u : 0u);
-  uint32_t top = 0, finite = 0;
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m01 & 0x7fff7fffu, v.y & m23 & 0x7fff7fffu),
                                  __vmaxu2(v.z & m01 & 0x7fff7fffu, v.w & m23 & 0x7fff7fffu)));
-    finite = finite_max(finite_max(finite, v.x & m01), v.y & m23);
-    finite = finite_max(finite_max(finite, v.z & m01), v.w & m23);
+  }
+  uint32_t finite = max(top & 0xffffu, top >> 16);
+  const bool plain = __all_sync(0xffffffffu, finite < 0x7f80u);
+  if (!plain) {
+    finite = 0;
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+      const uint4 v = vb[((i >> 1) * 32 + lane) * 2 + (i & 1)];
+      finite = finite_max(finite_max(finite, v.x & m01), v.y & m23);
+      finite = finite_max(finite_max(finite, v.z & m01), v.w & m23);
+    }
   }
   finite = __reduce_max_sync(0xffffffffu, finite);
   const int up = finite ? scale_up(finite) : static_cast<int>(-kZeroLog2);
@@ -356,10 +367,9 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
   float w[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - s.m[r & 1]);
-  add_sums<D>(s, w, lg, off, power_of_two(up) * (1.f / 4096.f));
+  add_sums<D>(s, w, lg, off, power_of_two(up) * kLiftedUnit);
   const float mul = power_of_two(up);
-  const bool plain = (top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u;
-  if (q.vis_min >= page0 + n && __all_sync(0xffffffffu, plain)) {
+  if (q.vis_min >= page0 + n && plain) {
     const __nv_bfloat162 mul2 = __float2bfloat162_rn(mul);
     uint32_t bh[2], bl[2];
     const uint32_t h0 = pack_bf162(w[0], w[1]), h1 = pack_bf162(w[2], w[3]);
@@ -501,11 +511,10 @@ __device__ __forceinline__ void start_part(const Kv8Params& p, const Entry& t, i
 // Channels ch .. ch + 3 of an output row; a row that sees nothing (l = 0) gets zeros.
 __device__ __forceinline__ void store_row(const Kv8Params& p, int b, int h, int gcol, int ch, int D,
                                           float4 o, float l) {
-  const Inverse inv = inverse_of(l);
+  const Inverse inv = inverse_of<kLiftedSum>(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D + ch;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf162(o.x * inv.a * inv.b, o.y * inv.a * inv.b),
-                                              pack_bf162(o.z * inv.a * inv.b, o.w * inv.a * inv.b));
+  *reinterpret_cast<uint2*>(dst) = make_uint2(over_sum(o.x, o.y, inv), over_sum(o.z, o.w, inv));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -815,13 +824,12 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
   if (!live) return;
-  const Inverse inv = inverse_of(l);
+  const Inverse inv = inverse_of<kLiftedSum>(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + kPer * lane);
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2)
-    dst[k / 2] = pack_bf162(acc[k] * inv.a * inv.b, acc[k + 1] * inv.a * inv.b);
+  for (int k = 0; k < kPer; k += 2) dst[k / 2] = over_sum(acc[k], acc[k + 1], inv);
 }
 
 // The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns

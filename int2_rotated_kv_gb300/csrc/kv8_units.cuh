@@ -16,27 +16,31 @@ constexpr float kLag = 8.f;                   // the maximum is raised when pass
 // of huge values that nothing attends to takes no bits from the others.  Outputs are sums of
 // w code, l the sum of w / s_V, both in units of 2^m.  Value scales go from 2^-109 to 2^121:
 //   - a page of zeros counts as one of scale 2^-110, below every other (kZeroLog2);
-//   - l is carried times 2^-12, so that 2^25 tokens of the least scale stay below 2^128;
-//   - where a scale lies 2^96 or more below the largest met (kFar), w / s_V may be lost with w, and
-//     2^(logit - m) takes its place;
+//   - l is carried times 2^-12 (2^-18 where m lies 2^6 lower, for weights of up to 2^14), so that
+//     2^25 tokens of the least scale stay below 2^128;
+//   - w / s_V is lost with w where a scale lies 2^100 below another's, which takes one outside
+//     [2^-64, 2^32] (is_odd): from then on 2^(logit - m) takes the place of a w that is 0;
 //   - a change of m by x takes l times 2^(x/2) twice, as 2^x alone may underflow;
 //   - 1 / l is two factors.
 constexpr float kZeroLog2 = -110.f;
-constexpr float kSumLog2 = -12.f;
-constexpr float kFar = 96.f;
+constexpr int kSumLog2 = -12;
+constexpr float kSumUnit = 1.f / 4096.f;   // 2^kSumLog2
+constexpr float kZeroScale = 7.703719777548943e-34f;   // 2^kZeroLog2
+__device__ __forceinline__ bool is_odd(float log2_scale) { return fabsf(log2_scale + 16.f) > 48.f; }
 
 __device__ __forceinline__ float power_of_two(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.  (Magnitudes
-// below 2^-113 come lower: both the power and its inverse stay normal.)
+// Power of two that brings a bf16 magnitude (bits) to [2^7, 2^8), as its exponent.  (From 2^120 on
+// it comes higher, to 65280 at most, which fp16 holds; below 2^-113 lower.  The power, its
+// inverse and the factors made of it stay normal.)
 __device__ __forceinline__ int scale_up(uint32_t amax) {
-  return amax ? max(-120, min(120, 134 - static_cast<int>(amax >> 7))) : 0;
+  return amax ? max(-112, min(120, 134 - static_cast<int>(amax >> 7))) : 0;
 }
 // A logit per unit of a column's q.K: the key scale times the column's factor, whose product may
 // overflow where q.K is 0 all the same.
-__device__ __forceinline__ float logit_factor(float scale, float fac, float unit = 1.f) {
-  return fminf(scale * fac * unit, 3.402823466e38f);
+__device__ __forceinline__ float logit_factor(float scale, float fac) {
+  return fminf(scale * fac, 3.402823466e38f);
 }
 
 __device__ __forceinline__ float fast_log2(float x) {
@@ -56,15 +60,20 @@ __device__ __forceinline__ float whole_exp2(float x) {
   return y;
 }
 
-// 1 / l of a sum l (carried times 2^kSumLog2, perhaps subnormal), 0 for 0: the product of two.
+// 1 / l of a sum l (carried times 2^kLog2, perhaps subnormal), 0 for 0: the product of two.
 struct Inverse {
   float a, b;
 };
+template <int kLog2>
 __device__ __forceinline__ Inverse inverse_of(float l) {
   const float up = l < 7.888609052210118e-31f ? 1.2676506002282294e30f     // 2^-100, 2^100
                    : l > 1.2676506002282294e30f ? 7.888609052210118e-31f
                                                 : 1.f;
-  return {l == 0.f ? 0.f : 1.f / (l * up), up * (1.f / 4096.f)};
+  return {l == 0.f ? 0.f : 1.f / (l * up), up * (1.f / (1 << -kLog2))};
+}
+// Two outputs x / l, y / l.
+__device__ __forceinline__ uint32_t over_sum(float x, float y, Inverse inv) {
+  return pack_bf162(x * inv.a * inv.b, y * inv.a * inv.b);
 }
 
 struct Kv8Params {
