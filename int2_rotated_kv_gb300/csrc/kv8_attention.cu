@@ -867,15 +867,15 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
     float high = top;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) high = fmaxf(high, ml[j].x);
-    const float old = fast_exp2(top - high);
+    const float shift = fast_exp2(0.5f * (top - high)), old = shift * shift;
     top = high;
-    l *= old;
+    l = l * shift * shift;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] *= old;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
-      const float w = fast_exp2(ml[j].x - top);
-      l = fmaf(w, ml[j].y, l);
+      const float half = fast_exp2(0.5f * (ml[j].x - top)), w = half * half;
+      l = fmaf(half * ml[j].y, half, l);
       acc[0] = fmaf(w, v[j][0].x, acc[0]);
       acc[1] = fmaf(w, v[j][0].y, acc[1]);
       acc[2] = fmaf(w, v[j][0].z, acc[2]);
@@ -886,11 +886,11 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
       acc[7] = fmaf(w, v[j][1].w, acc[7]);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const Inverse inv = inverse_of<kSumLog2>(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   *reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + ch) =
-      make_uint4(pack_bf162(acc[0] * inv, acc[1] * inv), pack_bf162(acc[2] * inv, acc[3] * inv),
-                 pack_bf162(acc[4] * inv, acc[5] * inv), pack_bf162(acc[6] * inv, acc[7] * inv));
+      make_uint4(over_sum(acc[0], acc[1], inv), over_sum(acc[2], acc[3], inv),
+                 over_sum(acc[4], acc[5], inv), over_sum(acc[6], acc[7], inv));
 }
 
 template <typename Kern, typename... Args>

@@ -4,7 +4,7 @@
 // Same mathematics, unit division and partial results as kv8_attention.cu.  Per tile
 // of 128 tokens (8 pages):
 //   S = Q K^T   M = 128 columns of queries, N = 128 tokens, K = d   (Q, K in shared memory)
-//   w = 2^(s_K fac S + log2 s_V - m)                                (a thread per query)
+//   w = 2^(s_K fac S + log2 s_V - m)       (a thread per query; kv8_units.cuh has the ranges)
 //   O += w V    M = 128, N = d, K = 128 tokens      (w in tensor memory, V in shared memory)
 // Here the bound is arithmetic, so the codes are turned into fp16 operands once per
 // tile and CTA (exact: integers up to 127, or e4m3 values) and the MMAs run from
@@ -46,9 +46,6 @@ namespace oscar {
 constexpr int kRWarps = 18;
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRTile = 128;        // tokens of a tile
-// A page of zeros (value scale 0) counts its tokens as one of scale 2^-64: far enough below any
-// page that matters not to push its weights out of fp16, and still in reach of fp32 sums.
-constexpr int kRZero = 64;
 constexpr int kRHidden = 0x7fff0000;   // position of a page slot that holds no page
 
 template <int D>
@@ -58,10 +55,11 @@ struct RowsSmem {
   static constexpr int kK = 0;
   static constexpr int kV = 2 * kTile16;
   static constexpr int kQ = 4 * kTile16;
-  static constexpr int kMeta = 5 * kTile16;                  // float4 [4][8]: s_K, log2 s_V, 1/s_V, position
+  static constexpr int kMeta = 5 * kTile16;                  // float4 [4][8]: s_K, log2 s_V, 2^-12/s_V, position
   static constexpr int kFac = kMeta + 512;                 // float [2][128]
   static constexpr int kMl = kFac + 1024;                  // float2 [2][2][128]
   static constexpr int kBad = kMl + 4096;                  // int [4]: tails that are not finite
+  static constexpr int kOdd = kBad + 16;                   // int [2][2]: see note_odd
   static constexpr int kBars = kBad + 64;
   static constexpr int kMisc = kBars + 40 * 8;
   static constexpr int kBytes = kMisc + 64;
@@ -263,7 +261,7 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
   const int n = len % kPage;
   const int up = scale_up(tail_magnitude<D>(area, 0, n, lane, odd));
   const uint32_t top_v = tail_magnitude<D>(area + Kv8Fmt<D>::kTailHalf, 1, n, lane, odd);
-  const int up_v = top_v ? scale_up(top_v) : kRZero;
+  const int up_v = top_v ? scale_up(top_v) : static_cast<int>(-kZeroLog2);
   const float mul = power_of_two(up);
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
@@ -278,7 +276,7 @@ __device__ __noinline__ float4 tail_keys(const Kv8Params& p, int b, int h, int l
     *bad = odd && ok;
     if (!ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
   }
-  return make_float4(power_of_two(-up), static_cast<float>(-up_v), power_of_two(up_v),
+  return make_float4(power_of_two(-up), static_cast<float>(-up_v), power_of_two(up_v) * kSumUnit,
                      __int_as_float(ok ? len / kPage * kPage : kRHidden));
 }
 
@@ -381,8 +379,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // The largest exponent s_K fac S + log2 s_V of a thread's row over a tile's visible tokens.
-// Two pages' 32 columns at a time, the next two pages' on their way.
-template <bool kMasked>
+// Two pages' 32 columns at a time, the next two pages' on their way.  kCareful: where the tile has a
+// token that a row does not see, or the unit odd scales (note_odd).
+template <bool kCareful>
 __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float fac, int vis) {
   float big = -INFINITY;
   auto pages = [&](const uint32_t (&s)[32], int j0) {
@@ -392,12 +391,12 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
       const int seen = vis - __float_as_int(pm.w);
       float x[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = !kMasked || k < seen ? __uint_as_float(s[16 * j + k]) : -INFINITY;
+      for (int k = 0; k < 16; ++k) x[k] = !kCareful || k < seen ? __uint_as_float(s[16 * j + k]) : -INFINITY;
 #pragma unroll
       for (int k = 0; k < 5; ++k) x[k] = max3(x[k], x[k + 5], x[k + 10]);
       const float top = fmaxf(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[15]));
       // (a hidden page's -inf times a scale of 0 would be NaN)
-      big = fmaxf(big, kMasked && top == -INFINITY ? top : fmaf(top, logit_factor(pm.x, fac), pm.y));
+      big = fmaxf(big, kCareful && top == -INFINITY ? top : fmaf(top, kCareful ? logit_factor(pm.x, fac) : pm.x * fac, pm.y));
     }
   };
   uint32_t a[32], b[32];
@@ -417,7 +416,7 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
 
 // w = 2^(s_K fac S + log2 s_V - m) of the row, as fp16 over the columns of S that have been
 // read; returns the sum of w / s_V.
-template <bool kMasked>
+template <bool kCareful>
 __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const float4* mt, float fac, int vis, float m) {
   float l = 0.f;
   auto pages = [&](const uint32_t (&s)[32], int j0) {
@@ -425,7 +424,7 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
     for (int j = 0; j < 2; ++j) {
       uint32_t out[8];
       const float4 pm = mt[j0 + j];
-      const float f = logit_factor(pm.x, fac), off = pm.y - m;
+      const float f = kCareful ? logit_factor(pm.x, fac) : pm.x * fac, off = pm.y - m;
       const uint64_t f2 = two(f, f), off2 = two(off, off);
       const int seen = vis - __float_as_int(pm.w);
       uint64_t sum[2];
@@ -433,7 +432,7 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
       for (int k = 0; k < 16; k += 2) {
         const uint64_t e = fma2(two(__uint_as_float(s[16 * j + k]), __uint_as_float(s[16 * j + k + 1])), f2, off2);
         float x0 = rows_exp2(first(e)), x1 = rows_exp2(second(e));
-        if constexpr (kMasked) {
+        if constexpr (kCareful) {
           x0 = k < seen ? x0 : 0.f;
           x1 = k + 1 < seen ? x1 : 0.f;
         }
@@ -443,7 +442,7 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
       }
       tc_st8(ts + 8 * (j0 + j), out);
       const uint64_t all = add2(sum[0], sum[1]);
-      if (!kMasked || seen > 0) l = fmaf(first(all) + second(all), pm.z, l);
+      if (!kCareful || seen > 0) l = fmaf(first(all) + second(all), pm.z, l);
     }
   };
   uint32_t a[32], b[32];
@@ -467,6 +466,55 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
   return l;
 }
 
+// A row's O in tensor memory times a.  (Out of line, as are the next two: in line they cost the
+// common path 1 to 2% in registers.)
+template <int D>
+__device__ __noinline__ void rescale_output(uint32_t to, float a) {
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tc_request16(to + 16 * c, o);
+    tc_wait_ld(o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+    tc_st16(to + 16 * c, o);
+  }
+}
+
+// Unit `seg` has a value scale outside the window of is_odd, or keys whose scale times a column's
+// factor (2^110 at most) may overflow: its number into the first word of two, and into the second for a
+// scale above the window.  Two units' words, as the pages are ahead of the softmax by one.
+constexpr float kOddKeys = 131072.f;
+static __device__ __noinline__ void note_odd(volatile int* odd_scale, uint32_t seg, float log2_scale) {
+  volatile int* odd = odd_scale + 2 * (seg & 1);
+  if (log2_scale > 0.f) odd[1] = static_cast<int>(seg) + 1;
+  odd[0] = static_cast<int>(seg) + 1;
+}
+
+// p of the row's visible tokens whose weights underflow in rows_weights, times 2^kSumLog2: for
+// units with odd scales; high: one above the window of is_odd, else only pages below it can
+// lose any.  The same exponents as there, so each token counts once.
+static __device__ __noinline__ float rows_lost(uint32_t ts, const float4* mt, float fac, int vis, float m,
+                                                bool high) {
+  float l = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) {
+    const float4 pm = mt[j];
+    if (!high && !is_odd(pm.y)) continue;   // (the same for all lanes)
+    const float f = logit_factor(pm.x, fac), off = pm.y - m;
+    const int seen = vis - __float_as_int(pm.w);
+    uint32_t s[16];
+    tc_request16(ts + 16 * j, s);
+    tc_wait_ld(s);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = __uint_as_float(s[k]);
+      if (k < seen && rows_exp2(fmaf(x, f, off)) == 0.f) l += whole_exp2(fmaf(x, f, static_cast<float>(kSumLog2) - m));
+    }
+  }
+  return l;
+}
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kRThreads, 1)
 kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
@@ -482,6 +530,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   float* facs = reinterpret_cast<float*>(smem + S::kFac);
   float2* mls = reinterpret_cast<float2*>(smem + S::kMl);
   volatile int* bad_tail = reinterpret_cast<volatile int*>(smem + S::kBad);
+  volatile int* odd_scale = reinterpret_cast<volatile int*>(smem + S::kOdd);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -502,6 +551,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     mbar_init(&bar->odone, 2);
     mbar_init(&bar->mlfull, 8);
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) odd_scale[i] = 0;
     fence_mbar_init();
   }
   if (warp == 16) tc_alloc(tmem_slot, 512);
@@ -689,11 +739,12 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
         if (lane < 2) {   // what the softmax needs of the two pages
           const int slot = 4 * lane + w;
-          const bool live = sc.y > 0.f;
+          const float scale = fmaxf(sc.y, kZeroScale), off = fast_log2(scale);
           meta[(g & 3) * 8 + slot] =
-              shown ? make_float4(sc.x, live ? __log2f(sc.y) : -kRZero, live ? __fdividef(1.f, sc.y) : power_of_two(kRZero),
+              shown ? make_float4(sc.x, off, fast_inverse(scale) * kSumUnit,
                                   __int_as_float((u.p0 + 8 * i + slot) * kPage))
                     : make_float4(0.f, -INFINITY, 0.f, __int_as_float(kRHidden));   // weight 0 without a mask
+          if (shown && (is_odd(off) || sc.x > kOddKeys)) note_odd(odd_scale, seg, off);
         }
         const int slot = u.tail_slot(i);
         if (i + 1 < u.tiles) {
@@ -701,7 +752,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         } else if (slot >= 0 && (slot & 3) == w) {   // over the zeros that stood for it
           __syncwarp();
           const float4 m = tail_keys<D>(p, u.t.b, u.h, u.t.len, dst + 8192 * (slot >> 2), lane, bad_tail + (seg & 3));
-          if (lane == 0) meta[(g & 3) * 8 + slot] = m;
+          if (lane == 0) {
+            meta[(g & 3) * 8 + slot] = m;
+            if (is_odd(m.y) || m.x > kOddKeys) note_odd(odd_scale, seg, m.y);
+          }
         }
         fence_proxy_async();
         arrive(&bar->kfull[buf]);
@@ -734,6 +788,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         const float fac = facs[(seg & 1) * 128 + rr];
         const bool idle = __all_sync(0xffffffffu, gcol >= p.cols);
         const int vis_least = __reduce_min_sync(0xffffffffu, vis);
+        const int unit = static_cast<int>(seg) + 1;
+        const volatile int* odd = odd_scale + 2 * (seg & 1);
         bool ok = true;
         for (int i = st; i < u.tiles; i += 2) {
           if (!(ok = wait(&bar->sfull[st], count))) break;
@@ -746,27 +802,19 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
             arrive(&bar->pfull[2 + st]);
             continue;
           }
-          const bool masked = (u.p0 + 8 * i + 8) * kPage > vis_least;   // (always with a tail)
-          const float big = masked ? rows_max<true>(ts, mt, fac, vis) : rows_max<false>(ts, mt, fac, vis);
+          const bool is_odd_unit = __any_sync(0xffffffffu, odd[0] == unit);   // (one answer for all lanes)
+          const bool careful = (u.p0 + 8 * i + 8) * kPage > vis_least || is_odd_unit;   // (always with a tail)
+          const float big = careful ? rows_max<true>(ts, mt, fac, vis) : rows_max<false>(ts, mt, fac, vis);
           const bool over = big > m + kLag;
-          if (__any_sync(0xffffffffu, over)) {
+          if (__any_sync(0xffffffffu, over) || is_odd_unit) {
             const float up = over ? big : m;
-            const float a = over ? rows_exp2(m - up) : 1.f;
+            const float half = over ? rows_exp2(0.5f * (m - up)) : 1.f, a = half * half;
             m = up;
-            l *= a;
-            if (i > 1) {   // the stream's O so far (its last MMA finished before this S began)
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tc_request16(to + 16 * c, o);
-                tc_wait_ld(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                tc_st16(to + 16 * c, o);
-              }
-            }
+            l = l * half * half;
+            if (i > 1) rescale_output<D>(to, a);   // so far (its last MMA finished before this S began)
+            if (is_odd_unit) l += rows_lost(ts, mt, fac, vis, m, __any_sync(0xffffffffu, odd[1] == unit));
           }
-          l += masked ? rows_weights<true>(&bar->pfull[st], ts, mt, fac, vis, m) : rows_weights<false>(&bar->pfull[st], ts, mt, fac, vis, m);
+          l += careful ? rows_weights<true>(&bar->pfull[st], ts, mt, fac, vis, m) : rows_weights<false>(&bar->pfull[st], ts, mt, fac, vis, m);
           tc_wait_st();
           tc_fence_before();
           arrive(&bar->pfull[2 + st]);
@@ -780,10 +828,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         tc_fence_after();
         const float2 other = ml[128 * (1 - st) + rr];
         top = fmaxf(m, other.x);
-        const float mine = rows_exp2(m - top), theirs = rows_exp2(other.x - top);
-        l = l * mine + other.y * theirs;
-        a0 = st ? theirs : mine;
-        a1 = st ? mine : theirs;
+        const float mine = rows_exp2(0.5f * (m - top)), theirs = rows_exp2(0.5f * (other.x - top));
+        l = l * mine * mine + other.y * theirs * theirs;
+        a0 = st ? theirs * theirs : mine * mine;
+        a1 = st ? mine * mine : theirs * theirs;
       }
       // channels [st * D/2, (st + 1) * D/2) of this column
       const bool complete = u.p0 == 0 && u.p1 == u.t.pages;
@@ -793,7 +841,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const int64_t tail_id = p.tail_ids ? p.tail_ids[u.t.b] : u.t.b;
       const uint16_t* tail = reinterpret_cast<const uint16_t*>(p.tail + (tail_id * p.hkv + u.h) * F::kTailBytes) +
           F::kTailHalf;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const Inverse inv = inverse_of<kSumLog2>(l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {   // 16 channels
         const int ch = st * (D / 2) + 16 * c;
@@ -831,8 +879,8 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll
             for (int k = 0; k < 16; k += 8)
               *reinterpret_cast<uint4*>(dst + k) =
-                  make_uint4(pack_bf162(o[k] * inv, o[k + 1] * inv), pack_bf162(o[k + 2] * inv, o[k + 3] * inv),
-                             pack_bf162(o[k + 4] * inv, o[k + 5] * inv), pack_bf162(o[k + 6] * inv, o[k + 7] * inv));
+                  make_uint4(over_sum(o[k], o[k + 1], inv), over_sum(o[k + 2], o[k + 3], inv),
+                             over_sum(o[k + 4], o[k + 5], inv), over_sum(o[k + 6], o[k + 7], inv));
           } else {
 #pragma unroll
             for (int k = 0; k < 16; k += 4)

@@ -108,6 +108,55 @@ def test_a_page_of_huge_values_that_nothing_attends_to(fmt, m, wide, jump):
 @pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("up,down", [(60, -60), (119, -10), (119, -95), (100, None)])
+def test_scales_far_apart_all_attended_to(fmt, m, wide, up, down):
+    """Pages of 2^up among pages of 2^down (or zeros) with weights of the same order: the small
+    ones' weights count in the sum though their values do not show.  The last sequence has one
+    large page, and only small ones behind it."""
+    s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=up)
+    k, v = K.draw(s.rng, 645 + 320 + 151, 1, 128)
+    v = np.clip(v, -64, 64)
+    small = np.arange(len(v)) // 16 % 3 > 0
+    small[965:] = True
+    small[965 + 32:965 + 48] = False
+    v[~small] *= np.float32(2.0 ** up)
+    v[small] *= np.float32(0.0 if down is None else 2.0 ** down)
+    s.place([645, 320, 151], k, bf16(v))
+    q = K.queries(s.rng, 3, m, 4, 128)
+    pos = rows_of(s, m)
+    check(s, s.attend(q, pos, wide=wide), q, pos)
+    assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("where", ["pages", "tail"])
+def test_the_largest_values_there_are(fmt, m, wide, where):
+    """Values of the largest bf16, both signs, in all pages or in a tail behind ordinary ones:
+    no sum of them overflows.  (All of a channel's have one sign, so the output is about as
+    large, and 0.9 of the largest keeps its rounding errors finite.)"""
+    s = K.Sequences(2, 1, 4, 128, fmt, 400, seed=5)
+    k, v = K.draw(s.rng, 395 + 167, 1, 128)
+    most = np.where(s.rng.random(128) < 0.5, -0.9 * BIG, 0.9 * BIG)
+    if where == "pages":
+        v[:] = bf16(most)
+    else:
+        v[384:395], v[395 + 160:] = bf16(most), bf16(most)
+    s.place([395, 167], k, v)
+    q = K.queries(s.rng, 2, m, 4, 128)
+    pos = rows_of(s, m)
+    if m > 1:
+        pos = np.maximum(pos, np.array([[384], [160]]))
+    got = s.attend(q, pos, wide=wide)
+    assert np.isfinite(got).all()
+    check(s, got, q, pos)
+    assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
 def test_the_largest_keys_against_tiny_queries(fmt, m, wide):
     """Keys of about the largest bf16, queries of 2^-122 to 2^-121: logits of a few units."""
     s = K.Sequences(2, 1, 4, 128, fmt, 400, seed=6)
