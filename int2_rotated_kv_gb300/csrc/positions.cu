@@ -5,7 +5,7 @@
 // sequence of n tokens: pages(n) = max(0, ceil((n - hold_back) / 16)).  One CTA forms
 // both exclusive prefix sums over the batch (rows, new pages) and advances the
 // lengths and the free-list cursor; the rows and the new table entries follow in
-// the same CTA when they are few, else in a grid of their own that finds each row's
+// the same CTA when the row lists are short, else in a grid of their own that finds each row's
 // sequence by bisection of the prefix sums.  Bound by latency (a chain of a scan and
 // two dependent loads) for a decode step, by the 16 bytes written per row for a
 // large prefill.  Measured: 256 sequences, a token each 4.6 us; 0.8 million rows
@@ -46,7 +46,7 @@ constexpr int kFillThreads = 256;
 // Prefix sums that a filling CTA bisects in shared memory (0.8 million rows of 256 sequences: 7.4 us
 // against 8.6 from L1).
 constexpr int kSharedStarts = 2048;
-// Rows that the scan's CTA writes itself.  Itself against a grid of its own: 256 rows 4.7 us
+// Rows that the scan's CTA writes itself, with the table entries of the step.  Itself against a grid of its own: 256 rows 4.7 us
 // against 5.6, 2048 rows 4.6 against 5.5, 4096 rows 5.4 against 5.3, 8192 rows 7.6 against 5.7.
 constexpr int64_t kInlineRows = 4096;
 
@@ -73,9 +73,10 @@ __device__ __forceinline__ int pages_held(int n, int hold) {
   return n > hold ? (n - hold - 1) / kPage + 1 : 0;
 }
 
-// Index of the sequence whose [starts[b], starts[b + 1]) holds i (starts ascend).
-__device__ __forceinline__ int sequence_of(const int32_t* starts, int batch, int i) {
-  int lo = 0, hi = batch;   // starts[lo] <= i < starts[hi]
+// Index of the sequence, `lo` or one behind it, whose [starts[b], starts[b + 1]) holds i (starts
+// ascend).
+__device__ __forceinline__ int sequence_of(const int32_t* starts, int batch, int i, int lo = 0) {
+  int hi = batch;   // starts[lo] <= i < starts[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (starts[mid] <= i) lo = mid; else hi = mid;
@@ -89,9 +90,49 @@ __device__ __forceinline__ int fresh_page(const PagesParams& p, int first, int p
   return at < p.n_free ? p.free_pages[at] : -1;
 }
 
+// Many new table entries by the scan's CTA, as it has them when the caller takes few row lists of
+// many new tokens, or none: a warp takes runs of 32 * kRun, a lane every 32nd of them, with its loads in
+// flight together and a bisection only where a sequence ends.  256 prompts of 4096 tokens, 65280
+// entries: 18 us, where an entry at a time takes 56.  (Out of line, and not for the few of a decode
+// step or for a grid, which it makes slower: 4.6 us to 5.0, 7.4 to 8.9.)
+constexpr int kManyEntries = 8192;
+static __device__ __noinline__ void fill_entries(const PagesParams& p, int first, int fresh) {
+  constexpr int kRun = 8;
+  const int32_t* free_pages = p.free_pages + first;   // (not read where there are none)
+  const int here = static_cast<int>(max(static_cast<int64_t>(0), min(p.n_free - first, static_cast<int64_t>(fresh))));
+  for (int64_t j = 32 * kRun * (threadIdx.x >> 5) + (threadIdx.x & 31); j < fresh; j += kScanThreads * kRun) {
+    const int j0 = static_cast<int>(j), left = (fresh - j0 - 1) / 32 + 1;   // entries of this lane
+    int b = 0, end = j0, last = 0;   // entries [.., end) are sequence b's, of which [.., last) have a column
+    int32_t* row = nullptr;
+    int32_t* dst[kRun];
+    int id[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      dst[k] = nullptr;
+      if (k < left) {
+        const int at = j0 + 32 * k;
+        if (at >= end) {
+          b = sequence_of(p.page_starts, p.batch, first + at, b);
+          const int begin = p.page_starts[b] - first;
+          end = p.page_starts[b + 1] - first;
+          const int held = pages_held(p.lens_after[b] - (p.row_starts[b + 1] - p.row_starts[b]), p.hold);
+          row = p.table + static_cast<int64_t>(b) * p.max_pages + held - begin;
+          last = p.max_pages - held + begin;
+        }
+        if (at < last) dst[k] = row + at;
+        id[k] = at < here ? free_pages[at] : -1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (dst[k]) *dst[k] = id[k];
+  }
+}
+
 // Rows and new table entries, `i` of `n` workers.  A worker writes runs of four rows:
 // one bisection, then the next sequence where its rows end.  row_starts, page_starts: the
-// step's, or a copy of them in shared memory.
+// step's, or a copy of them in shared memory.  kScan: by the scan's CTA.
+template <bool kScan>
 __device__ __forceinline__ void fill_rows(const PagesParams& p, const int32_t* row_starts,
                                           const int32_t* page_starts, int64_t i, int64_t n) {
   const int64_t rows = row_starts[p.batch];
@@ -143,6 +184,10 @@ __device__ __forceinline__ void fill_rows(const PagesParams& p, const int32_t* r
   }
   const int first = page_starts[0];
   const int64_t fresh = static_cast<int64_t>(page_starts[p.batch]) - first;
+  if (kScan && fresh > kManyEntries) {
+    fill_entries(p, first, static_cast<int>(fresh));
+    return;
+  }
   for (int64_t j = i; j < fresh; j += n) {
     const int at = first + static_cast<int>(j);
     const int b = sequence_of(page_starts, p.batch, at);
@@ -221,7 +266,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_scan_kernel(const __grid_
   }
   if (p.fill) {
     __syncthreads();   // this CTA's global writes above are read back
-    fill_rows(p, p.row_starts, p.page_starts, tid, kScanThreads);
+    fill_rows<true>(p, p.row_starts, p.page_starts, tid, kScanThreads);
   }
 }
 
@@ -237,9 +282,9 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(const __grid_
     }
     __syncthreads();
   }
-  fill_rows(p, few ? starts[0] : p.row_starts, few ? starts[1] : p.page_starts,
-            static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x,
-            static_cast<int64_t>(gridDim.x) * kFillThreads);
+  fill_rows<false>(p, few ? starts[0] : p.row_starts, few ? starts[1] : p.page_starts,
+                   static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x,
+                   static_cast<int64_t>(gridDim.x) * kFillThreads);
 }
 
 // ----------------------------------------------------------------------- rotary
