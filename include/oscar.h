@@ -477,8 +477,10 @@ oscar_status oscar_kv8_gather(const oscar_kv8_desc* desc, const int32_t* seq_len
                               int64_t total_rows, int32_t max_rows, void* k_out, void* v_out,
                               void* stream);
 
-/* Bytes of device workspace for oscar_kv8_attention; 0 for invalid arguments.  Does
- * not grow with the batch (at most two partial results per resident CTA). */
+/* Bytes of device workspace for oscar_kv8_attention; 0 for invalid arguments.  Enough
+ * for every call on the same cache with no more sequences, rows and tokens than these
+ * too, whichever form of the kernel it takes.  At most two partial results per
+ * resident CTA, so it stops growing with the batch. */
 size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows,
                                 int32_t max_seq_len);
 
@@ -492,8 +494,8 @@ size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32
  *     q_pos[b][m].
  * A row that sees nothing (length 0, or a negative position: a padded row) gets
  * zeros; a length outside its range or a position at or behind the length does
- * too and sets OSCAR_DEVERR_SEQ_LEN.  workspace: oscar_kv8_workspace_size bytes,
- * 16-byte aligned, no initial contents; calls that may overlap on the GPU need one
+ * too and sets OSCAR_DEVERR_SEQ_LEN.  workspace: oscar_kv8_workspace_size bytes
+ * (of this call or a larger one), 16-byte aligned, no initial contents; calls that may overlap on the GPU need one
  * each.  The result does not depend on the order in which CTAs run.  Asynchronous. */
 oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
                                  const int32_t* q_pos, int32_t batch, int32_t m_rows,

@@ -972,7 +972,17 @@ struct Kv8Plan {
   int cluster, team;   // cluster > 0: CTAs per unit; team > 0: warps per unit
   int64_t tiles, entries, ctas;
   size_t info, total;   // workspace bytes: the CTAs' records, all
+  size_t most;          // no call of fewer sequences, rows or tokens takes more than this
 };
+
+// CTAs that share the pages of `units`, and the workspace bytes of their records and parts.
+inline int64_t share_ctas(bool rows, int64_t units, int64_t pages, int64_t sms) {
+  return std::min(std::min<int64_t>(kMaxCtas, rows ? sms : 2 * sms), (units * pages + kMinShare - 1) / kMinShare);
+}
+inline size_t record_bytes(int64_t ctas) { return (static_cast<size_t>(ctas) * sizeof(int4) + 255) / 256 * 256; }
+inline size_t share_bytes(bool rows, int d, int64_t ctas) {
+  return record_bytes(ctas) + static_cast<size_t>(ctas) * 2 * (rows ? 128 : 8) * (d + 2) * sizeof(float);
+}
 
 // Several sequences are taken as three quarters of the longest: the host does not know the
 // lengths.
@@ -1047,14 +1057,14 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
   p.tiles = p.rows ? tiles128 : tiles8;
   p.entries = batch * p.tiles;
   const int64_t units = p.entries * h;
-  const int64_t resident = std::min<int64_t>(kMaxCtas, p.rows ? sms : 2 * sms);
   p.ctas = p.team      ? (units * p.team + 7) / 8
            : p.cluster ? units * p.cluster
-                       : std::min(resident, (units * pages + kMinShare - 1) / kMinShare);
-  p.info = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
-  p.total = p.cluster || p.team
-                ? 16
-                : p.info + static_cast<size_t>(p.ctas) * 2 * (p.rows ? 128 : 8) * (d + 2) * sizeof(float);
+                       : share_ctas(p.rows, units, pages, sms);
+  p.info = record_bytes(p.ctas);
+  p.total = p.cluster || p.team ? 16 : share_bytes(p.rows, d, p.ctas);
+  // a smaller call may take another form: shares in narrow tiles at most, or in wide ones
+  p.most = share_bytes(false, d, share_ctas(false, units8, pages, sms));
+  if (cols > 8) p.most = std::max(p.most, share_bytes(true, d, share_ctas(true, batch * tiles128 * h, pages, sms)));
   *out = p;
   return true;
 }
@@ -1121,7 +1131,7 @@ size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32
   if (oscar_host::check_kv8(desc) != OSCAR_OK || batch < 1 || m_rows < 1 || max_seq_len < 1 ||
       !kv8_plan(desc, batch, m_rows, max_seq_len, &pl))
     return 0;
-  return pl.total;
+  return pl.most;
 }
 
 oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
