@@ -455,6 +455,13 @@ def _rows(fn: str, name: str, t, n: int, heads: int, d: int, index: int) -> int:
     return row if n > 1 else heads * d
 
 
+def _fits(fn: str, name: str, value: int) -> int:
+    """An argument that the library takes as int32: ctypes would cut it."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{fn}: {name} is outside the range of int32")
+    return value
+
+
 def _device_of(fn: str, name: str, t) -> int:
     if _INT32 is None:
         _bind_torch()
@@ -556,7 +563,7 @@ def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int
         raise ValueError(f"{fn}: row_starts must have batch + 1 entries, and the page table a row "
                          "per sequence")
     _launch(fn, index, stream, desc, k.data_ptr(), v.data_ptr(), ks, vs, lens, starts, batch, n,
-            max_new)
+            _fits(fn, "max_new", max_new))
 
 
 def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
@@ -575,13 +582,17 @@ def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int
     if first.numel() != batch or row_starts.numel() != batch + 1 or batch > rows:
         raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1, and the page "
                          "table a row per sequence")
-    _launch(fn, index, stream, desc, lens, begin, starts, batch, n, max_rows, k_out.data_ptr(),
-            v_out.data_ptr())
+    _launch(fn, index, stream, desc, lens, begin, starts, batch, n, _fits(fn, "max_rows", max_rows),
+            k_out.data_ptr(), v_out.data_ptr())
 
 
 def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
+    """Bytes for oscar_kv8_attention of no more sequences, rows and tokens; 0: invalid."""
     import torch
+    fn = "oscar_kv8_workspace_size"
     _, desc, index, _ = cache._checked()
+    for name, value in (("batch", batch), ("m_rows", m_rows), ("max_seq_len", max_seq_len)):
+        _fits(fn, name, value)
     with torch.cuda.device(index):   # its number of SMs counts
         return int(lib().oscar_kv8_workspace_size(desc, batch, m_rows, max_seq_len))
 
@@ -610,7 +621,8 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
     if batch > rows or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"{fn}: the page table must have a row per sequence, and the workspace be "
                          f"a contiguous tensor on cuda:{index}")
-    _launch(fn, index, stream, desc, q.data_ptr(), lens, pos, batch, m_rows, max_seq_len,
+    _launch(fn, index, stream, desc, q.data_ptr(), lens, pos, batch, m_rows,
+            _fits(fn, "max_seq_len", max_seq_len),
             out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
@@ -641,7 +653,8 @@ def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_af
                               or not slots.is_contiguous() or slots.numel() != rows):
         raise ValueError(f"{fn}: slots must be a contiguous int64 tensor on cuda:{index} with a "
                          "row per seq_ids row")
-    _launch(fn, index, stream, table, page_table.shape[1], before, new, batch, hold_back, free,
+    _launch(fn, index, stream, table, page_table.shape[1], before, new, batch,
+            _fits(fn, "hold_back", hold_back), free,
             free_pages.numel(), at, after, ps, rs, ids, pos, _ptr(slots), rows,
             None if status is None else _i32(fn, "status", status, index))
 
@@ -650,6 +663,8 @@ def oscar_rope_phases(base: float, rotary_dim: int, factor: float = 1.0, origina
                       low_turns: float = 1.0, high_turns: float = 32.0) -> np.ndarray:
     """Rotary frequencies of oscar_rope, uint64 [rotary_dim / 2] (turns per token times
     2^64): unscaled, divided by `factor`, or (original_len > 0) scaled by parts."""
+    for name, value in (("rotary_dim", rotary_dim), ("original_len", original_len)):
+        _fits("oscar_rope_phases", name, int(value))
     out = np.zeros(max(int(rotary_dim) // 2, 1), np.uint64)
     _check("oscar_rope_phases",
            lib().oscar_rope_phases(float(base), int(rotary_dim), float(factor), int(original_len),
