@@ -492,11 +492,19 @@ size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32
  *   q_pos: null for a decode step (m_rows = 1: the row sees all tokens), else
  *     device int32 [batch][m_rows]: row m of sequence b sees positions 0 ..
  *     q_pos[b][m].
+ *   The form of the kernel, and so the time, goes by max_seq_len and not by the lengths:
+ *   256 sequences of 100-200 tokens take 23 us with 200 announced, 56 us with 131072.
+ * Arithmetic: q.k of 8-bit keys in fp32 from exact codes and q rounded to fp16 after a
+ * power of two (exact down to 2^-21 of a head's largest channel); the weight p times the
+ * page's value scale rounded to fp16, relative to the largest such product that the row
+ * has met (11 bits down to 2^-20 of it, in the form for many rows to 2^-14, and fewer
+ * below); sums in fp32.  Any finite keys, values and queries whose logits fit fp32.
  * A row that sees nothing (length 0, or a negative position: a padded row) gets
  * zeros; a length outside its range or a position at or behind the length does
  * too and sets OSCAR_DEVERR_SEQ_LEN.  workspace: oscar_kv8_workspace_size bytes
- * (of this call or a larger one), 16-byte aligned, no initial contents; calls that may overlap on the GPU need one
- * each.  The result does not depend on the order in which CTAs run.  Asynchronous. */
+ * (of this call or a larger one), 16-byte aligned, no initial contents; calls that
+ * may overlap on the GPU need one each.  The result does not depend on the order in
+ * which CTAs run.  Asynchronous. */
 oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
                                  const int32_t* q_pos, int32_t batch, int32_t m_rows,
                                  int32_t max_seq_len, void* out, void* workspace,
@@ -521,6 +529,8 @@ oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, cons
  *     row_starts[batch] on (what oscar_prefill_quantize and oscar_rope take);
  *     slots [max_rows], optional: page id * 16 + position % 16, or -1 where the
  *     table has no page for the token.
+ *   max_rows: beyond 4096, a grid writes lists and table entries; up to it, 0 included, one
+ *     CTA does, and takes 18 us for the 65280 entries of 256 prompts of 4096 tokens.
  * All device memory; no two of the outputs may overlap.  A sequence with a
  * negative length or count, or whose tokens do not fit its table row, gets no
  * tokens, and rows beyond max_rows are not written (OSCAR_DEVERR_SEQ_LEN in
@@ -540,6 +550,10 @@ oscar_status oscar_extend_pages(int32_t* page_table, int32_t max_pages_per_seq, 
  *   original_len > 0: by parts.  With r = f_i * original_len turns over the original
  *     context and keep = clamp((r - low_turns) / (high_turns - low_turns), 0, 1):
  *     (1 - keep) f_i / factor + keep f_i.
+ * keep is linear in r.  Models are also served with a ramp that is linear in the pair's
+ * index i, between bounds rounded to integers: other angles for the same factor and
+ * lengths (base 10^6, rotary_dim 128, 32768 tokens, factor 4, turns 1 and 32: pair 31
+ * has 0.38 f_i here and 0.65 f_i there).  oscar_rope takes any words, the caller's own too.
  * base > 1, factor >= 1, low_turns < high_turns, all finite; rotary_dim even.
  * Host call; phases_out is host memory, to be copied to the device once. */
 oscar_status oscar_rope_phases(double base, int32_t rotary_dim, double factor, int32_t original_len,

@@ -601,7 +601,8 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
                         stream=None):
     """Attention over the 8-bit cache.  Decode: q, out bf16 [B][Hq][d], every row sees
     the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
-    row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros)."""
+    row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros).
+    max_seq_len decides the form of the kernel: announce no more than is needed."""
     fn = "oscar_kv8_attention"
     _, desc, index, rows = cache._checked()
     lens, batch = _i32(fn, "seq_lens", seq_lens, index), seq_lens.numel()
@@ -662,7 +663,9 @@ def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_af
 def oscar_rope_phases(base: float, rotary_dim: int, factor: float = 1.0, original_len: int = 0,
                       low_turns: float = 1.0, high_turns: float = 32.0) -> np.ndarray:
     """Rotary frequencies of oscar_rope, uint64 [rotary_dim / 2] (turns per token times
-    2^64): unscaled, divided by `factor`, or (original_len > 0) scaled by parts."""
+    2^64): unscaled, divided by `factor`, or (original_len > 0) scaled by parts, with a
+    ramp that is linear in the turns over original_len (not in the pair's index, as
+    some models have it: their words are the caller's to form)."""
     for name, value in (("rotary_dim", rotary_dim), ("original_len", original_len)):
         _fits("oscar_rope_phases", name, int(value))
     out = np.zeros(max(int(rotary_dim) // 2, 1), np.uint64)

@@ -38,9 +38,9 @@
 // next unit meanwhile.
 //
 // Bound by HBM: 2d + 1 bytes per token and KV head.  Measured, 8 KV heads, d = 128: 64
-// sequences of 4096-8192 tokens 135 us, 5990 GB/s (shares); one of 131071 tokens 48 us, 5610
+// sequences of 4096-8192 tokens 134 us, 6010 GB/s (shares); one of 131071 tokens 47.9 us, 5630
 // GB/s (clusters of 16 for 7 heads would leave one for a second round, so 12; 96 of 152 SMs);
-// one of 32768 18.7 us, 3600 GB/s, of which 5 us are the launch, the first pages and the merge.
+// one of 32768 18.5 us, 3640 GB/s, of which 5 us are the launch, the first pages and the merge.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -1015,7 +1015,7 @@ inline double rows_us(int d, int64_t batch, int64_t units, int64_t pages, int64_
 
 // The largest cluster of which the device holds one per unit at a time; 0: shares are faster,
 // as they touch only the tokens there are, or there is none.  Measured, 8 KV heads: one
-// sequence of 32k 18.6 us against 23.9, of 128k 48.7 against 54.
+// sequence of 32k 18.6 us against 23.9, of 128k 48.7 against 54 (both in one run).
 inline int cluster_of(int d, int64_t batch, int64_t units, int64_t pages) {
   const ClusterSizes s = cluster_sizes();
   int c = kMaxCluster;

@@ -27,7 +27,7 @@
 // at d = 128 and shared memory 1536 (fp16 tiles written once and read by the MMAs, Q read per
 // tile); a tile takes 2400, in which a K warp is busy for 1950 and a stream's chain S, softmax,
 // O is longer than its share.  Measured, d = 128, 8 KV heads, G = 4: 2048 rows over 32768 tokens
-// 1055 us, 1042 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86 us, 554 TFLOP/s of
+// 1050 us, 1047 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86.3 us, 552 TFLOP/s of
 // rows that exist (260 columns are 3 tiles: a third of the work is for 4 of them).
 // Registers: 96 a thread for 18 warps.  Whatever is spilled in a role's loop costs more than
 // it saves elsewhere (16 registers' worth: 7 of 98 us), and code that is fetched cold costs its
