@@ -12,8 +12,8 @@
 //   logit = s_K * (sum_c (u_c - 128) q_c),  the -128 sum_c q_c as the initial
 //     accumulator (int8); q enters as fp16 scaled by a power of two per column,
 //     which keeps all 8 bits of every bf16 within 2^-21 of the column's largest.
-//   o += (p s_V) code,  p s_V rounded once to fp16 (2^-12 relative, unbiased; the
-//     exponent carries s_V, see kv8_units.cuh) and lifted by 2^6, so that it has its
+//   o += (p s_V) code,  p s_V rounded once to fp16 (2^-12 relative, unbiased), in a unit of
+//     each column's own (kv8_units.cuh) that leaves it its
 //     11 bits down to 2^-20 of the column's largest p s_V.  int8 value
 //     codes lose their 128 before the MMA (one fp16 add per two codes): summed
 //     with it over hundreds of pages, the accumulator's truncation of sums of
@@ -38,9 +38,9 @@
 // next unit meanwhile.
 //
 // Bound by HBM: 2d + 1 bytes per token and KV head.  Measured, 8 KV heads, d = 128: 64
-// sequences of 4096-8192 tokens 134 us, 6010 GB/s (shares); one of 131071 tokens 47.9 us, 5630
+// sequences of 4096-8192 tokens 135 us, 5990 GB/s (shares); one of 131071 tokens 48.3 us, 5580
 // GB/s (clusters of 16 for 7 heads would leave one for a second round, so 12; 96 of 152 SMs);
-// one of 32768 18.5 us, 3640 GB/s, of which 5 us are the launch, the first pages and the merge.
+// one of 32768 18.8 us, 3590 GB/s, of which 5 us are the launch, the first pages and the merge.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -61,11 +61,12 @@ struct Kv8Cfg {
   static constexpr int kWarpRing = kStages * F::kBlock;
   static constexpr int kStride = D + 4;                     // floats per column when merging
   static constexpr int kMerge = kWarps * 8 * kStride * 4;
-  static constexpr int kStat = kWarps * 8 * 4;              // one of m, l
+  static constexpr int kStat = kWarps * 8 * 4;              // one of m, k, l
   static constexpr int kSlot = kv8_slot<D, 1>();
   static constexpr int kMergeOff = kWarps * kWarpRing;
   static constexpr int kStatOff = kMergeOff + kMerge;
-  static constexpr int kPartOff = kStatOff + 2 * kStat;     // a cluster's CTA: its partial
+  static constexpr int kUnitOff = kStatOff + 3 * kStat;     // float2: units that the parts are brought to
+  static constexpr int kPartOff = kUnitOff + kWarps * 8 * 8;   // a cluster's CTA: its partial
   static constexpr int kBarOff = kPartOff + (kMode == kCluster ? kSlot * 4 : 0);
   static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
   static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
@@ -142,35 +143,40 @@ __device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, i
 }
 
 // A warp's running result for its columns.  o: accumulator tiles, element
-// [2i + y][r + 2x] is channel 32i + 4gid + 2y + x of column 2tig + r.
+// [2i + y][r + 2x] is channel 32i + 4gid + 2y + x of column 2tig + r, in units of 2^(m + k).
+// l: the sum of p = 2^(logit - m).
 template <int D>
 struct Running {
   float o[D / 16][4];
-  float m[2], l[2];
-  bool odd;              // a scale has been above the window of is_odd
+  float m[2], k[2], l[2];
 };
-// Here m lies kLift below the largest logit + log2 s_V (weights reach 2^14).
-constexpr int kLift = 6;
-constexpr int kLiftedSum = kSumLog2 - kLift;                 // l is carried times 2^kLiftedSum
-constexpr float kLiftedUnit = kSumUnit / (1 << kLift);
+// Weights w = p 2^(log2 s_V - k) reach 2^(kLag + kLift): k lies kLift below the largest p s_V when it is set.
+constexpr float kLift = 6.f;
 
 template <int D>
 __device__ __forceinline__ void reset(Running<D>& s) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) s.o[i][0] = s.o[i][1] = s.o[i][2] = s.o[i][3] = 0.f;
-  s.m[0] = s.m[1] = kLowest;
+  s.m[0] = s.m[1] = kNoUnit.m;
+  s.k[0] = s.k[1] = kNoUnit.k;
   s.l[0] = s.l[1] = 0.f;
-  s.odd = false;
 }
 
-// Raises the running maxima where a logit passes one by more than kLag (so w <=
-// 2^(kLag + kLift)) and rescales; lg: logits plus log2 s_V, rows gid, gid + 8 of the tile in the
-// accumulator layout.
+// w and p of a tile of tokens with values of scale 2^off, p added to the sums.  lg: logits, rows gid,
+// gid + 8 of the tile in the accumulator layout.  Where a logit passes its column's m by more than kLag, or
+// a weight 2^(kLag + kLift), m and k are raised first: l changes with m, o with m + k.  (Both columns at
+// once where there is an instruction for it: 24 columns over 32k tokens 33.2 to 32.5 us.)
 template <int D>
-__device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
+__device__ __forceinline__ void weigh(Running<D>& s, const float (&lg)[4], float off, float (&w)[4]) {
+  float e[4], up[2];   // exponents of p; of a weight's factor beside it
   bool over = false;
+  const uint64_t less = two(-1.f, -1.f), m2 = two(s.m[0], s.m[1]);
+  const uint64_t e0 = fma2(m2, less, two(lg[0], lg[1])), e1 = fma2(m2, less, two(lg[2], lg[3]));
+  const uint64_t u2 = fma2(two(s.k[0], s.k[1]), less, two(off, off));
+  e[0] = first(e0); e[1] = second(e0); e[2] = first(e1); e[3] = second(e1);
+  up[0] = first(u2); up[1] = second(u2);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) over |= fmaxf(lg[c], lg[2 + c]) > s.m[c] + (kLag + kLift);
+  for (int c = 0; c < 2; ++c) over |= fmaxf(e[c], e[2 + c]) > fminf(kLag, kLag + kLift - up[c]);
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -178,10 +184,16 @@ __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      top = fmaxf(top - kLift, s.m[c]);
-      const float half = top == s.m[c] ? 1.f : fast_exp2(0.5f * (s.m[c] - top)), a = half * half;
-      s.m[c] = top;
-      s.l[c] = s.l[c] * half * half;
+      const float m = fmaxf(top, s.m[c]), down = s.m[c] - m;
+      // the unit as it is, seen from m; and what this page needs
+      const float k0 = s.k[c] + down, k = fmaxf(fmaxf(k0, top - m + off - kLift), kNoUnit.k);
+      s.l[c] *= fast_exp2(down);
+      const float a = fast_exp2(k0 - k);
+      s.m[c] = m;
+      s.k[c] = k;
+      e[c] = lg[c] - m;
+      e[2 + c] = lg[2 + c] - m;
+      up[c] = off - k;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         s.o[i][c] *= a;
@@ -189,32 +201,16 @@ __device__ __forceinline__ void raise_max(Running<D>& s, const float (&lg)[4]) {
       }
     }
   }
-}
-
-// p of the tokens whose weight w has underflowed, for the sums of the two columns; lg as in
-// raise_max.  Out of line: for pages of scales that are next to nothing beside others'.
-static __device__ __noinline__ float2 lost_sums(float4 w, float4 lg, float off, float m0, float m1) {
-  float2 l = make_float2(0.f, 0.f);
-  if (w.x == 0.f) l.x += whole_exp2(lg.x - off - m0 + kLiftedSum);
-  if (w.y == 0.f) l.y += whole_exp2(lg.y - off - m1 + kLiftedSum);
-  if (w.z == 0.f) l.x += whole_exp2(lg.z - off - m0 + kLiftedSum);
-  if (w.w == 0.f) l.y += whole_exp2(lg.w - off - m1 + kLiftedSum);
-  return l;
-}
-
-// Adds a page's weights to the sums; z: 2^kLiftedSum / s_V.
-template <int D>
-__device__ __forceinline__ void add_sums(Running<D>& s, const float (&w)[4], const float (&lg)[4], float off,
-                                         float z) {
-  s.l[0] = fmaf(w[0] + w[2], z, s.l[0]);
-  s.l[1] = fmaf(w[1] + w[3], z, s.l[1]);
-  if (is_odd(off) || s.odd) {
-    s.odd |= off > 0.f;
-    const float2 l = lost_sums(make_float4(w[0], w[1], w[2], w[3]), make_float4(lg[0], lg[1], lg[2], lg[3]),
-                               off, s.m[0], s.m[1]);
-    s.l[0] += l.x;
-    s.l[1] += l.y;
-  }
+  // (finite: it meets p of 0 where it is large)
+  const uint64_t scale = two(fast_exp2(fminf(up[0], 126.f)), fast_exp2(fminf(up[1], 126.f)));
+  const uint64_t p0 = two(fast_exp2(e[0]), fast_exp2(e[1])), p1 = two(fast_exp2(e[2]), fast_exp2(e[3]));
+  const uint64_t l = add2(two(s.l[0], s.l[1]), add2(p0, p1)), w0 = mul2(p0, scale), w1 = mul2(p1, scale);
+  s.l[0] = first(l);
+  s.l[1] = second(l);
+  w[0] = first(w0);
+  w[1] = second(w0);
+  w[2] = first(w1);
+  w[3] = second(w1);
 }
 
 // One page of codes at `st`.
@@ -242,11 +238,9 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
   }
   const float sk = kE4m3 ? sc.x : sc.x * 64.f;
   const float f0 = logit_factor(sk, q.fac[0]), f1 = logit_factor(sk, q.fac[1]);
-  const float scale = fmaxf(sc.y, kZeroScale), off = fast_log2(scale);
-  lg[0] = fmaf(lg[0], f0, off);
-  lg[1] = fmaf(lg[1], f1, off);
-  lg[2] = fmaf(lg[2], f0, off);
-  lg[3] = fmaf(lg[3], f1, off);
+  // (rounded by themselves, not on the way to a difference, so that equal logits stay equal)
+#pragma unroll
+  for (int r = 0; r < 4; ++r) lg[r] = __fmul_rn(lg[r], r & 1 ? f1 : f0);
   if (page0 + kPage > q.vis_min) {
     const int t = page0 + 2 * gid;
 #pragma unroll
@@ -255,11 +249,8 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
       if (t + 1 >= q.vis[c]) lg[2 + c] = -INFINITY;
     }
   }
-  raise_max<D>(s, lg);
   float w[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - s.m[r & 1]);
-  add_sums<D>(s, w, lg, off, fast_inverse(scale) * kLiftedUnit);
+  weigh<D>(s, lg, fast_log2(sc.y), w);   // (a page of zeros: log2 0 = -inf, weights of 0)
   // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed, the two
   // registers hold tokens (4tig, 4tig + 2) and (4tig + 1, 4tig + 3) of column gid
   uint32_t b0 = movmatrix_trans(pack_half2(w[0], w[1]));
@@ -355,20 +346,17 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
     }
   }
   finite = __reduce_max_sync(0xffffffffu, finite);
-  const int up = finite ? scale_up(finite) : static_cast<int>(-kZeroLog2);
-  const float off = static_cast<float>(-up);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int seen = min(n, q.vis[c] - page0);   // tokens of the tail this column sees
-    lg[c] = 2 * gid < seen ? fmaf(lg[c], p.scale_log2, off) : -INFINITY;
-    lg[2 + c] = 2 * gid + 1 < seen ? fmaf(lg[2 + c], p.scale_log2, off) : -INFINITY;
+    lg[c] = 2 * gid < seen ? __fmul_rn(lg[c], p.scale_log2) : -INFINITY;
+    lg[2 + c] = 2 * gid + 1 < seen ? __fmul_rn(lg[2 + c], p.scale_log2) : -INFINITY;
   }
-  raise_max<D>(s, lg);
-  float w[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) w[r] = fast_exp2(lg[r] - s.m[r & 1]);
-  add_sums<D>(s, w, lg, off, power_of_two(up) * kLiftedUnit);
+  const int up = scale_up(finite);
   const float mul = power_of_two(up);
+  float w[4];
+  // (values that are all zeros need no weight; beside a NaN or an infinity, any)
+  weigh<D>(s, lg, finite || !plain ? static_cast<float>(-up) : -INFINITY, w);
   if (q.vis_min >= page0 + n && plain) {
     const __nv_bfloat162 mul2 = __float2bfloat162_rn(mul);
     uint32_t bh[2], bl[2];
@@ -508,13 +496,17 @@ __device__ __forceinline__ void start_part(const Kv8Params& p, const Entry& t, i
   }
 }
 
-// Channels ch .. ch + 3 of an output row; a row that sees nothing (l = 0) gets zeros.
+// What outputs in units of 2^(u.m + u.k) are times, and sums of p in units of 2^u.m, to be the result: 0 for
+// a row that sees nothing (l = 0).
+__device__ __forceinline__ float output_factor(float k, float l) { return l == 0.f ? 0.f : fast_exp2(k) / l; }
+
+// Channels ch .. ch + 3 of an output row.
 __device__ __forceinline__ void store_row(const Kv8Params& p, int b, int h, int gcol, int ch, int D,
-                                          float4 o, float l) {
-  const Inverse inv = inverse_of<kLiftedSum>(l);
+                                          float4 o, float f) {
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint16_t* dst = p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + h * p.G + g) * D + ch;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(over_sum(o.x, o.y, inv), over_sum(o.z, o.w, inv));
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(pack_bf162(o.x * f, o.y * f), pack_bf162(o.z * f, o.w * f));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -527,11 +519,6 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float2 cluster_load2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ float4 cluster_load4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -540,32 +527,35 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t a) {
   return v;
 }
 
-// Merges the partials of a cluster's CTAs (8 columns in `slot` of each); every CTA
-// writes its share of the unit's outputs.
+// Merges the partials of a cluster's CTAs (8 columns in `slot` of each; stats: room for 8 float4 of each);
+// every CTA writes its share of the unit's outputs.
 template <int D>
 __device__ __forceinline__ void merge_cluster(const Kv8Params& p, const Entry& t, int h,
-                                              const float* slot) {
+                                              const float* slot, float4* stats) {
   cluster_sync();
   const int n = p.cluster, rank = blockIdx.x % n;
+  if (threadIdx.x < 8 * n)
+    stats[threadIdx.x] = cluster_load4(cluster_address(slot + 8 * D + 4 * (threadIdx.x & 7), threadIdx.x >> 3));
+  __syncthreads();
   const int per = (8 * D / 4 + n - 1) / n;      // float4 of each CTA
   const int i = rank * per + threadIdx.x;
   if (threadIdx.x < per && i < 8 * D / 4) {
     const int col = i / (D / 4), ch = 4 * (i % (D / 4)), gcol = t.tile * 8 + col;
     if (gcol < p.cols) {
-      float top = kLowest, l = 0.f;
-      for (int r = 0; r < n; ++r)
-        top = fmaxf(top, cluster_load2(cluster_address(slot + 8 * D + 2 * col, r)).x);
+      float m = kLowest, k = kLowest, l = 0.f;
+      for (int r = 0; r < n; ++r) m = fmaxf(m, stats[8 * r + col].x);
+      for (int r = 0; r < n; ++r) k = fmaxf(k, (stats[8 * r + col].x - m) + stats[8 * r + col].y);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int r = 0; r < n; ++r) {
-        const float2 ml = cluster_load2(cluster_address(slot + 8 * D + 2 * col, r));
+        const float4 part = stats[8 * r + col];
         const float4 x = cluster_load4(cluster_address(slot + col * D + ch, r));
-        const float half = fast_exp2(0.5f * (ml.x - top)), a = half * half;
-        l = fmaf(half * ml.y, half, l);
+        const float down = part.x - m, a = fast_exp2(down + part.y - k);
+        l = fmaf(fast_exp2(down), part.z, l);
         o.x = fmaf(a, x.x, o.x); o.y = fmaf(a, x.y, o.y);
         o.z = fmaf(a, x.z, o.z); o.w = fmaf(a, x.w, o.w);
       }
-      store_row(p, t.b, h, gcol, ch, D, o, l);
+      store_row(p, t.b, h, gcol, ch, D, o, output_factor(k, l));
     }
   }
   cluster_sync();   // no CTA leaves while its shared memory is read
@@ -597,7 +587,9 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   const int warp = (tid >> 5) - number * team;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff) + number * team * 8;
-  float* sm_l = sm_m + kWarps * 8;
+  float* sm_k = sm_m + kWarps * 8;
+  float* sm_l = sm_k + kWarps * 8;
+  float2* sm_unit = reinterpret_cast<float2*>(smem + C::kUnitOff) + number * 8;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
   if (tid < kWarps * C::kStages) mbar_init(bars + tid, 1);
   fence_mbar_init();
@@ -695,15 +687,11 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       start_part<C>(p, t, h, mine, team, lane, ring);
     }
 
+    if (gid == 0) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float l = s.l[c];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (gid == 0) {
+      for (int c = 0; c < 2; ++c) {
         sm_m[warp * 8 + 2 * tig + c] = s.m[c];
-        sm_l[warp * 8 + 2 * tig + c] = l;
+        sm_k[warp * 8 + 2 * tig + c] = s.k[c];
       }
     }
     team_sync<kMode>(team, number);
@@ -711,14 +699,25 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     float* slot = kMode == kCluster
         ? reinterpret_cast<float*>(smem + C::kPartOff)
         : p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * C::kSlot;
+    // the parts of a column in the unit of the largest m, and the k with which it lies as high as the highest
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float top = kLowest;
+      const int col = 2 * tig + c;
+      float m = kLowest, k = kLowest;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
-        if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[w * 8 + 2 * tig + c]);
-      const float a = fast_exp2(s.m[c] - top);
-      float* dst = merge + (warp * 8 + 2 * tig + c) * C::kStride + 4 * gid;
+        if (kMode != kTeams || w < team) m = fmaxf(m, sm_m[w * 8 + col]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (kMode != kTeams || w < team) k = fmaxf(k, (sm_m[w * 8 + col] - m) + sm_k[w * 8 + col]);
+      const float down = s.m[c] - m, a = fast_exp2(down + s.k[c] - k);
+      float l = s.l[c] * fast_exp2(down);
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (gid == 0) sm_l[warp * 8 + col] = l;
+      if (warp == 0 && gid == 0) sm_unit[col] = make_float2(m, k);
+      float* dst = merge + (warp * 8 + col) * C::kStride + 4 * gid;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
         *reinterpret_cast<float4*>(dst + 32 * i) =
@@ -730,30 +729,27 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const int col = i / (D / 4), ch = 4 * (i % (D / 4));
       const int gcol = tc.tile * 8 + col;
       if (kMode != kCluster && gcol >= p.cols) continue;
-      float top = kLowest, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (kMode != kTeams || w < team) top = fmaxf(top, sm_m[w * 8 + col]);
+      const float2 unit = sm_unit[col];
+      float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (kMode == kTeams && w >= team) break;
-        const float half = fast_exp2(0.5f * (sm_m[w * 8 + col] - top));
-        l = fmaf(sm_l[w * 8 + col] * half, half, l);
+        l += sm_l[w * 8 + col];
         const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
         o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
       }
       if (kMode != kCluster && (kMode == kTeams || complete)) {
-        store_row(p, tc.b, hc, gcol, ch, D, o, l);
+        store_row(p, tc.b, hc, gcol, ch, D, o, output_factor(unit.y, l));
       } else {
         *reinterpret_cast<float4*>(slot + col * D + ch) = o;
         if (ch == 0)
-          *reinterpret_cast<float2*>(slot + 8 * D + 2 * col) = make_float2(top, l);
+          *reinterpret_cast<float4*>(slot + 8 * D + 4 * col) = make_float4(unit.x, unit.y, l, 0.f);
       }
     }
     if (kMode != kTeams) __syncthreads();   // before the buffers are written again
     if constexpr (kMode == kCluster) {
-      merge_cluster<D>(p, tc, hc, slot);
+      merge_cluster<D>(p, tc, hc, slot, reinterpret_cast<float4*>(merge));
       return;
     }
     if constexpr (kMode == kTeams) return;
@@ -781,25 +777,30 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
   const int col = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 + col;
   const bool live = col < 8 && gcol < p.cols;
   float acc[kPer] = {};
-  float l = 0.f;
+  float m = kLowest, k = kLowest, l = 0.f;
   if (live) {
     // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
     auto slot = [&](int j) {
       return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
     };
-    auto stats = [&](int j) {   // (maximum, sum) of part j
-      return j < n ? *reinterpret_cast<const float2*>(slot(j) + 8 * D + 2 * col) : make_float2(kLowest, 0.f);
+    auto stats = [&](int j) {   // unit and sum of part j
+      return j < n ? *reinterpret_cast<const float4*>(slot(j) + 8 * D + 4 * col)
+                   : make_float4(kNoUnit.m, kNoUnit.k, 0.f, 0.f);
     };
-    float top = kLowest;
-    for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(j).x);
-    top = warp_max(top);
+    for (int j = lane; j < n; j += 32) m = fmaxf(m, stats(j).x);
+    m = warp_max(m);
+    for (int j = lane; j < n; j += 32) {
+      const float4 part = stats(j);
+      k = fmaxf(k, (part.x - m) + part.y);
+    }
+    k = warp_max(k);
     for (int j0 = 0; j0 < n; j0 += 32) {
-      const float2 ml = stats(j0 + lane);
-      const float half = j0 + lane < n ? fast_exp2(0.5f * (ml.x - top)) : 0.f, w = half * half;
-      l = fmaf(half * ml.y, half, l);
-      const int m = min(32, n - j0);
+      const float4 part = stats(j0 + lane);
+      const float down = part.x - m, w = fast_exp2(down + part.y - k);
+      l = fmaf(fast_exp2(down), part.z, l);
+      const int here = min(32, n - j0);
 #pragma unroll 8
-      for (int j = sub; j < m; j += kSplit) {
+      for (int j = sub; j < here; j += kSplit) {
         const float a = __shfl_sync(0xffffffffu, w, j);
         const float* x = slot(j0 + j) + col * D + kPer * lane;
         if constexpr (kPer == 4) {
@@ -824,12 +825,12 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += partial[warp + s][kPer * lane + k];
   if (!live) return;
-  const Inverse inv = inverse_of<kLiftedSum>(l);
+  const float f = output_factor(k, l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + kPer * lane);
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2) dst[k / 2] = over_sum(acc[k], acc[k + 1], inv);
+  for (int k = 0; k < kPer; k += 2) dst[k / 2] = pack_bf162(acc[k] * f, acc[k + 1] * f);
 }
 
 // The same for tiles of 128 columns, whose partial results lie by fours of channels, 128 columns
@@ -847,35 +848,39 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
   const int b = own.x / p.tiles, tile = own.x - b * p.tiles, gcol = tile * 128 + col;
   if (gcol >= p.cols) return;
   float acc[8] = {};
-  float top = kLowest, l = 0.f;
+  Unit u = kNoUnit;
+  float l = 0.f;
 #pragma unroll 1
   for (int j0 = 0; j0 < n; j0 += kFlight) {
-    float2 ml[kFlight];
+    float4 part[kFlight];
     float4 v[kFlight][2];
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
       // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
-      const int part = j0 + j;
-      ml[j] = make_float2(kLowest, 0.f);
+      const int i = j0 + j;
+      part[j] = make_float4(kNoUnit.m, kNoUnit.k, 0.f, 0.f);
       v[j][0] = v[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (part >= n) continue;
-      const float* slot = p.part + (2 * (blockIdx.x + static_cast<size_t>(part)) + (part == 0 ? 1 : 0)) * kSlot;
-      ml[j] = *reinterpret_cast<const float2*>(slot + 128 * D + 2 * col);
+      if (i >= n) continue;
+      const float* slot = p.part + (2 * (blockIdx.x + static_cast<size_t>(i)) + (i == 0 ? 1 : 0)) * kSlot;
+      part[j] = *reinterpret_cast<const float4*>(slot + 128 * D + 4 * col);
       v[j][0] = *reinterpret_cast<const float4*>(slot + 128 * ch + 4 * col);
       v[j][1] = *reinterpret_cast<const float4*>(slot + 128 * ch + 512 + 4 * col);
     }
-    float high = top;
+    float m = u.m, k = kLowest;
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) high = fmaxf(high, ml[j].x);
-    const float shift = fast_exp2(0.5f * (top - high)), old = shift * shift;
-    top = high;
+    for (int j = 0; j < kFlight; ++j) m = fmaxf(m, part[j].x);
+    k = (u.m - m) + u.k;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) k = fmaxf(k, (part[j].x - m) + part[j].y);
+    const float shift = fast_exp2(0.5f * ((u.m - m) + u.k - k)), old = shift * shift;
+    u = {m, k};
     l = l * shift * shift;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= old;
+    for (int i = 0; i < 8; ++i) acc[i] *= old;
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
-      const float half = fast_exp2(0.5f * (ml[j].x - top)), w = half * half;
-      l = fmaf(half * ml[j].y, half, l);
+      const float half = fast_exp2(0.5f * ((part[j].x - m) + part[j].y - k)), w = half * half;
+      l = fmaf(half * part[j].z, half, l);
       acc[0] = fmaf(w, v[j][0].x, acc[0]);
       acc[1] = fmaf(w, v[j][0].y, acc[1]);
       acc[2] = fmaf(w, v[j][0].z, acc[2]);
@@ -886,7 +891,7 @@ __global__ void __launch_bounds__(4 * D) kv8_merge_rows_kernel(const __grid_cons
       acc[7] = fmaf(w, v[j][1].w, acc[7]);
     }
   }
-  const Inverse inv = inverse_of<kSumLog2>(l);
+  const Inverse inv = inverse_of(l);
   const int row = gcol / p.G, g = gcol - row * p.G;
   *reinterpret_cast<uint4*>(p.out + ((static_cast<size_t>(b) * p.m_rows + row) * p.hq + own.y * p.G + g) * D + ch) =
       make_uint4(over_sum(acc[0], acc[1], inv), over_sum(acc[2], acc[3], inv),
@@ -981,7 +986,7 @@ inline int64_t share_ctas(bool rows, int64_t units, int64_t pages, int64_t sms) 
 }
 inline size_t record_bytes(int64_t ctas) { return (static_cast<size_t>(ctas) * sizeof(int4) + 255) / 256 * 256; }
 inline size_t share_bytes(bool rows, int d, int64_t ctas) {
-  return record_bytes(ctas) + static_cast<size_t>(ctas) * 2 * (rows ? 128 : 8) * (d + 2) * sizeof(float);
+  return record_bytes(ctas) + static_cast<size_t>(ctas) * 2 * (rows ? 128 : 8) * (d + 4) * sizeof(float);
 }
 
 // Several sequences are taken as three quarters of the longest: the host does not know the

@@ -4,7 +4,7 @@
 // Same mathematics, unit division and partial results as kv8_attention.cu.  Per tile
 // of 128 tokens (8 pages):
 //   S = Q K^T   M = 128 columns of queries, N = 128 tokens, K = d   (Q, K in shared memory)
-//   w = 2^(s_K fac S + log2 s_V - m)       (a thread per query; kv8_units.cuh has the ranges)
+//   w = 2^(s_K fac S + log2 s_V - m - k)   (a thread per query; kv8_units.cuh has unit and ranges)
 //   O += w V    M = 128, N = d, K = 128 tokens      (w in tensor memory, V in shared memory)
 // Here the bound is arithmetic, so the codes are turned into fp16 operands once per
 // tile and CTA (exact: integers up to 127, or e4m3 values) and the MMAs run from
@@ -27,7 +27,7 @@
 // at d = 128 and shared memory 1536 (fp16 tiles written once and read by the MMAs, Q read per
 // tile); a tile takes 2400, in which a K warp is busy for 1950 and a stream's chain S, softmax,
 // O is longer than its share.  Measured, d = 128, 8 KV heads, G = 4: 2048 rows over 32768 tokens
-// 1050 us, 1047 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86.3 us, 552 TFLOP/s of
+// 1050 us, 1047 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86.7 us, 550 TFLOP/s of
 // rows that exist (260 columns are 3 tiles: a third of the work is for 4 of them).
 // Registers: 96 a thread for 18 warps.  Whatever is spilled in a role's loop costs more than
 // it saves elsewhere (16 registers' worth: 7 of 98 us), and code that is fetched cold costs its
@@ -57,8 +57,8 @@ struct RowsSmem {
   static constexpr int kQ = 4 * kTile16;
   static constexpr int kMeta = 5 * kTile16;                  // float4 [4][8]: s_K, log2 s_V, 2^-12/s_V, position
   static constexpr int kFac = kMeta + 512;                 // float [2][128]
-  static constexpr int kMl = kFac + 1024;                  // float2 [2][2][128]
-  static constexpr int kBad = kMl + 4096;                  // int [4]: tails that are not finite
+  static constexpr int kMl = kFac + 1024;                  // float4 [2][2][128]: unit and sum
+  static constexpr int kBad = kMl + 8192;                  // int [4]: tails that are not finite
   static constexpr int kOdd = kBad + 16;                   // int [2][2]: see note_odd
   static constexpr int kBars = kBad + 64;
   static constexpr int kMisc = kBars + 40 * 8;
@@ -356,22 +356,6 @@ __device__ __forceinline__ float rows_exp2(float x) {
   return y;
 }
 
-// Two fp32 values in one operand, and arithmetic on both at once.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
-}
-__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
-__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -380,7 +364,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // The largest exponent s_K fac S + log2 s_V of a thread's row over a tile's visible tokens.
 // Two pages' 32 columns at a time, the next two pages' on their way.  kCareful: where the tile has a
-// token that a row does not see, or the unit odd scales (note_odd).
+// token that a row does not see, the unit odd scales (note_odd), or a row a steep maximum (kSteep).
 template <bool kCareful>
 __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float fac, int vis) {
   float big = -INFINITY;
@@ -414,23 +398,26 @@ __device__ __forceinline__ float rows_max(uint32_t ts, const float4* mt, float f
   return big;
 }
 
-// w = 2^(s_K fac S + log2 s_V - m) of the row, as fp16 over the columns of S that have been
-// read; returns the sum of w / s_V.
+// w = 2^(s_K fac S + log2 s_V - m - k) of the row, as fp16 over the columns of S that have been
+// read; returns the sum of w / s_V.  Where |m| is at most kSteep, log2 s_V - m is off by 2^-14 at most
+// as one number (and k is 0); else logits are rounded by themselves, so that equal ones stay equal.
 template <bool kCareful>
-__device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const float4* mt, float fac, int vis, float m) {
+__device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const float4* mt, float fac, int vis, Unit un) {
   float l = 0.f;
   auto pages = [&](const uint32_t (&s)[32], int j0) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t out[8];
       const float4 pm = mt[j0 + j];
-      const float f = kCareful ? logit_factor(pm.x, fac) : pm.x * fac, off = pm.y - m;
-      const uint64_t f2 = two(f, f), off2 = two(off, off);
+      const float f = kCareful ? logit_factor(pm.x, fac) : pm.x * fac, off = pm.y - (kCareful ? un.k : un.m);
+      const uint64_t f2 = two(f, f), off2 = two(off, off), m2 = two(-un.m, -un.m);
       const int seen = vis - __float_as_int(pm.w);
       uint64_t sum[2];
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
-        const uint64_t e = fma2(two(__uint_as_float(s[16 * j + k]), __uint_as_float(s[16 * j + k + 1])), f2, off2);
+        const float s0 = __uint_as_float(s[16 * j + k]), s1 = __uint_as_float(s[16 * j + k + 1]);
+        const uint64_t e = kCareful ? add2(add2(two(__fmul_rn(s0, f), __fmul_rn(s1, f)), m2), off2)
+                                    : fma2(two(s0, s1), f2, off2);
         float x0 = rows_exp2(first(e)), x1 = rows_exp2(second(e));
         if constexpr (kCareful) {
           x0 = k < seen ? x0 : 0.f;
@@ -466,21 +453,6 @@ __device__ __forceinline__ float rows_weights(uint64_t* half, uint32_t ts, const
   return l;
 }
 
-// A row's O in tensor memory times a.  (Out of line, as are the next two: in line they cost the
-// common path 1 to 2% in registers.)
-template <int D>
-__device__ __noinline__ void rescale_output(uint32_t to, float a) {
-#pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t o[16];
-    tc_request16(to + 16 * c, o);
-    tc_wait_ld(o);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-    tc_st16(to + 16 * c, o);
-  }
-}
-
 // Unit `seg` has a value scale outside the window of is_odd, or keys whose scale times a column's
 // factor (2^110 at most) may overflow: its number into the first word of two, and into the second for a
 // scale above the window.  Two units' words, as the pages are ahead of the softmax by one.
@@ -494,25 +466,89 @@ static __device__ __noinline__ void note_odd(volatile int* odd_scale, uint32_t s
 // p of the row's visible tokens whose weights underflow in rows_weights, times 2^kSumLog2: for
 // units with odd scales; high: one above the window of is_odd, else only pages below it can
 // lose any.  The same exponents as there, so each token counts once.
-static __device__ __noinline__ float rows_lost(uint32_t ts, const float4* mt, float fac, int vis, float m,
-                                                bool high) {
+__device__ __forceinline__ float rows_lost(uint32_t ts, const float4* mt, float fac, int vis, float m, float k, bool high) {
   float l = 0.f;
 #pragma unroll 1
   for (int j = 0; j < 8; ++j) {
     const float4 pm = mt[j];
     if (!high && !is_odd(pm.y)) continue;   // (the same for all lanes)
-    const float f = logit_factor(pm.x, fac), off = pm.y - m;
+    const float f = logit_factor(pm.x, fac), off = pm.y - k;
     const int seen = vis - __float_as_int(pm.w);
     uint32_t s[16];
     tc_request16(ts + 16 * j, s);
     tc_wait_ld(s);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float x = __uint_as_float(s[k]);
-      if (k < seen && rows_exp2(fmaf(x, f, off)) == 0.f) l += whole_exp2(fmaf(x, f, static_cast<float>(kSumLog2) - m));
+    for (int i = 0; i < 16; ++i) {
+      const float x = __fmul_rn(__uint_as_float(s[i]), f) - m;
+      if (i < seen && rows_exp2(x + off) == 0.f) l += whole_exp2(x - k + static_cast<float>(kSumLog2));
     }
   }
   return l;
+}
+
+// The unit that a row's visible tokens of a tile need: their largest logit, and the largest
+// logit + log2 s_V less that.
+__device__ __forceinline__ Unit steep_max(uint32_t ts, const float4* mt, float fac, int vis) {
+  Unit u{-INFINITY, 0.f};
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    float best = -INFINITY;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      const float4 pm = mt[j];
+      const int seen = vis - __float_as_int(pm.w);
+      uint32_t s[16];
+      tc_request16(ts + 16 * j, s);
+      tc_wait_ld(s);
+      float raw = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < seen) raw = fmaxf(raw, __uint_as_float(s[i]));
+      if (raw > -INFINITY) raw = __fmul_rn(raw, logit_factor(pm.x, fac));
+      best = fmaxf(best, pass == 0 ? raw : (raw - u.m) + pm.y);
+    }
+    if (pass == 0) u.m = best;
+    else u.k = u.m == -INFINITY ? 0.f : best;
+  }
+  return u;
+}
+
+// A row's O in tensor memory times a.
+template <int D>
+__device__ __forceinline__ void rescale_output(uint32_t to, float a) {
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tc_request16(to + 16 * c, o);
+    tc_wait_ld(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+    tc_st16(to + 16 * c, o);
+  }
+}
+
+struct RowState {
+  float m, k, l;   // unit and sum
+};
+// A row's unit and sum before the weights of a tile of an odd unit, or of one with a steep row.  (Out of
+// line: in line it costs the common path 1 to 2% in registers.)
+enum { kBegun = 1, kIsSteep = 2, kIsOdd = 4, kIsHigh = 8 };
+template <int D>
+__device__ __noinline__ RowState settle(RowState r, float big, uint32_t ts, uint32_t to, const float4* mt, float fac,
+                                        int vis, int what) {
+  Unit next{big, 0.f};
+  if (what & kIsSteep) next = steep_max(ts, mt, fac, vis);
+  const float x = above(Unit{r.m, r.k}, next.m, next.k);
+  const bool over = x > kLag;
+  const float half = over ? rows_exp2(-0.5f * x) : 1.f, a = half * half;
+  if (over) {
+    r.m = next.m;
+    r.k = next.k;
+  }
+  r.l = r.l * half * half;
+  if ((what & kBegun) && __any_sync(0xffffffffu, over)) rescale_output<D>(to, a);
+  if (what & kIsOdd) r.l += rows_lost(ts, mt, fac, vis, r.m, r.k, what & kIsHigh);
+  return r;
 }
 
 template <int D, bool kE4m3>
@@ -528,7 +564,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
   float4* meta = reinterpret_cast<float4*>(smem + S::kMeta);
   float* facs = reinterpret_cast<float*>(smem + S::kFac);
-  float2* mls = reinterpret_cast<float2*>(smem + S::kMl);
+  float4* mls = reinterpret_cast<float4*>(smem + S::kMl);
   volatile int* bad_tail = reinterpret_cast<volatile int*>(smem + S::kBad);
   volatile int* odd_scale = reinterpret_cast<volatile int*>(smem + S::kOdd);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -782,12 +818,14 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         if (p.q_pos && gcol < p.cols && p.q_pos[static_cast<size_t>(u.t.b) * p.m_rows + row] >= u.t.len)
           atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
       }
-      float m = kLowest, l = 0.f, top = kLowest, a0 = 0.f, a1 = 0.f;
+      RowState r{kLowest, 0.f, 0.f};
+      Unit top{kLowest, 0.f};
+      float a0 = 0.f, a1 = 0.f;
       if (u.tiles > 0) {
         if (!wait(&bar->qfull[seg & 1], seg >> 1)) break;
         const float fac = facs[(seg & 1) * 128 + rr];
         const bool idle = __all_sync(0xffffffffu, gcol >= p.cols);
-        const int vis_least = __reduce_min_sync(0xffffffffu, vis);
+        int vis_least = __reduce_min_sync(0xffffffffu, vis);   // -1 once a row's maximum is steep
         const int unit = static_cast<int>(seg) + 1;
         const volatile int* odd = odd_scale + 2 * (seg & 1);
         bool ok = true;
@@ -805,31 +843,37 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
           const bool is_odd_unit = __any_sync(0xffffffffu, odd[0] == unit);   // (one answer for all lanes)
           const bool careful = (u.p0 + 8 * i + 8) * kPage > vis_least || is_odd_unit;   // (always with a tail)
           const float big = careful ? rows_max<true>(ts, mt, fac, vis) : rows_max<false>(ts, mt, fac, vis);
-          const bool over = big > m + kLag;
-          if (__any_sync(0xffffffffu, over) || is_odd_unit) {
-            const float up = over ? big : m;
-            const float half = over ? rows_exp2(0.5f * (m - up)) : 1.f, a = half * half;
-            m = up;
-            l = l * half * half;
-            if (i > 1) rescale_output<D>(to, a);   // so far (its last MMA finished before this S began)
-            if (is_odd_unit) l += rows_lost(ts, mt, fac, vis, m, __any_sync(0xffffffffu, odd[1] == unit));
+          const bool over = big - r.m > kLag;
+          if (__any_sync(0xffffffffu, over) || is_odd_unit || vis_least < 0) {
+            if (__any_sync(0xffffffffu, over && fabsf(big) > kSteep)) vis_least = -1;
+            if (is_odd_unit || vis_least < 0) {
+              r = settle<D>(r, big, ts, to, mt, fac, vis,
+                            (i > 1 ? kBegun : 0) | (vis_least < 0 ? kIsSteep : 0) | (is_odd_unit ? kIsOdd : 0) |
+                                (__any_sync(0xffffffffu, odd[1] == unit) ? kIsHigh : 0));
+            } else {   // (k is 0)
+              const float half = over ? rows_exp2(0.5f * (r.m - big)) : 1.f;
+              r.m = over ? big : r.m;
+              r.l = r.l * half * half;
+              if (i > 1) rescale_output<D>(to, half * half);   // O so far (its last MMA finished before this S began)
+            }
           }
-          l += careful ? rows_weights<true>(&bar->pfull[st], ts, mt, fac, vis, m) : rows_weights<false>(&bar->pfull[st], ts, mt, fac, vis, m);
+          r.l += careful || vis_least < 0 ? rows_weights<true>(&bar->pfull[st], ts, mt, fac, vis, Unit{r.m, r.k})
+                                          : rows_weights<false>(&bar->pfull[st], ts, mt, fac, vis, Unit{r.m, r.k});
           tc_wait_st();
           tc_fence_before();
           arrive(&bar->pfull[2 + st]);
         }
         if (!ok) break;
-        // the other stream's maximum and sum
-        float2* ml = mls + (seg & 1) * 256;
-        ml[128 * st + rr] = make_float2(m, l);
+        // the other stream's unit and sum
+        float4* ml = mls + (seg & 1) * 256;
+        ml[128 * st + rr] = make_float4(r.m, r.k, r.l, 0.f);
         arrive(&bar->mlfull);
         if (!wait(&bar->mlfull, seg) || !wait(&bar->odone, seg)) break;
         tc_fence_after();
-        const float2 other = ml[128 * (1 - st) + rr];
-        top = fmaxf(m, other.x);
-        const float mine = rows_exp2(0.5f * (m - top)), theirs = rows_exp2(0.5f * (other.x - top));
-        l = l * mine * mine + other.y * theirs * theirs;
+        const float4 other = ml[128 * (1 - st) + rr];
+        top = higher(Unit{r.m, r.k}, other.x, other.y);
+        const float mine = rows_exp2(0.5f * above(top, r.m, r.k)), theirs = rows_exp2(0.5f * above(top, other.x, other.y));
+        r.l = r.l * mine * mine + other.z * theirs * theirs;
         a0 = st ? theirs * theirs : mine * mine;
         a1 = st ? mine * mine : theirs * theirs;
       }
@@ -841,7 +885,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const int64_t tail_id = p.tail_ids ? p.tail_ids[u.t.b] : u.t.b;
       const uint16_t* tail = reinterpret_cast<const uint16_t*>(p.tail + (tail_id * p.hkv + u.h) * F::kTailBytes) +
           F::kTailHalf;
-      const Inverse inv = inverse_of<kSumLog2>(l);
+      const Inverse inv = inverse_of(r.l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {   // 16 channels
         const int ch = st * (D / 2) + 16 * c;
@@ -885,7 +929,7 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll
             for (int k = 0; k < 16; k += 4)
               *reinterpret_cast<float4*>(slot + 128 * (ch + k) + 4 * rr) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            if (ch == 0) *reinterpret_cast<float2*>(slot + 128 * D + 2 * rr) = make_float2(top, l);
+            if (ch == 0) *reinterpret_cast<float4*>(slot + 128 * D + 4 * rr) = make_float4(top.m, top.k, r.l, 0.f);
           }
         }
       }

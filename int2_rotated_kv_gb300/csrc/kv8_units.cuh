@@ -11,21 +11,34 @@ constexpr int kMaxCtas = 1024;
 constexpr float kLowest = -3.402823466e38f;   // running maximum before the first logit
 constexpr float kLag = 8.f;                   // the maximum is raised when passed by 2^8
 
-// The running maximum m of a column is that of logit + log2 s_V (log2 domain), so a weight
-// w = 2^(logit + log2 s_V - m) is p s_V beside the largest p s_V that the column has met: a page
-// of huge values that nothing attends to takes no bits from the others.  Outputs are sums of
-// w code, l the sum of w / s_V, both in units of 2^m.  Value scales go from 2^-109 to 2^121:
+// Weights w = p s_V relative to the largest of a column: outputs are sums of w code in units of
+// 2^(m + k), so that a page of huge values that nothing attends to takes no bits from the others.  m is a
+// logit (log2 domain) and may be large, k an offset of about log2 s_V: differences of two m are exact
+// where they matter, and k is added to them, never to m.
+struct Unit {
+  float m, k;
+};
+constexpr Unit kNoUnit = {kLowest, -300.f};   // of a column that has seen nothing
+// How far (m, k) lies above u, or below.
+__device__ __forceinline__ float above(Unit u, float m, float k) { return (m - u.m) + (k - u.k); }
+// The higher of the two.
+__device__ __forceinline__ Unit higher(Unit u, float m, float k) { return above(u, m, k) > 0.f ? Unit{m, k} : u; }
+
+// Value scales go from 2^-109 to 2^121.  Tiles of 8 columns have m the largest logit, l the sum of p in
+// units of 2^m, and a factor beside p for w.  In tiles of 128 a product more for each weight is left out: the
+// scale rides in the exponent, (m, k) is the unit of both, and l is the sum of w / s_V.  Therefore, there:
+//   - up to kSteep m is logit + log2 s_V as one number, and k is 0;
 //   - a page of zeros counts as one of scale 2^-110, below every other (kZeroLog2);
-//   - l is carried times 2^-12 (2^-18 where m lies 2^6 lower, for weights of up to 2^14), so that
-//     2^25 tokens of the least scale stay below 2^128;
+//   - l is carried times 2^-12, so that 2^25 tokens of the least scale stay below 2^128;
 //   - w / s_V is lost with w where a scale lies 2^100 below another's, which takes one outside
-//     [2^-64, 2^32] (is_odd): from then on 2^(logit - m) takes the place of a w that is 0;
-//   - a change of m by x takes l times 2^(x/2) twice, as 2^x alone may underflow;
+//     [2^-64, 2^32] (is_odd): from then on 2^(logit - m - k) takes the place of a w that is 0;
+//   - a change of unit by 2^x takes l times 2^(x/2) twice, as 2^x alone may underflow;
 //   - 1 / l is two factors.
 constexpr float kZeroLog2 = -110.f;
 constexpr int kSumLog2 = -12;
 constexpr float kSumUnit = 1.f / 4096.f;   // 2^kSumLog2
 constexpr float kZeroScale = 7.703719777548943e-34f;   // 2^kZeroLog2
+constexpr float kSteep = 1024.f;   // beyond it that one number is off by 2^-14 and more
 __device__ __forceinline__ bool is_odd(float log2_scale) { return fabsf(log2_scale + 16.f) > 48.f; }
 
 __device__ __forceinline__ float power_of_two(int e) {
@@ -60,20 +73,42 @@ __device__ __forceinline__ float whole_exp2(float x) {
   return y;
 }
 
-// 1 / l of a sum l (carried times 2^kLog2, perhaps subnormal), 0 for 0: the product of two.
+// 1 / l of a sum l (carried times 2^kSumLog2, perhaps subnormal), 0 for 0: the product of two.
 struct Inverse {
   float a, b;
 };
-template <int kLog2>
 __device__ __forceinline__ Inverse inverse_of(float l) {
   const float up = l < 7.888609052210118e-31f ? 1.2676506002282294e30f     // 2^-100, 2^100
                    : l > 1.2676506002282294e30f ? 7.888609052210118e-31f
                                                 : 1.f;
-  return {l == 0.f ? 0.f : 1.f / (l * up), up * (1.f / (1 << -kLog2))};
+  return {l == 0.f ? 0.f : 1.f / (l * up), up * kSumUnit};
 }
 // Two outputs x / l, y / l.
 __device__ __forceinline__ uint32_t over_sum(float x, float y, Inverse inv) {
   return pack_bf162(x * inv.a * inv.b, y * inv.a * inv.b);
+}
+
+// Two fp32 values in one operand, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// (Beside add2 not to be used where the product has to be rounded by itself: the two become one operation.)
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 struct Kv8Params {
@@ -93,13 +128,13 @@ struct Kv8Params {
   int team;                // warps per unit when teams of warps do
   float scale_log2;
   int4* info;              // per CTA: unit entry, KV head, parts of the unit that starts in it
-  float* part;             // [2 * CTAs][8 * NT * (D + 2)]
+  float* part;             // [2 * CTAs][8 * NT * (D + 4)]
 };
 
-// Floats of one partial result of 8 * NT columns: outputs, then (maximum, sum) pairs.
+// Floats of one partial result of 8 * NT columns: outputs, then (unit, sum, -) of each column.
 template <int D, int NT>
 __host__ __device__ constexpr int kv8_slot() {
-  return 8 * NT * (D + 2);
+  return 8 * NT * (D + 4);
 }
 
 // A sequence's tile of query columns: pages it has to visit (at least one, so that

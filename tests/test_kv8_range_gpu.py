@@ -209,3 +209,37 @@ def test_logits_that_leave_one_token(fmt, m, wide, qexp, kexp):
                 bad = ~(np.abs(got[b, i, r] - want) <= (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -14) * 1.01 * np.abs(want))
                 assert not bad.any(), (b, i, r, u, best, got[b, i, r][bad][:4], want[bad][:4])
     assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("qexp", [0, 5, 12, 16, 20, 23, 25, 40])
+def test_equal_logits_however_large(fmt, m, wide, qexp):
+    """All tokens have the same key, whose code times scale is exact, so all logits of a row are the
+    same number, up to 2^44 and down to its negative: every weight is 1, whatever the values' scales
+    (2^-20 to 2^20 from page to page), and the output is the mean.  The bound is that of `check`
+    without errors of logits."""
+    lens = [645, 320, 151]
+    s = K.Sequences(3, 1, 4, 128, fmt, 700, seed=m + qexp)
+    n = sum(lens)
+    _, v = K.draw(s.rng, n, 1, 128)
+    v *= np.exp2(s.rng.integers(-20, 21, n // 16 + 1).astype(np.float32))[np.arange(n) // 16][:, None, None]
+    k = np.zeros((n, 1, 128), np.float32)
+    k[:, :, 9] = 448 if fmt == kv8.E4M3 else 127
+    s.place(lens, k, bf16(v))
+    q = np.zeros((3, m, 4, 128), np.float32)
+    q[..., 9] = 2.0 ** qexp * np.where(s.rng.random((3, m, 4)) < 0.3, -1, 1)
+    pos = rows_of(s, m)
+    got = s.attend(q, pos, wide=wide)
+    for b in range(3):
+        v64 = s.stored(b, 0)[1]
+        vmax = page_max(v64)
+        for i in range(m):
+            u = lens[b] if pos is None else pos[b, i] + 1
+            ref, w = v64[:u].mean(0), np.abs(v64[:u]).mean(0)
+            tol = (2.0 ** -12 + 2.0 ** -14 + (u // 16 + 16) * 2.0 ** -23) * w + 2.0 ** -24 * vmax[:u].max()
+            tol += 2.0 ** -8 * (np.abs(ref) + tol)
+            bad = ~(np.abs(got[b, i] - ref) <= tol)
+            assert not bad.any(), (b, i, u, int(bad.sum()), got[b, i][bad][:4])
+    assert H.status(s.cache) == 0
