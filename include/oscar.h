@@ -199,6 +199,22 @@ oscar_status oscar_quantize_append_trace(const oscar_cache_desc* desc, const voi
                                          const void* v_new, const int32_t* seq_lens_after,
                                          int32_t batch, float* y_out, void* stream);
 
+/* Reads tokens back as bf16, e.g. to move a prefix to another cache or hand it to another
+ * kernel: rows row_starts[b] .. row_starts[b+1] - 1 of k_out and v_out get the tokens of
+ * sequence b from position first[b] on; a BF16 token as it is stored, an INT2 (INT4) token as
+ * y_hat R^T, the key (value) that attention takes it for, rounded once.  seq_lens: tokens stored.
+ *   k_out, v_out: device bf16 [total_rows][num_kv_heads][d], 16-byte aligned; rows behind
+ *     row_starts[batch] are left as they were.
+ *   seq_lens, first [batch], row_starts [batch + 1] (ascending): device int32.
+ *   max_rows: no sequence asks for more.
+ * A sequence that asks for more than max_rows, for tokens behind seq_lens[b] or outside its table
+ * row, or for rows outside [0, total_rows), is skipped with OSCAR_DEVERR_SEQ_LEN; tokens whose
+ * page id is out of range are left as they were (OSCAR_DEVERR_PAGE_ID).  Arithmetic: y_hat in fp32, the
+ * product with R (fp32) to 2^-16 of sum |y||R|, one rounding to bf16.  Asynchronous. */
+oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens, const int32_t* first,
+                          const int32_t* row_starts, int32_t batch, int64_t total_rows,
+                          int32_t max_rows, void* k_out, void* v_out, void* stream);
+
 /* Bytes of device workspace oscar_decode_attention / _bf16 need for this batch
  * and maximum sequence length (depends on the device's SM count). */
 size_t oscar_decode_workspace_size(const oscar_cache_desc* desc, int32_t batch,
@@ -506,6 +522,60 @@ size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32
  * may overlap on the GPU need one each.  The result does not depend on the order in
  * which CTAs run.  Asynchronous. */
 oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
+                                 const int32_t* q_pos, int32_t batch, int32_t m_rows,
+                                 int32_t max_seq_len, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------------- the 4-bit cache
+ *
+ * The 8-bit cache's pages, tails, tables, arguments and rules with codes of 4 bits: 0.56 of its
+ * bytes, also without calibration.  (The INT4 variant above takes calibrated rotations and keeps
+ * sink and window in BF16.)
+ *   A value is code * s * g: code an e2m1 number (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), s the e4m3 scale of
+ *   a block of 16, g the fp32 scale of a page and KV head, keys and values apart.  A block of keys
+ *   is one channel of the page's 16 tokens, a block of values 16 channels of one token.
+ *   With a the largest finite magnitude of the page's 16 * d values, m that of the block:
+ *   g = fl32(a / 2688), s = e4m3(fl32(m * fl32(448 / a))), code = e2m1(fl32(x * r)) with
+ *   r = fl32(fl32(2688 / a) / s), both nearest, ties to even, codes saturating at 6; a block with
+ *   s = 0 is zeros, and so is a page with a < 2^-97.  A NaN is stored as 0 and an infinity
+ *   as +-a (OSCAR_DEVERR_NONFINITE is set); the tail keeps both as they are.
+ *   Block of (page, KV head): 18*d + 16 bytes at (page*num_kv_heads + head) times that: 8*d of
+ *   key codes, 8*d of value codes, d key scales, d value scales, fp32 key scale, fp32 value
+ *   scale, 8 spare bytes.  The order of elements is documented in csrc/kv4_layout.cuh.  Tail
+ *   blocks are those of the 8-bit cache. */
+typedef struct oscar_kv4_desc {
+  int32_t num_kv_heads;
+  int32_t num_q_heads;
+  int32_t head_dim;                /* 64 or 128                                       */
+  int32_t max_pages_per_seq;       /* row length of the page table                    */
+  int64_t num_pages;               /* physical pages in the pool                      */
+  int64_t num_tails;               /* tail blocks                                     */
+  void* pool;                      /* device                                          */
+  void* tail;                      /* device bf16                                     */
+  const int32_t* page_table;       /* device [batch][max_pages_per_seq]               */
+  const int32_t* tail_ids;         /* device [batch], or null: sequence b has tail b  */
+  int32_t* status;                 /* optional device word (OSCAR_DEVERR_* bits)      */
+} oscar_kv4_desc;
+
+/* As oscar_kv8_place. */
+oscar_status oscar_kv4_place(const oscar_kv4_desc* desc, const void* k, const void* v,
+                             int64_t k_stride, int64_t v_stride, const int32_t* lens_before,
+                             const int32_t* row_starts, int32_t batch, int64_t total_rows,
+                             int32_t max_new, void* stream);
+
+/* As oscar_kv8_gather; a value is fl32(code * s * g) (code * s is exact) rounded to bf16. */
+oscar_status oscar_kv4_gather(const oscar_kv4_desc* desc, const int32_t* seq_lens,
+                              const int32_t* first, const int32_t* row_starts, int32_t batch,
+                              int64_t total_rows, int32_t max_rows, void* k_out, void* v_out,
+                              void* stream);
+
+/* As oscar_kv8_workspace_size. */
+size_t oscar_kv4_workspace_size(const oscar_kv4_desc* desc, int32_t batch, int32_t m_rows,
+                                int32_t max_seq_len);
+
+/* As oscar_kv8_attention: code * s is exact in its arithmetic, and g takes the place of the
+ * 8-bit cache's scale. */
+oscar_status oscar_kv4_attention(const oscar_kv4_desc* desc, const void* q, const int32_t* seq_lens,
                                  const int32_t* q_pos, int32_t batch, int32_t m_rows,
                                  int32_t max_seq_len, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream);

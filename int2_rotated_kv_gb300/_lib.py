@@ -34,7 +34,8 @@ EXPORTED = ("oscar_query_covariance", "oscar_score_covariance", "oscar_build_rot
             "oscar_score_covariance_device", "oscar_clip_threshold_device",
             "oscar_prefill_quantize_trace", "oscar_quantize_append_trace",
             "oscar_kv8_place", "oscar_kv8_gather", "oscar_kv8_workspace_size",
-            "oscar_kv8_attention", "oscar_extend_pages", "oscar_rope_phases", "oscar_rope")
+            "oscar_kv8_attention", "oscar_kv4_place", "oscar_kv4_gather", "oscar_kv4_workspace_size",
+            "oscar_kv4_attention", "oscar_gather", "oscar_extend_pages", "oscar_rope_phases", "oscar_rope")
 
 
 class OscarError(RuntimeError):
@@ -59,7 +60,7 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
-class Kv8Desc(ctypes.Structure):
+class Kv4Desc(ctypes.Structure):
     _fields_ = [
         ("num_kv_heads", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
@@ -67,8 +68,11 @@ class Kv8Desc(ctypes.Structure):
         ("pool", ctypes.c_void_p), ("tail", ctypes.c_void_p),
         ("page_table", ctypes.c_void_p), ("tail_ids", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
-        ("format", ctypes.c_int32),
     ]
+
+
+class Kv8Desc(ctypes.Structure):
+    _fields_ = Kv4Desc._fields_ + [("format", ctypes.c_int32)]
 
 
 _LIB = None
@@ -111,6 +115,11 @@ def lib() -> ctypes.CDLL:
             "oscar_kv8_gather": (I32, [P, P, P, P, I32, I64, I32, P, P, P]),
             "oscar_kv8_workspace_size": (ctypes.c_size_t, [P, I32, I32, I32]),
             "oscar_kv8_attention": (I32, [P, P, P, P, I32, I32, I32, P, P, ctypes.c_size_t, P]),
+            "oscar_kv4_place": (I32, [P, P, P, I64, I64, P, P, I32, I64, I32, P]),
+            "oscar_kv4_gather": (I32, [P, P, P, P, I32, I64, I32, P, P, P]),
+            "oscar_kv4_workspace_size": (ctypes.c_size_t, [P, I32, I32, I32]),
+            "oscar_kv4_attention": (I32, [P, P, P, P, I32, I32, I32, P, P, ctypes.c_size_t, P]),
+            "oscar_gather": (I32, [P, P, P, P, I32, I64, I32, P, P, P]),
             "oscar_extend_pages": (I32, [P, I32, P, P, I32, I32, P, I64, P, P, P, P, P, P, P, I64, P,
                                          P]),
             "oscar_rope_phases": (I32, [D, I32, D, I32, D, D, P]),
@@ -411,7 +420,7 @@ def oscar_clip_threshold_device(x, r, percentile: float, clip_out, workspace, st
                                              _stream(stream)))
 
 
-# --------------------------------- 8-bit cache, page tables, rotary positions
+# ---------------- 8-bit and 4-bit cache, reading back, page tables, rotary positions
 #
 # These calls check their tensors (type, shape, strides, one device) and raise
 # ValueError; what the tensors hold is checked by the kernels.  They run on the
@@ -485,8 +494,85 @@ def _launch(fn: str, index: int, stream, *args) -> None:
         raise OscarError(fn, status)
 
 
+def oscar_gather(cache: Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out, stream=None):
+    """Read tokens of the calibrated cache back as bf16: rows row_starts[b] .. row_starts[b+1] - 1
+    of k_out and v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on,
+    BF16 ones as stored, INT2 or INT4 ones as code * s + z, rotated back."""
+    fn = "oscar_gather"
+    index = _device_of(fn, "int2_pool", cache.int2_pool)
+    d = cache.desc()
+    n, h, dim = k_out.shape[0], cache.num_kv_heads, cache.head_dim
+    if (_rows(fn, "k_out", k_out, n, h, dim, index) != h * dim
+            or _rows(fn, "v_out", v_out, n, h, dim, index) != h * dim):
+        raise ValueError(f"{fn}: k_out and v_out must be contiguous")
+    lens, begin = _i32(fn, "seq_lens", seq_lens, index), _i32(fn, "first", first, index)
+    starts = _i32(fn, "row_starts", row_starts, index)
+    _i32(fn, "int2_page_table", cache.int2_page_table, index)
+    _i32(fn, "bf16_page_table", cache.bf16_page_table, index)
+    batch, shape = seq_lens.numel(), cache.int2_page_table.shape
+    if first.numel() != batch or row_starts.numel() != batch + 1:
+        raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1")
+    if shape != cache.bf16_page_table.shape or len(shape) != 2 or batch > shape[0]:
+        raise ValueError(f"{fn}: the page tables must have the same shape, and a row per sequence")
+    for name in ("bf16_pool", "r_k", "r_v"):
+        t = getattr(cache, name)
+        if t is None or t.get_device() != index:
+            raise ValueError(f"{fn}: {name} must be on cuda:{index}")
+    _launch(fn, index, stream, ctypes.byref(d), lens, begin, starts, batch, n,
+            _fits(fn, "max_rows", max_rows), k_out.data_ptr(), v_out.data_ptr())
+
+
+class _PagedCache:
+    """What the 8-bit and the 4-bit cache share: checked tensors and a C descriptor."""
+    fmt = None   # Kv8Cache: which 8 bits
+
+    def desc(self):
+        return self._checked()[0]
+
+    def _checked(self):
+        """(descriptor, a pointer to it, device index, page-table rows), checked again when a
+        tensor or a field has been replaced."""
+        pool, tail, table, ids, status = (self.pool, self.tail, self.page_table, self.tail_ids,
+                                          self.status)
+        key = (pool.data_ptr(), pool.shape, pool.dtype, pool.is_contiguous(),
+               tail.data_ptr(), tail.shape, tail.dtype, tail.is_contiguous(),
+               table.data_ptr(), table.shape, table.dtype, table.is_contiguous(),
+               None if ids is None else (ids.data_ptr(), ids.shape, ids.dtype, ids.is_contiguous()),
+               None if status is None else (status.data_ptr(), status.dtype),
+               self.fmt, self.num_q_heads, self.num_kv_heads, self.head_dim)
+        cached = self.__dict__.get("_desc")
+        if cached is not None and cached[0] == key:
+            return cached[1]
+        import torch
+        fn, h, d = type(self).__name__, self.num_kv_heads, self.head_dim
+        size = self._block_bytes(d)
+        index = _device_of(fn, "pool", self.pool)
+        _need(self.pool.dtype is torch.uint8 and self.pool.is_contiguous()
+              and self.pool.shape[1:] == (h, size), fn,
+              f"pool must be a contiguous uint8 tensor [num_pages][{h}][{size}]")
+        _need(self.tail.dtype is torch.bfloat16 and self.tail.is_contiguous()
+              and self.tail.get_device() == index and self.tail.shape[1:] == (h, 2, 16 * d), fn,
+              f"tail must be a contiguous bfloat16 tensor [num_tails][{h}][2][{16 * d}] on cuda:{index}")
+        _i32(fn, "page_table", self.page_table, index)
+        _need(self.page_table.dim() == 2, fn, "page_table must be [batch][max_pages_per_seq]")
+        rows = int(self.page_table.shape[0])
+        if self.tail_ids is not None:
+            _i32(fn, "tail_ids", self.tail_ids, index)
+            _need(self.tail_ids.numel() == rows, fn,
+                  "tail_ids must have an entry per row of the page table")
+        if self.status is not None:
+            _i32(fn, "status", self.status, index)
+        desc = self._make_desc(h, self.num_q_heads, d, int(self.page_table.shape[1]),
+                               int(self.pool.shape[0]), int(self.tail.shape[0]), _ptr(self.pool),
+                               _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
+                               _ptr(self.status))
+        found = (desc, ctypes.byref(desc), index, rows)
+        self.__dict__["_desc"] = (key, found)
+        return found
+
+
 @dataclasses.dataclass
-class Kv8Cache:
+class Kv8Cache(_PagedCache):
     """Device tensors of one layer's 8-bit cache plus its C descriptor.
 
     pool: uint8 [num_pages, Hkv, 32d + 16]; tail: bfloat16 [num_tails, Hkv, 2, 16d];
@@ -504,56 +590,47 @@ class Kv8Cache:
     tail_ids: object = None
     status: object = None
 
-    def desc(self) -> Kv8Desc:
-        return self._checked()[0]
+    @staticmethod
+    def _block_bytes(d: int) -> int:
+        return 32 * d + 16
 
-    def _checked(self):
-        """(descriptor, device index, pages-table rows), checked again when a tensor or a
-        field has been replaced."""
-        pool, tail, table, ids, status = (self.pool, self.tail, self.page_table, self.tail_ids,
-                                          self.status)
-        key = (pool.data_ptr(), pool.shape, pool.dtype, pool.is_contiguous(),
-               tail.data_ptr(), tail.shape, tail.dtype, tail.is_contiguous(),
-               table.data_ptr(), table.shape, table.dtype, table.is_contiguous(),
-               None if ids is None else (ids.data_ptr(), ids.shape, ids.dtype, ids.is_contiguous()),
-               None if status is None else (status.data_ptr(), status.dtype),
-               self.fmt, self.num_q_heads, self.num_kv_heads, self.head_dim)
-        cached = self.__dict__.get("_desc")
-        if cached is not None and cached[0] == key:
-            return cached[1]
-        import torch
-        fn, h, d = "Kv8Cache", self.num_kv_heads, self.head_dim
-        index = _device_of(fn, "pool", self.pool)
-        _need(self.pool.dtype is torch.uint8 and self.pool.is_contiguous()
-              and self.pool.shape[1:] == (h, 32 * d + 16), fn,
-              f"pool must be a contiguous uint8 tensor [num_pages][{h}][{32 * d + 16}]")
-        _need(self.tail.dtype is torch.bfloat16 and self.tail.is_contiguous()
-              and self.tail.get_device() == index and self.tail.shape[1:] == (h, 2, 16 * d), fn,
-              f"tail must be a contiguous bfloat16 tensor [num_tails][{h}][2][{16 * d}] on cuda:{index}")
-        _i32(fn, "page_table", self.page_table, index)
-        _need(self.page_table.dim() == 2, fn, "page_table must be [batch][max_pages_per_seq]")
-        rows = int(self.page_table.shape[0])
-        if self.tail_ids is not None:
-            _i32(fn, "tail_ids", self.tail_ids, index)
-            _need(self.tail_ids.numel() == rows, fn,
-                  "tail_ids must have an entry per row of the page table")
-        if self.status is not None:
-            _i32(fn, "status", self.status, index)
-        desc = Kv8Desc(h, self.num_q_heads, d, int(self.page_table.shape[1]),
-                       int(self.pool.shape[0]), int(self.tail.shape[0]), _ptr(self.pool),
-                       _ptr(self.tail), _ptr(self.page_table), _ptr(self.tail_ids),
-                       _ptr(self.status), self.fmt)
-        found = (desc, ctypes.byref(desc), index, rows)
-        self.__dict__["_desc"] = (key, found)
-        return found
+    def _make_desc(self, *fields) -> Kv8Desc:
+        return Kv8Desc(*fields, self.fmt)
 
 
-def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int, stream=None):
-    """Place the rows of k and v (bf16 [n][Hkv][d], rows may be strided): sequence b's
-    rows row_starts[b] .. row_starts[b+1] - 1 go behind its lens_before[b] tokens.
-    max_new: the most rows that one sequence brings."""
-    fn = "oscar_kv8_place"
-    _, desc, index, rows = cache._checked()
+@dataclasses.dataclass
+class Kv4Cache(_PagedCache):
+    """Device tensors of one layer's 4-bit cache plus its C descriptor.
+
+    pool: uint8 [num_pages, Hkv, 18d + 16]; the others as ``Kv8Cache``'s.
+    ``pages.allocate_kv4`` makes one.
+    """
+    num_kv_heads: int
+    num_q_heads: int
+    head_dim: int
+    pool: object
+    tail: object
+    page_table: object
+    tail_ids: object = None
+    status: object = None
+
+    @staticmethod
+    def _block_bytes(d: int) -> int:
+        return 18 * d + 16
+
+    @staticmethod
+    def _make_desc(*fields) -> Kv4Desc:
+        return Kv4Desc(*fields)
+
+
+def _checked_cache(fn: str, cache, kind):
+    if not isinstance(cache, kind):
+        raise ValueError(f"{fn}: cache must be a {kind.__name__}")
+    return cache._checked()
+
+
+def _place(fn, kind, cache, k, v, lens_before, row_starts, max_new, stream):
+    _, desc, index, rows = _checked_cache(fn, cache, kind)
     n, h, d = k.shape[0], cache.num_kv_heads, cache.head_dim
     ks = _rows(fn, "k", k, n, h, d, index)
     vs = _rows(fn, "v", v, n, h, d, index)
@@ -566,12 +643,8 @@ def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int
             _fits(fn, "max_new", max_new))
 
 
-def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
-                     stream=None):
-    """Read tokens back as bf16: rows row_starts[b] .. row_starts[b+1] - 1 of k_out and
-    v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on."""
-    fn = "oscar_kv8_gather"
-    _, desc, index, rows = cache._checked()
+def _gather(fn, kind, cache, seq_lens, first, row_starts, max_rows, k_out, v_out, stream):
+    _, desc, index, rows = _checked_cache(fn, cache, kind)
     n, h, d = k_out.shape[0], cache.num_kv_heads, cache.head_dim
     if (_rows(fn, "k_out", k_out, n, h, d, index) != h * d
             or _rows(fn, "v_out", v_out, n, h, d, index) != h * d):
@@ -586,25 +659,17 @@ def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int
             k_out.data_ptr(), v_out.data_ptr())
 
 
-def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
-    """Bytes for oscar_kv8_attention of no more sequences, rows and tokens; 0: invalid."""
+def _workspace_size(fn, kind, cache, batch, m_rows, max_seq_len) -> int:
     import torch
-    fn = "oscar_kv8_workspace_size"
-    _, desc, index, _ = cache._checked()
+    _, desc, index, _ = _checked_cache(fn, cache, kind)
     for name, value in (("batch", batch), ("m_rows", m_rows), ("max_seq_len", max_seq_len)):
         _fits(fn, name, value)
     with torch.cuda.device(index):   # its number of SMs counts
-        return int(lib().oscar_kv8_workspace_size(desc, batch, m_rows, max_seq_len))
+        return int(getattr(lib(), fn)(desc, batch, m_rows, max_seq_len))
 
 
-def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,
-                        stream=None):
-    """Attention over the 8-bit cache.  Decode: q, out bf16 [B][Hq][d], every row sees
-    the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
-    row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros).
-    max_seq_len decides the form of the kernel: announce no more than is needed."""
-    fn = "oscar_kv8_attention"
-    _, desc, index, rows = cache._checked()
+def _attention(fn, kind, cache, q, seq_lens, max_seq_len, out, workspace, q_pos, stream):
+    _, desc, index, rows = _checked_cache(fn, cache, kind)
     lens, batch = _i32(fn, "seq_lens", seq_lens, index), seq_lens.numel()
     if q_pos is None:
         m_rows, pos, shape = 1, None, (batch, cache.num_q_heads, cache.head_dim)
@@ -625,6 +690,60 @@ def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, wor
     _launch(fn, index, stream, desc, q.data_ptr(), lens, pos, batch, m_rows,
             _fits(fn, "max_seq_len", max_seq_len),
             out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def oscar_kv8_place(cache: Kv8Cache, k, v, lens_before, row_starts, max_new: int, stream=None):
+    """Place the rows of k and v (bf16 [n][Hkv][d], rows may be strided): sequence b's
+    rows row_starts[b] .. row_starts[b+1] - 1 go behind its lens_before[b] tokens.
+    max_new: the most rows that one sequence brings."""
+    _place("oscar_kv8_place", Kv8Cache, cache, k, v, lens_before, row_starts, max_new, stream)
+
+
+def oscar_kv8_gather(cache: Kv8Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
+                     stream=None):
+    """Read tokens back as bf16: rows row_starts[b] .. row_starts[b+1] - 1 of k_out and
+    v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on."""
+    _gather("oscar_kv8_gather", Kv8Cache, cache, seq_lens, first, row_starts, max_rows, k_out, v_out,
+            stream)
+
+
+def oscar_kv8_workspace_size(cache: Kv8Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
+    """Bytes for oscar_kv8_attention of no more sequences, rows and tokens; 0: invalid."""
+    return _workspace_size("oscar_kv8_workspace_size", Kv8Cache, cache, batch, m_rows, max_seq_len)
+
+
+def oscar_kv8_attention(cache: Kv8Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,
+                        stream=None):
+    """Attention over the 8-bit cache.  Decode: q, out bf16 [B][Hq][d], every row sees
+    the seq_lens[b] tokens stored.  With q_pos (int32 [B][M]): q, out [B][M][Hq][d],
+    row (b, m) sees positions 0 .. q_pos[b][m] (negative: a padded row, zeros).
+    max_seq_len decides the form of the kernel: announce no more than is needed."""
+    _attention("oscar_kv8_attention", Kv8Cache, cache, q, seq_lens, max_seq_len, out, workspace, q_pos,
+               stream)
+
+
+def oscar_kv4_place(cache: Kv4Cache, k, v, lens_before, row_starts, max_new: int, stream=None):
+    """oscar_kv8_place into a 4-bit cache."""
+    _place("oscar_kv4_place", Kv4Cache, cache, k, v, lens_before, row_starts, max_new, stream)
+
+
+def oscar_kv4_gather(cache: Kv4Cache, seq_lens, first, row_starts, max_rows: int, k_out, v_out,
+                     stream=None):
+    """oscar_kv8_gather from a 4-bit cache."""
+    _gather("oscar_kv4_gather", Kv4Cache, cache, seq_lens, first, row_starts, max_rows, k_out, v_out,
+            stream)
+
+
+def oscar_kv4_workspace_size(cache: Kv4Cache, batch: int, m_rows: int, max_seq_len: int) -> int:
+    """Bytes for oscar_kv4_attention of no more sequences, rows and tokens; 0: invalid."""
+    return _workspace_size("oscar_kv4_workspace_size", Kv4Cache, cache, batch, m_rows, max_seq_len)
+
+
+def oscar_kv4_attention(cache: Kv4Cache, q, seq_lens, max_seq_len: int, out, workspace, q_pos=None,
+                        stream=None):
+    """oscar_kv8_attention over a 4-bit cache."""
+    _attention("oscar_kv4_attention", Kv4Cache, cache, q, seq_lens, max_seq_len, out, workspace, q_pos,
+               stream)
 
 
 def oscar_extend_pages(page_table, lens, new_tokens, free_pages, cursor, lens_after, page_starts,

@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liboscar.so")
-SOURCES = ["host_rotation.cpp", "quantize.cu", "decode.cu", "calib.cu",
-           "kv8_attention.cu", "kv8_rows.cu", "kv8_cache.cu", "positions.cu"]
+SOURCES = ["host_rotation.cpp", "quantize.cu", "decode.cu", "calib.cu", "gather.cu",
+           "kv8_attention.cu", "kv8_rows.cu", "kv8_cache.cu", "kv4_attention.cu", "kv4_cache.cu",
+           "positions.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -249,6 +249,10 @@ inline int code_planes(const oscar_cache_desc* c) { return c->code_bits == 4 ? 2
 // Checks shared by the calls on the 8-bit cache (kv8_attention.cu).
 oscar_status check_kv8(const oscar_kv8_desc* c);
 
+// And on the 4-bit cache (kv4_attention.cu): also its descriptor as the 8-bit kernels take it, with a
+// format of its own.
+oscar_status check_kv4(const oscar_kv4_desc* c, oscar_kv8_desc* as8);
+
 int sm_count();
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (function, device);

@@ -1,0 +1,421 @@
+// Placement into the 4-bit cache and reading back (kv4_layout.cuh).
+//
+//   a = max |x| over the 16 tokens and d channels of a page (finite values), g = fl32(a / 2688);
+//   per block of 16 (a channel's 16 tokens for keys, 16 channels of a token for values)
+//   s = e4m3(fl32(max|x| fl32(448 / a))), code = e2m1(fl32(x fl32(fl32(2688 / a) / s))).
+// As in the 8-bit cache a page is coded once, when its 16 tokens are there, and they lie in
+// the sequence's bf16 tail block until then.
+//
+// One warp does one (page, KV head, keys or values), its 16 x d values in registers: a lane has 4
+// channels of all tokens (of 8 tokens for d = 64), so that maxima over tokens stay in a lane and
+// those over 16 channels take two shuffles; the codes cross lanes once, to be stored 16 bytes a lane.
+#include "kv4_layout.cuh"
+#include "kv8_spans.cuh"
+
+namespace oscar {
+
+// A lane's values: channels 4 cg .. 4 cg + 3 (two words) of tokens t0 .. t0 + kTokens - 1.
+template <int D>
+struct Lane4 {
+  static constexpr int kTokens = D / 8;
+  static __device__ __forceinline__ int cg(int lane) { return lane % (D / 4); }
+  static __device__ __forceinline__ int t0(int lane) { return lane / (D / 4) * kTokens; }
+};
+
+// The values of page pg: tokens before s.t0 from the tail, the others from the rows.
+template <int D>
+__device__ __forceinline__ void load_values(const Kv8CacheParams& p, const Span& s, int h, int kv, int pg,
+                                            const uint16_t* tail, int lane,
+                                            uint32_t (&x)[Lane4<D>::kTokens][2]) {
+  const int cg = Lane4<D>::cg(lane), t0 = Lane4<D>::t0(lane);
+  const int64_t stride = kv ? p.v_stride : p.k_stride;
+  // row of the page's token 0 (not read where the token comes from the tail)
+  const uint16_t* base = (kv ? p.v : p.k) + (s.r0 + (static_cast<int64_t>(pg) * kPage - s.t0)) * stride + h * D + 4 * cg;
+  const int old = s.t0 - pg * kPage;   // tokens of the page that lie in the tail
+#pragma unroll
+  for (int i = 0; i < Lane4<D>::kTokens; ++i) {
+    const int t = t0 + i;
+    if (t >= old) {
+      const uint2 w = *reinterpret_cast<const uint2*>(base + t * stride);
+      x[i][0] = w.x;
+      x[i][1] = w.y;
+    } else if (kv == 0) {
+      const uint2 w = *reinterpret_cast<const uint2*>(tail + kv8_key_chunk(t, cg >> 2) * 16 + 4 * (cg & 3));
+      x[i][0] = w.x;
+      x[i][1] = w.y;
+    } else {
+      const uint16_t* w = tail + kv8_value_chunk(t >> 2, cg) * 16 + (t & 3);
+      x[i][0] = w[0] | (static_cast<uint32_t>(w[4]) << 16);
+      x[i][1] = w[8] | (static_cast<uint32_t>(w[12]) << 16);
+    }
+  }
+}
+
+// The largest finite magnitude (bf16 bits); NaN become 0, infinities that magnitude.
+template <int kTokens>
+__device__ __forceinline__ uint32_t finite_values(const Kv8CacheParams& p, uint32_t (&x)[kTokens][2]) {
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) top2 = __vmaxu2(top2, x[i][j] & 0x7fff7fffu);
+  uint32_t amax = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+  if (amax < 0x7f80u) return amax;
+  report(p, OSCAR_DEVERR_NONFINITE);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w = x[i][j];
+      if ((w & 0x7fffu) > 0x7f80u) w &= 0xffff0000u;
+      if ((w & 0x7fff0000u) > 0x7f800000u) w &= 0xffffu;
+      x[i][j] = w;
+      const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+      top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    }
+  amax = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w = x[i][j];
+      if ((w & 0x7fffu) == 0x7f80u) w = (w & 0xffff8000u) | amax;
+      if ((w & 0x7fff0000u) == 0x7f800000u) w = (w & 0x8000ffffu) | (amax << 16);
+      x[i][j] = w;
+    }
+  return amax;
+}
+
+// Scale byte of a block whose largest magnitude is m (bf16 bits), and what its values are times to
+// be codes: 0 for a block that is stored as zeros.
+struct PageScale {
+  float to_block, to_code;   // fl32(448 / a), fl32(2688 / a)
+};
+__device__ __forceinline__ uint32_t block_scale(uint32_t m, PageScale g, float& r) {
+  const float y = __fmul_rn(__uint_as_float(m << 16), g.to_block);
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(two) : "f"(0.f), "f"(y));
+  const uint32_t byte = two & 0xffu;
+  uint32_t lo, hi;
+  kv4_scales(byte, lo, hi);
+  const float s = half_lo(lo);
+  r = s > 0.f ? __fdiv_rn(g.to_code, s) : 0.f;
+  return byte;
+}
+
+__device__ __forceinline__ uint32_t codes8(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, const float (&r)[8]) {
+  const float y[8] = {__fmul_rn(bf16_lo_value(x0), r[0]), __fmul_rn(bf16_hi_value(x0), r[1]),
+                      __fmul_rn(bf16_lo_value(x1), r[2]), __fmul_rn(bf16_hi_value(x1), r[3]),
+                      __fmul_rn(bf16_lo_value(x2), r[4]), __fmul_rn(bf16_hi_value(x2), r[5]),
+                      __fmul_rn(bf16_lo_value(x3), r[6]), __fmul_rn(bf16_hi_value(x3), r[7])};
+  return kv4_codes8(y);
+}
+
+// v[k] of lane l among four neighbours becomes lane k's v[l].
+__device__ __forceinline__ void transpose_quad(uint32_t (&v)[4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & bit) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k | bit], bit);
+      if (up) v[k] = got;
+      else v[k | bit] = got;
+    }
+  }
+}
+
+// Codes and scales of a page's keys.
+template <int D>
+__device__ __forceinline__ void store_keys(uint8_t* blk, int lane, PageScale g, const uint32_t (&x)[Lane4<D>::kTokens][2]) {
+  constexpr int kTokens = Lane4<D>::kTokens;
+  const int cg = Lane4<D>::cg(lane), t0 = Lane4<D>::t0(lane);
+  uint32_t m[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) m[j] = __vmaxu2(m[j], x[i][j] & 0x7fff7fffu);
+  if constexpr (D == 64) {
+    m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 16));
+    m[1] = __vmaxu2(m[1], __shfl_xor_sync(0xffffffffu, m[1], 16));
+  }
+  float r[8];
+  uint32_t scales = block_scale(m[0] & 0xffffu, g, r[0]);
+  scales |= block_scale(m[0] >> 16, g, r[1]) << 8;
+  scales |= block_scale(m[1] & 0xffffu, g, r[2]) << 16;
+  scales |= block_scale(m[1] >> 16, g, r[3]) << 24;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[4 + i] = r[i];
+  if (t0 == 0) *reinterpret_cast<uint32_t*>(blk + Kv4Fmt<D>::kKeyScales + 4 * cg) = scales;
+  // two tokens of 4 channels a word; the four lanes of 16 channels share theirs out
+  const int l = lane & 3;
+  uint4* out = reinterpret_cast<uint4*>(blk) + (cg >> 4) * 32 + ((cg >> 2) & 3);
+#pragma unroll
+  for (int half = 0; half < kTokens / 8; ++half) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = 8 * half + 2 * k;
+      w[k] = codes8(x[i][0], x[i][1], x[i + 1][0], x[i + 1][1], r);
+    }
+    transpose_quad(w, lane);
+    out[4 * (t0 / 2 + 4 * half + l)] =
+        make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                   __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+  }
+}
+
+// Codes and scales of a page's values.
+template <int D>
+__device__ __forceinline__ void store_values(uint8_t* blk, int lane, PageScale g, const uint32_t (&x)[Lane4<D>::kTokens][2]) {
+  constexpr int kTokens = Lane4<D>::kTokens, kOwn = kTokens / 4;
+  const int cg = Lane4<D>::cg(lane), t0 = Lane4<D>::t0(lane), l = lane & 3;
+  // largest magnitudes of (token 2i, token 2i + 1) over the 16 channels of four lanes
+  uint32_t m[kTokens / 2];
+#pragma unroll
+  for (int i = 0; i < kTokens / 2; ++i) {
+    const uint32_t a = __vmaxu2(x[2 * i][0] & 0x7fff7fffu, x[2 * i][1] & 0x7fff7fffu);
+    const uint32_t b = __vmaxu2(x[2 * i + 1][0] & 0x7fff7fffu, x[2 * i + 1][1] & 0x7fff7fffu);
+    m[i] = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+    m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+  }
+  // a lane finds the scales of kOwn tokens, l kOwn and on
+  float own[kOwn];
+  uint32_t scales = 0;
+#pragma unroll
+  for (int k = 0; k < kOwn; k += 2) {
+    uint32_t pair = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (l == i) pair = m[(i * kOwn + k) / 2];
+    scales |= block_scale(pair & 0xffffu, g, own[k]) << (8 * k);
+    scales |= block_scale(pair >> 16, g, own[k + 1]) << (8 * k + 8);
+  }
+  uint8_t* at = blk + Kv4Fmt<D>::kValueScales + kv4_value_scale(t0 + l * kOwn, cg >> 2);
+  if constexpr (kOwn == 4) *reinterpret_cast<uint32_t*>(at) = scales;
+  else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(scales);
+  // four tokens of two channels a word: both words of a group of four tokens
+  uint32_t w[kTokens / 4][2];
+#pragma unroll
+  for (int q = 0; q < kTokens / 4; ++q) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = r[4 + i] = __shfl_sync(0xffffffffu, own[(4 * q + i) % kOwn], (lane & ~3) | ((4 * q + i) / kOwn));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t a = __byte_perm(x[4 * q][j], x[4 * q + 1][j], 0x5410);       // channel 2j of tokens 0, 1
+      const uint32_t b = __byte_perm(x[4 * q + 2][j], x[4 * q + 3][j], 0x5410);
+      const uint32_t c = __byte_perm(x[4 * q][j], x[4 * q + 1][j], 0x7632);       // channel 2j + 1
+      const uint32_t d = __byte_perm(x[4 * q + 2][j], x[4 * q + 3][j], 0x7632);
+      w[q][j] = codes8(a, b, c, d, r);
+    }
+  }
+  // with the lane of the channels 32 further: a chunk is 4 tokens of both lanes' channels
+  const int high = (cg >> 3) & 1;
+  uint4* out = reinterpret_cast<uint4*>(blk + Kv4Fmt<D>::kCodes) + (cg >> 4) * 32 + 4 * (cg & 7) + t0 / 4;
+  constexpr int kHalf = kTokens / 8;   // chunks a lane stores
+#pragma unroll
+  for (int q = 0; q < kHalf; ++q) {
+    uint32_t mine[2], got[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mine[j] = high ? w[kHalf + q][j] : w[q][j];
+      got[j] = __shfl_xor_sync(0xffffffffu, high ? w[q][j] : w[kHalf + q][j], 8);
+    }
+    out[high * kHalf + q] = high ? make_uint4(got[0], got[1], mine[0], mine[1]) : make_uint4(mine[0], mine[1], got[0], got[1]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_page(const Kv8CacheParams& p, int h, int kv, int64_t id, int lane,
+                                           uint32_t (&x)[Lane4<D>::kTokens][2]) {
+  using F = Kv4Fmt<D>;
+  const float a = __uint_as_float(finite_values(p, x) << 16);
+  const bool live = a >= kKv4Least;
+  const PageScale g = {live ? __fdiv_rn(kKv4BlockTop, a) : 0.f, live ? __fdiv_rn(kKv4Top, a) : 0.f};
+  uint8_t* blk = p.pool + (id * p.hkv + h) * F::kBlock;
+  if (kv == 0) store_keys<D>(blk, lane, g, x);
+  else store_values<D>(blk, lane, g, x);
+  if (lane < 2) {   // the scale and one spare word
+    float* w = reinterpret_cast<float*>(blk + F::kScales) + kv + 2 * lane;
+    *w = lane == 0 && live ? __fdiv_rn(a, kKv4Top) : 0.f;
+  }
+}
+
+// blockIdx.x: (sequence, page of its rows), blockIdx.y: kCWarps (KV head, K/V) each.
+// The warp of a sequence's first page also writes the tail: the first page may
+// take tokens from the tail that the last ones are about to overwrite.
+template <int D>
+__global__ void __launch_bounds__(32 * kCWarps, 8) kv4_place_kernel(const __grid_constant__ Kv8CacheParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, unit = blockIdx.y * kCWarps + (threadIdx.x >> 5);
+  if (unit >= 2 * p.hkv) return;
+  const int h = unit >> 1, kv = unit & 1;
+  const int b = blockIdx.x / p.pages_per_seq, i = blockIdx.x - b * p.pages_per_seq;
+  Span s;
+  if (!span_of(p, b, s)) return;
+  const int pg = s.t0 / kPage + i, whole = s.t1 / kPage;
+  uint16_t* tail = nullptr;
+  const bool reads_tail = i == 0 && pg < whole && s.t0 % kPage != 0;
+  const bool writes_tail = i == 0 && s.t1 % kPage != 0;
+  if (reads_tail || writes_tail) {
+    tail = tail_area<D>(p, b, h, kv);
+    if (!tail && pg >= whole) return;
+  }
+  if (pg < whole && !(reads_tail && !tail)) {
+    const int64_t id = page_id(p, b, pg);
+    if (id >= 0) {
+      uint32_t x[Lane4<D>::kTokens][2];
+      load_values<D>(p, s, h, kv, pg, tail, lane, x);
+      store_page<D>(p, h, kv, id, lane, x);
+    }
+    __syncwarp();   // the tail has been read
+  }
+  if (writes_tail && tail) store_tail<D>(p, s, h, kv, max(s.t0, whole * kPage), tail, lane);
+}
+
+// A lane's chunk of codes, and their scales, as four rows of eight (keys: two tokens x 16 channels) or of
+// four and four (values: four tokens x 2 x 4 channels) bf16.
+__device__ __forceinline__ uint32_t value_pair(uint32_t codes, uint32_t scales, float g) {
+  const uint32_t x = hmul2_u32(codes, scales);
+  return pack_bf162(__fmul_rn(half_lo(x), g), __fmul_rn(half_hi(x), g));
+}
+
+// Codes back to bf16, rounded once from fl32(code s g); tail tokens as they are.
+template <int D>
+__global__ void __launch_bounds__(32 * kCWarps) kv4_gather_kernel(const __grid_constant__ Kv8CacheParams p) {
+  using F = Kv4Fmt<D>;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, unit = blockIdx.y * kCWarps + (threadIdx.x >> 5);
+  if (unit >= 2 * p.hkv) return;
+  const int h = unit >> 1, kv = unit & 1;
+  const int b = blockIdx.x / p.pages_per_seq, i = blockIdx.x - b * p.pages_per_seq;
+  Span s;
+  if (!span_of(p, b, s)) return;
+  const int pg = s.t0 / kPage + i, len = p.seq_lens[b];
+  // rows behind the stored tokens are left as they were
+  if (s.t1 > len || len >= (static_cast<int64_t>(p.max_pages) + 1) * kPage) {
+    report(p, OSCAR_DEVERR_SEQ_LEN);
+    return;
+  }
+  if (pg * kPage >= s.t1) return;
+  const int lo = max(s.t0 - pg * kPage, 0), hi = min(s.t1 - pg * kPage, kPage);
+  uint16_t* out = (kv ? p.v_out : p.k_out) +
+      ((s.r0 + (static_cast<int64_t>(pg) * kPage - s.t0)) * p.hkv + h) * D;
+  const int64_t stride = static_cast<int64_t>(p.hkv) * D;
+  if (pg >= len / kPage) {
+    const uint16_t* tail = tail_area<D>(p, b, h, kv);
+    if (!tail) return;
+    constexpr int kPer = D / 4;
+    for (int n = lane; n < (hi - lo) * kPer; n += 32) {
+      const int t = lo + n / kPer, cg = n % kPer;
+      uint2 w;
+      if (kv == 0) {
+        w = *reinterpret_cast<const uint2*>(tail + kv8_key_chunk(t, cg >> 2) * 16 + 4 * (cg & 3));
+      } else {
+        const uint16_t* a = tail + kv8_value_chunk(t >> 2, cg) * 16 + (t & 3);
+        w = make_uint2(a[0] | (static_cast<uint32_t>(a[4]) << 16), a[8] | (static_cast<uint32_t>(a[12]) << 16));
+      }
+      *reinterpret_cast<uint2*>(out + t * stride + 4 * cg) = w;
+    }
+    return;
+  }
+  const int64_t id = page_id(p, b, pg);
+  if (id < 0) return;
+  const uint8_t* blk = p.pool + (id * p.hkv + h) * F::kBlock;
+  const float g = reinterpret_cast<const float*>(blk + F::kScales)[kv];
+  const int gid = lane >> 2, tig = lane & 3;
+  uint4 c[D / 64], sk[D / 64];
+  uint2 sv[D / 64];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    c[j] = reinterpret_cast<const uint4*>(blk + kv * F::kCodes)[32 * j + lane];
+    if (kv == 0) sk[j] = reinterpret_cast<const uint4*>(blk + F::kKeyScales)[4 * j + tig];
+    else sv[j] = reinterpret_cast<const uint2*>(blk + F::kValueScales)[8 * j + 4 * (gid >> 2) + tig];
+  }
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+    if (kv == 0) {
+      uint32_t s[8];
+      kv4_scales(sk[j].x, s[0], s[1]);
+      kv4_scales(sk[j].y, s[2], s[3]);
+      kv4_scales(sk[j].z, s[4], s[5]);
+      kv4_scales(sk[j].w, s[6], s[7]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 2 * gid + e;
+        if (t < lo || t >= hi) continue;
+        uint4* dst = reinterpret_cast<uint4*>(out + t * stride + 64 * j + 16 * tig);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[4];
+          kv4_pairs(w[2 * e + half], x[0], x[1], x[2], x[3]);
+          dst[half] = make_uint4(value_pair(x[0], s[4 * half], g), value_pair(x[1], s[4 * half + 1], g),
+                                 value_pair(x[2], s[4 * half + 2], g), value_pair(x[3], s[4 * half + 3], g));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t s01, s23;
+        kv4_scales(half ? sv[j].y : sv[j].x, s01, s23);
+        uint32_t x[8];   // channel c: tokens 0..3 in x[2c], x[2c + 1]
+        kv4_pairs(w[2 * half], x[0], x[1], x[2], x[3]);
+        kv4_pairs(w[2 * half + 1], x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = value_pair(x[k], k & 1 ? s23 : s01, g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 4 * tig + r;
+          const uint32_t sel = (r & 1) ? 0x7632 : 0x5410;
+          if (t >= lo && t < hi)
+            *reinterpret_cast<uint2*>(out + t * stride + 64 * j + 32 * half + 4 * gid) =
+                make_uint2(__byte_perm(x[r >> 1], x[2 + (r >> 1)], sel), __byte_perm(x[4 + (r >> 1)], x[6 + (r >> 1)], sel));
+        }
+      }
+    }
+  }
+}
+
+}  // namespace oscar
+
+using namespace oscar;
+
+extern "C" {
+
+oscar_status oscar_kv4_place(const oscar_kv4_desc* desc, const void* k, const void* v,
+                             int64_t k_stride, int64_t v_stride, const int32_t* lens_before,
+                             const int32_t* row_starts, int32_t batch, int64_t total_rows,
+                             int32_t max_new, void* stream) {
+  oscar_kv8_desc c;
+  oscar_status s = oscar_host::check_kv4(desc, &c);
+  if (s != OSCAR_OK) return s;
+  Kv8CacheParams p{};
+  s = place_params(&c, k, v, k_stride, v_stride, lens_before, row_starts, batch, total_rows, max_new, &p);
+  if (s != OSCAR_OK || p.batch == 0) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.head_dim == 128 ? launch_cache(kv4_place_kernel<128>, p, st) : launch_cache(kv4_place_kernel<64>, p, st);
+}
+
+oscar_status oscar_kv4_gather(const oscar_kv4_desc* desc, const int32_t* seq_lens,
+                              const int32_t* first, const int32_t* row_starts, int32_t batch,
+                              int64_t total_rows, int32_t max_rows, void* k_out, void* v_out,
+                              void* stream) {
+  oscar_kv8_desc c;
+  oscar_status s = oscar_host::check_kv4(desc, &c);
+  if (s != OSCAR_OK) return s;
+  Kv8CacheParams p{};
+  s = gather_params(&c, seq_lens, first, row_starts, batch, total_rows, max_rows, k_out, v_out, &p);
+  if (s != OSCAR_OK || p.batch == 0) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.head_dim == 128 ? launch_cache(kv4_gather_kernel<128>, p, st) : launch_cache(kv4_gather_kernel<64>, p, st);
+}
+
+}  // extern "C"

@@ -150,6 +150,12 @@ __device__ __forceinline__ uint4 load16(const uint8_t* src) {
   return x;
 }
 
+__device__ __forceinline__ uint2 load8(const uint8_t* src) {
+  uint2 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n" : "=r"(x.x), "=r"(x.y) : "l"(src));
+  return x;
+}
+
 // Four codes as fp16 pairs in order, exact.
 template <bool kE4m3>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -206,6 +212,47 @@ __device__ __forceinline__ void store_values(uint8_t* dst, int c, int w, int lan
     uint2 o;
     code_pairs<kE4m3>(in[k], o.x, o.y);
     *reinterpret_cast<uint2*>(dst + value_place(lane, c, w, k)) = o;
+  }
+}
+
+// A lane's chunk j of a page's 4-bit key codes, tokens 2 (lane / 4) and that + 1, channels 64 j + 16 (lane % 4)
+// and on, times the scales of the channels: chunks 2 j and 2 j + 1 of the 8-bit order.
+__device__ __forceinline__ void store_keys4(uint8_t* dst, int j, int lane, uint4 x, uint4 sc) {
+  const int turn = (lane >> 2) & 1;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {   // 8 channels of both tokens, the other 8
+    const int half = turn ^ k;
+    uint32_t s[4];
+    kv4_scales(half ? sc.z : sc.x, s[0], s[1]);
+    kv4_scales(half ? sc.w : sc.y, s[2], s[3]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t o[4];
+      kv4_pairs(half ? (e ? x.w : x.y) : (e ? x.z : x.x), o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + key_place(lane, 2 * j + e, half)) =
+          make_uint4(hmul2_u32(o[0], s[0]), hmul2_u32(o[1], s[1]), hmul2_u32(o[2], s[2]), hmul2_u32(o[3], s[3]));
+    }
+  }
+}
+
+// Its chunk i of 4-bit value codes, tokens 4 (lane % 4) and on, channels 64 i + 4 (lane / 4) and on and those 32 further:
+// chunks 2 i and 2 i + 1 of the 8-bit order.
+__device__ __forceinline__ void store_values4(uint8_t* dst, int i, int w, int lane, uint4 x, uint2 sc) {
+  const bool turn = value_channel(lane, 0);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t s01, s23;
+    kv4_scales(half ? sc.y : sc.x, s01, s23);
+    const uint32_t lo = half ? x.z : x.x, hi = half ? x.w : x.y;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      uint32_t o[4];
+      kv4_pairs(turn != (k != 0) ? hi : lo, o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint2*>(dst + value_place(lane, 2 * i + half, w, k)) =
+          make_uint2(hmul2_u32(o[0], s01), hmul2_u32(o[1], s23));
+      *reinterpret_cast<uint2*>(dst + value_place(lane, 2 * i + half, w, k + 1)) =
+          make_uint2(hmul2_u32(o[2], s01), hmul2_u32(o[3], s23));
+    }
   }
 }
 
@@ -551,11 +598,11 @@ __device__ __noinline__ RowState settle(RowState r, float big, uint32_t ts, uint
   return r;
 }
 
-template <int D, bool kE4m3>
+template <int D, int kCode>
 __global__ void __launch_bounds__(kRThreads, 1)
 kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   using S = RowsSmem<D>;
-  using F = Kv8Fmt<D>;
+  using F = KvFmt<D, kCode>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -695,7 +742,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
       PageBlocks blocks(p, u, lane);
-      uint4 x[2][D / 32];
+      constexpr int kChunks = F::kCodes / 512;   // 16 bytes a lane
+      uint4 x[2][kChunks];
+      uint2 vs[2][kCode == kCodeE2m1 ? kChunks : 1];   // their scales (4 bits)
       // the codes of this warp's pages of tile i
       auto request = [&](int i) {
         blocks.tile(p, u, i, lane);
@@ -704,7 +753,13 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         for (int half = 0; half < 2; ++half) {
           const uint8_t* src = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + F::kCodes + 16 * lane;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < kChunks; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
+          if constexpr (kCode == kCodeE2m1) {
+            const uint8_t* sc = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + F::kValueScales +
+                32 * (lane >> 4) + 8 * (lane & 3);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) vs[half][c] = b[half] >= 0 ? load8(sc + 64 * c) : make_uint2(0, 0);
+          }
         }
       };
       if (!wait(&bar->qempty, seg + 1)) break;
@@ -720,7 +775,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) store_values<kE4m3>(dst + half * (D * 128), c, w, lane, x[half][c]);
+          for (int c = 0; c < kChunks; ++c) {
+            if constexpr (kCode == kCodeE2m1) store_values4(dst + half * (D * 128), c, w, lane, x[half][c], vs[half][c]);
+            else store_values<kCode == kCodeE4m3>(dst + half * (D * 128), c, w, lane, x[half][c]);
+          }
         const int slot = u.tail_slot(i);
         if (i + 1 < u.tiles) {
           request(i + 1);
@@ -740,7 +798,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     for (bool go = true, ok = true; go && ok; go = u.next(p)) {
       if (u.tiles == 0) continue;
       PageBlocks blocks(p, u, lane);
-      uint4 x[2][D / 32];
+      constexpr int kChunks = F::kCodes / 512;   // 16 bytes a lane
+      uint4 x[2][kChunks];
+      uint4 ks[2][kCode == kCodeE2m1 ? kChunks : 1];   // their scales (4 bits)
       float2 sc;      // lanes 0 and 1: scales of the two pages
       bool shown;     // and whether there is one
       // codes and scales of this warp's pages of tile i
@@ -751,7 +811,12 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         for (int half = 0; half < 2; ++half) {
           const uint8_t* src = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + 16 * lane;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < kChunks; ++c) x[half][c] = b[half] >= 0 ? load16(src + 512 * c) : make_uint4(0, 0, 0, 0);
+          if constexpr (kCode == kCodeE2m1) {
+            const uint8_t* s = p.pool + static_cast<int64_t>(b[half]) * F::kBlock + F::kKeyScales + 16 * (lane & 3);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) ks[half][c] = b[half] >= 0 ? load16(s + 64 * c) : make_uint4(0, 0, 0, 0);
+          }
         }
         const int mine = lane ? b[1] : b[0];
         shown = mine >= 0;
@@ -772,7 +837,10 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) store_keys<kE4m3>(dst + 8192 * half, c, lane, x[half][c]);
+          for (int c = 0; c < kChunks; ++c) {
+            if constexpr (kCode == kCodeE2m1) store_keys4(dst + 8192 * half, c, lane, x[half][c], ks[half][c]);
+            else store_keys<kCode == kCodeE4m3>(dst + 8192 * half, c, lane, x[half][c]);
+          }
         if (lane < 2) {   // what the softmax needs of the two pages
           const int slot = 4 * lane + w;
           const float scale = fmaxf(sc.y, kZeroScale), off = fast_log2(scale);
@@ -955,9 +1023,9 @@ kv8_rows_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   }
 }
 
-template <int D, bool kE4m3>
+template <int D, int kCode>
 oscar_status launch_rows(const Kv8Params& p, int64_t ctas, int min_share, cudaStream_t st) {
-  const auto kernel = kv8_rows_kernel<D, kE4m3>;
+  const auto kernel = kv8_rows_kernel<D, kCode>;
   if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), RowsSmem<D>::kAlloc))
     return OSCAR_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
@@ -973,11 +1041,17 @@ oscar_status launch_rows(const Kv8Params& p, int64_t ctas, int min_share, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, p, min_share) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
-oscar_status run_kv8_rows(const Kv8Params& p, int head_dim, bool e4m3, int64_t ctas, int min_share,
+oscar_status run_kv8_rows(const Kv8Params& p, int head_dim, int code, int64_t ctas, int min_share,
                           cudaStream_t st) {
-  if (head_dim == 128)
-    return e4m3 ? launch_rows<128, true>(p, ctas, min_share, st) : launch_rows<128, false>(p, ctas, min_share, st);
-  return e4m3 ? launch_rows<64, true>(p, ctas, min_share, st) : launch_rows<64, false>(p, ctas, min_share, st);
+  const bool wide = head_dim == 128;
+  switch (code) {
+    case kCodeE4m3:
+      return wide ? launch_rows<128, kCodeE4m3>(p, ctas, min_share, st) : launch_rows<64, kCodeE4m3>(p, ctas, min_share, st);
+    case kCodeE2m1:
+      return wide ? launch_rows<128, kCodeE2m1>(p, ctas, min_share, st) : launch_rows<64, kCodeE2m1>(p, ctas, min_share, st);
+    default:
+      return wide ? launch_rows<128, kCodeInt8>(p, ctas, min_share, st) : launch_rows<64, kCodeInt8>(p, ctas, min_share, st);
+  }
 }
 
 }  // namespace oscar

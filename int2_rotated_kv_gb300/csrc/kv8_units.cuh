@@ -3,7 +3,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "kv8_layout.cuh"
+#include "kv4_layout.cuh"
 
 namespace oscar {
 
@@ -290,7 +290,7 @@ __device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity, int32_
 
 // Many query columns (tiles of 128) on the tensor-memory MMAs: kv8_rows.cu.
 constexpr int kRowsNT = 16;
-oscar_status run_kv8_rows(const Kv8Params& p, int head_dim, bool e4m3, int64_t ctas, int min_share,
+oscar_status run_kv8_rows(const Kv8Params& p, int head_dim, int code, int64_t ctas, int min_share,
                           cudaStream_t st);
 
 }  // namespace oscar

@@ -141,3 +141,25 @@ def allocate_kv8(num_pages: int, batch: int, max_pages: int, *, hkv: int, hq: in
                     dtype=torch.bfloat16, device=dev),
         torch.full((batch, max_pages), -1, dtype=torch.int32, device=dev), fmt,
         None, torch.zeros(1, dtype=torch.int32, device=dev) if with_status else None)
+
+
+def kv4_bytes_per_page(hkv: int, d: int) -> int:
+    """Pool bytes of one page of the 4-bit cache: codes and block scales of 16 keys and 16
+    values and two fp32 scales (and 8 spare bytes) per KV head."""
+    return hkv * (18 * d + 16)
+
+
+def allocate_kv4(num_pages: int, batch: int, max_pages: int, *, hkv: int, hq: int, d: int, device,
+                 num_tails: int | None = None, with_status: bool = True):
+    """``allocate_kv8`` for a 4-bit cache; returns a binding ``Kv4Cache``."""
+    import torch
+
+    from ._lib import Kv4Cache
+    dev = torch.device(device)
+    return Kv4Cache(
+        hkv, hq, d,
+        torch.zeros((num_pages, hkv, 18 * d + 16), dtype=torch.uint8, device=dev),
+        torch.zeros((batch if num_tails is None else num_tails, hkv, 2, 16 * d),
+                    dtype=torch.bfloat16, device=dev),
+        torch.full((batch, max_pages), -1, dtype=torch.int32, device=dev),
+        None, torch.zeros(1, dtype=torch.int32, device=dev) if with_status else None)
