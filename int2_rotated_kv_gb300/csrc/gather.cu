@@ -5,13 +5,28 @@
 //   x[j] = sum_c y[c] R[j][c],
 // what attention takes it for ("Technical Summary: OSCAR ...", section 2.2B: the rotation is undone
 // when the history is used).
+//
+// The product runs on tcgen05 as bf16 pieces, y = y1 + y2 and R = R1 + R2 (each to 2^-17):
+//   x = y2 R1^T + y1 R2^T + y1 R1^T,   fp32 accumulation in tensor memory.
+// M = 128 tokens (8 pages of one sequence), N = K = d; R's pieces lie in shared memory (rows of R
+// are the K-major rows of operand B as they are), y's pieces in tensor memory, where a thread writes
+// its own token's row.  A CTA keeps the R of one (KV head, keys or values) and walks over tiles of
+// tokens; two CTAs an SM, so that one's MMAs and stores run under the other's arithmetic.
+//   warps 0-7  a token and half of its channels a thread: codes to y1, y2; then the product's row to
+//              bf16 and out.  One lane of warp 0 issues the 3 d/16 MMAs of a tile.
+//   warp 8     tiles ahead: finds the next tiles that hold rows (32 at a look), and copies the codes
+//              of their pages into a ring of stages (bulk copies, one a page).
+// Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
+#include <algorithm>
+
 #include "common.cuh"
 #include "layout.cuh"
+#include "tcgen05.cuh"
 
 namespace oscar {
 
 struct GatherParams {
-  int hkv, max_pages, batch, pages_per_seq, max_rows, sink, window;
+  int hkv, max_pages, batch, tiles_per_seq, max_rows, sink, window, ctas_per_r;
   int64_t n_coded, n_plain, total_rows;
   const uint8_t* coded;
   const uint8_t* plain;
@@ -25,102 +40,369 @@ struct GatherParams {
   int32_t* status;
 };
 
-// The value of a coded token's channel j, kv: 0 key, 1 value.
+constexpr int kGTile = 128;                 // tokens of a tile
+constexpr int kGPages = kGTile / kPage;
+constexpr int kGStages = 4;
+constexpr int kGWarps = 8;                  // that compute
+constexpr int kGThreads = 32 * (kGWarps + 1);
+
+// A tile as the computing warps need it: positions of its tokens are pos0 + row.
+struct GatherTile {
+  int64_t row0;      // output row of the token at pos0 (rows before lo are not written)
+  int pos0, lo, hi;  // positions to be read back, [lo, hi)
+  int c0, c1;        // of which [c0, c1) are codes
+  int b;
+  uint32_t pages;    // bit per page: its codes are there
+  int stop;          // 1: there is no tile
+};
+
 template <int D, int P>
-__device__ __forceinline__ float coded_value(const uint8_t* blk, int kv, int t, int j) {
+struct GatherSmem {
   using F = Fmt<D, P>;
-  const int m = j >> 5, i = (j >> 4) & 1, h = (j >> 3) & 1;
-  const int at = kv ? value_byte<D>(t, j & 7, m) : key_byte<D>(t, (j >> 1) & 3, m, j & 1);
-  const uint8_t* codes = blk + (kv ? F::kVc : F::kKc) + at;
-  int code = 0;
-#pragma unroll
-  for (int q = 0; q < P; ++q) code = 4 * code + ((codes[q * F::kPlane] >> (4 * h + 2 * i)) & 3);
-  __half s, z;
-  if (kv) {
-    const int g = vsz_index<D>(t, m);
-    s = reinterpret_cast<const __half*>(blk + F::kVs)[g];
-    z = reinterpret_cast<const __half*>(blk + F::kVz)[g];
-  } else {
-    const __half2 w = reinterpret_cast<const __half2*>(blk + F::kKsz)[t * F::kNG + m];
-    s = __low2half(w);
-    z = __high2half(w);
-  }
-  return fmaf(static_cast<float>(code), __half2float(s), __half2float(z));
+  static constexpr int kPart = F::kInt2Block / 2;        // codes, scales and zeros of keys (values)
+  static_assert(F::kVc == kPart, "keys and values have the same size");
+  static constexpr int kPiece = D * D * 2;               // a piece of R
+  static constexpr int kRing = 2 * kPiece;
+  static constexpr int kTiles = kRing + kGStages * kGPages * kPart;
+  static constexpr int kBars = kTiles + kGStages * static_cast<int>(sizeof(GatherTile));
+  static constexpr int kMisc = kBars + (2 * kGStages + 2) * 8;
+  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kAlloc = kBytes + 1024;           // the base is rounded up to 1024 bytes
+  static_assert(kTiles % 16 == 0 && sizeof(GatherTile) % 8 == 0, "alignment");
+};
+
+// Two codes in the low bits of the halves of x, times s plus z, as two bf16 pieces each.
+__device__ __forceinline__ void split_pair(uint32_t x, float s, float z, uint32_t& hi, uint32_t& lo) {
+  constexpr float kMagic = 8388608.f;   // 2^23: its low bits are the code
+  const float c0 = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7610)) - kMagic;
+  const float c1 = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7632)) - kMagic;
+  const float y0 = fmaf(c0, s, z), y1 = fmaf(c1, s, z);
+  hi = pack_bf162(y0, y1);
+  lo = pack_bf162(y0 - bf16_lo_value(hi), y1 - bf16_hi_value(hi));
 }
 
-// blockIdx.x: (sequence, page of its rows), blockIdx.y: (KV head, keys or values); a thread per channel.
-template <int D, int P>
-__global__ void __launch_bounds__(D) gather_kernel(const __grid_constant__ GatherParams p) {
-  __shared__ float y[kPage][D];
-  pdl_wait();
-  pdl_trigger();
-  const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, j = threadIdx.x;
-  const int b = blockIdx.x / p.pages_per_seq, i = blockIdx.x - b * p.pages_per_seq;
-  const int64_t r0 = p.row_starts[b], n = p.row_starts[b + 1] - r0;
-  const int t0 = p.first[b], len = p.seq_lens[b];
-  if (n == 0) return;
-  if (n < 0 || n > p.max_rows || r0 < 0 || r0 + n > p.total_rows || t0 < 0 || t0 + n > len ||
-      len > static_cast<int64_t>(p.max_pages) * kPage) {
-    if (p.status && j == 0) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
-    return;
-  }
-  const int pg = t0 / kPage + i, t1 = t0 + static_cast<int>(n);
-  if (pg * kPage >= t1) return;
-  const int lo = max(t0 - pg * kPage, 0), hi = min(t1 - pg * kPage, kPage);
-  // tokens [lo, c0) and [c1, hi) of the page are in BF16
-  const int c0 = min(max(p.sink - pg * kPage, lo), hi), c1 = max(min(max(len - p.window, 0) - pg * kPage, hi), c0);
-  uint16_t* out = p.out[kv] + ((r0 + (static_cast<int64_t>(pg) * kPage - t0)) * p.hkv + h) * D + j;
-  const int64_t stride = static_cast<int64_t>(p.hkv) * D;
-  const size_t entry = static_cast<size_t>(b) * p.max_pages + pg;
-  if (c0 > lo || c1 < hi) {
-    const int id = p.plain_table[entry];
-    if (id < 0 || id >= p.n_plain) {
-      if (p.status && j == 0) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+// A thread's channels [half * D/2, ...) of the coded token t of the page at blk (keys' or values' part), to its
+// row of tensor memory: y1 from column a on, y2 from a + D/2 on, two channels a column.
+template <int D, int P, bool kValue>
+__device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, uint32_t a) {
+  using F = Fmt<D, P>;
+  constexpr int kOwn = F::kWords / 2;   // groups of 32 channels a thread has
+  const int th = t >> 3;
+  // words of a group: keys have channels 2q, 2q + 1 (and 8, 16, 24 further) of tokens t, t ^ 8 in word q, values
+  // channel gid of tokens t, t ^ 1, t ^ 8, t ^ 9 in word gid
+  uint32_t x[P][4][kOwn];
+#pragma unroll
+  for (int pl = 0; pl < P; ++pl)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint8_t* plane = blk + pl * F::kPlane + 4 * half * kOwn;
+      uint32_t w[2][kOwn];
+#pragma unroll
+      for (int e = 0; e < (kValue ? 2 : 1); ++e) {
+        const int lane = kValue ? 4 * (2 * q + e) + ((t >> 1) & 3) : 4 * (t & 7) + q;
+        if constexpr (kOwn == 2) {
+          const uint2 u = *reinterpret_cast<const uint2*>(plane + 4 * lane * F::kWords);
+          w[e][0] = u.x;
+          w[e][1] = u.y;
+        } else {
+          w[e][0] = *reinterpret_cast<const uint32_t*>(plane + 4 * lane * F::kWords);
+        }
+      }
+      // the token's byte of an even channel in the lower half, of the odd one in the upper half
+      const uint32_t sel = kValue ? 0x0400u + (2 * (t & 1) + th) * 0x0101u : 0x0200u + th * 0x0101u;
+#pragma unroll
+      for (int m = 0; m < kOwn; ++m) x[pl][q][m] = __byte_perm(w[0][m], kValue ? w[1][m] : 0u, sel);
+    }
+#pragma unroll
+  for (int m = 0; m < kOwn; ++m) {
+    const int g = half * kOwn + m;
+    float s, z;
+    if constexpr (kValue) {
+      const __half* vs = reinterpret_cast<const __half*>(blk + F::kVs - F::kVc);
+      const int at = vsz_index<D>(t, g);
+      s = __half2float(vs[at]);
+      z = __half2float(vs[(F::kVz - F::kVs) / 2 + at]);
     } else {
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(
-          p.plain + (static_cast<int64_t>(id) * p.hkv + h) * Fmt<D>::kBf16Block + kv * Fmt<D>::kBf16V);
-      for (int t = lo; t < hi; ++t)
-        if (t < c0 || t >= c1) out[t * stride] = src[kv ? bf16_value_elem(t, j) : bf16_key_elem(t, j)];
+      const uint32_t w = reinterpret_cast<const uint32_t*>(blk + F::kKsz)[t * F::kNG + g];
+      s = half_lo(w);
+      z = half_hi(w);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t c = (x[0][q][m] >> (4 * h + 2 * i)) & 0x00030003u;
+          if constexpr (P == 2) c = c * 4 + ((x[P - 1][q][m] >> (4 * h + 2 * i)) & 0x00030003u);
+          split_pair(c, s, z, hi[4 * h + q], lo[4 * h + q]);
+        }
+      tc_st8(a + 16 * g + 8 * i, hi);
+      tc_st8(a + D / 2 + 16 * g + 8 * i, lo);
     }
   }
-  if (c0 >= c1) return;
-  const int id = p.coded_table[entry];
-  if (id < 0 || id >= p.n_coded) {
-    if (p.status && j == 0) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-    return;
+}
+
+// Whether any of the computing threads says so; a barrier among them.
+__device__ __forceinline__ bool any_of(bool x) {
+  uint32_t y;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(y)
+               : "r"(static_cast<uint32_t>(x)), "n"(32 * kGWarps)
+               : "memory");
+  return y != 0;
+}
+
+// 32 bytes to a 16-byte aligned address.
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&x)[8]) {
+  reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+}
+
+template <int D, int P>
+__global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_constant__ GatherParams p) {
+  using S = GatherSmem<D, P>;
+  using F = Fmt<D, P>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  GatherTile* tiles = reinterpret_cast<GatherTile*>(smem + S::kTiles);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* empty = full + kGStages;
+  uint64_t* done = empty + kGStages;       // the MMAs of a tile; then those in flight after a give-up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int which = blockIdx.x / p.ctas_per_r, number = blockIdx.x - which * p.ctas_per_r;
+  const int h = which >> 1, kv = which & 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < kGStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kGWarps);
+    }
+    mbar_init(done, 1);
+    mbar_init(done + 1, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-  const uint8_t* blk = p.coded + (static_cast<int64_t>(id) * p.hkv + h) * Fmt<D, P>::kInt2Block;
-  for (int t = c0; t < c1; ++t) y[t][j] = coded_value<D, P>(blk, kv, t, j);
+  if (warp == 0) tc_alloc(tmem_slot, 2 * D);
+  // R as two bf16 pieces
+  const float* r = p.r[kv] + static_cast<size_t>(h) * D * D;
+  for (int i = tid; i < D * D / 8; i += kGThreads) {
+    const int row = i / (D / 8), k = 8 * (i % (D / 8));
+    const float4 a = reinterpret_cast<const float4*>(r + row * D + k)[0];
+    const float4 b = reinterpret_cast<const float4*>(r + row * D + k)[1];
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      hi[x] = pack_bf162(v[2 * x], v[2 * x + 1]);
+      lo[x] = pack_bf162(v[2 * x] - bf16_lo_value(hi[x]), v[2 * x + 1] - bf16_hi_value(hi[x]));
+    }
+    const uint32_t at = tc_sw128_offset(row, k, D);
+    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(smem + S::kPiece + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  fence_proxy_async();
+  tc_fence_before();
   __syncthreads();
-  const float4* r = reinterpret_cast<const float4*>(p.r[kv] + (static_cast<size_t>(h) * D + j) * D);
-  float acc[kPage] = {};
-  for (int c = 0; c < D / 4; ++c) {
-    const float4 w = r[c];
-#pragma unroll
-    for (int t = 0; t < kPage; ++t)
-      if (t >= c0 && t < c1) {
-        const float4 x = *reinterpret_cast<const float4*>(&y[t][4 * c]);
-        acc[t] = fmaf(x.x, w.x, fmaf(x.y, w.y, fmaf(x.z, w.z, fmaf(x.w, w.w, acc[t]))));
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == kGWarps) {
+    // ------------------------------------------------------------- tiles ahead
+    uint32_t n = 0;   // tiles published
+    bool ok = true;
+    const int64_t total = static_cast<int64_t>(p.batch) * p.tiles_per_seq;
+    auto slot_free = [&](uint32_t k) {
+      const bool got = mbar_wait(empty + k % kGStages, ((k / kGStages) & 1) ^ 1, p.status);
+      return __all_sync(0xffffffffu, got && !*abort_flag);
+    };
+    for (int64_t base = number; base < total && ok; base += static_cast<int64_t>(32) * p.ctas_per_r) {
+      // a tile a lane
+      const int64_t tile = base + static_cast<int64_t>(lane) * p.ctas_per_r;
+      GatherTile t{};
+      bool some = false;
+      if (tile < total) {
+        t.b = static_cast<int>(tile / p.tiles_per_seq);
+        const int i = static_cast<int>(tile - static_cast<int64_t>(t.b) * p.tiles_per_seq);
+        const int64_t r0 = p.row_starts[t.b], rows = p.row_starts[t.b + 1] - r0;
+        const int t0 = p.first[t.b], len = p.seq_lens[t.b];
+        if (rows != 0) {
+          if (rows < 0 || rows > p.max_rows || r0 < 0 || r0 + rows > p.total_rows || t0 < 0 || t0 + rows > len ||
+              len > static_cast<int64_t>(p.max_pages) * kPage) {
+            if (p.status) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+          } else {
+            const int64_t pos0 = (t0 / kPage + static_cast<int64_t>(kGPages) * i) * kPage;
+            if (pos0 < t0 + rows) {
+              some = true;
+              t.pos0 = static_cast<int>(pos0);
+              t.lo = max(t0, t.pos0);
+              t.hi = static_cast<int>(min(t0 + rows, pos0 + kGTile));
+              t.row0 = r0 + pos0 - t0;
+              t.c0 = min(max(t.lo, p.sink), t.hi);
+              t.c1 = max(t.c0, min(t.hi, max(len - p.window, 0)));
+            }
+          }
+        }
       }
-  }
+      for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        GatherTile u{};
+        u.b = __shfl_sync(0xffffffffu, t.b, src);
+        u.pos0 = __shfl_sync(0xffffffffu, t.pos0, src);
+        u.lo = __shfl_sync(0xffffffffu, t.lo, src);
+        u.hi = __shfl_sync(0xffffffffu, t.hi, src);
+        u.c0 = __shfl_sync(0xffffffffu, t.c0, src);
+        u.c1 = __shfl_sync(0xffffffffu, t.c1, src);
+        u.row0 = __shfl_sync(0xffffffffu, t.row0, src);
+        // the codes of a page a lane
+        const int at = u.pos0 + kPage * lane;
+        const bool coded = lane < kGPages && max(at, u.c0) < min(at + kPage, u.c1);
+        int id = -1;
+        if (coded) id = p.coded_table[static_cast<size_t>(u.b) * p.max_pages + at / kPage];
+        const bool there = coded && id >= 0 && id < p.n_coded;
+        if (coded && !there && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+        u.pages = __ballot_sync(0xffffffffu, there);
+        if (!(ok = slot_free(n))) break;
+        const int st = n % kGStages;
+        if (lane == 0) {
+          tiles[st] = u;
+          mbar_arrive_expect_tx(full + st, __popc(u.pages) * S::kPart);
+        }
+        __syncwarp();
+        if (there)
+          bulk_g2s(smem + S::kRing + (st * kGPages + lane) * S::kPart,
+                   p.coded + (static_cast<int64_t>(id) * p.hkv + h) * F::kInt2Block + kv * S::kPart, S::kPart, full + st);
+        ++n;
+      }
+    }
+    uint32_t k = n > kGStages ? n - kGStages : 0;
+    if (ok && slot_free(n)) {
+      if (n >= kGStages) k = n - kGStages + 1;   // (the slot's last tile has been used)
+      if (lane == 0) {
+        tiles[n % kGStages].stop = 1;
+        mbar_arrive_expect_tx(full + n % kGStages, 0);
+      }
+    }
+    // no copy is in flight when the CTA ends, whatever becomes of the others
+    for (; k < n; ++k) mbar_wait(full + k % kGStages, (k / kGStages) & 1, p.status);
+  } else {
+    // ------------------------------------------------------- codes to rows
+    constexpr uint32_t idesc = tc_idesc_bf16(kGTile, D);
+    constexpr int kAtom = D * 128;   // 64 channels of R's rows
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const bool leader = warp == 0 && tc_elect();
+    const uint32_t r1 = smem_u32(smem), r2 = r1 + S::kPiece;
+    const int64_t stride = static_cast<int64_t>(p.hkv) * D;
+    uint32_t n = 0;
+    for (;; ++n) {
+      const int st = n % kGStages;
+      const bool came = __all_sync(0xffffffffu, mbar_wait(full + st, (n / kGStages) & 1, p.status));
+      if (!came) *abort_flag = 1;
+      const GatherTile t = tiles[st];
+      const bool end = !came || t.stop;
+      const int pos = t.pos0 + row, slot = row / kPage;
+      if (!end) {
+        const uint8_t* blk = smem + S::kRing + (st * kGPages + slot) * S::kPart;
+        if (kv) uncode<D, P, true>(blk, row % kPage, half, lanes + D);
+        else uncode<D, P, false>(blk, row % kPage, half, lanes + D);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc_arrive(empty + st);
+      }
+      if (any_of(end || *abort_flag)) break;   // (all warps together)
+      if (leader) {
+        tc_fence_after();
 #pragma unroll
-  for (int t = 0; t < kPage; ++t)
-    if (t >= c0 && t < c1) out[t * stride] = static_cast<uint16_t>(pack_bf162(acc[t], 0.f));
+        for (int piece = 0; piece < 3; ++piece) {   // y2 R1, y1 R2, y1 R1
+          const uint32_t a = tmem + D + (piece == 0 ? D / 2 : 0), b = piece == 1 ? r2 : r1;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ts(tmem, a + 8 * kk, tc_desc_sw128(b + (kk >> 2) * kAtom + (kk & 3) * 32), idesc, piece != 0 || kk != 0);
+        }
+        tc_commit(done);
+      }
+      __syncwarp();
+      uint16_t* dst = p.out[kv] + ((t.row0 + row) * p.hkv + h) * D + half * (D / 2);
+      if (pos >= t.lo && pos < t.hi && (pos < t.c0 || pos >= t.c1)) {   // in BF16
+        const int id = p.plain_table[static_cast<size_t>(t.b) * p.max_pages + pos / kPage];
+        if (id < 0 || id >= p.n_plain) {
+          if (p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+        } else {
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(
+              p.plain + (static_cast<int64_t>(id) * p.hkv + h) * Fmt<D>::kBf16Block + kv * Fmt<D>::kBf16V);
+#pragma unroll 1
+          for (int j = 0; j < D / 2; j += 16) {
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int c = half * (D / 2) + j + 2 * k;
+              if (kv)
+                x[k] = src[bf16_value_elem(pos % kPage, c)] |
+                       (static_cast<uint32_t>(src[bf16_value_elem(pos % kPage, c + 1)]) << 16);
+              else
+                x[k] = *reinterpret_cast<const uint32_t*>(src + bf16_key_elem(pos % kPage, c));
+            }
+            store32(dst + j, x);
+          }
+        }
+      }
+      __syncwarp();
+      const bool got = __all_sync(0xffffffffu, mbar_wait(done, n & 1, p.status));
+      if (!got) *abort_flag = 1;
+      tc_fence_after();
+      const bool mine = got && pos >= t.c0 && pos < t.c1 && ((t.pages >> slot) & 1u);
+#pragma unroll
+      for (int j = 0; j < D / 2; j += 32) {
+        uint32_t y[32];
+        tc_request32(lanes + half * (D / 2) + j, y);
+        tc_wait_ld(y);
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+          uint32_t x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = pack_bf162(__uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
+          if (mine) store32(dst + j + k, x);
+        }
+      }
+      tc_fence_before();
+    }
+    if (*abort_flag && leader) {   // MMAs in flight finish before the CTA ends
+      tc_commit(done + 1);
+      mbar_wait(done + 1, 0, p.status);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tc_dealloc(tmem, 2 * D);
+  }
 }
 
 template <int D, int P>
 oscar_status launch_gather(const GatherParams& p, cudaStream_t st) {
+  using S = GatherSmem<D, P>;
+  const auto kernel = gather_kernel<D, P>;
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), S::kAlloc)) return OSCAR_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * static_cast<unsigned>(p.pages_per_seq),
-                     static_cast<unsigned>(2 * p.hkv));
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.hkv * p.ctas_per_r));
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = S::kAlloc;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_kernel<D, P>, p) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
 }
 
 }  // namespace oscar
@@ -140,13 +422,17 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15))
     return OSCAR_ERR_INVALID_ARG;
   if (total_rows > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;   // row_starts are int32
+  // tiles that max_rows consecutive positions can touch
   const int64_t pages = (static_cast<int64_t>(max_rows) + kPage - 2) / kPage + 1;
+  const int64_t tiles = (pages + kGPages - 1) / kGPages;
   if (pages * batch > 0x7fffffff || desc->num_kv_heads > 32767) return OSCAR_ERR_UNSUPPORTED;
   GatherParams p{};
   p.hkv = desc->num_kv_heads;
   p.max_pages = desc->max_pages_per_seq;
   p.batch = batch;
-  p.pages_per_seq = static_cast<int>(pages);
+  p.tiles_per_seq = static_cast<int>(tiles);
+  // two CTAs an SM, and no more for a rotation than there are tiles
+  p.ctas_per_r = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(oscar_host::sm_count() / p.hkv, tiles * batch)));
   p.max_rows = max_rows;
   p.sink = desc->sink;
   p.window = desc->window;
