@@ -27,6 +27,7 @@ namespace oscar {
 
 struct GatherParams {
   int hkv, max_pages, batch, tiles_per_seq, max_rows, sink, window, ctas_per_r;
+  bool whole;        // outputs start at a multiple of 32 bytes
   int64_t n_coded, n_plain, total_rows;
   const uint8_t* coded;
   const uint8_t* plain;
@@ -72,13 +73,14 @@ struct GatherSmem {
 };
 
 // Two codes in the low bits of the halves of x, times s plus z, as two bf16 pieces each.
-__device__ __forceinline__ void split_pair(uint32_t x, float s, float z, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split_pair(uint32_t x, uint64_t s, uint64_t z, uint32_t& hi, uint32_t& lo) {
   constexpr float kMagic = 8388608.f;   // 2^23: its low bits are the code
-  const float c0 = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7610)) - kMagic;
-  const float c1 = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7632)) - kMagic;
-  const float y0 = fmaf(c0, s, z), y1 = fmaf(c1, s, z);
-  hi = pack_bf162(y0, y1);
-  lo = pack_bf162(y0 - bf16_lo_value(hi), y1 - bf16_hi_value(hi));
+  const uint64_t c = add2(two(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7610)),
+                              __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7632))), two(-kMagic, -kMagic));
+  const uint64_t y = fma2(c, s, z);
+  hi = pack_bf162(first(y), second(y));
+  const uint64_t rest = fma2(two(bf16_lo_value(hi), bf16_hi_value(hi)), two(-1.f, -1.f), y);
+  lo = pack_bf162(first(rest), second(rest));
 }
 
 // A thread's channels [half * D/2, ...) of the coded token t of the page at blk (keys' or values' part), to its
@@ -136,7 +138,7 @@ __device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, uint
         for (int q = 0; q < 4; ++q) {
           uint32_t c = (x[0][q][m] >> (4 * h + 2 * i)) & 0x00030003u;
           if constexpr (P == 2) c = c * 4 + ((x[P - 1][q][m] >> (4 * h + 2 * i)) & 0x00030003u);
-          split_pair(c, s, z, hi[4 * h + q], lo[4 * h + q]);
+          split_pair(c, two(s, s), two(z, z), hi[4 * h + q], lo[4 * h + q]);
         }
       tc_st8(a + 16 * g + 8 * i, hi);
       tc_st8(a + D / 2 + 16 * g + 8 * i, lo);
@@ -154,10 +156,57 @@ __device__ __forceinline__ bool any_of(bool x) {
   return y != 0;
 }
 
-// 32 bytes to a 16-byte aligned address.
-__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&x)[8]) {
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+// 32 bytes, at once where every row starts at a multiple of 32.
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&x)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+// A tile's BF16 tokens, a warp each, four channels a lane (two for d = 64); kFlight tokens at once.
+template <int D, bool kValue>
+__device__ __forceinline__ void plain_tokens(const GatherParams& p, const GatherTile& t, int h, int warp, int lane) {
+  constexpr int kOwn = D / 32, kFlight = 4;
+  const int before = t.c0 - t.lo, n = before + t.hi - t.c1;
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += kGWarps * kFlight) {
+    int pos[kFlight], id[kFlight];
+    uint32_t x[kFlight][kOwn / 2];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int i = i0 + k * kGWarps;
+      pos[k] = i < before ? t.lo + i : t.c1 + i - before;
+      id[k] = i < n ? p.plain_table[static_cast<size_t>(t.b) * p.max_pages + pos[k] / kPage] : -1;
+      if (i < n && (id[k] < 0 || id[k] >= p.n_plain)) {
+        if (p.status && lane == 0) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+        id[k] = -1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(
+          p.plain + (static_cast<int64_t>(max(id[k], 0)) * p.hkv + h) * Fmt<D>::kBf16Block + (kValue ? Fmt<D>::kBf16V : 0));
+#pragma unroll
+      for (int c = 0; c < kOwn / 2; ++c) {
+        const int j = kOwn * lane + 2 * c, tk = pos[k] % kPage;
+        if (id[k] < 0) continue;
+        x[k][c] = kValue ? src[bf16_value_elem(tk, j)] | (static_cast<uint32_t>(src[bf16_value_elem(tk, j + 1)]) << 16)
+                         : *reinterpret_cast<const uint32_t*>(src + bf16_key_elem(tk, j));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (id[k] < 0) continue;
+      uint16_t* dst = p.out[kValue] + ((t.row0 + pos[k] - t.pos0) * p.hkv + h) * D + kOwn * lane;
+      if constexpr (kOwn == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(x[k][0], x[k][1]);
+      else *reinterpret_cast<uint32_t*>(dst) = x[k][0];
+    }
+  }
 }
 
 template <int D, int P>
@@ -330,30 +379,11 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
       }
       __syncwarp();
       uint16_t* dst = p.out[kv] + ((t.row0 + row) * p.hkv + h) * D + half * (D / 2);
-      if (pos >= t.lo && pos < t.hi && (pos < t.c0 || pos >= t.c1)) {   // in BF16
-        const int id = p.plain_table[static_cast<size_t>(t.b) * p.max_pages + pos / kPage];
-        if (id < 0 || id >= p.n_plain) {
-          if (p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-        } else {
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(
-              p.plain + (static_cast<int64_t>(id) * p.hkv + h) * Fmt<D>::kBf16Block + kv * Fmt<D>::kBf16V);
-#pragma unroll 1
-          for (int j = 0; j < D / 2; j += 16) {
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int c = half * (D / 2) + j + 2 * k;
-              if (kv)
-                x[k] = src[bf16_value_elem(pos % kPage, c)] |
-                       (static_cast<uint32_t>(src[bf16_value_elem(pos % kPage, c + 1)]) << 16);
-              else
-                x[k] = *reinterpret_cast<const uint32_t*>(src + bf16_key_elem(pos % kPage, c));
-            }
-            store32(dst + j, x);
-          }
-        }
+      if (t.c0 > t.lo || t.c1 < t.hi) {
+        if (kv) plain_tokens<D, true>(p, t, h, warp, lane);
+        else plain_tokens<D, false>(p, t, h, warp, lane);
+        __syncwarp();
       }
-      __syncwarp();
       const bool got = __all_sync(0xffffffffu, mbar_wait(done, n & 1, p.status));
       if (!got) *abort_flag = 1;
       tc_fence_after();
@@ -368,7 +398,7 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
           uint32_t x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = pack_bf162(__uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
-          if (mine) store32(dst + j + k, x);
+          if (mine) store32(dst + j + k, x, p.whole);
         }
       }
       tc_fence_before();
@@ -447,6 +477,7 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
   p.r[1] = desc->r_v;
   p.out[0] = static_cast<uint16_t*>(k_out);
   p.out[1] = static_cast<uint16_t*>(v_out);
+  p.whole = !((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31);
   p.seq_lens = seq_lens;
   p.first = first;
   p.row_starts = row_starts;
