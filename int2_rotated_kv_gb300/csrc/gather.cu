@@ -10,12 +10,15 @@
 //   x = y2 R1^T + y1 R2^T + y1 R1^T,   fp32 accumulation in tensor memory.
 // M = 128 tokens (8 pages of one sequence), N = K = d; R's pieces lie in shared memory (rows of R
 // are the K-major rows of operand B as they are), y's pieces in tensor memory, where a thread writes
-// its own token's row.  A CTA keeps the R of one (KV head, keys or values) and walks over tiles of
-// tokens; two CTAs an SM, so that one's MMAs and stores run under the other's arithmetic.
-//   warps 0-7  a token and half of its channels a thread: codes to y1, y2; then the product's row to
-//              bf16 and out.  One lane of warp 0 issues the 3 d/16 MMAs of a tile.
-//   warp 8     tiles ahead: finds the next tiles that hold rows (32 at a look), and copies the codes
-//              of their pages into a ring of stages (bulk copies, one a page).
+// its own token's row.  A CTA, one an SM, keeps the R of one (KV head, keys or values) and walks over
+// tiles of tokens, which pass through its roles:
+//   warp 24       finds the next tiles that hold rows (32 at a look), and copies the codes of their
+//                 pages into a ring of stages (bulk copies, one a page);
+//   warps 8-15,   codes to y1, y2 of even and odd tiles (each with its own columns of tensor memory),
+//   16-23         a token and half of its channels a thread;
+//   warp 25       the 3 d/16 MMAs of a tile, into one of two accumulators;
+//   warps 0-3,    the rows of even and odd tiles to bf16 and out, a token a thread, and the tile's BF16
+//   4-7           tokens.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 #include <algorithm>
 
@@ -43,9 +46,9 @@ struct GatherParams {
 
 constexpr int kGTile = 128;                 // tokens of a tile
 constexpr int kGPages = kGTile / kPage;
-constexpr int kGStages = 4;
-constexpr int kGWarps = 8;                  // that compute
-constexpr int kGThreads = 32 * (kGWarps + 1);
+constexpr int kGStages = 8;
+constexpr int kGWarps = 8;                  // of a role that computes
+constexpr int kGThreads = 32 * (3 * kGWarps + 2);
 
 // A tile as the computing warps need it: positions of its tokens are pos0 + row.
 struct GatherTile {
@@ -55,6 +58,7 @@ struct GatherTile {
   int b;
   uint32_t pages;    // bit per page: its codes are there
   int stop;          // 1: there is no tile
+  int plain[kGPages];   // id of a page with BF16 tokens, -1: refused
 };
 
 template <int D, int P>
@@ -66,7 +70,7 @@ struct GatherSmem {
   static constexpr int kRing = 2 * kPiece;
   static constexpr int kTiles = kRing + kGStages * kGPages * kPart;
   static constexpr int kBars = kTiles + kGStages * static_cast<int>(sizeof(GatherTile));
-  static constexpr int kMisc = kBars + (2 * kGStages + 2) * 8;
+  static constexpr int kMisc = kBars + (2 * kGStages + 7) * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;           // the base is rounded up to 1024 bytes
   static_assert(kTiles % 16 == 0 && sizeof(GatherTile) % 8 == 0, "alignment");
@@ -146,16 +150,6 @@ __device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, uint
   }
 }
 
-// Whether any of the computing threads says so; a barrier among them.
-__device__ __forceinline__ bool any_of(bool x) {
-  uint32_t y;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.or.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(y)
-               : "r"(static_cast<uint32_t>(x)), "n"(32 * kGWarps)
-               : "memory");
-  return y != 0;
-}
-
 // 32 bytes, at once where every row starts at a multiple of 32.
 __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&x)[8], bool whole) {
   if (whole) {
@@ -168,57 +162,54 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&x)[8], b
   }
 }
 
-// A tile's BF16 tokens, a warp each, four channels a lane (two for d = 64); kFlight tokens at once.
+// The BF16 tokens of page slot i of a tile, by a warp: 16 bytes a lane are channels 16 m + 2 tig, + 1, + 8, + 9 of two
+// tokens (keys), or the same transposed in 8x8 blocks (values).
 template <int D, bool kValue>
-__device__ __forceinline__ void plain_tokens(const GatherParams& p, const GatherTile& t, int h, int warp, int lane) {
-  constexpr int kOwn = D / 32, kFlight = 4;
-  const int before = t.c0 - t.lo, n = before + t.hi - t.c1;
-#pragma unroll 1
-  for (int i0 = warp; i0 < n; i0 += kGWarps * kFlight) {
-    int pos[kFlight], id[kFlight];
-    uint32_t x[kFlight][kOwn / 2];
+__device__ __forceinline__ void plain_page(const GatherParams& p, const GatherTile& t, int h, int i, int lane) {
+  const int gid = lane >> 2, tig = lane & 3, id = t.plain[i];
+  if (id < 0) return;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      p.plain + (static_cast<int64_t>(id) * p.hkv + h) * Fmt<D>::kBf16Block + (kValue ? Fmt<D>::kBf16V : 0)) + lane;
+  uint4 x[D / 16];
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const int i = i0 + k * kGWarps;
-      pos[k] = i < before ? t.lo + i : t.c1 + i - before;
-      id[k] = i < n ? p.plain_table[static_cast<size_t>(t.b) * p.max_pages + pos[k] / kPage] : -1;
-      if (i < n && (id[k] < 0 || id[k] >= p.n_plain)) {
-        if (p.status && lane == 0) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-        id[k] = -1;
-      }
+  for (int m = 0; m < D / 16; ++m) x[m] = src[32 * m];
+  if constexpr (kValue) {
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m) {   // then as keys: tokens gid and gid + 8, channels 2 tig and 2 tig + 8
+      const uint32_t up = movmatrix_trans(x[m].y), down = movmatrix_trans(x[m].z);
+      x[m].x = movmatrix_trans(x[m].x);
+      x[m].w = movmatrix_trans(x[m].w);
+      x[m].y = down;
+      x[m].z = up;
     }
+  }
+  uint16_t* dst = p.out[kValue] + (t.row0 * p.hkv + h) * D + 2 * tig;
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(
-          p.plain + (static_cast<int64_t>(max(id[k], 0)) * p.hkv + h) * Fmt<D>::kBf16Block + (kValue ? Fmt<D>::kBf16V : 0));
+  for (int th = 0; th < 2; ++th) {
+    const int row = kPage * i + 8 * th + gid, pos = t.pos0 + row;
+    if (pos < t.lo || pos >= t.hi || (pos >= t.c0 && pos < t.c1)) continue;
+    uint16_t* out = dst + static_cast<int64_t>(row) * p.hkv * D;
 #pragma unroll
-      for (int c = 0; c < kOwn / 2; ++c) {
-        const int j = kOwn * lane + 2 * c, tk = pos[k] % kPage;
-        if (id[k] < 0) continue;
-        x[k][c] = kValue ? src[bf16_value_elem(tk, j)] | (static_cast<uint32_t>(src[bf16_value_elem(tk, j + 1)]) << 16)
-                         : *reinterpret_cast<const uint32_t*>(src + bf16_key_elem(tk, j));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      if (id[k] < 0) continue;
-      uint16_t* dst = p.out[kValue] + ((t.row0 + pos[k] - t.pos0) * p.hkv + h) * D + kOwn * lane;
-      if constexpr (kOwn == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(x[k][0], x[k][1]);
-      else *reinterpret_cast<uint32_t*>(dst) = x[k][0];
+    for (int m = 0; m < D / 16; ++m) {
+      *reinterpret_cast<uint32_t*>(out + 16 * m) = th ? x[m].y : x[m].x;
+      *reinterpret_cast<uint32_t*>(out + 16 * m + 8) = th ? x[m].w : x[m].z;
     }
   }
 }
 
 template <int D, int P>
-__global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_constant__ GatherParams p) {
+__global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_constant__ GatherParams p) {
   using S = GatherSmem<D, P>;
   using F = Fmt<D, P>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   GatherTile* tiles = reinterpret_cast<GatherTile*>(smem + S::kTiles);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  uint64_t* empty = full + kGStages;
-  uint64_t* done = empty + kGStages;       // the MMAs of a tile; then those in flight after a give-up
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);   // a tile's codes are there
+  uint64_t* empty = full + kGStages;       // and may be overwritten
+  uint64_t* yfull = empty + kGStages;      // y of an even (odd) tile is there
+  uint64_t* done = yfull + 2;              // its MMAs are done
+  uint64_t* xempty = done + 2;             // its product has been read
+  uint64_t* last = xempty + 2;             // MMAs in flight after a give-up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -228,14 +219,18 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
   if (tid == 0) {
     for (int i = 0; i < kGStages; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, kGWarps);
+      mbar_init(empty + i, kGWarps + kGWarps / 2);
     }
-    mbar_init(done, 1);
-    mbar_init(done + 1, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(yfull + i, kGWarps);
+      mbar_init(done + i, 1);
+      mbar_init(xempty + i, kGWarps / 2);
+    }
+    mbar_init(last, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tc_alloc(tmem_slot, 2 * D);
+  if (warp == 0) tc_alloc(tmem_slot, 4 * D);
   // R as two bf16 pieces
   const float* r = p.r[kv] + static_cast<size_t>(h) * D * D;
   for (int i = tid; i < D * D / 8; i += kGThreads) {
@@ -257,19 +252,26 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot;   // products of even and odd tiles (d columns each), then their y
   pdl_wait();
   pdl_trigger();
 
-  if (warp == kGWarps) {
+  // A wait of a warp together; false: give up.
+  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, p.status) && !*abort_flag);
+    if (!ok) *abort_flag = 1;
+    return ok;
+  };
+  auto arrive = [&](uint64_t* b) {
+    __syncwarp();
+    if (lane == 0) tc_arrive(b);
+  };
+
+  if (warp == 3 * kGWarps) {
     // ------------------------------------------------------------- tiles ahead
     uint32_t n = 0;   // tiles published
     bool ok = true;
     const int64_t total = static_cast<int64_t>(p.batch) * p.tiles_per_seq;
-    auto slot_free = [&](uint32_t k) {
-      const bool got = mbar_wait(empty + k % kGStages, ((k / kGStages) & 1) ^ 1, p.status);
-      return __all_sync(0xffffffffu, got && !*abort_flag);
-    };
     for (int64_t base = number; base < total && ok; base += static_cast<int64_t>(32) * p.ctas_per_r) {
       // a tile a lane
       const int64_t tile = base + static_cast<int64_t>(lane) * p.ctas_per_r;
@@ -298,8 +300,11 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
           }
         }
       }
-      for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok; todo &= todo - 1) {
-        const int src = __ffs(todo) - 1;
+      for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok;) {
+        // the next four of them, eight lanes each (one at a time, the look-ups of page ids bound the walk)
+        uint32_t left = todo;
+        for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
+        const int src = left ? __ffs(left) - 1 : 0;
         GatherTile u{};
         u.b = __shfl_sync(0xffffffffu, t.b, src);
         u.pos0 = __shfl_sync(0xffffffffu, t.pos0, src);
@@ -308,104 +313,136 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
         u.c0 = __shfl_sync(0xffffffffu, t.c0, src);
         u.c1 = __shfl_sync(0xffffffffu, t.c1, src);
         u.row0 = __shfl_sync(0xffffffffu, t.row0, src);
-        // the codes of a page a lane
-        const int at = u.pos0 + kPage * lane;
-        const bool coded = lane < kGPages && max(at, u.c0) < min(at + kPage, u.c1);
-        int id = -1;
-        if (coded) id = p.coded_table[static_cast<size_t>(u.b) * p.max_pages + at / kPage];
-        const bool there = coded && id >= 0 && id < p.n_coded;
-        if (coded && !there && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-        u.pages = __ballot_sync(0xffffffffu, there);
-        if (!(ok = slot_free(n))) break;
-        const int st = n % kGStages;
-        if (lane == 0) {
-          tiles[st] = u;
-          mbar_arrive_expect_tx(full + st, __popc(u.pages) * S::kPart);
+        // a page a lane: its codes, and the id of its BF16 tokens
+        const int pg = lane & 7, at = u.pos0 + kPage * pg;
+        const bool coded = left && max(at, u.c0) < min(at + kPage, u.c1);
+        const bool plain = left && (max(at, u.lo) < min(at + kPage, u.c0) || max(at, u.c1) < min(at + kPage, u.hi));
+        const size_t entry = static_cast<size_t>(u.b) * p.max_pages + at / kPage;
+        int id = -1, id16 = -1;
+        if (coded) id = p.coded_table[entry];
+        if (plain) id16 = p.plain_table[entry];
+        const bool there = coded && id >= 0 && id < p.n_coded, there16 = plain && id16 >= 0 && id16 < p.n_plain;
+        if (((coded && !there) || (plain && !there16)) && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+        const uint32_t pages = __ballot_sync(0xffffffffu, there);
+        for (int g = 0; g < 4 && todo; ++g, todo &= todo - 1, ++n) {
+          const int st = n % kGStages;
+          if (!(ok = wait(empty + st, (n / kGStages) + 1))) break;
+          if (lane == 8 * g) {
+            u.pages = (pages >> (8 * g)) & 0xffu;
+            tiles[st] = u;
+          }
+          __syncwarp();
+          if (lane >> 3 == g) tiles[st].plain[pg] = there16 ? id16 : -1;
+          __syncwarp();
+          if (lane == 8 * g) mbar_arrive_expect_tx(full + st, __popc(u.pages) * S::kPart);
+          __syncwarp();
+          if (lane >> 3 == g && there)
+            bulk_g2s(smem + S::kRing + (st * kGPages + pg) * S::kPart,
+                     p.coded + (static_cast<int64_t>(id) * p.hkv + h) * F::kInt2Block + kv * S::kPart, S::kPart, full + st);
         }
-        __syncwarp();
-        if (there)
-          bulk_g2s(smem + S::kRing + (st * kGPages + lane) * S::kPart,
-                   p.coded + (static_cast<int64_t>(id) * p.hkv + h) * F::kInt2Block + kv * S::kPart, S::kPart, full + st);
-        ++n;
       }
     }
+    // the end, for the warps of even and of odd tiles
     uint32_t k = n > kGStages ? n - kGStages : 0;
-    if (ok && slot_free(n)) {
-      if (n >= kGStages) k = n - kGStages + 1;   // (the slot's last tile has been used)
+    for (int e = 0; e < 2 && ok; ++e) {
+      const uint32_t m = n + e;
+      if (!(ok = wait(empty + m % kGStages, (m / kGStages) + 1))) break;
+      if (m >= kGStages) k = m - kGStages + 1;   // (the slot's last tile has been used)
       if (lane == 0) {
-        tiles[n % kGStages].stop = 1;
-        mbar_arrive_expect_tx(full + n % kGStages, 0);
+        tiles[m % kGStages].stop = 1;
+        mbar_arrive_expect_tx(full + m % kGStages, 0);
       }
+      __syncwarp();
     }
     // no copy is in flight when the CTA ends, whatever becomes of the others
     for (; k < n; ++k) mbar_wait(full + k % kGStages, (k / kGStages) & 1, p.status);
-  } else {
-    // ------------------------------------------------------- codes to rows
+  } else if (warp == 3 * kGWarps + 1) {
+    // ------------------------------------------------------------------ MMAs
     constexpr uint32_t idesc = tc_idesc_bf16(kGTile, D);
     constexpr int kAtom = D * 128;   // 64 channels of R's rows
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const bool leader = warp == 0 && tc_elect();
+    const bool leader = tc_elect();
     const uint32_t r1 = smem_u32(smem), r2 = r1 + S::kPiece;
-    const int64_t stride = static_cast<int64_t>(p.hkv) * D;
-    uint32_t n = 0;
-    for (;; ++n) {
-      const int st = n % kGStages;
-      const bool came = __all_sync(0xffffffffu, mbar_wait(full + st, (n / kGStages) & 1, p.status));
-      if (!came) *abort_flag = 1;
-      const GatherTile t = tiles[st];
-      const bool end = !came || t.stop;
-      const int pos = t.pos0 + row, slot = row / kPage;
-      if (!end) {
-        const uint8_t* blk = smem + S::kRing + (st * kGPages + slot) * S::kPart;
-        if (kv) uncode<D, P, true>(blk, row % kPage, half, lanes + D);
-        else uncode<D, P, false>(blk, row % kPage, half, lanes + D);
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc_arrive(empty + st);
-      }
-      if (any_of(end || *abort_flag)) break;   // (all warps together)
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t e = n & 1;
+      if (!(ok = wait(full + n % kGStages, n / kGStages))) break;
+      if (tiles[n % kGStages].stop) break;
+      if (!(ok = wait(yfull + e, n >> 1) && wait(xempty + e, (n >> 1) + 1))) break;
       if (leader) {
         tc_fence_after();
+        const uint32_t x = tmem + e * D, y = tmem + 2 * D + e * D;
 #pragma unroll
         for (int piece = 0; piece < 3; ++piece) {   // y2 R1, y1 R2, y1 R1
-          const uint32_t a = tmem + D + (piece == 0 ? D / 2 : 0), b = piece == 1 ? r2 : r1;
+          const uint32_t a = y + (piece == 0 ? D / 2 : 0), b = piece == 1 ? r2 : r1;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ts(tmem, a + 8 * kk, tc_desc_sw128(b + (kk >> 2) * kAtom + (kk & 3) * 32), idesc, piece != 0 || kk != 0);
+            tc_mma_ts(x, a + 8 * kk, tc_desc_sw128(b + (kk >> 2) * kAtom + (kk & 3) * 32), idesc, piece != 0 || kk != 0);
         }
-        tc_commit(done);
+        tc_commit(done + e);
       }
       __syncwarp();
-      uint16_t* dst = p.out[kv] + ((t.row0 + row) * p.hkv + h) * D + half * (D / 2);
-      if (t.c0 > t.lo || t.c1 < t.hi) {
-        if (kv) plain_tokens<D, true>(p, t, h, warp, lane);
-        else plain_tokens<D, false>(p, t, h, warp, lane);
-        __syncwarp();
-      }
-      const bool got = __all_sync(0xffffffffu, mbar_wait(done, n & 1, p.status));
-      if (!got) *abort_flag = 1;
+    }
+    if (!ok && leader) {   // MMAs in flight finish before the CTA ends
+      tc_commit(last);
+      mbar_wait(last, 0, p.status);
+    }
+  } else if (warp >= kGWarps) {
+    // ------------------------------------------------------------- codes to y
+    const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1, odd = (warp - kGWarps) / kGWarps;
+    const uint32_t y = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 2 * D + odd * D;
+    for (uint32_t n = odd;; n += 2) {
+      const int st = n % kGStages;
+      if (!wait(full + st, n / kGStages) || tiles[st].stop) break;
+      if (!wait(done + odd, (n >> 1) + 1)) break;   // y of the tile before has been used
       tc_fence_after();
-      const bool mine = got && pos >= t.c0 && pos < t.c1 && ((t.pages >> slot) & 1u);
+      const uint8_t* blk = smem + S::kRing + (st * kGPages + row / kPage) * S::kPart;
+      if (kv) uncode<D, P, true>(blk, row % kPage, half, y);
+      else uncode<D, P, false>(blk, row % kPage, half, y);
+      tc_wait_st();
+      tc_fence_before();
+      arrive(yfull + odd);
+      if (lane == 0) tc_arrive(empty + st);
+    }
+  } else {
+    // ----------------------------------------------------------- rows to bf16
+    const int row = 32 * (warp & 3) + lane, odd = warp >> 2;
+    const uint32_t x = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + odd * D;
+    for (uint32_t n = odd;; n += 2) {
+      const int st = n % kGStages;
+      if (!wait(full + st, n / kGStages)) break;
+      const GatherTile& t = tiles[st];
+      if (t.stop || !wait(done + odd, n >> 1)) break;
+      tc_fence_after();
+      const int pos = t.pos0 + row;
+      uint16_t* dst = p.out[kv] + ((t.row0 + row) * p.hkv + h) * D;
+      const bool mine = pos >= t.c0 && pos < t.c1 && ((t.pages >> (row / kPage)) & 1u);
 #pragma unroll
-      for (int j = 0; j < D / 2; j += 32) {
+      for (int j = 0; j < D; j += 32) {
         uint32_t y[32];
-        tc_request32(lanes + half * (D / 2) + j, y);
+        tc_request32(x + j, y);
         tc_wait_ld(y);
+        if (j + 32 == D) {
+          tc_fence_before();
+          arrive(xempty + odd);
+        }
 #pragma unroll
         for (int k = 0; k < 32; k += 16) {
-          uint32_t x[8];
+          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = pack_bf162(__uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
-          if (mine) store32(dst + j + k, x, p.whole);
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf162(__uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
+          if (mine) store32(dst + j + k, w, p.whole);
         }
       }
-      tc_fence_before();
-    }
-    if (*abort_flag && leader) {   // MMAs in flight finish before the CTA ends
-      tc_commit(done + 1);
-      mbar_wait(done + 1, 0, p.status);
+      __syncwarp();
+      if (t.c0 > t.lo || t.c1 < t.hi) {
+#pragma unroll 1
+        for (int i = warp & 3; i < kGPages; i += kGWarps / 2) {
+          if (kv) plain_page<D, true>(p, t, h, i, lane);
+          else plain_page<D, false>(p, t, h, i, lane);
+          __syncwarp();
+        }
+      }
+      arrive(empty + st);
     }
   }
   __syncwarp();
@@ -413,7 +450,7 @@ __global__ void __launch_bounds__(kGThreads, 2) gather_kernel(const __grid_const
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tc_dealloc(tmem, 2 * D);
+    tc_dealloc(tmem, 4 * D);
   }
 }
 
@@ -461,8 +498,8 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
   p.max_pages = desc->max_pages_per_seq;
   p.batch = batch;
   p.tiles_per_seq = static_cast<int>(tiles);
-  // two CTAs an SM, and no more for a rotation than there are tiles
-  p.ctas_per_r = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(oscar_host::sm_count() / p.hkv, tiles * batch)));
+  // a CTA an SM, and no more for a rotation than there are tiles
+  p.ctas_per_r = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(oscar_host::sm_count() / (2 * p.hkv), tiles * batch)));
   p.max_rows = max_rows;
   p.sink = desc->sink;
   p.window = desc->window;
