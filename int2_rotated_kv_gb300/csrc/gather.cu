@@ -70,7 +70,8 @@ struct GatherSmem {
   static constexpr int kRing = 2 * kPiece;
   static constexpr int kTiles = kRing + kGStages * kGPages * kPart;
   static constexpr int kBars = kTiles + kGStages * static_cast<int>(sizeof(GatherTile));
-  static constexpr int kMisc = kBars + (2 * kGStages + 7) * 8;
+  static constexpr int kSteps = D / 64;                  // a tile's channels pass from role to role in so many steps
+  static constexpr int kMisc = kBars + (2 * kGStages + 4 * kSteps + 3) * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;           // the base is rounded up to 1024 bytes
   static_assert(kTiles % 16 == 0 && sizeof(GatherTile) % 8 == 0, "alignment");
@@ -87,25 +88,28 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint64_t s, uint64_t z, u
   lo = pack_bf162(first(rest), second(rest));
 }
 
-// A thread's channels [half * D/2, ...) of the coded token t of the page at blk (keys' or values' part), to its
-// row of tensor memory: y1 from column a on, y2 from a + D/2 on, two channels a column.
+// The words of codes that a thread needs for its half of a token's channels, of the page at blk (keys' or
+// values' part): x[plane][q][m] has, of group half * kOwn + m, channels 2q, 2q + 1 in its two halves (and 8, 16, 24
+// further: bits 4h + 2i of the lower byte for channel 2q + 8h + 16i).
 template <int D, int P, bool kValue>
-__device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, uint32_t a) {
+__device__ __forceinline__ void load_codes(const uint8_t* blk, int t, int half, uint32_t (&x)[P][4][D / 64]) {
   using F = Fmt<D, P>;
-  constexpr int kOwn = F::kWords / 2;   // groups of 32 channels a thread has
+  constexpr int kOwn = D / 64;
   const int th = t >> 3;
-  // words of a group: keys have channels 2q, 2q + 1 (and 8, 16, 24 further) of tokens t, t ^ 8 in word q, values
-  // channel gid of tokens t, t ^ 1, t ^ 8, t ^ 9 in word gid
-  uint32_t x[P][4][kOwn];
+  // in memory, a word holds channels 2q, 2q + 1 of tokens t, t ^ 8 (keys: its bytes th and 2 + th are this
+  // token's), or one channel of tokens t, t ^ 1, t ^ 8, t ^ 9 (values: two words' byte 2 (t & 1) + th)
+  const uint32_t sel = kValue ? 0x0400u + (2 * (t & 1) + th) * 0x0101u : 0x0200u + th * 0x0101u;
+  // eight tokens' keys lie 64 bytes apart: each two of them begin at another q, for the banks
+  const int turn = kValue ? 0 : (t >> 1) & 3;
 #pragma unroll
-  for (int pl = 0; pl < P; ++pl)
+  for (int pl = 0; pl < P; ++pl) {
+    const uint8_t* plane = blk + pl * F::kPlane + 4 * half * kOwn;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint8_t* plane = blk + pl * F::kPlane + 4 * half * kOwn;
-      uint32_t w[2][kOwn];
+      uint32_t w[2][kOwn] = {};
 #pragma unroll
       for (int e = 0; e < (kValue ? 2 : 1); ++e) {
-        const int lane = kValue ? 4 * (2 * q + e) + ((t >> 1) & 3) : 4 * (t & 7) + q;
+        const int lane = kValue ? 4 * (2 * q + e) + ((t >> 1) & 3) : 4 * (t & 7) + ((q + turn) & 3);
         if constexpr (kOwn == 2) {
           const uint2 u = *reinterpret_cast<const uint2*>(plane + 4 * lane * F::kWords);
           w[e][0] = u.x;
@@ -114,39 +118,53 @@ __device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, uint
           w[e][0] = *reinterpret_cast<const uint32_t*>(plane + 4 * lane * F::kWords);
         }
       }
-      // the token's byte of an even channel in the lower half, of the odd one in the upper half
-      const uint32_t sel = kValue ? 0x0400u + (2 * (t & 1) + th) * 0x0101u : 0x0200u + th * 0x0101u;
 #pragma unroll
-      for (int m = 0; m < kOwn; ++m) x[pl][q][m] = __byte_perm(w[0][m], kValue ? w[1][m] : 0u, sel);
+      for (int m = 0; m < kOwn; ++m) x[pl][q][m] = __byte_perm(w[0][m], w[1][m], sel);
     }
+    if constexpr (!kValue) {   // back in order
 #pragma unroll
-  for (int m = 0; m < kOwn; ++m) {
-    const int g = half * kOwn + m;
-    float s, z;
-    if constexpr (kValue) {
-      const __half* vs = reinterpret_cast<const __half*>(blk + F::kVs - F::kVc);
-      const int at = vsz_index<D>(t, g);
-      s = __half2float(vs[at]);
-      z = __half2float(vs[(F::kVz - F::kVs) / 2 + at]);
-    } else {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(blk + F::kKsz)[t * F::kNG + g];
-      s = half_lo(w);
-      z = half_hi(w);
+      for (int m = 0; m < kOwn; ++m) {
+        uint32_t y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = turn & 1 ? x[pl][(q + 3) & 3][m] : x[pl][q][m];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[pl][q][m] = turn & 2 ? y[(q + 2) & 3] : y[q];
+      }
     }
+  }
+}
+
+// Group half * kOwn + m of the token's channels to its row of tensor memory: y1 from column a on, y2 from a + D/2 on,
+// two channels a column.
+template <int D, int P, bool kValue>
+__device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, int m, const uint32_t (&x)[P][4][D / 64],
+                                       uint32_t a) {
+  using F = Fmt<D, P>;
+  const int g = half * (D / 64) + m;
+  float s, z;
+  if constexpr (kValue) {
+    const __half* vs = reinterpret_cast<const __half*>(blk + F::kVs - F::kVc);
+    const int at = vsz_index<D>(t, g);
+    s = __half2float(vs[at]);
+    z = __half2float(vs[(F::kVz - F::kVs) / 2 + at]);
+  } else {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(blk + F::kKsz)[t * F::kNG + g];
+    s = half_lo(w);
+    z = half_hi(w);
+  }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t hi[8], lo[8];
+  for (int i = 0; i < 2; ++i) {
+    uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t c = (x[0][q][m] >> (4 * h + 2 * i)) & 0x00030003u;
-          if constexpr (P == 2) c = c * 4 + ((x[P - 1][q][m] >> (4 * h + 2 * i)) & 0x00030003u);
-          split_pair(c, two(s, s), two(z, z), hi[4 * h + q], lo[4 * h + q]);
-        }
-      tc_st8(a + 16 * g + 8 * i, hi);
-      tc_st8(a + D / 2 + 16 * g + 8 * i, lo);
-    }
+      for (int q = 0; q < 4; ++q) {
+        uint32_t c = (x[0][q][m] >> (4 * h + 2 * i)) & 0x00030003u;
+        if constexpr (P == 2) c = c * 4 + ((x[P - 1][q][m] >> (4 * h + 2 * i)) & 0x00030003u);
+        split_pair(c, two(s, s), two(z, z), hi[4 * h + q], lo[4 * h + q]);
+      }
+    tc_st8(a + 16 * g + 8 * i, hi);
+    tc_st8(a + D / 2 + 16 * g + 8 * i, lo);
   }
 }
 
@@ -197,6 +215,20 @@ __device__ __forceinline__ void plain_page(const GatherParams& p, const GatherTi
   }
 }
 
+// The rest of a wait that did not end at once: false when it takes too long, or the CTA has given up.
+static __device__ __noinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > 2000000000ull) {
+      *abort_flag = 1;
+      if (status) atomicOr(status, OSCAR_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 template <int D, int P>
 __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_constant__ GatherParams p) {
   using S = GatherSmem<D, P>;
@@ -206,9 +238,10 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
   GatherTile* tiles = reinterpret_cast<GatherTile*>(smem + S::kTiles);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);   // a tile's codes are there
   uint64_t* empty = full + kGStages;       // and may be overwritten
-  uint64_t* yfull = empty + kGStages;      // y of an even (odd) tile is there
-  uint64_t* done = yfull + 2;              // its MMAs are done
-  uint64_t* xempty = done + 2;             // its product has been read
+  constexpr int kSteps = S::kSteps;
+  uint64_t* yfull = empty + kGStages;      // y of an even (odd) tile is there, [kSteps] each
+  uint64_t* done = yfull + 2 * kSteps;     // its MMAs are done, likewise
+  uint64_t* xempty = done + 2 * kSteps;    // its product has been read
   uint64_t* last = xempty + 2;             // MMAs in flight after a give-up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
@@ -221,11 +254,11 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
       mbar_init(full + i, 1);
       mbar_init(empty + i, kGWarps + kGWarps / 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * kSteps; ++i) {
       mbar_init(yfull + i, kGWarps);
       mbar_init(done + i, 1);
-      mbar_init(xempty + i, kGWarps / 2);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(xempty + i, kGWarps / 2);
     mbar_init(last, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -258,9 +291,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
 
   // A wait of a warp together; false: give up.
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(b, parity & 1u, p.status) && !*abort_flag);
-    if (!ok) *abort_flag = 1;
-    return ok;
+    return __all_sync(0xffffffffu, mbar_try_wait(b, parity & 1u) || wait_or_give_up(b, parity & 1u, p.status, abort_flag));
   };
   auto arrive = [&](uint64_t* b) {
     __syncwarp();
@@ -367,20 +398,27 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
       const uint32_t e = n & 1;
       if (!(ok = wait(full + n % kGStages, n / kGStages))) break;
       if (tiles[n % kGStages].stop) break;
-      if (!(ok = wait(yfull + e, n >> 1) && wait(xempty + e, (n >> 1) + 1))) break;
-      if (leader) {
-        tc_fence_after();
-        const uint32_t x = tmem + e * D, y = tmem + 2 * D + e * D;
+      if (!(ok = wait(xempty + e, (n >> 1) + 1))) break;
+      const uint32_t x = tmem + e * D, y = tmem + 2 * D + e * D;
 #pragma unroll
-        for (int piece = 0; piece < 3; ++piece) {   // y2 R1, y1 R2, y1 R1
-          const uint32_t a = y + (piece == 0 ? D / 2 : 0), b = piece == 1 ? r2 : r1;
+      for (int m = 0; m < kSteps; ++m) {   // groups m and kSteps + m of 32 channels
+        if (!(ok = wait(yfull + e * kSteps + m, n >> 1))) break;
+        if (leader) {
+          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ts(x, a + 8 * kk, tc_desc_sw128(b + (kk >> 2) * kAtom + (kk & 3) * 32), idesc, piece != 0 || kk != 0);
+          for (int piece = 0; piece < 3; ++piece) {   // y2 R1, y1 R2, y1 R1
+            const uint32_t a = y + (piece == 0 ? D / 2 : 0), b = piece == 1 ? r2 : r1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int kk = 2 * (m + (k >> 1) * kSteps) + (k & 1);
+              tc_mma_ts(x, a + 8 * kk, tc_desc_sw128(b + (kk >> 2) * kAtom + (kk & 3) * 32), idesc,
+                        m != 0 || piece != 0 || k != 0);
+            }
+          }
+          tc_commit(done + e * kSteps + m);
         }
-        tc_commit(done + e);
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (!ok && leader) {   // MMAs in flight finish before the CTA ends
       tc_commit(last);
@@ -393,14 +431,23 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
     for (uint32_t n = odd;; n += 2) {
       const int st = n % kGStages;
       if (!wait(full + st, n / kGStages) || tiles[st].stop) break;
-      if (!wait(done + odd, (n >> 1) + 1)) break;   // y of the tile before has been used
-      tc_fence_after();
       const uint8_t* blk = smem + S::kRing + (st * kGPages + row / kPage) * S::kPart;
-      if (kv) uncode<D, P, true>(blk, row % kPage, half, y);
-      else uncode<D, P, false>(blk, row % kPage, half, y);
-      tc_wait_st();
-      tc_fence_before();
-      arrive(yfull + odd);
+      uint32_t x[P][4][kSteps];
+      if (kv) load_codes<D, P, true>(blk, row % kPage, half, x);
+      else load_codes<D, P, false>(blk, row % kPage, half, x);
+      bool ok = true;
+#pragma unroll
+      for (int m = 0; m < kSteps; ++m) {
+        // y of the tile before has been used
+        if (!(ok = wait(done + odd * kSteps + m, (n >> 1) + 1))) break;
+        tc_fence_after();
+        if (kv) uncode<D, P, true>(blk, row % kPage, half, m, x, y);
+        else uncode<D, P, false>(blk, row % kPage, half, m, x, y);
+        tc_wait_st();
+        tc_fence_before();
+        arrive(yfull + odd * kSteps + m);
+      }
+      if (!ok) break;
       if (lane == 0) tc_arrive(empty + st);
     }
   } else {
@@ -411,7 +458,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
       const int st = n % kGStages;
       if (!wait(full + st, n / kGStages)) break;
       const GatherTile& t = tiles[st];
-      if (t.stop || !wait(done + odd, n >> 1)) break;
+      if (t.stop || !wait(done + odd * kSteps + kSteps - 1, n >> 1)) break;
       tc_fence_after();
       const int pos = t.pos0 + row;
       uint16_t* dst = p.out[kv] + ((t.row0 + row) * p.hkv + h) * D;
