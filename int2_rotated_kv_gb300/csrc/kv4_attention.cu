@@ -5,11 +5,607 @@
 // with k_t = code s(channel) g_K(page, head), v_t = code s(token, 16 channels) g_V(page, head) for
 // tokens in whole pages and bf16 keys and values for the tokens of the tail.
 //
-// The forms, the division of work and the arithmetic are those of the 8-bit cache
+// The arithmetic, the units of weights and the division of work are those of the 8-bit cache
 // (kv8_attention.cu), with code * s, exact in fp16, where that one has codes, and g for its scale: the
 // only roundings are q (exact down to 2^-21 of a column's largest), p g_V (11 bits, unbiased) and
 // the output.
+//
+// What differs: with half the bytes a page, instructions bound the loop before HBM does (a page's
+// 1024 keys and values take 64 conversions and 64 products of a warp before the 16 MMAs).
+//   - A warp takes two pages at a time: one wait, one softmax step for 32 tokens, and two
+//     independent chains of instructions.
+//   - Tiles of 8, 16 or 24 query columns: what was converted serves all of them, and every page is read
+//     once.  (For more columns, several tiles, or tiles of 128: kv8_rows.cu.)
 #include "kv8_tiles.cuh"
+
+namespace oscar {
+
+constexpr int kMaxNT = 3;      // tiles of 8 columns that share a page's operands
+constexpr int kPair = 2;       // pages of a step
+
+template <int D, int NT, Kv8Mode kMode>
+struct Kv4Cfg {
+  using F = Kv4Fmt<D>;
+  static constexpr int kWarps = kMode == kCluster && NT == 1 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = NT == 1 && kMode != kCluster ? 2 : 1;   // per SM
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 2 : 3) : 4;
+  static constexpr int kStage = kPair * F::kBlock;
+  static constexpr int kWarpRing = kStages * kStage;
+  static constexpr int kStride = D + 4;                     // floats per column when merging
+  static constexpr int kMerge = kWarps * 8 * kStride * 4;   // 8 columns at a time
+  static constexpr int kStat = kWarps * 8 * NT * 4;         // one of m, k, l
+  static constexpr int kMergeOff = kWarps * kWarpRing;
+  static constexpr int kStatOff = kMergeOff + kMerge;
+  static constexpr int kUnitOff = kStatOff + 3 * kStat;     // float2: units that the parts are brought to
+  static constexpr int kPartOff = kUnitOff + kWarps * 8 * NT * 8;   // a cluster's CTA: its partial
+  static constexpr int kBarOff = kPartOff + (kMode == kCluster ? kv8_slot<D, NT>() * 4 : 0);
+  static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
+  static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
+  static_assert(kStage % 16 == 0 && kMergeOff % 16 == 0 && kUnitOff % 16 == 0 && kPartOff % 16 == 0, "alignment");
+};
+
+// weigh (kv8_tiles.cuh) for the tokens of two pages: logits lg[n] in the accumulator layout, value scales 2^off[n].
+template <int D>
+__device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPair][4], const float (&off)[kPair],
+                                           float (&w)[kPair][4]) {
+  float e[kPair][4], up[kPair][2];
+  bool over = false;
+  const uint64_t less = two(-1.f, -1.f), m2 = two(s.m[0], s.m[1]), k2 = two(s.k[0], s.k[1]);
+#pragma unroll
+  for (int n = 0; n < kPair; ++n) {
+    const uint64_t e0 = fma2(m2, less, two(lg[n][0], lg[n][1])), e1 = fma2(m2, less, two(lg[n][2], lg[n][3]));
+    const uint64_t u2 = fma2(k2, less, two(off[n], off[n]));
+    e[n][0] = first(e0); e[n][1] = second(e0); e[n][2] = first(e1); e[n][3] = second(e1);
+    up[n][0] = first(u2); up[n][1] = second(u2);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) over |= fmaxf(e[n][c], e[n][2 + c]) > fminf(kLag, kLag + kLift - up[n][c]);
+  }
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float top[kPair], m = s.m[c];
+#pragma unroll
+      for (int n = 0; n < kPair; ++n) {
+        top[n] = fmaxf(lg[n][c], lg[n][2 + c]);
+        top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 4));
+        top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 8));
+        top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 16));
+        m = fmaxf(m, top[n]);
+      }
+      const float down = s.m[c] - m, k0 = s.k[c] + down;
+      // the unit as it is, seen from m; and what these pages need
+      float k = fmaxf(k0, kNoUnit.k);
+#pragma unroll
+      for (int n = 0; n < kPair; ++n) k = fmaxf(k, top[n] - m + off[n] - kLift);
+      s.l[c] *= fast_exp2(down);
+      const float a = fast_exp2(k0 - k);
+      s.m[c] = m;
+      s.k[c] = k;
+#pragma unroll
+      for (int n = 0; n < kPair; ++n) {
+        e[n][c] = lg[n][c] - m;
+        e[n][2 + c] = lg[n][2 + c] - m;
+        up[n][c] = off[n] - k;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        s.o[i][c] *= a;
+        s.o[i][2 + c] *= a;
+      }
+    }
+  }
+  uint64_t l = two(s.l[0], s.l[1]);
+#pragma unroll
+  for (int n = 0; n < kPair; ++n) {
+    // (finite: it meets p of 0 where it is large)
+    const uint64_t scale = two(fast_exp2(fminf(up[n][0], 126.f)), fast_exp2(fminf(up[n][1], 126.f)));
+    const uint64_t p0 = two(fast_exp2(e[n][0]), fast_exp2(e[n][1])), p1 = two(fast_exp2(e[n][2]), fast_exp2(e[n][3]));
+    l = add2(l, add2(p0, p1));
+    const uint64_t w0 = mul2(p0, scale), w1 = mul2(p1, scale);
+    w[n][0] = first(w0);
+    w[n][1] = second(w0);
+    w[n][2] = first(w1);
+    w[n][3] = second(w1);
+  }
+  s.l[0] = first(l);
+  s.l[1] = second(l);
+}
+
+// Two pages of codes, at st and st + kBlock, their tokens from page0[n] on; `there`: bit per page.
+template <int D, int NT>
+__device__ __forceinline__ void page_pair(const uint8_t* st, const int (&page0)[kPair], uint32_t there, int lane,
+                                          const Query<D> (&q)[NT], Running<D> (&s)[NT]) {
+  using F = Kv4Fmt<D>;
+  const int gid = lane >> 2, tig = lane & 3;
+  // one that is not there is read as the other, and weighs nothing
+  const uint8_t* at[kPair] = {st + (there & 1u ? 0 : F::kBlock), st + (there & 2u ? F::kBlock : 0)};
+  float lg[NT][kPair][4];
+  float off[kPair], sk[kPair];
+#pragma unroll
+  for (int n = 0; n < kPair; ++n) {
+    const float2 sc = *reinterpret_cast<const float2*>(at[n] + F::kScales);
+    sk[n] = sc.x;
+    off[n] = fast_log2(sc.y);   // (a page of zeros: -inf, weights of 0)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) lg[t][n][0] = lg[t][n][1] = lg[t][n][2] = lg[t][n][3] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+#pragma unroll
+    for (int n = 0; n < kPair; ++n) {
+      const uint4 k = reinterpret_cast<const uint4*>(at[n])[32 * j + lane];   // tokens 2 gid, 2 gid + 1
+      const uint4 sc = reinterpret_cast<const uint4*>(at[n] + F::kKeyScales)[4 * j + tig];
+      const uint32_t t0[2] = {k.x, k.y}, t1[2] = {k.z, k.w}, s4[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {   // 8 channels: two k-steps
+        uint32_t a[4], b[4], x[4];
+        kv4_pairs(t0[w], a[0], a[1], a[2], a[3]);
+        kv4_pairs(t1[w], b[0], b[1], b[2], b[3]);
+        kv4_scales(s4[2 * w], x[0], x[1]);
+        kv4_scales(s4[2 * w + 1], x[2], x[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = hmul2_u32(a[i], x[i]);
+          b[i] = hmul2_u32(b[i], x[i]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t (&qb)[D / 16][2] = q[t].b;
+          mma_f16(lg[t][n], a[0], b[0], a[1], b[1], qb[4 * j + 2 * w][0], qb[4 * j + 2 * w][1]);
+          mma_f16(lg[t][n], a[2], b[2], a[3], b[3], qb[4 * j + 2 * w + 1][0], qb[4 * j + 2 * w + 1][1]);
+        }
+      }
+    }
+  }
+  uint32_t wb[NT][kPair][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int n = 0; n < kPair; ++n) {
+      const float f0 = logit_factor(sk[n], q[t].fac[0]), f1 = logit_factor(sk[n], q[t].fac[1]);
+      // (rounded by themselves, not on the way to a difference, so that equal logits stay equal)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) lg[t][n][r] = __fmul_rn(lg[t][n][r], r & 1 ? f1 : f0);
+      if (page0[n] + kPage > q[t].vis_min || !((there >> n) & 1u)) {
+        const int tk = page0[n] + 2 * gid;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int vis = (there >> n) & 1u ? q[t].vis[c] : 0;
+          if (tk >= vis) lg[t][n][c] = -INFINITY;
+          if (tk + 1 >= vis) lg[t][n][2 + c] = -INFINITY;
+        }
+      }
+    }
+    float w[kPair][4];
+    weigh_pair<D>(s[t], lg[t], off, w);
+    // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed and put in order, the two
+    // registers hold tokens (4tig, 4tig + 1) and (4tig + 2, 4tig + 3) of column gid
+#pragma unroll
+    for (int n = 0; n < kPair; ++n) {
+      const uint32_t b0 = movmatrix_trans(pack_half2(w[n][0], w[n][1]));
+      const uint32_t b1 = movmatrix_trans(pack_half2(w[n][2], w[n][3]));
+      wb[t][n][0] = __byte_perm(b0, b1, 0x5410);
+      wb[t][n][1] = __byte_perm(b0, b1, 0x7632);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+#pragma unroll
+    for (int n = 0; n < kPair; ++n) {
+      // channels 64i + 4 gid and on, 64i + 32 + 4 gid and on, of tokens 4 tig and on
+      const uint4 v = reinterpret_cast<const uint4*>(at[n] + F::kCodes)[32 * i + lane];
+      const uint2 sc = reinterpret_cast<const uint2*>(at[n] + F::kValueScales)[8 * i + 4 * (gid >> 2) + tig];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t s01, s23;
+        kv4_scales(half ? sc.y : sc.x, s01, s23);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {   // two channels
+          uint32_t a0, a1, a2, a3;
+          kv4_pairs(w[2 * half + y], a0, a2, a1, a3);
+          a0 = hmul2_u32(a0, s01);
+          a1 = hmul2_u32(a1, s01);
+          a2 = hmul2_u32(a2, s23);
+          a3 = hmul2_u32(a3, s23);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma_f16(s[t].o[4 * i + 2 * half + y], a0, a1, a2, a3, wb[t][n][0], wb[t][n][1]);
+        }
+      }
+    }
+  }
+}
+
+// A warp's ring of copies, two pages a stage: as Ring, with two bits per stage in `shown` and a page's id in
+// each of the first two lanes.
+//
+// Asks for the pages pg and pg + step (those below end), and looks up the ids of the two behind them.
+template <typename C>
+__device__ __forceinline__ void issue_pair(const Kv8Params& p, const Entry& t, int h, int pg, int end, int step,
+                                           int lane, Ring& r) {
+  const int st = r.n_in % C::kStages, mine = pg + lane * step;
+  const bool have = lane < kPair && mine < end, ok = have && r.next_id >= 0 && r.next_id < p.n_pages;
+  const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+  if (have && !ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+  r.shown = (r.shown & ~(3u << (2 * st))) | (mask << (2 * st));
+  if (lane == 0) mbar_arrive_expect_tx(r.bars + st, __popc(mask) * C::F::kBlock);
+  __syncwarp();
+  if (ok)
+    bulk_g2s(r.base + st * C::kStage + lane * C::F::kBlock,
+             p.pool + (static_cast<int64_t>(r.next_id) * p.hkv + h) * C::F::kBlock, C::F::kBlock, r.bars + st);
+  ++r.n_in;
+  const int next = mine + kPair * step;
+  if (lane < kPair && next < end) r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + next];
+}
+
+template <typename C>
+__device__ __forceinline__ void start_pairs(const Kv8Params& p, const Entry& t, int h, const Part& a, int step,
+                                            int lane, Ring& r) {
+  r.tail_issued = false;
+  if (!r.alive) return;
+  if (a.first < a.end) {
+    const int mine = a.first + lane * step;
+    if (lane < kPair && mine < a.end) r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + mine];
+#pragma unroll 1
+    for (int i = 0; i < C::kStages; ++i)
+      if (a.first + i * kPair * step < a.end) issue_pair<C>(p, t, h, a.first + i * kPair * step, a.end, step, lane, r);
+  } else if (a.tail) {
+    issue_tail<C>(p, t, h, lane, r);
+  }
+}
+
+// merge_cluster for NT tiles of 8 columns.
+template <int D, int NT>
+__device__ __forceinline__ void merge_cluster4(const Kv8Params& p, const Entry& t, int h, const float* slot, float4* stats) {
+  cluster_sync();
+  const int n = p.cluster, rank = blockIdx.x % n;
+  constexpr int kOne = kv8_slot<D, 1>();
+  for (int i = threadIdx.x; i < 8 * NT * n; i += blockDim.x) {
+    const int col = i % (8 * NT);
+    stats[i] = cluster_load4(cluster_address(slot + col / 8 * kOne + 8 * D + 4 * (col % 8), i / (8 * NT)));
+  }
+  __syncthreads();
+  constexpr int kAll = 8 * NT * D / 4;          // float4 of a unit
+  const int per = (kAll + n - 1) / n, end = min(kAll, (rank + 1) * per);
+  for (int i = rank * per + threadIdx.x; i < end; i += blockDim.x) {
+    const int col = i / (D / 4), ch = 4 * (i % (D / 4)), gcol = t.tile * 8 * NT + col;
+    if (gcol >= p.cols) continue;
+    float m = kLowest, k = kLowest, l = 0.f;
+    for (int r = 0; r < n; ++r) m = fmaxf(m, stats[8 * NT * r + col].x);
+    for (int r = 0; r < n; ++r) k = fmaxf(k, (stats[8 * NT * r + col].x - m) + stats[8 * NT * r + col].y);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) {
+      const float4 part = stats[8 * NT * r + col];
+      const float4 x = cluster_load4(cluster_address(slot + col / 8 * kOne + col % 8 * D + ch, r));
+      const float down = part.x - m, a = fast_exp2(down + part.y - k);
+      l = fmaf(fast_exp2(down), part.z, l);
+      o.x = fmaf(a, x.x, o.x); o.y = fmaf(a, x.y, o.y);
+      o.z = fmaf(a, x.z, o.z); o.w = fmaf(a, x.w, o.w);
+    }
+    store_row(p, t.b, h, gcol, ch, D, o, output_factor(k, l));
+  }
+  cluster_sync();   // no CTA leaves while its shared memory is read
+}
+
+template <int D, int NT, Kv8Mode kMode>
+__global__ void __launch_bounds__((Kv4Cfg<D, NT, kMode>::kThreads), (Kv4Cfg<D, NT, kMode>::kCtas))
+kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
+  using C = Kv4Cfg<D, NT, kMode>;
+  constexpr int kWarps = C::kWarps, kCols = 8 * NT, kOne = kv8_slot<D, 1>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  // the warps of a unit (all, or a team of them) and this one's place among them
+  const int team = kMode == kTeams ? p.team : kWarps;
+  const int number = kMode == kTeams ? (tid >> 5) / team : 0;
+  const int warp = (tid >> 5) - number * team;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  float* sm_m = reinterpret_cast<float*>(smem + C::kStatOff) + number * team * kCols;
+  float* sm_k = sm_m + kWarps * kCols;
+  float* sm_l = sm_k + kWarps * kCols;
+  float2* sm_unit = reinterpret_cast<float2*>(smem + C::kUnitOff) + number * kCols;
+  float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
+  if (tid < kWarps * C::kStages) mbar_init(bars + tid, 1);
+  fence_mbar_init();
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  // this team's pages [at, end) of all units laid end to end, and its first unit
+  int e = 0, h = 0;
+  int64_t at = 0, end = 0, share = 0, unit0 = 0;   // unit0: first page of the current unit
+  Entry t;
+  if constexpr (kMode == kTeams) {   // a whole unit
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kWarps / team) + number;
+    if (unit >= static_cast<int64_t>(p.entries) * p.hkv) return;
+    e = static_cast<int>(unit / p.hkv);
+    h = static_cast<int>(unit - static_cast<int64_t>(e) * p.hkv);
+    t = entry_of<NT>(p, e);
+    end = t.pages;
+  } else if constexpr (kMode == kCluster) {   // this CTA's run of the cluster's unit
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
+    e = unit / p.hkv;
+    h = unit - e * p.hkv;
+    t = entry_of<NT>(p, e);
+    at = static_cast<int64_t>(t.pages) * rank / p.cluster;
+    end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
+  } else {
+    bool any;
+    const Share sh = find_share<NT, kWarps>(p, min_share, any);
+    if (!any) {
+      if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    at = sh.at;
+    end = sh.end;
+    share = sh.share;
+    unit0 = sh.unit0;
+    e = sh.e;
+    h = sh.h;
+    t = sh.t;
+  }
+
+  Ring ring{smem + (tid >> 5) * C::kWarpRing, bars + (tid >> 5) * C::kStages, 0, 0, 0, 0, true, false};
+  int4 owned = make_int4(0, 0, 0, 0);
+  int p0 = static_cast<int>(at - unit0);
+  int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
+  Part mine = part_of(t, p0, p1, warp, team);
+  start_pairs<C>(p, t, h, mine, team, lane, ring);
+
+  for (;;) {
+    Query<D> q[NT];
+    Running<D> s[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      load_query<D, kCodeE2m1>(p, t, h, t.tile * kCols + 8 * n, lane, q[n]);
+      reset<D>(s[n]);
+    }
+    if (p0 == 0 && h == 0 && t.tile == 0 && warp == 0 && lane == 0 && p.status) {
+      const int len = p.seq_lens[t.b];
+      if (len < 0 || len > p.max_len) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+    }
+    if (p.q_pos && p0 == 0 && h == 0 && warp == 0 && lane < kCols && p.status) {
+      const int row = (t.tile * kCols + lane) / p.G;
+      if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
+        atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+    }
+#pragma unroll 1
+    for (int pg = mine.first; pg < mine.end && ring.alive; pg += kPair * team) {
+      int st;
+      if (!copied<C>(p, ring, st)) break;
+      const uint32_t there = (ring.shown >> (2 * st)) & 3u;
+      const int page0[kPair] = {pg * kPage, (pg + team) * kPage};
+      // (a refused id's stands for nothing)
+      if (there) page_pair<D, NT>(ring.base + st * C::kStage, page0, there, lane, q, s);
+      __syncwarp();
+      if (pg + C::kStages * kPair * team < mine.end)
+        issue_pair<C>(p, t, h, pg + C::kStages * kPair * team, mine.end, team, lane, ring);
+    }
+    if (mine.tail && ring.alive) {
+      if (!ring.tail_issued) issue_tail<C>(p, t, h, lane, ring);
+      int st;
+      if (copied<C>(p, ring, st) && ((ring.shown >> st) & 1u)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q[n], s[n]);
+      }
+      __syncwarp();
+    }
+
+    // the next unit of this CTA: its copies start before this one is merged
+    const Entry tc = t;
+    const int hc = h, c0 = p0, c1 = p1;
+    const int64_t u0 = unit0;
+    const bool more = kMode == kShares && u0 + c1 < end;
+    if (more) {
+      unit0 = u0 + tc.pages;
+      if (++h == p.hkv) {
+        h = 0;
+        t = entry_of<NT>(p, ++e);
+      }
+      p0 = 0;
+      p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
+      mine = part_of(t, p0, p1, warp, team);
+      start_pairs<C>(p, t, h, mine, team, lane, ring);
+    }
+
+    if (gid == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          sm_m[warp * kCols + 8 * n + 2 * tig + c] = s[n].m[c];
+          sm_k[warp * kCols + 8 * n + 2 * tig + c] = s[n].k[c];
+        }
+    }
+    team_sync<kMode>(team, number);
+    const bool complete = c0 == 0 && c1 == tc.pages;
+    float* slot = kMode == kCluster
+        ? reinterpret_cast<float*>(smem + C::kPartOff)
+        : p.part + (2 * static_cast<size_t>(blockIdx.x) + (c0 == 0 ? 1 : 0)) * (NT * kOne);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {   // 8 columns at a time
+      // the parts of a column in the unit of the largest m, and the k with which it lies as high as the highest
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 2 * tig + c, at_col = 8 * n + col;
+        float m = kLowest, k = kLowest;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (kMode != kTeams || w < team) m = fmaxf(m, sm_m[w * kCols + at_col]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (kMode != kTeams || w < team) k = fmaxf(k, (sm_m[w * kCols + at_col] - m) + sm_k[w * kCols + at_col]);
+        const float down = s[n].m[c] - m, a = fast_exp2(down + s[n].k[c] - k);
+        float l = s[n].l[c] * fast_exp2(down);
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (gid == 0) sm_l[warp * kCols + at_col] = l;
+        if (warp == 0 && gid == 0) sm_unit[at_col] = make_float2(m, k);
+        float* dst = merge + (warp * 8 + col) * C::kStride + 4 * gid;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          *reinterpret_cast<float4*>(dst + 32 * i) =
+              make_float4(s[n].o[2 * i][c] * a, s[n].o[2 * i][2 + c] * a,
+                          s[n].o[2 * i + 1][c] * a, s[n].o[2 * i + 1][2 + c] * a);
+      }
+      team_sync<kMode>(team, number);
+      for (int i = warp * 32 + lane; i < 8 * D / 4; i += 32 * team) {
+        const int col = i / (D / 4), ch = 4 * (i % (D / 4));
+        const int gcol = tc.tile * kCols + 8 * n + col;
+        if (kMode != kCluster && gcol >= p.cols) continue;
+        const float2 unit = sm_unit[8 * n + col];
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (kMode == kTeams && w >= team) break;
+          l += sm_l[w * kCols + 8 * n + col];
+          const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + col) * C::kStride + ch);
+          o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+        }
+        if (kMode != kCluster && (kMode == kTeams || complete)) {
+          store_row(p, tc.b, hc, gcol, ch, D, o, output_factor(unit.y, l));
+        } else {
+          *reinterpret_cast<float4*>(slot + n * kOne + col * D + ch) = o;
+          if (ch == 0)
+            *reinterpret_cast<float4*>(slot + n * kOne + 8 * D + 4 * col) = make_float4(unit.x, unit.y, l, 0.f);
+        }
+      }
+      if (kMode != kTeams) __syncthreads();   // before the buffers are written again
+    }
+    if constexpr (kMode == kCluster) {
+      merge_cluster4<D, NT>(p, tc, hc, slot, reinterpret_cast<float4*>(merge));
+      return;
+    }
+    if constexpr (kMode == kTeams) return;
+    if (!complete && c0 == 0)   // the unit goes on in the next CTAs: they hold its other parts
+      owned = make_int4(e, hc, static_cast<int>((u0 + tc.pages - 1) / share) - blockIdx.x + 1, 0);
+    if (!more) break;
+  }
+  if (tid == 0) p.info[blockIdx.x] = owned;
+}
+
+struct Kv4Plan {
+  int nt;              // tiles of 8 columns that share pages; 0: tiles of 128 columns (kv8_rows.cu)
+  int cluster, team;   // cluster > 0: CTAs per unit; team > 0: warps per unit
+  int64_t tiles, entries, ctas;
+  size_t info, total;   // workspace bytes: the CTAs' records, all
+  size_t most;          // no call of fewer sequences, rows or tokens takes more than this
+};
+
+// CTAs that share the pages of `units`.
+inline int64_t share_ctas4(int nt, int64_t units, int64_t pages, int64_t sms) {
+  return std::min(std::min<int64_t>(kMaxCtas, nt == 1 ? 2 * sms : sms), (units * pages + kMinShare - 1) / kMinShare);
+}
+
+// Estimates in us, as kv8_plan's.
+inline double shares_us4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
+  return 6.0 + (0.00028 + 0.00010 * nt) / 128 * (d + 16) * visited(batch, units, pages);
+}
+inline double cluster_us4(int d, int nt, int64_t pages, int c) {
+  return (0.03 + 0.015 * nt) / 128 * (d + 16) * static_cast<double>(pages) / c;
+}
+inline double rows_us4(int d, int64_t batch, int64_t units, int64_t pages, int64_t sms) {
+  return rows_us(d, batch, units, pages, sms);
+}
+
+inline int cluster_of4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
+  const ClusterSizes s = cluster_sizes<kCodeInt8>();   // (every cluster kernel fills an SM)
+  int c = kMaxCluster;
+  while (c > 0 && s.active[c] < units) --c;
+  if (c == 0) return 0;
+  c = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c, pages / 8)));   // half the warps busy
+  return cluster_us4(d, nt, pages, c) < shares_us4(d, nt, batch, units, pages) ? c : 0;
+}
+
+// false: sizes outside the supported range.
+inline bool kv4_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int64_t max_len, Kv4Plan* out) {
+  Kv4Plan p{};
+  const int64_t cols = m_rows * (c->num_q_heads / c->num_kv_heads);
+  const int64_t tiles8 = (cols + 7) / 8, tiles128 = (cols + 127) / 128;
+  // (positions, and those of the pages behind the last, fit int32)
+  if (max_len > (1 << 30) || cols > (1 << 30) || batch * tiles8 > (1 << 30) || batch * tiles8 * c->num_kv_heads > 0x7fffffff)
+    return false;
+  const int d = c->head_dim, h = c->num_kv_heads;
+  const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);
+  const int64_t sms = oscar_host::sm_count(), units8 = batch * tiles8 * h;
+  double best = 0;
+  for (int nt = 1; nt <= kMaxNT && (nt == 1 || tiles8 > nt - 1); ++nt) {
+    Kv4Plan x{};
+    x.nt = nt;
+    x.tiles = (tiles8 + nt - 1) / nt;
+    const int64_t units = batch * x.tiles * h;
+    if (nt == 1) x.team = team_of(units, pages, sms);
+    if (!x.team) x.cluster = cluster_of4(d, nt, batch, units, pages);
+    const double us = x.cluster ? 6.0 + cluster_us4(d, nt, pages, x.cluster) : shares_us4(d, nt, batch, units, pages);
+    if (nt == 1 || us < best) {
+      best = us;
+      p = x;
+    }
+  }
+  if (cols > 8 && rows_us4(d, batch, batch * tiles128 * h, pages, sms) < best) {
+    p = Kv4Plan{};
+    p.tiles = tiles128;
+  }
+  p.entries = batch * p.tiles;
+  const int64_t units = p.entries * h;
+  p.ctas = p.team      ? (units * p.team + 7) / 8
+           : p.cluster ? units * p.cluster
+           : p.nt      ? share_ctas4(p.nt, units, pages, sms)
+                       : share_ctas(true, units, pages, sms);
+  p.info = record_bytes(p.ctas);
+  p.total = p.cluster || p.team ? 16 : part_bytes(p.nt ? 8 * p.nt : 128, d, p.ctas);
+  // a smaller call may take another form: shares of any number of columns up to these, or wide tiles
+  for (int nt = 1; nt <= kMaxNT && (nt == 1 || tiles8 > nt - 1); ++nt)
+    p.most = std::max(p.most, part_bytes(8 * nt, d, share_ctas4(nt, units8, pages, sms)));
+  if (cols > 8) p.most = std::max(p.most, share_bytes(true, d, share_ctas(true, batch * tiles128 * h, pages, sms)));
+  *out = p;
+  return true;
+}
+
+template <int D, int NT, Kv8Mode kMode>
+oscar_status launch_attention4(const Kv8Params& p, const Kv4Plan& pl, cudaStream_t st) {
+  using C = Kv4Cfg<D, NT, kMode>;
+  const auto kernel = kv4_attention_kernel<D, NT, kMode>;
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, kMode == kCluster))
+    return OSCAR_ERR_CUDA;
+  return launch_kv8(kernel, kMode == kCluster ? pl.cluster : 1, dim3(static_cast<unsigned>(pl.ctas)),
+                    C::kThreads, C::kBytes, st, p, kMinShare) == cudaSuccess
+             ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+template <int D, int NT>
+oscar_status run_tiles4(const Kv8Params& p, const Kv4Plan& pl, cudaStream_t st) {
+  if constexpr (NT == 1)
+    if (pl.team) return launch_attention4<D, 1, kTeams>(p, pl, st);
+  if (pl.cluster) return launch_attention4<D, NT, kCluster>(p, pl, st);
+  const oscar_status s = launch_attention4<D, NT, kShares>(p, pl, st);
+  if (s != OSCAR_OK) return s;
+  // four warps a column
+  return launch_kv8(kv8_merge_kernel<D, NT>, 1, dim3(static_cast<unsigned>(pl.ctas), (std::min(p.cols, 8 * NT) + 1) / 2),
+                    256, 0, st, p) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+template <int D>
+oscar_status run_kv4(const Kv8Params& p, const Kv4Plan& pl, cudaStream_t st) {
+  switch (pl.nt) {
+    case 1: return run_tiles4<D, 1>(p, pl, st);
+    case 2: return run_tiles4<D, 2>(p, pl, st);
+    case 3: return run_tiles4<D, 3>(p, pl, st);
+    default: break;
+  }
+  const oscar_status s = run_kv8_rows(p, D, kCodeE2m1, pl.ctas, kMinShare, st);
+  if (s != OSCAR_OK) return s;
+  return launch_kv8(kv8_merge_rows_kernel<D>, 1, dim3(static_cast<unsigned>(pl.ctas), (std::min(p.cols, 128) + 31) / 32),
+                    4 * D, 0, st, p) == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA;
+}
+
+}  // namespace oscar
 
 namespace oscar_host {
 
@@ -31,8 +627,11 @@ extern "C" {
 size_t oscar_kv4_workspace_size(const oscar_kv4_desc* desc, int32_t batch, int32_t m_rows,
                                 int32_t max_seq_len) {
   oscar_kv8_desc c;
-  if (oscar_host::check_kv4(desc, &c) != OSCAR_OK) return 0;
-  return workspace_of<kCodeE2m1>(&c, batch, m_rows, max_seq_len);
+  Kv4Plan pl;
+  if (oscar_host::check_kv4(desc, &c) != OSCAR_OK || batch < 1 || m_rows < 1 || max_seq_len < 1 ||
+      !kv4_plan(&c, batch, m_rows, max_seq_len, &pl))
+    return 0;
+  return pl.most;
 }
 
 oscar_status oscar_kv4_attention(const oscar_kv4_desc* desc, const void* q, const int32_t* seq_lens,
@@ -40,10 +639,18 @@ oscar_status oscar_kv4_attention(const oscar_kv4_desc* desc, const void* q, cons
                                  int32_t max_seq_len, void* out, void* workspace,
                                  size_t workspace_bytes, void* stream) {
   oscar_kv8_desc c;
-  const oscar_status s = oscar_host::check_kv4(desc, &c);
+  oscar_status s = oscar_host::check_kv4(desc, &c);
   if (s != OSCAR_OK) return s;
-  return attend<kCodeE2m1>(&c, q, seq_lens, q_pos, batch, m_rows, max_seq_len, out, workspace,
-                           workspace_bytes, stream);
+  bool work;
+  s = check_attention(&c, q, seq_lens, q_pos, batch, m_rows, max_seq_len, out, workspace, &work);
+  if (s != OSCAR_OK || !work) return s;
+  Kv4Plan pl;
+  if (!kv4_plan(&c, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
+  if (workspace_bytes < pl.total) return OSCAR_ERR_WORKSPACE;
+  const Kv8Params p = attention_params(&c, q, seq_lens, q_pos, m_rows, max_seq_len, out, workspace, pl.tiles,
+                                       pl.entries, pl.cluster, pl.team, pl.info);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.head_dim == 128 ? run_kv4<128>(p, pl, st) : run_kv4<64>(p, pl, st);
 }
 
 }  // extern "C"

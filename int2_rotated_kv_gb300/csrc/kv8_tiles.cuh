@@ -1,6 +1,6 @@
-// Tiles of 8 query columns of attention over a paged cache of 8-bit or 4-bit codes, the merges of
-// partial results and the choice of form: kv8_attention.cu and kv4_attention.cu have the mathematics,
-// and what each measured.
+// Tiles of 8 query columns of attention over the 8-bit cache, the merges of partial results and the choice
+// of form: kv8_attention.cu has the mathematics, and what they measured.  Much of it serves the 4-bit
+// cache too (kv4_attention.cu).
 #pragma once
 
 #include <algorithm>
@@ -19,7 +19,7 @@ struct Kv8Cfg {
   static constexpr int kWarps = kMode == kCluster ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = kMode != kCluster ? 2 : 1;   // per SM
-  static constexpr int kStages = D == 128 && kCode != kCodeE2m1 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kWarpRing = kStages * F::kBlock;
   static constexpr int kStride = D + 4;                     // floats per column when merging
   static constexpr int kMerge = kWarps * 8 * kStride * 4;
@@ -47,10 +47,10 @@ struct Query {
 };
 
 template <int D, int kCode>
-__device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, int h, int lane,
+__device__ __forceinline__ void load_query(const Kv8Params& p, const Entry& t, int h, int col0, int lane,
                                            Query<D>& q) {
   const int gid = lane >> 2, tig = lane & 3;
-  const int col = t.tile * 8 + gid;
+  const int col = col0 + gid;
   const uint16_t* src = column(p, t, h, col, D);
   int vis = 0x7fffffff;
   if (src) vis = p.q_pos ? row_limit(p, t.b, col / p.G, t.len) : t.len;
@@ -175,61 +175,6 @@ __device__ __forceinline__ void weigh(Running<D>& s, const float (&lg)[4], float
   w[3] = second(w1);
 }
 
-// Logits of a page of 4-bit codes: codes times the scales of their channels, exact in fp16, are the
-// A operand.
-template <int D>
-__device__ __forceinline__ void kv4_key_products(const uint8_t* st, int lane, const uint32_t (&qb)[D / 16][2],
-                                                 float (&lg)[4]) {
-  const uint4* kb = reinterpret_cast<const uint4*>(st);
-  const uint4* ks = reinterpret_cast<const uint4*>(st + Kv4Fmt<D>::kKeyScales);
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j) {
-    const uint4 k = kb[32 * j + lane], sc = ks[4 * j + (lane & 3)];   // tokens 2 gid, 2 gid + 1
-    const uint32_t t0[2] = {k.x, k.y}, t1[2] = {k.z, k.w}, s4[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {   // 8 channels: two k-steps
-      uint32_t a[4], b[4], s[4];
-      kv4_pairs(t0[w], a[0], a[1], a[2], a[3]);
-      kv4_pairs(t1[w], b[0], b[1], b[2], b[3]);
-      kv4_scales(s4[2 * w], s[0], s[1]);
-      kv4_scales(s4[2 * w + 1], s[2], s[3]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        a[x] = hmul2_u32(a[x], s[x]);
-        b[x] = hmul2_u32(b[x], s[x]);
-      }
-      mma_f16(lg, a[0], b[0], a[1], b[1], qb[4 * j + 2 * w][0], qb[4 * j + 2 * w][1]);
-      mma_f16(lg, a[2], b[2], a[3], b[3], qb[4 * j + 2 * w + 1][0], qb[4 * j + 2 * w + 1][1]);
-    }
-  }
-}
-
-// The same for outputs: b0, b1 hold the weights of tokens (4tig, 4tig + 1), (4tig + 2, 4tig + 3).
-template <int D>
-__device__ __forceinline__ void kv4_value_products(const uint8_t* st, int lane, uint32_t b0, uint32_t b1,
-                                                   float (&o)[D / 16][4]) {
-  const uint4* vb = reinterpret_cast<const uint4*>(st + Kv4Fmt<D>::kCodes);
-  const uint2* vs = reinterpret_cast<const uint2*>(st + Kv4Fmt<D>::kValueScales) + 4 * (lane >> 4) + (lane & 3);
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const uint4 v = vb[32 * i + lane];   // channels 64i + 4 gid and on, 64i + 32 + 4 gid and on
-    const uint2 sc = vs[8 * i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t s01, s23;
-      kv4_scales(half ? sc.y : sc.x, s01, s23);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {   // two channels
-        uint32_t a0, a1, a2, a3;
-        kv4_pairs(w[2 * half + y], a0, a2, a1, a3);
-        mma_f16(o[4 * i + 2 * half + y], hmul2_u32(a0, s01), hmul2_u32(a1, s01), hmul2_u32(a2, s23),
-                hmul2_u32(a3, s23), b0, b1);
-      }
-    }
-  }
-}
-
 // One page of codes at `st`.
 template <int D, int kCode>
 __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, const Query<D>& q,
@@ -241,20 +186,16 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
   lg[0] = lg[2] = q.init[0];
   lg[1] = lg[3] = q.init[1];
   const float2 sc = *reinterpret_cast<const float2*>(st + F::kScales);
-  if constexpr (kCode == kCodeE2m1) {
-    kv4_key_products<D>(st, lane, q.b, lg);
-  } else {
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const uint4 k0 = kb[(2 * j) * 32 + lane], k1 = kb[(2 * j + 1) * 32 + lane];
-      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+  for (int j = 0; j < D / 64; ++j) {
+    const uint4 k0 = kb[(2 * j) * 32 + lane], k1 = kb[(2 * j + 1) * 32 + lane];
+    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t a0, a1, a2, a3;
-        kv8_operands<kCode == kCodeE4m3>(w0[w], a0, a2);
-        kv8_operands<kCode == kCodeE4m3>(w1[w], a1, a3);
-        mma_f16(lg, a0, a1, a2, a3, q.b[4 * j + w][0], q.b[4 * j + w][1]);
-      }
+    for (int w = 0; w < 4; ++w) {
+      uint32_t a0, a1, a2, a3;
+      kv8_operands<kCode == kCodeE4m3>(w0[w], a0, a2);
+      kv8_operands<kCode == kCodeE4m3>(w1[w], a1, a3);
+      mma_f16(lg, a0, a1, a2, a3, q.b[4 * j + w][0], q.b[4 * j + w][1]);
     }
   }
   const float sk = kCode != kCodeInt8 ? sc.x : sc.x * 64.f;
@@ -280,10 +221,6 @@ __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, con
     const uint32_t lo = __byte_perm(b0, b1, 0x5410);
     b1 = __byte_perm(b0, b1, 0x7632);
     b0 = lo;
-  }
-  if constexpr (kCode == kCodeE2m1) {
-    kv4_value_products<D>(st, lane, b0, b1, s.o);
-    return;
   }
   const uint4* vb = reinterpret_cast<const uint4*>(st + F::kCodes);
 #pragma unroll
@@ -328,7 +265,7 @@ __device__ __forceinline__ uint32_t bf16_times(uint32_t w, __nv_bfloat162 x) {
 // fp32 on the CUDA cores instead, which keeps a NaN or an infinity of a token out of
 // the rows that do not see it.
 template <int D>
-__device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uint8_t* st, int page0,
+__device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, int col0, const uint8_t* st, int page0,
                             int n, int lane, const Query<D>& q, Running<D>& s) {
   using F = Kv8Fmt<D>;
   const int gid = lane >> 2, tig = lane & 3;
@@ -340,7 +277,7 @@ __device__ void tail_tokens(const Kv8Params& p, const Entry& t, int h, const uin
 #pragma unroll
     for (int x = 0; x < 2; ++x) {   // 8 channels: two k-steps
       const uint4 k0 = kb[c0 + x], k1 = kb[c1 + x];
-      const uint16_t* src = column(p, t, h, t.tile * 8 + gid, D);
+      const uint16_t* src = column(p, t, h, col0 + gid, D);
       const uint4 qv = src ? *reinterpret_cast<const uint4*>(src + 64 * j + 16 * tig + 8 * x)
                            : make_uint4(0, 0, 0, 0);
       mma_bf16(lg, k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
@@ -665,7 +602,7 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 
   for (;;) {
     Query<D> q;
-    load_query<D, kCode>(p, t, h, lane, q);
+    load_query<D, kCode>(p, t, h, t.tile * 8, lane, q);
     Running<D> s;
     reset<D>(s);
     if (p0 == 0 && h == 0 && t.tile == 0 && warp == 0 && lane == 0 && p.status) {
@@ -691,7 +628,7 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (!ring.tail_issued) issue_tail<C>(p, t, h, lane, ring);
       int st;
       if (copied<C>(p, ring, st) && ((ring.shown >> st) & 1u))
-        tail_tokens<D>(p, t, h, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q, s);
+        tail_tokens<D>(p, t, h, t.tile * 8, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q, s);
       __syncwarp();
     }
 
@@ -787,10 +724,11 @@ kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
 
 // Merges the units that lie in several CTAs.  Block: (CTA in which the unit starts, columns);
 // kSplit warps share the parts of a column, a lane has D / 32 channels.
-template <int D>
+// (NT: tiles of 8 columns that a unit has, one after the other in a partial result.)
+template <int D, int NT = 1>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ Kv8Params p) {
   constexpr int kSplit = 4;   // warps of a column: few columns, with many parts each
-  constexpr int kSlot = kv8_slot<D, 1>(), kPer = D / 32;
+  constexpr int kSlot = kv8_slot<D, NT>(), kPer = D / 32;
   __shared__ float partial[8][D];
   pdl_wait();
   pdl_trigger();
@@ -799,14 +737,15 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const __grid_constant__ 
   if (n == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kSplit;
   const int b = own.x / p.tiles, tile = own.x - b * p.tiles;
-  const int col = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 + col;
-  const bool live = col < 8 && gcol < p.cols;
+  const int all = blockIdx.y * (8 / kSplit) + warp / kSplit, gcol = tile * 8 * NT + all;
+  const int col = all % 8, first = all / 8 * kv8_slot<D, 1>();   // its tile in a partial result
+  const bool live = all < 8 * NT && gcol < p.cols;
   float acc[kPer] = {};
   float m = kLowest, k = kLowest, l = 0.f;
   if (live) {
     // part 0: the CTA's own second slot; part j: the first slot of the j-th CTA after it
     auto slot = [&](int j) {
-      return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot;
+      return p.part + (2 * (blockIdx.x + static_cast<size_t>(j)) + (j == 0 ? 1 : 0)) * kSlot + first;
     };
     auto stats = [&](int j) {   // unit and sum of part j
       return j < n ? *reinterpret_cast<const float4*>(slot(j) + 8 * D + 4 * col)
@@ -1012,9 +951,10 @@ inline int64_t share_ctas(bool rows, int64_t units, int64_t pages, int64_t sms) 
   return std::min(std::min<int64_t>(kMaxCtas, rows ? sms : 2 * sms), (units * pages + kMinShare - 1) / kMinShare);
 }
 inline size_t record_bytes(int64_t ctas) { return (static_cast<size_t>(ctas) * sizeof(int4) + 255) / 256 * 256; }
-inline size_t share_bytes(bool rows, int d, int64_t ctas) {
-  return record_bytes(ctas) + static_cast<size_t>(ctas) * 2 * (rows ? 128 : 8) * (d + 4) * sizeof(float);
+inline size_t part_bytes(int cols, int d, int64_t ctas) {
+  return record_bytes(ctas) + static_cast<size_t>(ctas) * 2 * cols * (d + 4) * sizeof(float);
 }
+inline size_t share_bytes(bool rows, int d, int64_t ctas) { return part_bytes(rows ? 128 : 8, d, ctas); }
 
 // Several sequences are taken as three quarters of the longest: the host does not know the
 // lengths.
@@ -1135,12 +1075,12 @@ oscar_status run_kv8(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
   return launch_merge<D>(p, pl, st);
 }
 
-// Attention over a cache whose descriptor has been checked (of the 4-bit cache too, as the
-// 8-bit one's with another size of its blocks).
-template <int kCode>
-oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens, const int32_t* q_pos,
-                    int32_t batch, int32_t m_rows, int32_t max_seq_len, void* out, void* workspace,
-                    size_t workspace_bytes, void* stream) {
+// Arguments of attention over a cache whose descriptor has been checked (of the 4-bit cache too, as the 8-bit
+// one's with a block format of its own); nothing to do: OSCAR_OK and no work.
+inline oscar_status check_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
+                                    const int32_t* q_pos, int32_t batch, int32_t m_rows, int32_t max_seq_len,
+                                    const void* out, const void* workspace, bool* work) {
+  *work = false;
   if (batch < 0 || m_rows < 0 || max_seq_len < 1 || (!q_pos && m_rows > 1))
     return OSCAR_ERR_INVALID_ARG;
   if (batch == 0 || m_rows == 0) return OSCAR_OK;
@@ -1151,9 +1091,14 @@ oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* se
   // whole pages go through the table, the last tokens through the tail
   if (max_seq_len > static_cast<int64_t>(desc->max_pages_per_seq) * kPage + kPage - 1)
     return OSCAR_ERR_INVALID_ARG;
-  Kv8Plan pl;
-  if (!kv8_plan<kCode>(desc, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
-  if (workspace_bytes < pl.total) return OSCAR_ERR_WORKSPACE;
+  *work = true;
+  return OSCAR_OK;
+}
+
+// What the kernels take, for units of `entries` tiles of columns; info: bytes of the CTAs' records.
+inline Kv8Params attention_params(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,
+                                  const int32_t* q_pos, int32_t m_rows, int32_t max_seq_len, void* out,
+                                  void* workspace, int64_t tiles, int64_t entries, int cluster, int team, size_t info) {
   Kv8Params p{};
   p.hkv = desc->num_kv_heads;
   p.hq = desc->num_q_heads;
@@ -1172,14 +1117,29 @@ oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* se
   p.q_pos = q_pos;
   p.m_rows = m_rows;
   p.cols = m_rows * p.G;
-  p.tiles = static_cast<int>(pl.tiles);
-  p.entries = static_cast<int>(pl.entries);
+  p.tiles = static_cast<int>(tiles);
+  p.entries = static_cast<int>(entries);
   p.max_len = max_seq_len;
-  p.cluster = pl.cluster;
-  p.team = pl.team;
+  p.cluster = cluster;
+  p.team = team;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(desc->head_dim)));
   p.info = static_cast<int4*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.info);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + info);
+  return p;
+}
+
+template <int kCode>
+oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens, const int32_t* q_pos,
+                    int32_t batch, int32_t m_rows, int32_t max_seq_len, void* out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  bool work;
+  const oscar_status s = check_attention(desc, q, seq_lens, q_pos, batch, m_rows, max_seq_len, out, workspace, &work);
+  if (s != OSCAR_OK || !work) return s;
+  Kv8Plan pl;
+  if (!kv8_plan<kCode>(desc, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
+  if (workspace_bytes < pl.total) return OSCAR_ERR_WORKSPACE;
+  const Kv8Params p = attention_params(desc, q, seq_lens, q_pos, m_rows, max_seq_len, out, workspace, pl.tiles,
+                                       pl.entries, pl.cluster, pl.team, pl.info);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return desc->head_dim == 128 ? run_kv8<128, kCode>(p, pl, st) : run_kv8<64, kCode>(p, pl, st);
 }
