@@ -112,12 +112,13 @@ __device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPai
   s.l[1] = second(l);
 }
 
-// Two pages of codes, at st and st + kBlock, their tokens from page0[n] on; `there`: bit per page.
+// Two pages of codes, at st and st + kBlock, their tokens from first_token and first_token + step on; `there`: bit per page.
 template <int D, int NT>
-__device__ __forceinline__ void page_pair(const uint8_t* st, const int (&page0)[kPair], uint32_t there, int lane,
+__device__ __forceinline__ void page_pair(const uint8_t* st, int first_token, int step, uint32_t there, int lane,
                                           const Query<D> (&q)[NT], Running<D> (&s)[NT]) {
   using F = Kv4Fmt<D>;
   const int gid = lane >> 2, tig = lane & 3;
+  const int page0[kPair] = {first_token, first_token + step};
   // one that is not there is read as the other, and weighs nothing
   const uint8_t* at[kPair] = {st + (there & 1u ? 0 : F::kBlock), st + (there & 2u ? F::kBlock : 0)};
   float lg[NT][kPair][4];
@@ -218,43 +219,83 @@ __device__ __forceinline__ void page_pair(const uint8_t* st, const int (&page0)[
   }
 }
 
-// A warp's ring of copies, two pages a stage: as Ring, with two bits per stage in `shown` and a page's id in
-// each of the first two lanes.
-//
-// Asks for the pages pg and pg + step (those below end), and looks up the ids of the two behind them.
+// A warp's ring of copies, two pages a stage, a lane each.  Stages are used in turn, each when its step before
+// has been consumed; a stage's barrier counts two arrivals.
 template <typename C>
-__device__ __forceinline__ void issue_pair(const Kv8Params& p, const Entry& t, int h, int pg, int end, int step,
-                                           int lane, Ring& r) {
-  const int st = r.n_in % C::kStages, mine = pg + lane * step;
-  const bool have = lane < kPair && mine < end, ok = have && r.next_id >= 0 && r.next_id < p.n_pages;
-  const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-  if (have && !ok && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-  r.shown = (r.shown & ~(3u << (2 * st))) | (mask << (2 * st));
-  if (lane == 0) mbar_arrive_expect_tx(r.bars + st, __popc(mask) * C::F::kBlock);
-  __syncwarp();
-  if (ok)
-    bulk_g2s(r.base + st * C::kStage + lane * C::F::kBlock,
-             p.pool + (static_cast<int64_t>(r.next_id) * p.hkv + h) * C::F::kBlock, C::F::kBlock, r.bars + st);
-  ++r.n_in;
-  const int next = mine + kPair * step;
-  if (lane < kPair && next < end) r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + next];
-}
+struct Ring4 {
+  uint8_t* base;
+  uint64_t* bars;
+  int32_t* status;
+  uint32_t phases;         // bit per stage
+  uint32_t there;          // two bits per step in flight, the oldest lowest: pages whose copies were made
+  int at, flying;          // stage of the oldest step, steps in flight
+  bool alive;              // false after a copy that did not arrive in time
+  // lanes 0 and 1: their pages to come of the unit's part
+  const int32_t* ids;
+  int left, stride, next_id;
 
-template <typename C>
-__device__ __forceinline__ void start_pairs(const Kv8Params& p, const Entry& t, int h, const Part& a, int step,
-                                            int lane, Ring& r) {
-  r.tail_issued = false;
-  if (!r.alive) return;
-  if (a.first < a.end) {
-    const int mine = a.first + lane * step;
-    if (lane < kPair && mine < a.end) r.next_id = p.page_table[static_cast<size_t>(t.b) * p.max_pages + mine];
-#pragma unroll 1
-    for (int i = 0; i < C::kStages; ++i)
-      if (a.first + i * kPair * step < a.end) issue_pair<C>(p, t, h, a.first + i * kPair * step, a.end, step, lane, r);
-  } else if (a.tail) {
-    issue_tail<C>(p, t, h, lane, r);
+  static __device__ __forceinline__ int after(int st) { return st + 1 == C::kStages ? 0 : st + 1; }
+
+  // The next step, into the stage behind those in flight; `src` is the KV head's first block.
+  __device__ __forceinline__ void issue(const Kv8Params& p, const uint8_t* src, int st, int lane) {
+    bool ok = false;
+    if (lane < kPair) {
+      ok = left > 0 && next_id >= 0 && next_id < p.n_pages;
+      mbar_arrive_expect_tx(bars + st, ok ? C::F::kBlock : 0);
+      if (ok)
+        bulk_g2s(base + st * C::kStage + lane * C::F::kBlock,
+                 src + static_cast<int64_t>(next_id) * p.hkv * C::F::kBlock, C::F::kBlock, bars + st);
+      else if (left > 0 && status)
+        atomicOr(status, OSCAR_DEVERR_PAGE_ID);
+      ids += stride;
+      if (--left > 0) next_id = *ids;
+    }
+    there |= __ballot_sync(0xffffffffu, ok) << (2 * flying);
+    ++flying;
   }
-}
+  __device__ __forceinline__ void issue_tail(const Kv8Params& p, const Entry& t, int h, int lane) {
+    const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
+    const bool ok = id >= 0 && id < p.n_tails;
+    if (lane < kPair) {
+      mbar_arrive_expect_tx(bars + at, ok && lane == 0 ? C::F::kTailBytes : 0);
+      if (lane == 0) {
+        if (ok) bulk_g2s(base, p.tail + (id * p.hkv + h) * C::F::kTailBytes, C::F::kTailBytes, bars + at);
+        else if (status) atomicOr(status, OSCAR_DEVERR_PAGE_ID);
+      }
+    }
+    there = ok;
+    flying = 1;
+  }
+  // Starts a warp's part of a unit (nothing is in flight): as many steps as there are stages, or the tail.
+  __device__ __forceinline__ void start(const Kv8Params& p, const Entry& t, int h, const Part& a, int step, int lane) {
+    there = 0;
+    flying = 0;
+    if (!alive) return;
+    const int pages = a.first < a.end ? (a.end - a.first + step - 1) / step : 0;
+    ids = p.page_table + static_cast<size_t>(t.b) * p.max_pages + a.first + lane * step;
+    stride = kPair * step;
+    left = (pages - lane + 1) / kPair;   // (of lanes 0 and 1)
+    if (lane < kPair && left > 0) next_id = *ids;
+    const uint8_t* src = p.pool + static_cast<int64_t>(h) * C::F::kBlock;
+    int st = at;
+#pragma unroll 1
+    for (int i = 0; i < C::kStages && kPair * i < pages; ++i, st = after(st)) issue(p, src, st, lane);
+    if (pages == 0 && a.tail) issue_tail(p, t, h, lane);
+  }
+  // Waits for the oldest step and takes it off; which of its copies were made; ~0u: it did not come in time, and no
+  // copy is left in flight.
+  __device__ __forceinline__ uint32_t take() {
+    const bool got = wait_copy(bars + at, (phases >> at) & 1u, status);
+    phases ^= 1u << at;
+    const uint32_t mask = there & 3u;
+    there >>= 2;
+    --flying;
+    if (__all_sync(0xffffffffu, got)) return mask;
+    for (int st = after(at); flying > 0; --flying, st = after(st)) wait_longer(bars + st, (phases >> st) & 1u, status);
+    alive = false;
+    return ~0u;
+  }
+};
 
 // merge_cluster for NT tiles of 8 columns.
 template <int D, int NT>
@@ -308,7 +349,7 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   float* sm_l = sm_k + kWarps * kCols;
   float2* sm_unit = reinterpret_cast<float2*>(smem + C::kUnitOff) + number * kCols;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
-  if (tid < kWarps * C::kStages) mbar_init(bars + tid, 1);
+  if (tid < kWarps * C::kStages) mbar_init(bars + tid, kPair);
   fence_mbar_init();
   __syncthreads();
   pdl_wait();
@@ -348,12 +389,13 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     t = sh.t;
   }
 
-  Ring ring{smem + (tid >> 5) * C::kWarpRing, bars + (tid >> 5) * C::kStages, 0, 0, 0, 0, true, false};
+  Ring4<C> ring{smem + (tid >> 5) * C::kWarpRing, bars + (tid >> 5) * C::kStages, p.status, 0, 0, 0, 0, true,
+                nullptr, 0, 0, 0};
   int4 owned = make_int4(0, 0, 0, 0);
   int p0 = static_cast<int>(at - unit0);
   int p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
   Part mine = part_of(t, p0, p1, warp, team);
-  start_pairs<C>(p, t, h, mine, team, lane, ring);
+  ring.start(p, t, h, mine, team, lane);
 
   for (;;) {
     Query<D> q[NT];
@@ -372,27 +414,29 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
         atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
+    const uint8_t* src = p.pool + static_cast<int64_t>(h) * C::F::kBlock;
+    // (from start on, a step is issued for each that is taken, while there are more)
+    int left = mine.first < mine.end ? (mine.end - mine.first + kPair * team - 1) / (kPair * team) : 0;
+    bool tail_here = mine.tail && left == 0;
 #pragma unroll 1
-    for (int pg = mine.first; pg < mine.end && ring.alive; pg += kPair * team) {
-      int st;
-      if (!copied<C>(p, ring, st)) break;
-      const uint32_t there = (ring.shown >> (2 * st)) & 3u;
-      const int page0[kPair] = {pg * kPage, (pg + team) * kPage};
+    for (int page0 = mine.first * kPage; left > 0 && ring.alive; --left, page0 += kPair * team * kPage) {
+      const uint32_t there = ring.take();
+      if (there == ~0u) break;
       // (a refused id's stands for nothing)
-      if (there) page_pair<D, NT>(ring.base + st * C::kStage, page0, there, lane, q, s);
+      if (there) page_pair<D, NT>(ring.base + ring.at * C::kStage, page0, team * kPage, there, lane, q, s);
       __syncwarp();
-      if (pg + C::kStages * kPair * team < mine.end)
-        issue_pair<C>(p, t, h, pg + C::kStages * kPair * team, mine.end, team, lane, ring);
+      if (left > C::kStages) ring.issue(p, src, ring.at, lane);
+      ring.at = ring.after(ring.at);
     }
     if (mine.tail && ring.alive) {
-      if (!ring.tail_issued) issue_tail<C>(p, t, h, lane, ring);
-      int st;
-      if (copied<C>(p, ring, st) && ((ring.shown >> st) & 1u)) {
+      if (!tail_here) ring.issue_tail(p, t, h, lane);
+      if (ring.take() == 1u) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q[n], s[n]);
       }
       __syncwarp();
+      ring.at = ring.after(ring.at);
     }
 
     // the next unit of this CTA: its copies start before this one is merged
@@ -409,7 +453,7 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       p0 = 0;
       p1 = static_cast<int>(min(static_cast<int64_t>(t.pages), end - unit0));
       mine = part_of(t, p0, p1, warp, team);
-      start_pairs<C>(p, t, h, mine, team, lane, ring);
+      ring.start(p, t, h, mine, team, lane);
     }
 
     if (gid == 0) {
