@@ -18,24 +18,6 @@
 
 namespace oscar {
 
-// A lane's part of one block: kUnits chunks of 16 values, as packed bf16 pairs in
-// chunk order.  Keys: 16 channels of a token; values: 4 channels x 4 tokens.
-template <int D>
-struct Lane {
-  static constexpr int kUnits = D / 32;
-  // chunk u of this lane
-  static __device__ __forceinline__ void key(int lane, int u, int& t, int& cc) {
-    constexpr int kPer = D / 16;                 // chunks of a token: neighbouring lanes
-    t = lane / kPer + u * (32 / kPer);
-    cc = lane % kPer;
-  }
-  static __device__ __forceinline__ void value(int lane, int u, int& tg, int& cg) {
-    constexpr int kPer = D / 4;                  // channel groups of a row
-    tg = (lane + 32 * u) / kPer;
-    cg = (lane + 32 * u) % kPer;
-  }
-};
-
 // The 16 x D values of page pg (tokens before s.t0 from the tail, the others from
 // the rows) in chunk order.
 template <int D>
@@ -282,10 +264,10 @@ oscar_status oscar_kv8_place(const oscar_kv8_desc* desc, const void* k, const vo
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = desc->format == OSCAR_KV8_E4M3;
   if (desc->head_dim == 128)
-    return e4m3 ? launch_cache(kv8_place_kernel<128, true>, p, st)
-                : launch_cache(kv8_place_kernel<128, false>, p, st);
-  return e4m3 ? launch_cache(kv8_place_kernel<64, true>, p, st)
-              : launch_cache(kv8_place_kernel<64, false>, p, st);
+    return e4m3 ? launch_cache(kv8_place_kernel<128, true>, p, st, 2 * p.hkv)
+                : launch_cache(kv8_place_kernel<128, false>, p, st, 2 * p.hkv);
+  return e4m3 ? launch_cache(kv8_place_kernel<64, true>, p, st, 2 * p.hkv)
+              : launch_cache(kv8_place_kernel<64, false>, p, st, 2 * p.hkv);
 }
 
 oscar_status oscar_kv8_gather(const oscar_kv8_desc* desc, const int32_t* seq_lens,
@@ -300,10 +282,10 @@ oscar_status oscar_kv8_gather(const oscar_kv8_desc* desc, const int32_t* seq_len
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = desc->format == OSCAR_KV8_E4M3;
   if (desc->head_dim == 128)
-    return e4m3 ? launch_cache(kv8_gather_kernel<128, true>, p, st)
-                : launch_cache(kv8_gather_kernel<128, false>, p, st);
-  return e4m3 ? launch_cache(kv8_gather_kernel<64, true>, p, st)
-              : launch_cache(kv8_gather_kernel<64, false>, p, st);
+    return e4m3 ? launch_cache(kv8_gather_kernel<128, true>, p, st, 2 * p.hkv)
+                : launch_cache(kv8_gather_kernel<128, false>, p, st, 2 * p.hkv);
+  return e4m3 ? launch_cache(kv8_gather_kernel<64, true>, p, st, 2 * p.hkv)
+              : launch_cache(kv8_gather_kernel<64, false>, p, st, 2 * p.hkv);
 }
 
 }  // extern "C"

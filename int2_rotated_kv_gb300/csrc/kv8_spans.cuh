@@ -74,6 +74,24 @@ __device__ __forceinline__ uint16_t* tail_area(const Kv8CacheParams& p, int b, i
   return p.tail + ((id * p.hkv + h) * 2 + kv) * Kv8Fmt<D>::kTailHalf;
 }
 
+// A lane's part of one block: kUnits chunks of 16 values, as packed bf16 pairs in
+// chunk order.  Keys: 16 channels of a token; values: 4 channels x 4 tokens.
+template <int D>
+struct Lane {
+  static constexpr int kUnits = D / 32;
+  // chunk u of this lane
+  static __device__ __forceinline__ void key(int lane, int u, int& t, int& cc) {
+    constexpr int kPer = D / 16;                 // chunks of a token: neighbouring lanes
+    t = lane / kPer + u * (32 / kPer);
+    cc = lane % kPer;
+  }
+  static __device__ __forceinline__ void value(int lane, int u, int& tg, int& cg) {
+    constexpr int kPer = D / 4;                  // channel groups of a row
+    tg = (lane + 32 * u) / kPer;
+    cg = (lane + 32 * u) % kPer;
+  }
+};
+
 // Four rows of 4 channels (row r in w[2r], w[2r + 1]) <-> chunk order (channel x:
 // tokens 0..3 in w[2x], w[2x + 1]), as packed pairs of 16-bit values.
 __device__ __forceinline__ void transpose4(uint32_t (&w)[8]) {
@@ -112,10 +130,10 @@ __device__ __forceinline__ void store_tail(const Kv8CacheParams& p, const Span& 
 }
 
 template <typename Kern>
-oscar_status launch_cache(Kern kernel, const Kv8CacheParams& p, cudaStream_t st) {
+oscar_status launch_cache(Kern kernel, const Kv8CacheParams& p, cudaStream_t st, int units) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * static_cast<unsigned>(p.pages_per_seq),
-                     static_cast<unsigned>((2 * p.hkv + kCWarps - 1) / kCWarps));
+                     static_cast<unsigned>((units + kCWarps - 1) / kCWarps));   // a warp each
   cfg.blockDim = dim3(32 * kCWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
