@@ -22,14 +22,55 @@ namespace oscar {
 
 constexpr int kMaxNT = 3;      // tiles of 8 columns that share a page's operands
 constexpr int kPair = 2;       // pages of a step
+#ifndef WIDEWARPS
+#define WIDEWARPS 12
+#endif
+constexpr int kWideWarps = WIDEWARPS;
+
+// The columns of a tile (kv8_tiles.cuh's Query) in shared memory, for all warps of a CTA: where there are several
+// tiles, their operands would take the registers of a third of the warps.
+template <int D>
+struct SharedQuery {
+  uint2 b[D / 16][32];
+  float2 fac[32];
+  int2 vis[32];
+  int vis_min, pad[3];
+
+  __device__ __forceinline__ void put(const Query<D>& q, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) b[i][lane] = make_uint2(q.b[i][0], q.b[i][1]);
+    fac[lane] = make_float2(q.fac[0], q.fac[1]);
+    vis[lane] = make_int2(q.vis[0], q.vis[1]);
+    if (lane == 0) vis_min = q.vis_min;
+  }
+};
+// One tile's columns as the products see them: in registers, or there.
+template <int D, bool kShared>
+struct Columns;
+template <int D>
+struct Columns<D, false> : Query<D> {
+  __device__ __forceinline__ uint2 operand(int i, int) const { return make_uint2(this->b[i][0], this->b[i][1]); }
+  __device__ __forceinline__ float2 factors(int) const { return make_float2(this->fac[0], this->fac[1]); }
+  __device__ __forceinline__ int2 seen(int) const { return make_int2(this->vis[0], this->vis[1]); }
+  __device__ __forceinline__ int seen_least() const { return this->vis_min; }
+};
+template <int D>
+struct Columns<D, true> {
+  const SharedQuery<D>* q;
+  __device__ __forceinline__ uint2 operand(int i, int lane) const { return q->b[i][lane]; }
+  __device__ __forceinline__ float2 factors(int lane) const { return q->fac[lane]; }
+  __device__ __forceinline__ int2 seen(int lane) const { return q->vis[lane]; }
+  __device__ __forceinline__ int seen_least() const { return q->vis_min; }
+};
 
 template <int D, int NT, Kv8Mode kMode>
 struct Kv4Cfg {
   using F = Kv4Fmt<D>;
-  static constexpr int kWarps = kMode == kCluster && NT == 1 ? 16 : 8;
+  static constexpr int kWarps = NT > 1 ? kWideWarps : kMode == kCluster ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kAtOnce = NT < 3 ? kPair : 1;        // pages whose logits are in registers
   static constexpr int kCtas = NT == 1 && kMode != kCluster ? 2 : 1;   // per SM
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 2 : 3) : 4;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kStage = kPair * F::kBlock;
   static constexpr int kWarpRing = kStages * kStage;
   static constexpr int kStride = D + 4;                     // floats per column when merging
@@ -39,21 +80,27 @@ struct Kv4Cfg {
   static constexpr int kStatOff = kMergeOff + kMerge;
   static constexpr int kUnitOff = kStatOff + 3 * kStat;     // float2: units that the parts are brought to
   static constexpr int kPartOff = kUnitOff + kWarps * 8 * NT * 8;   // a cluster's CTA: its partial
-  static constexpr int kBarOff = kPartOff + (kMode == kCluster ? kv8_slot<D, NT>() * 4 : 0);
-  static constexpr int kBytes = kBarOff + kWarps * kStages * 8;
+  static constexpr int kQueryOff = kPartOff + (kMode == kCluster ? kv8_slot<D, NT>() * 4 : 0);
+  static constexpr int kBarOff = kQueryOff + (NT > 1 ? NT * static_cast<int>(sizeof(SharedQuery<D>)) : 0);
+  // The tail's block goes to where the parts are merged later, so that it comes while the pages do; a team's share of that
+  // may be smaller, and its tail takes the ring when the pages are through.
+  static constexpr bool kTailApart = kMode != kTeams;
+  static constexpr int kTailBar = kBarOff + kWarps * kStages * 8;
+  static constexpr int kBytes = kTailBar + kWarps * 8;   // a warp each
+  static_assert(kMerge >= F::kTailBytes || !kTailApart, "a tail block fits where parts are merged");
   static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
   static_assert(kStage % 16 == 0 && kMergeOff % 16 == 0 && kUnitOff % 16 == 0 && kPartOff % 16 == 0, "alignment");
 };
 
-// weigh (kv8_tiles.cuh) for the tokens of two pages: logits lg[n] in the accumulator layout, value scales 2^off[n].
-template <int D>
-__device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPair][4], const float (&off)[kPair],
-                                           float (&w)[kPair][4]) {
-  float e[kPair][4], up[kPair][2];
+// weigh (kv8_tiles.cuh) for the tokens of N pages: logits lg[n] in the accumulator layout, value scales 2^off[n].
+template <int D, int N>
+__device__ __forceinline__ void weigh_pages(Running<D>& s, const float (&lg)[N][4], const float (&off)[N],
+                                            float (&w)[N][4]) {
+  float e[N][4], up[N][2];
   bool over = false;
   const uint64_t less = two(-1.f, -1.f), m2 = two(s.m[0], s.m[1]), k2 = two(s.k[0], s.k[1]);
 #pragma unroll
-  for (int n = 0; n < kPair; ++n) {
+  for (int n = 0; n < N; ++n) {
     const uint64_t e0 = fma2(m2, less, two(lg[n][0], lg[n][1])), e1 = fma2(m2, less, two(lg[n][2], lg[n][3]));
     const uint64_t u2 = fma2(k2, less, two(off[n], off[n]));
     e[n][0] = first(e0); e[n][1] = second(e0); e[n][2] = first(e1); e[n][3] = second(e1);
@@ -64,9 +111,9 @@ __device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPai
   if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float top[kPair], m = s.m[c];
+      float top[N], m = s.m[c];
 #pragma unroll
-      for (int n = 0; n < kPair; ++n) {
+      for (int n = 0; n < N; ++n) {
         top[n] = fmaxf(lg[n][c], lg[n][2 + c]);
         top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 4));
         top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 8));
@@ -77,13 +124,13 @@ __device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPai
       // the unit as it is, seen from m; and what these pages need
       float k = fmaxf(k0, kNoUnit.k);
 #pragma unroll
-      for (int n = 0; n < kPair; ++n) k = fmaxf(k, top[n] - m + off[n] - kLift);
+      for (int n = 0; n < N; ++n) k = fmaxf(k, top[n] - m + off[n] - kLift);
       s.l[c] *= fast_exp2(down);
       const float a = fast_exp2(k0 - k);
       s.m[c] = m;
       s.k[c] = k;
 #pragma unroll
-      for (int n = 0; n < kPair; ++n) {
+      for (int n = 0; n < N; ++n) {
         e[n][c] = lg[n][c] - m;
         e[n][2 + c] = lg[n][2 + c] - m;
         up[n][c] = off[n] - k;
@@ -97,7 +144,7 @@ __device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPai
   }
   uint64_t l = two(s.l[0], s.l[1]);
 #pragma unroll
-  for (int n = 0; n < kPair; ++n) {
+  for (int n = 0; n < N; ++n) {
     // (finite: it meets p of 0 where it is large)
     const uint64_t scale = two(fast_exp2(fminf(up[n][0], 126.f)), fast_exp2(fminf(up[n][1], 126.f)));
     const uint64_t p0 = two(fast_exp2(e[n][0]), fast_exp2(e[n][1])), p1 = two(fast_exp2(e[n][2]), fast_exp2(e[n][3]));
@@ -112,19 +159,23 @@ __device__ __forceinline__ void weigh_pair(Running<D>& s, const float (&lg)[kPai
   s.l[1] = second(l);
 }
 
-// Two pages of codes, at st and st + kBlock, their tokens from first_token and first_token + step on; `there`: bit per page.
-template <int D, int NT>
-__device__ __forceinline__ void page_pair(const uint8_t* st, int first_token, int step, uint32_t there, int lane,
-                                          const Query<D> (&q)[NT], Running<D> (&s)[NT]) {
+// N pages of codes, at st and kBlock on, their tokens from first_token and first_token + step on; `there`: bit per page.
+template <int D, int NT, int N>
+__device__ __forceinline__ void take_pages(const uint8_t* st, int first_token, int step, uint32_t there, int lane,
+                                          const Columns<D, (NT > 1)> (&q)[NT], Running<D> (&s)[NT]) {
   using F = Kv4Fmt<D>;
   const int gid = lane >> 2, tig = lane & 3;
-  const int page0[kPair] = {first_token, first_token + step};
-  // one that is not there is read as the other, and weighs nothing
-  const uint8_t* at[kPair] = {st + (there & 1u ? 0 : F::kBlock), st + (there & 2u ? F::kBlock : 0)};
-  float lg[NT][kPair][4];
-  float off[kPair], sk[kPair];
+  int page0[N];
+  const uint8_t* at[N];
 #pragma unroll
-  for (int n = 0; n < kPair; ++n) {
+  for (int n = 0; n < N; ++n) {   // one that is not there is read as the other, and weighs nothing
+    page0[n] = first_token + n * step;
+    at[n] = N == 1 || ((there >> n) & 1u) ? st + n * F::kBlock : st + (1 - n) * F::kBlock;
+  }
+  float lg[NT][N][4];
+  float off[N], sk[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
     const float2 sc = *reinterpret_cast<const float2*>(at[n] + F::kScales);
     sk[n] = sc.x;
     off[n] = fast_log2(sc.y);   // (a page of zeros: -inf, weights of 0)
@@ -134,7 +185,7 @@ __device__ __forceinline__ void page_pair(const uint8_t* st, int first_token, in
 #pragma unroll
   for (int j = 0; j < D / 64; ++j) {
 #pragma unroll
-    for (int n = 0; n < kPair; ++n) {
+    for (int n = 0; n < N; ++n) {
       const uint4 k = reinterpret_cast<const uint4*>(at[n])[32 * j + lane];   // tokens 2 gid, 2 gid + 1
       const uint4 sc = reinterpret_cast<const uint4*>(at[n] + F::kKeyScales)[4 * j + tig];
       const uint32_t t0[2] = {k.x, k.y}, t1[2] = {k.z, k.w}, s4[4] = {sc.x, sc.y, sc.z, sc.w};
@@ -152,38 +203,40 @@ __device__ __forceinline__ void page_pair(const uint8_t* st, int first_token, in
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint32_t (&qb)[D / 16][2] = q[t].b;
-          mma_f16(lg[t][n], a[0], b[0], a[1], b[1], qb[4 * j + 2 * w][0], qb[4 * j + 2 * w][1]);
-          mma_f16(lg[t][n], a[2], b[2], a[3], b[3], qb[4 * j + 2 * w + 1][0], qb[4 * j + 2 * w + 1][1]);
+          const uint2 q0 = q[t].operand(4 * j + 2 * w, lane), q1 = q[t].operand(4 * j + 2 * w + 1, lane);
+          mma_f16(lg[t][n], a[0], b[0], a[1], b[1], q0.x, q0.y);
+          mma_f16(lg[t][n], a[2], b[2], a[3], b[3], q1.x, q1.y);
         }
       }
     }
   }
-  uint32_t wb[NT][kPair][2];
+  uint32_t wb[NT][N][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    const float2 fac = q[t].factors(lane);
 #pragma unroll
-    for (int n = 0; n < kPair; ++n) {
-      const float f0 = logit_factor(sk[n], q[t].fac[0]), f1 = logit_factor(sk[n], q[t].fac[1]);
+    for (int n = 0; n < N; ++n) {
+      const float f0 = logit_factor(sk[n], fac.x), f1 = logit_factor(sk[n], fac.y);
       // (rounded by themselves, not on the way to a difference, so that equal logits stay equal)
 #pragma unroll
       for (int r = 0; r < 4; ++r) lg[t][n][r] = __fmul_rn(lg[t][n][r], r & 1 ? f1 : f0);
-      if (page0[n] + kPage > q[t].vis_min || !((there >> n) & 1u)) {
+      if (page0[n] + kPage > q[t].seen_least() || (N > 1 && !((there >> n) & 1u))) {
         const int tk = page0[n] + 2 * gid;
+        const int2 seen = q[t].seen(lane);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int vis = (there >> n) & 1u ? q[t].vis[c] : 0;
+          const int vis = N == 1 || ((there >> n) & 1u) ? (c ? seen.y : seen.x) : 0;
           if (tk >= vis) lg[t][n][c] = -INFINITY;
           if (tk + 1 >= vis) lg[t][n][2 + c] = -INFINITY;
         }
       }
     }
-    float w[kPair][4];
-    weigh_pair<D>(s[t], lg[t], off, w);
+    float w[N][4];
+    weigh_pages<D, N>(s[t], lg[t], off, w);
     // rows gid of the logits were tokens 2 gid and 2 gid + 1: transposed and put in order, the two
     // registers hold tokens (4tig, 4tig + 1) and (4tig + 2, 4tig + 3) of column gid
 #pragma unroll
-    for (int n = 0; n < kPair; ++n) {
+    for (int n = 0; n < N; ++n) {
       const uint32_t b0 = movmatrix_trans(pack_half2(w[n][0], w[n][1]));
       const uint32_t b1 = movmatrix_trans(pack_half2(w[n][2], w[n][3]));
       wb[t][n][0] = __byte_perm(b0, b1, 0x5410);
@@ -193,7 +246,7 @@ __device__ __forceinline__ void page_pair(const uint8_t* st, int first_token, in
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
 #pragma unroll
-    for (int n = 0; n < kPair; ++n) {
+    for (int n = 0; n < N; ++n) {
       // channels 64i + 4 gid and on, 64i + 32 + 4 gid and on, of tokens 4 tig and on
       const uint4 v = reinterpret_cast<const uint4*>(at[n] + F::kCodes)[32 * i + lane];
       const uint2 sc = reinterpret_cast<const uint2*>(at[n] + F::kValueScales)[8 * i + 4 * (gid >> 2) + tig];
@@ -280,7 +333,7 @@ struct Ring4 {
     int st = at;
 #pragma unroll 1
     for (int i = 0; i < C::kStages && kPair * i < pages; ++i, st = after(st)) issue(p, src, st, lane);
-    if (pages == 0 && a.tail) issue_tail(p, t, h, lane);
+    if (!C::kTailApart && pages == 0 && a.tail) issue_tail(p, t, h, lane);
   }
   // Waits for the oldest step and takes it off; which of its copies were made; ~0u: it did not come in time, and no
   // copy is left in flight.
@@ -349,7 +402,10 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   float* sm_l = sm_k + kWarps * kCols;
   float2* sm_unit = reinterpret_cast<float2*>(smem + C::kUnitOff) + number * kCols;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
+  uint64_t* tail_bar = reinterpret_cast<uint64_t*>(smem + C::kTailBar) + (tid >> 5);
+  uint32_t tail_phase = 0;
   if (tid < kWarps * C::kStages) mbar_init(bars + tid, kPair);
+  if (lane == 0) mbar_init(tail_bar, 1);
   fence_mbar_init();
   __syncthreads();
   pdl_wait();
@@ -398,13 +454,23 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   ring.start(p, t, h, mine, team, lane);
 
   for (;;) {
-    Query<D> q[NT];
+    Columns<D, (NT > 1)> q[NT];
     Running<D> s[NT];
+    if constexpr (NT > 1) {   // a warp a tile, for all
+      SharedQuery<D>* shared = reinterpret_cast<SharedQuery<D>*>(smem + C::kQueryOff);
+      if (warp < NT) {
+        Query<D> one;
+        load_query<D, kCodeE2m1>(p, t, h, t.tile * kCols + 8 * warp, lane, one);
+        shared[warp].put(one, lane);
+      }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      load_query<D, kCodeE2m1>(p, t, h, t.tile * kCols + 8 * n, lane, q[n]);
-      reset<D>(s[n]);
+      for (int n = 0; n < NT; ++n) q[n].q = shared + n;
+      __syncthreads();
+    } else {
+      load_query<D, kCodeE2m1>(p, t, h, t.tile * kCols, lane, q[0]);
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) reset<D>(s[n]);
     if (p0 == 0 && h == 0 && t.tile == 0 && warp == 0 && lane == 0 && p.status) {
       const int len = p.seq_lens[t.b];
       if (len < 0 || len > p.max_len) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
@@ -413,6 +479,20 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const int row = (t.tile * kCols + lane) / p.G;
       if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
         atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
+    }
+    bool tail_there = false;
+    const bool tail_asked = C::kTailApart && mine.tail && ring.alive;
+    if (tail_asked) {
+      const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
+      tail_there = id >= 0 && id < p.n_tails;
+      if (lane == 0) {
+        fence_proxy_async();   // (parts of the unit before were read there)
+        mbar_arrive_expect_tx(tail_bar, tail_there ? C::F::kTailBytes : 0);
+        if (tail_there)
+          bulk_g2s(smem + C::kMergeOff, p.tail + (id * p.hkv + h) * C::F::kTailBytes, C::F::kTailBytes, tail_bar);
+        else if (p.status)
+          atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+      }
     }
     const uint8_t* src = p.pool + static_cast<int64_t>(h) * C::F::kBlock;
     // (from start on, a step is issued for each that is taken, while there are more)
@@ -423,20 +503,43 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       const uint32_t there = ring.take();
       if (there == ~0u) break;
       // (a refused id's stands for nothing)
-      if (there) page_pair<D, NT>(ring.base + ring.at * C::kStage, page0, team * kPage, there, lane, q, s);
+      const uint8_t* st = ring.base + ring.at * C::kStage;
+      if constexpr (C::kAtOnce == kPair) {
+        if (there) take_pages<D, NT, kPair>(st, page0, team * kPage, there, lane, q, s);
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < kPair; ++n)
+          if ((there >> n) & 1u) take_pages<D, NT, 1>(st + n * C::F::kBlock, page0 + n * team * kPage, 0, 1u, lane, q, s);
+      }
       __syncwarp();
       if (left > C::kStages) ring.issue(p, src, ring.at, lane);
       ring.at = ring.after(ring.at);
     }
-    if (mine.tail && ring.alive) {
-      if (!tail_here) ring.issue_tail(p, t, h, lane);
-      if (ring.take() == 1u) {
+    if (tail_asked || (!C::kTailApart && mine.tail && ring.alive)) {
+      const uint8_t* block = ring.base;
+      if constexpr (C::kTailApart) {
+        const bool got = __all_sync(0xffffffffu, wait_copy(tail_bar, tail_phase, p.status));
+        tail_phase ^= 1u;
+        ring.alive = ring.alive && got;
+        tail_there = tail_there && got;
+        block = smem + C::kMergeOff;
+      } else {
+        if (!tail_here) ring.issue_tail(p, t, h, lane);
+        tail_there = ring.take() == 1u;
+        ring.at = ring.after(ring.at);
+      }
+      if (tail_there) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, ring.base, t.len / kPage * kPage, t.len % kPage, lane, q[n], s[n]);
+        for (int n = 0; n < NT; ++n) {
+          Query<D> seen;   // (of which only this is looked at)
+          const int2 vis = q[n].seen(lane);
+          seen.vis[0] = vis.x;
+          seen.vis[1] = vis.y;
+          seen.vis_min = q[n].seen_least();
+          tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, block, t.len / kPage * kPage, t.len % kPage, lane, seen, s[n]);
+        }
       }
       __syncwarp();
-      ring.at = ring.after(ring.at);
     }
 
     // the next unit of this CTA: its copies start before this one is merged
