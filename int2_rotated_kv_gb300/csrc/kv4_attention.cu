@@ -22,10 +22,9 @@ namespace oscar {
 
 constexpr int kMaxNT = 3;      // tiles of 8 columns that share a page's operands
 constexpr int kPair = 2;       // pages of a step
-#ifndef WIDEWARPS
-#define WIDEWARPS 12
-#endif
-constexpr int kWideWarps = WIDEWARPS;
+
+// CTAs per SM that divide the pages among them.
+__host__ __device__ constexpr int kv4_share_ctas(int nt) { return nt == 1 ? 2 : 3; }
 
 // The columns of a tile (kv8_tiles.cuh's Query) in shared memory, for all warps of a CTA: where there are several
 // tiles, their operands would take the registers of a third of the warps.
@@ -63,13 +62,25 @@ struct Columns<D, true> {
   __device__ __forceinline__ int seen_least() const { return q->vis_min; }
 };
 
+// A CTA's walk over its share of the units, as a warp keeps it in shared memory while the pages are in hand: in registers
+// it would push others out of the loop.
+struct Kv4Walk {
+  int64_t unit0, end, share;   // first page of the current unit, end of the share, its size
+  int4 owned;
+  Entry t;
+  int e, h, p0, p1;
+};
+
 template <int D, int NT, Kv8Mode kMode>
 struct Kv4Cfg {
   using F = Kv4Fmt<D>;
-  static constexpr int kWarps = NT > 1 ? kWideWarps : kMode == kCluster ? 16 : 8;
+  // (Shares of several column tiles by small CTAs: while one of them changes units, which takes 10 us of 12 warps
+  // and three tiles, the SM's others go on.  64 sequences x 5 rows over 2000-4000 tokens 134 us for 180; of one
+  // tile, 101 us both.)
+  static constexpr int kWarps = kMode == kShares ? (NT > 1 ? 4 : 8) : kMode == kTeams ? 8 : NT > 1 ? 12 : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kAtOnce = NT < 3 ? kPair : 1;        // pages whose logits are in registers
-  static constexpr int kCtas = NT == 1 && kMode != kCluster ? 2 : 1;   // per SM
+  static constexpr int kCtas = kMode == kShares ? kv4_share_ctas(NT) : kMode == kTeams ? 2 : 1;   // per SM
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kStage = kPair * F::kBlock;
   static constexpr int kWarpRing = kStages * kStage;
@@ -86,7 +97,8 @@ struct Kv4Cfg {
   // may be smaller, and its tail takes the ring when the pages are through.
   static constexpr bool kTailApart = kMode != kTeams;
   static constexpr int kTailBar = kBarOff + kWarps * kStages * 8;
-  static constexpr int kBytes = kTailBar + kWarps * 8;   // a warp each
+  static constexpr int kWalk = (kTailBar + 8 + 15) / 16 * 16;   // a warp each
+  static constexpr int kBytes = kWalk + (kMode == kShares ? kWarps * static_cast<int>(sizeof(Kv4Walk)) : 0);
   static_assert(kMerge >= F::kTailBytes || !kTailApart, "a tail block fits where parts are merged");
   static_assert(kWarpRing >= F::kTailBytes, "a warp's ring holds a tail block");
   static_assert(kStage % 16 == 0 && kMergeOff % 16 == 0 && kUnitOff % 16 == 0 && kPartOff % 16 == 0, "alignment");
@@ -402,10 +414,10 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
   float* sm_l = sm_k + kWarps * kCols;
   float2* sm_unit = reinterpret_cast<float2*>(smem + C::kUnitOff) + number * kCols;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff) + number * team * 8 * C::kStride;
-  uint64_t* tail_bar = reinterpret_cast<uint64_t*>(smem + C::kTailBar) + (tid >> 5);
+  uint64_t* tail_bar = reinterpret_cast<uint64_t*>(smem + C::kTailBar);
   uint32_t tail_phase = 0;
   if (tid < kWarps * C::kStages) mbar_init(bars + tid, kPair);
-  if (lane == 0) mbar_init(tail_bar, 1);
+  if (tid == 0) mbar_init(tail_bar, 1);
   fence_mbar_init();
   __syncthreads();
   pdl_wait();
@@ -480,12 +492,14 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (row < p.m_rows && p.q_pos[static_cast<size_t>(t.b) * p.m_rows + row] >= t.len)
         atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
     }
+    // the tail's block, for all warps: each takes a tile of its columns, those with the fewest pages
     bool tail_there = false;
-    const bool tail_asked = C::kTailApart && mine.tail && ring.alive;
+    const bool tail_asked = C::kTailApart && p1 > t.n8 && t.vis > t.len / kPage * kPage;
+    const int tail_tile = tail_asked ? (warp + kWarps - (max(t.n8, p0) - p0) % kWarps) % kWarps : kWarps;
     if (tail_asked) {
       const int64_t id = p.tail_ids ? p.tail_ids[t.b] : t.b;
       tail_there = id >= 0 && id < p.n_tails;
-      if (lane == 0) {
+      if (tid == 0) {
         fence_proxy_async();   // (parts of the unit before were read there)
         mbar_arrive_expect_tx(tail_bar, tail_there ? C::F::kTailBytes : 0);
         if (tail_there)
@@ -493,6 +507,10 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
         else if (p.status)
           atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
       }
+    }
+    Kv4Walk* walk = reinterpret_cast<Kv4Walk*>(smem + C::kWalk) + (tid >> 5);
+    if constexpr (kMode == kShares) {
+      if (lane == 0) *walk = {unit0, end, share, owned, t, e, h, p0, p1};
     }
     const uint8_t* src = p.pool + static_cast<int64_t>(h) * C::F::kBlock;
     // (from start on, a step is issued for each that is taken, while there are more)
@@ -515,32 +533,45 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       if (left > C::kStages) ring.issue(p, src, ring.at, lane);
       ring.at = ring.after(ring.at);
     }
-    if (tail_asked || (!C::kTailApart && mine.tail && ring.alive)) {
-      const uint8_t* block = ring.base;
-      if constexpr (C::kTailApart) {
+    if constexpr (kMode == kShares) {
+      __syncwarp();
+      asm volatile("" ::: "memory");   // (from there)
+      unit0 = walk->unit0;
+      end = walk->end;
+      share = walk->share;
+      owned = walk->owned;
+      t = walk->t;
+      e = walk->e;
+      h = walk->h;
+      p0 = walk->p0;
+      p1 = walk->p1;
+    }
+    const uint8_t* tail_block = ring.base;
+    if constexpr (C::kTailApart) {
+      if (tail_asked) {
         const bool got = __all_sync(0xffffffffu, wait_copy(tail_bar, tail_phase, p.status));
         tail_phase ^= 1u;
-        ring.alive = ring.alive && got;
         tail_there = tail_there && got;
-        block = smem + C::kMergeOff;
-      } else {
-        if (!tail_here) ring.issue_tail(p, t, h, lane);
-        tail_there = ring.take() == 1u;
-        ring.at = ring.after(ring.at);
       }
-      if (tail_there) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          Query<D> seen;   // (of which only this is looked at)
-          const int2 vis = q[n].seen(lane);
-          seen.vis[0] = vis.x;
-          seen.vis[1] = vis.y;
-          seen.vis_min = q[n].seen_least();
-          tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, block, t.len / kPage * kPage, t.len % kPage, lane, seen, s[n]);
-        }
-      }
-      __syncwarp();
+      tail_block = smem + C::kMergeOff;
+    } else if (mine.tail && ring.alive) {
+      if (!tail_here) ring.issue_tail(p, t, h, lane);
+      tail_there = ring.take() == 1u;
+      ring.at = ring.after(ring.at);
     }
+    if (tail_there) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (C::kTailApart && n != tail_tile) continue;
+        Query<D> seen;   // (of which only this is looked at)
+        const int2 vis = q[n].seen(lane);
+        seen.vis[0] = vis.x;
+        seen.vis[1] = vis.y;
+        seen.vis_min = q[n].seen_least();
+        tail_tokens<D>(p, t, h, t.tile * kCols + 8 * n, tail_block, t.len / kPage * kPage, t.len % kPage, lane, seen, s[n]);
+      }
+    }
+    __syncwarp();
 
     // the next unit of this CTA: its copies start before this one is merged
     const Entry tc = t;
@@ -647,18 +678,25 @@ struct Kv4Plan {
 
 // CTAs that share the pages of `units`.
 inline int64_t share_ctas4(int nt, int64_t units, int64_t pages, int64_t sms) {
-  return std::min(std::min<int64_t>(kMaxCtas, nt == 1 ? 2 * sms : sms), (units * pages + kMinShare - 1) / kMinShare);
+  return std::min(std::min<int64_t>(kMaxCtas, kv4_share_ctas(nt) * sms), (units * pages + kMinShare - 1) / kMinShare);
 }
 
-// Estimates in us, as kv8_plan's.
+// Estimates in us of nt column tiles, fitted to what is measured below (kv8_plan says what they stand for).  A page
+// costs d = 64 two thirds of what it costs d = 128.
+inline double page_us4(int d) { return 0.35 + 0.65 / 128 * d; }
 inline double shares_us4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
-  return 6.0 + (0.00028 + 0.00010 * nt) / 128 * (d + 16) * visited(batch, units, pages);
+  const double start[] = {12, 15, 21}, page[] = {0.000456, 0.00066, 0.0009}, unit[] = {0.015, 0.02, 0.05};
+  return start[nt - 1] + page[nt - 1] * page_us4(d) * visited(batch, units, pages) + unit[nt - 1] * static_cast<double>(units);
 }
 inline double cluster_us4(int d, int nt, int64_t pages, int c) {
-  return (0.03 + 0.015 * nt) / 128 * (d + 16) * static_cast<double>(pages) / c;
+  const double start[] = {7, 8, 8}, page[] = {0.063, 0.095, 0.115};
+  return start[nt - 1] + page[nt - 1] * page_us4(d) * static_cast<double>(pages) / c;
+}
+inline double team_us4(int d, int64_t units, int64_t pages, int64_t sms) {
+  return 7 + 0.095 * page_us4(d) * static_cast<double>(units) * static_cast<double>(pages) / static_cast<double>(sms);
 }
 inline double rows_us4(int d, int64_t batch, int64_t units, int64_t pages, int64_t sms) {
-  return rows_us(d, batch, units, pages, sms);
+  return rows_us(d, batch, units, pages, sms) - 0.00008 / 128 * d * visited(batch, units, pages);
 }
 
 inline int cluster_of4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
@@ -687,9 +725,14 @@ inline bool kv4_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
     x.nt = nt;
     x.tiles = (tiles8 + nt - 1) / nt;
     const int64_t units = batch * x.tiles * h;
-    if (nt == 1) x.team = team_of(units, pages, sms);
-    if (!x.team) x.cluster = cluster_of4(d, nt, batch, units, pages);
-    const double us = x.cluster ? 6.0 + cluster_us4(d, nt, pages, x.cluster) : shares_us4(d, nt, batch, units, pages);
+    x.cluster = cluster_of4(d, nt, batch, units, pages);
+    double us = x.cluster ? cluster_us4(d, nt, pages, x.cluster) : shares_us4(d, nt, batch, units, pages);
+    const int team = nt == 1 ? team_of(units, pages, sms) : 0;
+    if (team && team_us4(d, units, pages, sms) < us) {
+      us = team_us4(d, units, pages, sms);
+      x.team = team;
+      x.cluster = 0;
+    }
     if (nt == 1 || us < best) {
       best = us;
       p = x;

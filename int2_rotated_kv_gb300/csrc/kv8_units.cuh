@@ -203,7 +203,7 @@ struct Share {
 template <int NT, int kWarps>
 __device__ __forceinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
   // threads of an entry, for its rows' positions; entries at a time
-  constexpr int kLanes = NT > 2 ? 8 : 1, kAtOnce = 32 * kWarps / kLanes;
+  constexpr int kLanes = NT > 4 ? 8 : 1, kAtOnce = 32 * kWarps / kLanes;
   __shared__ int64_t scratch[kWarps];
   __shared__ Entry found;
   __shared__ int found_number;
