@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(32 * kCWarps, kGatherCtas) kv4_gather_kernel(c
     report(p, OSCAR_DEVERR_SEQ_LEN);
     return;
   }
-  if (pg * kPage >= s.t1) return;
+  if (pg > (s.t1 - 1) / kPage) return;
   const int lo = max(s.t0 - pg * kPage, 0), hi = min(s.t1 - pg * kPage, kPage);
   const int64_t first = ((s.r0 + (static_cast<int64_t>(pg) * kPage - s.t0)) * p.hkv + h) * D;
   const int64_t stride = static_cast<int64_t>(p.hkv) * D;

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * kCWarps) kv8_gather_kernel(const __grid_c
     report(p, OSCAR_DEVERR_SEQ_LEN);
     return;
   }
-  if (pg * kPage >= s.t1) return;
+  if (pg > (s.t1 - 1) / kPage) return;
   const int lo = max(s.t0 - pg * kPage, 0), hi = min(s.t1 - pg * kPage, kPage);
   const uint8_t* blk = nullptr;
   const uint16_t* tail = nullptr;

@@ -43,7 +43,7 @@ __device__ __forceinline__ bool span_of(const Kv8CacheParams& p, int b, Span& s)
   const int r0 = p.row_starts[b], r1 = p.row_starts[b + 1], t0 = p.first[b];
   const int64_t n = static_cast<int64_t>(r1) - r0;
   if (n == 0) return false;
-  if (n < 0 || n > p.max_rows || r0 < 0 || r1 > p.total_rows || t0 < 0 ||
+  if (n < 0 || n > p.max_rows || r0 < 0 || r1 > p.total_rows || t0 < 0 || t0 + n > 0x7fffffff ||
       t0 + n > static_cast<int64_t>(p.max_pages) * kPage + kPage - 1) {
     report(p, OSCAR_DEVERR_SEQ_LEN);
     return false;
@@ -151,13 +151,13 @@ inline oscar_status cache_params(const oscar_kv8_desc* c, const int32_t* first, 
   if (batch == 0 || total_rows == 0 || max_rows == 0) return OSCAR_OK;
   if (!first || !row_starts) return OSCAR_ERR_INVALID_ARG;
   if (total_rows > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;   // row_starts are int32
-  // pages that max_rows consecutive positions can touch
-  const int64_t pages = (static_cast<int64_t>(max_rows) + kPage - 2) / kPage + 1;
-  if (pages * batch > 0x7fffffff || c->num_kv_heads > kCWarps * 65535 / 2) return OSCAR_ERR_UNSUPPORTED;
+  // pages that so many consecutive positions can touch
+  const auto pages = [](int64_t rows) { return (rows + kPage - 2) / kPage + 1; };
+  if (pages(max_rows) * batch > 0x7fffffff || c->num_kv_heads > kCWarps * 65535 / 2) return OSCAR_ERR_UNSUPPORTED;
   p->hkv = c->num_kv_heads;
   p->max_pages = c->max_pages_per_seq;
   p->batch = batch;
-  p->pages_per_seq = static_cast<int>(pages);
+  p->pages_per_seq = static_cast<int>(pages(std::min<int64_t>(max_rows, total_rows)));   // (no sequence has more)
   p->max_rows = max_rows;
   p->n_pages = c->num_pages;
   p->n_tails = c->num_tails;

@@ -505,3 +505,20 @@ def test_binding_refuses_tensors():
         L.oscar_kv4_gather(s.cache, i[:2], i[:2], i, 3, k[:, :, :32], k)
     with pytest.raises(L.OscarError):
         L.oscar_kv4_attention(s.cache, q, i[:2], 0, q, ws)
+
+
+@pytest.mark.parametrize("most", [(1 << 31) - 1, (1 << 31) - 20])
+def test_a_bound_of_rows_that_says_nothing(most):
+    """max_new and max_rows of all that an int32 holds: the rows that there are bound the work."""
+    t, L = H.torch(), H.lib()
+    s = K.Sequences(1, 3, 3, 64, 400, seed=4)
+    s.place([21], max_new=most)
+    s.place([302], max_new=most)
+    s.check_pools()
+    k, v = (t.full((325, 3, 64), 7.0, dtype=t.bfloat16, device=H.DEV) for _ in range(2))
+    L.oscar_kv4_gather(s.cache, s.i32([323]), s.i32([5]), s.i32([0, 318]), most, k, v)
+    for h in range(3):
+        for got, want in zip((k, v), s.stored(0, h)):
+            np.testing.assert_array_equal(H.from_bf16(got)[:318, h], synth.bf16_round(want[5:].astype(np.float32)))
+    assert (k[318:] == 7).all() and (v[318:] == 7).all()
+    assert H.status(s.cache) == 0
