@@ -514,10 +514,12 @@ def oscar_gather(cache: Cache, seq_lens, first, row_starts, max_rows: int, k_out
         raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1")
     if shape != cache.bf16_page_table.shape or len(shape) != 2 or batch > shape[0]:
         raise ValueError(f"{fn}: the page tables must have the same shape, and a row per sequence")
-    for name in ("bf16_pool", "r_k", "r_v"):
+    for name, size in (("int2_pool", 1), ("bf16_pool", 2), ("r_k", 4), ("r_v", 4)):
         t = getattr(cache, name)
-        if t is None or t.get_device() != index:
-            raise ValueError(f"{fn}: {name} must be on cuda:{index}")
+        _need(t is not None and t.get_device() == index and t.element_size() == size and t.is_contiguous()
+              and (size < 4 or t.numel() == h * dim * dim), fn,
+              f"{name} must be a contiguous tensor of {size}-byte elements on cuda:{index}"
+              + (f", [{h}][{dim}][{dim}]" if size == 4 else ""))
     _launch(fn, index, stream, ctypes.byref(d), lens, begin, starts, batch, n,
             _fits(fn, "max_rows", max_rows), k_out.data_ptr(), v_out.data_ptr())
 

@@ -17,8 +17,8 @@
 //   warps 8-15,   codes to y1, y2 of even and odd tiles (each with its own columns of tensor memory),
 //   16-23         a token and half of its channels a thread;
 //   warp 25       the 3 d/16 MMAs of a tile, into one of two accumulators;
-//   warps 0-3,    the rows of even and odd tiles to bf16 and out, a token a thread, and the tile's BF16
-//   4-7           tokens.
+//   warps 0-3,    R's pieces, while the first codes come; then the rows of even and odd tiles to bf16 and
+//   4-7           out, a token a thread, and the tile's BF16 tokens.
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 #include <algorithm>
 
@@ -71,7 +71,7 @@ struct GatherSmem {
   static constexpr int kTiles = kRing + kGStages * kGPages * kPart;
   static constexpr int kBars = kTiles + kGStages * static_cast<int>(sizeof(GatherTile));
   static constexpr int kSteps = D / 64;                  // a tile's channels pass from role to role in so many steps
-  static constexpr int kMisc = kBars + (2 * kGStages + 4 * kSteps + 3) * 8;
+  static constexpr int kMisc = kBars + (2 * kGStages + 4 * kSteps + 4) * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;           // the base is rounded up to 1024 bytes
   static_assert(kTiles % 16 == 0 && sizeof(GatherTile) % 8 == 0, "alignment");
@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
   uint64_t* yfull = empty + kGStages;      // y of an even (odd) tile is there, [kSteps] each
   uint64_t* done = yfull + 2 * kSteps;     // its MMAs are done, likewise
   uint64_t* xempty = done + 2 * kSteps;    // its product has been read
-  uint64_t* last = xempty + 2;             // MMAs in flight after a give-up
+  uint64_t* rfull = xempty + 2;            // R's pieces are there
+  uint64_t* last = rfull + 1;              // MMAs in flight after a give-up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -259,29 +260,12 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
       mbar_init(done + i, 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(xempty + i, kGWarps / 2);
+    mbar_init(rfull, kGWarps);
     mbar_init(last, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) tc_alloc(tmem_slot, 4 * D);
-  // R as two bf16 pieces
-  const float* r = p.r[kv] + static_cast<size_t>(h) * D * D;
-  for (int i = tid; i < D * D / 8; i += kGThreads) {
-    const int row = i / (D / 8), k = 8 * (i % (D / 8));
-    const float4 a = reinterpret_cast<const float4*>(r + row * D + k)[0];
-    const float4 b = reinterpret_cast<const float4*>(r + row * D + k)[1];
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      hi[x] = pack_bf162(v[2 * x], v[2 * x + 1]);
-      lo[x] = pack_bf162(v[2 * x] - bf16_lo_value(hi[x]), v[2 * x + 1] - bf16_hi_value(hi[x]));
-    }
-    const uint32_t at = tc_sw128_offset(row, k, D);
-    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(smem + S::kPiece + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  }
-  fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -393,7 +377,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
     constexpr int kAtom = D * 128;   // 64 channels of R's rows
     const bool leader = tc_elect();
     const uint32_t r1 = smem_u32(smem), r2 = r1 + S::kPiece;
-    bool ok = true;
+    bool ok = wait(rfull, 0);
     for (uint32_t n = 0; ok; ++n) {
       const uint32_t e = n & 1;
       if (!(ok = wait(full + n % kGStages, n / kGStages))) break;
@@ -452,6 +436,26 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
     }
   } else {
     // ----------------------------------------------------------- rows to bf16
+    // R as two bf16 pieces
+    const float* r = p.r[kv] + static_cast<size_t>(h) * D * D;
+#pragma unroll
+    for (int j = 0; j < D * D / 8 / (32 * kGWarps); ++j) {
+      const int i = tid + 32 * kGWarps * j, at_row = i / (D / 8), k = 8 * (i % (D / 8));
+      const float4 a = reinterpret_cast<const float4*>(r + at_row * D + k)[0];
+      const float4 b = reinterpret_cast<const float4*>(r + at_row * D + k)[1];
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        hi[c] = pack_bf162(v[2 * c], v[2 * c + 1]);
+        lo[c] = pack_bf162(v[2 * c] - bf16_lo_value(hi[c]), v[2 * c + 1] - bf16_hi_value(hi[c]));
+      }
+      const uint32_t at = tc_sw128_offset(at_row, k, D);
+      *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + S::kPiece + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_proxy_async();
+    arrive(rfull);
     const int row = 32 * (warp & 3) + lane, odd = warp >> 2;
     const uint32_t x = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + odd * D;
     for (uint32_t n = odd;; n += 2) {
@@ -536,10 +540,10 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
       ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15))
     return OSCAR_ERR_INVALID_ARG;
   if (total_rows > 0x7fffffff) return OSCAR_ERR_UNSUPPORTED;   // row_starts are int32
-  // tiles that max_rows consecutive positions can touch
-  const int64_t pages = (static_cast<int64_t>(max_rows) + kPage - 2) / kPage + 1;
-  const int64_t tiles = (pages + kGPages - 1) / kGPages;
-  if (pages * batch > 0x7fffffff || desc->num_kv_heads > 32767) return OSCAR_ERR_UNSUPPORTED;
+  // pages that so many consecutive positions can touch, and tiles of them
+  const auto pages = [](int64_t rows) { return (rows + kPage - 2) / kPage + 1; };
+  if (pages(max_rows) * batch > 0x7fffffff || desc->num_kv_heads > 32767) return OSCAR_ERR_UNSUPPORTED;
+  const int64_t tiles = (pages(std::min<int64_t>(max_rows, total_rows)) + kGPages - 1) / kGPages;   // (no sequence has more)
   GatherParams p{};
   p.hkv = desc->num_kv_heads;
   p.max_pages = desc->max_pages_per_seq;

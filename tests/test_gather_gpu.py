@@ -276,3 +276,40 @@ def test_offsets_beyond_4_gib():
     m.cache.int2_page_table.copy_(t.from_numpy(new[None]))
     starts, outs = m.run(np.array([0]), np.array([200]))
     m.check(np.array([0]), np.array([200]), starts, outs, heads={(0, 0), (0, 7)})
+
+
+def test_a_bound_of_rows_that_says_nothing():
+    """max_rows of all that an int32 holds: the rows that there are bound the work."""
+    m = Model([500], 2, 64, 2, seed=6)
+    full = np.array([7]), np.array([493])
+    starts, outs = m.run(*full, max_rows=(1 << 31) - 1)
+    m.check(*full, starts, outs)
+    assert int(m.cache.status.item()) == 0
+
+
+def test_rotations_written_just_before():
+    """Codes turned back by the rotations that the stream's call before has put there."""
+    t = H.torch()
+    m = Model([300], 2, 128, 4, seed=9)
+    full = np.array([0]), np.array([300])
+    old = m.r.copy()
+    for turn in range(3):
+        m.r = np.ascontiguousarray(np.roll(old, turn + 1, axis=-1))
+        new = [t.from_numpy(x).to(H.DEV) for x in m.r]
+        m.cache.r_k.copy_(new[0].view_as(m.cache.r_k)), m.cache.r_v.copy_(new[1].view_as(m.cache.r_v))
+        starts, outs = m.run(*full)
+        m.check(*full, starts, outs)
+
+
+def test_refuses_rotations_and_pools():
+    t, L = H.torch(), H.lib()
+    m = Model([40], 2, 64, 2, seed=3)
+    x = t.zeros(40, 2, 64, dtype=t.bfloat16, device=H.DEV)
+    lens, zero, rows = (t.tensor(a, dtype=t.int32, device=H.DEV) for a in ([40], [0], [0, 40]))
+    for name, bad in (("r_k", m.cache.r_k.bfloat16()), ("r_v", m.cache.r_v.flatten()[:-1].clone()),
+                      ("r_k", m.cache.r_k.cpu()), ("bf16_pool", m.cache.bf16_pool.float())):
+        good = getattr(m.cache, name)
+        setattr(m.cache, name, bad)
+        with pytest.raises(ValueError):
+            L.oscar_gather(m.cache, lens, zero, rows, 40, x, x.clone())
+        setattr(m.cache, name, good)
