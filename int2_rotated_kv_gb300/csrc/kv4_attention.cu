@@ -351,16 +351,26 @@ struct Ring4 {
   // copy is left in flight.
   __device__ __forceinline__ uint32_t take() {
     const bool got = wait_copy(bars + at, (phases >> at) & 1u, status);
-    phases ^= 1u << at;
-    const uint32_t mask = there & 3u;
-    there >>= 2;
-    --flying;
-    if (__all_sync(0xffffffffu, got)) return mask;
-    for (int st = after(at); flying > 0; --flying, st = after(st)) wait_longer(bars + st, (phases >> st) & 1u, status);
+    if (__all_sync(0xffffffffu, got)) {
+      phases ^= 1u << at;
+      const uint32_t mask = there & 3u;
+      there >>= 2;
+      --flying;
+      return mask;
+    }
+    for (int st = at; flying > 0; --flying, st = after(st)) wait_longer(bars + st, (phases >> st) & 1u, status);
     alive = false;
     return ~0u;
   }
 };
+
+// The rest of a wait for the tail's block: false when it did not come in time.  (Parts are put there next, so it has
+// another while not to be in flight any more.)
+static __device__ __noinline__ bool wait_tail(uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (mbar_wait(bar, parity, status)) return true;
+  mbar_wait(bar, parity, status);
+  return false;
+}
 
 // merge_cluster for NT tiles of 8 columns.
 template <int D, int NT>
@@ -549,7 +559,7 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     const uint8_t* tail_block = ring.base;
     if constexpr (C::kTailApart) {
       if (tail_asked) {
-        const bool got = __all_sync(0xffffffffu, wait_copy(tail_bar, tail_phase, p.status));
+        const bool got = __all_sync(0xffffffffu, mbar_try_wait(tail_bar, tail_phase) || wait_tail(tail_bar, tail_phase, p.status));
         tail_phase ^= 1u;
         tail_there = tail_there && got;
       }
@@ -700,7 +710,7 @@ inline double rows_us4(int d, int64_t batch, int64_t units, int64_t pages, int64
 }
 
 inline int cluster_of4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
-  const ClusterSizes s = cluster_sizes<kCodeInt8>();   // (every cluster kernel fills an SM)
+  const ClusterSizes s = cluster_sizes();   // (every cluster kernel fills an SM)
   int c = kMaxCluster;
   while (c > 0 && s.active[c] < units) --c;
   if (c == 0) return 0;

@@ -43,6 +43,53 @@
 // one of 32768 18.8 us, 3590 GB/s, of which 5 us are the launch, the first pages and the merge.
 #include "kv8_tiles.cuh"
 
+namespace oscar {
+
+// (The kernel for d = 128 stands for all: every cluster kernel fills an SM.)
+static ClusterSizes count_clusters() {
+  using C = Kv8Cfg<128, kCluster>;
+  const auto kernel = kv8_attention_kernel<128, kCodeInt8, kCluster>;
+  ClusterSizes s{};
+  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) return s;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(c);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(c));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&s.active[c], kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      s.active[c] = 0;
+    }
+  }
+  return s;
+}
+
+// Counted once per device.  (Threads that are the first at once all count, to the same end.)
+ClusterSizes cluster_sizes() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];   // [0]: whether the others are
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return {};
+  if (dev >= kDevices) return count_clusters();
+  ClusterSizes s{};
+  if (known[dev][0].load(std::memory_order_acquire)) {
+    for (int c = 1; c <= kMaxCluster; ++c) s.active[c] = known[dev][c].load(std::memory_order_relaxed);
+    return s;
+  }
+  s = count_clusters();
+  for (int c = 1; c <= kMaxCluster; ++c) known[dev][c].store(s.active[c], std::memory_order_relaxed);
+  known[dev][0].store(1, std::memory_order_release);
+  return s;
+}
+
+}  // namespace oscar
+
 namespace oscar_host {
 
 oscar_status check_kv8(const oscar_kv8_desc* c) {
@@ -68,8 +115,7 @@ extern "C" {
 size_t oscar_kv8_workspace_size(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows,
                                 int32_t max_seq_len) {
   if (oscar_host::check_kv8(desc) != OSCAR_OK) return 0;
-  return desc->format == OSCAR_KV8_E4M3 ? workspace_of<kCodeE4m3>(desc, batch, m_rows, max_seq_len)
-                                        : workspace_of<kCodeInt8>(desc, batch, m_rows, max_seq_len);
+  return workspace_of(desc, batch, m_rows, max_seq_len);
 }
 
 oscar_status oscar_kv8_attention(const oscar_kv8_desc* desc, const void* q, const int32_t* seq_lens,

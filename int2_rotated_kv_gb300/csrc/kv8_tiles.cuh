@@ -13,9 +13,9 @@ namespace oscar {
 
 enum Kv8Mode { kShares, kCluster, kTeams };
 
-template <int D, int kCode, Kv8Mode kMode>
+template <int D, Kv8Mode kMode>
 struct Kv8Cfg {
-  using F = KvFmt<D, kCode>;
+  using F = Kv8Fmt<D>;
   static constexpr int kWarps = kMode == kCluster ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = kMode != kCluster ? 2 : 1;   // per SM
@@ -179,7 +179,7 @@ __device__ __forceinline__ void weigh(Running<D>& s, const float (&lg)[4], float
 template <int D, int kCode>
 __device__ __forceinline__ void page(const uint8_t* st, int page0, int lane, const Query<D>& q,
                                      Running<D>& s) {
-  using F = KvFmt<D, kCode>;
+  using F = Kv8Fmt<D>;
   const int gid = lane >> 2;
   const uint4* kb = reinterpret_cast<const uint4*>(st);
   float lg[4];
@@ -536,9 +536,9 @@ __device__ __forceinline__ void team_sync(int team, int number) {
 }
 
 template <int D, int kCode, Kv8Mode kMode>
-__global__ void __launch_bounds__((Kv8Cfg<D, kCode, kMode>::kThreads), (Kv8Cfg<D, kCode, kMode>::kCtas))
+__global__ void __launch_bounds__((Kv8Cfg<D, kMode>::kThreads), (Kv8Cfg<D, kMode>::kCtas))
 kv8_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
-  using C = Kv8Cfg<D, kCode, kMode>;
+  using C = Kv8Cfg<D, kMode>;
   constexpr int kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -893,50 +893,7 @@ struct ClusterSizes {
   int active[kMaxCluster + 1];
 };
 
-// (The kernel for d = 128 stands for all: every cluster kernel fills an SM.)
-template <int kCode>
-ClusterSizes count_clusters() {
-  using C = Kv8Cfg<128, kCode, kCluster>;
-  const auto kernel = kv8_attention_kernel<128, kCode, kCluster>;
-  ClusterSizes s{};
-  if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, true)) return s;
-  for (int c = 1; c <= kMaxCluster; ++c) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(c);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(c));
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kBytes;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&s.active[c], kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      s.active[c] = 0;
-    }
-  }
-  return s;
-}
-
-// Counted once per device.  (Threads that are the first at once all count, to the same end.)
-template <int kCode>
-ClusterSizes cluster_sizes() {
-  constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices][kMaxCluster + 1];   // [0]: whether the others are
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return {};
-  if (dev >= kDevices) return count_clusters<kCode>();
-  ClusterSizes s{};
-  if (known[dev][0].load(std::memory_order_acquire)) {
-    for (int c = 1; c <= kMaxCluster; ++c) s.active[c] = known[dev][c].load(std::memory_order_relaxed);
-    return s;
-  }
-  s = count_clusters<kCode>();
-  for (int c = 1; c <= kMaxCluster; ++c) known[dev][c].store(s.active[c], std::memory_order_relaxed);
-  known[dev][0].store(1, std::memory_order_release);
-  return s;
-}
+ClusterSizes cluster_sizes();   // kv8_attention.cu
 
 struct Kv8Plan {
   bool rows;           // tiles of 128 columns (kv8_rows.cu), else of 8
@@ -988,9 +945,8 @@ inline double rows_us(int d, int64_t batch, int64_t units, int64_t pages, int64_
 // The largest cluster of which the device holds one per unit at a time; 0: shares are faster,
 // as they touch only the tokens there are, or there is none.  Measured, 8 KV heads: one
 // sequence of 32k 18.6 us against 23.9, of 128k 48.7 against 54 (both in one run).
-template <int kCode>
 inline int cluster_of(int d, int64_t batch, int64_t units, int64_t pages) {
-  const ClusterSizes s = cluster_sizes<kCode>();
+  const ClusterSizes s = cluster_sizes();
   int c = kMaxCluster;
   while (c > 0 && s.active[c] < units) --c;
   if (c == 0) return 0;
@@ -1011,7 +967,6 @@ inline int team_of(int64_t units, int64_t pages, int64_t sms) {
 }
 
 // false: sizes outside the supported range.
-template <int kCode>
 inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int64_t max_len,
                      Kv8Plan* out) {
   Kv8Plan p{};
@@ -1024,7 +979,7 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
   const int64_t pages = std::max<int64_t>(1, (max_len + kPage - 1) / kPage);
   const int64_t sms = oscar_host::sm_count(), units8 = batch * tiles8 * h;
   p.team = team_of(units8, pages, sms);
-  if (!p.team) p.cluster = cluster_of<kCode>(d, batch, units8, pages);
+  if (!p.team) p.cluster = cluster_of(d, batch, units8, pages);
   const double narrow = p.cluster ? 6.0 + cluster_us(d, pages, p.cluster) : shares_us(d, batch, units8, pages);
   p.rows = cols > 8 && rows_us(d, batch, batch * tiles128 * h, pages, sms) < narrow;
   if (p.rows) p.team = p.cluster = 0;
@@ -1045,7 +1000,7 @@ inline bool kv8_plan(const oscar_kv8_desc* c, int64_t batch, int64_t m_rows, int
 
 template <int D, int kCode, Kv8Mode kMode>
 oscar_status launch_attention(const Kv8Params& p, const Kv8Plan& pl, cudaStream_t st) {
-  using C = Kv8Cfg<D, kCode, kMode>;
+  using C = Kv8Cfg<D, kMode>;
   const auto kernel = kv8_attention_kernel<D, kCode, kMode>;
   if (!oscar_host::allow_smem(reinterpret_cast<const void*>(kernel), C::kBytes, kMode == kCluster))
     return OSCAR_ERR_CUDA;
@@ -1136,7 +1091,7 @@ oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* se
   const oscar_status s = check_attention(desc, q, seq_lens, q_pos, batch, m_rows, max_seq_len, out, workspace, &work);
   if (s != OSCAR_OK || !work) return s;
   Kv8Plan pl;
-  if (!kv8_plan<kCode>(desc, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
+  if (!kv8_plan(desc, batch, m_rows, max_seq_len, &pl)) return OSCAR_ERR_UNSUPPORTED;
   if (workspace_bytes < pl.total) return OSCAR_ERR_WORKSPACE;
   const Kv8Params p = attention_params(desc, q, seq_lens, q_pos, m_rows, max_seq_len, out, workspace, pl.tiles,
                                        pl.entries, pl.cluster, pl.team, pl.info);
@@ -1144,10 +1099,9 @@ oscar_status attend(const oscar_kv8_desc* desc, const void* q, const int32_t* se
   return desc->head_dim == 128 ? run_kv8<128, kCode>(p, pl, st) : run_kv8<64, kCode>(p, pl, st);
 }
 
-template <int kCode>
-size_t workspace_of(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows, int32_t max_seq_len) {
+inline size_t workspace_of(const oscar_kv8_desc* desc, int32_t batch, int32_t m_rows, int32_t max_seq_len) {
   Kv8Plan pl;
-  if (batch < 1 || m_rows < 1 || max_seq_len < 1 || !kv8_plan<kCode>(desc, batch, m_rows, max_seq_len, &pl)) return 0;
+  if (batch < 1 || m_rows < 1 || max_seq_len < 1 || !kv8_plan(desc, batch, m_rows, max_seq_len, &pl)) return 0;
   return pl.most;
 }
 
