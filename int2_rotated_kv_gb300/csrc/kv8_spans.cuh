@@ -13,6 +13,7 @@ constexpr int kCWarps = 4;
 
 struct Kv8CacheParams {
   int hkv, max_pages, batch, pages_per_seq, max_rows;
+  int room;                   // most tokens of a sequence: whole pages of its table row, a tail's, what int32 holds
   int64_t n_pages, n_tails, total_rows, k_stride, v_stride;
   uint8_t* pool;
   uint16_t* tail;
@@ -43,8 +44,7 @@ __device__ __forceinline__ bool span_of(const Kv8CacheParams& p, int b, Span& s)
   const int r0 = p.row_starts[b], r1 = p.row_starts[b + 1], t0 = p.first[b];
   const int64_t n = static_cast<int64_t>(r1) - r0;
   if (n == 0) return false;
-  if (n < 0 || n > p.max_rows || r0 < 0 || r1 > p.total_rows || t0 < 0 || t0 + n > 0x7fffffff ||
-      t0 + n > static_cast<int64_t>(p.max_pages) * kPage + kPage - 1) {
+  if (n < 0 || n > p.max_rows || r0 < 0 || r1 > p.total_rows || t0 < 0 || t0 + n > p.room) {
     report(p, OSCAR_DEVERR_SEQ_LEN);
     return false;
   }
@@ -159,6 +159,7 @@ inline oscar_status cache_params(const oscar_kv8_desc* c, const int32_t* first, 
   p->batch = batch;
   p->pages_per_seq = static_cast<int>(pages(std::min<int64_t>(max_rows, total_rows)));   // (no sequence has more)
   p->max_rows = max_rows;
+  p->room = static_cast<int>(std::min<int64_t>(0x7fffffff, static_cast<int64_t>(c->max_pages_per_seq) * kPage + kPage - 1));
   p->n_pages = c->num_pages;
   p->n_tails = c->num_tails;
   p->total_rows = total_rows;
