@@ -10,12 +10,22 @@
 // only roundings are q (exact down to 2^-21 of a column's largest), p g_V (11 bits, unbiased) and
 // the output.
 //
-// What differs: with half the bytes a page, instructions bound the loop before HBM does (a page's
-// 1024 keys and values take 64 conversions and 64 products of a warp before the 16 MMAs).
-//   - A warp takes two pages at a time: one wait, one softmax step for 32 tokens, and two
-//     independent chains of instructions.
-//   - Tiles of 8, 16 or 24 query columns: what was converted serves all of them, and every page is read
-//     once.  (For more columns, several tiles, or tiles of 128: kv8_rows.cu.)
+// What differs: with half the bytes a page, instructions bound the loop before HBM does.  A page of d = 128 takes a
+// warp 64 conversions and 64 products of codes, 24 conversions of scales and 16 MMAs, 350 instructions in all; an SM
+// needs 125 cycles for it, where HBM's share of an SM brings one in 95.
+//   - A warp takes two pages at a time: one wait, one softmax step for 32 tokens, and two independent chains of
+//     instructions (64 sequences of 4096-8192 tokens 107 us for 115, one of 131071 43 for 54).
+//   - Tiles of 8, 16 or 24 query columns: what was converted serves all of them, and every page is read once.  Of 20
+//     columns, 16 sequences of 2000-9001 tokens 69.7 us, as three tiles apart 89; 64 of 2000-4000 134 and 178.  (For more
+//     columns, several such tiles, or tiles of 128: kv8_rows.cu.)
+//   - The units of weights, queries and merges are the 8-bit cache's, per tile of 8 columns.
+//
+// Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 102 us (HBM's floor 67; issue slots 62% busy, the ALU
+// 56%); one of 131071 of 64/8 heads 42.3 us (22.5), one of 32768 18.8 (5.6, of which 7 are launch, queries, first
+// pages and merge); 600 tokens, 4/1 heads of 64, 6.7.
+// Tried: a CTA's warps on the same pages, each with 16 channels of the values and weights through shared memory (126 us for
+// 105 of 64 sequences, 50 for 42 of 131071 tokens: two barriers a step); scales converted by byte permutes and a
+// product (118 us for 115.5); CTAs of 4 warps for one tile (131071 tokens 46 us for 42).
 #include "kv8_tiles.cuh"
 
 namespace oscar {
@@ -691,8 +701,23 @@ inline int64_t share_ctas4(int nt, int64_t units, int64_t pages, int64_t sms) {
   return std::min(std::min<int64_t>(kMaxCtas, kv4_share_ctas(nt) * sms), (units * pages + kMinShare - 1) / kMinShare);
 }
 
-// Estimates in us of nt column tiles, fitted to what is measured below (kv8_plan says what they stand for).  A page
-// costs d = 64 two thirds of what it costs d = 128.
+// Estimates in us of nt column tiles (kv8_plan says what they stand for).  A page costs d = 64 two thirds of what it costs
+// d = 128.  Fitted to these, 32/8 heads of 128, in us ("-": more units than SMs; nt = 1, 2, 3 in turn):
+//                                      shares             clusters           teams   128 columns
+//   1 x 1 row over 512, 8000           8.4, 14.7          7.2, 10.2
+//   1 x 1 row over 32768, 131071       20.3, 42.2         17.8, 47.9
+//   16 x 1 row over 4000-8000          37.9               36.7               291
+//   64 x 1 row over 500-1000           33.8               -                  24.1
+//   40 x 1 row over 1000-2000          33.0               -                  35.0
+//   256 x 1 row over 100-200           61.3               -                  22.2
+//   1 x 3 rows over 32768              26.5, 26.5         28.1, 23.0                 38.0
+//   1 x 5 rows over 32768              34.4, 34.1, 36.1   32.0, 37.0, 29.6           38.4
+//   1 x 16 rows over 32768             64.2, 51.9, 62.2   65.7, 50.6, 56.4           40.4
+//   16 x 5 rows over 2000-9001         89.4, 77.0, 70.3   -, -, 69.5         313     79.4
+//   64 x 3 rows over 2000-4000         123, 89.8          -                  156     169
+//   64 x 4 rows over 200-400           63.2, 46.9         -                  25.9    76.4
+//   1 x 64 rows over 500               21.6, 22.9, 25.2   -, 11.8, 13.2      11.5    21.8
+// The rule took the fastest of a row in 32 of the 35 sizes that were measured, and one within 3% in the others.
 inline double page_us4(int d) { return 0.35 + 0.65 / 128 * d; }
 inline double shares_us4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
   const double start[] = {12, 15, 21}, page[] = {0.000456, 0.00066, 0.0009}, unit[] = {0.015, 0.02, 0.05};

@@ -9,6 +9,12 @@
 // One warp does one (page, KV head, keys or values), its 16 x d values in registers: a lane has 4
 // channels of all tokens (of 8 tokens for d = 64), so that maxima over tokens stay in a lane and
 // those over 16 channels take two shuffles; the codes cross lanes once, to be stored 16 bytes a lane.
+//
+// Bound by HBM at long prompts: 4 d + 1.125 d + 1 bytes per token and KV head.  24 prompts of 2500-5000 tokens, 8 KV heads
+// of 128: placing 87 us, 5.4 TB/s, with the issue slots 64% busy; reading back 77, 6.1 TB/s; 16 prefixes of 4097-8192
+// tokens read back 74 us, 6.25 TB/s.  A token of 64 sequences: 6.2 and 4.2 us, a chain of lengths, ids and values.
+// Placing is near its instructions' bound too: products two at a time, maxima of pairs of bf16 and each block's scale
+// found by one lane took placing and reading back of the prompts from 183 to 163 us.
 #include "kv4_layout.cuh"
 #include "kv8_spans.cuh"
 
@@ -307,6 +313,7 @@ __device__ __forceinline__ void store_values(const Kv8CacheParams& p, uint8_t* b
 }
 
 // blockIdx.x: (sequence, page of its rows), blockIdx.y: kCWarps (KV head, K/V) each.
+// (8 CTAs an SM, 64 registers: the prompts 86 us; 5, 6 and 7: 104, 95 and 90.5; 9, with more spilled, 85.)
 // The warp of a sequence's first page also writes the tail: the first page may
 // take tokens from the tail that the last ones are about to overwrite.
 template <int D>
@@ -385,7 +392,8 @@ __device__ __forceinline__ void tail_rows(const uint16_t* tail, int kv, int lo, 
 
 constexpr int kGatherCtas = 10;   // 48 registers a thread
 // Codes back to bf16, rounded once from fl32(code s g); tail tokens as they are.  A warp does a page's keys and
-// values of a KV head: every load of both is on its way before the first use.
+// values of a KV head: every load of both is on its way before the first use (16 prefixes of 4097-8192 tokens 74 us; keys
+// and values by warps of their own, 80).
 template <int D>
 __global__ void __launch_bounds__(32 * kCWarps, kGatherCtas) kv4_gather_kernel(const __grid_constant__ Kv8CacheParams p) {
   using F = Kv4Fmt<D>;

@@ -1,7 +1,8 @@
 // Attention over the 8-bit cache for many query columns of a KV head (a chunk of
 // prefill, a long verification): tiles of 128 (row, query head) columns on tcgen05.
 //
-// Same mathematics, unit division and partial results as kv8_attention.cu.  Per tile
+// Same mathematics, unit division and partial results as kv8_attention.cu, for the 4-bit cache too (kv4_attention.cu),
+// whose operands are code * s.  Per tile
 // of 128 tokens (8 pages):
 //   S = Q K^T   M = 128 columns of queries, N = 128 tokens, K = d   (Q, K in shared memory)
 //   w = 2^(s_K fac S + log2 s_V - m - k)   (a thread per query; kv8_units.cuh has unit and ranges)
@@ -28,7 +29,8 @@
 // tile); a tile takes 2400, in which a K warp is busy for 1950 and a stream's chain S, softmax,
 // O is longer than its share.  Measured, d = 128, 8 KV heads, G = 4: 2048 rows over 32768 tokens
 // 1050 us, 1047 TFLOP/s; 4 sequences x 65 rows over 6000-16385 tokens 86.7 us, 550 TFLOP/s of
-// rows that exist (260 columns are 3 tiles: a third of the work is for 4 of them).
+// rows that exist (260 columns are 3 tiles: a third of the work is for 4 of them).  4 bits: 1000 rows
+// over 17000 tokens 308 us, 905 TFLOP/s.
 // Registers: 96 a thread for 18 warps.  Whatever is spilled in a role's loop costs more than
 // it saves elsewhere (16 registers' worth: 7 of 98 us), and code that is fetched cold costs its
 // fetches, so what runs once per unit is out of line or rolled.
