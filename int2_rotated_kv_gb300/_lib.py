@@ -435,14 +435,14 @@ def _need(ok: bool, fn: str, what: str) -> None:
 # on the host: each of these reads an attribute of a tensor once, and a message is put
 # together only when it is raised.
 
-_INT32 = _INT64 = _BF16 = _raw_stream = _current_device = None
+_INT32 = _INT64 = _BF16 = _FP32 = _raw_stream = _current_device = None
 
 
 def _bind_torch() -> None:
     """What the checks use of torch, which is imported when the first tensor comes."""
-    global _INT32, _INT64, _BF16, _raw_stream, _current_device
+    global _INT32, _INT64, _BF16, _FP32, _raw_stream, _current_device
     import torch
-    _INT32, _INT64, _BF16 = torch.int32, torch.int64, torch.bfloat16
+    _INT32, _INT64, _BF16, _FP32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
     # the current stream's handle without a Stream object around it
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
@@ -507,19 +507,23 @@ def oscar_gather(cache: Cache, seq_lens, first, row_starts, max_rows: int, k_out
         raise ValueError(f"{fn}: k_out and v_out must be contiguous")
     lens, begin = _i32(fn, "seq_lens", seq_lens, index), _i32(fn, "first", first, index)
     starts = _i32(fn, "row_starts", row_starts, index)
-    _i32(fn, "int2_page_table", cache.int2_page_table, index)
-    _i32(fn, "bf16_page_table", cache.bf16_page_table, index)
-    batch, shape = seq_lens.numel(), cache.int2_page_table.shape
+    coded, plain = cache.int2_page_table, cache.bf16_page_table
+    _i32(fn, "int2_page_table", coded, index)
+    _i32(fn, "bf16_page_table", plain, index)
+    batch, shape = seq_lens.numel(), coded.shape
     if first.numel() != batch or row_starts.numel() != batch + 1:
         raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1")
-    if shape != cache.bf16_page_table.shape or len(shape) != 2 or batch > shape[0]:
+    if shape != plain.shape or len(shape) != 2 or batch > shape[0]:
         raise ValueError(f"{fn}: the page tables must have the same shape, and a row per sequence")
-    for name, size in (("int2_pool", 1), ("bf16_pool", 2), ("r_k", 4), ("r_v", 4)):
-        t = getattr(cache, name)
-        _need(t is not None and t.get_device() == index and t.element_size() == size and t.is_contiguous()
-              and (size < 4 or t.numel() == h * dim * dim), fn,
-              f"{name} must be a contiguous tensor of {size}-byte elements on cuda:{index}"
-              + (f", [{h}][{dim}][{dim}]" if size == 4 else ""))
+    for pool, size in ((cache.int2_pool, 1), (cache.bf16_pool, 2)):
+        if pool.get_device() != index or pool.element_size() != size or not pool.is_contiguous():
+            raise ValueError(f"{fn}: int2_pool and bf16_pool must be contiguous tensors of bytes and of "
+                             f"bfloat16 on cuda:{index}")
+    for r in (cache.r_k, cache.r_v):
+        if (r is None or r.get_device() != index or r.dtype is not _FP32 or r.numel() != h * dim * dim
+                or not r.is_contiguous()):
+            raise ValueError(f"{fn}: r_k and r_v must be contiguous float32 tensors [{h}][{dim}][{dim}] "
+                             f"on cuda:{index}")
     _launch(fn, index, stream, ctypes.byref(d), lens, begin, starts, batch, n,
             _fits(fn, "max_rows", max_rows), k_out.data_ptr(), v_out.data_ptr())
 
