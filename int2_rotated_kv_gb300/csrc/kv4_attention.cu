@@ -21,8 +21,8 @@
 //   - The units of weights, queries and merges are the 8-bit cache's, per tile of 8 columns.
 //
 // Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 102 us (HBM's floor 67; issue slots 62% busy, the ALU
-// 56%); one of 131071 of 64/8 heads 42.3 us (22.5), one of 32768 18.8 (5.6, of which 7 are launch, queries, first
-// pages and merge); 600 tokens, 4/1 heads of 64, 6.7.
+// 56%); one of 131071 of 64/8 heads 42.3 us (22.5), one of 32768 18.3 (5.6, of which 7 are launch, queries, first
+// pages and merge); 600 tokens, 4/1 heads of 64, 6.5.
 // Tried: a CTA's warps on the same pages, each with 16 channels of the values and weights through shared memory (126 us for
 // 105 of 64 sequences, 50 for 42 of 131071 tokens: two barriers a step); scales converted by byte permutes and a
 // product (118 us for 115.5); CTAs of 4 warps for one tile (131071 tokens 46 us for 42).
@@ -181,18 +181,18 @@ __device__ __forceinline__ void weigh_pages(Running<D>& s, const float (&lg)[N][
   s.l[1] = second(l);
 }
 
-// N pages of codes, at st and kBlock on, their tokens from first_token and first_token + step on; `there`: bit per page.
+// N pages of codes, at st and kBlock on, their tokens from first_token and first_token + step on.
 template <int D, int NT, int N>
-__device__ __forceinline__ void take_pages(const uint8_t* st, int first_token, int step, uint32_t there, int lane,
+__device__ __forceinline__ void take_pages(const uint8_t* st, int first_token, int step, int lane,
                                           const Columns<D, (NT > 1)> (&q)[NT], Running<D> (&s)[NT]) {
   using F = Kv4Fmt<D>;
   const int gid = lane >> 2, tig = lane & 3;
   int page0[N];
   const uint8_t* at[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {   // one that is not there is read as the other, and weighs nothing
+  for (int n = 0; n < N; ++n) {
     page0[n] = first_token + n * step;
-    at[n] = N == 1 || ((there >> n) & 1u) ? st + n * F::kBlock : st + (1 - n) * F::kBlock;
+    at[n] = st + n * F::kBlock;
   }
   float lg[NT][N][4];
   float off[N], sk[N];
@@ -242,12 +242,12 @@ __device__ __forceinline__ void take_pages(const uint8_t* st, int first_token, i
       // (rounded by themselves, not on the way to a difference, so that equal logits stay equal)
 #pragma unroll
       for (int r = 0; r < 4; ++r) lg[t][n][r] = __fmul_rn(lg[t][n][r], r & 1 ? f1 : f0);
-      if (page0[n] + kPage > q[t].seen_least() || (N > 1 && !((there >> n) & 1u))) {
+      if (page0[n] + kPage > q[t].seen_least()) {
         const int tk = page0[n] + 2 * gid;
         const int2 seen = q[t].seen(lane);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int vis = N == 1 || ((there >> n) & 1u) ? (c ? seen.y : seen.x) : 0;
+          const int vis = c ? seen.y : seen.x;
           if (tk >= vis) lg[t][n][c] = -INFINITY;
           if (tk + 1 >= vis) lg[t][n][2 + c] = -INFINITY;
         }
@@ -543,11 +543,16 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
       // (a refused id's stands for nothing)
       const uint8_t* st = ring.base + ring.at * C::kStage;
       if constexpr (C::kAtOnce == kPair) {
-        if (there) take_pages<D, NT, kPair>(st, page0, team * kPage, there, lane, q, s);
+        if (there == 3u) {
+          take_pages<D, NT, kPair>(st, page0, team * kPage, lane, q, s);
+        } else if (there) {   // the last of an odd number, or beside a refused id (as a pair: 32768 tokens 18.9 us for 18.3)
+          const int n = there >> 1;
+          take_pages<D, NT, 1>(st + n * C::F::kBlock, page0 + n * team * kPage, 0, lane, q, s);
+        }
       } else {
 #pragma unroll 1
         for (int n = 0; n < kPair; ++n)
-          if ((there >> n) & 1u) take_pages<D, NT, 1>(st + n * C::F::kBlock, page0 + n * team * kPage, 0, 1u, lane, q, s);
+          if ((there >> n) & 1u) take_pages<D, NT, 1>(st + n * C::F::kBlock, page0 + n * team * kPage, 0, lane, q, s);
       }
       __syncwarp();
       if (left > C::kStages) ring.issue(p, src, ring.at, lane);
