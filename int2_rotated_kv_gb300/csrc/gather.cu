@@ -165,13 +165,16 @@ __device__ __forceinline__ void uncode(const uint8_t* blk, int t, int half, int 
   for (int i = 0; i < 2; ++i) {
     uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t c = (x[0][q][m] >> (4 * h + 2 * i)) & 0x00030003u;
-        if constexpr (P == 2) c = c * 4 + ((x[P - 1][q][m] >> (4 * h + 2 * i)) & 0x00030003u);
-        split_pair(c, two(s, s), two(z, z), hi[4 * h + q], lo[4 * h + q]);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t c = x[0][q][m] >> (2 * i);
+      if constexpr (P == 2) {   // both planes' bits of a code side by side
+        const uint32_t up = i ? x[0][q][m] : x[0][q][m] << 2, down = x[P - 1][q][m] >> (2 * i);
+        c = (up & 0xccccccccu) | (down & 0x33333333u);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        split_pair((c >> (4 * h)) & (P == 2 ? 0x000f000fu : 0x00030003u), two(s, s), two(z, z), hi[4 * h + q], lo[4 * h + q]);
+    }
     tc_st8(a + 16 * g + 8 * i, hi);
     tc_st8(a + D / 2 + 16 * g + 8 * i, lo);
   }
