@@ -18,13 +18,18 @@
 //   16-23         a token and half of its channels a thread;
 //   warp 25       the 3 d/16 MMAs of a tile, into one of two accumulators;
 //   warps 0-3,    R's pieces, while the first codes come; then the rows of even and odd tiles to bf16 and
-//   4-7           out, a token a thread, and the tile's BF16 tokens.
+//   4-7           out, a token a thread;
+//   warps 26, 27  the tiles' BF16 tokens, as soon as a tile is found (2000 tokens of INT2 4.7 us, by the warps that store
+//                 rows 5.1).
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 //
-// What bounds it: the roles share an SM's issue slots, and none of its parts is far from its limit.  INT4, 16 sequences
-// of 2048-4096 tokens, 8 KV heads of 128: 63.8 us, 3.6 TB/s and 1050 TFLOP/s of bf16 products (a tile's 24 MMAs take 1536
-// cycles, of 2600), with the ALU 59%, the tensor cores 56% and shared memory 57% busy; bytes and products by themselves
-// would take 34 and 34 us.  2000 tokens of INT2, 4 heads of 64: 5.1 us.
+// What bounds it: the chain of a group of uncoding warps.  INT4, 16 sequences of 2048-4096 tokens, 8 KV heads of 128: 63.8
+// us, 3.6 TB/s and 1050 TFLOP/s of bf16 products (a tile's 24 MMAs take 1536 cycles), with the ALU 59%, the tensor cores
+// 56% and shared memory 57% busy; bytes and products by themselves would take 34 and 34 us.  A group takes 3650 cycles for its
+// every second tile, 1090 of them for codes from shared memory, and waits for 340; 10000 pass before the first products.
+// Fewer instructions there (the larger piece by splitting in fp32, 64.9 us; codes by one operation less, 64.1) and the
+// next words uncoded while the last are stored (65.0) change nothing; more warps would have 56 registers.  2000
+// tokens of INT2, 4 heads of 64: 4.7 us.
 // The same in its steps: without tensor cores 1156 us; a CTA that does one thing after another 124; rows stored by 32 bytes
 // 111 (two CTAs of 8 warps an SM no faster); roles and two accumulators 74; a tile's channels in two steps, so
 // that MMAs start on the first half, and keys' codes read without bank conflicts 67; R turned into pieces beside
@@ -57,7 +62,8 @@ constexpr int kGTile = 128;                 // tokens of a tile
 constexpr int kGPages = kGTile / kPage;
 constexpr int kGStages = 8;
 constexpr int kGWarps = 8;                  // of a role that computes
-constexpr int kGThreads = 32 * (3 * kGWarps + 2);
+constexpr int kGPlain = 2;                  // and of the BF16 tokens
+constexpr int kGThreads = 32 * (3 * kGWarps + 2 + kGPlain);
 
 // A tile as the computing warps need it: positions of its tokens are pos0 + row.
 struct GatherTile {
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
   if (tid == 0) {
     for (int i = 0; i < kGStages; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, kGWarps + kGWarps / 2);
+      mbar_init(empty + i, kGWarps + kGWarps / 2 + kGPlain);
     }
     for (int i = 0; i < 2 * kSteps; ++i) {
       mbar_init(yfull + i, kGWarps);
@@ -420,6 +426,23 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
       tc_commit(last);
       mbar_wait(last, 0, p.status);
     }
+  } else if (warp > 3 * kGWarps + 1) {
+    // ------------------------------------------------------------ BF16 tokens
+    for (uint32_t n = 0;; ++n) {
+      const int st = n % kGStages;
+      if (!wait(full + st, n / kGStages)) break;
+      const GatherTile& t = tiles[st];
+      if (t.stop) break;
+      if (t.c0 > t.lo || t.c1 < t.hi) {
+#pragma unroll 1
+        for (int i = warp & 1; i < kGPages; i += kGPlain) {
+          if (kv) plain_page<D, true>(p, t, h, i, lane);
+          else plain_page<D, false>(p, t, h, i, lane);
+          __syncwarp();
+        }
+      }
+      arrive(empty + st);
+    }
   } else if (warp >= kGWarps) {
     // ------------------------------------------------------------- codes to y
     const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1, odd = (warp - kGWarps) / kGWarps;
@@ -494,15 +517,6 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = pack_bf162(__uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
           if (mine) store32(dst + j + k, w, p.whole);
-        }
-      }
-      __syncwarp();
-      if (t.c0 > t.lo || t.c1 < t.hi) {
-#pragma unroll 1
-        for (int i = warp & 3; i < kGPages; i += kGWarps / 2) {
-          if (kv) plain_page<D, true>(p, t, h, i, lane);
-          else plain_page<D, false>(p, t, h, i, lane);
-          __syncwarp();
         }
       }
       arrive(empty + st);
