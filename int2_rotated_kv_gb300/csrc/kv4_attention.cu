@@ -16,12 +16,12 @@
 //   - A warp takes two pages at a time: one wait, one softmax step for 32 tokens, and two independent chains of
 //     instructions (64 sequences of 4096-8192 tokens 107 us for 115, one of 131071 43 for 54).
 //   - Tiles of 8, 16 or 24 query columns: what was converted serves all of them, and every page is read once.  Of 20
-//     columns, 16 sequences of 2000-9001 tokens 69.7 us, as three tiles apart 89; 64 of 2000-4000 134 and 178.  (For more
+//     columns, 16 sequences of 2000-9001 tokens 64.3 us, as three tiles apart 82; 64 of 2000-4000 124 and 169.  (For more
 //     columns, several such tiles, or tiles of 128: kv8_rows.cu.)
 //   - The units of weights, queries and merges are the 8-bit cache's, per tile of 8 columns.
 //
-// Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 102 us (HBM's floor 67; issue slots 62% busy, the ALU
-// 56%); one of 131071 of 64/8 heads 42.3 us (22.5), one of 32768 18.3 (5.6, of which 7 are launch, queries, first
+// Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 99.6 us (HBM's floor 67; issue slots 62% busy, the ALU
+// 54%); one of 131071 of 64/8 heads 41.1 us (22.5), one of 32768 18.3 (5.6, of which 7 are launch, queries, first
 // pages and merge); 600 tokens, 4/1 heads of 64, 6.5.
 // Tried: a CTA's warps on the same pages, each with 16 channels of the values and weights through shared memory (126 us for
 // 105 of 64 sequences, 50 for 42 of 131071 tokens: two barriers a step); scales converted by byte permutes and a
@@ -32,6 +32,11 @@ namespace oscar {
 
 constexpr int kMaxNT = 3;      // tiles of 8 columns that share a page's operands
 constexpr int kPair = 2;       // pages of a step
+
+// In shares, a unit counts for so many pages before its own: the change to it takes a CTA that long.  (Of pages alone, 0, a
+// CTA with many short units ends last: 30 sequences of 100-6000 tokens, 2 rows of 40 heads, 84.7 us for 46.5; 100 of
+// 50-4000 113 for 72.5; 64 of 4096-8192 102.5 for 99.5.  8 and 16: 71 and 58, 95 and 89, 102 and 100; 72: 51, 73, 99.3.)
+constexpr int kLead = 40;
 
 // CTAs per SM that divide the pages among them.
 __host__ __device__ constexpr int kv4_share_ctas(int nt) { return nt == 1 ? 2 : 3; }
@@ -463,15 +468,16 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     end = static_cast<int64_t>(t.pages) * (rank + 1) / p.cluster;
   } else {
     bool any;
-    const Share sh = find_share<NT, kWarps>(p, min_share, any);
-    if (!any) {
+    const Share sh = find_share<NT, kWarps, kLead>(p, min_share, any);
+    // (a share that ends in a unit's lead has no page of it)
+    if (!any || sh.end - sh.unit0 <= kLead) {
       if (tid == 0) p.info[blockIdx.x] = make_int4(0, 0, 0, 0);
       return;
     }
-    at = sh.at;
+    at = max(sh.at, sh.unit0 + kLead);
     end = sh.end;
     share = sh.share;
-    unit0 = sh.unit0;
+    unit0 = sh.unit0 + kLead;   // (a unit's first page stands behind its lead)
     e = sh.e;
     h = sh.h;
     t = sh.t;
@@ -602,9 +608,9 @@ kv4_attention_kernel(const __grid_constant__ Kv8Params p, int min_share) {
     const Entry tc = t;
     const int hc = h, c0 = p0, c1 = p1;
     const int64_t u0 = unit0;
-    const bool more = kMode == kShares && u0 + c1 < end;
+    const bool more = kMode == kShares && u0 + tc.pages + kLead < end;
     if (more) {
-      unit0 = u0 + tc.pages;
+      unit0 = u0 + tc.pages + kLead;
       if (++h == p.hkv) {
         h = 0;
         t = entry_of<NT>(p, ++e);
@@ -703,29 +709,32 @@ struct Kv4Plan {
 
 // CTAs that share the pages of `units`.
 inline int64_t share_ctas4(int nt, int64_t units, int64_t pages, int64_t sms) {
-  return std::min(std::min<int64_t>(kMaxCtas, kv4_share_ctas(nt) * sms), (units * pages + kMinShare - 1) / kMinShare);
+  return std::min(std::min<int64_t>(kMaxCtas, kv4_share_ctas(nt) * sms), (units * (pages + kLead) + kMinShare - 1) / kMinShare);
 }
 
 // Estimates in us of nt column tiles (kv8_plan says what they stand for).  A page costs d = 64 two thirds of what it costs
 // d = 128.  Fitted to these, 32/8 heads of 128, in us ("-": more units than SMs; nt = 1, 2, 3 in turn):
 //                                      shares             clusters           teams   128 columns
-//   1 x 1 row over 512, 8000           8.4, 14.7          7.2, 10.2
-//   1 x 1 row over 32768, 131071       20.3, 42.2         17.8, 47.9
-//   16 x 1 row over 4000-8000          37.9               36.7               291
-//   64 x 1 row over 500-1000           33.8               -                  24.1
-//   40 x 1 row over 1000-2000          33.0               -                  35.0
-//   256 x 1 row over 100-200           61.3               -                  22.2
-//   1 x 3 rows over 32768              26.5, 26.5         28.1, 23.0                 38.0
-//   1 x 5 rows over 32768              34.4, 34.1, 36.1   32.0, 37.0, 29.6           38.4
-//   1 x 16 rows over 32768             64.2, 51.9, 62.2   65.7, 50.6, 56.4           40.4
-//   16 x 5 rows over 2000-9001         89.4, 77.0, 70.3   -, -, 69.5         313     79.4
-//   64 x 3 rows over 2000-4000         123, 89.8          -                  156     169
-//   64 x 4 rows over 200-400           63.2, 46.9         -                  25.9    76.4
-//   1 x 64 rows over 500               21.6, 22.9, 25.2   -, 11.8, 13.2      11.5    21.8
-// The rule took the fastest of a row in 32 of the 35 sizes that were measured, and one within 3% in the others.
+//   1 x 1 row over 512, 8000           8.2, 12.0          6.9, 9.7
+//   1 x 1 row over 32768, 131071       18.0, 40.1         17.2, 46.6
+//   16 x 1 row over 4000-8000          35.8               35.9               283
+//   64 x 1 row over 500-1000           29.6               -                  22.9
+//   40 x 1 row over 1000-2000          29.1               -                  34.2
+//   100 x 1 row over 50-4000           72.6               -                  147
+//   256 x 1 row over 100-200           51.3               -                  21.2
+//   1 x 3 rows over 32768              24.3, 24.5         27.3, 22.5                 37.9
+//   1 x 5 rows over 32768              31.2, 33.8, 33.3   31.2, 35.5, 29.5           38.1
+//   1 x 16 rows over 32768             62.1, 50.4, 58.9   64.7, 48.7, 56.1           40.2
+//   16 x 5 rows over 2000-9001         82.2, 73.1, 64.5   -, -, 69.7         305     79.0
+//   16 x 5 rows over 9000-9001         111, 101, 87.5     -, -, 74.5                 94.8
+//   64 x 3 rows over 2000-4000         117, 82.1          -                  153     169
+//   64 x 4 rows over 200-400           46.0, 37.7         -                  24.9    76.1
+//   1 x 64 rows over 500               18.3, 20.5, 23.9   -, 11.4, 13.3      11.1    21.7
+// The rule takes the fastest of a row, to 1%, in 36 of the 40 sizes that were measured, one within 4% in three, and shares
+// for 16 x 5 rows of one length, which the host takes for three quarters of it.
 inline double page_us4(int d) { return 0.35 + 0.65 / 128 * d; }
 inline double shares_us4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
-  const double start[] = {12, 15, 21}, page[] = {0.000456, 0.00066, 0.0009}, unit[] = {0.015, 0.02, 0.05};
+  const double start[] = {11.5, 14, 19}, page[] = {0.00044, 0.00062, 0.00085}, unit[] = {0.015, 0.015, 0.04};
   return start[nt - 1] + page[nt - 1] * page_us4(d) * visited(batch, units, pages) + unit[nt - 1] * static_cast<double>(units);
 }
 inline double cluster_us4(int d, int nt, int64_t pages, int c) {

@@ -199,8 +199,8 @@ struct Share {
 };
 
 // (Its loops rolled: code that a CTA runs once costs its fetches.  Not out of line: there the
-// parameters are read through memory, 2% of the 65-row case.)
-template <int NT, int kWarps>
+// parameters are read through memory, 2% of the 65-row case.)  kLead: pages that a unit counts for before its own.
+template <int NT, int kWarps, int kLead = 0>
 __device__ __forceinline__ Share find_share(const Kv8Params& p, int min_share, bool& any) {
   // threads of an entry, for its rows' positions; entries at a time
   constexpr int kLanes = NT > 4 ? 8 : 1, kAtOnce = 32 * kWarps / kLanes;
@@ -222,7 +222,7 @@ __device__ __forceinline__ Share find_share(const Kv8Params& p, int min_share, b
     for (int e0 = 0; e0 < p.entries; e0 += kAtOnce) {
       if (pass == 0 || !few) {
         own = make_entry<NT, kLanes>(p, min(e0 + own_e, p.entries - 1));
-        v = e0 + own_e < p.entries && threadIdx.x % kLanes == 0 ? static_cast<int64_t>(own.pages) * p.hkv : 0;
+        v = e0 + own_e < p.entries && threadIdx.x % kLanes == 0 ? static_cast<int64_t>(own.pages + kLead) * p.hkv : 0;
         incl = block_scan<kWarps>(v, scratch, all);
       }
       if (pass == 0) {
@@ -252,8 +252,8 @@ __device__ __forceinline__ Share find_share(const Kv8Params& p, int min_share, b
   s.e = found_number;
   s.t = found;
   // (the entry's pages are fewer than 2^31 for all heads of a cache that exists)
-  s.h = static_cast<int>((s.at - found_before) / s.t.pages);
-  s.unit0 = found_before + static_cast<int64_t>(s.h) * s.t.pages;
+  s.h = static_cast<int>((s.at - found_before) / (s.t.pages + kLead));
+  s.unit0 = found_before + static_cast<int64_t>(s.h) * (s.t.pages + kLead);
   return s;
 }
 

@@ -522,3 +522,18 @@ def test_a_bound_of_rows_that_says_nothing(most):
             np.testing.assert_array_equal(H.from_bf16(got)[:318, h], synth.bf16_round(want[5:].astype(np.float32)))
     assert (k[318:] == 7).all() and (v[318:] == 7).all()
     assert H.status(s.cache) == 0
+
+
+@pytest.mark.parametrize("m,top", [(1, 4100), (3, 4100), (5, 4100), (5, 40000)])
+def test_short_and_empty_sequences_among_long_ones(m, top):
+    """Shares that end before a unit's pages, in them and behind them; sequences without a token."""
+    lens = np.array([3000, 0, 1, 5, 16, 0, 0, 700, 17, 40, 2, 0, 1500, 31, 0] * 2)
+    s = K.Sequences(len(lens), 8, 32, 128, 4096, seed=m)
+    s.place(lens)
+    q = K8.queries(s.rng, len(lens), m, 32, 128)
+    pos = None if m == 1 else np.maximum(s.lens[:, None] - m + np.arange(m), -1)
+    got = s.attend(q, pos, wide=top // 16)
+    some = {(b, h) for b in range(len(lens)) for h in ((b % 8, 7 - b % 8) if lens[b] > 1000 else range(8))}
+    s.check_attention(got, q, pos, heads=some)
+    assert H.status(s.cache) == 0
+    np.testing.assert_array_equal(got, s.attend(q, pos, wide=top // 16))
