@@ -499,6 +499,8 @@ def oscar_gather(cache: Cache, seq_lens, first, row_starts, max_rows: int, k_out
     of k_out and v_out (contiguous [n][Hkv][d]) get sequence b's tokens from position first[b] on,
     BF16 ones as stored, INT2 or INT4 ones as code * s + z, rotated back."""
     fn = "oscar_gather"
+    if cache.int2_pool is None or cache.bf16_pool is None:
+        raise ValueError(f"{fn}: the cache must have both pools")
     index = _device_of(fn, "int2_pool", cache.int2_pool)
     d = cache.desc()
     n, h, dim = k_out.shape[0], cache.num_kv_heads, cache.head_dim
@@ -510,6 +512,8 @@ def oscar_gather(cache: Cache, seq_lens, first, row_starts, max_rows: int, k_out
     coded, plain = cache.int2_page_table, cache.bf16_page_table
     _i32(fn, "int2_page_table", coded, index)
     _i32(fn, "bf16_page_table", plain, index)
+    if cache.status is not None:
+        _i32(fn, "status", cache.status, index)
     batch, shape = seq_lens.numel(), coded.shape
     if first.numel() != batch or row_starts.numel() != batch + 1:
         raise ValueError(f"{fn}: first must have batch entries, row_starts batch + 1")

@@ -135,3 +135,10 @@ def test_binding_refuses_what_it_can_see(L):
                  lambda: L.oscar_kv8_attention(c, x, i[:1], 16, x, x)):
         with pytest.raises(ValueError, match="cache must be a Kv"):
             call()
+
+
+def test_gather_needs_both_pools(L):
+    for pools in ((None, 1), (1, None)):
+        cache = L.Cache(2, 2, 64, 4, 64, *pools, None, None, None, None, None, None)
+        with pytest.raises(ValueError):
+            L.oscar_gather(cache, None, None, None, 1, None, None)
