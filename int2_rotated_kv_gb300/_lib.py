@@ -222,9 +222,13 @@ class Cache:
     code_bits: int = 2
 
     def desc(self) -> CacheDesc:
+        # made again when a field, a tensor or the size of a pool or table has changed
         key = tuple(_ptr(t) for t in (self.int2_pool, self.bf16_pool, self.int2_page_table,
                                       self.bf16_page_table, self.r_k, self.r_v, self.clip_k,
-                                      self.clip_v, self.status)) + (self.code_bits,)
+                                      self.clip_v, self.status))
+        key += (None if self.int2_pool is None else self.int2_pool.shape, self.bf16_pool.shape,
+                self.bf16_page_table.shape, self.num_kv_heads, self.num_q_heads, self.head_dim,
+                self.sink, self.window, self.code_bits)
         cached = self.__dict__.get("_desc")
         if cached is not None and cached[0] == key:
             return cached[1]
