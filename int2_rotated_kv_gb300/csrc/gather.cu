@@ -12,7 +12,7 @@
 // are the K-major rows of operand B as they are), y's pieces in tensor memory, where a thread writes
 // its own token's row.  A CTA, one an SM, keeps the R of one (KV head, keys or values) and walks over
 // tiles of tokens, which pass through its roles:
-//   warp 24       finds the next tiles that hold rows (32 at a look), and copies the codes of their
+//   warp 24       finds the next tiles that hold rows (of 32 sequences at a look), and copies the codes of their
 //                 pages into a ring of stages (bulk copies, one a page);
 //   warps 8-15,   codes to y1, y2 of even and odd tiles (each with its own columns of tensor memory),
 //   16-23         a token and half of its channels a thread;
@@ -43,7 +43,7 @@
 namespace oscar {
 
 struct GatherParams {
-  int hkv, max_pages, batch, tiles_per_seq, max_rows, sink, window, ctas_per_r;
+  int hkv, max_pages, batch, max_rows, sink, window, ctas_per_r;
   bool whole;        // outputs start at a multiple of 32 bytes
   int64_t n_coded, n_plain, total_rows;
   const uint8_t* coded;
@@ -302,78 +302,103 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
 
   if (warp == 3 * kGWarps) {
     // ------------------------------------------------------------- tiles ahead
+    // The tiles that hold rows, of all sequences laid end to end, go round the rotation's CTAs.  (By number of sequence and
+    // announced rows, a batch of one-tile sequences beside a longer one could fall to one CTA: 255 of 100 tokens and one of
+    // 1130, 8 heads of 128, 1071 us for 138.)
     uint32_t n = 0;   // tiles published
     bool ok = true;
-    const int64_t total = static_cast<int64_t>(p.batch) * p.tiles_per_seq;
-    for (int64_t base = number; base < total && ok; base += static_cast<int64_t>(32) * p.ctas_per_r) {
-      // a tile a lane
-      const int64_t tile = base + static_cast<int64_t>(lane) * p.ctas_per_r;
-      GatherTile t{};
-      bool some = false;
-      if (tile < total) {
-        t.b = static_cast<int>(tile / p.tiles_per_seq);
-        const int i = static_cast<int>(tile - static_cast<int64_t>(t.b) * p.tiles_per_seq);
-        const int64_t r0 = p.row_starts[t.b], rows = p.row_starts[t.b + 1] - r0;
-        const int t0 = p.first[t.b], len = p.seq_lens[t.b];
+    int ahead = number;   // of the tiles from sequence b0 on, this CTA's next
+    // lanes with a sequence, up to a power of two (with 32, one sequence of 2000 tokens of INT2 4.9 us for 4.7)
+    const int among = p.batch < 32 ? 1 << (32 - __clz(p.batch - 1)) : 32;
+    for (int64_t b0 = 0; b0 < p.batch && ok; b0 += 32) {
+      // a sequence a lane
+      const int b = static_cast<int>(b0) + lane;
+      int t0 = 0, end = 0, len = 0, count = 0;
+      int64_t r0 = 0;
+      if (b0 + lane < p.batch) {
+        r0 = p.row_starts[b];
+        const int64_t rows = p.row_starts[b + 1] - r0;
+        t0 = p.first[b];
+        len = p.seq_lens[b];
         if (rows != 0) {
           if (rows < 0 || rows > p.max_rows || r0 < 0 || r0 + rows > p.total_rows || t0 < 0 || t0 + rows > len ||
               len > static_cast<int64_t>(p.max_pages) * kPage) {
             if (p.status) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
           } else {
-            const int64_t pos0 = (t0 / kPage + static_cast<int64_t>(kGPages) * i) * kPage;
-            if (pos0 < t0 + rows) {
-              some = true;
-              t.pos0 = static_cast<int>(pos0);
-              t.lo = max(t0, t.pos0);
-              t.hi = static_cast<int>(min(t0 + rows, pos0 + kGTile));
-              t.row0 = r0 + pos0 - t0;
-              t.c0 = min(max(t.lo, p.sink), t.hi);
-              t.c1 = max(t.c0, min(t.hi, max(len - p.window, 0)));
+            end = t0 + static_cast<int>(rows);
+            count = static_cast<int>((t0 % kPage + rows + kGTile - 1) / kGTile);
+          }
+        }
+      }
+      int upto = count;   // tiles of these sequences up to and with the lane's
+#pragma unroll 1
+      for (int o = 1; o < among; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, among - 1);
+      for (int next = ahead; next < all && ok; next += 32 * p.ctas_per_r) {
+        // a tile a lane, and its sequence's lane
+        const bool some = next + lane * p.ctas_per_r < all;
+        const int tile = some ? next + lane * p.ctas_per_r : all - 1;
+        int of = 0;
+#pragma unroll 1
+        for (int o = among >> 1; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, of + o - 1) <= tile) of += o;
+        GatherTile t{};
+        t.b = static_cast<int>(b0) + of;
+        const int from = __shfl_sync(0xffffffffu, t0, of), to = __shfl_sync(0xffffffffu, end, of);
+        const int i = tile - __shfl_sync(0xffffffffu, upto - count, of);
+        t.pos0 = (from / kPage + kGPages * i) * kPage;
+        t.lo = max(from, t.pos0);
+        t.hi = t.pos0 + min(to - t.pos0, kGTile);
+        t.row0 = __shfl_sync(0xffffffffu, r0, of) + t.pos0 - from;
+        t.c0 = min(max(t.lo, p.sink), t.hi);
+        t.c1 = max(t.c0, min(t.hi, max(__shfl_sync(0xffffffffu, len, of) - p.window, 0)));
+        for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok;) {
+          // the next four of them, eight lanes each (one at a time, the look-ups of page ids bound the walk)
+          uint32_t left = todo;
+          for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
+          const int src = left ? __ffs(left) - 1 : 0;
+          GatherTile u{};
+          u.b = __shfl_sync(0xffffffffu, t.b, src);
+          u.pos0 = __shfl_sync(0xffffffffu, t.pos0, src);
+          u.lo = __shfl_sync(0xffffffffu, t.lo, src);
+          u.hi = __shfl_sync(0xffffffffu, t.hi, src);
+          u.c0 = __shfl_sync(0xffffffffu, t.c0, src);
+          u.c1 = __shfl_sync(0xffffffffu, t.c1, src);
+          u.row0 = __shfl_sync(0xffffffffu, t.row0, src);
+          // a page a lane: its codes, and the id of its BF16 tokens
+          const int pg = lane & 7, at = u.pos0 + kPage * pg;
+          const bool coded = left && max(at, u.c0) < min(at + kPage, u.c1);
+          const bool plain = left && (max(at, u.lo) < min(at + kPage, u.c0) || max(at, u.c1) < min(at + kPage, u.hi));
+          const size_t entry = static_cast<size_t>(u.b) * p.max_pages + at / kPage;
+          int id = -1, id16 = -1;
+          if (coded) id = p.coded_table[entry];
+          if (plain) id16 = p.plain_table[entry];
+          const bool there = coded && id >= 0 && id < p.n_coded, there16 = plain && id16 >= 0 && id16 < p.n_plain;
+          if (((coded && !there) || (plain && !there16)) && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
+          const uint32_t pages = __ballot_sync(0xffffffffu, there);
+          for (int g = 0; g < 4 && todo; ++g, todo &= todo - 1, ++n) {
+            const int st = n % kGStages;
+            if (!(ok = wait(empty + st, (n / kGStages) + 1))) break;
+            if (lane == 8 * g) {
+              u.pages = (pages >> (8 * g)) & 0xffu;
+              tiles[st] = u;
             }
+            __syncwarp();
+            if (lane >> 3 == g) tiles[st].plain[pg] = there16 ? id16 : -1;
+            __syncwarp();
+            if (lane == 8 * g) mbar_arrive_expect_tx(full + st, __popc(u.pages) * S::kPart);
+            __syncwarp();
+            if (lane >> 3 == g && there)
+              bulk_g2s(smem + S::kRing + (st * kGPages + pg) * S::kPart,
+                       p.coded + (static_cast<int64_t>(id) * p.hkv + h) * F::kInt2Block + kv * S::kPart, S::kPart, full + st);
           }
         }
       }
-      for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok;) {
-        // the next four of them, eight lanes each (one at a time, the look-ups of page ids bound the walk)
-        uint32_t left = todo;
-        for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
-        const int src = left ? __ffs(left) - 1 : 0;
-        GatherTile u{};
-        u.b = __shfl_sync(0xffffffffu, t.b, src);
-        u.pos0 = __shfl_sync(0xffffffffu, t.pos0, src);
-        u.lo = __shfl_sync(0xffffffffu, t.lo, src);
-        u.hi = __shfl_sync(0xffffffffu, t.hi, src);
-        u.c0 = __shfl_sync(0xffffffffu, t.c0, src);
-        u.c1 = __shfl_sync(0xffffffffu, t.c1, src);
-        u.row0 = __shfl_sync(0xffffffffu, t.row0, src);
-        // a page a lane: its codes, and the id of its BF16 tokens
-        const int pg = lane & 7, at = u.pos0 + kPage * pg;
-        const bool coded = left && max(at, u.c0) < min(at + kPage, u.c1);
-        const bool plain = left && (max(at, u.lo) < min(at + kPage, u.c0) || max(at, u.c1) < min(at + kPage, u.hi));
-        const size_t entry = static_cast<size_t>(u.b) * p.max_pages + at / kPage;
-        int id = -1, id16 = -1;
-        if (coded) id = p.coded_table[entry];
-        if (plain) id16 = p.plain_table[entry];
-        const bool there = coded && id >= 0 && id < p.n_coded, there16 = plain && id16 >= 0 && id16 < p.n_plain;
-        if (((coded && !there) || (plain && !there16)) && p.status) atomicOr(p.status, OSCAR_DEVERR_PAGE_ID);
-        const uint32_t pages = __ballot_sync(0xffffffffu, there);
-        for (int g = 0; g < 4 && todo; ++g, todo &= todo - 1, ++n) {
-          const int st = n % kGStages;
-          if (!(ok = wait(empty + st, (n / kGStages) + 1))) break;
-          if (lane == 8 * g) {
-            u.pages = (pages >> (8 * g)) & 0xffu;
-            tiles[st] = u;
-          }
-          __syncwarp();
-          if (lane >> 3 == g) tiles[st].plain[pg] = there16 ? id16 : -1;
-          __syncwarp();
-          if (lane == 8 * g) mbar_arrive_expect_tx(full + st, __popc(u.pages) * S::kPart);
-          __syncwarp();
-          if (lane >> 3 == g && there)
-            bulk_g2s(smem + S::kRing + (st * kGPages + pg) * S::kPart,
-                     p.coded + (static_cast<int64_t>(id) * p.hkv + h) * F::kInt2Block + kv * S::kPart, S::kPart, full + st);
-        }
-      }
+      if (ahead < all) ahead += (all - ahead + p.ctas_per_r - 1) / p.ctas_per_r * p.ctas_per_r;
+      ahead -= all;
     }
     // the end, for the warps of even and of odd tiles
     uint32_t k = n > kGStages ? n - kGStages : 0;
@@ -574,7 +599,6 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
   p.hkv = desc->num_kv_heads;
   p.max_pages = desc->max_pages_per_seq;
   p.batch = batch;
-  p.tiles_per_seq = static_cast<int>(tiles);
   // a CTA an SM, and no more for a rotation than there are tiles
   p.ctas_per_r = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(oscar_host::sm_count() / (2 * p.hkv), tiles * batch)));
   p.max_rows = max_rows;
