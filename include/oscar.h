@@ -207,6 +207,7 @@ oscar_status oscar_quantize_append_trace(const oscar_cache_desc* desc, const voi
  *     row_starts[batch] are left as they were.
  *   seq_lens, first [batch], row_starts [batch + 1] (ascending): device int32.
  *   max_rows: no sequence asks for more.
+ *   desc: clip_k and clip_v may be null.
  * A sequence that asks for more than max_rows, for tokens behind seq_lens[b] or outside its table
  * row, or for rows outside [0, total_rows), is skipped with OSCAR_DEVERR_SEQ_LEN; tokens whose
  * page id is out of range are left as they were (OSCAR_DEVERR_PAGE_ID).  Arithmetic: y_hat in fp32, the

@@ -243,8 +243,8 @@ inline TensorMapEncodeTiled tensor_map_encoder() {
 
 inline bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
-// Checks shared by the device calls.  needs_int2: INT2 fields must be valid.
-inline oscar_status check_desc(const oscar_cache_desc* c, bool needs_int2, bool needs_bf16) {
+// Checks shared by the device calls.  needs_int2: INT2 fields must be valid; needs_clips: the clips among them.
+inline oscar_status check_desc(const oscar_cache_desc* c, bool needs_int2, bool needs_bf16, bool needs_clips = true) {
   if (!c) return OSCAR_ERR_INVALID_ARG;
   if (c->num_kv_heads < 1 || c->num_q_heads < 1 || c->sink < 0 || c->window < 1 ||
       c->max_pages_per_seq < 1)
@@ -257,7 +257,7 @@ inline oscar_status check_desc(const oscar_cache_desc* c, bool needs_int2, bool 
   if (needs_bf16 && (!c->bf16_pool || !c->bf16_page_table || c->num_bf16_pages < 1))
     return OSCAR_ERR_INVALID_ARG;
   if (needs_int2 && (!c->int2_pool || !c->int2_page_table || c->num_int2_pages < 1 || !c->r_k ||
-                     !c->r_v || !c->clip_k || !c->clip_v))
+                     !c->r_v || (needs_clips && (!c->clip_k || !c->clip_v))))
     return OSCAR_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(c->int2_pool) | reinterpret_cast<uintptr_t>(c->bf16_pool)) & 15)
     return OSCAR_ERR_INVALID_ARG;

@@ -583,7 +583,7 @@ extern "C" {
 oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens, const int32_t* first,
                           const int32_t* row_starts, int32_t batch, int64_t total_rows,
                           int32_t max_rows, void* k_out, void* v_out, void* stream) {
-  oscar_status s = oscar_host::check_desc(desc, true, true);
+  oscar_status s = oscar_host::check_desc(desc, true, true, false);
   if (s != OSCAR_OK) return s;
   if (batch < 0 || total_rows < 0 || max_rows < 0) return OSCAR_ERR_INVALID_ARG;
   if (batch == 0 || total_rows == 0 || max_rows == 0) return OSCAR_OK;
