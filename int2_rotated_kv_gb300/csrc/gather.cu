@@ -43,7 +43,7 @@
 namespace oscar {
 
 struct GatherParams {
-  int hkv, max_pages, batch, max_rows, sink, window, ctas_per_r;
+  int hkv, max_pages, batch, max_rows, sink, window, ctas_per_r, turn;
   bool whole;        // outputs start at a multiple of 32 bytes
   int64_t n_coded, n_plain, total_rows;
   const uint8_t* coded;
@@ -302,22 +302,40 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
 
   if (warp == 3 * kGWarps) {
     // ------------------------------------------------------------- tiles ahead
-    // The tiles that hold rows, of all sequences laid end to end, go round the rotation's CTAs.  (By number of sequence and
-    // announced rows, a batch of one-tile sequences beside a longer one could fall to one CTA: 255 of 100 tokens and one of
-    // 1130, 8 heads of 128, 1071 us for 138.)
+    // The tiles that hold rows go round the rotation's CTAs: the fast ones, of codes alone, in order; the slow ones, with BF16
+    // tokens (2 us for one page, 4.7 for eight, where codes take 1.5; less between fast ones), by themselves, each round
+    // turned against the one before.  (Handed out by number of sequence and announced rows, one-tile sequences beside a
+    // longer one fell to one CTA: 255 of 100 tokens and one of 1130, 8 heads of 128, 1071 us for 136.  All in one order,
+    // the slow tiles of sequences of as many tiles as there are CTAs do: 64 of 1132 tokens 298 us for 121, 1024 of 300 1262
+    // for 969.)
     uint32_t n = 0;   // tiles published
     bool ok = true;
-    int ahead = number;   // of the tiles from sequence b0 on, this CTA's next
-    // lanes with a sequence, up to a power of two (with 32, one sequence of 2000 tokens of INT2 4.9 us for 4.7)
+    // lanes with a sequence, up to a power of two
     const int among = p.batch < 32 ? 1 << (32 - __clz(p.batch - 1)) : 32;
+    const int ctas = p.ctas_per_r;
+    // of a look's fast tiles this CTA's first; of its slow ones the first of the present round (or one before the look's), and
+    // this CTA's place in it
+    int next_fast = ctas - 1 - number, round0 = 0, place = number;
+    const auto slow_of = [&](int round) {   // this CTA's in the round that is so many on
+      const int x = (place - p.turn * round) % ctas;
+      return round0 + round * ctas + (x < 0 ? x + ctas : x);
+    };
+    // the lane (of those with a sequence) that holds number x of what `upto` counts
+    const auto holder = [&](int upto, int x) {
+      int of = 0;
+#pragma unroll 1
+      for (int o = among >> 1; o > 0; o >>= 1)
+        if (__shfl_sync(0xffffffffu, upto, of + o - 1) <= x) of += o;
+      return of;
+    };
     for (int64_t b0 = 0; b0 < p.batch && ok; b0 += 32) {
       // a sequence a lane
       const int b = static_cast<int>(b0) + lane;
-      int t0 = 0, end = 0, len = 0, count = 0;
-      int64_t r0 = 0;
+      int t0 = 0, end = 0, len = 0;
+      int r0 = 0, before = 0, slow = 0, fast = 0;   // its tiles: the fast ones come after `before` of the slow ones
       if (b0 + lane < p.batch) {
         r0 = p.row_starts[b];
-        const int64_t rows = p.row_starts[b + 1] - r0;
+        const int64_t rows = static_cast<int64_t>(p.row_starts[b + 1]) - r0;
         t0 = p.first[b];
         len = p.seq_lens[b];
         if (rows != 0) {
@@ -326,48 +344,73 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
             if (p.status) atomicOr(p.status, OSCAR_DEVERR_SEQ_LEN);
           } else {
             end = t0 + static_cast<int>(rows);
-            count = static_cast<int>((t0 % kPage + rows + kGTile - 1) / kGTile);
+            const int count = static_cast<int>((t0 % kPage + rows + kGTile - 1) / kGTile), page0 = t0 / kPage;
+            const int recent = min(max(max(len - p.window, 0) / kPage - page0, 0) / kGPages, count);   // the window's first
+            before = min(t0 < p.sink ? ((p.sink - 1) / kPage - page0) / kGPages + 1 : 0, recent);
+            fast = recent - before;
+            slow = count - fast;
           }
         }
       }
-      int upto = count;   // tiles of these sequences up to and with the lane's
+      int upto_slow = slow, upto_fast = fast;   // up to and with the lane's sequence
 #pragma unroll 1
       for (int o = 1; o < among; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += u;
+        const int u = __shfl_up_sync(0xffffffffu, upto_slow, o), v = __shfl_up_sync(0xffffffffu, upto_fast, o);
+        if (lane >= o) {
+          upto_slow += u;
+          upto_fast += v;
+        }
       }
-      const int all = __shfl_sync(0xffffffffu, upto, among - 1);
-      for (int next = ahead; next < all && ok; next += 32 * p.ctas_per_r) {
-        // a tile a lane, and its sequence's lane
-        const bool some = next + lane * p.ctas_per_r < all;
-        const int tile = some ? next + lane * p.ctas_per_r : all - 1;
-        int of = 0;
-#pragma unroll 1
-        for (int o = among >> 1; o > 0; o >>= 1)
-          if (__shfl_sync(0xffffffffu, upto, of + o - 1) <= tile) of += o;
-        GatherTile t{};
-        t.b = static_cast<int>(b0) + of;
-        const int from = __shfl_sync(0xffffffffu, t0, of), to = __shfl_sync(0xffffffffu, end, of);
-        const int i = tile - __shfl_sync(0xffffffffu, upto - count, of);
-        t.pos0 = (from / kPage + kGPages * i) * kPage;
-        t.lo = max(from, t.pos0);
-        t.hi = t.pos0 + min(to - t.pos0, kGTile);
-        t.row0 = __shfl_sync(0xffffffffu, r0, of) + t.pos0 - from;
-        t.c0 = min(max(t.lo, p.sink), t.hi);
-        t.c1 = max(t.c0, min(t.hi, max(__shfl_sync(0xffffffffu, len, of) - p.window, 0)));
+      const int all_slow = __shfl_sync(0xffffffffu, upto_slow, among - 1);
+      const int all_fast = __shfl_sync(0xffffffffu, upto_fast, among - 1);
+      // no more tiles than CTAs: one each, found with fewer steps (2000 tokens of INT2 4.85 us, like the others 5.3)
+      const bool few = p.batch <= 32 && all_slow + all_fast <= ctas;
+      int slows = 0, fasts = few && number < all_slow + all_fast, skip = 0;   // this CTA's; skip: had in the look before
+      if (!few) {
+        if (all_fast > next_fast) fasts = (all_fast - next_fast + ctas - 1) / ctas;
+        const int rounds = (all_slow - round0 + ctas - 1) / ctas;
+        skip = slow_of(0) < 0;
+        if (rounds > skip) slows = rounds - skip - (slow_of(rounds - 1) >= all_slow);
+      }
+      // the slow ones are spread among the fast ones: of the first q tiles, q slows / all are slow (in 32 bits: a CTA
+      // has far fewer than 2^26 tiles)
+      const uint32_t all = slows + fasts;
+      uint32_t had = 0, rest = 0;   // of the first `base`; what the division has left
+      for (uint32_t base = 0; base < all && ok; base += 32) {
+        // a tile a lane: its number among the slow or the fast ones, its sequence's lane and its number there
+        const bool some = base + lane < all;
+        int of, i;
+        if (__builtin_expect(few, 1)) {
+          of = holder(upto_slow + upto_fast, number);
+          i = number - __shfl_sync(0xffffffffu, upto_slow + upto_fast - slow - fast, of);
+        } else {
+          const uint32_t v = rest + lane * slows, q = v / all, before_it = had + q;
+          const bool is_slow = v - q * all + slows >= all;
+          const int slow_at = slow_of(skip + before_it), fast_at = next_fast + static_cast<int>(base + lane - before_it) * ctas;
+          const int of_slow = holder(upto_slow, slow_at), of_fast = holder(upto_fast, fast_at);
+          of = is_slow ? of_slow : of_fast;
+          const int x = slow_at - __shfl_sync(0xffffffffu, upto_slow - slow, of_slow);
+          const int y = fast_at - __shfl_sync(0xffffffffu, upto_fast - fast, of_fast);
+          const int head = __shfl_sync(0xffffffffu, before, of), its_fast = __shfl_sync(0xffffffffu, fast, of);
+          i = !is_slow ? head + y : x < head ? x : x + its_fast;
+          had += (rest + 32 * slows) / all;
+          rest = (rest + 32 * slows) % all;
+        }
         for (uint32_t todo = __ballot_sync(0xffffffffu, some); todo && ok;) {
           // the next four of them, eight lanes each (one at a time, the look-ups of page ids bound the walk)
           uint32_t left = todo;
           for (int k = 0; k < (lane >> 3); ++k) left &= left - 1;
           const int src = left ? __ffs(left) - 1 : 0;
+          const int from_lane = __shfl_sync(0xffffffffu, of, src);
+          const int from = __shfl_sync(0xffffffffu, t0, from_lane), to = __shfl_sync(0xffffffffu, end, from_lane);
           GatherTile u{};
-          u.b = __shfl_sync(0xffffffffu, t.b, src);
-          u.pos0 = __shfl_sync(0xffffffffu, t.pos0, src);
-          u.lo = __shfl_sync(0xffffffffu, t.lo, src);
-          u.hi = __shfl_sync(0xffffffffu, t.hi, src);
-          u.c0 = __shfl_sync(0xffffffffu, t.c0, src);
-          u.c1 = __shfl_sync(0xffffffffu, t.c1, src);
-          u.row0 = __shfl_sync(0xffffffffu, t.row0, src);
+          u.b = static_cast<int>(b0) + from_lane;
+          u.pos0 = (from / kPage + kGPages * __shfl_sync(0xffffffffu, i, src)) * kPage;
+          u.lo = max(from, u.pos0);
+          u.hi = u.pos0 + min(to - u.pos0, kGTile);
+          u.row0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, r0, from_lane)) + u.pos0 - from;
+          u.c0 = min(max(u.lo, p.sink), u.hi);
+          u.c1 = max(u.c0, min(u.hi, max(__shfl_sync(0xffffffffu, len, from_lane) - p.window, 0)));
           // a page a lane: its codes, and the id of its BF16 tokens
           const int pg = lane & 7, at = u.pos0 + kPage * pg;
           const bool coded = left && max(at, u.c0) < min(at + kPage, u.c1);
@@ -397,8 +440,10 @@ __global__ void __launch_bounds__(kGThreads, 1) gather_kernel(const __grid_const
           }
         }
       }
-      if (ahead < all) ahead += (all - ahead + p.ctas_per_r - 1) / p.ctas_per_r * p.ctas_per_r;
-      ahead -= all;
+      next_fast += fasts * ctas - all_fast;
+      const int whole = (all_slow - round0) / ctas;
+      place = slow_of(whole) - round0 - whole * ctas;
+      round0 += whole * ctas - all_slow;
     }
     // the end, for the warps of even and of odd tiles
     uint32_t k = n > kGStages ? n - kGStages : 0;
@@ -601,6 +646,7 @@ oscar_status oscar_gather(const oscar_cache_desc* desc, const int32_t* seq_lens,
   p.batch = batch;
   // a CTA an SM, and no more for a rotation than there are tiles
   p.ctas_per_r = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(oscar_host::sm_count() / (2 * p.hkv), tiles * batch)));
+  p.turn = std::max(1, p.ctas_per_r * 5 / 8);   // (near the golden section, so that turns come back to a CTA late)
   p.max_rows = max_rows;
   p.sink = desc->sink;
   p.window = desc->window;

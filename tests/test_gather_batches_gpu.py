@@ -51,6 +51,20 @@ def test_short_sequences_beside_a_longer_one(hkv, batch):
     assert H.status(m.cache) == 0
 
 
+@pytest.mark.parametrize("hkv", [8, 4])
+def test_sequences_of_as_many_tiles_as_ctas(hkv):
+    """The tiles that hold a sequence's BF16 tokens, its last, do not all fall to the same CTA: a tile takes as long as
+    where a sequence has one tile more."""
+    ctas = H.lib().lib().oscar_device_sm_count() // (2 * hkv)
+    times = []
+    for tiles in (ctas, ctas + 1):
+        lens = np.full(64, 128 * tiles - 20)
+        m = Model(lens, hkv, 128, 2, seed=hkv)
+        times.append(_microseconds(m, np.zeros(64, int), lens, int(lens[0])) / tiles)
+    print(f"{hkv} heads: {times[0]:.2f} and {times[1]:.2f} us for a tile of each")
+    assert times[0] < 1.3 * times[1]
+
+
 @pytest.mark.parametrize("d,hkv,bits", [(64, 2, 2), (128, 8, 4), (128, 1, 2)])
 def test_sequences_without_rows_among_others(d, hkv, bits):
     """Batches that pass 32 sequences, most of which ask for nothing, a few rows, or several tiles; one of them
