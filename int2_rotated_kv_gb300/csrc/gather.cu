@@ -20,20 +20,22 @@
 //   warps 0-3,    R's pieces, while the first codes come; then the rows of even and odd tiles to bf16 and
 //   4-7           out, a token a thread;
 //   warps 26, 27  the tiles' BF16 tokens, as soon as a tile is found (2000 tokens of INT2 4.7 us, by the warps that store
-//                 rows 5.1).
+//                 rows 5.1, when it was measured).
 // Every wait is bounded; a CTA that gives up finishes its copies and MMAs first.
 //
-// What bounds it: the chain of a group of uncoding warps.  INT4, 16 sequences of 2048-4096 tokens, 8 KV heads of 128: 63.8
-// us, 3.6 TB/s and 1050 TFLOP/s of bf16 products (a tile's 24 MMAs take 1536 cycles), with the ALU 59%, the tensor cores
-// 56% and shared memory 57% busy; bytes and products by themselves would take 34 and 34 us.  A group takes 3650 cycles for its
+// What bounds it: the chain of a group of uncoding warps.  INT4, 16 sequences of 2048-4096 tokens, 8 KV heads of 128: 59.3
+// us, 3.8 TB/s and 1130 TFLOP/s of bf16 products (a tile's 24 MMAs take 1536 cycles), with the ALU 60%, the tensor cores
+// 58% and shared memory 64% busy; bytes and products by themselves would take 34 and 34 us.  A group takes 3650 cycles for its
 // every second tile, 1090 of them for codes from shared memory, and waits for 340; 10000 pass before the first products.
 // Fewer instructions there (the larger piece by splitting in fp32, 64.9 us; codes by one operation less, 64.1) and the
-// next words uncoded while the last are stored (65.0) change nothing; more warps would have 56 registers.  2000
-// tokens of INT2, 4 heads of 64: 4.7 us.
+// next words uncoded while the last are stored (65.0) changed nothing (63.8 at the time); more warps would have 56
+// registers.  INT2, as many tokens of other lengths 63.8 us for INT4's 65.9.  2000 tokens of INT2, 4 heads of 64: 4.85 us.
+// BF16 tokens are far from it: two warps a CTA copy them, a page each at a time, at 0.6 us a page.  With a window of 1024
+// tokens those 16 sequences take 115 us (46 by their bytes), of BF16 alone 214 (60); 256 sequences of 130 tokens 177 (40).
 // The same in its steps: without tensor cores 1156 us; a CTA that does one thing after another 124; rows stored by 32 bytes
 // 111 (two CTAs of 8 warps an SM no faster); roles and two accumulators 74; a tile's channels in two steps, so
 // that MMAs start on the first half, and keys' codes read without bank conflicts 67; R turned into pieces beside
-// the first tiles 63.8.
+// the first tiles 63.8; tiles with BF16 tokens shared out by themselves 59.3.
 #include <algorithm>
 
 #include "common.cuh"

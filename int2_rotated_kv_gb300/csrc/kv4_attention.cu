@@ -5,27 +5,30 @@
 // with k_t = code s(channel) g_K(page, head), v_t = code s(token, 16 channels) g_V(page, head) for
 // tokens in whole pages and bf16 keys and values for the tokens of the tail.
 //
-// The arithmetic, the units of weights and the division of work are those of the 8-bit cache
-// (kv8_attention.cu), with code * s, exact in fp16, where that one has codes, and g for its scale: the
-// only roundings are q (exact down to 2^-21 of a column's largest), p g_V (11 bits, unbiased) and
-// the output.
+// The arithmetic and the units of weights are those of the 8-bit cache (kv8_attention.cu), with
+// code * s, exact in fp16, where that one has codes, and g for its scale: the only roundings are
+// q (exact down to 2^-21 of a column's largest), p g_V (11 bits, unbiased) and the output.  The
+// division of work is that one's too, but that a unit counts for kLead pages more in shares.
 //
-// What differs: with half the bytes a page, instructions bound the loop before HBM does.  A page of d = 128 takes a
-// warp 64 conversions and 64 products of codes, 24 conversions of scales and 16 MMAs, 350 instructions in all; an SM
-// needs 125 cycles for it, where HBM's share of an SM brings one in 95.
+// What differs: with half the bytes a page, HBM does not bound the loop.  A page of d = 128 takes a warp 64 conversions and 64
+// products of codes, 24 conversions of scales and 16 MMAs, 340 instructions in all with its part of queries and merges,
+// which would fill an SM's issue slots for 85 cycles where HBM's share of an SM brings a page in 100.  Neither is at its
+// limit (64 sequences: issue slots 61% busy, ALU 54%, HBM 64%): the latency of few warps is, four a scheduler, which
+// issue once in 6.5 cycles each.
 //   - A warp takes two pages at a time: one wait, one softmax step for 32 tokens, and two independent chains of
-//     instructions (64 sequences of 4096-8192 tokens 107 us for 115, one of 131071 43 for 54).
+//     instructions (64 sequences of 4096-8192 tokens 107 us for 115, one of 131071 43 for 54, at the time).
 //   - Tiles of 8, 16 or 24 query columns: what was converted serves all of them, and every page is read once.  Of 20
-//     columns, 16 sequences of 2000-9001 tokens 64.3 us, as three tiles apart 82; 64 of 2000-4000 124 and 169.  (For more
+//     columns, 16 sequences of 2000-9001 tokens 64.3 us, as three tiles apart 82; 64 of 2000-4000 124 and 170.  (For more
 //     columns, several such tiles, or tiles of 128: kv8_rows.cu.)
 //   - The units of weights, queries and merges are the 8-bit cache's, per tile of 8 columns.
 //
-// Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 99.6 us (HBM's floor 67; issue slots 62% busy, the ALU
-// 54%); one of 131071 of 64/8 heads 41.1 us (22.5), one of 32768 18.3 (5.6, of which 7 are launch, queries, first
-// pages and merge); 600 tokens, 4/1 heads of 64, 6.5.
-// Tried: a CTA's warps on the same pages, each with 16 channels of the values and weights through shared memory (126 us for
-// 105 of 64 sequences, 50 for 42 of 131071 tokens: two barriers a step); scales converted by byte permutes and a
-// product (118 us for 115.5); CTAs of 4 warps for one tile (131071 tokens 46 us for 42).
+// Measured, 32/8 heads of 128: 64 sequences of 4096-8192 tokens 99.6 us (HBM's floor 67); one of 131071 of 64/8 heads
+// 41.1 us (22.5), one of 32768 18.3 (5.6, of which 7 are launch, queries, first pages and merge); 600 tokens, 4/1 heads of
+// 64, 6.5; 64 sequences of 4000-8000, 16/4 heads of 64, 38.3 (16.5).
+// Tried, each against what there was at the time: a CTA's warps on the same pages, each with 16 channels of the values and
+// weights through shared memory (126 us for 105 of 64 sequences, 50 for 42 of 131071 tokens: two barriers a step);
+// scales converted by byte permutes and a product (118 us for 115.5); CTAs of 4 warps for one tile (131071 tokens 46 us
+// for 42).
 #include "kv8_tiles.cuh"
 
 namespace oscar {
@@ -35,7 +38,8 @@ constexpr int kPair = 2;       // pages of a step
 
 // In shares, a unit counts for so many pages before its own: the change to it takes a CTA that long.  (Of pages alone, 0, a
 // CTA with many short units ends last: 30 sequences of 100-6000 tokens, 2 rows of 40 heads, 84.7 us for 46.5; 100 of
-// 50-4000 113 for 72.5; 64 of 4096-8192 102.5 for 99.5.  8 and 16: 71 and 58, 95 and 89, 102 and 100; 72: 51, 73, 99.3.)
+// 50-4000 113 for 72.5; 64 of 4096-8192 102.5 for 99.6.  8 and 16: 71 and 58, 95 and 89, 102 and 100; 72: 51, 73, 99.3.
+// Of heads of 64, 64 sequences of 4000-8000 tokens, 16/4 heads, 40.8 for 38.5.)
 constexpr int kLead = 40;
 
 // CTAs per SM that divide the pages among them.
@@ -90,8 +94,8 @@ template <int D, int NT, Kv8Mode kMode>
 struct Kv4Cfg {
   using F = Kv4Fmt<D>;
   // (Shares of several column tiles by small CTAs: while one of them changes units, which takes 10 us of 12 warps
-  // and three tiles, the SM's others go on.  64 sequences x 5 rows over 2000-4000 tokens 134 us for 180; of one
-  // tile, 101 us both.)
+  // and three tiles, the SM's others go on.  64 sequences x 5 rows over 2000-4000 tokens 134 us for 180 before units had
+  // a lead, 124 since; 64 sequences with one tile, 101 us both at the time.)
   static constexpr int kWarps = kMode == kShares ? (NT > 1 ? 4 : 8) : kMode == kTeams ? 8 : NT > 1 ? 12 : 16;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kAtOnce = NT < 3 ? kPair : 1;        // pages whose logits are in registers
@@ -730,8 +734,8 @@ inline int64_t share_ctas4(int nt, int64_t units, int64_t pages, int64_t sms) {
 //   64 x 3 rows over 2000-4000         117, 82.1          -                  153     169
 //   64 x 4 rows over 200-400           46.0, 37.7         -                  24.9    76.1
 //   1 x 64 rows over 500               18.3, 20.5, 23.9   -, 11.4, 13.3      11.1    21.7
-// The rule takes the fastest of a row, to 1%, in 36 of the 40 sizes that were measured, one within 4% in three, and shares
-// for 16 x 5 rows of one length, which the host takes for three quarters of it.
+// The rule takes the fastest of each row but two: for 1 x 64 rows clusters (11.4 us for 11.1), and for 16 x 5 rows of one
+// length shares (87.5 for 74.5), as the host takes a batch's lengths for three quarters of the longest on average.
 inline double page_us4(int d) { return 0.35 + 0.65 / 128 * d; }
 inline double shares_us4(int d, int nt, int64_t batch, int64_t units, int64_t pages) {
   const double start[] = {11.5, 14, 19}, page[] = {0.00044, 0.00062, 0.00085}, unit[] = {0.015, 0.015, 0.04};

@@ -14,7 +14,7 @@
 // of 128: placing 87 us, 5.4 TB/s, with the issue slots 64% busy; reading back 77, 6.1 TB/s; 16 prefixes of 4097-8192
 // tokens read back 74 us, 6.25 TB/s.  A token of 64 sequences: 6.2 and 4.2 us, a chain of lengths, ids and values.
 // Placing is near its instructions' bound too: products two at a time, maxima of pairs of bf16 and each block's scale
-// found by one lane took placing and reading back of the prompts from 183 to 163 us.
+// found by one lane took placing and reading back of the prompts from 183 to 165 us.
 #include "kv4_layout.cuh"
 #include "kv8_spans.cuh"
 
