@@ -91,3 +91,19 @@ def test_sequences_without_rows_among_others(d, hkv, bits):
         assert (a[s] == 7).all()
         a[s] = b[s]
         np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("hkv", [1, 2, 16, 38, 40, 80])
+def test_every_number_of_ctas(hkv):
+    """From as many CTAs a rotation as there are SM pairs to one, and more rotations than SMs; batches of one look
+    and of three, of more tiles than CTAs and of fewer."""
+    rng = np.random.default_rng(hkv)
+    for batch, top in ((1, 900), (9, 40), (32, 300), (70, 500)):
+        lens = rng.integers(1, top, batch)
+        lens[batch // 2] = 2 * top
+        m = Model(lens, hkv, 64, 2, seed=batch)
+        first = np.where(rng.random(batch) < 0.5, 0, rng.integers(0, lens))
+        count = lens - first
+        starts, outs = m.run(first, count)
+        m.check(first, count, starts, outs, heads={(b, h) for b in range(batch) for h in {0, hkv - 1}})
+        assert H.status(m.cache) == 0
